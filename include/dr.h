@@ -329,6 +329,184 @@ const char *dr_status_string(int status);
  * "kalman" the exact Kalman memory, token by token (DR_EKDN, any shape). */
 const char *dr_chunk_fwd_path(int variant, int dtype, int dk, int dv, int chunk);
 
+/* ======================================================================
+ * Layers that stand next to the recurrence in a hybrid stack: attention with a
+ * sliding window and sinks, the short causal convolution, the selective state
+ * space scan.  Each has a prompt form, a backward pass and a form for single
+ * tokens whose state has a constant size.  They follow the rules above:
+ * caller-owned buffers, asynchronous on `stream`, capturable, argument errors
+ * before any launch, nothing traps.  Activations are fp32 (DR_FP32) or bf16
+ * (DR_BF16), all of one call in the same type; sums, softmax statistics and
+ * states are fp32.  Gradients of activations come in the activations' type,
+ * gradients of parameters and states in fp32; every gradient is a sum in a
+ * fixed order, so the same call gives the same bits.
+ * Strides are in elements.  `lens` is a device array [B] of the sequences' real
+ * lengths, or NULL where every sequence is full; values are clamped to
+ * [0, length].
+ * ====================================================================== */
+
+/*
+ * Window attention.  Query row i of a sequence stands at position p = q_start + i
+ * and sees key j where
+ *     j <= p,  j < lens[b],  and  (p - j < window  or  j < n_sink).
+ *     s_j = scale q.k_j;  lse = log sum_j exp(s_j);  out = sum_j exp(s_j - lse) v_j
+ * A row that sees no key has out = 0 and lse = -infinity.  H query heads share
+ * Hkv key/value heads, H / Hkv neighbouring query heads each.
+ */
+typedef struct dr_attn {
+  int dtype;               /* dr_dtype of q, k, v, out and their gradients             */
+  int B, T, S;             /* batch, query rows, key rows                             */
+  int H, Hkv, d;           /* query heads, key/value heads (H % Hkv == 0), 64 or 128  */
+  int window;              /* >= 1                                                    */
+  int n_sink;              /* 0 .. 128 first positions that stay visible              */
+  int q_start;             /* position of query row 0                                 */
+  float scale;             /* 0: 1 / sqrt(d)                                          */
+  const int *lens;         /* [B] real keys per sequence, or NULL (S each)            */
+  long long q_sb, q_st, q_sh;   /* batch, token and head stride of q; the channels of */
+  long long k_sb, k_st, k_sh;   /* a head are contiguous.  16-byte multiples.         */
+  long long v_sb, v_st, v_sh;
+} dr_attn;
+
+/* Fill *a with zeros, dtype DR_BF16 and window INT_MAX. */
+void dr_attn_init(dr_attn *a);
+
+/* Forward.  q [B,T,H,d], k, v [B,S,Hkv,d] with a's strides; out [B,T,H,d]
+ * contiguous; lse fp32 [B,H,T] or NULL.  16-byte aligned. */
+int dr_window_attn_fwd(const dr_attn *a, const void *q, const void *k, const void *v, void *out,
+                       float *lse, dr_stream_t stream);
+
+/* Backward: dq [B,T,H,d], dk, dv [B,S,Hkv,d] (contiguous, overwritten) from the
+ * forward's out and lse and from d_out [B,T,H,d] (contiguous):
+ *     P = exp(s - lse);  dV = P^T dO;  dS = P * (dO V^T - rowsum(dO * O));
+ *     dQ = scale dS K;  dK = scale dS^T Q
+ * dK and dV sum over the query heads of their head.  Keys nobody sees get 0. */
+int dr_window_attn_bwd(const dr_attn *a, const void *q, const void *k, const void *v,
+                       const void *out, const float *lse, const void *d_out, void *dq, void *dk,
+                       void *dv, void *workspace, size_t workspace_bytes, dr_stream_t stream);
+/* Bytes of dr_window_attn_bwd's workspace (256-byte aligned): the rows' sums
+ * of dO * O, and the parts of the sink keys' gradients. */
+size_t dr_window_attn_bwd_workspace_bytes(const dr_attn *a);
+
+/*
+ * One token for every sequence, over a cache of n_sink + window slots per head:
+ * k_cache, v_cache [B,Hkv,n_sink+window,d] (contiguous).  pos [B] (device) is the
+ * token's position.  Position p lives in slot p where p < n_sink and in slot
+ * n_sink + (p - n_sink) mod window otherwise, so the new token takes the place of
+ * the one that has just left the window.  The call writes k and v [B,Hkv,d] into
+ * that slot and attends from q [B,H,d] over what the position sees; out [B,H,d].
+ * A sequence with pos < 0 is left alone and gets out = 0.  Everything is
+ * contiguous; a's T, S, q_start, lens and strides are not used.
+ * The workspace (256-byte aligned) is optional: with it, few sequences with a long
+ * cache are cut along the slots and their parts joined by a second launch.
+ */
+int dr_window_attn_step(const dr_attn *a, const void *q, const void *k, const void *v,
+                        void *k_cache, void *v_cache, const int *pos, void *out, void *workspace,
+                        size_t workspace_bytes, dr_stream_t stream);
+/* Bytes of dr_window_attn_step's workspace on the current device; 0 where none is used. */
+size_t dr_window_attn_step_workspace_bytes(const dr_attn *a);
+
+/* Lays a prompt's keys and values (k, v [B,S,Hkv,d] with a's strides, lens) out in
+ * the slots of dr_window_attn_step, for decoding to go on at position lens[b]:
+ * the sinks and the last `window` positions.  Other slots are left as they are. */
+int dr_window_cache_fill(const dr_attn *a, const void *k, const void *v, void *k_cache,
+                         void *v_cache, dr_stream_t stream);
+
+/*
+ * Short causal convolution, one filter per channel:
+ *     u_t[c] = bias[c] + sum_{j<K} weight[c,j] x_{t-K+1+j}[c];   y = u or u sigmoid(u)
+ * Tokens before the first come from init_state [B,K-1,D] (oldest first, x's type;
+ * NULL: zero).  Rows at and after lens[b] give y = 0 and are not part of the state.
+ */
+typedef struct dr_conv {
+  int dtype;               /* dr_dtype of x, y, states and their gradients            */
+  int B, T, D;             /* batch, tokens, channels                                 */
+  int K;                   /* 2, 3 or 4 taps                                          */
+  int silu;                /* 1: y = u sigmoid(u)                                     */
+  const int *lens;         /* [B] or NULL                                             */
+  long long x_sb, x_st;    /* batch and token stride of x (channels contiguous)       */
+} dr_conv;
+
+/* Forward.  x [B,T,D] with a's strides; weight fp32 [D,K]; bias fp32 [D] or NULL;
+ * y [B,T,D]; final_state [B,K-1,D] or NULL: the last K-1 inputs. */
+int dr_short_conv_fwd(const dr_conv *a, const void *x, const float *weight, const float *bias,
+                      const void *init_state, void *y, void *final_state, dr_stream_t stream);
+
+/* Backward from d_y [B,T,D]: dx [B,T,D], d_weight fp32 [D,K], d_bias fp32 [D] or
+ * NULL, d_init_state [B,K-1,D] (x's type) or NULL.  d_final_state [B,K-1,D] or NULL
+ * is the gradient of the final state. */
+int dr_short_conv_bwd(const dr_conv *a, const void *x, const float *weight, const float *bias,
+                      const void *init_state, const void *d_y, const void *d_final_state, void *dx,
+                      float *d_weight, float *d_bias, void *d_init_state, void *workspace,
+                      size_t workspace_bytes, dr_stream_t stream);
+/* Bytes of dr_short_conv_bwd's workspace (256-byte aligned): the weight
+ * gradients' parts. */
+size_t dr_short_conv_bwd_workspace_bytes(const dr_conv *a);
+
+/* One token: x, y [B,D] (batch stride a->x_sb for x), state [B,K-1,D] read, state_out
+ * written; state_out may be state.  a's T, x_st and lens are not used. */
+int dr_short_conv_step(const dr_conv *a, const void *x, const float *weight, const float *bias,
+                       const void *state, void *state_out, void *y, dr_stream_t stream);
+
+/*
+ * Selective state space scan, N states per channel:
+ *     dt = softplus(dt_raw + dt_bias)            (or dt_raw + dt_bias)
+ *     h_t[c,n] = exp(dt_t[c] A[c,n]) h_{t-1}[c,n] + dt_t[c] Bm_t[g,n] x_t[c]
+ *     y_t[c] = (sum_n Cm_t[g,n] h_t[c,n] + D[c] x_t[c]) (z_t[c] sigmoid(z_t[c]))
+ * with g = c / (D / G) and the gate where z is given.  Rows at and after lens[b]
+ * leave the state alone and give y = 0.
+ */
+typedef struct dr_scan {
+  int dtype;               /* dr_dtype of x, dt, z, Bm, Cm, y and their gradients     */
+  int B, T, D;             /* batch, tokens, channels                                 */
+  int N, G;                /* states per channel: 8, 16, 32 or 64; groups, D % G == 0 */
+  int softplus;            /* 1: dt = softplus(dt_raw + dt_bias)                      */
+  const int *lens;         /* [B] or NULL                                             */
+  const float *A;          /* [D,N]                                                   */
+  const float *Dskip;      /* [D] or NULL (0)                                         */
+  const float *dt_bias;    /* [D] or NULL (0)                                         */
+  long long x_sb, x_st;    /* batch and token strides; the channels of a token (and   */
+  long long dt_sb, dt_st;  /* the G N values of Bm and Cm) are contiguous             */
+  long long z_sb, z_st;
+  long long B_sb, B_st;
+  long long C_sb, C_st;
+} dr_scan;
+
+/* Forward.  x, dt, z [B,T,D] (z NULL: no gate), Bm, Cm [B,T,G,N] with a's strides;
+ * init_state fp32 [B,D,N] or NULL (zero); y [B,T,D]; final_state fp32 [B,D,N] or
+ * NULL.  The workspace (256-byte aligned) is optional: with it, few rows and many
+ * tokens are cut along the tokens; without it one block walks each row. */
+int dr_selective_scan_fwd(const dr_scan *a, const void *x, const void *dt, const void *Bm,
+                          const void *Cm, const void *z, const float *init_state, void *y,
+                          float *final_state, void *workspace, size_t workspace_bytes,
+                          dr_stream_t stream);
+/* Bytes of the forward's workspace on the current device; 0 where none is used. */
+size_t dr_selective_scan_fwd_workspace_bytes(const dr_scan *a);
+
+/* Gradients of the scan (device, overwritten; NULL where marked). */
+typedef struct dr_scan_grads {
+  void *dx, *ddt;          /* [B,T,D] in the activations' type; ddt: of dt_raw        */
+  void *dz;                /* [B,T,D], needed with z                                  */
+  void *dB, *dC;           /* [B,T,G,N] in the activations' type                      */
+  float *dA;               /* [D,N]                                                   */
+  float *dDskip;           /* [D], or NULL                                            */
+  float *ddt_bias;         /* [D], or NULL                                            */
+  float *d_init_state;     /* [B,D,N], or NULL                                        */
+} dr_scan_grads;
+
+/* Backward from d_y [B,T,D] (contiguous) and d_final_state fp32 [B,D,N] (or NULL);
+ * the forward is run again inside.  Needs its workspace. */
+int dr_selective_scan_bwd(const dr_scan *a, const void *x, const void *dt, const void *Bm,
+                          const void *Cm, const void *z, const float *init_state, const void *d_y,
+                          const float *d_final_state, const dr_scan_grads *g, void *workspace,
+                          size_t workspace_bytes, dr_stream_t stream);
+size_t dr_selective_scan_bwd_workspace_bytes(const dr_scan *a);
+
+/* One token: x, dt, z [B,D] (batch strides x_sb, dt_sb, z_sb), Bm, Cm [B,G,N] (B_sb,
+ * C_sb); state fp32 [B,D,N] read, state_out written (may be state); y [B,D]. */
+int dr_selective_scan_step(const dr_scan *a, const void *x, const void *dt, const void *Bm,
+                           const void *Cm, const void *z, const float *state, float *state_out,
+                           void *y, dr_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

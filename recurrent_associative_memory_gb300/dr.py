@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_float, c_int, c_size_t, c_void_p, c_char_p
+from ctypes import c_float, c_int, c_longlong, c_size_t, c_void_p, c_char_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdr.so")
@@ -210,3 +210,150 @@ def dr_chunk_bwd(q, k, v, log_alpha, params: DrParams, variant: int, eps: float,
 
 def dr_chunk_bwd_workspace_bytes(variant, dtype, B, T, H, dk, dv, chunk) -> int:
     return _lib.dr_chunk_bwd_workspace_bytes(variant, dtype, B, T, H, dk, dv, chunk)
+
+
+# ---------------------------------------------------------------- layers next to the recurrence
+
+
+class DrAttn(ctypes.Structure):
+    """Mirror of ``dr_attn``."""
+    _fields_ = [(n, c_int) for n in ("dtype", "B", "T", "S", "H", "Hkv", "d", "window", "n_sink",
+                                     "q_start")] + [
+        ("scale", c_float), ("lens", c_void_p)] + [
+        (f"{t}_{a}", c_longlong) for t in "qkv" for a in ("sb", "st", "sh")]
+
+
+class DrConv(ctypes.Structure):
+    """Mirror of ``dr_conv``."""
+    _fields_ = [(n, c_int) for n in ("dtype", "B", "T", "D", "K", "silu")] + [
+        ("lens", c_void_p), ("x_sb", c_longlong), ("x_st", c_longlong)]
+
+
+class DrScan(ctypes.Structure):
+    """Mirror of ``dr_scan``."""
+    _fields_ = [(n, c_int) for n in ("dtype", "B", "T", "D", "N", "G", "softplus")] + [
+        ("lens", c_void_p), ("A", c_void_p), ("Dskip", c_void_p), ("dt_bias", c_void_p)] + [
+        (f"{t}_{a}", c_longlong) for t in ("x", "dt", "z", "B", "C") for a in ("sb", "st")]
+
+
+class DrScanGrads(ctypes.Structure):
+    """Mirror of ``dr_scan_grads``."""
+    _fields_ = [(n, c_void_p) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dDskip", "ddt_bias",
+                                        "d_init_state")]
+
+
+def _declare(name, args, struct, res=c_int):
+    """``args``: p pointer, s struct by reference, n size_t, g dr_scan_grads by reference."""
+    kinds = {"p": c_void_p, "n": c_size_t, "s": ctypes.POINTER(struct),
+             "g": ctypes.POINTER(DrScanGrads)}
+    f = getattr(_lib, name)
+    f.argtypes = [kinds[a] for a in args]
+    f.restype = res
+    return f
+
+
+_declare("dr_attn_init", "s", DrAttn, None)
+_declare("dr_window_attn_fwd", "s" + "p" * 6, DrAttn)
+_declare("dr_window_attn_bwd", "s" + "p" * 10 + "np", DrAttn)
+_declare("dr_window_attn_bwd_workspace_bytes", "s", DrAttn, c_size_t)
+_declare("dr_window_attn_step", "s" + "p" * 8 + "np", DrAttn)
+_declare("dr_window_attn_step_workspace_bytes", "s", DrAttn, c_size_t)
+_declare("dr_window_cache_fill", "s" + "p" * 5, DrAttn)
+_declare("dr_short_conv_fwd", "s" + "p" * 7, DrConv)
+_declare("dr_short_conv_bwd", "s" + "p" * 11 + "np", DrConv)
+_declare("dr_short_conv_bwd_workspace_bytes", "s", DrConv, c_size_t)
+_declare("dr_short_conv_step", "s" + "p" * 7, DrConv)
+_declare("dr_selective_scan_fwd", "s" + "p" * 9 + "np", DrScan)
+_declare("dr_selective_scan_fwd_workspace_bytes", "s", DrScan, c_size_t)
+_declare("dr_selective_scan_bwd", "s" + "p" * 8 + "gpnp", DrScan)
+_declare("dr_selective_scan_bwd_workspace_bytes", "s", DrScan, c_size_t)
+_declare("dr_selective_scan_step", "s" + "p" * 9, DrScan)
+
+
+def dr_attn_init() -> DrAttn:
+    a = DrAttn()
+    _lib.dr_attn_init(ctypes.byref(a))
+    return a
+
+
+def dr_window_attn_fwd(a: DrAttn, q, k, v, out, lse, stream=None) -> int:
+    return _lib.dr_window_attn_fwd(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                   _stream(stream))
+
+
+def dr_window_attn_bwd(a: DrAttn, q, k, v, out, lse, d_out, dq, dk, dv, workspace,
+                       workspace_bytes: int, stream=None) -> int:
+    return _lib.dr_window_attn_bwd(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                   _ptr(d_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                   workspace_bytes, _stream(stream))
+
+
+def dr_window_attn_bwd_workspace_bytes(a: DrAttn) -> int:
+    return _lib.dr_window_attn_bwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_window_attn_step(a: DrAttn, q, k, v, k_cache, v_cache, pos, out, workspace=None,
+                        workspace_bytes: int = 0, stream=None) -> int:
+    return _lib.dr_window_attn_step(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(pos), _ptr(out), _ptr(workspace),
+                                    workspace_bytes, _stream(stream))
+
+
+def dr_window_attn_step_workspace_bytes(a: DrAttn) -> int:
+    return _lib.dr_window_attn_step_workspace_bytes(ctypes.byref(a))
+
+
+def dr_window_cache_fill(a: DrAttn, k, v, k_cache, v_cache, stream=None) -> int:
+    return _lib.dr_window_cache_fill(ctypes.byref(a), _ptr(k), _ptr(v), _ptr(k_cache),
+                                     _ptr(v_cache), _stream(stream))
+
+
+def dr_short_conv_fwd(a: DrConv, x, weight, bias, init_state, y, final_state, stream=None) -> int:
+    return _lib.dr_short_conv_fwd(ctypes.byref(a), _ptr(x), _ptr(weight), _ptr(bias),
+                                  _ptr(init_state), _ptr(y), _ptr(final_state), _stream(stream))
+
+
+def dr_short_conv_bwd(a: DrConv, x, weight, bias, init_state, d_y, d_final_state, dx, d_weight,
+                      d_bias, d_init_state, workspace, workspace_bytes: int, stream=None) -> int:
+    return _lib.dr_short_conv_bwd(ctypes.byref(a), _ptr(x), _ptr(weight), _ptr(bias),
+                                  _ptr(init_state), _ptr(d_y), _ptr(d_final_state), _ptr(dx),
+                                  _ptr(d_weight), _ptr(d_bias), _ptr(d_init_state),
+                                  _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dr_short_conv_bwd_workspace_bytes(a: DrConv) -> int:
+    return _lib.dr_short_conv_bwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_short_conv_step(a: DrConv, x, weight, bias, state, state_out, y, stream=None) -> int:
+    return _lib.dr_short_conv_step(ctypes.byref(a), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state),
+                                   _ptr(state_out), _ptr(y), _stream(stream))
+
+
+def dr_selective_scan_fwd(a: DrScan, x, dt, Bm, Cm, z, init_state, y, final_state, workspace=None,
+                          workspace_bytes: int = 0, stream=None) -> int:
+    return _lib.dr_selective_scan_fwd(ctypes.byref(a), _ptr(x), _ptr(dt), _ptr(Bm), _ptr(Cm),
+                                      _ptr(z), _ptr(init_state), _ptr(y), _ptr(final_state),
+                                      _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dr_selective_scan_fwd_workspace_bytes(a: DrScan) -> int:
+    return _lib.dr_selective_scan_fwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_selective_scan_bwd(a: DrScan, x, dt, Bm, Cm, z, init_state, d_y, d_final_state,
+                          grads: DrScanGrads, workspace, workspace_bytes: int, stream=None) -> int:
+    return _lib.dr_selective_scan_bwd(ctypes.byref(a), _ptr(x), _ptr(dt), _ptr(Bm), _ptr(Cm),
+                                      _ptr(z), _ptr(init_state), _ptr(d_y), _ptr(d_final_state),
+                                      ctypes.byref(grads), _ptr(workspace), workspace_bytes,
+                                      _stream(stream))
+
+
+def dr_selective_scan_bwd_workspace_bytes(a: DrScan) -> int:
+    return _lib.dr_selective_scan_bwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_selective_scan_step(a: DrScan, x, dt, Bm, Cm, z, state, state_out, y, stream=None) -> int:
+    return _lib.dr_selective_scan_step(ctypes.byref(a), _ptr(x), _ptr(dt), _ptr(Bm), _ptr(Cm),
+                                       _ptr(z), _ptr(state), _ptr(state_out), _ptr(y),
+                                       _stream(stream))

@@ -21,6 +21,9 @@ backward    Reverse-mode gradients of the tokenwise recurrence (every variant)
 ridge       Side oracles fixed by closed forms: exact ridge regression (ATQ),
             its Sherman-Morrison recursion (ATK), the diagonal counterexample
             and a dense-covariance Kalman filter.
+layers      The layers next to the recurrence (window attention with sinks,
+            short causal convolution, selective scan) and their gradients,
+            pinned by ``tests/test_layers_oracle.py``.
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 against values printed on the pages, closed forms, library routines or

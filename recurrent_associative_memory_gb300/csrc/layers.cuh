@@ -46,7 +46,8 @@ struct KeyTiles {
     w_begin = lo / tile;
     const int n_win = hi >= lo ? hi / tile + 1 - w_begin : 0;
     const int sinks = max(0, min(n_sink, hi + 1));
-    n_first = min((sinks + tile - 1) / tile, w_begin);
+    n_first = (sinks + tile - 1) / tile;
+    if (n_win > 0) n_first = min(n_first, w_begin);
     n = n_first + n_win;
   }
   __device__ __forceinline__ int operator[](int i) const {

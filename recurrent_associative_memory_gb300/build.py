@@ -20,8 +20,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdr.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-rdc=true", "-Xcompiler", "-fPIC",
+FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "-Xptxas", "-warn-spills", "--expt-relaxed-constexpr"]
+# compiled as whole programs: relocatable device code would ignore their register split
+WHOLE = ("attn_tc.cu",)
 
 
 def nvcc() -> str:
@@ -43,7 +45,9 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     cc = nvcc()
-    cmds = [[cc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
+    rdc = ["-rdc=false" if os.path.basename(s) in WHOLE else "-rdc=true" for s in srcs]
+    cmds = [[cc, *ARCH, *FLAGS, r, *extra_flags, "-c", s, "-o", o]
+            for s, r, o in zip(srcs, rdc, objs)]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
         logs = list(ex.map(_run, cmds))
     tmp = LIB + ".tmp"

@@ -1,0 +1,329 @@
+// attn_tc.cu — window attention with sinks, forward, bf16 on tcgen05.
+//
+// One CTA owns 256 query rows of a head, two tiles of 128, and walks the 128-key tiles
+// that they can see.  Per tile w and key tile n:
+//   S_w = Q_w K_n^T      M = N = 128, K = d     (operands in shared memory, S in TMEM)
+//   P_w = exp2(S c - m)  one thread per row; bf16, written over S in TMEM
+//   O_w += P_w V_n       M = 128, N = d, K = 128 keys  (A = P from TMEM)
+// The two tiles take turns: while the eight softmax warps (four per tile) work on one,
+// the tensor cores run the other's P V and next S.  The running maximum m is only
+// raised when it would grow by more than 2^8 (P stays far below bf16's and fp32's
+// range, and the final division takes any m), so O is rarely rescaled; S of tile n is
+// issued behind P V of tile n - 1, so a thread that has S may touch O.
+//   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
+//   warp 8          TMA: K and V tiles, two slots each (d = 64: four)
+//   warp 9          one lane issues every MMA
+// Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
+// The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
+// 0 times whatever stands there may be NaN; scores are masked by selection.
+#include <type_traits>
+
+#include "attn_tc.cuh"
+
+namespace dr {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 384;   // three warpgroups; the third has two idle warps
+// registers per thread after the split: 2 x 216 + 72 = 3 x 168, what the launch takes
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
+constexpr float kRaise = 8.f;   // log2 of the growth of P that is let through
+
+template <int D> struct Smem {
+  static constexpr int kTile = kM * D * 2;                  // bytes of 128 rows
+  static constexpr int kSlots = D == 64 ? 4 : 2;
+  static constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kSlots * kTile, kBytes = oV + kSlots * kTile + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, AttnArgs a) {
+  using L = Smem<D>;
+  constexpr int NS = L::kSlots;
+  constexpr uint32_t ID_S = idesc_bf16(128, 128, 0, 0), ID_S32 = idesc_bf16(128, 32, 0, 0);
+  constexpr uint32_t ID_O = idesc_bf16(128, D, 0, 1);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t b_q, b_kf[NS], b_ke[NS], b_vf[NS], b_ve[NS], b_fix, b_s[2], b_p[2], b_o[2], b_end;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int n_block = (a.T + 2 * kM - 1) / (2 * kM);
+  // heads of a group are neighbours: they read the same K and V
+  const int h = blockIdx.x % a.H, i0 = (blockIdx.x / a.H) % n_block * 2 * kM, b = blockIdx.x / a.H / n_block;
+  const int hk = h / a.G, len = real_len(a.lens, b, a.S);
+  const TileSet set0(a, i0, len), set1(a, i0 + kM, len);
+  const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + 2 * kM, a.T) - 1, len, a.window, a.n_sink, kM);
+  // a tile outside every row's window is there for its sinks only
+  auto sinks_only = [&](int tile) { return tile < tiles.n_first && a.n_sink - tile * kM <= 32; };
+
+  if (tid == 0) {
+    mbar_init(&b_q, 1);
+    for (int i = 0; i < NS; ++i)
+      mbar_init(&b_kf[i], 1), mbar_init(&b_ke[i], 1), mbar_init(&b_vf[i], 1), mbar_init(&b_ve[i], 1);
+    mbar_init(&b_fix, 1);
+    mbar_init(&b_end, 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 128), mbar_init(&b_o[w], 1);
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == 9) tmem_alloc(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, kWaitNs)) return true;
+    s_abort = 1;
+    set_status(DR_ERR_TIMEOUT);
+    return false;
+  };
+
+  if (warp < 8) {   // ---------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + w * kM + row, p = a.q_start + i;
+    const TileSet& set = w ? set1 : set0;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + lanes;
+    const float c2 = a.scale * 1.4426950408889634f;
+    float m = -INFINITY, l = 0.f;
+    uint32_t phase = 0;
+    bool any = false, ok = true;
+    const int p0 = a.q_start + i0 + w * kM, p1 = p0 + kM - 1;
+
+    auto one_tile = [&](auto nch, int j0) {   // nch.value blocks of 32 columns
+      constexpr int NC = decltype(nch)::value;
+      float s[32 * NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+      tmem_ld_wait();
+      const bool whole = j0 + 32 * NC - 1 <= p0 && j0 + 32 * NC <= len && p1 - j0 < a.window;
+      if (!whole) {
+        const RowMask mask(a, p, j0, len);
+#pragma unroll
+        for (int c = 0; c < 32 * NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 32 * NC; c += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float f = 1.f;
+      if (m == -INFINITY) {
+        m = top;                                  // nothing summed so far
+      } else if ((top - m) * c2 > kRaise) {
+        f = ex2((m - top) * c2);
+        m = top;
+      }
+      if (any && __any_sync(0xffffffffu, f != 1.f)) {
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st32(tO + c, o);
+        }
+      }
+      const float at = m == -INFINITY ? 0.f : -m * c2;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c0 = 0; c0 < 32 * NC; c0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = c0; c < c0 + 32; c += 2) {
+          fma2(s[c], s[c + 1], c2, at);
+          s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
+          sum[c & 2] += s[c], sum[(c & 2) + 1] += s[c + 1];
+          pk[(c - c0) / 2] = tc::pack_bf16(s[c], s[c + 1]);
+        }
+        tmem_st16(tS + c0 / 2, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    };
+
+    for (int n = 0; n < tiles.n && ok; ++n) {
+      const int tile = tiles[n];
+      if (!set.has(tile)) continue;
+      ok = wait(&b_s[w], phase);
+      ok = __all_sync(0xffffffffu, ok);   // the warp's TMEM accesses are collective
+      if (!ok) break;
+      phase ^= 1;
+      tc_fence_after();
+      if (sinks_only(tile))
+        one_tile(std::integral_constant<int, 1>{}, tile * kM);
+      else
+        one_tile(std::integral_constant<int, 4>{}, tile * kM);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&b_p[w]);
+      any = true;
+    }
+    if (any && ok) {
+      ok = wait(&b_o[w], 0);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok && i0 + w * kM < a.T) {
+      const float f = l != 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.T + i) * a.H + h) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        if (any) {
+          tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+        }
+        if (i < a.T) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 u;
+            uint32_t* q = &u.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              q[k] = any ? tc::pack_bf16(__uint_as_float(v[e + 2 * k]) * f, __uint_as_float(v[e + 2 * k + 1]) * f)
+                         : 0u;
+            *reinterpret_cast<uint4*>(o + c + e) = u;
+          }
+        }
+      }
+      if (a.lse && i < a.T)
+        a.lse[((long long)b * a.H + h) * a.T + i] =
+            l != 0.f ? m * a.scale + logf(l) : -INFINITY;
+    }
+    tc_fence_before();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
+  if (warp == 8) {   // ------------------------------------------------------------- loads
+    const int fix_tile = len < a.S && len % kM ? len / kM : -1;   // its V rows from len on become 0
+    int kn = 0, vn = 0, n_fix = 0;                                // tiles whose loads are under way
+    if (lane == 0 && tiles.n > 0) {
+      mbar_expect_tx(&b_q, 2 * L::kTile);
+      for (int w = 0; w < 2; ++w)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sm + L::oQ + w * L::kTile + c * kM * 128, &tmQ, &b_q, 64 * c, h, i0 + w * kM, b);
+    }
+    bool ok = true;
+    for (int n = 0; n < tiles.n; ++n) {
+      const int slot = n % NS, tile = tiles[n];
+      if (n >= NS) ok = wait(&b_ke[slot], (n / NS - 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (lane == 0) {
+        mbar_expect_tx(&b_kf[slot], L::kTile);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sm + L::oK + slot * L::kTile + c * kM * 128, &tmK, &b_kf[slot], 64 * c, hk, tile * kM, b);
+      }
+      kn = n + 1;
+      if (n >= NS) ok = wait(&b_ve[slot], (n / NS - 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      uint8_t* v = sm + L::oV + slot * L::kTile;
+      uint64_t* full = tile == fix_tile ? &b_fix : &b_vf[slot];
+      if (lane == 0) {
+        mbar_expect_tx(full, L::kTile);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(v + c * kM * 128, &tmV, full, 64 * c, hk, tile * kM, b);
+      }
+      if (tile == fix_tile) {
+        ok = wait(&b_fix, n_fix & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ++n_fix;
+        const int r0 = len % kM;   // rows are 128 bytes in each block of 64 channels
+        for (int e = lane; e < (kM - r0) * 8 * (D / 64); e += 32) {
+          const int c = e / ((kM - r0) * 8), x = e % ((kM - r0) * 8);
+          reinterpret_cast<uint4*>(v + c * kM * 128 + r0 * 128)[x] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_vf[slot]);
+      }
+      vn = n + 1;
+    }
+    if (!ok || s_abort) {   // no copy may be in flight when the CTA ends
+      if (tiles.n > 0) mbar_wait(&b_q, 0, kWaitNs);
+      for (int n = max(0, kn - NS); n < kn; ++n) mbar_wait(&b_kf[n % NS], (n / NS) & 1, kWaitNs);
+      for (int n = max(0, vn - NS); n < vn; ++n) mbar_wait(&b_vf[n % NS], (n / NS) & 1, kWaitNs);
+    }
+  } else if (warp == 9 && lane == 0 && tiles.n > 0) {   // --------------------------- MMAs
+    const uint32_t q0 = smem_u32(sm + L::oQ), k0 = smem_u32(sm + L::oK), v0 = smem_u32(sm + L::oV);
+    int pend[2] = {-1, -1};       // the key tile whose P V is still to come
+    uint32_t np[2] = {0, 0};
+    bool ok = wait(&b_q, 0);
+    for (int n = 0; n <= tiles.n && ok; ++n) {
+      const int slot = n % NS;
+      if (n < tiles.n) ok = wait(&b_kf[slot], (n / NS) & 1);
+      if (n > 0 && ok) ok = wait(&b_vf[(n - 1) % NS], ((n - 1) / NS) & 1);
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (pend[w] >= 0) {
+          if (!(ok = wait(&b_p[w], np[w] & 1))) break;
+          tc_fence_after();
+          const int steps = sinks_only(tiles[pend[w]]) ? 2 : kM / 16;
+          const uint32_t v = v0 + (pend[w] % NS) * L::kTile;
+          for (int k = 0; k < steps; ++k)
+            mma_bf16_ta(tmem + 256 + w * D, tmem + w * 128 + 8 * k, desc_mnmajor<kM>(v, k), ID_O,
+                        np[w] > 0 || k > 0);
+          ++np[w];
+          pend[w] = -1;
+        }
+        if (n < tiles.n && (w ? set1 : set0).has(tiles[n])) {
+          const uint32_t id = sinks_only(tiles[n]) ? ID_S32 : ID_S;
+          for (int k = 0; k < D / 16; ++k)
+            mma_bf16(tmem + w * 128, desc_kmajor<kM>(q0 + w * L::kTile, k), desc_kmajor<kM>(k0 + slot * L::kTile, k),
+                     id, k > 0);
+          mma_commit(&b_s[w]);
+          pend[w] = n;
+        }
+        if (n == tiles.n) mma_commit(&b_o[w]);
+      }
+      if (!ok) break;
+      if (n < tiles.n) mma_commit(&b_ke[slot]);
+      if (n > 0) mma_commit(&b_ve[(n - 1) % NS]);
+    }
+    mma_commit(&b_end);           // no MMA may be under way when the CTA ends
+    mbar_wait(&b_end, 0, kWaitNs);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
+  CUtensorMap q, k, v;
+  if (!make_map(&q, a.q, a.B, a.T, a.H, D, a.q_sb, a.q_st, a.q_sh) ||
+      !make_map(&k, a.k, a.B, a.S, a.Hkv, D, a.k_sb, a.k_st, a.k_sh) ||
+      !make_map(&v, a.v, a.B, a.S, a.Hkv, D, a.v_sb, a.v_st, a.v_sh))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attn_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long grid = (long long)a.B * a.H * ((a.T + 2 * kM - 1) / (2 * kM));
+  attn_fwd_tc_kernel<D><<<static_cast<unsigned>(grid), kThreads, Smem<D>::kBytes, st>>>(q, k, v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// bf16 with strides that a tensor map can hold
+bool attn_tc_supported(const AttnArgs& a, int dtype) {
+  return dtype == DR_BF16 && map_strides_ok(a.B, a.T, a.H, a.q_sb, a.q_st, a.q_sh) &&
+         map_strides_ok(a.B, a.S, a.Hkv, a.k_sb, a.k_st, a.k_sh) &&
+         map_strides_ok(a.B, a.S, a.Hkv, a.v_sb, a.v_st, a.v_sh);
+}
+
+cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st) { return take_status(word, st); }
+
+cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st) {
+  return a.d == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+}
+
+}  // namespace dr

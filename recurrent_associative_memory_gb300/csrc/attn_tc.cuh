@@ -1,0 +1,143 @@
+// attn_tc.cuh — what the tcgen05 window-attention kernels share: TMEM loads and stores,
+// the MMA with its A operand in TMEM, packed fp32 arithmetic, tile masks, tensor maps.
+// Their translation units are compiled as whole programs: with relocatable device code
+// the compiler ignores setmaxnreg, and a row of 128 scores does not fit the registers
+// that an even split leaves (428 bytes of spills per thread).
+#pragma once
+
+#include "layers.cuh"
+#include "tc_common.cuh"
+
+namespace dr {
+namespace attn {
+
+using namespace umma;
+
+constexpr uint64_t kWaitNs = 2000000000ull;   // a wait gives up after this long
+constexpr int kM = 128;                       // rows of a tile, on either axis
+
+// D(tmem) (+)= A(tmem) * B(smem desc): row r of A in lane r, two bf16 per column
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// 32 lanes x 32 consecutive columns (lane = thread)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21,"
+      " %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22,"
+      " %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (x0, x1) * m + a on a pair of fp32 at once
+__device__ __forceinline__ void fma2(float& x0, float& x1, float m, float a) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(m), "f"(a));
+}
+
+// The key tiles of kM keys that a tile of query rows can see, as a set.
+struct TileSet {
+  int n_first, w_begin, w_end;
+  __device__ __forceinline__ TileSet(const AttnArgs& a, int i0, int len) {
+    const KeyTiles t(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kM);
+    n_first = t.n_first, w_begin = t.w_begin, w_end = t.w_begin + t.n - t.n_first;
+    if (i0 >= a.T) n_first = w_end = 0;
+  }
+  __device__ __forceinline__ bool has(int tile) const {
+    return tile < n_first || (tile >= w_begin && tile < w_end);
+  }
+};
+
+// Which columns of a tile of keys from j0 a row at position p sees: columns of
+// [lo, hi], and those below `sink` that are at most hi.
+struct RowMask {
+  int lo, hi, sink;
+  __device__ __forceinline__ RowMask(const AttnArgs& a, int p, int j0, int len) {
+    lo = p - a.window + 1 - j0;
+    hi = min(p, len - 1) - j0;
+    sink = a.n_sink - j0;
+  }
+  __device__ __forceinline__ bool sees(int c) const { return c <= hi && (c >= lo || c < sink); }
+};
+
+// K-major operand of `rows` rows in 64-column blocks: the descriptor at k-step `k` (16 columns)
+template <int ROWS>
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t base, int k) {
+  return desc_sw128(base + (k >> 2) * (ROWS * 128) + (k & 3) * 32, 0, 1024);
+}
+// MN-major operand whose `ROWS` rows are the k axis: the descriptor at k-step `k` (16 rows)
+template <int ROWS>
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base, int k) {
+  return desc_sw128(base + k * 2048, ROWS * 128, 1024);
+}
+
+// ------------------------------------------------------------------ host side
+
+// Enqueues the read and the clearing of this translation unit's status word.
+static inline cudaError_t take_status(int* word, cudaStream_t st) {
+  static const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+}
+
+// [B, rows, heads, d] bf16 with strides in elements; box of 64 channels x kM rows
+inline bool make_map(CUtensorMap* m, const void* ptr, int B, int rows, int heads, int d, long long sb,
+                     long long st, long long sh) {
+  tc::EncodeTiledFn enc = tc::get_encode();
+  if (!enc) return false;
+  auto bytes = [](int n, long long s) { return static_cast<cuuint64_t>(n > 1 ? 2 * s : 16); };
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)B};
+  cuuint64_t strides[3] = {bytes(heads, sh), bytes(rows, st), bytes(B, sb)};
+  cuuint32_t box[4] = {64, 1, kM, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// a tensor map takes positive strides below 2^40 bytes
+inline bool map_strides_ok(int B, int rows, int heads, long long sb, long long st, long long sh) {
+  auto ok = [](int n, long long s) { return n == 1 || (s > 0 && s < (1LL << 39)); };
+  return ok(B, sb) && ok(rows, st) && ok(heads, sh);
+}
+
+}  // namespace attn
+}  // namespace dr

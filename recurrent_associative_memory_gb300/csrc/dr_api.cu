@@ -27,6 +27,7 @@ bool kdn_split_supported(int variant, int dtype, int dk, int dv, int chunk);
 size_t kdn_split_workspace_bytes(int B, int T, int H);
 bool chunk_bwd_supported(int variant, int dtype, int dk, int dv, int chunk);
 size_t chunk_bwd_workspace_bytes(int variant, int B, int T, int H);
+cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st);
 cudaError_t launch_chunk_bwd(const FwdArgs& fa, const void* d_out, const float* dS_final,
                              const dr_grads& g, void* workspace, cudaStream_t st);
 
@@ -282,8 +283,10 @@ int dr_get_device_status(dr_stream_t stream) {
   if (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
       cudaSuccess)
     return DR_ERR_CUDA;
+  int tc = 0;   // whole-program translation units keep their own word
+  if (attn_fwd_tc_status(&tc, s) != cudaSuccess) return DR_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return DR_ERR_CUDA;
-  return h;
+  return h ? h : tc;
 }
 
 }  // extern "C"

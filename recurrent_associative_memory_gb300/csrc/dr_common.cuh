@@ -53,8 +53,14 @@ struct FwdArgs {
   float* seg_buf;
 };
 
-// Sticky device status: the first non-OK code written stays until read.
+// Sticky device status: the first non-OK code written stays until read.  A
+// translation unit compiled as a whole program has a word of its own, which
+// dr_get_device_status() reads too.
+#ifdef __CUDACC_RDC__
 extern __device__ int g_status;
+#else
+static __device__ int g_status = 0;
+#endif
 
 __device__ __forceinline__ void set_status(int code) { atomicCAS(&g_status, 0, code); }
 

@@ -10,6 +10,8 @@ namespace dr {
 
 cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
+bool attn_tc_supported(const AttnArgs& a, int dtype);
+cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st);
 int attn_step_pieces(const AttnStepArgs& a, int sms);
 cudaError_t launch_attn_step(const AttnStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_fill(const AttnArgs& a, int dtype, void* kc, void* vc, cudaStream_t st);
@@ -171,6 +173,7 @@ int dr_window_attn_fwd(const dr_attn* a, const void* q, const void* k, const voi
   if (!aligned16(q, k, v, out) || !strides_ok(a, true)) return DR_ERR_ALIGN;
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = out, r.lse = lse;
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, stream_of(stream)));
   return status_of(launch_attn_fwd_simt(r, a->dtype, stream_of(stream)));
 }
 

@@ -359,7 +359,7 @@ typedef struct dr_attn {
   int H, Hkv, d;           /* query heads, key/value heads (H % Hkv == 0), 64 or 128  */
   int window;              /* >= 1                                                    */
   int n_sink;              /* 0 .. 128 first positions that stay visible              */
-  int q_start;             /* position of query row 0                                 */
+  int q_start;             /* position of query row 0; positions end at 2^30          */
   float scale;             /* 0: 1 / sqrt(d)                                          */
   const int *lens;         /* [B] real keys per sequence, or NULL (S each)            */
   long long q_sb, q_st, q_sh;   /* batch, token and head stride of q; the channels of */

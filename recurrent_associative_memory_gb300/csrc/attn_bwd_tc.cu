@@ -1,0 +1,510 @@
+// attn_bwd_tc.cu — window attention with sinks, backward, bf16 on tcgen05.
+//
+//   P = exp(s - lse);  dV = P^T dO;  dS = P * (dO V^T - delta);  dQ = c dS K;  dK = c dS^T Q
+// with delta = rowsum(dO * O), in three launches and a fourth for the sinks:
+//   rows   -lse log2(e) and -delta of every query row, padded to whole tiles of 64 (rows
+//          that see nothing get -infinity, which makes their P zero by itself)
+//   dK/dV  a CTA owns 128 keys of a key/value head and walks the 64-row query tiles of
+//          the group's heads that see them:  S^T = K Q^T and dP^T = V dO^T into TMEM, one
+//          thread per key forms P^T and dS^T in bf16 in their place, and from there they
+//          are the A operands of  dV += P^T dO,  dK += dS^T Q  (Q and dO rows as the k axis)
+//   dQ     a CTA owns 128 query rows and walks 64-key tiles: S, dP, dS in place,
+//          dQ += dS K
+// S and dP are formed twice (7 products instead of 5): the alternative, one kernel that
+// adds its dQ parts to memory, would depend on the order of atomics.  Two TMEM slots let
+// the softmax warpgroup of one tile work while the tensor cores run the other's products.
+// The sinks' keys are seen by every later row: rows that see nothing else of key tile 0
+// are cut into pieces of their own, whose sums are joined in a fixed order at the end.
+// Rounding: P and dS to bf16 as operands, the gradients once at the end.
+#include <limits.h>
+
+#include "attn_tc.cuh"
+
+namespace dr {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 384;
+constexpr int kN = 64;         // rows of a tile on the walked axis
+constexpr int kStages = 4;
+
+template <int D> struct Smem {
+  static constexpr int kOwn = kM * D * 2, kTile = kN * D * 2;
+  static constexpr int oX = 0, oY = kOwn, oA = 2 * kOwn, oB = oA + kStages * kTile;
+  static constexpr int oVec = oB + kStages * kTile, kBytes = oVec + kStages * 2 * kN * 4 + 1024;
+};
+
+__device__ __forceinline__ bool bounded(uint64_t* bar, uint32_t parity) {
+  if (mbar_wait(bar, parity, kWaitNs)) return true;
+  set_status(DR_ERR_TIMEOUT);
+  return false;
+}
+
+// ------------------------------------------------------------------ the rows' numbers
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
+  constexpr int LK = D / 8;
+  const long long e = (long long)blockIdx.x * (256 / LK) + threadIdx.x / LK;   // [B,Tp,H]
+  const int c = 8 * (threadIdx.x % LK);
+  const bool in = e < (long long)a.B * a.Tp * a.H;
+  const int h = e % a.H, t = e / a.H % a.Tp, b = in ? e / a.H / a.Tp : 0;
+  float s = 0.f;
+  if (in && t < a.T) {
+    const long long row = ((long long)b * a.T + t) * a.H + h;
+    float o[8], g[8];
+    load8<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(a.out) + row * D + c, 8, o);
+    load8<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(a.d_out) + row * D + c, 8, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += o[i] * g[i];
+  }
+#pragma unroll
+  for (int w = LK / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+  if (!in || c) return;
+  const long long at = ((long long)b * a.H + h) * a.Tp + t;
+  const float lse = t < a.T ? a.lse[((long long)b * a.H + h) * a.T + t] : -INFINITY;
+  a.nlse2[at] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+  a.delta[at] = -s;
+}
+
+// ------------------------------------------------------------------ the shared pipeline
+
+// One CTA's pipeline over n steps.  X, Y: the own tiles (dK/dV: K, V; dQ: Q, dO), A, B: the
+// walked ones (Q, dO; K, V).  Per step: slot S = X A^T, slot dP = Y B^T; then, from what
+// the softmax warps left in their place, acc0 += [S] B (dK/dV only) and acc1 += [dP] A.
+struct Pipe {
+  uint64_t own, full[kStages], empty[kStages], fix, s[2], p[2], acc, end;
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
+  if (tid == 0) {
+    mbar_init(&q.own, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&q.full[i], 1), mbar_init(&q.empty[i], 1);
+    mbar_init(&q.fix, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 128);
+    mbar_init(&q.acc, 1);
+    mbar_init(&q.end, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&q.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+// The MMA lane.  TMEM: slot i at 128 i (S, then 64 columns on dP), accumulators at 256 and
+// 256 + D.  KV: the dK/dV products, else dQ's.
+template <int D, bool KV>
+__device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, int n) {
+  using L = Smem<D>;
+  constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0), ID_ACC = idesc_bf16(kM, D, 0, 1);
+  const uint32_t x = smem_u32(sm + L::oX), y = smem_u32(sm + L::oY), A = smem_u32(sm + L::oA),
+                 B = smem_u32(sm + L::oB), tm = q.tmem;
+  bool ok = bounded(&q.own, 0);
+  for (int i = 0; i < n + 2 && ok; ++i) {
+    if (i >= 2) {   // step i - 2: its slot is the one that step i takes
+      const int j = i - 2, st = j % kStages, slot = j & 1;
+      if (!(ok = bounded(&q.p[slot], (j >> 1) & 1))) break;
+      tc_fence_after();
+      if (KV)
+        for (int k = 0; k < kN / 16; ++k)
+          mma_bf16_ta(tm + 256, tm + 128 * slot + 8 * k, desc_mnmajor<kN>(B + st * L::kTile, k), ID_ACC,
+                      j > 0 || k > 0);
+      for (int k = 0; k < kN / 16; ++k)
+        mma_bf16_ta(tm + 256 + D, tm + 128 * slot + 64 + 8 * k, desc_mnmajor<kN>(A + st * L::kTile, k), ID_ACC,
+                    j > 0 || k > 0);
+      mma_commit(&q.empty[st]);
+    }
+    if (i < n) {
+      const int st = i % kStages, slot = i & 1;
+      if (!(ok = bounded(&q.full[st], (i / kStages) & 1))) break;
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16(tm + 128 * slot, desc_kmajor<kM>(x, k), desc_kmajor<kN>(A + st * L::kTile, k), ID_S, k > 0);
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16(tm + 128 * slot + 64, desc_kmajor<kM>(y, k), desc_kmajor<kN>(B + st * L::kTile, k), ID_S, k > 0);
+      mma_commit(&q.s[slot]);
+    }
+  }
+  mma_commit(&q.acc);
+  mma_commit(&q.end);   // no MMA may be under way when the CTA ends
+  mbar_wait(&q.end, 0, kWaitNs);
+  tc_fence_before();
+}
+
+// The load warp gave up or is done: no copy may be in flight when the CTA ends.
+__device__ __forceinline__ void pipe_drain(Pipe& q, int issued) {
+  mbar_wait(&q.own, 0, kWaitNs);
+  for (int i = max(0, issued - kStages); i < issued; ++i)
+    mbar_wait(&q.full[i % kStages], (i / kStages) & 1, kWaitNs);
+}
+
+// 128 lanes' rows of D accumulator columns -> bf16 rows (or fp32 parts)
+template <int D>
+__device__ __forceinline__ void store_acc(uint32_t tacc, bool any, float f, __nv_bfloat16* o, float* part) {
+#pragma unroll
+  for (int c = 0; c < D; c += 32) {
+    uint32_t v[32];
+    if (any) {
+      tmem_ld32(tacc + c, v);
+      tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0u;
+    }
+    if (part) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else if (o) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v[e + k]) * f;
+        *reinterpret_cast<uint4*>(o + c + e) = tc::pack8(x);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       AttnArgs a) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Pipe q;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int hk = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv % a.B, item = blockIdx.x / a.Hkv / a.B;
+  const bool far = item < a.n_far;              // first: they are as long as the others or longer
+  const int j0 = far ? 0 : (item - a.n_far) * kM;
+  const int len = real_len(a.lens, b, a.S);
+  int i_begin, i_end;                           // query rows, i_begin a multiple of kN
+  if (far) {
+    i_begin = a.far_first + item * a.far_rows;
+    i_end = len > 0 ? min(a.T, i_begin + a.far_rows) : i_begin;
+  } else {
+    const QueryRows r(j0, min(j0 + kM, a.S) - 1, len, a.window, a.n_sink, a.q_start, a.T);
+    i_begin = r.begin / kN * kN;
+    i_end = j0 == 0 && a.n_far ? min(r.end, a.far_first) : r.end;
+  }
+  const int per = i_end > i_begin ? (i_end - i_begin + kN - 1) / kN : 0, n = per * a.G;
+  pipe_init(q, tid, warp);
+  const uint32_t tmem = q.tmem;
+
+  if (warp < 8) {   // one thread per key; the warpgroups take the steps in turn
+    const int w = warp / 4, row = (warp % 4) * 32 + lane, j = j0 + row;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tS = tmem + 128 * w + lanes;
+    const float c2 = a.scale * 1.4426950408889634f;
+    const int key_hi = j < a.n_sink ? INT_MAX : j + a.window - 1;   // last position that sees this key
+    bool ok = true;
+    for (int i = w; i < n; i += 2) {
+      const int st = i % kStages, i0 = i_begin + (i % per) * kN;
+      ok = bounded(&q.s[w], (i >> 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      ok = bounded(&q.full[st], (i / kStages) & 1);   // this stage's numbers (with its tiles)
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc_fence_after();
+      const float4* nl = reinterpret_cast<const float4*>(sm + L::oVec + st * 2 * kN * 4);
+      const float4* nd = nl + kN / 4;
+      const int p0 = a.q_start + i0;
+      const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
+                         (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
+      const int lo = j < len ? j - p0 : INT_MAX, hi = key_hi == INT_MAX ? INT_MAX : key_hi - p0;
+#pragma unroll
+      for (int c0 = 0; c0 < kN; c0 += 32) {
+        float s[32], g[32];
+        uint32_t pk[16];
+        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 l4 = nl[(c0 + c) / 4];
+          fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
+          fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = ex2(s[c]);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = c0 + c >= lo && c0 + c <= hi ? s[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
+        tmem_st16(tS + c0 / 2, pk);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d4 = nd[(c0 + c) / 4];
+          add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
+          add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
+        }
+        if (!whole) {   // what a key past the end holds may be NaN
+#pragma unroll
+          for (int c = 0; c < 32; ++c) g[c] = s[c] != 0.f ? g[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+        tmem_st16(tS + 64 + c0 / 2, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&q.p[w]);
+    }
+    if (n > 0) {
+      ok = bounded(&q.acc, 0) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok) {   // warpgroup 0: dV, 1: dK
+      const long long o = (((long long)b * a.S + j) * a.Hkv + hk) * D;
+      const bool part = a.n_far && j0 == 0 && j < a.n_sink;
+      float* p = part ? a.sink_part + (((((long long)b * a.Hkv + hk) * (1 + a.n_far) + (far ? 1 + item : 0)) * 2 +
+                                        (1 - w)) * a.n_sink + j) * D
+                      : nullptr;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(w ? a.dk : a.dv) + o;
+      store_acc<D>(tmem + 256 + w * D + lanes, n > 0, w ? a.scale : 1.f,
+                   j < a.S && !part && !far ? out : nullptr, p);
+    }
+    tc_fence_before();
+  } else if (warp == 8) {
+    int issued = 0;
+    if (lane == 0 && n > 0) {
+      mbar_expect_tx(&q.own, 2 * L::kOwn);
+      for (int c = 0; c < D / 64; ++c) {
+        tma_load_4d(sm + L::oX + c * kM * 128, &tmK, &q.own, 64 * c, hk, j0, b);
+        tma_load_4d(sm + L::oY + c * kM * 128, &tmV, &q.own, 64 * c, hk, j0, b);
+      }
+      for (int i = 0; i < n; ++i) {
+        const int st = i % kStages, h = hk * a.G + i / per, i0 = i_begin + (i % per) * kN;
+        if (i >= kStages && !bounded(&q.empty[st], (i / kStages - 1) & 1)) break;
+        mbar_expect_tx(&q.full[st], 2 * L::kTile + 2 * kN * 4);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmQ, &q.full[st], 64 * c, h, i0, b);
+          tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmO, &q.full[st], 64 * c, h, i0, b);
+        }
+        const long long at = ((long long)b * a.H + h) * a.Tp + i0;
+        bulk_load(sm + L::oVec + st * 2 * kN * 4, a.nlse2 + at, kN * 4, &q.full[st]);
+        bulk_load(sm + L::oVec + st * 2 * kN * 4 + kN * 4, a.delta + at, kN * 4, &q.full[st]);
+        issued = i + 1;
+      }
+      pipe_drain(q, issued);
+    }
+  } else if (warp == 9 && lane == 0 && n > 0) {
+    pipe_mma<D, true>(q, sm, n);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// The sinks' gradients: their pieces in order.
+template <int D>
+__global__ void __launch_bounds__(D) attn_sink_join_kernel(AttnArgs a) {
+  const int j = blockIdx.x % a.n_sink, x = blockIdx.x / a.n_sink % 2;   // x = 0: dk, 1: dv
+  const long long bh = blockIdx.x / a.n_sink / 2;
+  if (j >= a.S) return;
+  const float* p = a.sink_part + (bh * (1 + a.n_far) * 2 + x) * a.n_sink * D + j * D + threadIdx.x;
+  float s = 0.f;
+  for (int i = 0; i <= a.n_far; ++i) s += p[(long long)i * 2 * a.n_sink * D];
+  const long long b = bh / a.Hkv, hk = bh % a.Hkv;
+  const long long o = ((b * a.S + j) * a.Hkv + hk) * D + threadIdx.x;
+  static_cast<__nv_bfloat16*>(x ? a.dv : a.dk)[o] = __float2bfloat16_rn(x ? s : s * a.scale);
+}
+
+// ------------------------------------------------------------------ dQ
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      AttnArgs a) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Pipe q;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int n_block = (a.T + kM - 1) / kM;
+  const int h = blockIdx.x % a.H, i0 = blockIdx.x / a.H % n_block * kM, b = blockIdx.x / a.H / n_block;
+  const int hk = h / a.G, len = real_len(a.lens, b, a.S);
+  const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN);
+  const int n = tiles.n;
+  pipe_init(q, tid, warp);
+  const uint32_t tmem = q.tmem;
+
+  if (warp < 8) {   // one thread per query row; the warpgroups take the steps in turn
+    const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + row, p = a.q_start + i;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tS = tmem + 128 * w + lanes;
+    const float c2 = a.scale * 1.4426950408889634f;
+    float nl = -INFINITY, nd = 0.f;
+    if (i < a.T) {
+      const long long at = ((long long)b * a.H + h) * a.Tp + i;
+      nl = a.nlse2[at], nd = a.delta[at];
+    }
+    bool ok = true;
+    for (int k = w; k < n; k += 2) {
+      const int t0 = tiles[k] * kN;
+      ok = bounded(&q.s[w], (k >> 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc_fence_after();
+      const bool whole = t0 + kN - 1 <= a.q_start + i0 && t0 + kN <= len && a.q_start + i0 + kM - 1 - t0 < a.window;
+      const RowMask mask(a, p, t0, len);
+#pragma unroll
+      for (int c0 = 0; c0 < kN; c0 += 32) {
+        float s[32], g[32];
+        uint32_t pk[16];
+        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          fma2(s[c], s[c + 1], c2, nl);
+          s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
+          add_mul2(g[c], g[c + 1], nd, nd, s[c], s[c + 1]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) g[c] = mask.sees(c0 + c) && s[c] != 0.f ? g[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+        tmem_st16(tS + 64 + c0 / 2, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&q.p[w]);
+    }
+    if (w == 0) {
+      if (n > 0) {
+        ok = bounded(&q.acc, 0) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      if (ok)
+        store_acc<D>(tmem + 256 + D + lanes, n > 0, a.scale,
+                     i < a.T ? static_cast<__nv_bfloat16*>(a.dq) + (((long long)b * a.T + i) * a.H + h) * D : nullptr,
+                     nullptr);
+    }
+    tc_fence_before();
+  } else if (warp == 8) {
+    const int fix_tile = len < a.S && len % kN ? len / kN : -1;   // its K rows from len on become 0
+    int issued = 0, n_fix = 0;
+    bool ok = true;
+    if (lane == 0 && n > 0) {
+      mbar_expect_tx(&q.own, 2 * L::kOwn);
+      for (int c = 0; c < D / 64; ++c) {
+        tma_load_4d(sm + L::oX + c * kM * 128, &tmQ, &q.own, 64 * c, h, i0, b);
+        tma_load_4d(sm + L::oY + c * kM * 128, &tmO, &q.own, 64 * c, h, i0, b);
+      }
+    }
+    for (int k = 0; k < n; ++k) {
+      const int st = k % kStages, t0 = tiles[k] * kN;
+      if (k >= kStages) ok = bounded(&q.empty[st], (k / kStages - 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      uint64_t* full = tiles[k] == fix_tile ? &q.fix : &q.full[st];
+      if (lane == 0) {
+        mbar_expect_tx(full, 2 * L::kTile);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmK, full, 64 * c, hk, t0, b);
+          tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmV, full, 64 * c, hk, t0, b);
+        }
+      }
+      if (tiles[k] == fix_tile) {
+        ok = bounded(&q.fix, n_fix & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ++n_fix;
+        const int r0 = len % kN;
+        for (int e = lane; e < (kN - r0) * 8 * (D / 64); e += 32) {
+          const int c = e / ((kN - r0) * 8), x = e % ((kN - r0) * 8);
+          reinterpret_cast<uint4*>(sm + L::oA + st * L::kTile + c * kN * 128 + r0 * 128)[x] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q.full[st]);
+      }
+      issued = k + 1;
+    }
+    if (n > 0) pipe_drain(q, issued);
+  } else if (warp == 9 && lane == 0 && n > 0) {
+    pipe_mma<D, false>(q, sm, n);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// How the query rows that see only the sinks of key tile 0 are cut: pieces about as long
+// as what any other key tile is seen by.
+void cut_far(AttnArgs& a) {
+  a.Tp = (a.T + kN - 1) / kN * kN;
+  a.n_far = 0, a.far_first = a.Tp, a.far_rows = kN;
+  if (a.n_sink == 0) return;
+  const long long first = ((long long)kM - 1 + a.window - a.q_start + kN - 1) / kN * kN;
+  if (first >= a.T) return;
+  a.far_first = first > 0 ? static_cast<int>(first) : 0;
+  const long long rows = ((long long)a.window + kM + kN - 1) / kN * kN;
+  a.far_rows = static_cast<int>(rows < 512 ? 512 : rows);
+  a.n_far = (a.T - a.far_first + a.far_rows - 1) / a.far_rows;
+}
+
+template <int D>
+cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
+  using L = Smem<D>;
+  constexpr int LK = D / 8;
+  const long long rows = (long long)a.B * a.Tp * a.H;
+  attn_rows_kernel<D><<<static_cast<unsigned>((rows * LK + 255) / 256), 256, 0, st>>>(a);
+  const long long o_st = (long long)a.H * D, o_sb = o_st * a.T;
+  CUtensorMap q, o, k, v;
+  auto maps = [&](int q_rows, int k_rows) {
+    return make_map(&q, a.q, a.B, a.T, a.H, D, a.q_sb, a.q_st, a.q_sh, q_rows) &&
+           make_map(&o, a.d_out, a.B, a.T, a.H, D, o_sb, o_st, D, q_rows) &&
+           make_map(&k, a.k, a.B, a.S, a.Hkv, D, a.k_sb, a.k_st, a.k_sh, k_rows) &&
+           make_map(&v, a.v, a.B, a.S, a.Hkv, D, a.v_sb, a.v_st, a.v_sh, k_rows);
+  };
+  cudaError_t e = cudaFuncSetAttribute(attn_dkv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  if (!maps(kN, kM)) return cudaErrorInvalidValue;
+  const long long items = (a.S + kM - 1) / kM + a.n_far;
+  attn_dkv_tc_kernel<D><<<static_cast<unsigned>(items * a.B * a.Hkv), kThreads, L::kBytes, st>>>(q, o, k, v, a);
+  if (!maps(kM, kN)) return cudaErrorInvalidValue;
+  attn_dq_tc_kernel<D><<<static_cast<unsigned>((long long)a.B * a.H * ((a.T + kM - 1) / kM)), kThreads, L::kBytes,
+                         st>>>(q, o, k, v, a);
+  if (a.n_far) attn_sink_join_kernel<D><<<static_cast<unsigned>((long long)a.B * a.Hkv * 2 * a.n_sink), D, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_bwd_tc_workspace(const AttnArgs& in) {
+  AttnArgs a = in;
+  cut_far(a);
+  const size_t rows = align256(static_cast<size_t>(a.B) * a.H * a.Tp * 4);
+  return 2 * rows +
+         (a.n_far ? align256(static_cast<size_t>(a.B) * a.Hkv * (1 + a.n_far) * 2 * a.n_sink * a.d * 4) : 0);
+}
+
+cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st) {
+  cut_far(a);
+  const size_t rows = align256(static_cast<size_t>(a.B) * a.H * a.Tp * 4);
+  char* p = static_cast<char*>(workspace);
+  a.nlse2 = reinterpret_cast<float*>(p);
+  a.delta = reinterpret_cast<float*>(p + rows);
+  a.sink_part = reinterpret_cast<float*>(p + 2 * rows);
+  return a.d == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
+}
+
+}  // namespace dr

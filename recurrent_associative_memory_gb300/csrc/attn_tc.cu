@@ -16,6 +16,9 @@
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
 // The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
 // 0 times whatever stands there may be NaN; scores are masked by selection.
+// This file is compiled as a whole program: with relocatable device code the compiler
+// ignores setmaxnreg, and a row of 128 scores does not fit the registers that an even
+// split leaves (428 bytes of spills per thread instead of 24).
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -320,7 +323,13 @@ bool attn_tc_supported(const AttnArgs& a, int dtype) {
          map_strides_ok(a.B, a.S, a.Hkv, a.v_sb, a.v_st, a.v_sh);
 }
 
-cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st) { return take_status(word, st); }
+// Enqueues the read and the clearing of this translation unit's status word.
+cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st) {
+  static const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+}
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st) {
   return a.d == 64 ? fwd<64>(a, st) : fwd<128>(a, st);

@@ -1,8 +1,5 @@
 // attn_tc.cuh — what the tcgen05 window-attention kernels share: TMEM loads and stores,
 // the MMA with its A operand in TMEM, packed fp32 arithmetic, tile masks, tensor maps.
-// Their translation units are compiled as whole programs: with relocatable device code
-// the compiler ignores setmaxnreg, and a row of 128 scores does not fit the registers
-// that an even split leaves (428 bytes of spills per thread).
 #pragma once
 
 #include "layers.cuh"
@@ -72,6 +69,22 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float m, float a) {
       : "f"(m), "f"(a));
 }
 
+// (x0, x1) * m + (a0, a1) and (x0 + a0, x1 + a1) * (y0, y1), a pair of fp32 at once
+__device__ __forceinline__ void fma2v(float& x0, float& x1, float m, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %4};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(m), "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void add_mul2(float& x0, float& x1, float a0, float a1, float y0, float y1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 z, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, z;\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1), "f"(y0), "f"(y1));
+}
+
 // The key tiles of kM keys that a tile of query rows can see, as a set.
 struct TileSet {
   int n_first, w_begin, w_end;
@@ -110,23 +123,15 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base, int k) {
 
 // ------------------------------------------------------------------ host side
 
-// Enqueues the read and the clearing of this translation unit's status word.
-static inline cudaError_t take_status(int* word, cudaStream_t st) {
-  static const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-}
-
-// [B, rows, heads, d] bf16 with strides in elements; box of 64 channels x kM rows
+// [B, rows, heads, d] bf16 with strides in elements; box of 64 channels x box_rows rows
 inline bool make_map(CUtensorMap* m, const void* ptr, int B, int rows, int heads, int d, long long sb,
-                     long long st, long long sh) {
+                     long long st, long long sh, int box_rows = kM) {
   tc::EncodeTiledFn enc = tc::get_encode();
   if (!enc) return false;
   auto bytes = [](int n, long long s) { return static_cast<cuuint64_t>(n > 1 ? 2 * s : 16); };
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)B};
   cuuint64_t strides[3] = {bytes(heads, sh), bytes(rows, st), bytes(B, sb)};
-  cuuint32_t box[4] = {64, 1, kM, 1};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -283,7 +283,7 @@ int dr_get_device_status(dr_stream_t stream) {
   if (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
       cudaSuccess)
     return DR_ERR_CUDA;
-  int tc = 0;   // whole-program translation units keep their own word
+  int tc = 0;   // the whole-program translation unit keeps its own word
   if (attn_fwd_tc_status(&tc, s) != cudaSuccess) return DR_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return DR_ERR_CUDA;
   return h ? h : tc;

@@ -24,8 +24,14 @@ struct AttnArgs {
   void* dq;
   void* dk;
   void* dv;
-  float* delta;                // [B,H,T] rowsum(dO * O)
-  float* sink_part;            // parts of the sink keys' gradients
+  float* delta;                // fp32: [B,H,T] rowsum(dO * O); bf16: -delta [B,H,Tp]
+  float* nlse2;                // bf16: -lse log2(e) [B,H,Tp], -infinity for rows that see nothing
+  int Tp;                      // T rounded up to 64
+  // bf16: the query rows from far_first on see nothing of key tile 0 but its sinks; their
+  // part of the sinks' gradients is cut into n_far pieces of far_rows rows, which leave
+  // [B,Hkv,1 + n_far][dk, dv][n_sink][d] (piece 0: from the rows before)
+  int far_first, far_rows, n_far;
+  float* sink_part;
 };
 
 __device__ __forceinline__ int real_len(const int* lens, int b, int n) {

@@ -12,6 +12,8 @@ cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 bool attn_tc_supported(const AttnArgs& a, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st);
+size_t attn_bwd_tc_workspace(const AttnArgs& a);
+cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st);
 int attn_step_pieces(const AttnStepArgs& a, int sms);
 cudaError_t launch_attn_step(const AttnStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_fill(const AttnArgs& a, int dtype, void* kc, void* vc, cudaStream_t st);
@@ -28,6 +30,7 @@ cudaError_t launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t st);
 namespace {
 
 constexpr long long kMaxElements = 1LL << 40;   // of one tensor
+constexpr int kMaxPositions = 1 << 30;          // position + window stays an int
 constexpr long long kMaxBlocks = 0x7fffffffLL;  // of one launch
 
 template <typename... P> bool aligned16(const P*... p) {
@@ -69,8 +72,8 @@ bool strides_ok(const dr_attn* a, bool with_q) {
 int check_attn(const dr_attn* a) {
   int st = check_heads(a);
   if (st != DR_OK) return st;
-  if (a->T < 1 || a->S < 1) return DR_ERR_SHAPE;
-  if (a->q_start < 0 || (long long)a->q_start + a->T > INT_MAX) return DR_ERR_ARG;
+  if (a->T < 1 || a->S < 1 || a->S > kMaxPositions) return DR_ERR_SHAPE;
+  if (a->q_start < 0 || (long long)a->q_start + a->T > kMaxPositions) return DR_ERR_ARG;
   const long long rows = (long long)a->B * a->T * a->H, keys = (long long)a->B * a->S * a->Hkv;
   if (rows >= kMaxElements / a->d || keys >= kMaxElements / a->d) return DR_ERR_SHAPE;
   // blocks of the launches: a query tile of 64 rows, a warp per row, a tile of 64 keys
@@ -95,6 +98,8 @@ AttnArgs attn_args(const dr_attn* a) {
 }
 
 size_t attn_bwd_workspace(const dr_attn* a) {
+  const AttnArgs r = attn_args(a);
+  if (attn_tc_supported(r, a->dtype)) return attn_bwd_tc_workspace(r);
   return (static_cast<size_t>(a->B) * a->H * a->T * 4 + 255) & ~size_t(255);
 }
 
@@ -194,6 +199,7 @@ int dr_window_attn_bwd(const dr_attn* a, const void* q, const void* k, const voi
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = const_cast<void*>(out), r.lse = const_cast<float*>(lse);
   r.d_out = d_out, r.dq = dq, r.dk = dk, r.dv = dv;
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_bwd_tc(r, workspace, stream_of(stream)));
   r.delta = static_cast<float*>(workspace);
   return status_of(launch_attn_bwd_simt(r, a->dtype, stream_of(stream)));
 }

@@ -5,10 +5,11 @@
 //
 // Per (token, channel, state): one exponential, two products, two multiply-adds;
 // the exponential units and the issue slots bound it, not the bytes.  N / 4
-// neighbouring lanes own a channel, four states each in registers, and walk the
-// tokens; B_t and C_t are the same for all channels of a group and come from shared
-// memory as broadcast reads.  The lanes' parts of y are summed for N / 4 tokens at
-// once by exchanging halves (N / 4 - 1 shuffles for N / 4 tokens).
+// neighbouring lanes own a pair of channels, four states of each in registers as
+// packed pairs (one instruction for two products), and walk the tokens; B_t and C_t are
+// the same for all channels of a group and come from shared memory as broadcast reads,
+// once for both channels.  The lanes' parts of y are summed for N / 4 tokens at once by
+// exchanging halves (N / 4 - 1 shuffles for N / 4 tokens).
 //
 // Few rows and many tokens are cut into pieces along the tokens: over a piece the
 // state is h_end = exp(A sum dt) h_start + (end from zero), so a first pass takes
@@ -29,20 +30,32 @@
 namespace dr {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 32;     // tokens in shared memory at a time (forward)
-constexpr int kPiece = 64;    // tokens of a backward piece
+constexpr int kPiece = 32;    // tokens of a backward piece
 constexpr int kSub = 8;       // tokens whose states are in registers (backward)
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int N> struct Shape {
-  static constexpr int LPC = N / 4;            // lanes per channel
-  static constexpr int CPC = kThreads / LPC;   // channels per CTA
-  static constexpr int CW = 32 / LPC;          // channels per warp
+  static constexpr int LPC = N / 4;               // lanes per pair of channels
+  static constexpr int CPC = 2 * kThreads / LPC;  // channels per CTA
+  static constexpr int CW = 32 / LPC;             // pairs of channels per warp
+  static constexpr int kTile = N == 8 ? 16 : 32;  // tokens in shared memory at a time (forward)
 };
 
-__device__ __forceinline__ float softplus_f(float v) { return v > 20.f ? v : log1pf(__expf(v)); }
+// log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|).  The alternating series below
+// 1/16 (its sixth term is under 2^-24 of the first), the base-2 logarithm above, where
+// its absolute error of 2^-22 is small against log(17/16).
+__device__ __forceinline__ float softplus_f(float v) {
+  const float e = ex2(-fabsf(v) * kLog2e);
+  float lg;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(1.f + e));
+  float s = fmaf(e, 0.2f, -0.25f);
+  s = fmaf(e, s, 1.f / 3.f);
+  s = fmaf(e, s, -0.5f);
+  s = fmaf(e * e, s, e);
+  return fmaxf(v, 0.f) + (e < 0.0625f ? s : lg * kLn2);
+}
 
 // 8 neighbouring values as loaded
 template <typename T> struct alignas(16) Raw8 { T v[8]; };
@@ -58,6 +71,14 @@ __device__ __forceinline__ void fetch8(Raw8<T>& r, const T* p, int n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.v[i] = i < n ? p[i] : from_f<T>(0.f);
   }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch8(float (&f)[8], const T* p, int n) {
+  Raw8<T> r;
+  fetch8<T, VEC>(r, p, n);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = to_f<T>(r.v[i]);
 }
 
 // Sum over L lanes, STRIDE apart, of M values each: halves are exchanged as long as a
@@ -97,110 +118,172 @@ struct ChannelTile {
   }
 };
 
-template <int N>
-__device__ __forceinline__ void load_rates(const ScanArgs& a, int c, bool real, int part, float (&A)[4]) {
-  const float4 v = real ? *reinterpret_cast<const float4*>(a.A + (long long)c * N + 4 * part)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-  A[0] = v.x, A[1] = v.y, A[2] = v.z, A[3] = v.w;
+// Four states of one channel: two register pairs.
+struct Four { f2 a, b; };
+__device__ __forceinline__ Four load4(const float* p) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  return {v.x, v.y};
+}
+__device__ __forceinline__ void store4(float* p, const Four& v) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v.a, v.b);
+}
+__device__ __forceinline__ Four both(f2 x) { return {x, x}; }
+__device__ __forceinline__ Four mul(const Four& x, const Four& y) { return {mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ Four mul(const Four& x, f2 y) { return {mul2(x.a, y), mul2(x.b, y)}; }
+__device__ __forceinline__ Four fma(const Four& x, const Four& y, const Four& z) {
+  return {fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)};
+}
+__device__ __forceinline__ Four fma(const Four& x, f2 y, const Four& z) {
+  return {fma2(x.a, y, z.a), fma2(x.b, y, z.b)};
+}
+__device__ __forceinline__ Four exp2_4(const Four& x) { return {ex2_2(x.a), ex2_2(x.b)}; }
+// sum over the four of x y
+__device__ __forceinline__ float dot(const Four& x, const Four& y) { return sum2(fma2(x.a, y.a, mul2(x.b, y.b))); }
+
+// dt, dt x of a pair of neighbouring channels, each value twice
+struct Steps { f2 dt[2], dx[2]; };
+__device__ __forceinline__ Steps load_steps(const float2* p) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  return {{pack2(v.x, v.x), pack2(v.z, v.z)}, {pack2(v.y, v.y), pack2(v.w, v.w)}};
 }
 
-__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+// A log2(e) of this lane's four states of its two channels
+template <int N>
+__device__ __forceinline__ void load_rates(const ScanArgs& a, int c, int n, int part, Four (&A2)[2]) {
+  const f2 k = pack2(kLog2e, kLog2e);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    A2[i] = i < n ? mul(load4(a.A + (long long)(c + i) * N + 4 * part), k) : both(0);
 }
+
+__device__ __forceinline__ float bias_of(const ScanArgs& a, int c) { return a.bias ? a.bias[c] : 0.f; }
 
 // ------------------------------------------------------------------ forward
+
+template <int N> constexpr int fwd_floats(bool full) {   // u, (skip, gate), y, B, C, bias and D
+  return Shape<N>::kTile * (Shape<N>::CPC * (full ? 5 : 2) + 2 * N) + 2 * Shape<N>::CPC;
+}
 
 // FULL: outputs from the state at the piece's start; otherwise the piece's end from
 // zero and its sum of dt.
 template <int N, typename T, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, FULL ? 4 : 5) scan_fwd_kernel(ScanArgs a) {
   using S = Shape<N>;
-  constexpr int CPC = S::CPC, LPC = S::LPC;
-  constexpr int NV = (kTile * CPC / 8 + kThreads - 1) / kThreads;   // 8-value loads per thread
-  __shared__ float2 s_u[kTile][CPC];                                // dt, dt x
-  __shared__ float s_y[FULL ? kTile : 1][CPC];
-  __shared__ __align__(16) float s_B[kTile][N], s_C[kTile][N];
-  const int tid = threadIdx.x, lane = tid % 32, part = tid % LPC, ch = tid / LPC;
+  constexpr int CPC = S::CPC, LPC = S::LPC, TT = S::kTile;
+  constexpr int NV = (TT * CPC / 8 + kThreads - 1) / kThreads;   // 8-value loads per thread
+  extern __shared__ __align__(16) float sm[];
+  float* s_B = sm;                                               // [TT][N]
+  float* s_C = s_B + TT * N;
+  float2* s_u = reinterpret_cast<float2*>(s_C + TT * N);         // [TT][CPC] dt, dt x
+  float2* s_par = s_u + TT * CPC;                                // bias, D
+  float2* s_e = s_par + CPC;                                     // D x, silu(z)
+  float* s_y = reinterpret_cast<float*>(s_e + TT * CPC);
+  const int tid = threadIdx.x, lane = tid % 32, part = tid % LPC, ch = 2 * (tid / LPC);
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const ChannelTile ct(a, CPC, blockIdx.x % tiles);
   const int piece = (blockIdx.x / tiles) % a.n_piece, b = blockIdx.x / tiles / a.n_piece;
   const int t_begin = piece * a.piece, t_end = min(a.T, t_begin + a.piece);
   const int len = real_len(a.lens, b, a.T);
-  const bool real = ch < ct.n;
-  const int c = ct.c0 + ch;
+  const int c = ct.c0 + ch, real = ct.n - ch;   // channels of the pair that exist: real > 0, > 1
 
-  float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  Four A2[2], h[2] = {both(0), both(0)};
+  float sum[2] = {0.f, 0.f};
   load_rates<N>(a, c, real, part, A2);
+  if (FULL) {
+    const float* from = a.n_piece > 1 ? a.hs + ((long long)b * a.n_piece + piece) * a.D * N
+                                      : (a.h0 ? a.h0 + (long long)b * a.D * N : nullptr);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
-  if (FULL && real) {
-    if (a.n_piece > 1)
-      load4(a.hs + (((long long)b * a.n_piece + piece) * a.D + c) * N + 4 * part, h);
-    else if (a.h0)
-      load4(a.h0 + ((long long)b * a.D + c) * N + 4 * part, h);
+    for (int i = 0; i < 2; ++i)
+      if (from && i < real) h[i] = load4(from + (long long)(c + i) * N + 4 * part);
   }
 
-  // this thread's loads of a tile: token vt, channels vc .. vc + 7 of the tile
+  for (int e = tid; e < CPC; e += kThreads)
+    s_par[e] = make_float2(e < ct.n ? bias_of(a, ct.c0 + e) : 0.f,
+                           e < ct.n && a.Dskip ? a.Dskip[ct.c0 + e] : 0.f);
+  __syncthreads();
+  // this thread's loads of a tile: token vt, channels vc .. vc + 7 of the tile; B and C
+  constexpr int NB = (TT * N + kThreads - 1) / kThreads;
   Raw8<T> rx[NV], rd[NV], rz[NV];
+  T rB[NB], rC[NB];
   auto fetch = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int e = tid + i * kThreads, t = t0 + e / N, n = e % N;
+      const bool in = e < TT * N && t < min(len, t_end);
+      rB[i] = in ? static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n] : from_f<T>(0.f);
+      if (FULL) rC[i] = in ? static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n] : from_f<T>(0.f);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
-      const int t = t0 + vt, n = vt < kTile && t < t_end ? ct.n - vc : 0;
+      const int t = t0 + vt, n = vt < TT && t < min(len, t_end) ? ct.n - vc : 0;
       fetch8<T, VEC>(rx[i], static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, n);
       fetch8<T, VEC>(rd[i], static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, n);
       if (FULL && a.z)
         fetch8<T, VEC>(rz[i], static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, n);
     }
   };
+  // one token of one channel: (dt, dt x), (D x, gate); nothing of a token that is not there
+  auto stage = [&](float x, float d, float z, bool ok, int k, float& dt, float& dx, float& skip, float& gate) {
+    const float2 par = s_par[k];
+    dt = d + par.x;
+    if (a.softplus) dt = softplus_f(dt);
+    dt = ok ? dt : 0.f;   // the state stays as it is
+    dx = ok ? dt * x : 0.f;
+    skip = par.y * x;
+    gate = a.z ? z * sigmoid_f(z) : 1.f;
+  };
   fetch(t_begin);
-  for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
-    Raw8<T> cx[NV], cz[NV];
+  for (int t0 = t_begin; t0 < t_end; t0 += TT) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
-      if (vt >= kTile) break;
-      const bool in = t0 + vt < min(len, t_end);
+      if (vt >= TT) break;
+      const int n = t0 + vt < min(len, t_end) ? ct.n - vc : 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool ok = in && vc + k < ct.n;
-        float d = ok ? to_f<T>(rd[i].v[k]) + (a.bias ? a.bias[ct.c0 + vc + k] : 0.f) : 0.f;
-        if (a.softplus) d = softplus_f(d);
-        if (!ok) d = 0.f;
-        s_u[vt][vc + k] = make_float2(d, ok ? d * to_f<T>(rx[i].v[k]) : 0.f);
+      for (int k = 0; k < 8; k += 2) {
+        float4 u, e;
+        stage(to_f<T>(rx[i].v[k]), to_f<T>(rd[i].v[k]), to_f<T>(rz[i].v[k]), k < n, vc + k, u.x, u.y, e.x, e.y);
+        stage(to_f<T>(rx[i].v[k + 1]), to_f<T>(rd[i].v[k + 1]), to_f<T>(rz[i].v[k + 1]), k + 1 < n, vc + k + 1, u.z,
+              u.w, e.z, e.w);
+        *reinterpret_cast<float4*>(s_u + vt * CPC + vc + k) = u;
+        if (FULL) *reinterpret_cast<float4*>(s_e + vt * CPC + vc + k) = e;
       }
-      cx[i] = rx[i], cz[i] = rz[i];
     }
-    for (int e = tid; e < kTile * N; e += kThreads) {
-      const int t = t0 + e / N, n = e % N;
-      const bool in = t < t_end;
-      s_B[e / N][n] = in ? to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n]) : 0.f;
-      if (FULL)
-        s_C[e / N][n] = in ? to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int e = tid + i * kThreads;
+      if (e >= TT * N) break;
+      s_B[e] = to_f<T>(rB[i]);
+      if (FULL) s_C[e] = to_f<T>(rC[i]);
     }
     __syncthreads();
-    if (t0 + kTile < t_end) fetch(t0 + kTile);
+    if (t0 + TT < t_end) fetch(t0 + TT);
 #pragma unroll 1
-    for (int g = 0; g < kTile; g += LPC) {
-      float y[LPC];
+    for (int g = 0; g < TT; g += LPC) {
+      float y[2][LPC];
 #pragma unroll
       for (int k = 0; k < LPC; ++k) {
-        const float2 u = s_u[g + k][ch];
-        float B[4], C[4];
-        load4(&s_B[g + k][4 * part], B);
-        if (FULL) load4(&s_C[g + k][4 * part], C);
-        if (!FULL) sum += u.x;
-        y[k] = 0.f;
+        const Steps u = load_steps(s_u + (g + k) * CPC + ch);
+        const Four B = load4(s_B + (g + k) * N + 4 * part);
+        Four C = B;
+        if (FULL) C = load4(s_C + (g + k) * N + 4 * part);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[i] = ex2(u.x * A2[i]) * h[i] + u.y * B[i];
-          if (FULL) y[k] += C[i] * h[i];
+        for (int i = 0; i < 2; ++i) {
+          h[i] = fma(exp2_4(mul(A2[i], u.dt[i])), h[i], mul(B, u.dx[i]));
+          if (FULL) {
+            y[i][k] = dot(C, h[i]);
+          } else {
+            float d, same;
+            unpack2(u.dt[i], d, same);
+            sum[i] += d;
+          }
         }
       }
       if (FULL) {
-        lane_sums<LPC, LPC, 1>(y, lane);
-        s_y[g + part][ch] = y[0];
+        lane_sums<LPC, LPC, 1>(y[0], lane);
+        lane_sums<LPC, LPC, 1>(y[1], lane);
+        *reinterpret_cast<float2*>(s_y + (g + part) * CPC + ch) = make_float2(y[0][0], y[1][0]);
       }
     }
     __syncthreads();
@@ -209,58 +292,76 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a) {
       for (int i = 0; i < NV; ++i) {
         const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
         const int t = t0 + vt;
-        if (vt >= kTile || t >= t_end || vc >= ct.n) break;
+        if (vt >= TT || t >= t_end || vc >= ct.n) break;
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const bool ok = t < len && vc + k < ct.n;
-          o[k] = ok ? s_y[vt][vc + k] + (a.Dskip ? a.Dskip[ct.c0 + vc + k] * to_f<T>(cx[i].v[k]) : 0.f) : 0.f;
-          if (a.z && ok) {
-            const float z = to_f<T>(cz[i].v[k]);
-            o[k] *= z * sigmoid_f(z);
-          }
+          const float2 e = s_e[vt * CPC + vc + k];
+          o[k] = t < len ? (s_y[vt * CPC + vc + k] + e.x) * e.y : 0.f;
         }
         store8<T, VEC>(static_cast<T*>(a.y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, ct.n - vc, o);
       }
+      __syncthreads();   // s_e is written again
     }
   }
-  if (!real) return;
-  const float4 hv = make_float4(h[0], h[1], h[2], h[3]);
-  if (!FULL) {
-    const long long row = ((long long)b * a.n_piece + piece) * a.D + c;
-    *reinterpret_cast<float4*>(a.hs + row * N + 4 * part) = hv;
-    if (part == 0) a.sum_dt[row] = sum;
-  } else if (a.hT && piece == a.n_piece - 1) {
-    *reinterpret_cast<float4*>(a.hT + ((long long)b * a.D + c) * N + 4 * part) = hv;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= real) break;
+    const long long row = ((long long)b * a.n_piece + piece) * a.D + c + i;
+    if (!FULL) {
+      store4(a.hs + row * N + 4 * part, h[i]);
+      if (part == 0) a.sum_dt[row] = sum[i];
+    } else if (a.hT && piece == a.n_piece - 1) {
+      store4(a.hT + ((long long)b * a.D + c + i) * N + 4 * part, h[i]);
+    }
   }
 }
 
 // Joins the pieces: hs becomes the state at each piece's start; BWD: es the gradient
-// at each piece's end, and the gradient of the initial state.
+// at each piece's end, and the gradient of the initial state.  One thread per state;
+// kBatch pieces are loaded ahead of the chain that goes through them.
 template <bool BWD>
 __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
+  constexpr int kBatch = 8;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x, per = (long long)a.D * a.N;
   if (e >= a.B * per) return;
   const long long b = e / per, cn = e % per, c = cn / a.N;
   const float A2 = a.A[cn] * kLog2e;
+  float* hs = a.hs + b * a.n_piece * per + cn;
+  const float* sd = a.sum_dt + b * a.n_piece * a.D + c;
   float h = a.h0 ? a.h0[e] : 0.f;
-#pragma unroll 4
-  for (int p = 0; p < a.n_piece; ++p) {
-    const long long row = b * a.n_piece + p;
-    float* s = a.hs + row * per + cn;
-    const float end = *s;
-    *s = h;
-    h = ex2(A2 * a.sum_dt[row * a.D + c]) * h + end;
+  for (int p0 = 0; p0 < a.n_piece; p0 += kBatch) {
+    float end[kBatch], d[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = p0 + k < a.n_piece;
+      end[k] = in ? hs[(p0 + k) * per] : 0.f;
+      d[k] = in ? sd[(long long)(p0 + k) * a.D] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (p0 + k >= a.n_piece) break;
+      hs[(p0 + k) * per] = h;
+      h = ex2(A2 * d[k]) * h + end[k];
+    }
   }
   if (!BWD) return;
+  float* es = a.es + b * a.n_piece * per + cn;
   float g = a.d_hT ? a.d_hT[e] : 0.f;
-#pragma unroll 4
-  for (int p = a.n_piece - 1; p >= 0; --p) {
-    const long long row = b * a.n_piece + p;
-    float* s = a.es + row * per + cn;
-    const float start = *s;
-    *s = g;
-    g = ex2(A2 * a.sum_dt[row * a.D + c]) * g + start;
+  for (int p0 = a.n_piece - 1; p0 >= 0; p0 -= kBatch) {
+    float start[kBatch], d[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = p0 - k >= 0;
+      start[k] = in ? es[(p0 - k) * per] : 0.f;
+      d[k] = in ? sd[(long long)(p0 - k) * a.D] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (p0 - k < 0) break;
+      es[(p0 - k) * per] = g;
+      g = ex2(A2 * d[k]) * g + start[k];
+    }
   }
   if (a.g.d_init_state) a.g.d_init_state[e] = g;
 }
@@ -273,31 +374,40 @@ __device__ __forceinline__ void load_piece(const ScanArgs& a, const ChannelTile&
                                            float2* s_u, float* s_dy, float* s_B, float* s_C) {
   constexpr int CPC = Shape<N>::CPC;
   const int tid = threadIdx.x;
+  float bias[8];   // of this thread's channels: the same in every round
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int vc = 8 * (tid % (CPC / 8)) + k;
+    bias[k] = vc < ct.n ? bias_of(a, ct.c0 + vc) : 0.f;
+  }
+#pragma unroll 2
   for (int v = tid; v < kPiece * CPC / 8; v += kThreads) {
     const int vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8)), t = t0 + vt;
     const int n = t < len ? ct.n - vc : 0;
-    Raw8<T> rx, rd, rg, rz;
-    fetch8<T, VEC>(rx, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, n);
-    fetch8<T, VEC>(rd, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, n);
-    fetch8<T, VEC>(rg, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, n);
-    if (a.z) fetch8<T, VEC>(rz, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, n);
+    float x[8], d[8], g[8], z[8];
+    fetch8<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, n);
+    fetch8<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, n);
+    fetch8<T, VEC>(g, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, n);
+    if (a.z) fetch8<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, n);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const bool ok = k < n;
-      float d = ok ? to_f<T>(rd.v[k]) + (a.bias ? a.bias[ct.c0 + vc + k] : 0.f) : 0.f;
-      if (a.softplus) d = softplus_f(d);
-      if (!ok) d = 0.f;
-      s_u[vt * CPC + vc + k] = make_float2(d, ok ? d * to_f<T>(rx.v[k]) : 0.f);
-      float g = ok ? to_f<T>(rg.v[k]) : 0.f;
-      if (a.z && ok) {
-        const float z = to_f<T>(rz.v[k]);
-        g *= z * sigmoid_f(z);
-      }
-      s_dy[vt * CPC + vc + k] = g;
+      d[k] += bias[k];
+      if (a.softplus) d[k] = softplus_f(d[k]);
+      d[k] = ok ? d[k] : 0.f;
+      x[k] = ok ? d[k] * x[k] : 0.f;
+      if (a.z) g[k] *= z[k] * sigmoid_f(z[k]);
     }
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      *reinterpret_cast<float4*>(s_u + vt * CPC + vc + k) = make_float4(d[k], x[k], d[k + 1], x[k + 1]);
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+      *reinterpret_cast<float4*>(s_dy + vt * CPC + vc + k) = make_float4(g[k], g[k + 1], g[k + 2], g[k + 3]);
   }
-  for (int e = tid; e < kPiece * N; e += kThreads) {
-    const int t = t0 + e / N, n = e % N;
+#pragma unroll
+  for (int e0 = 0; e0 < kPiece * N; e0 += kThreads) {
+    const int e = e0 + tid, t = t0 + e / N, n = e % N;
     const bool in = t < len;
     s_B[e] = in ? to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n]) : 0.f;
     s_C[e] = in ? to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n]) : 0.f;
@@ -308,9 +418,14 @@ template <int N> constexpr int piece_floats() {   // of load_piece
   return kPiece * (3 * Shape<N>::CPC + 2 * N);
 }
 
+__device__ __forceinline__ void load_dy(const float* p, f2 (&dy)[2]) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  dy[0] = pack2(v.x, v.x), dy[1] = pack2(v.y, v.y);
+}
+
 // A piece's end state from zero, the gradient that reaches its start, its sum of dt.
 template <int N, typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_bwd_ends_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) scan_bwd_ends_kernel(ScanArgs a) {
   using S = Shape<N>;
   constexpr int CPC = S::CPC, LPC = S::LPC;
   extern __shared__ __align__(16) float sm[];
@@ -318,139 +433,147 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_ends_kernel(ScanArgs a) {
   float* s_dy = sm + 2 * kPiece * CPC;
   float* s_B = s_dy + kPiece * CPC;
   float* s_C = s_B + kPiece * N;
-  const int tid = threadIdx.x, part = tid % LPC, ch = tid / LPC;
+  const int tid = threadIdx.x, part = tid % LPC, ch = 2 * (tid / LPC);
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const ChannelTile ct(a, CPC, blockIdx.x % tiles);
   const int piece = (blockIdx.x / tiles) % a.n_piece, b = blockIdx.x / tiles / a.n_piece;
-  const int c = ct.c0 + ch;
-  float A2[4], h[4] = {}, e[4] = {}, cp[4] = {1.f, 1.f, 1.f, 1.f}, sum = 0.f;
-  load_rates<N>(a, c, ch < ct.n, part, A2);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
+  const int c = ct.c0 + ch, real = ct.n - ch;
+  const f2 one = pack2(1.f, 1.f);
+  Four A2[2], h[2] = {both(0), both(0)}, e[2] = {both(0), both(0)}, cp[2] = {both(one), both(one)};
+  float sum[2] = {0.f, 0.f};
+  load_rates<N>(a, c, real, part, A2);
   load_piece<N, T, VEC>(a, ct, b, piece * kPiece, real_len(a.lens, b, a.T), s_u, s_dy, s_B, s_C);
   __syncthreads();
 #pragma unroll 4
   for (int t = 0; t < kPiece; ++t) {
-    const float2 u = s_u[t * CPC + ch];
-    const float dy = s_dy[t * CPC + ch];
-    float B[4], C[4];
-    load4(s_B + t * N + 4 * part, B);
-    load4(s_C + t * N + 4 * part, C);
-    sum += u.x;
+    const Steps u = load_steps(s_u + t * CPC + ch);
+    f2 dy[2];
+    load_dy(s_dy + t * CPC + ch, dy);
+    const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = ex2(u.x * A2[i]);
-      h[i] = x * h[i] + u.y * B[i];
-      cp[i] *= x;
-      e[i] += cp[i] * (C[i] * dy);
+    for (int i = 0; i < 2; ++i) {
+      const Four x = exp2_4(mul(A2[i], u.dt[i]));
+      h[i] = fma(x, h[i], mul(B, u.dx[i]));
+      cp[i] = mul(cp[i], x);
+      e[i] = fma(cp[i], mul(C, dy[i]), e[i]);
+      float d, same;
+      unpack2(u.dt[i], d, same);
+      sum[i] += d;
     }
   }
-  if (ch >= ct.n) return;
-  const long long row = ((long long)b * a.n_piece + piece) * a.D + c;
-  *reinterpret_cast<float4*>(a.hs + row * N + 4 * part) = make_float4(h[0], h[1], h[2], h[3]);
-  *reinterpret_cast<float4*>(a.es + row * N + 4 * part) = make_float4(e[0], e[1], e[2], e[3]);
-  if (part == 0) a.sum_dt[row] = sum;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= real) break;
+    const long long row = ((long long)b * a.n_piece + piece) * a.D + c + i;
+    store4(a.hs + row * N + 4 * part, h[i]);
+    store4(a.es + row * N + 4 * part, e[i]);
+    if (part == 0) a.sum_dt[row] = sum[i];
+  }
 }
 
 template <int N> constexpr int bwd_smem() {
   using S = Shape<N>;
-  return 4 * (piece_floats<N>() + kPiece * S::CPC + kWarps * kSub * 2 * N + 4 * kThreads * (kPiece / kSub));
+  return 4 * (piece_floats<N>() + kPiece * S::CPC + kWarps * kSub * 2 * N + 8 * kThreads * (kPiece / kSub));
 }
 
 template <int N, typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
   using S = Shape<N>;
   constexpr int CPC = S::CPC, LPC = S::LPC, CW = S::CW;
   constexpr int TG = LPC < kSub ? LPC : kSub;   // tokens whose sums over a channel's lanes go together
   extern __shared__ __align__(16) float sm[];
-  float2* s_u = reinterpret_cast<float2*>(sm);         // (dt, dt x), then (sum g B, sum e A)
-  float* s_dy = sm + 2 * kPiece * CPC;
+  float2* s_u = reinterpret_cast<float2*>(sm);         // (dt, dt x), then (dt, sum_n g B)
+  float* s_dy = sm + 2 * kPiece * CPC;                 // dy, then sum_n g a h A
   float* s_B = s_dy + kPiece * CPC;
   float* s_C = s_B + kPiece * N;
-  float* s_y = s_C + kPiece * N;                       // sum_n C h
+  float* s_h = s_C + kPiece * N;                       // states at the sub-tiles' starts
+  float* s_y = s_h + 8 * kThreads * (kPiece / kSub);   // sum_n C h
   float* s_bc = s_y + kPiece * CPC;                    // [warp][kSub][2N] sums over a warp's channels
-  float4* s_h = reinterpret_cast<float4*>(s_bc + kWarps * kSub * 2 * N);   // states at the sub-tiles' starts
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = tid / LPC;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = 2 * (tid / LPC);
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const int tile = blockIdx.x % tiles;
   const ChannelTile ct(a, CPC, tile);
   const int piece = (blockIdx.x / tiles) % a.n_piece, b = blockIdx.x / tiles / a.n_piece;
   const int t0 = piece * kPiece, len = real_len(a.lens, b, a.T);
-  const int c = ct.c0 + ch;
-  const bool real = ch < ct.n;
+  const int c = ct.c0 + ch, real = ct.n - ch;
   const long long row = ((long long)b * a.n_piece + piece) * a.D + c;
-  float A[4], A2[4], h[4] = {}, gc[4] = {}, dA[4] = {};
-  load_rates<N>(a, c, real, part, A);
+  Four A2[2], h[2] = {both(0), both(0)}, gc[2] = {both(0), both(0)}, dA[2] = {both(0), both(0)};
+  load_rates<N>(a, c, real, part, A2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] = A[i] * kLog2e;
-  if (real) {
-    load4(a.hs + row * N + 4 * part, h);
-    load4(a.es + row * N + 4 * part, gc);
-  }
+  for (int i = 0; i < 2; ++i)
+    if (i < real) {
+      h[i] = load4(a.hs + (row + i) * N + 4 * part);
+      gc[i] = load4(a.es + (row + i) * N + 4 * part);
+    }
   load_piece<N, T, VEC>(a, ct, b, t0, len, s_u, s_dy, s_B, s_C);
   __syncthreads();
   // the state at each sub-tile's start
+  float* own = s_h + 4 * tid;   // [sub][channel][thread][4]
   for (int s = 0; s < kPiece / kSub; ++s) {
-    s_h[s * kThreads + tid] = make_float4(h[0], h[1], h[2], h[3]);
+    store4(own + (2 * s) * 4 * kThreads, h[0]);
+    store4(own + (2 * s + 1) * 4 * kThreads, h[1]);
     if (s == kPiece / kSub - 1) break;
 #pragma unroll
     for (int k = 0; k < kSub; ++k) {
       const int t = s * kSub + k;
-      const float2 u = s_u[t * CPC + ch];
-      float B[4];
-      load4(s_B + t * N + 4 * part, B);
+      const Steps u = load_steps(s_u + t * CPC + ch);
+      const Four B = load4(s_B + t * N + 4 * part);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = ex2(u.x * A2[i]) * h[i] + u.y * B[i];
+      for (int i = 0; i < 2; ++i) h[i] = fma(exp2_4(mul(A2[i], u.dt[i])), h[i], mul(B, u.dx[i]));
     }
   }
+#pragma unroll 1
   for (int s = kPiece / kSub - 1; s >= 0; --s) {
-    float hh[kSub + 1][4];   // hh[k]: the state before token k
-    const float4 hv = s_h[s * kThreads + tid];
-    hh[0][0] = hv.x, hh[0][1] = hv.y, hh[0][2] = hv.z, hh[0][3] = hv.w;
+    Four hh[kSub + 1][2];   // hh[k]: the state before token k
+#pragma unroll
+    for (int i = 0; i < 2; ++i) hh[0][i] = load4(own + (2 * s + i) * 4 * kThreads);
 #pragma unroll
     for (int g = 0; g < kSub; g += TG) {
-      float y[TG];
+      float y[2][TG];
 #pragma unroll
       for (int k = 0; k < TG; ++k) {
         const int t = s * kSub + g + k;
-        const float2 u = s_u[t * CPC + ch];
-        float B[4], C[4];
-        load4(s_B + t * N + 4 * part, B);
-        load4(s_C + t * N + 4 * part, C);
-        y[k] = 0.f;
+        const Steps u = load_steps(s_u + t * CPC + ch);
+        const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hh[g + k + 1][i] = ex2(u.x * A2[i]) * hh[g + k][i] + u.y * B[i];
-          y[k] += C[i] * hh[g + k + 1][i];
+        for (int i = 0; i < 2; ++i) {
+          hh[g + k + 1][i] = fma(exp2_4(mul(A2[i], u.dt[i])), hh[g + k][i], mul(B, u.dx[i]));
+          y[i][k] = dot(C, hh[g + k + 1][i]);
         }
       }
-      lane_sums<TG, LPC, 1>(y, lane);
-      s_y[(s * kSub + g + part * TG / LPC) * CPC + ch] = y[0];
+      if (a.z) {
+        lane_sums<TG, LPC, 1>(y[0], lane);
+        lane_sums<TG, LPC, 1>(y[1], lane);
+        *reinterpret_cast<float2*>(s_y + (s * kSub + g + part * TG / LPC) * CPC + ch) =
+            make_float2(y[0][0], y[1][0]);
+      }
     }
     __syncthreads();   // the last sub-tile's s_bc has been read
 #pragma unroll
     for (int g = kSub - TG; g >= 0; g -= TG) {
-      float q[2 * TG];   // token k: sum g B, sum e A
+      float q[2][2 * TG];   // token k: sum g B, sum e A
 #pragma unroll
       for (int k = TG - 1; k >= 0; --k) {
         const int t = s * kSub + g + k;
-        const float2 u = s_u[t * CPC + ch];
-        const float dy = s_dy[t * CPC + ch];
-        float B[4], C[4], v[8];
-        load4(s_B + t * N + 4 * part, B);
-        load4(s_C + t * N + 4 * part, C);
-        q[2 * k] = q[2 * k + 1] = 0.f;
+        const Steps u = load_steps(s_u + t * CPC + ch);
+        f2 dy[2];
+        load_dy(s_dy + t * CPC + ch, dy);
+        const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
+        Four sB = both(0), sC = both(0);   // dB and dC of this lane's channels
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float gi = gc[i] + C[i] * dy;
-          q[2 * k] += gi * B[i];
-          v[i] = gi * u.y;
-          v[4 + i] = hh[g + k + 1][i] * dy;
-          gc[i] = gi * ex2(u.x * A2[i]);
-          const float e = gc[i] * hh[g + k][i];
-          q[2 * k + 1] += e * A[i];
-          dA[i] += e * u.x;
+        for (int i = 0; i < 2; ++i) {
+          const Four gi = fma(C, dy[i], gc[i]);
+          q[i][2 * k] = dot(gi, B);
+          sB = i ? fma(gi, u.dx[i], sB) : mul(gi, u.dx[i]);
+          sC = i ? fma(hh[g + k + 1][i], dy[i], sC) : mul(hh[g + k + 1][i], dy[i]);
+          gc[i] = mul(gi, exp2_4(mul(A2[i], u.dt[i])));
+          const Four e = mul(gc[i], hh[g + k][i]);
+          q[i][2 * k + 1] = dot(e, A2[i]);
+          dA[i] = fma(e, u.dt[i], dA[i]);
         }
+        float v[8];
+        unpack2(sB.a, v[0], v[1]), unpack2(sB.b, v[2], v[3]);
+        unpack2(sC.a, v[4], v[5]), unpack2(sC.b, v[6], v[7]);
         lane_sums<8, CW, LPC>(v, lane);
         float* bc = s_bc + (warp * kSub + g + k) * 2 * N + 4 * part;
         constexpr int PER = 8 / CW > 0 ? 8 / CW : 1;   // values a lane ends with
@@ -460,12 +583,18 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a) {
           bc[(idx / 4) * N + idx % 4] = v[i];
         }
       }
-      lane_sums<2 * TG, LPC, 1>(q, lane);
       constexpr int PER = 2 * TG / LPC;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int idx = part * PER + i;
-        reinterpret_cast<float*>(s_u + (s * kSub + g + idx / 2) * CPC + ch)[idx % 2] = q[i];
+      for (int i = 0; i < 2; ++i) {
+        lane_sums<2 * TG, LPC, 1>(q[i], lane);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int idx = part * PER + k, at = (s * kSub + g + idx / 2) * CPC + ch + i;
+          if (idx % 2 == 0)
+            s_u[at].y = q[i][k];
+          else
+            s_dy[at] = q[i][k] * kLn2;   // A2 carries log2(e)
+        }
       }
     }
     __syncthreads();
@@ -478,35 +607,39 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a) {
       a.part_bc[(((long long)tile * a.B + b) * a.T + t) * 2 * N + e % (2 * N)] = v;
     }
   }
-  if (real)
-    *reinterpret_cast<float4*>(a.hs + row * N + 4 * part) = make_float4(dA[0], dA[1], dA[2], dA[3]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (i < real) store4(a.hs + (row + i) * N + 4 * part, dA[i]);
   // dx, ddt, dz of 8 channels per thread and token; the sums over the piece for dD and d bias
-  float sd[8] = {}, sb[8] = {};
+  float sd[8] = {}, sb[8] = {}, skip[8], bias[8];
   const int vc = 8 * (tid % (CPC / 8)), n = ct.n - vc;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    skip[k] = k < n && a.Dskip ? a.Dskip[ct.c0 + vc + k] : 0.f;
+    bias[k] = k < n ? bias_of(a, ct.c0 + vc + k) : 0.f;
+  }
   for (int vt = tid / (CPC / 8); vt < kPiece; vt += kThreads / (CPC / 8)) {
     const int t = t0 + vt;
     if (t >= a.T || n <= 0) break;
     const int nr = t < len ? n : 0;
     float x[8], d[8], gy[8], z[8], dx[8], ddt[8], dz[8];
-    load8<T, VEC>(static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, nr, x);
-    load8<T, VEC>(static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, nr, d);
-    load8<T, VEC>(static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, nr, gy);
-    if (a.z) load8<T, VEC>(static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, nr, z);
+    fetch8<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, nr);
+    if (a.softplus) fetch8<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, nr);
+    fetch8<T, VEC>(gy, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, nr);
+    if (a.z) fetch8<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, nr);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const bool ok = k < nr;
-      const float2 q = s_u[vt * CPC + vc + k];
-      const float skip = ok && a.Dskip ? a.Dskip[ct.c0 + vc + k] : 0.f;
-      const float raw = d[k] + (ok && a.bias ? a.bias[ct.c0 + vc + k] : 0.f);
-      const float dt = a.softplus ? softplus_f(raw) : raw;
+      const float2 u = s_u[vt * CPC + vc + k];   // dt, sum g B
       float dy = gy[k];
       if (a.z) {
-        const float sg = sigmoid_f(z[k]), y = s_y[vt * CPC + vc + k] + skip * x[k];
+        const float sg = sigmoid_f(z[k]), y = s_y[vt * CPC + vc + k] + skip[k] * x[k];
         dz[k] = ok ? gy[k] * y * sg * (1.f + z[k] * (1.f - sg)) : 0.f;
         dy *= z[k] * sg;
       }
-      dx[k] = ok ? q.x * dt + skip * dy : 0.f;
-      ddt[k] = ok ? (q.y + q.x * x[k]) * (a.softplus ? sigmoid_f(raw) : 1.f) : 0.f;
+      dx[k] = ok ? u.y * u.x + skip[k] * dy : 0.f;
+      ddt[k] = ok ? s_dy[vt * CPC + vc + k] + u.y * x[k] : 0.f;
+      if (a.softplus && ok) ddt[k] *= sigmoid_f(d[k] + bias[k]);
       sd[k] += ok ? dy * x[k] : 0.f;
       sb[k] += ddt[k];
     }
@@ -533,14 +666,16 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a) {
 }
 
 // out[col] = sum of `rows` rows of `cols` values, 8 threads per column
-__global__ void __launch_bounds__(kThreads) column_sum_kernel(const float* in, long long rows, long long cols,
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* in, long long rows, long long cols,
                                                               long long split, float* o0, float* o1) {
   __shared__ float s[8][33];
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
   const long long col = (long long)blockIdx.x * 32 + x;
   float v = 0.f;
-  if (col < cols)
+  if (col < cols) {
+#pragma unroll 4
     for (long long r = y; r < rows; r += 8) v += in[r * cols + col];
+  }
   s[y][x] = v;
   __syncthreads();
   if (y || col >= cols) return;
@@ -578,24 +713,22 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
   const bool real = e < (long long)a.B * a.D * LPC;
   const long long bc = (real ? e : 0) / LPC;
   const int part = e % LPC, c = bc % a.D, b = bc / a.D, g = c / (a.D / a.G);
-  float h[4], A[4];
-  load4(a.h0 + bc * N + 4 * part, h);
-  load4(a.A + (long long)c * N + 4 * part, A);
+  Four h = load4(a.h0 + bc * N + 4 * part);
+  const Four A = load4(a.A + (long long)c * N + 4 * part);
   const T* Bp = static_cast<const T*>(a.Bm) + b * a.B_sb + g * N + 4 * part;
   const T* Cp = static_cast<const T*>(a.Cm) + b * a.C_sb + g * N + 4 * part;
+  const Four B = {pack2(to_f<T>(Bp[0]), to_f<T>(Bp[1])), pack2(to_f<T>(Bp[2]), to_f<T>(Bp[3]))};
+  const Four C = {pack2(to_f<T>(Cp[0]), to_f<T>(Cp[1])), pack2(to_f<T>(Cp[2]), to_f<T>(Cp[3]))};
   const float x = to_f<T>(static_cast<const T*>(a.x)[b * a.x_sb + c]);
-  float dt = to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + (a.bias ? a.bias[c] : 0.f);
+  float dt = to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + bias_of(a, c);
   if (a.softplus) dt = softplus_f(dt);
-  float y = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = ex2(dt * A[i] * kLog2e) * h[i] + dt * x * to_f<T>(Bp[i]);
-    y += to_f<T>(Cp[i]) * h[i];
-  }
+  const float d2 = dt * kLog2e, dx = dt * x;
+  h = fma(exp2_4(mul(A, pack2(d2, d2))), h, mul(B, pack2(dx, dx)));
+  float y = dot(C, h);
 #pragma unroll
   for (int w = LPC / 2; w >= 1; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
   if (!real) return;
-  *reinterpret_cast<float4*>(a.hT + bc * N + 4 * part) = make_float4(h[0], h[1], h[2], h[3]);
+  store4(a.hT + bc * N + 4 * part, h);
   if (part) return;
   if (a.Dskip) y += a.Dskip[c] * x;
   if (a.z) {
@@ -610,38 +743,43 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
 unsigned blocks(long long n) { return static_cast<unsigned>((n + kThreads - 1) / kThreads); }
 
 int tiles_of(int D, int G, int N) {
-  const int cpc = kThreads / (N / 4);
+  const int cpc = 2 * kThreads / (N / 4);
   return G * ((D / G + cpc - 1) / cpc);
+}
+
+template <typename K>
+cudaError_t launch(K kernel, long long grid, int smem, const ScanArgs& a, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <int N, typename T, bool VEC>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((long long)tiles_of(a.D, a.G, N) * a.B * a.n_piece);
+  const long long grid = (long long)tiles_of(a.D, a.G, N) * a.B * a.n_piece;
+  cudaError_t e = cudaSuccess;
   if (a.n_piece > 1) {
-    scan_fwd_kernel<N, T, VEC, false><<<grid, kThreads, 0, st>>>(a);
-    scan_join_kernel<false><<<blocks((long long)a.B * a.D * N), kThreads, 0, st>>>(a);
+    e = launch(scan_fwd_kernel<N, T, VEC, false>, grid, 4 * fwd_floats<N>(false), a, st);
+    if (e == cudaSuccess) e = launch(scan_join_kernel<false>, blocks((long long)a.B * a.D * N), 0, a, st);
   }
-  scan_fwd_kernel<N, T, VEC, true><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return e == cudaSuccess ? launch(scan_fwd_kernel<N, T, VEC, true>, grid, 4 * fwd_floats<N>(true), a, st) : e;
 }
 
 template <int N, typename T, bool VEC>
 cudaError_t bwd(const ScanArgs& a, cudaStream_t st) {
   const int tiles = tiles_of(a.D, a.G, N);
-  const unsigned grid = static_cast<unsigned>((long long)tiles * a.B * a.n_piece);
-  constexpr int smem_ends = 4 * piece_floats<N>(), smem = bwd_smem<N>();
-  cudaError_t e = cudaFuncSetAttribute(scan_bwd_ends_kernel<N, T, VEC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem_ends);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(scan_bwd_kernel<N, T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const long long grid = (long long)tiles * a.B * a.n_piece;
+  cudaError_t e = launch(scan_bwd_ends_kernel<N, T, VEC>, grid, 4 * piece_floats<N>(), a, st);
+  if (e == cudaSuccess) e = launch(scan_join_kernel<true>, blocks((long long)a.B * a.D * N), 0, a, st);
+  if (e == cudaSuccess) e = launch(scan_bwd_kernel<N, T, VEC>, grid, bwd_smem<N>(), a, st);
   if (e != cudaSuccess) return e;
-  scan_bwd_ends_kernel<N, T, VEC><<<grid, kThreads, smem_ends, st>>>(a);
-  scan_join_kernel<true><<<blocks((long long)a.B * a.D * N), kThreads, 0, st>>>(a);
-  scan_bwd_kernel<N, T, VEC><<<grid, kThreads, smem, st>>>(a);
   const long long rows = (long long)a.B * a.n_piece, cols = (long long)a.D * N;
-  column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), kThreads, 0, st>>>(a.hs, rows, cols, cols,
+  column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), 256, 0, st>>>(a.hs, rows, cols, cols,
                                                                                    a.g.dA, nullptr);
-  column_sum_kernel<<<(2 * a.D + 31) / 32, kThreads, 0, st>>>(a.part_d, rows, 2LL * a.D, a.D, a.g.dDskip,
+  column_sum_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(a.part_d, rows, 2LL * a.D, a.D, a.g.dDskip,
                                                               a.g.ddt_bias);
   scan_bc_kernel<T><<<blocks((long long)a.B * a.T * a.G * 2 * N), kThreads, 0, st>>>(a, tiles);
   return cudaGetLastError();
@@ -680,15 +818,17 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
   }                            \
   return cudaErrorInvalidValue;
 
-// Pieces along the tokens: where the rows give fewer than half the SMs a CTA.
+// Pieces along the tokens, each token walked twice: where the rows alone leave the SMs
+// with fewer than two of the up to four CTAs that they hold, cut for four.
 void scan_fwd_pieces(const ScanArgs& a, int sms, int* n_piece, int* piece) {
   const long long rows = (long long)tiles_of(a.D, a.G, a.N) * a.B;
-  long long n = 2LL * sms / rows;
-  const long long most = (a.T + 2 * kTile - 1) / (2 * kTile);
+  const int tile = 32;   // of tokens; pieces are whole tiles
+  long long n = 4LL * sms / rows;
+  const long long most = (a.T + 2 * tile - 1) / (2 * tile);
   if (n > most) n = most;
   *n_piece = 1, *piece = a.T;
-  if (n < 4) return;
-  const long long len = ((a.T + n - 1) / n + kTile - 1) / kTile * kTile;
+  if (n < 3) return;
+  const long long len = ((a.T + n - 1) / n + tile - 1) / tile * tile;
   *piece = static_cast<int>(len);
   *n_piece = static_cast<int>((a.T + len - 1) / len);
 }

@@ -5,6 +5,10 @@
 // what position p sees is exactly the slots 0 .. min(p, n_sink + window - 1): no
 // masks, and no slot that was never written is read.  Bandwidth-bound: both caches
 // are read once, 4 d bytes (bf16) per slot for 4 G d multiply-adds.
+//   bf16  the heads of a group are the rows of warp-level m16n8k16 products (a row of the
+//         tensor cores' 128 would be one in 16 or 32 used): about 8 instructions per slot
+//         where multiply-adds on the CUDA cores take 96 at G = 4
+//   fp32  CUDA cores
 #include "layers.cuh"
 
 namespace dr {
@@ -22,6 +26,7 @@ __device__ __forceinline__ long long slot_of(int p, int n_sink, int window) {
 // slots at once, with a running maximum and sum of its own.
 template <int D, int GB, typename T>
 __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");   // the join waits for this grid's end
   constexpr int LK = D / 8, KPW = 32 / LK, U = 4;
   __shared__ float s_o[kWarps][GB][D], s_m[kWarps][GB], s_l[kWarps][GB];
   const int nb = (a.G + GB - 1) / GB;
@@ -146,14 +151,199 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
   }
 }
 
+// ------------------------------------------------------------------ bf16
+
+constexpr int kMmaThreads = 128;
+constexpr int kMmaWarps = kMmaThreads / 32;
+
+// d (16 x 8) += a (16 x 16) b (16 x 8), bf16
+__device__ __forceinline__ void mma16816(float& d0, float& d1, float& d2, float& d3, uint32_t a0, uint32_t a1,
+                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(d0), "+f"(d1), "+f"(d2), "+f"(d3)
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One CTA per (sequence, key/value head, block of 8 R query heads, piece of the slots);
+// a warp takes 16 slots at a time.  With lane = 4 g + t, a fragment's row or column is g
+// and its pairs along the summed axis belong to t.  That axis may be numbered freely as
+// long as both operands agree, so every operand comes straight from memory in 16-byte
+// pieces:
+//   S = Q K^T    lane (g, t) holds channels 32 s + 8 t .. + 7 of slot g and of head g
+//   O += P V     P is S's own accumulator; lane (g, t) holds channels 64 f + 8 g .. + 7 of
+//                the slots 2t, 2t+1, 2t+8, 2t+9, and product e of a block takes channel e
+//                of each lane's 8
+// R = 1: the rows 8 .. 15 are not there and share two registers that stay 0.
+template <int D, int R>
+__global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_kernel(AttnStepArgs a) {
+  using T = __nv_bfloat16;
+  constexpr int HB = 8 * R, KS = D / 32, VF = D / 64;
+  __shared__ float s_o[kMmaWarps][HB][D], s_m[kMmaWarps][HB], s_l[kMmaWarps][HB];
+  asm volatile("griddepcontrol.launch_dependents;");   // the join waits for this grid's end
+  const int nb = (a.G + HB - 1) / HB;
+  const int piece = blockIdx.x % a.n_piece, hb = (blockIdx.x / a.n_piece) % nb;
+  const int hk = (blockIdx.x / a.n_piece / nb) % a.Hkv, b = blockIdx.x / a.n_piece / nb / a.Hkv;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+  const int h0 = hk * a.G + hb * HB, nh = min(HB, a.G - hb * HB);
+  const int pos = a.pos[b];
+  const int C = a.n_sink + a.window;
+  const int n = pos < 0 ? 0 : min(pos, C - 1) + 1;
+  const int per = (n + a.n_piece - 1) / a.n_piece;
+  const int begin = min(n, piece * per), end = min(n, begin + per);
+  T* kc = static_cast<T*>(a.kc) + ((long long)b * a.Hkv + hk) * C * D;
+  T* vc = static_cast<T*>(a.vc) + ((long long)b * a.Hkv + hk) * C * D;
+  if (n > 0) {   // the new token, written by the CTAs that read its slot
+    const long long s = slot_of(pos, a.n_sink, a.window);
+    if (s >= begin && s < end && threadIdx.x < D) {
+      kc[s * D + threadIdx.x] = static_cast<const T*>(a.k)[((long long)b * a.Hkv + hk) * D + threadIdx.x];
+      vc[s * D + threadIdx.x] = static_cast<const T*>(a.v)[((long long)b * a.Hkv + hk) * D + threadIdx.x];
+    }
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 q[R][KS];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      q[r][s] = g + 8 * r < nh ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                                 ((long long)b * a.H + h0 + g + 8 * r) * D + 32 * s +
+                                                                 8 * t)
+                               : zero;
+  __syncthreads();
+
+  float o[R][VF][8][2], m[R], l[R], z0 = 0.f, z1 = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int f = 0; f < VF; ++f)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[r][f][e][0] = o[r][f][e][1] = 0.f;
+  }
+  const float c2 = a.scale * 1.4426950408889634f;
+  for (int j0 = begin + 16 * warp; j0 < end; j0 += 16 * kMmaWarps) {
+    uint4 k[2][KS], v[VF][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int j = j0 + 8 * u + g;
+        k[u][s] = j < end ? *reinterpret_cast<const uint4*>(kc + (long long)j * D + 32 * s + 8 * t) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int f = 0; f < VF; ++f) {
+        const int j = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
+        v[f][u] = j < end ? *reinterpret_cast<const uint4*>(vc + (long long)j * D + 64 * f + 8 * g) : zero;
+      }
+    float s[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const uint4 q1 = R == 2 ? q[R - 1][i] : zero;
+        mma16816(s[u][0], s[u][1], s[u][2], s[u][3], q[0][i].x, q1.x, q[0][i].y, q1.y, k[u][i].x, k[u][i].y);
+        mma16816(s[u][0], s[u][1], s[u][2], s[u][3], q[0][i].z, q1.z, q[0][i].w, q1.w, k[u][i].z, k[u][i].w);
+      }
+    }
+    uint32_t p[2][2] = {{0u, 0u}, {0u, 0u}};   // [slots 0-7, 8-15][heads 0-7, 8-15]
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float x[4], top = m[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = j0 + 8 * (e >> 1) + 2 * t + (e & 1) < end ? s[e >> 1][2 * r + (e & 1)] * c2 : -INFINITY;
+        top = fmaxf(top, x[e]);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (__any_sync(0xffffffffu, top > m[r])) {
+        const float f = top == -INFINITY ? 1.f : ex2(m[r] - top);
+        m[r] = top;
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < VF; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[r][i][e][0] *= f, o[r][i][e][1] *= f;
+      }
+      const float at = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = ex2(x[e] - at);
+        l[r] += x[e];
+      }
+      p[0][r] = pack_bf16(x[0], x[1]), p[1][r] = pack_bf16(x[2], x[3]);
+    }
+#pragma unroll
+    for (int f = 0; f < VF; ++f)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+        const uint32_t* v0 = &v[f][0].x + e / 2;
+        const uint32_t b0 = __byte_perm(v0[0], v0[4], sel), b1 = __byte_perm(v0[8], v0[12], sel);
+        mma16816(o[0][f][e][0], o[0][f][e][1], R == 2 ? o[R - 1][f][e][0] : z0, R == 2 ? o[R - 1][f][e][1] : z1,
+                 p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (t == 0) s_m[warp][g + 8 * r] = m[r], s_l[warp][g + 8 * r] = l[r];
+#pragma unroll
+    for (int f = 0; f < VF; ++f)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+          *reinterpret_cast<float4*>(&s_o[warp][g + 8 * r][64 * f + 8 * (2 * t + x) + e]) = make_float4(
+              o[r][f][e][x], o[r][f][e + 1][x], o[r][f][e + 2][x], o[r][f][e + 3][x]);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < nh * D; e += kMmaThreads) {
+    const int h = e / D, c = e % D;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kMmaWarps; ++w) mx = fmaxf(mx, s_m[w][h]);
+    const float at = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMmaWarps; ++w) {
+      const float f = ex2(s_m[w][h] - at);
+      sum += s_l[w][h] * f;
+      acc += s_o[w][h][c] * f;
+    }
+    const long long row = (long long)b * a.H + h0 + h;
+    if (a.n_piece == 1) {
+      static_cast<T*>(a.out)[row * D + c] = __float2bfloat16_rn(sum != 0.f ? acc / sum : 0.f);
+    } else {
+      float* part = a.part + (row * a.n_piece + piece) * (D + 2);
+      part[c] = acc;
+      if (c == 0) part[D] = mx, part[D + 1] = sum;
+    }
+  }
+}
+
 // out = sum over the pieces of o exp2(m - max) / sum of l exp2(m - max)
 template <int D, typename T>
 __global__ void __launch_bounds__(D) attn_step_join_kernel(AttnStepArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* p = a.part + (long long)blockIdx.x * a.n_piece * (D + 2);
   float mx = -INFINITY;
+#pragma unroll 8
   for (int i = 0; i < a.n_piece; ++i) mx = fmaxf(mx, p[i * (D + 2) + D]);
   const float at = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f, acc = 0.f;
+#pragma unroll 8
   for (int i = 0; i < a.n_piece; ++i) {
     const float f = ex2(p[i * (D + 2) + D] - at);
     sum += p[i * (D + 2) + D + 1] * f;
@@ -162,21 +352,47 @@ __global__ void __launch_bounds__(D) attn_step_join_kernel(AttnStepArgs a) {
   static_cast<T*>(a.out)[(long long)blockIdx.x * D + threadIdx.x] = from_f<T>(sum != 0.f ? acc / sum : 0.f);
 }
 
-template <int D, int GB, typename T>
-cudaError_t step(const AttnStepArgs& a, cudaStream_t st) {
-  const long long grid = (long long)a.B * a.Hkv * ((a.G + GB - 1) / GB) * a.n_piece;
-  attn_step_simt_kernel<D, GB, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+// The join may be launched while the pieces still run; it waits for them itself.
+template <int D, typename T>
+cudaError_t join(const AttnStepArgs& a, cudaStream_t st) {
+  if (a.n_piece == 1) return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.H));
+  cfg.blockDim = dim3(D);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_piece == 1) return e;
-  attn_step_join_kernel<D, T><<<static_cast<unsigned>(a.B * a.H), D, 0, st>>>(a);
-  return cudaGetLastError();
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, attn_step_join_kernel<D, T>, a) : e;
 }
 
-template <int D, typename T>
-cudaError_t step_heads(const AttnStepArgs& a, cudaStream_t st) {
-  if (a.G == 1) return step<D, 1, T>(a, st);
-  if (a.G == 2) return step<D, 2, T>(a, st);
-  return step<D, 4, T>(a, st);
+template <int D, int GB>
+cudaError_t step(const AttnStepArgs& a, cudaStream_t st) {
+  const long long grid = (long long)a.B * a.Hkv * ((a.G + GB - 1) / GB) * a.n_piece;
+  attn_step_simt_kernel<D, GB, float><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+  return join<D, float>(a, st);
+}
+
+template <int D>
+cudaError_t step_fp32(const AttnStepArgs& a, cudaStream_t st) {
+  if (a.G == 1) return step<D, 1>(a, st);
+  if (a.G == 2) return step<D, 2>(a, st);
+  return step<D, 4>(a, st);
+}
+
+template <int D, int R>
+cudaError_t step_mma(const AttnStepArgs& a, cudaStream_t st) {
+  const long long grid = (long long)a.B * a.Hkv * ((a.G + 8 * R - 1) / (8 * R)) * a.n_piece;
+  attn_step_mma_kernel<D, R><<<static_cast<unsigned>(grid), kMmaThreads, 0, st>>>(a);
+  return join<D, __nv_bfloat16>(a, st);
+}
+
+template <int D>
+cudaError_t step_bf16(const AttnStepArgs& a, cudaStream_t st) {
+  return a.G <= 8 ? step_mma<D, 1>(a, st) : step_mma<D, 2>(a, st);
 }
 
 // Each block copies 8-channel pieces of one slot row per thread.
@@ -204,17 +420,18 @@ __global__ void __launch_bounds__(kThreads) cache_fill_kernel(AttnArgs a, T* kc,
 
 }  // namespace
 
-// Pieces along the slots: as many as fill two CTAs on every SM, of 128 slots at least.
-int attn_step_pieces(const AttnStepArgs& a, int sms) {
-  const long long rows = (long long)a.B * a.Hkv * ((a.G + 3) / 4);
+// Pieces along the slots: as many as fill three CTAs on every SM, of 128 slots at least.
+int attn_step_pieces(const AttnStepArgs& a, int dtype, int sms) {
+  const int heads = dtype == DR_FP32 ? 4 : (a.G <= 8 ? 8 : 16);   // of one CTA
+  const long long rows = (long long)a.B * a.Hkv * ((a.G + heads - 1) / heads);
   const long long most = ((long long)a.n_sink + a.window + 127) / 128;
-  const long long want = 2LL * sms / rows;
+  const long long want = 3LL * sms / rows;
   return static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
 }
 
 cudaError_t launch_attn_step(const AttnStepArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == DR_FP32) return a.d == 64 ? step_heads<64, float>(a, st) : step_heads<128, float>(a, st);
-  return a.d == 64 ? step_heads<64, __nv_bfloat16>(a, st) : step_heads<128, __nv_bfloat16>(a, st);
+  if (dtype == DR_FP32) return a.d == 64 ? step_fp32<64>(a, st) : step_fp32<128>(a, st);
+  return a.d == 64 ? step_bf16<64>(a, st) : step_bf16<128>(a, st);
 }
 
 cudaError_t launch_cache_fill(const AttnArgs& a, int dtype, void* kc, void* vc, cudaStream_t st) {

@@ -179,7 +179,11 @@ __device__ __forceinline__ f2 ex2_2(f2 v) {
   return pack2(ex2(x), ex2(y));
 }
 
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid_f(float x) {   // far below zero: 1 / infinity = 0
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * -1.4426950408889634f)));
+  return r;
+}
 
 // 8 consecutive values <-> fp32; VEC: 16-byte aligned, otherwise value by value
 // up to n of them (the rest are 0 / not stored)

@@ -14,7 +14,7 @@ bool attn_tc_supported(const AttnArgs& a, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st);
 size_t attn_bwd_tc_workspace(const AttnArgs& a);
 cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st);
-int attn_step_pieces(const AttnStepArgs& a, int sms);
+int attn_step_pieces(const AttnStepArgs& a, int dtype, int sms);
 cudaError_t launch_attn_step(const AttnStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_fill(const AttnArgs& a, int dtype, void* kc, void* vc, cudaStream_t st);
 cudaError_t launch_conv_fwd(const ConvArgs& a, int dtype, cudaStream_t st);
@@ -207,7 +207,7 @@ int dr_window_attn_bwd(const dr_attn* a, const void* q, const void* k, const voi
 size_t dr_window_attn_step_workspace_bytes(const dr_attn* a) {
   AttnStepArgs s{};
   if (!a || check_step(a, &s) != DR_OK) return 0;
-  return step_workspace(s, attn_step_pieces(s, sm_count()));
+  return step_workspace(s, attn_step_pieces(s, a->dtype, sm_count()));
 }
 
 int dr_window_attn_step(const dr_attn* a, const void* q, const void* k, const void* v, void* k_cache,
@@ -219,7 +219,7 @@ int dr_window_attn_step(const dr_attn* a, const void* q, const void* k, const vo
   if (st != DR_OK) return st;
   if (!aligned16(q, k, v, k_cache, v_cache, out)) return DR_ERR_ALIGN;
   if (workspace) {
-    s.n_piece = attn_step_pieces(s, sm_count());
+    s.n_piece = attn_step_pieces(s, a->dtype, sm_count());
     if (workspace_bytes < step_workspace(s, s.n_piece)) return DR_ERR_WORKSPACE;
     if (!aligned256(workspace)) return DR_ERR_ALIGN;
   }

@@ -40,7 +40,7 @@ template <int N> struct Shape {
   static constexpr int LPC = N / 4;               // lanes per pair of channels
   static constexpr int CPC = 2 * kThreads / LPC;  // channels per CTA
   static constexpr int CW = 32 / LPC;             // pairs of channels per warp
-  static constexpr int kTile = N == 8 ? 16 : 32;  // tokens in shared memory at a time (forward)
+  static constexpr int kTile = N < 32 ? N : 32;   // tokens in shared memory at a time (forward)
 };
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|).  The alternating series below
@@ -167,7 +167,7 @@ template <int N> constexpr int fwd_floats(bool full) {   // u, (skip, gate), y, 
 // FULL: outputs from the state at the piece's start; otherwise the piece's end from
 // zero and its sum of dt.
 template <int N, typename T, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kThreads, FULL ? 4 : 5) scan_fwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 4 : 5) : 6) scan_fwd_kernel(ScanArgs a) {
   using S = Shape<N>;
   constexpr int CPC = S::CPC, LPC = S::LPC, TT = S::kTile;
   constexpr int NV = (TT * CPC / 8 + kThreads - 1) / kThreads;   // 8-value loads per thread
@@ -317,53 +317,40 @@ __global__ void __launch_bounds__(kThreads, FULL ? 4 : 5) scan_fwd_kernel(ScanAr
   }
 }
 
-// Joins the pieces: hs becomes the state at each piece's start; BWD: es the gradient
-// at each piece's end, and the gradient of the initial state.  One thread per state;
-// kBatch pieces are loaded ahead of the chain that goes through them.
-template <bool BWD>
+// Joins the pieces: hs becomes the state at each piece's start; for the backward, whose
+// blocks are twice as many, es the gradient at each piece's end, and the gradient of the
+// initial state.  One thread per state; kBatch pieces are loaded ahead of the chain that
+// goes through them.
 __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
   constexpr int kBatch = 8;
-  const long long e = (long long)blockIdx.x * kThreads + threadIdx.x, per = (long long)a.D * a.N;
-  if (e >= a.B * per) return;
+  const long long per = (long long)a.D * a.N, all = a.B * per;
+  const unsigned half = static_cast<unsigned>((all + kThreads - 1) / kThreads);
+  const bool back = blockIdx.x >= half;
+  const long long e = (long long)(back ? blockIdx.x - half : blockIdx.x) * kThreads + threadIdx.x;
+  if (e >= all) return;
   const long long b = e / per, cn = e % per, c = cn / a.N;
   const float A2 = a.A[cn] * kLog2e;
-  float* hs = a.hs + b * a.n_piece * per + cn;
+  float* s = (back ? a.es : a.hs) + b * a.n_piece * per + cn;
   const float* sd = a.sum_dt + b * a.n_piece * a.D + c;
-  float h = a.h0 ? a.h0[e] : 0.f;
+  const float* from = back ? a.d_hT : a.h0;
+  float h = from ? from[e] : 0.f;
   for (int p0 = 0; p0 < a.n_piece; p0 += kBatch) {
     float end[kBatch], d[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
+      const int p = back ? a.n_piece - 1 - p0 - k : p0 + k;
       const bool in = p0 + k < a.n_piece;
-      end[k] = in ? hs[(p0 + k) * per] : 0.f;
-      d[k] = in ? sd[(long long)(p0 + k) * a.D] : 0.f;
+      end[k] = in ? s[p * per] : 0.f;
+      d[k] = in ? sd[(long long)p * a.D] : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (p0 + k >= a.n_piece) break;
-      hs[(p0 + k) * per] = h;
+      s[(back ? a.n_piece - 1 - p0 - k : p0 + k) * per] = h;
       h = ex2(A2 * d[k]) * h + end[k];
     }
   }
-  if (!BWD) return;
-  float* es = a.es + b * a.n_piece * per + cn;
-  float g = a.d_hT ? a.d_hT[e] : 0.f;
-  for (int p0 = a.n_piece - 1; p0 >= 0; p0 -= kBatch) {
-    float start[kBatch], d[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const bool in = p0 - k >= 0;
-      start[k] = in ? es[(p0 - k) * per] : 0.f;
-      d[k] = in ? sd[(long long)(p0 - k) * a.D] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (p0 - k < 0) break;
-      es[(p0 - k) * per] = g;
-      g = ex2(A2 * d[k]) * g + start[k];
-    }
-  }
-  if (a.g.d_init_state) a.g.d_init_state[e] = g;
+  if (back && a.g.d_init_state) a.g.d_init_state[e] = h;
 }
 
 // ------------------------------------------------------------------ backward
@@ -665,22 +652,23 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
   }
 }
 
-// out[col] = sum of `rows` rows of `cols` values, 8 threads per column
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* in, long long rows, long long cols,
+// out[col] = sum of `rows` rows of `cols` values, kRowThreads threads per column
+constexpr int kRowThreads = 16;
+__global__ void __launch_bounds__(32 * kRowThreads) column_sum_kernel(const float* in, long long rows, long long cols,
                                                               long long split, float* o0, float* o1) {
-  __shared__ float s[8][33];
+  __shared__ float s[kRowThreads][33];
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
   const long long col = (long long)blockIdx.x * 32 + x;
   float v = 0.f;
   if (col < cols) {
-#pragma unroll 4
-    for (long long r = y; r < rows; r += 8) v += in[r * cols + col];
+#pragma unroll 8
+    for (long long r = y; r < rows; r += kRowThreads) v += in[r * cols + col];
   }
   s[y][x] = v;
   __syncthreads();
   if (y || col >= cols) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += s[i][x];
+  for (int i = 1; i < kRowThreads; ++i) v += s[i][x];
   if (col < split) {
     if (o0) o0[col] = v;
   } else if (o1) {
@@ -763,7 +751,7 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.n_piece > 1) {
     e = launch(scan_fwd_kernel<N, T, VEC, false>, grid, 4 * fwd_floats<N>(false), a, st);
-    if (e == cudaSuccess) e = launch(scan_join_kernel<false>, blocks((long long)a.B * a.D * N), 0, a, st);
+    if (e == cudaSuccess) e = launch(scan_join_kernel, blocks((long long)a.B * a.D * N), 0, a, st);
   }
   return e == cudaSuccess ? launch(scan_fwd_kernel<N, T, VEC, true>, grid, 4 * fwd_floats<N>(true), a, st) : e;
 }
@@ -773,13 +761,13 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st) {
   const int tiles = tiles_of(a.D, a.G, N);
   const long long grid = (long long)tiles * a.B * a.n_piece;
   cudaError_t e = launch(scan_bwd_ends_kernel<N, T, VEC>, grid, 4 * piece_floats<N>(), a, st);
-  if (e == cudaSuccess) e = launch(scan_join_kernel<true>, blocks((long long)a.B * a.D * N), 0, a, st);
+  if (e == cudaSuccess) e = launch(scan_join_kernel, 2LL * blocks((long long)a.B * a.D * N), 0, a, st);
   if (e == cudaSuccess) e = launch(scan_bwd_kernel<N, T, VEC>, grid, bwd_smem<N>(), a, st);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.B * a.n_piece, cols = (long long)a.D * N;
-  column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), 256, 0, st>>>(a.hs, rows, cols, cols,
+  column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), 32 * kRowThreads, 0, st>>>(a.hs, rows, cols, cols,
                                                                                    a.g.dA, nullptr);
-  column_sum_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(a.part_d, rows, 2LL * a.D, a.D, a.g.dDskip,
+  column_sum_kernel<<<(2 * a.D + 31) / 32, 32 * kRowThreads, 0, st>>>(a.part_d, rows, 2LL * a.D, a.D, a.g.dDskip,
                                                               a.g.ddt_bias);
   scan_bc_kernel<T><<<blocks((long long)a.B * a.T * a.G * 2 * N), kThreads, 0, st>>>(a, tiles);
   return cudaGetLastError();

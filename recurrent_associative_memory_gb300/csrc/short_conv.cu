@@ -12,80 +12,76 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRun = 64;          // tokens a thread walks
-constexpr int kAhead = 16;        // tokens whose loads go together (backward: half)
+constexpr int kAhead = 8;         // tokens whose loads go together
 constexpr int kLanes = 32;        // threads along the channels of a CTA (backward)
 constexpr int kRows = kThreads / kLanes;
 
-// CH neighbouring channels as they lie in memory
-template <typename T, int CH> struct alignas(sizeof(T) * CH) Raw { T v[CH]; };
-template <typename T, int CH>
-__device__ __forceinline__ Raw<T, CH> raw_ch(const T* p) {
-  if constexpr (CH == 2 && sizeof(T) == 2) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return *reinterpret_cast<const Raw<T, CH>*>(&u);
-  } else if constexpr (CH == 2) {
-    const float2 u = *reinterpret_cast<const float2*>(p);
-    return {u.x, u.y};
-  } else {
-    return {*p};
-  }
-}
+// CH neighbouring channels as they lie in memory: one access (CH = 2) or a single value
+// (CH = 1).  In registers they are a pair of fp32, the second 0 where CH = 1.
+template <typename T, int CH> struct Raw;
+template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
+template <> struct Raw<__nv_bfloat16, 1> { uint16_t v; };
+template <> struct Raw<float, 2> { f2 v; };
+template <> struct Raw<float, 1> { float v; };
 
-// CH neighbouring channels: one access (CH = 2) or a single value (CH = 1)
 template <typename T, int CH>
-__device__ __forceinline__ void load_ch(const T* p, bool in, float (&f)[CH]) {
-  if constexpr (CH == 1) {
-    f[0] = in ? to_f<T>(*p) : 0.f;
-  } else if constexpr (sizeof(T) == 2) {
-    const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-    f[0] = __uint_as_float(v << 16), f[1] = __uint_as_float(v & 0xFFFF0000u);
-  } else {
-    const float2 v = in ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f);
-    f[0] = v.x, f[1] = v.y;
-  }
+__device__ __forceinline__ Raw<T, CH> raw_ch(const T* p) { return *reinterpret_cast<const Raw<T, CH>*>(p); }
+
+__device__ __forceinline__ f2 pair_of(Raw<__nv_bfloat16, 2> r) {
+  return pack2(__uint_as_float(r.v << 16), __uint_as_float(r.v & 0xFFFF0000u));
+}
+__device__ __forceinline__ f2 pair_of(Raw<__nv_bfloat16, 1> r) { return pack2(__uint_as_float((uint32_t)r.v << 16), 0.f); }
+__device__ __forceinline__ f2 pair_of(Raw<float, 2> r) { return r.v; }
+__device__ __forceinline__ f2 pair_of(Raw<float, 1> r) { return pack2(r.v, 0.f); }
+
+template <typename T, int CH>
+__device__ __forceinline__ f2 load_ch(const T* p, bool in) {
+  return in ? pair_of(raw_ch<T, CH>(p)) : 0ull;
 }
 template <typename T, int CH>
-__device__ __forceinline__ void store_ch(T* p, const float (&f)[CH]) {
-  if constexpr (CH == 1) {
-    *p = from_f<T>(f[0]);
-  } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0], f[1]);
-  } else {
-    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-  }
+__device__ __forceinline__ void store_ch(T* p, f2 v) {
+  float x, y;
+  unpack2(v, x, y);
+  if constexpr (CH == 1)
+    *p = from_f<T>(x);
+  else if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+  else
+    *reinterpret_cast<f2*>(p) = v;
 }
 
 // input t of the sequence, t >= -(K - 1): of the state before the first token
 template <int K, typename T, int CH>
-__device__ __forceinline__ void load_in(const ConvArgs& a, int b, int t, int c, bool in, float (&f)[CH]) {
-  if (t >= 0)
-    load_ch<T, CH>(static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + c, in, f);
-  else
-    load_ch<T, CH>(static_cast<const T*>(a.s0) + ((long long)b * (K - 1) + t + K - 1) * a.D + c, in && a.s0, f);
+__device__ __forceinline__ f2 load_in(const ConvArgs& a, int b, int t, int c) {
+  return t >= 0 ? load_ch<T, CH>(static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + c, true)
+                : load_ch<T, CH>(static_cast<const T*>(a.s0) + ((long long)b * (K - 1) + t + K - 1) * a.D + c,
+                                 a.s0 != nullptr);
 }
 
 template <int K, int CH>
-__device__ __forceinline__ void load_filter(const ConvArgs& a, int c, float (&w)[K][CH], float (&bias)[CH]) {
+__device__ __forceinline__ void load_filter(const ConvArgs& a, int c, f2 (&w)[K], f2& bias) {
+  bias = pack2(a.bias ? a.bias[c] : 0.f, a.bias && CH == 2 ? a.bias[c + 1] : 0.f);
 #pragma unroll
-  for (int v = 0; v < CH; ++v) {
-    bias[v] = a.bias ? a.bias[c + v] : 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j][v] = a.w[(long long)(c + v) * K + j];
-  }
+  for (int j = 0; j < K; ++j)
+    w[j] = pack2(a.w[(long long)c * K + j], CH == 2 ? a.w[(long long)(c + 1) * K + j] : 0.f);
 }
 
 // u of the token whose input is x[K - 1]
-template <int K, int CH>
-__device__ __forceinline__ float filtered(const float (&w)[K][CH], const float (&bias)[CH],
-                                          const float (&x)[K][CH], int v) {
-  float u = bias[v];
+template <int K>
+__device__ __forceinline__ f2 filtered(const f2 (&w)[K], f2 bias, const f2 (&x)[K]) {
+  f2 u = bias;
 #pragma unroll
-  for (int j = 0; j < K; ++j) u += w[j][v] * x[j][v];
+  for (int j = 0; j < K; ++j) u = fma2(w[j], x[j], u);
   return u;
+}
+__device__ __forceinline__ f2 sigmoid2(f2 u) {
+  float x, y;
+  unpack2(u, x, y);
+  return pack2(sigmoid_f(x), sigmoid_f(y));
 }
 
 template <int K, typename T, int CH>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvArgs a) {
   const int groups = a.D / CH, runs = (a.T + kRun - 1) / kRun;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int c = CH * (e % groups);
@@ -93,15 +89,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
   if (r >= (long long)a.B * runs) return;
   const int b = r / runs, t0 = (r % runs) * kRun, last = min(t0 + kRun, a.T);
   const int len = real_len(a.lens, b, a.T), state0 = len - (K - 1);
-  float w[K][CH], bias[CH], x[K][CH];
-  load_filter<K, CH>(a, c, w, bias);
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) {
-    const int t = t0 - (K - 1) + j;
-    load_in<K, T, CH>(a, b, t, c, true, x[j]);
-    if (a.s1 && t < 0 && t >= state0)   // a short sequence keeps some of its initial state
-      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[j]);
-  }
+  f2 w[K], bias, x[K];
   const T* xp = static_cast<const T*>(a.x) + b * a.x_sb + t0 * a.x_st + c;
   T* y = static_cast<T*>(a.y) + ((long long)b * a.T + t0) * a.D + c;
   Raw<T, CH> next[kAhead];
@@ -113,6 +101,14 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
     }
   };
   fetch(t0);
+  load_filter<K, CH>(a, c, w, bias);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    const int t = t0 - (K - 1) + j;
+    x[j] = load_in<K, T, CH>(a, b, t, c);
+    if (a.s1 && t < 0 && t >= state0)   // a short sequence keeps some of its initial state
+      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[j]);
+  }
   for (int tb = t0; tb < last; tb += kAhead) {
     Raw<T, CH> now[kAhead];
 #pragma unroll
@@ -123,22 +119,16 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
     for (int i = 0; i < kAhead; ++i) {
       const int t = tb + i;
       if (!plain && t >= last) break;
-      float u[CH];
-#pragma unroll
-      for (int v = 0; v < CH; ++v) {
-        x[K - 1][v] = to_f<T>(now[i].v[v]);
-        u[v] = filtered<K, CH>(w, bias, x, v);
-        if (a.silu) u[v] *= sigmoid_f(u[v]);
-        if (!plain && t >= len) u[v] = 0.f;
-      }
+      x[K - 1] = pair_of(now[i]);
+      f2 u = filtered<K>(w, bias, x);
+      if (a.silu) u = mul2(u, sigmoid2(u));
+      if (!plain && t >= len) u = 0;
       store_ch<T, CH>(y, u);
       y += a.D;
       if (!plain && a.s1 && t >= state0 && t < len)
         store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[K - 1]);
 #pragma unroll
-      for (int v = 0; v < CH; ++v)
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) x[j][v] = x[j + 1][v];
+      for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1];
     }
   }
 }
@@ -150,87 +140,74 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
 // owns dx of the initial state (t < 0).  A CTA is 32 threads along the channels x 8
 // runs; the runs' sums meet in shared memory and leave as one part per CTA.
 template <int K, typename T, int CH>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
-  __shared__ float s_sum[kRows][K + 1][kLanes * CH];
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
+  __shared__ f2 s_sum[kRows][K + 1][kLanes];
   const int cgs = (a.D + CH * kLanes - 1) / (CH * kLanes);
   const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
   const int c0 = (blockIdx.x % cgs) * CH * kLanes, c = c0 + CH * lane;
   const int blocks = (a.T + kRun * kRows - 1) / (kRun * kRows);
   const int part = blockIdx.x / cgs, b = part / blocks, t0 = (part % blocks) * kRun * kRows + row * kRun;
   const int len = real_len(a.lens, b, a.T);
-  float dw[K + 1][CH];
+  const f2 one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f);
+  f2 dw[K + 1];
 #pragma unroll
-  for (int j = 0; j <= K; ++j)
-#pragma unroll
-    for (int v = 0; v < CH; ++v) dw[j][v] = 0.f;
+  for (int j = 0; j <= K; ++j) dw[j] = 0;
   if (c < a.D && t0 < a.T) {
-    float w[K][CH], bias[CH], x[K][CH], du[K][CH];
-    load_filter<K, CH>(a, c, w, bias);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-      load_in<K, T, CH>(a, b, t0 - (K - 1) + j, c, true, x[j]);
-#pragma unroll
-      for (int v = 0; v < CH; ++v) du[j][v] = 0.f;
-    }
+    f2 w[K], bias, x[K], du[K];
     const int first = t0 == 0 ? -(K - 1) : t0, last = min(t0 + kRun, a.T);   // own dx rows
-    constexpr int A = kAhead / 2;
     const T* xp = static_cast<const T*>(a.x) + b * a.x_sb + t0 * a.x_st + c;
     const T* gp = static_cast<const T*>(a.d_y) + ((long long)b * a.T + t0) * a.D + c;
     T* dx = static_cast<T*>(a.dx) + ((long long)b * a.T + t0 - (K - 1)) * a.D + c;   // of the row that is complete
     const int loads = min(len, last + K - 1);   // du is 0 from len on
-    Raw<T, CH> xn[A], gn[A];
+    Raw<T, CH> xn[kAhead], gn[kAhead];
     auto fetch = [&](int tb) {
 #pragma unroll
-      for (int i = 0; i < A; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         if (tb + i < loads) xn[i] = raw_ch<T, CH>(xp), gn[i] = raw_ch<T, CH>(gp);
         xp += a.x_st, gp += a.D;
       }
     };
     fetch(t0);
-    for (int tb = t0; tb < last + K - 1; tb += A) {
-      Raw<T, CH> xr[A], gr[A];
+    load_filter<K, CH>(a, c, w, bias);
 #pragma unroll
-      for (int i = 0; i < A; ++i) xr[i] = xn[i], gr[i] = gn[i];
-      if (tb + A < last + K - 1) fetch(tb + A);
+    for (int j = 0; j < K - 1; ++j) {
+      x[j] = load_in<K, T, CH>(a, b, t0 - (K - 1) + j, c);
+      du[j] = 0;
+    }
+    for (int tb = t0; tb < last + K - 1; tb += kAhead) {
+      Raw<T, CH> xr[kAhead], gr[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) xr[i] = xn[i], gr[i] = gn[i];
+      if (tb + kAhead < last + K - 1) fetch(tb + kAhead);
       // every token real, within the run, behind its first rows, before the final state's
-      const bool plain = tb + A <= min(last, len) && tb - (K - 1) >= t0 && (!a.d_s1 || tb + A <= len - (K - 1));
+      const bool plain =
+          tb + kAhead <= min(last, len) && tb - (K - 1) >= t0 && (!a.d_s1 || tb + kAhead <= len - (K - 1));
 #pragma unroll
-      for (int i = 0; i < A; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const int t = tb + i;
         if (!plain && t >= last + K - 1) break;
+        const bool in = plain || t < loads;
+        x[K - 1] = in ? pair_of(xr[i]) : 0ull;
+        f2 g = in ? pair_of(gr[i]) : 0ull;
+        if (a.silu) {   // silu'(u) = s (1 + u (1 - s))
+          const f2 u = filtered<K>(w, bias, x), s = sigmoid2(u);
+          g = mul2(g, mul2(s, fma2(u, fma2(s, minus, one), one)));
+        }
+        du[K - 1] = g;
+        if (plain || t < last) {
+          dw[K] = add2(dw[K], g);
 #pragma unroll
-        for (int v = 0; v < CH; ++v) {
-          const bool in = plain || t < loads;
-          x[K - 1][v] = in ? to_f<T>(xr[i].v[v]) : 0.f;
-          float g = in ? to_f<T>(gr[i].v[v]) : 0.f;
-          if (a.silu) {
-            const float u = filtered<K, CH>(w, bias, x, v), s = sigmoid_f(u);
-            g *= s * (1.f + u * (1.f - s));
-          }
-          du[K - 1][v] = g;
-          if (plain || t < last) {
-            dw[K][v] += g;
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][v] += g * x[j][v];
-          }
+          for (int j = 0; j < K; ++j) dw[j] = fma2(g, x[j], dw[j]);
         }
         // du[j] holds du_{t-K+1+j}: row t-K+1 is complete
         const int r = t - (K - 1);
         if (plain || r >= first) {
-          float o[CH];
+          f2 o = mul2(w[K - 1], du[0]);
 #pragma unroll
-          for (int v = 0; v < CH; ++v) {
-            o[v] = 0.f;
-#pragma unroll
-            for (int j = 0; j < K; ++j) o[v] += w[K - 1 - j][v] * du[j][v];
-          }
+          for (int j = 1; j < K; ++j) o = fma2(w[K - 1 - j], du[j], o);
           const int f = r - (len - (K - 1));   // its place in the final state
-          if (!plain && a.d_s1 && f >= 0 && f < K - 1) {
-            float g[CH];
-            load_ch<T, CH>(static_cast<const T*>(a.d_s1) + ((long long)b * (K - 1) + f) * a.D + c, true, g);
-#pragma unroll
-            for (int v = 0; v < CH; ++v) o[v] += g[v];
-          }
+          if (!plain && a.d_s1 && f >= 0 && f < K - 1)
+            o = add2(o, load_ch<T, CH>(static_cast<const T*>(a.d_s1) + ((long long)b * (K - 1) + f) * a.D + c, true));
           if (plain || r >= 0)
             store_ch<T, CH>(dx, o);
           else if (a.d_s0)
@@ -238,24 +215,20 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
         }
         dx += a.D;
 #pragma unroll
-        for (int v = 0; v < CH; ++v)
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) x[j][v] = x[j + 1][v], du[j][v] = du[j + 1][v];
+        for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1], du[j] = du[j + 1];
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j <= K; ++j)
-#pragma unroll
-    for (int v = 0; v < CH; ++v) s_sum[row][j][CH * lane + v] = dw[j][v];
+  for (int j = 0; j <= K; ++j) s_sum[row][j][lane] = dw[j];
   __syncthreads();
-  for (int e = threadIdx.x; e < (K + 1) * CH * kLanes; e += kThreads) {
-    const int j = e / (CH * kLanes), i = e % (CH * kLanes);
-    if (c0 + i >= a.D) continue;
-    float s = 0.f;
+  for (int e = threadIdx.x; e < (K + 1) * kLanes; e += kThreads) {
+    const int j = e / kLanes, i = e % kLanes;
+    if (c0 + CH * i >= a.D) continue;
+    f2 s = 0;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) s += s_sum[r][j][i];
-    a.part[((long long)part * (K + 1) + j) * a.D + c0 + i] = s;
+    for (int r = 0; r < kRows; ++r) s = add2(s, s_sum[r][j][i]);
+    store_ch<float, CH>(a.part + ((long long)part * (K + 1) + j) * a.D + c0 + CH * i, s);
   }
 }
 
@@ -287,15 +260,12 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
   const int c = CH * (e % groups);
   const int b = e / groups;
   if (b >= a.B) return;
-  float w[K][CH], bias[CH], x[K][CH], u[CH];
+  f2 w[K], bias, x[K];
 #pragma unroll
-  for (int j = 0; j < K; ++j) load_in<K, T, CH>(a, b, j - (K - 1), c, true, x[j]);
+  for (int j = 0; j < K; ++j) x[j] = load_in<K, T, CH>(a, b, j - (K - 1), c);
   load_filter<K, CH>(a, c, w, bias);
-#pragma unroll
-  for (int v = 0; v < CH; ++v) {
-    u[v] = filtered<K, CH>(w, bias, x, v);
-    if (a.silu) u[v] *= sigmoid_f(u[v]);
-  }
+  f2 u = filtered<K>(w, bias, x);
+  if (a.silu) u = mul2(u, sigmoid2(u));
   store_ch<T, CH>(static_cast<T*>(a.y) + (long long)b * a.D + c, u);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j)

@@ -21,6 +21,18 @@ __device__ __forceinline__ long long slot_of(int p, int n_sink, int window) {
   return p < n_sink ? p : n_sink + (p - n_sink) % window;
 }
 
+// The parts: o [B,H,pieces][D], then (m, l) [B,H,pieces].
+template <int D>
+__device__ __forceinline__ float2* part_ml(const AttnStepArgs& a) {
+  return reinterpret_cast<float2*>(a.part + (long long)a.B * a.H * a.n_piece * D);
+}
+template <int D>
+__device__ __forceinline__ void put_part(const AttnStepArgs& a, long long row, int piece, int c, float o, float m,
+                                         float l) {
+  a.part[(row * a.n_piece + piece) * D + c] = o;
+  if (c == 0) part_ml<D>(a)[row * a.n_piece + piece] = make_float2(m, l);
+}
+
 // One CTA per (sequence, key/value head, block of GB query heads, piece of the
 // slots).  D / 8 lanes hold a slot's row, 8 channels each, so a warp takes 256 / D
 // slots at once, with a running maximum and sum of its own.
@@ -144,9 +156,7 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
     if (a.n_piece == 1) {
       static_cast<T*>(a.out)[row * D + c] = from_f<T>(sum != 0.f ? acc / sum : 0.f);
     } else {
-      float* p = a.part + (row * a.n_piece + piece) * (D + 2);
-      p[c] = acc;
-      if (c == 0) p[D] = mx, p[D + 1] = sum;
+      put_part<D>(a, row, piece, c, acc, mx, sum);
     }
   }
 }
@@ -228,8 +238,8 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
       for (int e = 0; e < 8; ++e) o[r][f][e][0] = o[r][f][e][1] = 0.f;
   }
   const float c2 = a.scale * 1.4426950408889634f;
-  for (int j0 = begin + 16 * warp; j0 < end; j0 += 16 * kMmaWarps) {
-    uint4 k[2][KS], v[VF][4];
+  uint4 k[2][KS];
+  auto load_k = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -237,6 +247,10 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
         const int j = j0 + 8 * u + g;
         k[u][s] = j < end ? *reinterpret_cast<const uint4*>(kc + (long long)j * D + 32 * s + 8 * t) : zero;
       }
+  };
+  load_k(begin + 16 * warp);
+  for (int j0 = begin + 16 * warp; j0 < end; j0 += 16 * kMmaWarps) {
+    uint4 v[VF][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -255,6 +269,7 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
         mma16816(s[u][0], s[u][1], s[u][2], s[u][3], q[0][i].z, q1.z, q[0][i].w, q1.w, k[u][i].z, k[u][i].w);
       }
     }
+    load_k(j0 + 16 * kMmaWarps);   // on their way while this block's softmax and P V run
     uint32_t p[2][2] = {{0u, 0u}, {0u, 0u}};   // [slots 0-7, 8-15][heads 0-7, 8-15]
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -326,30 +341,46 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
     if (a.n_piece == 1) {
       static_cast<T*>(a.out)[row * D + c] = __float2bfloat16_rn(sum != 0.f ? acc / sum : 0.f);
     } else {
-      float* part = a.part + (row * a.n_piece + piece) * (D + 2);
-      part[c] = acc;
-      if (c == 0) part[D] = mx, part[D + 1] = sum;
+      put_part<D>(a, row, piece, c, acc, mx, sum);
     }
   }
 }
 
-// out = sum over the pieces of o exp2(m - max) / sum of l exp2(m - max)
+// out = sum over the pieces of o exp2(m - max) / sum of l exp2(m - max).  The warps take
+// the pieces in turn, D / 32 channels per lane.
+constexpr int kJoinWarps = 8;
+
 template <int D, typename T>
-__global__ void __launch_bounds__(D) attn_step_join_kernel(AttnStepArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_step_join_kernel(AttnStepArgs a) {
+  constexpr int PER = D / 32;
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float* p = a.part + (long long)blockIdx.x * a.n_piece * (D + 2);
-  float mx = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < a.n_piece; ++i) mx = fmaxf(mx, p[i * (D + 2) + D]);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const float2* ml = part_ml<D>(a) + (long long)blockIdx.x * a.n_piece;
+  const float* o = a.part + (long long)blockIdx.x * a.n_piece * D + lane;
+  float mx = -INFINITY;   // every warp forms it for itself
+  for (int i = lane; i < a.n_piece; i += 32) mx = fmaxf(mx, ml[i].x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
   const float at = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f, acc = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < a.n_piece; ++i) {
-    const float f = ex2(p[i * (D + 2) + D] - at);
-    sum += p[i * (D + 2) + D + 1] * f;
-    acc += p[i * (D + 2) + threadIdx.x] * f;
+  float sum = 0.f, acc[PER] = {};
+#pragma unroll 4
+  for (int i = warp; i < a.n_piece; i += kJoinWarps) {
+    const float2 p = ml[i];
+    const float f = ex2(p.x - at);
+    sum += p.y * f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] += o[(long long)i * D + 32 * c] * f;
   }
-  static_cast<T*>(a.out)[(long long)blockIdx.x * D + threadIdx.x] = from_f<T>(sum != 0.f ? acc / sum : 0.f);
+#pragma unroll
+  for (int c = 0; c < PER; ++c) s_o[warp][lane + 32 * c] = acc[c];
+  if (lane == 0) s_l[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float l = 0.f, x = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l += s_l[w], x += s_o[w][threadIdx.x];
+  static_cast<T*>(a.out)[(long long)blockIdx.x * D + threadIdx.x] = from_f<T>(l != 0.f ? x / l : 0.f);
 }
 
 // The join may be launched while the pieces still run; it waits for them itself.
@@ -358,7 +389,7 @@ cudaError_t join(const AttnStepArgs& a, cudaStream_t st) {
   if (a.n_piece == 1) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.H));
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

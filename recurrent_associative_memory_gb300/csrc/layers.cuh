@@ -83,7 +83,7 @@ struct AttnStepArgs {
   void* vc;
   const int* pos;
   void* out;
-  float* part;                 // [B,H,pieces][d + 2]: o, m, l of each piece
+  float* part;                 // o [B,H,pieces][d], then (m, l) [B,H,pieces]
   int B, H, Hkv, G, d, window, n_sink, n_piece;
   float scale;
 };

@@ -693,37 +693,58 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
 
 // ------------------------------------------------------------------ one token
 
-// Four states per lane as above; the state is read once and written once.
+// Four states per lane as above; the state is read once and written once.  A CTA owns
+// kStepRounds x kThreads / LPC channels of one sequence and one group, all of its states'
+// loads issued before the first is used.
+constexpr int kStepRounds = 4;
+
 template <int N, typename T>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
-  constexpr int LPC = N / 4;
-  const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;   // [B][D][LPC]
-  const bool real = e < (long long)a.B * a.D * LPC;
-  const long long bc = (real ? e : 0) / LPC;
-  const int part = e % LPC, c = bc % a.D, b = bc / a.D, g = c / (a.D / a.G);
-  Four h = load4(a.h0 + bc * N + 4 * part);
-  const Four A = load4(a.A + (long long)c * N + 4 * part);
-  const T* Bp = static_cast<const T*>(a.Bm) + b * a.B_sb + g * N + 4 * part;
-  const T* Cp = static_cast<const T*>(a.Cm) + b * a.C_sb + g * N + 4 * part;
-  const Four B = {pack2(to_f<T>(Bp[0]), to_f<T>(Bp[1])), pack2(to_f<T>(Bp[2]), to_f<T>(Bp[3]))};
-  const Four C = {pack2(to_f<T>(Cp[0]), to_f<T>(Cp[1])), pack2(to_f<T>(Cp[2]), to_f<T>(Cp[3]))};
-  const float x = to_f<T>(static_cast<const T*>(a.x)[b * a.x_sb + c]);
-  float dt = to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + bias_of(a, c);
-  if (a.softplus) dt = softplus_f(dt);
-  const float d2 = dt * kLog2e, dx = dt * x;
-  h = fma(exp2_4(mul(A, pack2(d2, d2))), h, mul(B, pack2(dx, dx)));
-  float y = dot(C, h);
+  constexpr int LPC = N / 4, PER = kThreads / LPC, CPC = kStepRounds * PER;
+  __shared__ __align__(16) float s_B[N], s_C[N];
+  const int tiles = gridDim.x / a.B, b = blockIdx.x / tiles;
+  const ChannelTile ct(a, CPC, blockIdx.x % tiles);
+  const int tid = threadIdx.x, part = tid % LPC;
+  const float* h0 = a.h0 + ((long long)b * a.D + ct.c0) * N;
+  Four h[kStepRounds], A[kStepRounds];
+  float x[kStepRounds], dt[kStepRounds];
 #pragma unroll
-  for (int w = LPC / 2; w >= 1; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-  if (!real) return;
-  store4(a.hT + bc * N + 4 * part, h);
-  if (part) return;
-  if (a.Dskip) y += a.Dskip[c] * x;
-  if (a.z) {
-    const float z = to_f<T>(static_cast<const T*>(a.z)[b * a.z_sb + c]);
-    y *= z * sigmoid_f(z);
+  for (int r = 0; r < kStepRounds; ++r) {
+    const int k = r * PER + tid / LPC, c = ct.c0 + k;
+    const bool real = k < ct.n;
+    h[r] = real ? load4(h0 + k * N + 4 * part) : both(0);
+    A[r] = real ? load4(a.A + (long long)c * N + 4 * part) : both(0);
+    x[r] = real ? to_f<T>(static_cast<const T*>(a.x)[b * a.x_sb + c]) : 0.f;
+    dt[r] = real ? to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + bias_of(a, c) : 0.f;
   }
-  static_cast<T*>(a.y)[bc] = from_f<T>(y);
+  for (int e = tid; e < 2 * N; e += kThreads) {
+    const int n = e % N;
+    if (e < N)
+      s_B[n] = to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + ct.g * N + n]);
+    else
+      s_C[n] = to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + ct.g * N + n]);
+  }
+  __syncthreads();
+  const Four B = load4(s_B + 4 * part), C = load4(s_C + 4 * part);
+  const f2 k2 = pack2(kLog2e, kLog2e);
+#pragma unroll
+  for (int r = 0; r < kStepRounds; ++r) {
+    const int k = r * PER + tid / LPC, c = ct.c0 + k;
+    const float d = a.softplus ? softplus_f(dt[r]) : dt[r], dx = d * x[r];
+    h[r] = fma(exp2_4(mul(mul(A[r], k2), pack2(d, d))), h[r], mul(B, pack2(dx, dx)));
+    float y = dot(C, h[r]);
+#pragma unroll
+    for (int w = LPC / 2; w >= 1; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+    if (k >= ct.n) continue;
+    store4(a.hT + ((long long)b * a.D + c) * N + 4 * part, h[r]);
+    if (part) continue;
+    if (a.Dskip) y += a.Dskip[c] * x[r];
+    if (a.z) {
+      const float z = to_f<T>(static_cast<const T*>(a.z)[b * a.z_sb + c]);
+      y *= z * sigmoid_f(z);
+    }
+    static_cast<T*>(a.y)[(long long)b * a.D + c] = from_f<T>(y);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -775,8 +796,9 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st) {
 
 template <int N, typename T>
 cudaError_t step(const ScanArgs& a, cudaStream_t st) {
-  scan_step_kernel<N, T><<<blocks((long long)a.B * a.D * (N / 4)), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  constexpr int cpc = kStepRounds * kThreads / (N / 4);
+  const long long tiles = (long long)a.G * ((a.D / a.G + cpc - 1) / cpc);
+  return launch(scan_step_kernel<N, T>, tiles * a.B, 0, a, st);
 }
 
 bool vec_ok(const ScanArgs& a, int dtype) {

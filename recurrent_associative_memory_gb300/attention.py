@@ -19,35 +19,34 @@ from __future__ import annotations
 import torch
 
 from . import dr
-from .tensors import activations, check, launch, like_x, scratch, size_of
+from .tensors import activations, call, check, check_rows, ptr, scratch
 
 __all__ = ["window_attn_fwd", "window_attn_bwd", "window_attn_step", "window_cache",
            "window_cache_fill"]
 
 
 def _describe(q, k, v, window, n_sink, q_start, lens, scale):
-    a = dr.DrAttn()
-    a.dtype = activations(q, "q", 4)
-    B, T, H, d = q.shape
+    """The call's dr_attn and its device, its tensors checked."""
+    code, dev = activations(q, "q", 4)
     activations(k, "k", 4)
+    B, T, H, d = q.shape
     S, Hkv = k.shape[1:3]
-    like_x(k, "k", (B, S, Hkv, d), q)
-    like_x(v, "v", (B, S, Hkv, d), q)
-    check(lens, "lens", (B,), torch.int32, q)
-    a.B, a.T, a.S, a.H, a.Hkv, a.d = B, T, S, H, Hkv, d
-    a.window, a.n_sink, a.q_start = window, n_sink, q_start
-    a.scale = 0.0 if scale is None else _positive(scale)
-    a.lens = None if lens is None else lens.data_ptr()
-    a.q_sb, a.q_st, a.q_sh = q.stride()[:3]
-    a.k_sb, a.k_st, a.k_sh = k.stride()[:3]
-    a.v_sb, a.v_st, a.v_sh = v.stride()[:3]
-    return a
+    keys = (B, S, Hkv, d)
+    check_rows(k, "k", keys, q.dtype, dev)
+    check_rows(v, "v", keys, q.dtype, dev)
+    if lens is not None:
+        check(lens, "lens", (B,), torch.int32, dev)
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    return dr.DrAttn(code, B, T, S, H, Hkv, d, window, n_sink, q_start, _scale(scale), ptr(lens),
+                     qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), dev
 
 
-def _positive(scale):
+def _scale(scale):
+    if scale is None:
+        return 0.0   # 1 / sqrt(d)
     if not scale > 0:
         raise ValueError(f"scale must be positive, got {scale}")
-    return float(scale)
+    return scale
 
 
 def window_attn_fwd(q, k, v, window, n_sink=0, *, q_start=0, lens=None, scale=None, want_lse=False,
@@ -57,15 +56,16 @@ def window_attn_fwd(q, k, v, window, n_sink=0, *, q_start=0, lens=None, scale=No
     q [B,T,H,d] stands at positions q_start .. q_start+T-1; k, v [B,S,Hkv,d] at 0 .. S-1.
     They may be slices with any batch, token and head strides of whole 16 bytes.
     ``lens`` int32 [B]: the sequences' real keys.  ``scale``: default 1/sqrt(d)."""
-    a = _describe(q, k, v, window, n_sink, q_start, lens, scale)
+    a, dev = _describe(q, k, v, window, n_sink, q_start, lens, scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(a.B, a.H, a.T, dtype=torch.float32, device=q.device)
-    check(out, "out", q.shape, q.dtype, q)
-    check(lse, "lse", (a.B, a.H, a.T), torch.float32, q)
-    with launch(q, stream) as s:
-        dr.check(dr.dr_window_attn_fwd(a, q, k, v, out, lse, s), "dr_window_attn_fwd")
+        out = q.new_empty(q.shape)
+    else:
+        check(out, "out", q.shape, q.dtype, dev)
+    if lse is not None:
+        check(lse, "lse", (a.B, a.H, a.T), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((a.B, a.H, a.T), dtype=torch.float32)
+    call("dr_window_attn_fwd", dev, stream, dr.dr_window_attn_fwd, a, q, k, v, out, lse)
     return out, lse
 
 
@@ -73,19 +73,19 @@ def window_attn_bwd(q, k, v, out, lse, d_out, window, n_sink=0, *, q_start=0, le
                     workspace="auto", grads=None, stream=None):
     """Returns dict(dq [B,T,H,d], dk, dv [B,S,Hkv,d]) in q's type, from the forward's out
     and lse.  ``grads`` may hold output tensors under these names."""
-    a = _describe(q, k, v, window, n_sink, q_start, lens, scale)
-    check(out, "out", q.shape, q.dtype, q)
-    check(lse, "lse", (a.B, a.H, a.T), torch.float32, q)
-    check(d_out, "d_out", q.shape, q.dtype, q)
+    a, dev = _describe(q, k, v, window, n_sink, q_start, lens, scale)
+    check(out, "out", q.shape, q.dtype, dev)
+    check(lse, "lse", (a.B, a.H, a.T), torch.float32, dev)
+    check(d_out, "d_out", q.shape, q.dtype, dev)
     g = dict(grads or {})
     for name, t in (("dq", q), ("dk", k), ("dv", v)):
         if g.get(name) is None:
-            g[name] = torch.empty(t.shape, dtype=q.dtype, device=q.device)
-        check(g[name], name, t.shape, q.dtype, q)
-    with launch(q, stream) as s:
-        ws = scratch(dr.dr_window_attn_bwd_workspace_bytes(a), q, workspace)
-        dr.check(dr.dr_window_attn_bwd(a, q, k, v, out, lse, d_out, g["dq"], g["dk"], g["dv"], ws,
-                                       size_of(ws), s), "dr_window_attn_bwd")
+            g[name] = q.new_empty(t.shape)
+        else:
+            check(g[name], name, t.shape, q.dtype, dev)
+    ws, n = scratch(dr.dr_window_attn_bwd_workspace_bytes, a, q, dev, workspace)
+    call("dr_window_attn_bwd", dev, stream, dr.dr_window_attn_bwd, a, q, k, v, out, lse, d_out,
+         g["dq"], g["dk"], g["dv"], ws, n)
     return g
 
 
@@ -96,19 +96,17 @@ def window_cache(B, Hkv, d, window, n_sink=0, dtype=torch.bfloat16, device="cuda
                  for _ in range(2))
 
 
-def _cache(k_cache, v_cache, window, n_sink, B, Hkv, d, like):
-    shape = (B, Hkv, n_sink + window, d)
-    check(k_cache, "k_cache", shape, like.dtype, like)
-    check(v_cache, "v_cache", shape, like.dtype, like)
+def _check_cache(k_cache, v_cache, B, Hkv, slots, d, dtype, dev):
+    check(k_cache, "k_cache", (B, Hkv, slots, d), dtype, dev)
+    check(v_cache, "v_cache", (B, Hkv, slots, d), dtype, dev)
 
 
 def window_cache_fill(k, v, k_cache, v_cache, window, n_sink=0, *, lens=None, stream=None):
     """Lays a prompt's k, v [B,S,Hkv,d] out in the caches, for decoding to go on at position
     lens[b] (default S)."""
-    a = _describe(k, k, v, window, n_sink, 0, lens, None)
-    _cache(k_cache, v_cache, window, n_sink, a.B, a.Hkv, a.d, k)
-    with launch(k, stream) as s:
-        dr.check(dr.dr_window_cache_fill(a, k, v, k_cache, v_cache, s), "dr_window_cache_fill")
+    a, dev = _describe(k, k, v, window, n_sink, 0, lens, None)
+    _check_cache(k_cache, v_cache, a.B, a.Hkv, n_sink + window, a.d, k.dtype, dev)
+    call("dr_window_cache_fill", dev, stream, dr.dr_window_cache_fill, a, k, v, k_cache, v_cache)
 
 
 def window_attn_step(q, k, v, k_cache, v_cache, pos, window, n_sink=0, *, scale=None, out=None,
@@ -117,23 +115,21 @@ def window_attn_step(q, k, v, k_cache, v_cache, pos, window, n_sink=0, *, scale=
     device) into the caches and returns out [B,H,d].  A sequence with pos < 0 is left alone
     and gives 0.  ``workspace``: "auto" lets few sequences with a long cache be cut along
     the slots, None runs without one, or a uint8 tensor to reuse."""
-    a = dr.DrAttn()
-    a.dtype = activations(q, "q", 3)
-    B, H, d = q.shape
+    code, dev = activations(q, "q", 3)
     activations(k, "k", 3)
+    B, H, d = q.shape
     Hkv = k.shape[1]
-    check(q, "q", (B, H, d), q.dtype, q)
-    check(k, "k", (B, Hkv, d), q.dtype, q)
-    check(v, "v", (B, Hkv, d), q.dtype, q)
-    check(pos, "pos", (B,), torch.int32, q)
-    _cache(k_cache, v_cache, window, n_sink, B, Hkv, d, q)
-    a.B, a.H, a.Hkv, a.d, a.window, a.n_sink = B, H, Hkv, d, window, n_sink
-    a.scale = 0.0 if scale is None else _positive(scale)
+    check(q, "q", (B, H, d), q.dtype, dev)
+    check(k, "k", (B, Hkv, d), q.dtype, dev)
+    check(v, "v", (B, Hkv, d), q.dtype, dev)
+    check(pos, "pos", (B,), torch.int32, dev)
+    _check_cache(k_cache, v_cache, B, Hkv, n_sink + window, d, q.dtype, dev)
+    a = dr.DrAttn(code, B, 1, 1, H, Hkv, d, window, n_sink, 0, _scale(scale))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    check(out, "out", q.shape, q.dtype, q)
-    with launch(q, stream) as s:
-        ws = scratch(dr.dr_window_attn_step_workspace_bytes(a), q, workspace)
-        dr.check(dr.dr_window_attn_step(a, q, k, v, k_cache, v_cache, pos, out, ws, size_of(ws), s),
-                 "dr_window_attn_step")
+        out = q.new_empty(q.shape)
+    else:
+        check(out, "out", q.shape, q.dtype, dev)
+    ws, n = scratch(dr.dr_window_attn_step_workspace_bytes, a, q, dev, workspace)
+    call("dr_window_attn_step", dev, stream, dr.dr_window_attn_step, a, q, k, v, k_cache, v_cache,
+         pos, out, ws, n)
     return out

@@ -107,9 +107,7 @@ def check(status: int, where: str = "libdr") -> None:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 

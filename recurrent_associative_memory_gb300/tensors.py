@@ -1,7 +1,9 @@
 """Argument checks shared by the layers' Python entry points.
 
 The C entry points check sizes, alignment and scalars, but a pointer says nothing
-about a tensor's device, type or shape: that is checked here, before the call.
+about a tensor's device, type or shape: that is checked here, before the call.  A
+serving step is a few microseconds of GPU work, so a tensor that is as it should be
+costs one short expression, and only a wrong one pays for its message.
 """
 
 from __future__ import annotations
@@ -12,72 +14,90 @@ from . import dr
 
 DTYPES = {torch.float32: dr.DR_FP32, torch.bfloat16: dr.DR_BF16}
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
-def check(t, name, shape, dtype, like, contiguous=True):
-    """``t`` (None passes) must be a tensor of this shape and type on ``like``'s device."""
-    if t is None:
-        return
+
+def _refuse(t, name, shape, dtype, device, contiguous):
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if contiguous and not t.is_contiguous():
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if contiguous:
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must have contiguous channels (last stride 1)")
+
+
+def check(t, name, shape, dtype, device):
+    """``t`` must be a contiguous tensor of this shape and type on CUDA device ``device``."""
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.is_cuda and t.get_device() == device
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device, True)
+
+
+def check_rows(t, name, shape, dtype, device):
+    """As ``check``, but only the last dimension has to be contiguous."""
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.is_cuda and t.get_device() == device
+                and (t.stride(-1) == 1 or t.shape[-1] == 1)):
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device, False)
 
 
 def activations(t, name, dims):
-    """The dr_dtype of a CUDA tensor with ``dims`` dimensions and contiguous channels."""
+    """(dr_dtype, CUDA device) of a tensor with ``dims`` dimensions and contiguous channels."""
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype not in DTYPES:
+    code = DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have contiguous channels (last stride 1)")
-    return DTYPES[t.dtype]
+    return code, t.get_device()
 
 
-def like_x(t, name, shape, x):
-    """``t`` (None passes): x's type and device, this shape, contiguous channels."""
-    if t is None:
-        return
-    check(t, name, shape, x.dtype, x, contiguous=False)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have contiguous channels (last stride 1)")
+def ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-class launch:
-    """The context of one call: its device is current, its stream as in ``dr``."""
-
-    def __init__(self, x, stream):
-        self.device, self.stream = torch.cuda.device(x.device), stream
-
-    def __enter__(self):
-        self.device.__enter__()
-        return torch.cuda.current_stream().cuda_stream if self.stream is None else self.stream
-
-    def __exit__(self, *exc):
-        return self.device.__exit__(*exc)
+def call(name, device, stream, fn, *args):
+    """``fn(*args, stream)`` with ``device`` current, on ``stream`` (None: the current one of
+    that device); raises ``dr.DrError`` for a status other than DR_OK."""
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return call(name, device, stream, fn, *args)
+    status = fn(*args, _current_stream(device) if stream is None else stream)
+    if status:
+        dr.check(status, name)
 
 
-def scratch(n_bytes, x, workspace):
-    """The workspace of a call: "auto" allocates what the call asks for, None goes without
-    one, or a contiguous uint8 tensor on x's device to reuse."""
+def scratch(size_of, description, x, device, workspace):
+    """(tensor or None, bytes) of a call's workspace.  "auto" allocates what ``size_of`` asks
+    for, None goes without one, or a contiguous uint8 tensor on x's device to reuse."""
+    if workspace is None:
+        return None, 0
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a uint8 tensor')
-        return torch.empty(n_bytes, dtype=torch.uint8, device=x.device) if n_bytes else None
-    if workspace is not None:
-        check(workspace, "workspace", workspace.shape, torch.uint8, x)
-    return workspace
-
-
-def size_of(workspace):
-    return 0 if workspace is None else workspace.numel()
+        if device != _current_device():
+            with torch.cuda.device(device):
+                n = size_of(description)
+        else:
+            n = size_of(description)
+        return (x.new_empty(n, dtype=torch.uint8), n) if n else (None, 0)
+    check(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
+    return workspace, workspace.numel()

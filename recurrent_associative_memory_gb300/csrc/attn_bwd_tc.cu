@@ -36,7 +36,7 @@ template <int D> struct Smem {
 };
 
 __device__ __forceinline__ bool bounded(uint64_t* bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, kWaitNs)) return true;
+  if (wait_phase(bar, parity)) return true;
   set_status(DR_ERR_TIMEOUT);
   return false;
 }
@@ -100,44 +100,49 @@ template <int D, bool KV>
 __device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, int n) {
   using L = Smem<D>;
   constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0), ID_ACC = idesc_bf16(kM, D, 0, 1);
-  const uint32_t x = smem_u32(sm + L::oX), y = smem_u32(sm + L::oY), A = smem_u32(sm + L::oA),
-                 B = smem_u32(sm + L::oB), tm = q.tmem;
+  const uint64_t x = desc_kmajor(smem_u32(sm + L::oX)), y = desc_kmajor(smem_u32(sm + L::oY));
+  const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB), tm = q.tmem;
   bool ok = bounded(&q.own, 0);
   for (int i = 0; i < n + 2 && ok; ++i) {
     if (i >= 2) {   // step i - 2: its slot is the one that step i takes
       const int j = i - 2, st = j % kStages, slot = j & 1;
       if (!(ok = bounded(&q.p[slot], (j >> 1) & 1))) break;
       tc_fence_after();
-      if (KV)
+      const uint64_t dA = desc_mnmajor<kN>(A + st * L::kTile), dB = desc_mnmajor<kN>(B + st * L::kTile);
+      if (KV) {
+#pragma unroll
         for (int k = 0; k < kN / 16; ++k)
-          mma_bf16_ta(tm + 256, tm + 128 * slot + 8 * k, desc_mnmajor<kN>(B + st * L::kTile, k), ID_ACC,
-                      j > 0 || k > 0);
+          mma_bf16_ta(tm + 256, tm + 128 * slot + 8 * k, dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+      }
+#pragma unroll
       for (int k = 0; k < kN / 16; ++k)
-        mma_bf16_ta(tm + 256 + D, tm + 128 * slot + 64 + 8 * k, desc_mnmajor<kN>(A + st * L::kTile, k), ID_ACC,
-                    j > 0 || k > 0);
+        mma_bf16_ta(tm + 256 + D, tm + 128 * slot + 64 + 8 * k, dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
       mma_commit(&q.empty[st]);
     }
     if (i < n) {
       const int st = i % kStages, slot = i & 1;
       if (!(ok = bounded(&q.full[st], (i / kStages) & 1))) break;
+      const uint64_t dA = desc_kmajor(A + st * L::kTile), dB = desc_kmajor(B + st * L::kTile);
+#pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_bf16(tm + 128 * slot, desc_kmajor<kM>(x, k), desc_kmajor<kN>(A + st * L::kTile, k), ID_S, k > 0);
+        mma_bf16(tm + 128 * slot, x + step_kmajor<kM>(k), dA + step_kmajor<kN>(k), ID_S, k > 0);
+#pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_bf16(tm + 128 * slot + 64, desc_kmajor<kM>(y, k), desc_kmajor<kN>(B + st * L::kTile, k), ID_S, k > 0);
+        mma_bf16(tm + 128 * slot + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
       mma_commit(&q.s[slot]);
     }
   }
   mma_commit(&q.acc);
   mma_commit(&q.end);   // no MMA may be under way when the CTA ends
-  mbar_wait(&q.end, 0, kWaitNs);
+  wait_phase(&q.end, 0);
   tc_fence_before();
 }
 
 // The load warp gave up or is done: no copy may be in flight when the CTA ends.
 __device__ __forceinline__ void pipe_drain(Pipe& q, int issued) {
-  mbar_wait(&q.own, 0, kWaitNs);
+  wait_phase(&q.own, 0);
   for (int i = max(0, issued - kStages); i < issued; ++i)
-    mbar_wait(&q.full[i % kStages], (i / kStages) & 1, kWaitNs);
+    wait_phase(&q.full[i % kStages], (i / kStages) & 1);
 }
 
 // 128 lanes' rows of D accumulator columns -> bf16 rows (or fp32 parts)

@@ -3,16 +3,18 @@
 // One CTA owns 256 query rows of a head, two tiles of 128, and walks the 128-key tiles
 // that they can see.  Per tile w and key tile n:
 //   S_w = Q_w K_n^T      M = N = 128, K = d     (operands in shared memory, S in TMEM)
-//   P_w = exp2(S c - m)  one thread per row; bf16, written over S in TMEM
+//   P_w = exp2(S c - m)  two threads per row, 64 keys each; bf16, written over S in TMEM
 //   O_w += P_w V_n       M = 128, N = d, K = 128 keys  (A = P from TMEM)
-// The two tiles take turns: while the eight softmax warps (four per tile) work on one,
-// the tensor cores run the other's P V and next S.  The running maximum m is only
+// The two tiles take turns: while the eight softmax warps of one work, the tensor cores run
+// the other's P V and next S.  S and P V of a tile wait for each other, so a turn is the
+// softmax's latency plus two products: two threads per row (a barrier for the common
+// maximum between them) halve that latency against one.  The running maximum m is only
 // raised when it would grow by more than 2^8 (P stays far below bf16's and fp32's
 // range, and the final division takes any m), so O is rarely rescaled; S of tile n is
 // issued behind P V of tile n - 1, so a thread that has S may touch O.
-//   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
-//   warp 8          TMA: K and V tiles, two slots each (d = 64: four)
-//   warp 9          one lane issues every MMA
+//   warps 0-7, 8-15  softmax and epilogue of the tiles 0 and 1
+//   warp 16          TMA: K and V tiles, two slots each (d = 64: four)
+//   warp 17          one lane issues every MMA
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
 // The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
 // 0 times whatever stands there may be NaN; scores are masked by selection.
@@ -28,10 +30,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 384;   // three warpgroups; the third has two idle warps
-// registers per thread after the split: 2 x 216 + 72 = 3 x 168, what the launch takes
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
+constexpr int kThreads = 640;   // five warpgroups; the last has two idle warps
+// registers per thread after the split: 4 x 104 + 64 = 5 x 96, what the launch takes
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSoftmaxRegs + kOtherRegs == 5 * kLaunchRegs, "a larger sum would wait for ever");
+constexpr int kLoadWarp = 16, kMmaWarp = 17;
 constexpr float kRaise = 8.f;   // log2 of the growth of P that is let through
 
 template <int D> struct Smem {
@@ -53,12 +56,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t b_q, b_kf[NS], b_ke[NS], b_vf[NS], b_ve[NS], b_fix, b_s[2], b_p[2], b_o[2], b_end;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
+  __shared__ float s_row[2][2][kM];   // [tile][half of the keys][row]: maximum, at the end the sum
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + 2 * kM - 1) / (2 * kM);
   // heads of a group are neighbours: they read the same K and V
   const int h = blockIdx.x % a.H, i0 = (blockIdx.x / a.H) % n_block * 2 * kM, b = blockIdx.x / a.H / n_block;
-  const int hk = h / a.G, len = real_len(a.lens, b, a.S);
+  const int hk = h / a.G, len = uniform(real_len(a.lens, b, a.S));
   const TileSet set0(a, i0, len), set1(a, i0 + kM, len);
   const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + 2 * kM, a.T) - 1, len, a.window, a.n_sink, kM);
   // a tile outside every row's window is there for its sinks only
@@ -70,53 +74,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b_kf[i], 1), mbar_init(&b_ke[i], 1), mbar_init(&b_vf[i], 1), mbar_init(&b_ve[i], 1);
     mbar_init(&b_fix, 1);
     mbar_init(&b_end, 1);
-    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 128), mbar_init(&b_o[w], 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 256), mbar_init(&b_o[w], 1);
     fence_mbar_init();
     s_abort = 0;
   }
-  if (warp == 9) tmem_alloc(&s_tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uniform(s_tmem);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity, kWaitNs)) return true;
+    if (wait_phase(bar, parity)) return true;
     s_abort = 1;
     set_status(DR_ERR_TIMEOUT);
     return false;
   };
 
-  if (warp < 8) {   // ---------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + w * kM + row, p = a.q_start + i;
+  if (warp < 16) {   // --------------------------------------------------------- softmax
+    more_registers<kSoftmaxRegs>();
+    const int w = warp / 8, half = warp / 4 % 2;
+    const int row = (warp % 4) * 32 + lane, i = i0 + w * kM + row, p = a.q_start + i;
     const TileSet& set = w ? set1 : set0;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + lanes;
+    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + half * (D / 2) + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
     uint32_t phase = 0;
     bool any = false, ok = true;
     const int p0 = a.q_start + i0 + w * kM, p1 = p0 + kM - 1;
 
-    auto one_tile = [&](auto nch, int j0) {   // nch.value blocks of 32 columns
-      constexpr int NC = decltype(nch)::value;
-      float s[32 * NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+    auto one_tile = [&](auto cols, int j0) {   // this thread's half of 2 cols.value keys from j0
+      constexpr int NC = decltype(cols)::value;
+      const int k0 = j0 + half * NC;
+      float s[NC];
+      if constexpr (NC == 64) {
+        tmem_ld32(tS + half * NC, reinterpret_cast<uint32_t*>(s));
+        tmem_ld32(tS + half * NC + 32, reinterpret_cast<uint32_t*>(s) + 32);
+      } else {
+        tmem_ld16(tS + half * NC, s);
+      }
       tmem_ld_wait();
-      const bool whole = j0 + 32 * NC - 1 <= p0 && j0 + 32 * NC <= len && p1 - j0 < a.window;
+      const bool whole = k0 + NC - 1 <= p0 && k0 + NC <= len && p1 - k0 < a.window;
       if (!whole) {
-        const RowMask mask(a, p, j0, len);
+        const RowMask mask(a, p, k0, len);
 #pragma unroll
-        for (int c = 0; c < 32 * NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
+        for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < 32 * NC; c += 4)
+      for (int c = 4; c + 8 <= NC; c += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
+      const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      s_row[w][half][row] = mine;
+      // behind this barrier both halves of S are in registers: P may go over them
+      named_barrier(1 + w, 256);
+      const float top = fmaxf(mine, s_row[w][half ^ 1][row]);
       float f = 1.f;
       if (m == -INFINITY) {
         m = top;                                  // nothing summed so far
@@ -127,44 +143,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any && __any_sync(0xffffffffu, f != 1.f)) {
         l *= f;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + c, o);
+        for (int c = 0; c < D / 2; c += 16) {
+          float o[16];
+          tmem_ld16(tO + c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32(tO + c, o);
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tmem_st16(tO + c, reinterpret_cast<uint32_t*>(o));
         }
       }
       const float at = m == -INFINITY ? 0.f : -m * c2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      f2 sum[2] = {0, 0};
+      const f2 cc = pack2(c2, c2), aa = pack2(at, at);
 #pragma unroll
-      for (int c0 = 0; c0 < 32 * NC; c0 += 32) {
-        uint32_t pk[16];
+      for (int c0 = 0; c0 < NC; c0 += 16) {
+        uint32_t pk[8];
 #pragma unroll
-        for (int c = c0; c < c0 + 32; c += 2) {
-          fma2(s[c], s[c + 1], c2, at);
-          s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
-          sum[c & 2] += s[c], sum[(c & 2) + 1] += s[c + 1];
-          pk[(c - c0) / 2] = tc::pack_bf16(s[c], s[c + 1]);
+        for (int c = 0; c < 16; c += 2) {
+          const f2 e = ex2_2(dr::fma2(pack2(s[c0 + c], s[c0 + c + 1]), cc, aa));
+          sum[c / 2 % 2] = add2(sum[c / 2 % 2], e);
+          float x, y;
+          unpack2(e, x, y);
+          pk[c / 2] = tc::pack_bf16(x, y);
         }
-        tmem_st16(tS + c0 / 2, pk);
+        tmem_st8(tS + half * (NC / 2) + c0 / 2, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += sum2(add2(sum[0], sum[1]));
     };
 
-    for (int n = 0; n < tiles.n && ok; ++n) {
+    for (int n = 0; n < tiles.n; ++n) {
       const int tile = tiles[n];
       if (!set.has(tile)) continue;
-      ok = wait(&b_s[w], phase);
+      if (ok) ok = wait(&b_s[w], phase);
       ok = __all_sync(0xffffffffu, ok);   // the warp's TMEM accesses are collective
-      if (!ok) break;
       phase ^= 1;
+      if (!ok) {   // goes on to every barrier, so that no other warp is left waiting
+        named_barrier(1 + w, 256);
+        mbar_arrive(&b_p[w]);
+        continue;
+      }
       tc_fence_after();
       if (sinks_only(tile))
-        one_tile(std::integral_constant<int, 1>{}, tile * kM);
+        one_tile(std::integral_constant<int, 16>{}, tile * kM);
       else
-        one_tile(std::integral_constant<int, 4>{}, tile * kM);
+        one_tile(std::integral_constant<int, 64>{}, tile * kM);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&b_p[w]);
@@ -175,11 +197,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
+    // the rows' sums
+    named_barrier(1 + w, 256);
+    s_row[w][half][row] = l;
+    named_barrier(1 + w, 256);
+    l += s_row[w][half ^ 1][row];
     if (ok && i0 + w * kM < a.T) {
       const float f = l != 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.T + i) * a.H + h) * D;
+      __nv_bfloat16* o =
+          static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.T + i) * a.H + h) * D + half * (D / 2);
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t v[32];
         if (any) {
           tmem_ld32(tO + c, v);
@@ -198,15 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (a.lse && i < a.T)
+      if (a.lse && half == 0 && i < a.T)
         a.lse[((long long)b * a.H + h) * a.T + i] =
             l != 0.f ? m * a.scale + logf(l) : -INFINITY;
     }
     tc_fence_before();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    fewer_registers<kOtherRegs>();
   }
-  if (warp == 8) {   // ------------------------------------------------------------- loads
+  if (warp == kLoadWarp) {   // ------------------------------------------------------------- loads
     const int fix_tile = len < a.S && len % kM ? len / kM : -1;   // its V rows from len on become 0
     int kn = 0, vn = 0, n_fix = 0;                                // tiles whose loads are under way
     if (lane == 0 && tiles.n > 0) {
@@ -251,52 +279,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       vn = n + 1;
     }
     if (!ok || s_abort) {   // no copy may be in flight when the CTA ends
-      if (tiles.n > 0) mbar_wait(&b_q, 0, kWaitNs);
-      for (int n = max(0, kn - NS); n < kn; ++n) mbar_wait(&b_kf[n % NS], (n / NS) & 1, kWaitNs);
-      for (int n = max(0, vn - NS); n < vn; ++n) mbar_wait(&b_vf[n % NS], (n / NS) & 1, kWaitNs);
+      if (tiles.n > 0) wait_phase(&b_q, 0);
+      for (int n = max(0, kn - NS); n < kn; ++n) wait_phase(&b_kf[n % NS], (n / NS) & 1);
+      for (int n = max(0, vn - NS); n < vn; ++n) wait_phase(&b_vf[n % NS], (n / NS) & 1);
     }
-  } else if (warp == 9 && lane == 0 && tiles.n > 0) {   // --------------------------- MMAs
-    const uint32_t q0 = smem_u32(sm + L::oQ), k0 = smem_u32(sm + L::oK), v0 = smem_u32(sm + L::oV);
+  } else if (warp == kMmaWarp && tiles.n > 0) {   // ---------------------------------- MMAs
+    // the whole warp walks the loop, one lane issues
+    const uint64_t q0 = desc_kmajor(smem_u32(sm + L::oQ)), k0 = desc_kmajor(smem_u32(sm + L::oK));
+    const uint64_t v0 = desc_mnmajor<kM>(smem_u32(sm + L::oV));
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     int pend[2] = {-1, -1};       // the key tile whose P V is still to come
     uint32_t np[2] = {0, 0};
-    bool ok = wait(&b_q, 0);
+    bool ok = all_wait(&b_q, 0);
     for (int n = 0; n <= tiles.n && ok; ++n) {
       const int slot = n % NS;
-      if (n < tiles.n) ok = wait(&b_kf[slot], (n / NS) & 1);
-      if (n > 0 && ok) ok = wait(&b_vf[(n - 1) % NS], ((n - 1) / NS) & 1);
-      for (int w = 0; w < 2 && ok; ++w) {
+      if (n < tiles.n) ok = all_wait(&b_kf[slot], (n / NS) & 1);
+      if (n > 0 && ok) ok = all_wait(&b_vf[(n - 1) % NS], ((n - 1) / NS) & 1);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!ok) break;
+        const uint32_t o = tmem + 256 + w * D, s = tmem + w * 128;
         if (pend[w] >= 0) {
-          if (!(ok = wait(&b_p[w], np[w] & 1))) break;
+          if (!(ok = all_wait(&b_p[w], np[w] & 1))) break;
           tc_fence_after();
-          const int steps = sinks_only(tiles[pend[w]]) ? 2 : kM / 16;
-          const uint32_t v = v0 + (pend[w] % NS) * L::kTile;
-          for (int k = 0; k < steps; ++k)
-            mma_bf16_ta(tmem + 256 + w * D, tmem + w * 128 + 8 * k, desc_mnmajor<kM>(v, k), ID_O,
-                        np[w] > 0 || k > 0);
+          const uint64_t v = v0 + (pend[w] % NS) * (L::kTile >> 4);
+          if (elect_one()) {
+            mma_bf16_ta(o, s, v, ID_O, np[w] > 0);
+            mma_bf16_ta(o, s + 8, v + step_mnmajor(1), ID_O, true);
+            if (!sinks_only(tiles[pend[w]])) {
+#pragma unroll
+              for (int k = 2; k < kM / 16; ++k) mma_bf16_ta(o, s + 8 * k, v + step_mnmajor(k), ID_O, true);
+            }
+          }
           ++np[w];
           pend[w] = -1;
         }
         if (n < tiles.n && (w ? set1 : set0).has(tiles[n])) {
           const uint32_t id = sinks_only(tiles[n]) ? ID_S32 : ID_S;
-          for (int k = 0; k < D / 16; ++k)
-            mma_bf16(tmem + w * 128, desc_kmajor<kM>(q0 + w * L::kTile, k), desc_kmajor<kM>(k0 + slot * L::kTile, k),
-                     id, k > 0);
-          mma_commit(&b_s[w]);
+          const uint64_t q = q0 + w * (L::kTile >> 4), k = k0 + slot * (L::kTile >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e)
+              mma_bf16(s, q + step_kmajor<kM>(e), k + step_kmajor<kM>(e), id, e > 0);
+            mma_commit(&b_s[w]);
+          }
           pend[w] = n;
         }
-        if (n == tiles.n) mma_commit(&b_o[w]);
+        if (n == tiles.n && elect_one()) mma_commit(&b_o[w]);
       }
       if (!ok) break;
-      if (n < tiles.n) mma_commit(&b_ke[slot]);
-      if (n > 0) mma_commit(&b_ve[(n - 1) % NS]);
+      if (elect_one()) {
+        if (n < tiles.n) mma_commit(&b_ke[slot]);
+        if (n > 0) mma_commit(&b_ve[(n - 1) % NS]);
+      }
     }
-    mma_commit(&b_end);           // no MMA may be under way when the CTA ends
-    mbar_wait(&b_end, 0, kWaitNs);
+    __syncwarp();
+    if (elect_one()) mma_commit(&b_end);   // no MMA may be under way when the CTA ends
+    wait_phase(&b_end, 0);
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int D>

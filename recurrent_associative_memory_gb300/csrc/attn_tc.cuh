@@ -13,6 +13,36 @@ using namespace umma;
 constexpr uint64_t kWaitNs = 2000000000ull;   // a wait gives up after this long
 constexpr int kM = 128;                       // rows of a tile, on either axis
 
+// Bounded wait.  The global timer is only read every 256 polls: sixteen warps that read it
+// at every poll slow the one that issues the MMAs.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitNs) return false;
+    }
+  }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The same value in every lane, known as such to the compiler: an MMA's descriptors, built
+// from such values under uniform control flow, stay in uniform registers, where the
+// instruction wants them.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // D(tmem) (+)= A(tmem) * B(smem desc): row r of A in lane r, two bf16 per column
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             bool accumulate) {
@@ -56,6 +86,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -110,15 +146,34 @@ struct RowMask {
   __device__ __forceinline__ bool sees(int c) const { return c <= hi && (c >= lo || c < sink); }
 };
 
-// K-major operand of `rows` rows in 64-column blocks: the descriptor at k-step `k` (16 columns)
-template <int ROWS>
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t base, int k) {
-  return desc_sw128(base + (k >> 2) * (ROWS * 128) + (k & 3) * 32, 0, 1024);
+// Operands in shared memory: a descriptor at the tile's start, plus a constant per k-step of
+// 16.  One thread issues every MMA, so what it computes for each is on the critical path.
+//   K-major: ROWS rows in blocks of 64 columns;  MN-major: the ROWS rows are the k axis
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t base) { return desc_sw128(base, 0, 1024); }
+template <int ROWS> __host__ __device__ constexpr uint32_t step_kmajor(int k) {
+  return ((k >> 2) * (ROWS * 128) + (k & 3) * 32) >> 4;
 }
-// MN-major operand whose `ROWS` rows are the k axis: the descriptor at k-step `k` (16 rows)
-template <int ROWS>
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base, int k) {
-  return desc_sw128(base + k * 2048, ROWS * 128, 1024);
+template <int ROWS> __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base) {
+  return desc_sw128(base, ROWS * 128, 1024);
+}
+__host__ __device__ constexpr uint32_t step_mnmajor(int k) { return (k * 2048) >> 4; }
+
+// the largest of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <uint32_t REGS> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <uint32_t REGS> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 // ------------------------------------------------------------------ host side

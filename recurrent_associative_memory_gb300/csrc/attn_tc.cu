@@ -3,18 +3,20 @@
 // One CTA owns 256 query rows of a head, two tiles of 128, and walks the 128-key tiles
 // that they can see.  Per tile w and key tile n:
 //   S_w = Q_w K_n^T      M = N = 128, K = d     (operands in shared memory, S in TMEM)
-//   P_w = exp2(S c - m)  two threads per row, 64 keys each; bf16, written over S in TMEM
+//   P_w = exp2(S c - m)  one thread per row; bf16, written over S in TMEM
 //   O_w += P_w V_n       M = 128, N = d, K = 128 keys  (A = P from TMEM)
-// The two tiles take turns: while the eight softmax warps of one work, the tensor cores run
-// the other's P V and next S.  S and P V of a tile wait for each other, so a turn is the
-// softmax's latency plus two products: two threads per row (a barrier for the common
-// maximum between them) halve that latency against one.  The running maximum m is only
-// raised when it would grow by more than 2^8 (P stays far below bf16's and fp32's
-// range, and the final division takes any m), so O is rarely rescaled; S of tile n is
-// issued behind P V of tile n - 1, so a thread that has S may touch O.
-//   warps 0-7, 8-15  softmax and epilogue of the tiles 0 and 1
-//   warp 16          TMA: K and V tiles, two slots each (d = 64: four)
-//   warp 17          one lane issues every MMA
+// The two tiles take turns: while the four softmax warps of one work, the tensor cores run
+// the other's P V and next S.  S and P V of a tile wait for each other, so a step is the
+// longer of four products (2048 cycles at d = 128) and the softmax's latency plus two.
+// The running maximum m is only raised when it would grow by more than 2^8 (P stays far
+// below bf16's and fp32's range, and the final division takes any m), so O is rarely
+// rescaled; S of tile n is issued behind P V of tile n - 1, so a thread that has S may
+// touch O.
+//   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
+//   warp 8          TMA: K and V tiles, two slots each (d = 64: four)
+//   warp 9          the MMAs: the warp walks its loop together and one lane issues (issued
+//                   under a branch on the lane, an MMA takes 51 cycles instead of 14, its
+//                   descriptors going through vector registers)
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
 // The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
 // 0 times whatever stands there may be NaN; scores are masked by selection.
@@ -30,11 +32,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 640;   // five warpgroups; the last has two idle warps
-// registers per thread after the split: 4 x 104 + 64 = 5 x 96, what the launch takes
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
-static_assert(4 * kSoftmaxRegs + kOtherRegs == 5 * kLaunchRegs, "a larger sum would wait for ever");
-constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 384;   // three warpgroups; the third has two idle warps
+// registers per thread after the split: 2 x 208 + 88 = 3 x 168, what the launch takes
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kRaise = 8.f;   // log2 of the growth of P that is let through
 
 template <int D> struct Smem {
@@ -56,7 +58,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t b_q, b_kf[NS], b_ke[NS], b_vf[NS], b_ve[NS], b_fix, b_s[2], b_p[2], b_o[2], b_end;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ float s_row[2][2][kM];   // [tile][half of the keys][row]: maximum, at the end the sum
 
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + 2 * kM - 1) / (2 * kM);
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b_kf[i], 1), mbar_init(&b_ke[i], 1), mbar_init(&b_vf[i], 1), mbar_init(&b_ve[i], 1);
     mbar_init(&b_fix, 1);
     mbar_init(&b_end, 1);
-    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 256), mbar_init(&b_o[w], 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 128), mbar_init(&b_o[w], 1);
     fence_mbar_init();
     s_abort = 0;
   }
@@ -91,33 +92,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  if (warp < 16) {   // --------------------------------------------------------- softmax
+  if (warp < 8) {   // ---------------------------------------------------------- softmax
     more_registers<kSoftmaxRegs>();
-    const int w = warp / 8, half = warp / 4 % 2;
-    const int row = (warp % 4) * 32 + lane, i = i0 + w * kM + row, p = a.q_start + i;
+    const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + w * kM + row, p = a.q_start + i;
     const TileSet& set = w ? set1 : set0;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + half * (D / 2) + lanes;
+    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
     uint32_t phase = 0;
     bool any = false, ok = true;
     const int p0 = a.q_start + i0 + w * kM, p1 = p0 + kM - 1;
 
-    auto one_tile = [&](auto cols, int j0) {   // this thread's half of 2 cols.value keys from j0
+    auto one_tile = [&](auto cols, int j0) {   // cols.value keys from j0
       constexpr int NC = decltype(cols)::value;
-      const int k0 = j0 + half * NC;
       float s[NC];
-      if constexpr (NC == 64) {
-        tmem_ld32(tS + half * NC, reinterpret_cast<uint32_t*>(s));
-        tmem_ld32(tS + half * NC + 32, reinterpret_cast<uint32_t*>(s) + 32);
-      } else {
-        tmem_ld16(tS + half * NC, s);
-      }
+#pragma unroll
+      for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
       tmem_ld_wait();
-      const bool whole = k0 + NC - 1 <= p0 && k0 + NC <= len && p1 - k0 < a.window;
+      const bool whole = j0 + NC - 1 <= p0 && j0 + NC <= len && p1 - j0 < a.window;
       if (!whole) {
-        const RowMask mask(a, p, k0, len);
+        const RowMask mask(a, p, j0, len);
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
       }
@@ -126,13 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 4; c + 8 <= NC; c += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
-      const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      s_row[w][half][row] = mine;
-      // behind this barrier both halves of S are in registers: P may go over them
-      named_barrier(1 + w, 256);
-      const float top = fmaxf(mine, s_row[w][half ^ 1][row]);
+      const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[NC - 4], s[NC - 3], s[NC - 2]), s[NC - 1], m));
       float f = 1.f;
       if (m == -INFINITY) {
         m = top;                                  // nothing summed so far
@@ -143,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any && __any_sync(0xffffffffu, f != 1.f)) {
         l *= f;
 #pragma unroll
-        for (int c = 0; c < D / 2; c += 16) {
+        for (int c = 0; c < D; c += 16) {
           float o[16];
           tmem_ld16(tO + c, o);
           tmem_ld_wait();
@@ -156,37 +145,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       f2 sum[2] = {0, 0};
       const f2 cc = pack2(c2, c2), aa = pack2(at, at);
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += 16) {
-        uint32_t pk[8];
+      for (int c0 = 0; c0 < NC; c0 += 32) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
+        for (int c = 0; c < 32; c += 2) {
           const f2 e = ex2_2(dr::fma2(pack2(s[c0 + c], s[c0 + c + 1]), cc, aa));
           sum[c / 2 % 2] = add2(sum[c / 2 % 2], e);
           float x, y;
           unpack2(e, x, y);
           pk[c / 2] = tc::pack_bf16(x, y);
         }
-        tmem_st8(tS + half * (NC / 2) + c0 / 2, pk);
+        tmem_st16(tS + c0 / 2, pk);
       }
       l += sum2(add2(sum[0], sum[1]));
     };
 
-    for (int n = 0; n < tiles.n; ++n) {
+    for (int n = 0; n < tiles.n && ok; ++n) {
       const int tile = tiles[n];
       if (!set.has(tile)) continue;
-      if (ok) ok = wait(&b_s[w], phase);
+      ok = wait(&b_s[w], phase);
       ok = __all_sync(0xffffffffu, ok);   // the warp's TMEM accesses are collective
+      if (!ok) break;
       phase ^= 1;
-      if (!ok) {   // goes on to every barrier, so that no other warp is left waiting
-        named_barrier(1 + w, 256);
-        mbar_arrive(&b_p[w]);
-        continue;
-      }
       tc_fence_after();
       if (sinks_only(tile))
-        one_tile(std::integral_constant<int, 16>{}, tile * kM);
+        one_tile(std::integral_constant<int, 32>{}, tile * kM);
       else
-        one_tile(std::integral_constant<int, 64>{}, tile * kM);
+        one_tile(std::integral_constant<int, 128>{}, tile * kM);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&b_p[w]);
@@ -197,17 +182,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
-    // the rows' sums
-    named_barrier(1 + w, 256);
-    s_row[w][half][row] = l;
-    named_barrier(1 + w, 256);
-    l += s_row[w][half ^ 1][row];
     if (ok && i0 + w * kM < a.T) {
       const float f = l != 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* o =
-          static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.T + i) * a.H + h) * D + half * (D / 2);
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.T + i) * a.H + h) * D;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
         if (any) {
           tmem_ld32(tO + c, v);
@@ -226,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (a.lse && half == 0 && i < a.T)
+      if (a.lse && i < a.T)
         a.lse[((long long)b * a.H + h) * a.T + i] =
             l != 0.f ? m * a.scale + logf(l) : -INFINITY;
     }
@@ -293,8 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = all_wait(&b_q, 0);
     for (int n = 0; n <= tiles.n && ok; ++n) {
       const int slot = n % NS;
-      if (n < tiles.n) ok = all_wait(&b_kf[slot], (n / NS) & 1);
-      if (n > 0 && ok) ok = all_wait(&b_vf[(n - 1) % NS], ((n - 1) / NS) & 1);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!ok) break;
@@ -314,7 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++np[w];
           pend[w] = -1;
         }
-        if (n < tiles.n && (w ? set1 : set0).has(tiles[n])) {
+        // between two batches of MMAs at most one wait: the queue holds eight, 512 cycles
+        if (w == 0 && n < tiles.n) ok = all_wait(&b_kf[slot], (n / NS) & 1);
+        if (w == 1 && n < tiles.n && ok) ok = all_wait(&b_vf[slot], (n / NS) & 1);   // for the next step
+        if (ok && n < tiles.n && (w ? set1 : set0).has(tiles[n])) {
           const uint32_t id = sinks_only(tiles[n]) ? ID_S32 : ID_S;
           const uint64_t q = q0 + w * (L::kTile >> 4), k = k0 + slot * (L::kTile >> 4);
           if (elect_one()) {

@@ -8,15 +8,20 @@
 // The two tiles take turns: while the four softmax warps of one work, the tensor cores run
 // the other's P V and next S.  S and P V of a tile wait for each other, so a step is the
 // longer of four products (2048 cycles at d = 128) and the softmax's latency plus two.
-// The running maximum m is only raised when it would grow by more than 2^8 (P stays far
-// below bf16's and fp32's range, and the final division takes any m), so O is rarely
-// rescaled; S of tile n is issued behind P V of tile n - 1, so a thread that has S may
-// touch O.
+// To keep that latency short, a tile's exponentials take the maximum m of the tiles before
+// it, so that they need not wait for its own: any m is right as long as nothing overflows
+// (the final division takes it out), and P up to 2^64 is far inside the range of bf16 and
+// fp32.  A tile that goes further (the first always does) is taken again with its own
+// maximum.  m is raised, and O rescaled, where it is 2^8 behind; S of tile n is issued
+// behind P V of tile n - 1, so a thread that has S may touch O.
 //   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
 //   warp 8          TMA: K and V tiles, two slots each (d = 64: four)
-//   warp 9          the MMAs: the warp walks its loop together and one lane issues (issued
-//                   under a branch on the lane, an MMA takes 51 cycles instead of 14, its
-//                   descriptors going through vector registers)
+//   warps 9, 10     the MMAs of the tiles 0 and 1: a warp walks its loop together and one
+//                   lane issues.  (Issued under a branch on the lane, an MMA takes 51
+//                   cycles instead of 14, its descriptors going through vector registers;
+//                   one warp for both tiles spends 2300 cycles of a step on its waits.)
+//                   They issue P V and the next S of their tile in turns: interleaved, both
+//                   tiles would finish together and their softmax would run at the same time.
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
 // The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
 // 0 times whatever stands there may be NaN; scores are masked by selection.
@@ -32,12 +37,13 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 384;   // three warpgroups; the third has two idle warps
+constexpr int kThreads = 384;   // three warpgroups; the third has an idle warp
 // registers per thread after the split: 2 x 208 + 88 = 3 x 168, what the launch takes
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr float kRaise = 8.f;   // log2 of the growth of P that is let through
+constexpr int kLoadWarp = 8, kMmaWarp = 9;   // and the one after it
+constexpr float kRaise = 8.f;    // log2 of P above which m is raised for the tiles to come
+constexpr float kAgain = 64.f;   // and above which this tile is taken again
 
 template <int D> struct Smem {
   static constexpr int kTile = kM * D * 2;                  // bytes of 128 rows
@@ -55,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t ID_O = idesc_bf16(128, D, 0, 1);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t b_q, b_kf[NS], b_ke[NS], b_vf[NS], b_ve[NS], b_fix, b_s[2], b_p[2], b_o[2], b_end;
+  __shared__ uint64_t b_q, b_kf[NS], b_ke[NS], b_vf[NS], b_ve[NS], b_fix, b_s[2], b_p[2], b_o[2], b_end[2], b_turn[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
 
@@ -72,11 +78,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&b_q, 1);
     for (int i = 0; i < NS; ++i)
-      mbar_init(&b_kf[i], 1), mbar_init(&b_ke[i], 1), mbar_init(&b_vf[i], 1), mbar_init(&b_ve[i], 1);
+      mbar_init(&b_kf[i], 1), mbar_init(&b_ke[i], 2), mbar_init(&b_vf[i], 1), mbar_init(&b_ve[i], 2);
     mbar_init(&b_fix, 1);
-    mbar_init(&b_end, 1);
-    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 128), mbar_init(&b_o[w], 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&b_s[w], 1), mbar_init(&b_p[w], 128), mbar_init(&b_o[w], 1), mbar_init(&b_end[w], 1), mbar_init(&b_turn[w], 1);
     fence_mbar_init();
+    mbar_arrive(&b_turn[0]);   // tile 0 goes first
     s_abort = 0;
   }
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, 512);
@@ -104,60 +110,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool any = false, ok = true;
     const int p0 = a.q_start + i0 + w * kM, p1 = p0 + kM - 1;
 
+    float top = -INFINITY;   // the largest score so far
+    // l and O to the maximum of the rows whose `to` is above their m
+    auto raise = [&](bool mine) {
+      const float f = mine && m != -INFINITY ? ex2((m - top) * c2) : 1.f;
+      if (mine) m = top;
+      l *= f;
+      if (!any) return;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        tmem_ld16(tO + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= f;
+        tmem_st16(tO + c, reinterpret_cast<uint32_t*>(o));
+      }
+    };
+
     auto one_tile = [&](auto cols, int j0) {   // cols.value keys from j0
       constexpr int NC = decltype(cols)::value;
-      float s[NC];
-#pragma unroll
-      for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
-      tmem_ld_wait();
       const bool whole = j0 + NC - 1 <= p0 && j0 + NC <= len && p1 - j0 < a.window;
-      if (!whole) {
-        const RowMask mask(a, p, j0, len);
+      if (__any_sync(0xffffffffu, (top - m) * c2 > kRaise)) raise((top - m) * c2 > kRaise);
+      uint32_t pk[NC / 2];
+      f2 sum[2];
+      for (;;) {
+        float s[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+        for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
+        tmem_ld_wait();
+        if (!whole) {
+          const RowMask mask(a, p, j0, len);
 #pragma unroll
-      for (int c = 4; c + 8 <= NC; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-      const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[NC - 4], s[NC - 3], s[NC - 2]), s[NC - 1], m));
-      float f = 1.f;
-      if (m == -INFINITY) {
-        m = top;                                  // nothing summed so far
-      } else if ((top - m) * c2 > kRaise) {
-        f = ex2((m - top) * c2);
-        m = top;
-      }
-      if (any && __any_sync(0xffffffffu, f != 1.f)) {
-        l *= f;
-#pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(tO + c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= f;
-          tmem_st16(tO + c, reinterpret_cast<uint32_t*>(o));
+          for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
         }
-      }
-      const float at = m == -INFINITY ? 0.f : -m * c2;
-      f2 sum[2] = {0, 0};
-      const f2 cc = pack2(c2, c2), aa = pack2(at, at);
+        const float at = m == -INFINITY ? 0.f : -m * c2;
+        const f2 cc = pack2(c2, c2), aa = pack2(at, at);
+        float mx[4] = {top, s[0], s[1], s[2]};
+        sum[0] = sum[1] = 0;
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const f2 e = ex2_2(dr::fma2(pack2(s[c0 + c], s[c0 + c + 1]), cc, aa));
+        for (int c = 0; c < NC; c += 2) {
+          mx[c / 2 % 4] = max3(mx[c / 2 % 4], s[c], s[c + 1]);
+          const f2 e = ex2_2(dr::fma2(pack2(s[c], s[c + 1]), cc, aa));
           sum[c / 2 % 2] = add2(sum[c / 2 % 2], e);
           float x, y;
           unpack2(e, x, y);
           pk[c / 2] = tc::pack_bf16(x, y);
         }
-        tmem_st16(tS + c0 / 2, pk);
+        top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const bool far = (top - m) * c2 > kAgain;   // true too where nothing was summed so far
+        if (!__any_sync(0xffffffffu, far)) break;
+        raise(far);
       }
       l += sum2(add2(sum[0], sum[1]));
+#pragma unroll
+      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tS + c, pk + c);
     };
 
     for (int n = 0; n < tiles.n && ok; ++n) {
@@ -262,60 +269,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = max(0, kn - NS); n < kn; ++n) wait_phase(&b_kf[n % NS], (n / NS) & 1);
       for (int n = max(0, vn - NS); n < vn; ++n) wait_phase(&b_vf[n % NS], (n / NS) & 1);
     }
-  } else if (warp == kMmaWarp && tiles.n > 0) {   // ---------------------------------- MMAs
-    // the whole warp walks the loop, one lane issues
-    const uint64_t q0 = desc_kmajor(smem_u32(sm + L::oQ)), k0 = desc_kmajor(smem_u32(sm + L::oK));
+  } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && tiles.n > 0) {   // --------- MMAs
+    const int w = warp - kMmaWarp;
+    const TileSet& set = w ? set1 : set0;
+    const uint64_t q = desc_kmajor(smem_u32(sm + L::oQ + w * L::kTile)), k0 = desc_kmajor(smem_u32(sm + L::oK));
     const uint64_t v0 = desc_mnmajor<kM>(smem_u32(sm + L::oV));
+    const uint32_t o = tmem + 256 + w * D, s = tmem + w * 128;
     auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    int pend[2] = {-1, -1};       // the key tile whose P V is still to come
-    uint32_t np[2] = {0, 0};
+    int pend = -1;                // the key tile whose P V is still to come
+    uint32_t np = 0;
     bool ok = all_wait(&b_q, 0);
     for (int n = 0; n <= tiles.n && ok; ++n) {
       const int slot = n % NS;
+      if (n < tiles.n && !(ok = all_wait(&b_kf[slot], (n / NS) & 1))) break;
+      if (pend >= 0 && !(ok = all_wait(&b_p[w], np & 1))) break;
+      if (!(ok = all_wait(&b_turn[w], n & 1))) break;
+      if (pend >= 0) {
+        tc_fence_after();
+        const uint64_t v = v0 + (pend % NS) * (L::kTile >> 4);
+        if (elect_one()) {
+          mma_bf16_ta(o, s, v, ID_O, np > 0);
+          mma_bf16_ta(o, s + 8, v + step_mnmajor(1), ID_O, true);
+          if (!sinks_only(tiles[pend])) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (!ok) break;
-        const uint32_t o = tmem + 256 + w * D, s = tmem + w * 128;
-        if (pend[w] >= 0) {
-          if (!(ok = all_wait(&b_p[w], np[w] & 1))) break;
-          tc_fence_after();
-          const uint64_t v = v0 + (pend[w] % NS) * (L::kTile >> 4);
-          if (elect_one()) {
-            mma_bf16_ta(o, s, v, ID_O, np[w] > 0);
-            mma_bf16_ta(o, s + 8, v + step_mnmajor(1), ID_O, true);
-            if (!sinks_only(tiles[pend[w]])) {
-#pragma unroll
-              for (int k = 2; k < kM / 16; ++k) mma_bf16_ta(o, s + 8 * k, v + step_mnmajor(k), ID_O, true);
-            }
+            for (int k = 2; k < kM / 16; ++k) mma_bf16_ta(o, s + 8 * k, v + step_mnmajor(k), ID_O, true);
           }
-          ++np[w];
-          pend[w] = -1;
         }
-        // between two batches of MMAs at most one wait: the queue holds eight, 512 cycles
-        if (w == 0 && n < tiles.n) ok = all_wait(&b_kf[slot], (n / NS) & 1);
-        if (w == 1 && n < tiles.n && ok) ok = all_wait(&b_vf[slot], (n / NS) & 1);   // for the next step
-        if (ok && n < tiles.n && (w ? set1 : set0).has(tiles[n])) {
-          const uint32_t id = sinks_only(tiles[n]) ? ID_S32 : ID_S;
-          const uint64_t q = q0 + w * (L::kTile >> 4), k = k0 + slot * (L::kTile >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int e = 0; e < D / 16; ++e)
-              mma_bf16(s, q + step_kmajor<kM>(e), k + step_kmajor<kM>(e), id, e > 0);
-            mma_commit(&b_s[w]);
-          }
-          pend[w] = n;
-        }
-        if (n == tiles.n && elect_one()) mma_commit(&b_o[w]);
+        ++np;
+        pend = -1;
       }
-      if (!ok) break;
+      if (n > 0 && elect_one()) mma_commit(&b_ve[(n - 1) % NS]);
+      if (n < tiles.n && set.has(tiles[n])) {
+        const uint32_t id = sinks_only(tiles[n]) ? ID_S32 : ID_S;
+        const uint64_t k = k0 + slot * (L::kTile >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) mma_bf16(s, q + step_kmajor<kM>(e), k + step_kmajor<kM>(e), id, e > 0);
+          mma_commit(&b_s[w]);
+        }
+        pend = n;
+      }
       if (elect_one()) {
+        mbar_arrive(&b_turn[w ^ 1]);
         if (n < tiles.n) mma_commit(&b_ke[slot]);
-        if (n > 0) mma_commit(&b_ve[(n - 1) % NS]);
       }
+      if (n < tiles.n) ok = all_wait(&b_vf[slot], (n / NS) & 1);   // for the next step
     }
     __syncwarp();
-    if (elect_one()) mma_commit(&b_end);   // no MMA may be under way when the CTA ends
-    wait_phase(&b_end, 0);
+    if (elect_one()) {
+      mma_commit(&b_o[w]);
+      mma_commit(&b_end[w]);      // no MMA may be under way when the CTA ends
+    }
+    wait_phase(&b_end[w], 0);
     tc_fence_before();
   }
   __syncthreads();

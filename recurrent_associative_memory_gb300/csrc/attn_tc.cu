@@ -8,12 +8,13 @@
 // The two tiles take turns: while the four softmax warps of one work, the tensor cores run
 // the other's P V and next S.  S and P V of a tile wait for each other, so a step is the
 // longer of four products (2048 cycles at d = 128) and the softmax's latency plus two.
-// To keep that latency short, a tile's exponentials take the maximum m of the tiles before
-// it, so that they need not wait for its own: any m is right as long as nothing overflows
-// (the final division takes it out), and P up to 2^64 is far inside the range of bf16 and
-// fp32.  A tile that goes further (the first always does) is taken again with its own
-// maximum.  m is raised, and O rescaled, where it is 2^8 behind; S of tile n is issued
-// behind P V of tile n - 1, so a thread that has S may touch O.
+// To keep that latency short, a tile's exponentials take a reference m from the tiles
+// before it and no maximum of their own: any m is right as long as nothing overflows (the
+// final division takes it out), and P up to 2^64 is far inside the range of bf16 and fp32.
+// Where a row's sum over a tile passes 2^8, m grows by its logarithm before the next tile;
+// where it passes 2^64 (or m is not set: the first tile), the tile is taken again from its
+// true maximum.  Raising m rescales O; S of tile n is issued behind P V of tile n - 1, so a
+// thread that has S may touch O.
 //   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
 //   warp 8          TMA: K and V tiles, two slots each (d = 64: four)
 //   warps 9, 10     the MMAs of the tiles 0 and 1: a warp walks its loop together and one
@@ -42,8 +43,8 @@ constexpr int kThreads = 384;   // three warpgroups; the third has an idle warp
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;   // and the one after it
-constexpr float kRaise = 8.f;    // log2 of P above which m is raised for the tiles to come
-constexpr float kAgain = 64.f;   // and above which this tile is taken again
+constexpr float kRaise = 0x1p8f;    // a tile's sum above which m grows
+constexpr float kAgain = 0x1p64f;   // and above which the tile is taken again
 
 template <int D> struct Smem {
   static constexpr int kTile = kM * D * 2;                  // bytes of 128 rows
@@ -105,16 +106,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * D + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, grow = 0.f;   // m and what it grows by, in base 2
     uint32_t phase = 0;
     bool any = false, ok = true;
     const int p0 = a.q_start + i0 + w * kM, p1 = p0 + kM - 1;
 
-    float top = -INFINITY;   // the largest score so far
-    // l and O to the maximum of the rows whose `to` is above their m
-    auto raise = [&](bool mine) {
-      const float f = mine && m != -INFINITY ? ex2((m - top) * c2) : 1.f;
-      if (mine) m = top;
+    auto rescale = [&](float f) {   // l and O, of all rows of the warp
       l *= f;
       if (!any) return;
 #pragma unroll
@@ -131,10 +128,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto one_tile = [&](auto cols, int j0) {   // cols.value keys from j0
       constexpr int NC = decltype(cols)::value;
       const bool whole = j0 + NC - 1 <= p0 && j0 + NC <= len && p1 - j0 < a.window;
-      if (__any_sync(0xffffffffu, (top - m) * c2 > kRaise)) raise((top - m) * c2 > kRaise);
+      if (__any_sync(0xffffffffu, grow != 0.f)) {
+        m += grow;
+        rescale(ex2(-grow));
+      }
       uint32_t pk[NC / 2];
-      f2 sum[2];
-      for (;;) {
+      float total;
+      bool exact = m == -INFINITY;
+      for (int again = 0;; ++again) {
         float s[NC];
 #pragma unroll
         for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
@@ -144,25 +145,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
         }
-        const float at = m == -INFINITY ? 0.f : -m * c2;
+        if (__any_sync(0xffffffffu, exact)) {
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < NC; c += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+          const bool raise = exact && top > m;
+          rescale(raise && m != -INFINITY ? ex2(m - top) : 1.f);
+          if (raise) m = top;
+        }
+        const float at = m == -INFINITY ? 0.f : -m;   // a row that has seen nothing so far
         const f2 cc = pack2(c2, c2), aa = pack2(at, at);
-        float mx[4] = {top, s[0], s[1], s[2]};
-        sum[0] = sum[1] = 0;
+        f2 sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          mx[c / 2 % 4] = max3(mx[c / 2 % 4], s[c], s[c + 1]);
           const f2 e = ex2_2(dr::fma2(pack2(s[c], s[c + 1]), cc, aa));
           sum[c / 2 % 2] = add2(sum[c / 2 % 2], e);
           float x, y;
           unpack2(e, x, y);
           pk[c / 2] = tc::pack_bf16(x, y);
         }
-        top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        const bool far = (top - m) * c2 > kAgain;   // true too where nothing was summed so far
-        if (!__any_sync(0xffffffffu, far)) break;
-        raise(far);
+        total = sum2(add2(sum[0], sum[1]));
+        exact = !(total <= kAgain);
+        if (again || !__any_sync(0xffffffffu, exact)) break;
       }
-      l += sum2(add2(sum[0], sum[1]));
+      l += total;
+      grow = 0.f;
+      if (total > kRaise) asm("lg2.approx.f32 %0, %1;" : "=f"(grow) : "f"(total));
 #pragma unroll
       for (int c = 0; c < NC / 2; c += 16) tmem_st16(tS + c, pk + c);
     };
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (a.lse && i < a.T)
         a.lse[((long long)b * a.H + h) * a.T + i] =
-            l != 0.f ? m * a.scale + logf(l) : -INFINITY;
+            l != 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
     }
     tc_fence_before();
   } else {

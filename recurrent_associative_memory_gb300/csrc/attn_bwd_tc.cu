@@ -94,46 +94,57 @@ __device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
   tc_fence_after();
 }
 
-// The MMA lane.  TMEM: slot i at 128 i (S, then 64 columns on dP), accumulators at 256 and
-// 256 + D.  KV: the dK/dV products, else dQ's.
+// The MMA warp: it walks the steps together and one lane issues, so that the descriptors
+// stay in uniform registers.  TMEM: slot i at 128 i (S, then 64 columns on dP), accumulators
+// at 256 and 256 + D.  KV: the dK/dV products, else dQ's.
 template <int D, bool KV>
-__device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, int n) {
+__device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, uint32_t tm, int n) {
   using L = Smem<D>;
   constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0), ID_ACC = idesc_bf16(kM, D, 0, 1);
   const uint64_t x = desc_kmajor(smem_u32(sm + L::oX)), y = desc_kmajor(smem_u32(sm + L::oY));
-  const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB), tm = q.tmem;
-  bool ok = bounded(&q.own, 0);
+  const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB);
+  auto all_wait = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, bounded(bar, parity)) != 0; };
+  bool ok = all_wait(&q.own, 0);
   for (int i = 0; i < n + 2 && ok; ++i) {
-    if (i >= 2) {   // step i - 2: its slot is the one that step i takes
-      const int j = i - 2, st = j % kStages, slot = j & 1;
-      if (!(ok = bounded(&q.p[slot], (j >> 1) & 1))) break;
+    const int j = i - 2, slot = i & 1;   // step j had the slot that step i takes
+    if (i < n && !(ok = all_wait(&q.full[i % kStages], (i / kStages) & 1))) break;
+    if (j >= 0) {
+      const int st = j % kStages;
+      if (!(ok = all_wait(&q.p[slot], (j >> 1) & 1))) break;
       tc_fence_after();
       const uint64_t dA = desc_mnmajor<kN>(A + st * L::kTile), dB = desc_mnmajor<kN>(B + st * L::kTile);
-      if (KV) {
+      const uint32_t p = tm + 128 * slot;
+      if (elect_one()) {
+        if (KV) {
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k)
+            mma_bf16_ta(tm + 256, p + 8 * k, dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+        }
 #pragma unroll
         for (int k = 0; k < kN / 16; ++k)
-          mma_bf16_ta(tm + 256, tm + 128 * slot + 8 * k, dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+          mma_bf16_ta(tm + 256 + D, p + 64 + 8 * k, dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+        mma_commit(&q.empty[st]);
       }
-#pragma unroll
-      for (int k = 0; k < kN / 16; ++k)
-        mma_bf16_ta(tm + 256 + D, tm + 128 * slot + 64 + 8 * k, dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
-      mma_commit(&q.empty[st]);
     }
     if (i < n) {
-      const int st = i % kStages, slot = i & 1;
-      if (!(ok = bounded(&q.full[st], (i / kStages) & 1))) break;
+      const int st = i % kStages;
       const uint64_t dA = desc_kmajor(A + st * L::kTile), dB = desc_kmajor(B + st * L::kTile);
+      const uint32_t s = tm + 128 * slot;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16(tm + 128 * slot, x + step_kmajor<kM>(k), dA + step_kmajor<kN>(k), ID_S, k > 0);
+        for (int k = 0; k < D / 16; ++k) mma_bf16(s, x + step_kmajor<kM>(k), dA + step_kmajor<kN>(k), ID_S, k > 0);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16(tm + 128 * slot + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
-      mma_commit(&q.s[slot]);
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16(s + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
+        mma_commit(&q.s[slot]);
+      }
     }
   }
-  mma_commit(&q.acc);
-  mma_commit(&q.end);   // no MMA may be under way when the CTA ends
+  __syncwarp();
+  if (elect_one()) {
+    mma_commit(&q.acc);
+    mma_commit(&q.end);   // no MMA may be under way when the CTA ends
+  }
   wait_phase(&q.end, 0);
   tc_fence_before();
 }
@@ -185,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Pipe q;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int hk = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv % a.B, item = blockIdx.x / a.Hkv / a.B;
   const bool far = item < a.n_far;              // first: they are as long as the others or longer
   const int j0 = far ? 0 : (item - a.n_far) * kM;
-  const int len = real_len(a.lens, b, a.S);
+  const int len = uniform(real_len(a.lens, b, a.S));
   int i_begin, i_end;                           // query rows, i_begin a multiple of kN
   if (far) {
     i_begin = a.far_first + item * a.far_rows;
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int per = i_end > i_begin ? (i_end - i_begin + kN - 1) / kN : 0, n = per * a.G;
   pipe_init(q, tid, warp);
-  const uint32_t tmem = q.tmem;
+  const uint32_t tmem = uniform(q.tmem);
 
   if (warp < 8) {   // one thread per key; the warpgroups take the steps in turn
     const int w = warp / 4, row = (warp % 4) * 32 + lane, j = j0 + row;
@@ -302,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       pipe_drain(q, issued);
     }
-  } else if (warp == 9 && lane == 0 && n > 0) {
-    pipe_mma<D, true>(q, sm, n);
+  } else if (warp == 9 && n > 0) {
+    pipe_mma<D, true>(q, sm, tmem, n);
   }
   __syncthreads();
   tc_fence_after();
@@ -335,14 +346,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Pipe q;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + kM - 1) / kM;
   const int h = blockIdx.x % a.H, i0 = blockIdx.x / a.H % n_block * kM, b = blockIdx.x / a.H / n_block;
-  const int hk = h / a.G, len = real_len(a.lens, b, a.S);
+  const int hk = h / a.G, len = uniform(real_len(a.lens, b, a.S));
   const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN);
   const int n = tiles.n;
   pipe_init(q, tid, warp);
-  const uint32_t tmem = q.tmem;
+  const uint32_t tmem = uniform(q.tmem);
 
   if (warp < 8) {   // one thread per query row; the warpgroups take the steps in turn
     const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + row, p = a.q_start + i;
@@ -438,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       issued = k + 1;
     }
     if (n > 0) pipe_drain(q, issued);
-  } else if (warp == 9 && lane == 0 && n > 0) {
-    pipe_mma<D, false>(q, sm, n);
+  } else if (warp == 9 && n > 0) {
+    pipe_mma<D, false>(q, sm, tmem, n);
   }
   __syncthreads();
   tc_fence_after();

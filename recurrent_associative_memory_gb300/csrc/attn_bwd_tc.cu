@@ -25,7 +25,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 384;
+// 16 softmax warps, 8 per TMEM slot: two threads per row, 32 columns each, as a slot's turn
+// is their latency plus its products; then the load warp and the MMA warp, two idle ones
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kHalf = 32;
 constexpr int kN = 64;         // rows of a tile on the walked axis
 constexpr int kStages = 4;
 
@@ -34,6 +38,10 @@ template <int D> struct Smem {
   static constexpr int oX = 0, oY = kOwn, oA = 2 * kOwn, oB = oA + kStages * kTile;
   static constexpr int oVec = oB + kStages * kTile, kBytes = oVec + kStages * 2 * kN * 4 + 1024;
 };
+
+// Column of k-step k of P or dS: each thread leaves its 32 values, packed in 16 columns,
+// over the first of the 32 that it read, so the two threads of a row need no barrier.
+__host__ __device__ constexpr uint32_t half_col(int k) { return (k >> 1) * kHalf + (k & 1) * 8; }
 
 __device__ __forceinline__ bool bounded(uint64_t* bar, uint32_t parity) {
   if (wait_phase(bar, parity)) return true;
@@ -83,12 +91,12 @@ __device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
     mbar_init(&q.own, 1);
     for (int i = 0; i < kStages; ++i) mbar_init(&q.full[i], 1), mbar_init(&q.empty[i], 1);
     mbar_init(&q.fix, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 256);
     mbar_init(&q.acc, 1);
     mbar_init(&q.end, 1);
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&q.tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(&q.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -118,11 +126,11 @@ __device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, uint32_t tm, int 
         if (KV) {
 #pragma unroll
           for (int k = 0; k < kN / 16; ++k)
-            mma_bf16_ta(tm + 256, p + 8 * k, dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+            mma_bf16_ta(tm + 256, p + half_col(k), dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
         }
 #pragma unroll
         for (int k = 0; k < kN / 16; ++k)
-          mma_bf16_ta(tm + 256 + D, p + 64 + 8 * k, dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+          mma_bf16_ta(tm + 256 + D, p + 64 + half_col(k), dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
         mma_commit(&q.empty[st]);
       }
     }
@@ -156,29 +164,29 @@ __device__ __forceinline__ void pipe_drain(Pipe& q, int issued) {
     wait_phase(&q.full[i % kStages], (i / kStages) & 1);
 }
 
-// 128 lanes' rows of D accumulator columns -> bf16 rows (or fp32 parts)
-template <int D>
+// 128 lanes' rows of N accumulator columns -> bf16 rows (or fp32 parts)
+template <int N>
 __device__ __forceinline__ void store_acc(uint32_t tacc, bool any, float f, __nv_bfloat16* o, float* part) {
 #pragma unroll
-  for (int c = 0; c < D; c += 32) {
-    uint32_t v[32];
+  for (int c = 0; c < N; c += 16) {
+    float v[16];
     if (any) {
-      tmem_ld32(tacc + c, v);
+      tmem_ld16(tacc + c, v);
       tmem_ld_wait();
     } else {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0u;
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
     }
     if (part) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     } else if (o) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
+      for (int e = 0; e < 16; e += 8) {
         float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v[e + k]) * f;
+        for (int k = 0; k < 8; ++k) x[k] = v[e + k] * f;
         *reinterpret_cast<uint4*>(o + c + e) = tc::pack8(x);
       }
     }
@@ -214,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
 
-  if (warp < 8) {   // one thread per key; the warpgroups take the steps in turn
-    const int w = warp / 4, row = (warp % 4) * 32 + lane, j = j0 + row;
+  if (warp < 16) {   // two threads per key; the slots' warps take the steps in turn
+    const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, j = j0 + row;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
@@ -234,42 +242,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
                          (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
       const int lo = j < len ? j - p0 : INT_MAX, hi = key_hi == INT_MAX ? INT_MAX : key_hi - p0;
+      const int c0 = kHalf * half;
+      float s[kHalf], g[kHalf];
+      uint32_t pk[kHalf / 2];
+      tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+      tmem_ld_wait();
 #pragma unroll
-      for (int c0 = 0; c0 < kN; c0 += 32) {
-        float s[32], g[32];
-        uint32_t pk[16];
-        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
-        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 l4 = nl[(c0 + c) / 4];
-          fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
-          fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = ex2(s[c]);
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = c0 + c >= lo && c0 + c <= hi ? s[c] : 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
-        tmem_st16(tS + c0 / 2, pk);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 d4 = nd[(c0 + c) / 4];
-          add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
-          add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
-        }
-        if (!whole) {   // what a key past the end holds may be NaN
-#pragma unroll
-          for (int c = 0; c < 32; ++c) g[c] = s[c] != 0.f ? g[c] : 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-        tmem_st16(tS + 64 + c0 / 2, pk);
+      for (int c = 0; c < kHalf; c += 4) {
+        const float4 l4 = nl[(c0 + c) / 4];
+        fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
+        fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
       }
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) s[c] = ex2(s[c]);
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) s[c] = c0 + c >= lo && c0 + c <= hi ? s[c] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
+      tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+      tmem_st16(tS + c0, pk);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 4) {
+        const float4 d4 = nd[(c0 + c) / 4];
+        add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
+        add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
+      }
+      if (!whole) {   // what a key past the end holds may be NaN
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) g[c] = s[c] != 0.f ? g[c] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+      tmem_st16(tS + 64 + c0, pk);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&q.p[w]);
@@ -279,18 +286,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
-    if (ok) {   // warpgroup 0: dV, 1: dK
+    if (ok) {   // slot 0's warps: dV, slot 1's: dK
       const long long o = (((long long)b * a.S + j) * a.Hkv + hk) * D;
       const bool part = a.n_far && j0 == 0 && j < a.n_sink;
       float* p = part ? a.sink_part + (((((long long)b * a.Hkv + hk) * (1 + a.n_far) + (far ? 1 + item : 0)) * 2 +
-                                        (1 - w)) * a.n_sink + j) * D
+                                        (1 - w)) * a.n_sink + j) * D + half * (D / 2)
                       : nullptr;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(w ? a.dk : a.dv) + o;
-      store_acc<D>(tmem + 256 + w * D + lanes, n > 0, w ? a.scale : 1.f,
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(w ? a.dk : a.dv) + o + half * (D / 2);
+      store_acc<D / 2>(tmem + 256 + w * D + half * (D / 2) + lanes, n > 0, w ? a.scale : 1.f,
                    j < a.S && !part && !far ? out : nullptr, p);
     }
     tc_fence_before();
-  } else if (warp == 8) {
+  } else if (warp == kLoadWarp) {
     int issued = 0;
     if (lane == 0 && n > 0) {
       mbar_expect_tx(&q.own, 2 * L::kOwn);
@@ -313,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       pipe_drain(q, issued);
     }
-  } else if (warp == 9 && n > 0) {
+  } else if (warp == kMmaWarp && n > 0) {
     pipe_mma<D, true>(q, sm, tmem, n);
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // The sinks' gradients: their pieces in order.
@@ -355,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
 
-  if (warp < 8) {   // one thread per query row; the warpgroups take the steps in turn
-    const int w = warp / 4, row = (warp % 4) * 32 + lane, i = i0 + row, p = a.q_start + i;
+  if (warp < 16) {   // two threads per query row; the slots' warps take the steps in turn
+    const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, i = i0 + row, p = a.q_start + i;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
@@ -373,44 +380,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = t0 + kN - 1 <= a.q_start + i0 && t0 + kN <= len && a.q_start + i0 + kM - 1 - t0 < a.window;
       const RowMask mask(a, p, t0, len);
+      const int c0 = kHalf * half;
+      float s[kHalf], g[kHalf];
+      uint32_t pk[kHalf / 2];
+      tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+      tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+      tmem_ld_wait();
 #pragma unroll
-      for (int c0 = 0; c0 < kN; c0 += 32) {
-        float s[32], g[32];
-        uint32_t pk[16];
-        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
-        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          fma2(s[c], s[c + 1], c2, nl);
-          s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
-          add_mul2(g[c], g[c + 1], nd, nd, s[c], s[c + 1]);
-        }
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) g[c] = mask.sees(c0 + c) && s[c] != 0.f ? g[c] : 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-        tmem_st16(tS + 64 + c0 / 2, pk);
+      for (int c = 0; c < kHalf; c += 2) {
+        fma2(s[c], s[c + 1], c2, nl);
+        s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
+        add_mul2(g[c], g[c + 1], nd, nd, s[c], s[c + 1]);
       }
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) g[c] = mask.sees(c0 + c) && s[c] != 0.f ? g[c] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+      tmem_st16(tS + 64 + c0, pk);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&q.p[w]);
     }
-    if (w == 0) {
-      if (n > 0) {
-        ok = bounded(&q.acc, 0) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-      }
-      if (ok)
-        store_acc<D>(tmem + 256 + D + lanes, n > 0, a.scale,
-                     i < a.T ? static_cast<__nv_bfloat16*>(a.dq) + (((long long)b * a.T + i) * a.H + h) * D : nullptr,
-                     nullptr);
+    if (n > 0) {
+      ok = bounded(&q.acc, 0) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok) {   // a quarter of the channels each
+      const int c0 = warp / 4 * (D / 4);
+      store_acc<D / 4>(tmem + 256 + D + c0 + lanes, n > 0, a.scale,
+                       i < a.T ? static_cast<__nv_bfloat16*>(a.dq) + (((long long)b * a.T + i) * a.H + h) * D + c0
+                               : nullptr,
+                       nullptr);
     }
     tc_fence_before();
-  } else if (warp == 8) {
+  } else if (warp == kLoadWarp) {
     const int fix_tile = len < a.S && len % kN ? len / kN : -1;   // its K rows from len on become 0
     int issued = 0, n_fix = 0;
     bool ok = true;
@@ -449,12 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       issued = k + 1;
     }
     if (n > 0) pipe_drain(q, issued);
-  } else if (warp == 9 && n > 0) {
+  } else if (warp == kMmaWarp && n > 0) {
     pipe_mma<D, false>(q, sm, tmem, n);
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ host side

@@ -241,8 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = a.q_start + i0;
       const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
                          (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
-      const int lo = j < len ? j - p0 : INT_MAX, hi = key_hi == INT_MAX ? INT_MAX : key_hi - p0;
-      const int c0 = kHalf * half;
+      const int c0 = kHalf * half;   // the rows of this half that see this key, as bits
+      const uint32_t word =
+          j < len ? bits_below(key_hi == INT_MAX ? 32 : key_hi - p0 + 1 - c0) & ~bits_below(j - p0 - c0) : 0u;
       float s[kHalf], g[kHalf];
       uint32_t pk[kHalf / 2];
       tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kHalf; ++c) s[c] = ex2(s[c]);
       if (!whole) {
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) s[c] = c0 + c >= lo && c0 + c <= hi ? s[c] : 0.f;
+        for (int c = 0; c < kHalf; ++c) s[c] = word & (1u << c) ? s[c] : 0.f;
       }
 #pragma unroll
       for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!whole) {   // what a key past the end holds may be NaN
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) g[c] = s[c] != 0.f ? g[c] : 0.f;
+        for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
       }
 #pragma unroll
       for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
       const bool whole = t0 + kN - 1 <= a.q_start + i0 && t0 + kN <= len && a.q_start + i0 + kM - 1 - t0 < a.window;
-      const RowMask mask(a, p, t0, len);
       const int c0 = kHalf * half;
+      const uint32_t word = RowMask(a, p, t0, len).word(c0);
       float s[kHalf], g[kHalf];
       uint32_t pk[kHalf / 2];
       tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!whole) {
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) g[c] = mask.sees(c0 + c) && s[c] != 0.f ? g[c] : 0.f;
+        for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
       }
 #pragma unroll
       for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);

@@ -143,7 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) {
           const RowMask mask(a, p, j0, len);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) s[c] = mask.sees(c) ? s[c] : -INFINITY;
+          for (int c0 = 0; c0 < NC; c0 += 32) {
+            const uint32_t word = mask.word(c0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c0 + c] = word & (1u << c) ? s[c0 + c] : -INFINITY;
+          }
         }
         if (__any_sync(0xffffffffu, exact)) {
           float mx[4] = {s[0], s[1], s[2], s[3]};

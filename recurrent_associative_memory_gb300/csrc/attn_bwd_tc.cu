@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = bounded(&q.full[st], (i / kStages) & 1);   // this stage's numbers (with its tiles)
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
-      const float4* nl = reinterpret_cast<const float4*>(sm + L::oVec + st * 2 * kN * 4);
-      const float4* nd = nl + kN / 4;
+      const uint32_t nl = smem_u32(sm + L::oVec + st * 2 * kN * 4) + 4 * kHalf * half, nd = nl + kN * 4;
       const int p0 = a.q_start + i0;
       const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
                          (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < kHalf; c += 4) {
-        const float4 l4 = nl[(c0 + c) / 4];
+        const float4 l4 = lds128(nl + 4 * c);
         fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
         fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
       }
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < kHalf; c += 4) {
-        const float4 d4 = nd[(c0 + c) / 4];
+        const float4 d4 = lds128(nd + 4 * c);
         add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
         add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
       }

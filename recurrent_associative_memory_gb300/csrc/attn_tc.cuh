@@ -134,6 +134,14 @@ struct TileSet {
   }
 };
 
+// 16 bytes of shared memory by their 32-bit address: behind the rounding of the dynamic
+// array's start the compiler no longer knows the space and would load generically.
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 // The bits below `n` of a word.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
 

@@ -11,7 +11,7 @@ namespace dr {
 cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 bool attn_tc_supported(const AttnArgs& a, int dtype);
-cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_fwd_tc(const AttnArgs& a, int sms, cudaStream_t st);
 size_t attn_bwd_tc_workspace(const AttnArgs& a);
 cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st);
 int attn_step_pieces(const AttnStepArgs& a, int dtype, int sms);
@@ -178,7 +178,7 @@ int dr_window_attn_fwd(const dr_attn* a, const void* q, const void* k, const voi
   if (!aligned16(q, k, v, out) || !strides_ok(a, true)) return DR_ERR_ALIGN;
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = out, r.lse = lse;
-  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, stream_of(stream)));
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, sm_count(), stream_of(stream)));
   return status_of(launch_attn_fwd_simt(r, a->dtype, stream_of(stream)));
 }
 

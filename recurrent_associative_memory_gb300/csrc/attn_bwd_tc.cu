@@ -26,9 +26,9 @@ namespace {
 using namespace attn;
 
 // 16 softmax warps, 8 per TMEM slot: two threads per row, 32 columns each, as a slot's turn
-// is their latency plus its products; then the load warp and the MMA warp, two idle ones
+// is their latency plus its products; then the load warp, two MMA warps and an idle one
 constexpr int kThreads = 640;
-constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kLoadWarp = 16, kMmaWarp = 17;   // and the one after it
 constexpr int kHalf = 32;
 constexpr int kN = 64;         // rows of a tile on the walked axis
 constexpr int kStages = 4;
@@ -51,49 +51,63 @@ __device__ __forceinline__ bool bounded(uint64_t* bar, uint32_t parity) {
 
 // ------------------------------------------------------------------ the rows' numbers
 
+// D / 8 lanes per row, kRowsAhead rows whose loads go together.
+constexpr int kRowsAhead = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
-  constexpr int LK = D / 8;
-  const long long e = (long long)blockIdx.x * (256 / LK) + threadIdx.x / LK;   // [B,Tp,H]
+  constexpr int LK = D / 8, G = 256 / LK;
   const int c = 8 * (threadIdx.x % LK);
-  const bool in = e < (long long)a.B * a.Tp * a.H;
-  const int h = e % a.H, t = e / a.H % a.Tp, b = in ? e / a.H / a.Tp : 0;
-  float s = 0.f;
-  if (in && t < a.T) {
-    const long long row = ((long long)b * a.T + t) * a.H + h;
-    float o[8], g[8];
-    load8<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(a.out) + row * D + c, 8, o);
-    load8<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(a.d_out) + row * D + c, 8, g);
+  const long long e0 = (long long)blockIdx.x * (G * kRowsAhead) + threadIdx.x / LK;   // [B,Tp,H]
+  const long long all = (long long)a.B * a.Tp * a.H;
+  uint4 o[kRowsAhead], g[kRowsAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += o[i] * g[i];
+  for (int r = 0; r < kRowsAhead; ++r) {
+    const long long e = e0 + r * G, bt = e / a.H;
+    const int t = bt % a.Tp;
+    const bool in = e < all && t < a.T;
+    const long long at = ((bt / a.Tp * a.T + t) * a.H + e % a.H) * D + c;
+    o[r] = in ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + at) : make_uint4(0, 0, 0, 0);
+    g[r] = in ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_out) + at) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int w = LK / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-  if (!in || c) return;
-  const long long at = ((long long)b * a.H + h) * a.Tp + t;
-  const float lse = t < a.T ? a.lse[((long long)b * a.H + h) * a.T + t] : -INFINITY;
-  a.nlse2[at] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
-  a.delta[at] = -s;
+  for (int r = 0; r < kRowsAhead; ++r) {
+    float x[8], y[8], s = 0.f;
+    tc::unpack8(o[r], x);
+    tc::unpack8(g[r], y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += x[i] * y[i];
+#pragma unroll
+    for (int w = LK / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    const long long e = e0 + r * G, bt = e / a.H;
+    if (c || e >= all) continue;
+    const int t = bt % a.Tp;
+    const long long bh = bt / a.Tp * a.H + e % a.H;
+    const float lse = t < a.T ? a.lse[bh * a.T + t] : -INFINITY;
+    a.nlse2[bh * a.Tp + t] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    a.delta[bh * a.Tp + t] = -s;
+  }
 }
 
 // ------------------------------------------------------------------ the shared pipeline
 
-// One CTA's pipeline over n steps.  X, Y: the own tiles (dK/dV: K, V; dQ: Q, dO), A, B: the
-// walked ones (Q, dO; K, V).  Per step: slot S = X A^T, slot dP = Y B^T; then, from what
-// the softmax warps left in their place, acc0 += [S] B (dK/dV only) and acc1 += [dP] A.
+// One CTA per SM walks its work items, an item's steps one after another; steps and items
+// are numbered through, so that the next item's loads and first products run behind the last
+// one's softmax and stores.  X, Y: the own tiles (dK/dV: K, V; dQ: Q, dO), A, B: the walked
+// ones (Q, dO; K, V).  Per step: slot S = X A^T, slot dP = Y B^T; then, from what the softmax
+// warps left in their place, acc0 += [S] B (dK/dV only) and acc1 += [dP] A.
 struct Pipe {
-  uint64_t own, full[kStages], empty[kStages], fix, s[2], p[2], acc, end;
+  uint64_t own_full, own_empty, full[kStages], empty[kStages], fix, s[2], p[2], free[2], acc_full, acc_empty, end[2];
   uint32_t tmem;
 };
 
 __device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
   if (tid == 0) {
-    mbar_init(&q.own, 1);
+    mbar_init(&q.own_full, 1), mbar_init(&q.own_empty, 1);
     for (int i = 0; i < kStages; ++i) mbar_init(&q.full[i], 1), mbar_init(&q.empty[i], 1);
     mbar_init(&q.fix, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 256);
-    mbar_init(&q.acc, 1);
-    mbar_init(&q.end, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 256), mbar_init(&q.free[i], 1), mbar_init(&q.end[i], 1);
+    mbar_init(&q.acc_full, 1), mbar_init(&q.acc_empty, 512);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&q.tmem, 512);
@@ -102,65 +116,85 @@ __device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
   tc_fence_after();
 }
 
-// The MMA warp: it walks the steps together and one lane issues, so that the descriptors
-// stay in uniform registers.  TMEM: slot i at 128 i (S, then 64 columns on dP), accumulators
-// at 256 and 256 + D.  KV: the dK/dV products, else dQ's.
-template <int D, bool KV>
-__device__ __forceinline__ void pipe_mma(Pipe& q, uint8_t* sm, uint32_t tm, int n) {
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity) {   // of a whole warp
+  return __all_sync(0xffffffffu, bounded(bar, parity)) != 0;
+}
+
+// Where a warp stands: items (with steps) and steps gone by.
+struct Walk { uint32_t items, steps; };
+
+// The MMA warps' parts of an item of n steps: one issues S and dP, the other the products
+// into the accumulators (in order, so that sums keep their order).  A wait costs either of
+// them 200 to 300 cycles even where nothing is waited for, in which the queue of issued
+// products runs dry; two warps cover each other's.  A warp walks together and one lane
+// issues, so that the descriptors stay in uniform registers.  TMEM: slot i at 128 i (S, then
+// 64 columns on dP), accumulators at 256 and 256 + D.  KV: the dK/dV products, else dQ's.
+template <int D>
+__device__ __forceinline__ bool scores_item(Pipe& q, uint8_t* sm, uint32_t tm, Walk& at, int n) {
   using L = Smem<D>;
-  constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0), ID_ACC = idesc_bf16(kM, D, 0, 1);
+  constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0);
   const uint64_t x = desc_kmajor(smem_u32(sm + L::oX)), y = desc_kmajor(smem_u32(sm + L::oY));
   const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB);
-  auto all_wait = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, bounded(bar, parity)) != 0; };
-  bool ok = all_wait(&q.own, 0);
-  for (int i = 0; i < n + 2 && ok; ++i) {
-    const int j = i - 2, slot = i & 1;   // step j had the slot that step i takes
-    if (i < n && !(ok = all_wait(&q.full[i % kStages], (i / kStages) & 1))) break;
-    if (j >= 0) {
-      const int st = j % kStages;
-      if (!(ok = all_wait(&q.p[slot], (j >> 1) & 1))) break;
-      tc_fence_after();
-      const uint64_t dA = desc_mnmajor<kN>(A + st * L::kTile), dB = desc_mnmajor<kN>(B + st * L::kTile);
-      const uint32_t p = tm + 128 * slot;
-      if (elect_one()) {
-        if (KV) {
+  if (!all_wait(&q.own_full, at.items & 1)) return false;
+  for (int i = 0; i < n; ++i, ++at.steps) {
+    const uint32_t gi = at.steps, slot = gi & 1, st = gi % kStages, s = tm + 128 * slot;
+    if (!all_wait(&q.full[st], (gi / kStages) & 1)) return false;
+    if (gi >= 2 && !all_wait(&q.free[slot], ((gi >> 1) - 1) & 1)) return false;
+    const uint64_t dA = desc_kmajor(A + st * L::kTile), dB = desc_kmajor(B + st * L::kTile);
+    if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kN / 16; ++k)
-            mma_bf16_ta(tm + 256, p + half_col(k), dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
-        }
+      for (int k = 0; k < D / 16; ++k) mma_bf16(s, x + step_kmajor<kM>(k), dA + step_kmajor<kN>(k), ID_S, k > 0);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) mma_bf16(s + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
+      mma_commit(&q.s[slot]);
+      if (i == n - 1) mma_commit(&q.own_empty);
+    }
+  }
+  at.items += 1;
+  return true;
+}
+
+template <int D, bool KV>
+__device__ __forceinline__ bool sums_item(Pipe& q, uint8_t* sm, uint32_t tm, Walk& at, int n) {
+  using L = Smem<D>;
+  constexpr uint32_t ID_ACC = idesc_bf16(kM, D, 0, 1);
+  const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB);
+  if (at.items > 0 && !all_wait(&q.acc_empty, (at.items - 1) & 1)) return false;
+  for (int j = 0; j < n; ++j, ++at.steps) {
+    const uint32_t gj = at.steps, slot = gj & 1, st = gj % kStages, p = tm + 128 * slot;
+    if (!all_wait(&q.p[slot], (gj >> 1) & 1)) return false;
+    tc_fence_after();
+    const uint64_t dA = desc_mnmajor<kN>(A + st * L::kTile), dB = desc_mnmajor<kN>(B + st * L::kTile);
+    if (elect_one()) {
+      if (KV) {
 #pragma unroll
         for (int k = 0; k < kN / 16; ++k)
-          mma_bf16_ta(tm + 256 + D, p + 64 + half_col(k), dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
-        mma_commit(&q.empty[st]);
+          mma_bf16_ta(tm + 256, p + half_col(k), dB + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
       }
-    }
-    if (i < n) {
-      const int st = i % kStages;
-      const uint64_t dA = desc_kmajor(A + st * L::kTile), dB = desc_kmajor(B + st * L::kTile);
-      const uint32_t s = tm + 128 * slot;
-      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) mma_bf16(s, x + step_kmajor<kM>(k), dA + step_kmajor<kN>(k), ID_S, k > 0);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16(s + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
-        mma_commit(&q.s[slot]);
-      }
+      for (int k = 0; k < kN / 16; ++k)
+        mma_bf16_ta(tm + 256 + D, p + 64 + half_col(k), dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+      mma_commit(&q.free[slot]);
+      mma_commit(&q.empty[st]);
+      if (j == n - 1) mma_commit(&q.acc_full);
     }
   }
+  at.items += 1;
+  return true;
+}
+
+// An MMA warp's end: no MMA may be under way when the CTA ends.
+__device__ __forceinline__ void mma_end(uint64_t* bar) {
   __syncwarp();
-  if (elect_one()) {
-    mma_commit(&q.acc);
-    mma_commit(&q.end);   // no MMA may be under way when the CTA ends
-  }
-  wait_phase(&q.end, 0);
+  if (elect_one()) mma_commit(bar);
+  wait_phase(bar, 0);
   tc_fence_before();
 }
 
-// The load warp gave up or is done: no copy may be in flight when the CTA ends.
-__device__ __forceinline__ void pipe_drain(Pipe& q, int issued) {
-  wait_phase(&q.own, 0);
-  for (int i = max(0, issued - kStages); i < issued; ++i)
+// The load warp's end: no copy may be in flight when the CTA ends.
+__device__ __forceinline__ void load_end(Pipe& q, const Walk& at) {
+  if (at.items > 0) wait_phase(&q.own_full, (at.items - 1) & 1);
+  for (uint32_t i = at.steps > kStages ? at.steps - kStages : 0; i < at.steps; ++i)
     wait_phase(&q.full[i % kStages], (i / kStages) & 1);
 }
 
@@ -195,6 +229,32 @@ __device__ __forceinline__ void store_acc(uint32_t tacc, bool any, float f, __nv
 
 // ------------------------------------------------------------------ dK, dV
 
+// One work item: 128 keys of a key/value head and the query rows that see them, or one piece
+// of the rows that see only the sinks (first: they are as long as the others or longer).
+struct KeyItem {
+  int hk, b, j0, len, i_begin, per, n, piece;   // steps: `per` tiles of kN rows from i_begin, for each head
+  bool far;
+  __device__ __forceinline__ KeyItem(const AttnArgs& a, long long it) {
+    hk = static_cast<int>(it % a.Hkv), b = static_cast<int>(it / a.Hkv % a.B);
+    const int item = static_cast<int>(it / a.Hkv / a.B);
+    far = item < a.n_far;
+    piece = far ? 1 + item : 0;
+    j0 = far ? 0 : (item - a.n_far) * kM;
+    len = uniform(real_len(a.lens, b, a.S));
+    int i_end;   // i_begin is a multiple of kN
+    if (far) {
+      i_begin = a.far_first + item * a.far_rows;
+      i_end = len > 0 ? min(a.T, i_begin + a.far_rows) : i_begin;
+    } else {
+      const QueryRows r(j0, min(j0 + kM, a.S) - 1, len, a.window, a.n_sink, a.q_start, a.T);
+      i_begin = r.begin / kN * kN;
+      i_end = j0 == 0 && a.n_far ? min(r.end, a.far_first) : r.end;
+    }
+    per = i_end > i_begin ? (i_end - i_begin + kN - 1) / kN : 0;
+    n = per * a.G;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -205,123 +265,130 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Pipe q;
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
-  const int hk = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv % a.B, item = blockIdx.x / a.Hkv / a.B;
-  const bool far = item < a.n_far;              // first: they are as long as the others or longer
-  const int j0 = far ? 0 : (item - a.n_far) * kM;
-  const int len = uniform(real_len(a.lens, b, a.S));
-  int i_begin, i_end;                           // query rows, i_begin a multiple of kN
-  if (far) {
-    i_begin = a.far_first + item * a.far_rows;
-    i_end = len > 0 ? min(a.T, i_begin + a.far_rows) : i_begin;
-  } else {
-    const QueryRows r(j0, min(j0 + kM, a.S) - 1, len, a.window, a.n_sink, a.q_start, a.T);
-    i_begin = r.begin / kN * kN;
-    i_end = j0 == 0 && a.n_far ? min(r.end, a.far_first) : r.end;
-  }
-  const int per = i_end > i_begin ? (i_end - i_begin + kN - 1) / kN : 0, n = per * a.G;
+  const long long n_item = ((long long)(a.S + kM - 1) / kM + a.n_far) * a.B * a.Hkv;
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
+  Walk at = {0, 0};
+  bool ok = true;
 
   if (warp < 16) {   // two threads per key; the slots' warps take the steps in turn
-    const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, j = j0 + row;
+    const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, c0 = kHalf * half;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
-    const int key_hi = j < a.n_sink ? INT_MAX : j + a.window - 1;   // last position that sees this key
-    bool ok = true;
-    for (int i = w; i < n; i += 2) {
-      const int st = i % kStages, i0 = i_begin + (i % per) * kN;
-      ok = bounded(&q.s[w], (i >> 1) & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      ok = bounded(&q.full[st], (i / kStages) & 1);   // this stage's numbers (with its tiles)
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc_fence_after();
-      const uint32_t nl = smem_u32(sm + L::oVec + st * 2 * kN * 4) + 4 * kHalf * half, nd = nl + kN * 4;
-      const int p0 = a.q_start + i0;
-      const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
-                         (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
-      const int c0 = kHalf * half;   // the rows of this half that see this key, as bits
-      const uint32_t word =
-          j < len ? bits_below(key_hi == INT_MAX ? 32 : key_hi - p0 + 1 - c0) & ~bits_below(j - p0 - c0) : 0u;
-      float s[kHalf], g[kHalf];
-      uint32_t pk[kHalf / 2];
-      tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
-      tmem_ld_wait();
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const KeyItem x(a, it);
+      const int j = x.j0 + row;
+      const int key_hi = j < a.n_sink ? INT_MAX : j + a.window - 1;   // last position that sees this key
+      for (int i = (w - at.steps) & 1; i < x.n; i += 2) {
+        const uint32_t gi = at.steps + i, st = gi % kStages;
+        if (!(ok = all_wait(&q.s[w], (gi >> 1) & 1))) break;
+        // this stage's numbers (with its tiles)
+        if (!(ok = all_wait(&q.full[st], (gi / kStages) & 1))) break;
+        tc_fence_after();
+        const uint32_t nl = smem_u32(sm + L::oVec + st * 2 * kN * 4) + 4 * c0, nd = nl + kN * 4;
+        const int p0 = a.q_start + x.i_begin + (i % x.per) * kN;
+        const bool whole = p0 >= x.j0 + kM - 1 && x.j0 + kM <= x.len &&
+                           (p0 + kN - 1 - x.j0 < a.window || x.j0 + kM <= a.n_sink);
+        // the rows of this half that see this key, as bits
+        const uint32_t word =
+            j < x.len ? bits_below(key_hi == INT_MAX ? 32 : key_hi - p0 + 1 - c0) & ~bits_below(j - p0 - c0) : 0u;
+        float s[kHalf], g[kHalf];
+        uint32_t pk[kHalf / 2];
+        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 4) {
-        const float4 l4 = lds128(nl + 4 * c);
-        fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
-        fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
-      }
-#pragma unroll
-      for (int c = 0; c < kHalf; ++c) s[c] = ex2(s[c]);
-      if (!whole) {
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c) s[c] = word & (1u << c) ? s[c] : 0.f;
-      }
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
-      tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
-      tmem_st16(tS + c0, pk);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 4) {
-        const float4 d4 = lds128(nd + 4 * c);
-        add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
-        add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
-      }
-      if (!whole) {   // what a key past the end holds may be NaN
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
-      }
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-      tmem_st16(tS + 64 + c0, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&q.p[w]);
-    }
-    if (n > 0) {
-      ok = bounded(&q.acc, 0) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok) {   // slot 0's warps: dV, slot 1's: dK
-      const long long o = (((long long)b * a.S + j) * a.Hkv + hk) * D;
-      const bool part = a.n_far && j0 == 0 && j < a.n_sink;
-      float* p = part ? a.sink_part + (((((long long)b * a.Hkv + hk) * (1 + a.n_far) + (far ? 1 + item : 0)) * 2 +
-                                        (1 - w)) * a.n_sink + j) * D + half * (D / 2)
-                      : nullptr;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(w ? a.dk : a.dv) + o + half * (D / 2);
-      store_acc<D / 2>(tmem + 256 + w * D + half * (D / 2) + lanes, n > 0, w ? a.scale : 1.f,
-                   j < a.S && !part && !far ? out : nullptr, p);
-    }
-    tc_fence_before();
-  } else if (warp == kLoadWarp) {
-    int issued = 0;
-    if (lane == 0 && n > 0) {
-      mbar_expect_tx(&q.own, 2 * L::kOwn);
-      for (int c = 0; c < D / 64; ++c) {
-        tma_load_4d(sm + L::oX + c * kM * 128, &tmK, &q.own, 64 * c, hk, j0, b);
-        tma_load_4d(sm + L::oY + c * kM * 128, &tmV, &q.own, 64 * c, hk, j0, b);
-      }
-      for (int i = 0; i < n; ++i) {
-        const int st = i % kStages, h = hk * a.G + i / per, i0 = i_begin + (i % per) * kN;
-        if (i >= kStages && !bounded(&q.empty[st], (i / kStages - 1) & 1)) break;
-        mbar_expect_tx(&q.full[st], 2 * L::kTile + 2 * kN * 4);
-        for (int c = 0; c < D / 64; ++c) {
-          tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmQ, &q.full[st], 64 * c, h, i0, b);
-          tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmO, &q.full[st], 64 * c, h, i0, b);
+        for (int c = 0; c < kHalf; c += 4) {
+          const float4 l4 = lds128(nl + 4 * c);
+          fma2v(s[c], s[c + 1], c2, l4.x, l4.y);
+          fma2v(s[c + 2], s[c + 3], c2, l4.z, l4.w);
         }
-        const long long at = ((long long)b * a.H + h) * a.Tp + i0;
-        bulk_load(sm + L::oVec + st * 2 * kN * 4, a.nlse2 + at, kN * 4, &q.full[st]);
-        bulk_load(sm + L::oVec + st * 2 * kN * 4 + kN * 4, a.delta + at, kN * 4, &q.full[st]);
-        issued = i + 1;
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) s[c] = ex2(s[c]);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) s[c] = word & (1u << c) ? s[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(s[c], s[c + 1]);
+        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+        tmem_st16(tS + c0, pk);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 4) {
+          const float4 d4 = lds128(nd + 4 * c);
+          add_mul2(g[c], g[c + 1], d4.x, d4.y, s[c], s[c + 1]);
+          add_mul2(g[c + 2], g[c + 3], d4.z, d4.w, s[c + 2], s[c + 3]);
+        }
+        if (!whole) {   // what a key past the end holds may be NaN
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+        tmem_st16(tS + 64 + c0, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&q.p[w]);
       }
-      pipe_drain(q, issued);
+      if (!ok || (x.n > 0 && !(ok = all_wait(&q.acc_full, at.items & 1)))) break;
+      tc_fence_after();
+      // slot 0's warps: dV, slot 1's: dK, half of the channels each
+      const long long o = (((long long)x.b * a.S + j) * a.Hkv + x.hk) * D + half * (D / 2);
+      const bool part = a.n_far && x.j0 == 0 && j < a.n_sink;
+      float* p = part ? a.sink_part + (((((long long)x.b * a.Hkv + x.hk) * (1 + a.n_far) + x.piece) * 2 + (1 - w)) *
+                                           a.n_sink + j) * D + half * (D / 2)
+                      : nullptr;
+      store_acc<D / 2>(tmem + 256 + w * D + half * (D / 2) + lanes, x.n > 0, w ? a.scale : 1.f,
+                       j < a.S && !part && !x.far ? static_cast<__nv_bfloat16*>(w ? a.dk : a.dv) + o : nullptr, p);
+      tc_fence_before();
+      if (x.n > 0) mbar_arrive(&q.acc_empty);
+      at.steps += x.n, at.items += x.n > 0;
     }
-  } else if (warp == kMmaWarp && n > 0) {
-    pipe_mma<D, true>(q, sm, tmem, n);
+  } else if (warp == kLoadWarp) {   // the whole warp walks, one lane issues
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const KeyItem x(a, it);
+      for (int i = 0; i < x.n; ++i) {
+        const uint32_t gi = at.steps, st = gi % kStages;
+        const int h = x.hk * a.G + i / x.per, i0 = x.i_begin + (i % x.per) * kN;
+        if (gi >= kStages && !(ok = all_wait(&q.empty[st], (gi / kStages - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_expect_tx(&q.full[st], 2 * L::kTile + 2 * kN * 4);
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmQ, &q.full[st], 64 * c, h, i0, x.b);
+            tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmO, &q.full[st], 64 * c, h, i0, x.b);
+          }
+          const long long row = ((long long)x.b * a.H + h) * a.Tp + i0;
+          bulk_load(sm + L::oVec + st * 2 * kN * 4, a.nlse2 + row, kN * 4, &q.full[st]);
+          bulk_load(sm + L::oVec + st * 2 * kN * 4 + kN * 4, a.delta + row, kN * 4, &q.full[st]);
+        }
+        ++at.steps;
+        if (i == 0) {
+          if (at.items > 0 && !(ok = all_wait(&q.own_empty, (at.items - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_expect_tx(&q.own_full, 2 * L::kOwn);
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_4d(sm + L::oX + c * kM * 128, &tmK, &q.own_full, 64 * c, x.hk, x.j0, x.b);
+              tma_load_4d(sm + L::oY + c * kM * 128, &tmV, &q.own_full, 64 * c, x.hk, x.j0, x.b);
+            }
+          }
+          ++at.items;
+        }
+      }
+    }
+    load_end(q, at);
+  } else if (warp == kMmaWarp) {
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const KeyItem x(a, it);
+      if (x.n > 0) ok = scores_item<D>(q, sm, tmem, at, x.n);
+    }
+    mma_end(&q.end[0]);
+  } else if (warp == kMmaWarp + 1) {
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const KeyItem x(a, it);
+      if (x.n > 0) ok = sums_item<D, true>(q, sm, tmem, at, x.n);
+    }
+    mma_end(&q.end[1]);
   }
   __syncthreads();
   tc_fence_after();
@@ -344,6 +411,19 @@ __global__ void __launch_bounds__(D) attn_sink_join_kernel(AttnArgs a) {
 
 // ------------------------------------------------------------------ dQ
 
+// One work item: 128 query rows of a head; steps: the tiles of kN keys that they see.
+struct RowItem {
+  int h, i0, b, hk, len;
+  KeyTiles tiles;
+  __device__ __forceinline__ RowItem(const AttnArgs& a, int n_block, long long it)
+      : h(static_cast<int>(it % a.H)),
+        i0(static_cast<int>(it / a.H % n_block) * kM),
+        b(static_cast<int>(it / a.H / n_block)),
+        hk(h / a.G),
+        len(uniform(real_len(a.lens, b, a.S))),
+        tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN) {}
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -355,108 +435,120 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Pipe q;
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + kM - 1) / kM;
-  const int h = blockIdx.x % a.H, i0 = blockIdx.x / a.H % n_block * kM, b = blockIdx.x / a.H / n_block;
-  const int hk = h / a.G, len = uniform(real_len(a.lens, b, a.S));
-  const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN);
-  const int n = tiles.n;
+  const long long n_item = (long long)a.B * a.H * n_block;
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
+  Walk at = {0, 0};
+  bool ok = true;
 
   if (warp < 16) {   // two threads per query row; the slots' warps take the steps in turn
-    const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, i = i0 + row, p = a.q_start + i;
+    const int w = warp / 8, row = (warp % 4) * 32 + lane, c0 = kHalf * (warp / 4 % 2);
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
-    float nl = -INFINITY, nd = 0.f;
-    if (i < a.T) {
-      const long long at = ((long long)b * a.H + h) * a.Tp + i;
-      nl = a.nlse2[at], nd = a.delta[at];
-    }
-    bool ok = true;
-    for (int k = w; k < n; k += 2) {
-      const int t0 = tiles[k] * kN;
-      ok = bounded(&q.s[w], (k >> 1) & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc_fence_after();
-      const bool whole = t0 + kN - 1 <= a.q_start + i0 && t0 + kN <= len && a.q_start + i0 + kM - 1 - t0 < a.window;
-      const int c0 = kHalf * half;
-      const uint32_t word = RowMask(a, p, t0, len).word(c0);
-      float s[kHalf], g[kHalf];
-      uint32_t pk[kHalf / 2];
-      tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
-      tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 2) {
-        fma2(s[c], s[c + 1], c2, nl);
-        s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
-        add_mul2(g[c], g[c + 1], nd, nd, s[c], s[c + 1]);
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const RowItem x(a, n_block, it);
+      const int n = x.tiles.n, i = x.i0 + row, p = a.q_start + i, p0 = a.q_start + x.i0;
+      float nl = -INFINITY, nd = 0.f;
+      if (i < a.T) {
+        const long long r = ((long long)x.b * a.H + x.h) * a.Tp + i;
+        nl = a.nlse2[r], nd = a.delta[r];
       }
-      if (!whole) {
+      for (int k = (w - at.steps) & 1; k < n; k += 2) {
+        const int t0 = x.tiles[k] * kN;
+        if (!(ok = all_wait(&q.s[w], ((at.steps + k) >> 1) & 1))) break;
+        tc_fence_after();
+        const bool whole = t0 + kN - 1 <= p0 && t0 + kN <= x.len && p0 + kM - 1 - t0 < a.window;
+        const uint32_t word = RowMask(a, p, t0, x.len).word(c0);
+        float s[kHalf], g[kHalf];
+        uint32_t pk[kHalf / 2];
+        tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
+        tmem_ld32(tS + 64 + c0, reinterpret_cast<uint32_t*>(g));
+        tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
+        for (int c = 0; c < kHalf; c += 2) {
+          fma2(s[c], s[c + 1], c2, nl);
+          s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
+          add_mul2(g[c], g[c + 1], nd, nd, s[c], s[c + 1]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
+        tmem_st16(tS + 64 + c0, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&q.p[w]);
       }
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-      tmem_st16(tS + 64 + c0, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&q.p[w]);
-    }
-    if (n > 0) {
-      ok = bounded(&q.acc, 0) && ok;
-      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || (n > 0 && !(ok = all_wait(&q.acc_full, at.items & 1)))) break;
       tc_fence_after();
-    }
-    if (ok) {   // a quarter of the channels each
-      const int c0 = warp / 4 * (D / 4);
-      store_acc<D / 4>(tmem + 256 + D + c0 + lanes, n > 0, a.scale,
-                       i < a.T ? static_cast<__nv_bfloat16*>(a.dq) + (((long long)b * a.T + i) * a.H + h) * D + c0
+      const int o = warp / 4 * (D / 4);   // a quarter of the channels each
+      store_acc<D / 4>(tmem + 256 + D + o + lanes, n > 0, a.scale,
+                       i < a.T ? static_cast<__nv_bfloat16*>(a.dq) + (((long long)x.b * a.T + i) * a.H + x.h) * D + o
                                : nullptr,
                        nullptr);
+      tc_fence_before();
+      if (n > 0) mbar_arrive(&q.acc_empty);
+      at.steps += n, at.items += n > 0;
     }
-    tc_fence_before();
   } else if (warp == kLoadWarp) {
-    const int fix_tile = len < a.S && len % kN ? len / kN : -1;   // its K rows from len on become 0
-    int issued = 0, n_fix = 0;
-    bool ok = true;
-    if (lane == 0 && n > 0) {
-      mbar_expect_tx(&q.own, 2 * L::kOwn);
-      for (int c = 0; c < D / 64; ++c) {
-        tma_load_4d(sm + L::oX + c * kM * 128, &tmQ, &q.own, 64 * c, h, i0, b);
-        tma_load_4d(sm + L::oY + c * kM * 128, &tmO, &q.own, 64 * c, h, i0, b);
+    uint32_t n_fix = 0;
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const RowItem x(a, n_block, it);
+      const int fix_tile = x.len < a.S && x.len % kN ? x.len / kN : -1;   // its K rows from len on become 0
+      for (int k = 0; k < x.tiles.n; ++k) {
+        const uint32_t gi = at.steps, st = gi % kStages;
+        const int t0 = x.tiles[k] * kN;
+        if (gi >= kStages && !(ok = all_wait(&q.empty[st], (gi / kStages - 1) & 1))) break;
+        uint64_t* full = x.tiles[k] == fix_tile ? &q.fix : &q.full[st];
+        if (lane == 0) {
+          mbar_expect_tx(full, 2 * L::kTile);
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmK, full, 64 * c, x.hk, t0, x.b);
+            tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmV, full, 64 * c, x.hk, t0, x.b);
+          }
+        }
+        if (k == 0) {
+          if (at.items > 0 && !(ok = all_wait(&q.own_empty, (at.items - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_expect_tx(&q.own_full, 2 * L::kOwn);
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_4d(sm + L::oX + c * kM * 128, &tmQ, &q.own_full, 64 * c, x.h, x.i0, x.b);
+              tma_load_4d(sm + L::oY + c * kM * 128, &tmO, &q.own_full, 64 * c, x.h, x.i0, x.b);
+            }
+          }
+          ++at.items;
+        }
+        if (full == &q.fix) {
+          if (!(ok = all_wait(&q.fix, n_fix & 1))) break;
+          ++n_fix;
+          const int r0 = x.len % kN;
+          for (int e = lane; e < (kN - r0) * 8 * (D / 64); e += 32) {
+            const int c = e / ((kN - r0) * 8), y = e % ((kN - r0) * 8);
+            reinterpret_cast<uint4*>(sm + L::oA + st * L::kTile + c * kN * 128 + r0 * 128)[y] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q.full[st]);
+        }
+        ++at.steps;
       }
     }
-    for (int k = 0; k < n; ++k) {
-      const int st = k % kStages, t0 = tiles[k] * kN;
-      if (k >= kStages) ok = bounded(&q.empty[st], (k / kStages - 1) & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      uint64_t* full = tiles[k] == fix_tile ? &q.fix : &q.full[st];
-      if (lane == 0) {
-        mbar_expect_tx(full, 2 * L::kTile);
-        for (int c = 0; c < D / 64; ++c) {
-          tma_load_4d(sm + L::oA + st * L::kTile + c * kN * 128, &tmK, full, 64 * c, hk, t0, b);
-          tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmV, full, 64 * c, hk, t0, b);
-        }
-      }
-      if (tiles[k] == fix_tile) {
-        ok = bounded(&q.fix, n_fix & 1);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        ++n_fix;
-        const int r0 = len % kN;
-        for (int e = lane; e < (kN - r0) * 8 * (D / 64); e += 32) {
-          const int c = e / ((kN - r0) * 8), x = e % ((kN - r0) * 8);
-          reinterpret_cast<uint4*>(sm + L::oA + st * L::kTile + c * kN * 128 + r0 * 128)[x] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q.full[st]);
-      }
-      issued = k + 1;
+    load_end(q, at);
+  } else if (warp == kMmaWarp) {
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const RowItem x(a, n_block, it);
+      if (x.tiles.n > 0) ok = scores_item<D>(q, sm, tmem, at, x.tiles.n);
     }
-    if (n > 0) pipe_drain(q, issued);
-  } else if (warp == kMmaWarp && n > 0) {
-    pipe_mma<D, false>(q, sm, tmem, n);
+    mma_end(&q.end[0]);
+  } else if (warp == kMmaWarp + 1) {
+    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      const RowItem x(a, n_block, it);
+      if (x.tiles.n > 0) ok = sums_item<D, false>(q, sm, tmem, at, x.tiles.n);
+    }
+    mma_end(&q.end[1]);
   }
   __syncthreads();
   tc_fence_after();
@@ -482,11 +574,12 @@ void cut_far(AttnArgs& a) {
 }
 
 template <int D>
-cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
+cudaError_t bwd(const AttnArgs& a, int sms, cudaStream_t st) {
   using L = Smem<D>;
   constexpr int LK = D / 8;
   const long long rows = (long long)a.B * a.Tp * a.H;
-  attn_rows_kernel<D><<<static_cast<unsigned>((rows * LK + 255) / 256), 256, 0, st>>>(a);
+  const long long per = 256 / LK * kRowsAhead;
+  attn_rows_kernel<D><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(a);
   const long long o_st = (long long)a.H * D, o_sb = o_st * a.T;
   CUtensorMap q, o, k, v;
   auto maps = [&](int q_rows, int k_rows) {
@@ -500,11 +593,12 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     e = cudaFuncSetAttribute(attn_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   if (!maps(kN, kM)) return cudaErrorInvalidValue;
-  const long long items = (a.S + kM - 1) / kM + a.n_far;
-  attn_dkv_tc_kernel<D><<<static_cast<unsigned>(items * a.B * a.Hkv), kThreads, L::kBytes, st>>>(q, o, k, v, a);
+  auto grid = [&](long long items) { return static_cast<unsigned>(items < sms ? items : sms); };
+  const long long key_items = ((long long)(a.S + kM - 1) / kM + a.n_far) * a.B * a.Hkv;
+  attn_dkv_tc_kernel<D><<<grid(key_items), kThreads, L::kBytes, st>>>(q, o, k, v, a);
   if (!maps(kM, kN)) return cudaErrorInvalidValue;
-  attn_dq_tc_kernel<D><<<static_cast<unsigned>((long long)a.B * a.H * ((a.T + kM - 1) / kM)), kThreads, L::kBytes,
-                         st>>>(q, o, k, v, a);
+  const long long row_items = (long long)a.B * a.H * ((a.T + kM - 1) / kM);
+  attn_dq_tc_kernel<D><<<grid(row_items), kThreads, L::kBytes, st>>>(q, o, k, v, a);
   if (a.n_far) attn_sink_join_kernel<D><<<static_cast<unsigned>((long long)a.B * a.Hkv * 2 * a.n_sink), D, 0, st>>>(a);
   return cudaGetLastError();
 }
@@ -519,14 +613,14 @@ size_t attn_bwd_tc_workspace(const AttnArgs& in) {
          (a.n_far ? align256(static_cast<size_t>(a.B) * a.Hkv * (1 + a.n_far) * 2 * a.n_sink * a.d * 4) : 0);
 }
 
-cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st) {
+cudaError_t launch_attn_bwd_tc(AttnArgs a, int sms, void* workspace, cudaStream_t st) {
   cut_far(a);
   const size_t rows = align256(static_cast<size_t>(a.B) * a.H * a.Tp * 4);
   char* p = static_cast<char*>(workspace);
   a.nlse2 = reinterpret_cast<float*>(p);
   a.delta = reinterpret_cast<float*>(p + rows);
   a.sink_part = reinterpret_cast<float*>(p + 2 * rows);
-  return a.d == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
+  return a.d == 64 ? bwd<64>(a, sms, st) : bwd<128>(a, sms, st);
 }
 
 }  // namespace dr

@@ -13,7 +13,7 @@ cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 bool attn_tc_supported(const AttnArgs& a, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, int sms, cudaStream_t st);
 size_t attn_bwd_tc_workspace(const AttnArgs& a);
-cudaError_t launch_attn_bwd_tc(AttnArgs a, void* workspace, cudaStream_t st);
+cudaError_t launch_attn_bwd_tc(AttnArgs a, int sms, void* workspace, cudaStream_t st);
 int attn_step_pieces(const AttnStepArgs& a, int dtype, int sms);
 cudaError_t launch_attn_step(const AttnStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_fill(const AttnArgs& a, int dtype, void* kc, void* vc, cudaStream_t st);
@@ -199,7 +199,7 @@ int dr_window_attn_bwd(const dr_attn* a, const void* q, const void* k, const voi
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = const_cast<void*>(out), r.lse = const_cast<float*>(lse);
   r.d_out = d_out, r.dq = dq, r.dk = dk, r.dv = dv;
-  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_bwd_tc(r, workspace, stream_of(stream)));
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_bwd_tc(r, sm_count(), workspace, stream_of(stream)));
   r.delta = static_cast<float*>(workspace);
   return status_of(launch_attn_bwd_simt(r, a->dtype, stream_of(stream)));
 }

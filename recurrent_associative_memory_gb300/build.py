@@ -23,7 +23,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "-Xptxas", "-warn-spills", "--expt-relaxed-constexpr"]
 # compiled as whole programs: relocatable device code would ignore their register split
-WHOLE = ("attn_tc.cu",)
+WHOLE = ("attn_tc.cu", "attn_bwd_tc.cu")
 
 
 def nvcc() -> str:

@@ -30,14 +30,21 @@ using namespace attn;
 constexpr int kThreads = 640;
 constexpr int kLoadWarp = 16, kMmaWarp = 17;   // and the one after it
 constexpr int kHalf = 32;
+// registers per thread of the dK/dV kernel: 4 x 104 + 64 = 5 x 96, what the launch takes
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSoftmaxRegs + kOtherRegs == 5 * kLaunchRegs, "a larger sum would wait for ever");
 constexpr int kN = 64;         // rows of a tile on the walked axis
-constexpr int kStages = 4;
 
-template <int D> struct Smem {
+// dK/dV: few long items, four stages.  dQ: many short ones, so the next item's own tiles are
+// loaded behind this one (their load takes 5000 cycles, as long as four steps), three stages.
+template <int D, bool KV> struct Smem {
+  static constexpr int kStages = KV ? 4 : 3, kOwns = KV ? 1 : 2;
   static constexpr int kOwn = kM * D * 2, kTile = kN * D * 2;
-  static constexpr int oX = 0, oY = kOwn, oA = 2 * kOwn, oB = oA + kStages * kTile;
-  static constexpr int oVec = oB + kStages * kTile, kBytes = oVec + kStages * 2 * kN * 4 + 1024;
+  static constexpr int oX = 0, oY = kOwn, kOwnStride = 2 * kOwn;
+  static constexpr int oA = kOwns * kOwnStride, oB = oA + kStages * kTile;
+  static constexpr int oVec = oB + kStages * kTile, kBytes = oVec + (KV ? kStages * 2 * kN * 4 : 0) + 1024;
 };
+constexpr int kMostStages = 4;
 
 // Column of k-step k of P or dS: each thread leaves its 32 values, packed in 16 columns,
 // over the first of the 32 that it read, so the two threads of a row need no barrier.
@@ -58,15 +65,24 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
   constexpr int LK = D / 8, G = 256 / LK;
   const int c = 8 * (threadIdx.x % LK);
-  const long long e0 = (long long)blockIdx.x * (G * kRowsAhead) + threadIdx.x / LK;   // [B,Tp,H]
-  const long long all = (long long)a.B * a.Tp * a.H;
+  // a block's first row by one long division, its others by short ones
+  const long long all = (long long)a.B * a.Tp * a.H, e0 = (long long)blockIdx.x * (G * kRowsAhead);
+  const long long bt0 = e0 / a.H;
+  const int h0 = static_cast<int>(e0 - bt0 * a.H), b0 = static_cast<int>(bt0 / a.Tp),
+            t0 = static_cast<int>(bt0 - (long long)b0 * a.Tp);
   uint4 o[kRowsAhead], g[kRowsAhead];
+  int t[kRowsAhead];
+  long long bh[kRowsAhead];
 #pragma unroll
   for (int r = 0; r < kRowsAhead; ++r) {
-    const long long e = e0 + r * G, bt = e / a.H;
-    const int t = bt % a.Tp;
-    const bool in = e < all && t < a.T;
-    const long long at = ((bt / a.Tp * a.T + t) * a.H + e % a.H) * D + c;
+    const int x = threadIdx.x / LK + r * G;
+    const uint32_t hh = h0 + x, tt = t0 + hh / a.H, h = hh % a.H;
+    t[r] = tt % a.Tp;
+    const int b = b0 + tt / a.Tp;
+    bh[r] = (long long)b * a.H + h;
+    const bool in = e0 + x < all && t[r] < a.T;
+    if (e0 + x >= all) t[r] = -1;
+    const long long at = (((long long)b * a.T + t[r]) * a.H + h) * D + c;
     o[r] = in ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + at) : make_uint4(0, 0, 0, 0);
     g[r] = in ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_out) + at) : make_uint4(0, 0, 0, 0);
   }
@@ -79,13 +95,10 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
     for (int i = 0; i < 8; ++i) s += x[i] * y[i];
 #pragma unroll
     for (int w = LK / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    const long long e = e0 + r * G, bt = e / a.H;
-    if (c || e >= all) continue;
-    const int t = bt % a.Tp;
-    const long long bh = bt / a.Tp * a.H + e % a.H;
-    const float lse = t < a.T ? a.lse[bh * a.T + t] : -INFINITY;
-    a.nlse2[bh * a.Tp + t] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
-    a.delta[bh * a.Tp + t] = -s;
+    if (c || t[r] < 0) continue;
+    const float lse = t[r] < a.T ? a.lse[bh[r] * a.T + t[r]] : -INFINITY;
+    a.nlse2[bh[r] * a.Tp + t[r]] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    a.delta[bh[r] * a.Tp + t[r]] = -s;
   }
 }
 
@@ -97,16 +110,15 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
 // ones (Q, dO; K, V).  Per step: slot S = X A^T, slot dP = Y B^T; then, from what the softmax
 // warps left in their place, acc0 += [S] B (dK/dV only) and acc1 += [dP] A.
 struct Pipe {
-  uint64_t own_full, own_empty, full[kStages], empty[kStages], fix, s[2], p[2], free[2], acc_full, acc_empty, end[2];
+  uint64_t own_full[2], own_empty[2], full[kMostStages], empty[kMostStages], fix, s[2], p[2], free[2], acc_full, acc_empty, end[2];
   uint32_t tmem;
 };
 
 __device__ __forceinline__ void pipe_init(Pipe& q, int tid, int warp) {
   if (tid == 0) {
-    mbar_init(&q.own_full, 1), mbar_init(&q.own_empty, 1);
-    for (int i = 0; i < kStages; ++i) mbar_init(&q.full[i], 1), mbar_init(&q.empty[i], 1);
+    for (int i = 0; i < kMostStages; ++i) mbar_init(&q.full[i], 1), mbar_init(&q.empty[i], 1);
     mbar_init(&q.fix, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 256), mbar_init(&q.free[i], 1), mbar_init(&q.end[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&q.own_full[i], 1), mbar_init(&q.own_empty[i], 1), mbar_init(&q.s[i], 1), mbar_init(&q.p[i], 256), mbar_init(&q.free[i], 1), mbar_init(&q.end[i], 1);
     mbar_init(&q.acc_full, 1), mbar_init(&q.acc_empty, 512);
     fence_mbar_init();
   }
@@ -129,13 +141,15 @@ struct Walk { uint32_t items, steps; };
 // products runs dry; two warps cover each other's.  A warp walks together and one lane
 // issues, so that the descriptors stay in uniform registers.  TMEM: slot i at 128 i (S, then
 // 64 columns on dP), accumulators at 256 and 256 + D.  KV: the dK/dV products, else dQ's.
-template <int D>
+template <int D, bool KV>
 __device__ __forceinline__ bool scores_item(Pipe& q, uint8_t* sm, uint32_t tm, Walk& at, int n) {
-  using L = Smem<D>;
-  constexpr uint32_t ID_S = idesc_bf16(kM, kN, 0, 0);
-  const uint64_t x = desc_kmajor(smem_u32(sm + L::oX)), y = desc_kmajor(smem_u32(sm + L::oY));
+  using L = Smem<D, KV>;
+  constexpr uint32_t kStages = L::kStages, ID_S = idesc_bf16(kM, kN, 0, 0);
+  const uint32_t own = at.items % L::kOwns;
+  const uint64_t x = desc_kmajor(smem_u32(sm + L::oX + own * L::kOwnStride));
+  const uint64_t y = desc_kmajor(smem_u32(sm + L::oY + own * L::kOwnStride));
   const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB);
-  if (!all_wait(&q.own_full, at.items & 1)) return false;
+  if (!all_wait(&q.own_full[own], (at.items / L::kOwns) & 1)) return false;
   for (int i = 0; i < n; ++i, ++at.steps) {
     const uint32_t gi = at.steps, slot = gi & 1, st = gi % kStages, s = tm + 128 * slot;
     if (!all_wait(&q.full[st], (gi / kStages) & 1)) return false;
@@ -147,7 +161,7 @@ __device__ __forceinline__ bool scores_item(Pipe& q, uint8_t* sm, uint32_t tm, W
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) mma_bf16(s + 64, y + step_kmajor<kM>(k), dB + step_kmajor<kN>(k), ID_S, k > 0);
       mma_commit(&q.s[slot]);
-      if (i == n - 1) mma_commit(&q.own_empty);
+      if (i == n - 1) mma_commit(&q.own_empty[own]);
     }
   }
   at.items += 1;
@@ -156,8 +170,8 @@ __device__ __forceinline__ bool scores_item(Pipe& q, uint8_t* sm, uint32_t tm, W
 
 template <int D, bool KV>
 __device__ __forceinline__ bool sums_item(Pipe& q, uint8_t* sm, uint32_t tm, Walk& at, int n) {
-  using L = Smem<D>;
-  constexpr uint32_t ID_ACC = idesc_bf16(kM, D, 0, 1);
+  using L = Smem<D, KV>;
+  constexpr uint32_t kStages = L::kStages, ID_ACC = idesc_bf16(kM, D, 0, 1);
   const uint32_t A = smem_u32(sm + L::oA), B = smem_u32(sm + L::oB);
   if (at.items > 0 && !all_wait(&q.acc_empty, (at.items - 1) & 1)) return false;
   for (int j = 0; j < n; ++j, ++at.steps) {
@@ -192,10 +206,30 @@ __device__ __forceinline__ void mma_end(uint64_t* bar) {
 }
 
 // The load warp's end: no copy may be in flight when the CTA ends.
+template <class L>
 __device__ __forceinline__ void load_end(Pipe& q, const Walk& at) {
-  if (at.items > 0) wait_phase(&q.own_full, (at.items - 1) & 1);
-  for (uint32_t i = at.steps > kStages ? at.steps - kStages : 0; i < at.steps; ++i)
-    wait_phase(&q.full[i % kStages], (i / kStages) & 1);
+  for (uint32_t i = at.items > L::kOwns ? at.items - L::kOwns : 0; i < at.items; ++i)
+    wait_phase(&q.own_full[i % L::kOwns], (i / L::kOwns) & 1);
+  for (uint32_t i = at.steps > L::kStages ? at.steps - L::kStages : 0; i < at.steps; ++i)
+    wait_phase(&q.full[i % L::kStages], (i / L::kStages) & 1);
+}
+
+// Loads the own tiles of the load warp's next item: 128 rows from `row` of two tensors.
+template <class L, int D>
+__device__ __forceinline__ bool load_own(Pipe& q, uint8_t* sm, Walk& at, int lane, const CUtensorMap& X,
+                                         const CUtensorMap& Y, int h, int row, int b) {
+  const uint32_t own = at.items % L::kOwns;
+  if (at.items >= L::kOwns && !all_wait(&q.own_empty[own], (at.items / L::kOwns - 1) & 1)) return false;
+  if (lane == 0) {
+    uint8_t* to = sm + own * L::kOwnStride;
+    mbar_expect_tx(&q.own_full[own], 2 * L::kOwn);
+    for (int c = 0; c < D / 64; ++c) {
+      tma_load_4d(to + L::oX + c * kM * 128, &X, &q.own_full[own], 64 * c, h, row, b);
+      tma_load_4d(to + L::oY + c * kM * 128, &Y, &q.own_full[own], 64 * c, h, row, b);
+    }
+  }
+  ++at.items;
+  return true;
 }
 
 // 128 lanes' rows of N accumulator columns -> bf16 rows (or fp32 parts)
@@ -234,9 +268,9 @@ __device__ __forceinline__ void store_acc(uint32_t tacc, bool any, float f, __nv
 struct KeyItem {
   int hk, b, j0, len, i_begin, per, n, piece;   // steps: `per` tiles of kN rows from i_begin, for each head
   bool far;
-  __device__ __forceinline__ KeyItem(const AttnArgs& a, long long it) {
-    hk = static_cast<int>(it % a.Hkv), b = static_cast<int>(it / a.Hkv % a.B);
-    const int item = static_cast<int>(it / a.Hkv / a.B);
+  __device__ __forceinline__ KeyItem(const AttnArgs& a, uint32_t it) {
+    hk = it % a.Hkv, b = it / a.Hkv % a.B;
+    const int item = it / a.Hkv / a.B;
     far = item < a.n_far;
     piece = far ? 1 + item : 0;
     j0 = far ? 0 : (item - a.n_far) * kM;
@@ -260,39 +294,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        AttnArgs a) {
-  using L = Smem<D>;
+  using L = Smem<D, true>;
+  constexpr uint32_t kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Pipe q;
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
-  const long long n_item = ((long long)(a.S + kM - 1) / kM + a.n_far) * a.B * a.Hkv;
+  const uint32_t n_item = ((a.S + kM - 1) / kM + a.n_far) * a.B * a.Hkv;   // a grid's worth: below 2^31
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
   Walk at = {0, 0};
   bool ok = true;
 
   if (warp < 16) {   // two threads per key; the slots' warps take the steps in turn
+    more_registers<kSoftmaxRegs>();
     const int w = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, c0 = kHalf * half;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
-      const KeyItem x(a, it);
-      const int j = x.j0 + row;
-      const int key_hi = j < a.n_sink ? INT_MAX : j + a.window - 1;   // last position that sees this key
-      for (int i = (w - at.steps) & 1; i < x.n; i += 2) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+      int n, per, first, j0, len;
+      {
+        const KeyItem x(a, it);
+        n = x.n, per = x.per, first = a.q_start + x.i_begin, j0 = x.j0, len = x.len;
+      }
+      const int j = j0 + row;
+      for (int i = (w - at.steps) & 1; i < n; i += 2) {
         const uint32_t gi = at.steps + i, st = gi % kStages;
         if (!(ok = all_wait(&q.s[w], (gi >> 1) & 1))) break;
         // this stage's numbers (with its tiles)
         if (!(ok = all_wait(&q.full[st], (gi / kStages) & 1))) break;
         tc_fence_after();
         const uint32_t nl = smem_u32(sm + L::oVec + st * 2 * kN * 4) + 4 * c0, nd = nl + kN * 4;
-        const int p0 = a.q_start + x.i_begin + (i % x.per) * kN;
-        const bool whole = p0 >= x.j0 + kM - 1 && x.j0 + kM <= x.len &&
-                           (p0 + kN - 1 - x.j0 < a.window || x.j0 + kM <= a.n_sink);
+        const int p0 = first + (i % per) * kN;
+        const bool whole = p0 >= j0 + kM - 1 && j0 + kM <= len &&
+                           (p0 + kN - 1 - j0 < a.window || j0 + kM <= a.n_sink);
         // the rows of this half that see this key, as bits
         const uint32_t word =
-            j < x.len ? bits_below(key_hi == INT_MAX ? 32 : key_hi - p0 + 1 - c0) & ~bits_below(j - p0 - c0) : 0u;
+            j < len ? bits_below(j < a.n_sink ? 32 : j + a.window - p0 - c0) & ~bits_below(j - p0 - c0) : 0u;
         float s[kHalf], g[kHalf];
         uint32_t pk[kHalf / 2];
         tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(s));
@@ -331,8 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&q.p[w]);
       }
-      if (!ok || (x.n > 0 && !(ok = all_wait(&q.acc_full, at.items & 1)))) break;
+      if (!ok || (n > 0 && !(ok = all_wait(&q.acc_full, at.items & 1)))) break;
       tc_fence_after();
+      const KeyItem x(a, it);   // again: not carried through the steps
       // slot 0's warps: dV, slot 1's: dK, half of the channels each
       const long long o = (((long long)x.b * a.S + j) * a.Hkv + x.hk) * D + half * (D / 2);
       const bool part = a.n_far && x.j0 == 0 && j < a.n_sink;
@@ -345,8 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x.n > 0) mbar_arrive(&q.acc_empty);
       at.steps += x.n, at.items += x.n > 0;
     }
-  } else if (warp == kLoadWarp) {   // the whole warp walks, one lane issues
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+  } else {
+    fewer_registers<kOtherRegs>();
+  }
+  if (warp == kLoadWarp) {   // the whole warp walks, one lane issues
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const KeyItem x(a, it);
       for (int i = 0; i < x.n; ++i) {
         const uint32_t gi = at.steps, st = gi % kStages;
@@ -364,27 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++at.steps;
         if (i == 0) {
-          if (at.items > 0 && !(ok = all_wait(&q.own_empty, (at.items - 1) & 1))) break;
-          if (lane == 0) {
-            mbar_expect_tx(&q.own_full, 2 * L::kOwn);
-            for (int c = 0; c < D / 64; ++c) {
-              tma_load_4d(sm + L::oX + c * kM * 128, &tmK, &q.own_full, 64 * c, x.hk, x.j0, x.b);
-              tma_load_4d(sm + L::oY + c * kM * 128, &tmV, &q.own_full, 64 * c, x.hk, x.j0, x.b);
-            }
-          }
-          ++at.items;
+          if (!(ok = load_own<L, D>(q, sm, at, lane, tmK, tmV, x.hk, x.j0, x.b))) break;
         }
       }
     }
-    load_end(q, at);
+    load_end<L>(q, at);
   } else if (warp == kMmaWarp) {
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const KeyItem x(a, it);
-      if (x.n > 0) ok = scores_item<D>(q, sm, tmem, at, x.n);
+      if (x.n > 0) ok = scores_item<D, true>(q, sm, tmem, at, x.n);
     }
     mma_end(&q.end[0]);
   } else if (warp == kMmaWarp + 1) {
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const KeyItem x(a, it);
       if (x.n > 0) ok = sums_item<D, true>(q, sm, tmem, at, x.n);
     }
@@ -415,10 +450,10 @@ __global__ void __launch_bounds__(D) attn_sink_join_kernel(AttnArgs a) {
 struct RowItem {
   int h, i0, b, hk, len;
   KeyTiles tiles;
-  __device__ __forceinline__ RowItem(const AttnArgs& a, int n_block, long long it)
-      : h(static_cast<int>(it % a.H)),
-        i0(static_cast<int>(it / a.H % n_block) * kM),
-        b(static_cast<int>(it / a.H / n_block)),
+  __device__ __forceinline__ RowItem(const AttnArgs& a, int n_block, uint32_t it)
+      : h(it % a.H),
+        i0(it / a.H % n_block * kM),
+        b(it / a.H / n_block),
         hk(h / a.G),
         len(uniform(real_len(a.lens, b, a.S))),
         tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN) {}
@@ -429,13 +464,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       AttnArgs a) {
-  using L = Smem<D>;
+  using L = Smem<D, false>;
+  constexpr uint32_t kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Pipe q;
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + kM - 1) / kM;
-  const long long n_item = (long long)a.B * a.H * n_block;
+  const uint32_t n_item = a.B * a.H * n_block;   // a grid's worth: below 2^31
   pipe_init(q, tid, warp);
   const uint32_t tmem = uniform(q.tmem);
   Walk at = {0, 0};
@@ -446,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + 128 * w + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const RowItem x(a, n_block, it);
       const int n = x.tiles.n, i = x.i0 + row, p = a.q_start + i, p0 = a.q_start + x.i0;
       float nl = -INFINITY, nd = 0.f;
@@ -495,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kLoadWarp) {
     uint32_t n_fix = 0;
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    bool ahead = false;   // has this item's Q and dO been loaded with the last one?
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const RowItem x(a, n_block, it);
       const int fix_tile = x.len < a.S && x.len % kN ? x.len / kN : -1;   // its K rows from len on become 0
       for (int k = 0; k < x.tiles.n; ++k) {
@@ -510,16 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(sm + L::oB + st * L::kTile + c * kN * 128, &tmV, full, 64 * c, x.hk, t0, x.b);
           }
         }
-        if (k == 0) {
-          if (at.items > 0 && !(ok = all_wait(&q.own_empty, (at.items - 1) & 1))) break;
-          if (lane == 0) {
-            mbar_expect_tx(&q.own_full, 2 * L::kOwn);
-            for (int c = 0; c < D / 64; ++c) {
-              tma_load_4d(sm + L::oX + c * kM * 128, &tmQ, &q.own_full, 64 * c, x.h, x.i0, x.b);
-              tma_load_4d(sm + L::oY + c * kM * 128, &tmO, &q.own_full, 64 * c, x.h, x.i0, x.b);
-            }
+        if (k == 0 && !ahead && !(ok = load_own<L, D>(q, sm, at, lane, tmQ, tmO, x.h, x.i0, x.b))) break;
+        if (k == min(2, x.tiles.n - 1)) {
+          ahead = false;
+          if (it + gridDim.x < n_item) {
+            const RowItem y(a, n_block, it + gridDim.x);
+            ahead = y.tiles.n > 0;
+            if (ahead && !(ok = load_own<L, D>(q, sm, at, lane, tmQ, tmO, y.h, y.i0, y.b))) break;
           }
-          ++at.items;
         }
         if (full == &q.fix) {
           if (!(ok = all_wait(&q.fix, n_fix & 1))) break;
@@ -536,15 +571,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++at.steps;
       }
     }
-    load_end(q, at);
+    load_end<L>(q, at);
   } else if (warp == kMmaWarp) {
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const RowItem x(a, n_block, it);
-      if (x.tiles.n > 0) ok = scores_item<D>(q, sm, tmem, at, x.tiles.n);
+      if (x.tiles.n > 0) ok = scores_item<D, false>(q, sm, tmem, at, x.tiles.n);
     }
     mma_end(&q.end[0]);
   } else if (warp == kMmaWarp + 1) {
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const RowItem x(a, n_block, it);
       if (x.tiles.n > 0) ok = sums_item<D, false>(q, sm, tmem, at, x.tiles.n);
     }
@@ -575,7 +610,8 @@ void cut_far(AttnArgs& a) {
 
 template <int D>
 cudaError_t bwd(const AttnArgs& a, int sms, cudaStream_t st) {
-  using L = Smem<D>;
+  using KeySmem = Smem<D, true>;
+  using RowSmem = Smem<D, false>;
   constexpr int LK = D / 8;
   const long long rows = (long long)a.B * a.Tp * a.H;
   const long long per = 256 / LK * kRowsAhead;
@@ -588,22 +624,24 @@ cudaError_t bwd(const AttnArgs& a, int sms, cudaStream_t st) {
            make_map(&k, a.k, a.B, a.S, a.Hkv, D, a.k_sb, a.k_st, a.k_sh, k_rows) &&
            make_map(&v, a.v, a.B, a.S, a.Hkv, D, a.v_sb, a.v_st, a.v_sh, k_rows);
   };
-  cudaError_t e = cudaFuncSetAttribute(attn_dkv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(attn_dkv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KeySmem::kBytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    e = cudaFuncSetAttribute(attn_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowSmem::kBytes);
   if (e != cudaSuccess) return e;
   if (!maps(kN, kM)) return cudaErrorInvalidValue;
   auto grid = [&](long long items) { return static_cast<unsigned>(items < sms ? items : sms); };
   const long long key_items = ((long long)(a.S + kM - 1) / kM + a.n_far) * a.B * a.Hkv;
-  attn_dkv_tc_kernel<D><<<grid(key_items), kThreads, L::kBytes, st>>>(q, o, k, v, a);
+  attn_dkv_tc_kernel<D><<<grid(key_items), kThreads, KeySmem::kBytes, st>>>(q, o, k, v, a);
   if (!maps(kM, kN)) return cudaErrorInvalidValue;
   const long long row_items = (long long)a.B * a.H * ((a.T + kM - 1) / kM);
-  attn_dq_tc_kernel<D><<<grid(row_items), kThreads, L::kBytes, st>>>(q, o, k, v, a);
+  attn_dq_tc_kernel<D><<<grid(row_items), kThreads, RowSmem::kBytes, st>>>(q, o, k, v, a);
   if (a.n_far) attn_sink_join_kernel<D><<<static_cast<unsigned>((long long)a.B * a.Hkv * 2 * a.n_sink), D, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t attn_bwd_tc_status(int* word, cudaStream_t st) { return take_status(word, st); }
 
 size_t attn_bwd_tc_workspace(const AttnArgs& in) {
   AttnArgs a = in;

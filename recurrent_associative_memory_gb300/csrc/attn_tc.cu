@@ -28,9 +28,6 @@
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.
 // The tile that holds lens[b] has its V rows from there on zeroed in shared memory, as
 // 0 times whatever stands there may be NaN; scores are masked by selection.
-// This file is compiled as a whole program: with relocatable device code the compiler
-// ignores setmaxnreg, and a row of 128 scores does not fit the registers that an even
-// split leaves (428 bytes of spills per thread instead of 24).
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -60,10 +57,10 @@ struct Item {
   int h, i0, b, hk, len;
   TileSet set0, set1;
   KeyTiles tiles;
-  __device__ __forceinline__ Item(const AttnArgs& a, int n_block, long long it)
-      : h(static_cast<int>(it % a.H)),
-        i0(static_cast<int>(it / a.H % n_block) * 2 * kM),
-        b(static_cast<int>(it / a.H / n_block)),
+  __device__ __forceinline__ Item(const AttnArgs& a, int n_block, uint32_t it)
+      : h(it % a.H),
+        i0(it / a.H % n_block * 2 * kM),
+        b(it / a.H / n_block),
         hk(h / a.G),
         len(uniform(real_len(a.lens, b, a.S))),
         set0(a, i0, len),
@@ -93,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   const int n_block = (a.T + 2 * kM - 1) / (2 * kM);
-  const long long n_item = (long long)a.B * a.H * n_block;
+  const uint32_t n_item = a.B * a.H * n_block;   // a grid's worth: below 2^31
 
   if (tid == 0) {
     mbar_init(&b_qf, 1), mbar_init(&b_qe, 2), mbar_init(&b_fix, 1);
@@ -131,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0;   // phases of S and O that have gone by
     bool ok = true;
 
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const Item x(a, n_block, it);
       const int i = x.i0 + w * kM + row, p = a.q_start + i;
       const int p0 = a.q_start + x.i0 + w * kM, p1 = p0 + kM - 1;
@@ -271,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {   // ----------------------------------------------------- loads
     uint32_t nk = 0, nv = 0, nq = 0, n_fix = 0;   // loads issued so far
     bool ok = true;
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const Item x(a, n_block, it);
       const int fix_tile = x.len < a.S && x.len % kM ? x.len / kM : -1;   // its V rows from len on become 0
       for (int n = 0; n < x.tiles.n; ++n) {
@@ -327,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o = tmem + 256 + w * D, s = tmem + w * 128;
     uint32_t nt = 0, nq = 0, np = 0, turn = 0;   // key tiles, items, P tiles and turns gone by
     bool ok = true;
-    for (long long it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < n_item && ok; it += gridDim.x) {
       const Item x(a, n_block, it);
       if (x.tiles.n == 0) continue;
       const TileSet& set = w ? x.set1 : x.set0;
@@ -415,13 +412,7 @@ bool attn_tc_supported(const AttnArgs& a, int dtype) {
          map_strides_ok(a.B, a.S, a.Hkv, a.v_sb, a.v_st, a.v_sh);
 }
 
-// Enqueues the read and the clearing of this translation unit's status word.
-cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st) {
-  static const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-}
+cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st) { return take_status(word, st); }
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, int sms, cudaStream_t st) {
   return a.d == 64 ? fwd<64>(a, sms, st) : fwd<128>(a, sms, st);

@@ -1,5 +1,8 @@
 // attn_tc.cuh — what the tcgen05 window-attention kernels share: TMEM loads and stores,
 // the MMA with its A operand in TMEM, packed fp32 arithmetic, tile masks, tensor maps.
+// Their translation units are compiled as whole programs: with relocatable device code the
+// compiler ignores setmaxnreg, and a row of 128 scores does not fit the registers that an
+// even split leaves (428 bytes of spills per thread instead of none).
 #pragma once
 
 #include "layers.cuh"
@@ -191,6 +194,14 @@ template <uint32_t REGS> __device__ __forceinline__ void fewer_registers() {
 }
 
 // ------------------------------------------------------------------ host side
+
+// Enqueues the read and the clearing of this translation unit's status word.
+static inline cudaError_t take_status(int* word, cudaStream_t st) {
+  static const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+}
 
 // [B, rows, heads, d] bf16 with strides in elements; box of 64 channels x box_rows rows
 inline bool make_map(CUtensorMap* m, const void* ptr, int B, int rows, int heads, int d, long long sb,

@@ -28,6 +28,7 @@ size_t kdn_split_workspace_bytes(int B, int T, int H);
 bool chunk_bwd_supported(int variant, int dtype, int dk, int dv, int chunk);
 size_t chunk_bwd_workspace_bytes(int variant, int B, int T, int H);
 cudaError_t attn_fwd_tc_status(int* word, cudaStream_t st);
+cudaError_t attn_bwd_tc_status(int* word, cudaStream_t st);
 cudaError_t launch_chunk_bwd(const FwdArgs& fa, const void* d_out, const float* dS_final,
                              const dr_grads& g, void* workspace, cudaStream_t st);
 
@@ -283,10 +284,11 @@ int dr_get_device_status(dr_stream_t stream) {
   if (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
       cudaSuccess)
     return DR_ERR_CUDA;
-  int tc = 0;   // the whole-program translation unit keeps its own word
-  if (attn_fwd_tc_status(&tc, s) != cudaSuccess) return DR_ERR_CUDA;
+  int fwd = 0, bwd = 0;   // whole-program translation units keep their own words
+  if (attn_fwd_tc_status(&fwd, s) != cudaSuccess || attn_bwd_tc_status(&bwd, s) != cudaSuccess)
+    return DR_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return DR_ERR_CUDA;
-  return h ? h : tc;
+  return h ? h : (fwd ? fwd : bwd);
 }
 
 }  // extern "C"

@@ -431,9 +431,10 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) cache_fill_kernel(AttnArgs a, T* kc, T* vc) {
   const int C = a.n_sink + a.window, per = a.d / 8;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long row = e / per;   // [B,Hkv,C]
-  if (row >= (long long)a.B * a.Hkv * C) return;
-  const int slot = row % C, hk = (row / C) % a.Hkv, b = row / C / a.Hkv, c = 8 * (e % per);
+  long long row, bh, rb;   // row [B,Hkv,C]
+  const int c = 8 * div_mod(e, per, row), slot = div_mod(row, C, bh), hk = div_mod(bh, a.Hkv, rb);
+  if (rb >= a.B) return;
+  const int b = rb;
   const int len = real_len(a.lens, b, a.S);
   int p = slot;                   // the last position before len that lives in this slot
   if (slot >= a.n_sink) {

@@ -143,6 +143,18 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// q = e / d, returns e mod d (e >= 0): short where it fits, a long division takes a hundred
+// instructions
+__device__ __forceinline__ int div_mod(long long e, int d, long long& q) {
+  if (e >> 31 == 0) {
+    const uint32_t u = static_cast<uint32_t>(e), r = u / static_cast<uint32_t>(d);
+    q = r;
+    return static_cast<int>(u - r * static_cast<uint32_t>(d));
+  }
+  q = e / d;
+  return static_cast<int>(e - q * d);
+}
+
 // Two fp32 values in one register pair, and the arithmetic that takes both at once.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float x, float y) {

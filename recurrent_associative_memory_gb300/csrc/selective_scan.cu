@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;   // [B T][G][2N]
   const long long bt_n = (long long)a.B * a.T;
   if (e >= bt_n * a.G * 2 * a.N) return;
-  const int k = e % (2 * a.N), g = (e / (2 * a.N)) % a.G;
-  const long long bt = e / (2 * a.N) / a.G;
+  long long q, bt;
+  const int k = div_mod(e, 2 * a.N, q), g = div_mod(q, a.G, bt);
   const int per = tiles / a.G;
   float v = 0.f;
   for (int i = 0; i < per; ++i) v += a.part_bc[((g * per + i) * bt_n + bt) * 2 * a.N + k];

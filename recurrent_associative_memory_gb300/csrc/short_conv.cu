@@ -84,10 +84,11 @@ template <int K, typename T, int CH>
 __global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvArgs a) {
   const int groups = a.D / CH, runs = (a.T + kRun - 1) / kRun;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const int c = CH * (e % groups);
-  const long long r = e / groups;
-  if (r >= (long long)a.B * runs) return;
-  const int b = r / runs, t0 = (r % runs) * kRun, last = min(t0 + kRun, a.T);
+  long long r, rb;
+  const int c = CH * div_mod(e, groups, r);
+  const int t0 = div_mod(r, runs, rb) * kRun, last = min(t0 + kRun, a.T);
+  if (rb >= a.B) return;
+  const int b = rb;
   const int len = real_len(a.lens, b, a.T), state0 = len - (K - 1);
   f2 w[K], bias, x[K];
   const T* xp = static_cast<const T*>(a.x) + b * a.x_sb + t0 * a.x_st + c;
@@ -257,8 +258,8 @@ template <int K, typename T, int CH>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
   const int groups = a.D / CH;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const int c = CH * (e % groups);
-  const int b = e / groups;
+  long long b;
+  const int c = CH * div_mod(e, groups, b);
   if (b >= a.B) return;
   f2 w[K], bias, x[K];
 #pragma unroll

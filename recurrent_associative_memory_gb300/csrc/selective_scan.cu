@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPiece = 32;    // tokens of a backward piece
+constexpr int kTile = 16;     // tokens in shared memory at a time (forward)
 constexpr int kSub = 8;       // tokens whose states are in registers (backward)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -40,7 +41,9 @@ template <int N> struct Shape {
   static constexpr int LPC = N / 4;               // lanes per pair of channels
   static constexpr int CPC = 2 * kThreads / LPC;  // channels per CTA
   static constexpr int CW = 32 / LPC;             // pairs of channels per warp
-  static constexpr int kTile = N < 32 ? N : 32;   // tokens in shared memory at a time (forward)
+  static constexpr int HP = CPC / 2;              // pairs of channels per CTA
+  static constexpr int WC = 2 * CW;               // channels per warp
+  static constexpr int ROWS = kThreads / HP;      // tokens that the CTA loads at a time (backward)
 };
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|).  The alternating series below
@@ -57,28 +60,84 @@ __device__ __forceinline__ float softplus_f(float v) {
   return fmaxf(v, 0.f) + (e < 0.0625f ? s : lg * kLn2);
 }
 
-// 8 neighbouring values as loaded
-template <typename T> struct alignas(16) Raw8 { T v[8]; };
+// Two neighbouring channels as loaded.  A thread's pair of channels follows its
+// neighbour's: whole 128-byte rows in global memory, and 16 bytes a lane in shared memory
+// without a conflict of banks (8 channels a thread cost a third of the time there).
+template <typename T> struct alignas(2 * sizeof(T)) Raw2 { T v[2]; };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void fetch8(Raw8<T>& r, const T* p, int n) {
+__device__ __forceinline__ Raw2<T> fetch2(const T* p, int n) {
+  Raw2<T> r;
   if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(r.v)[i] =
-          n > 0 ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint32_t*>(&r) = n > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+    else
+      *reinterpret_cast<uint2*>(&r) = n > 0 ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < n ? p[i] : from_f<T>(0.f);
+    for (int i = 0; i < 2; ++i) r.v[i] = i < n ? p[i] : from_f<T>(0.f);
   }
+  return r;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void fetch8(float (&f)[8], const T* p, int n) {
-  Raw8<T> r;
-  fetch8<T, VEC>(r, p, n);
+__device__ __forceinline__ void fetch2(float (&f)[2], const T* p, int n) {
+  const Raw2<T> r = fetch2<T, VEC>(p, n);
+  f[0] = to_f<T>(r.v[0]), f[1] = to_f<T>(r.v[1]);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store2(T* p, int n, const float (&f)[2]) {
+  Raw2<T> r;
+  r.v[0] = from_f<T>(f[0]), r.v[1] = from_f<T>(f[1]);
+  if constexpr (VEC) {
+    if (n > 0) *reinterpret_cast<Raw2<T>*>(p) = r;
+  } else {
+    if (n > 0) p[0] = r.v[0];
+    if (n > 1) p[1] = r.v[1];
+  }
+}
+
+// Rows t0 .. t0 + kTile - 1 of `width` neighbouring values, src at row 0, into shared memory by
+// one warp: in 16-byte pieces, or as wide as a row, that go on in the background; zeros in
+// place of rows from t_real on and of values from n on.
+template <typename T, bool VEC, int WIDTH>
+__device__ __forceinline__ void fetch_rows(T* dst, const T* src, long long stride, int t0, int t_real, int n, int lane) {
+  if constexpr (VEC) {
+    constexpr int ROW = WIDTH * sizeof(T), CB = ROW < 16 ? ROW : 16, PER = ROW / CB, ALL = kTile * PER;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = to_f<T>(r.v[i]);
+    for (int e0 = 0; e0 < ALL; e0 += 32) {
+      const int e = e0 + lane, t = t0 + e / PER, k = e % PER * (CB / (int)sizeof(T));
+      const bool in = t < t_real && k < n;
+      if (ALL % 32 == 0 || e < ALL)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + e * CB),
+                     "l"(in ? src + t * stride + k : src), "n"(CB), "r"(in ? CB : 0)
+                     : "memory");
+    }
+  } else {
+    for (int e = lane; e < kTile * WIDTH; e += 32) {
+      const int t = t0 + e / WIDTH, k = e % WIDTH;
+      dst[e] = t < t_real && k < n ? src[t * stride + k] : from_f<T>(0.f);
+    }
+  }
+}
+
+// kTile rows of N values to fp32, by one warp
+template <int N, typename T>
+__device__ __forceinline__ void widen_rows(float* dst, const T* src, int lane) {
+#pragma unroll
+  for (int e = 4 * lane; e < kTile * N; e += 128) {
+    float4 f;
+    if constexpr (sizeof(T) == 2) {
+      const uint2 r = *reinterpret_cast<const uint2*>(src + e);
+      f = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                      __uint_as_float(r.y & 0xffff0000u));
+    } else {
+      f = *reinterpret_cast<const float4*>(src + e);
+    }
+    *reinterpret_cast<float4*>(dst + e) = f;
+  }
 }
 
 // Sum over L lanes, STRIDE apart, of M values each: halves are exchanged as long as a
@@ -160,31 +219,39 @@ __device__ __forceinline__ float bias_of(const ScanArgs& a, int c) { return a.bi
 
 // ------------------------------------------------------------------ forward
 
-template <int N> constexpr int fwd_floats(bool full) {   // u, (skip, gate), y, B, C, bias and D
-  return Shape<N>::kTile * (Shape<N>::CPC * (full ? 5 : 2) + 2 * N) + 2 * Shape<N>::CPC;
-}
+// One warp's shared memory: (dt, dt x), B and for outputs C and y in fp32; two tiles as
+// loaded: x, dt, B and for outputs z and C.
+template <int N, typename T, bool FULL> struct FwdTile {
+  static constexpr int WC = Shape<N>::WC;
+  static constexpr int kRaw = kTile * (FULL ? 3 * WC + 2 * N : 2 * WC + N);   // values of a tile as loaded
+  static constexpr int kBytes = 4 * kTile * (FULL ? 3 * WC + 2 * N : 2 * WC + N) + 2 * kRaw * (int)sizeof(T);
+};
 
 // FULL: outputs from the state at the piece's start; otherwise the piece's end from
-// zero and its sum of dt.
+// zero and its sum of dt.  The warps share nothing and never wait for each other: with one
+// tile for the CTA, its barriers and conflicts of banks cost 166 us instead of DR_NOW_FULL
+// (B4 T2048 D2048 N16).
 template <int N, typename T, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 4 : 5) : 6) scan_fwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 3 : N == 32 ? 4 : 5) : (N > 16 ? 5 : 6)) scan_fwd_kernel(ScanArgs a) {
   using S = Shape<N>;
-  constexpr int CPC = S::CPC, LPC = S::LPC, TT = S::kTile;
-  constexpr int NV = (TT * CPC / 8 + kThreads - 1) / kThreads;   // 8-value loads per thread
+  using W = FwdTile<N, T, FULL>;
+  constexpr int CPC = S::CPC, LPC = S::LPC, WC = S::WC, TT = kTile;
+  constexpr int NP = TT / LPC;   // tokens of a tile per lane
   extern __shared__ __align__(16) float sm[];
-  float* s_B = sm;                                               // [TT][N]
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = 2 * (tid / LPC);
+  float2* s_u = reinterpret_cast<float2*>(reinterpret_cast<char*>(sm) + warp * W::kBytes);   // [TT][WC]
+  float* s_B = reinterpret_cast<float*>(s_u + TT * WC);                                    // [TT][N]
   float* s_C = s_B + TT * N;
-  float2* s_u = reinterpret_cast<float2*>(s_C + TT * N);         // [TT][CPC] dt, dt x
-  float2* s_par = s_u + TT * CPC;                                // bias, D
-  float2* s_e = s_par + CPC;                                     // D x, silu(z)
-  float* s_y = reinterpret_cast<float*>(s_e + TT * CPC);
-  const int tid = threadIdx.x, lane = tid % 32, part = tid % LPC, ch = 2 * (tid / LPC);
+  float* s_y = s_C + (FULL ? TT * N : 0);                                                  // [TT][WC]
+  T* raw = reinterpret_cast<T*>(s_y + (FULL ? TT * WC : 0));
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const ChannelTile ct(a, CPC, blockIdx.x % tiles);
   const int piece = (blockIdx.x / tiles) % a.n_piece, b = blockIdx.x / tiles / a.n_piece;
   const int t_begin = piece * a.piece, t_end = min(a.T, t_begin + a.piece);
-  const int len = real_len(a.lens, b, a.T);
+  const int len = real_len(a.lens, b, a.T), t_real = min(len, t_end);
   const int c = ct.c0 + ch, real = ct.n - ch;   // channels of the pair that exist: real > 0, > 1
+  const int wc = ct.c0 + warp * WC, wn = ct.n - warp * WC;   // the warp's channels
+  if (wn <= 0) return;
 
   Four A2[2], h[2] = {both(0), both(0)};
   float sum[2] = {0.f, 0.f};
@@ -196,75 +263,58 @@ __global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 4 : 5) : 6) scan_f
     for (int i = 0; i < 2; ++i)
       if (from && i < real) h[i] = load4(from + (long long)(c + i) * N + 4 * part);
   }
-
-  for (int e = tid; e < CPC; e += kThreads)
-    s_par[e] = make_float2(e < ct.n ? bias_of(a, ct.c0 + e) : 0.f,
-                           e < ct.n && a.Dskip ? a.Dskip[ct.c0 + e] : 0.f);
-  __syncthreads();
-  // this thread's loads of a tile: token vt, channels vc .. vc + 7 of the tile; B and C
-  constexpr int NB = (TT * N + kThreads - 1) / kThreads;
-  Raw8<T> rx[NV], rd[NV], rz[NV];
-  T rB[NB], rC[NB];
-  auto fetch = [&](int t0) {
+  // between the tile as loaded and the walk a lane has tokens vt + i LPC, channels vc, vc + 1
+  const int vt = lane / S::CW, vc = 2 * (lane % S::CW), n = wn - vc;
+  float bias[2], skip[2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = tid + i * kThreads, t = t0 + e / N, n = e % N;
-      const bool in = e < TT * N && t < min(len, t_end);
-      rB[i] = in ? static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n] : from_f<T>(0.f);
-      if (FULL) rC[i] = in ? static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n] : from_f<T>(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
-      const int t = t0 + vt, n = vt < TT && t < min(len, t_end) ? ct.n - vc : 0;
-      fetch8<T, VEC>(rx[i], static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, n);
-      fetch8<T, VEC>(rd[i], static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, n);
-      if (FULL && a.z)
-        fetch8<T, VEC>(rz[i], static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, n);
+  for (int i = 0; i < 2; ++i) {
+    bias[i] = i < n ? bias_of(a, wc + vc + i) : 0.f;
+    skip[i] = i < n && a.Dskip ? a.Dskip[wc + vc + i] : 0.f;
+  }
+  auto fetch = [&](T* r, int t0) {
+    fetch_rows<T, VEC, WC>(r, static_cast<const T*>(a.x) + b * a.x_sb + wc, a.x_st, t0, t_real, wn, lane);
+    fetch_rows<T, VEC, WC>(r + TT * WC, static_cast<const T*>(a.dt) + b * a.dt_sb + wc, a.dt_st, t0, t_real, wn, lane);
+    fetch_rows<T, VEC, N>(r + 2 * TT * WC, static_cast<const T*>(a.Bm) + b * a.B_sb + ct.g * N, a.B_st, t0, t_real, N,
+                          lane);
+    if (FULL) {
+      fetch_rows<T, VEC, N>(r + TT * (2 * WC + N), static_cast<const T*>(a.Cm) + b * a.C_sb + ct.g * N, a.C_st, t0,
+                            t_real, N, lane);
+      if (a.z)
+        fetch_rows<T, VEC, WC>(r + TT * (2 * WC + 2 * N), static_cast<const T*>(a.z) + b * a.z_sb + wc, a.z_st, t0,
+                               t_real, wn, lane);
     }
   };
-  // one token of one channel: (dt, dt x), (D x, gate); nothing of a token that is not there
-  auto stage = [&](float x, float d, float z, bool ok, int k, float& dt, float& dx, float& skip, float& gate) {
-    const float2 par = s_par[k];
-    dt = d + par.x;
-    if (a.softplus) dt = softplus_f(dt);
-    dt = ok ? dt : 0.f;   // the state stays as it is
-    dx = ok ? dt * x : 0.f;
-    skip = par.y * x;
-    gate = a.z ? z * sigmoid_f(z) : 1.f;
-  };
-  fetch(t_begin);
+  fetch(raw, t_begin);
+  T* now = raw;
+  T* next = raw + W::kRaw;
   for (int t0 = t_begin; t0 < t_end; t0 += TT) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (t0 + TT < t_end) fetch(next, t0 + TT);
+    const Raw2<T>* x_in = reinterpret_cast<const Raw2<T>*>(now + vt * WC + vc);   // a lane's: 16 pairs apart
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
-      if (vt >= TT) break;
-      const int n = t0 + vt < min(len, t_end) ? ct.n - vc : 0;
+    for (int i = 0; i < NP; ++i) {
+      const int t = vt + i * LPC, k = t0 + t < t_real ? n : 0;
+      const Raw2<T> xr = x_in[i * 32], dr = x_in[i * 32 + TT * S::CW];
+      float d[2], u[2];   // nothing of a token that is not there: its state stays as it is
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) {
-        float4 u, e;
-        stage(to_f<T>(rx[i].v[k]), to_f<T>(rd[i].v[k]), to_f<T>(rz[i].v[k]), k < n, vc + k, u.x, u.y, e.x, e.y);
-        stage(to_f<T>(rx[i].v[k + 1]), to_f<T>(rd[i].v[k + 1]), to_f<T>(rz[i].v[k + 1]), k + 1 < n, vc + k + 1, u.z,
-              u.w, e.z, e.w);
-        *reinterpret_cast<float4*>(s_u + vt * CPC + vc + k) = u;
-        if (FULL) *reinterpret_cast<float4*>(s_e + vt * CPC + vc + k) = e;
+      for (int j = 0; j < 2; ++j) {
+        d[j] = to_f<T>(dr.v[j]) + bias[j];
+        if (a.softplus) d[j] = softplus_f(d[j]);
+        d[j] = j < k ? d[j] : 0.f;
+        u[j] = d[j] * to_f<T>(xr.v[j]);
       }
+      *reinterpret_cast<float4*>(s_u + t * WC + vc) = make_float4(d[0], u[0], d[1], u[1]);
     }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = tid + i * kThreads;
-      if (e >= TT * N) break;
-      s_B[e] = to_f<T>(rB[i]);
-      if (FULL) s_C[e] = to_f<T>(rC[i]);
-    }
-    __syncthreads();
-    if (t0 + TT < t_end) fetch(t0 + TT);
+    widen_rows<N>(s_B, now + 2 * TT * WC, lane);
+    if (FULL) widen_rows<N>(s_C, now + TT * (2 * WC + N), lane);
+    __syncwarp();
 #pragma unroll 1
     for (int g = 0; g < TT; g += LPC) {
       float y[2][LPC];
 #pragma unroll
       for (int k = 0; k < LPC; ++k) {
-        const Steps u = load_steps(s_u + (g + k) * CPC + ch);
+        const Steps u = load_steps(s_u + (g + k) * WC + 2 * (lane / LPC));
         const Four B = load4(s_B + (g + k) * N + 4 * part);
         Four C = B;
         if (FULL) C = load4(s_C + (g + k) * N + 4 * part);
@@ -283,26 +333,33 @@ __global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 4 : 5) : 6) scan_f
       if (FULL) {
         lane_sums<LPC, LPC, 1>(y[0], lane);
         lane_sums<LPC, LPC, 1>(y[1], lane);
-        *reinterpret_cast<float2*>(s_y + (g + part) * CPC + ch) = make_float2(y[0][0], y[1][0]);
+        *reinterpret_cast<float2*>(s_y + (g + part) * WC + 2 * (lane / LPC)) = make_float2(y[0][0], y[1][0]);
       }
     }
-    __syncthreads();
+    __syncwarp();
     if (FULL) {
+      const Raw2<T>* z_in = reinterpret_cast<const Raw2<T>*>(now + TT * (2 * WC + 2 * N) + vt * WC + vc);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * kThreads, vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8));
-        const int t = t0 + vt;
-        if (vt >= TT || t >= t_end || vc >= ct.n) break;
-        float o[8];
+      for (int i = 0; i < NP; ++i) {
+        const int t = t0 + vt + i * LPC;
+        if (t >= t_end) break;
+        const float2 y = *reinterpret_cast<const float2*>(s_y + (vt + i * LPC) * WC + vc);
+        const Raw2<T> xr = x_in[i * 32];
+        float o[2] = {y.x, y.y};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 e = s_e[vt * CPC + vc + k];
-          o[k] = t < len ? (s_y[vt * CPC + vc + k] + e.x) * e.y : 0.f;
+        for (int j = 0; j < 2; ++j) {
+          o[j] += skip[j] * to_f<T>(xr.v[j]);
+          if (a.z) {
+            const float z = to_f<T>(z_in[i * 32].v[j]);
+            o[j] *= z * sigmoid_f(z);
+          }
+          if (t >= len) o[j] = 0.f;
         }
-        store8<T, VEC>(static_cast<T*>(a.y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, ct.n - vc, o);
+        store2<T, VEC>(static_cast<T*>(a.y) + ((long long)b * a.T + t) * a.D + wc + vc, n, o);
       }
-      __syncthreads();   // s_e is written again
     }
+    T* const was = now;
+    now = next, next = was;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -359,38 +416,30 @@ __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
 template <int N, typename T, bool VEC>
 __device__ __forceinline__ void load_piece(const ScanArgs& a, const ChannelTile& ct, int b, int t0, int len,
                                            float2* s_u, float* s_dy, float* s_B, float* s_C) {
-  constexpr int CPC = Shape<N>::CPC;
-  const int tid = threadIdx.x;
-  float bias[8];   // of this thread's channels: the same in every round
+  using S = Shape<N>;
+  const int tid = threadIdx.x, vc = 2 * (tid % S::HP);
+  const long long c = ct.c0 + vc;
+  float bias[2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int vc = 8 * (tid % (CPC / 8)) + k;
-    bias[k] = vc < ct.n ? bias_of(a, ct.c0 + vc) : 0.f;
-  }
-#pragma unroll 2
-  for (int v = tid; v < kPiece * CPC / 8; v += kThreads) {
-    const int vt = v / (CPC / 8), vc = 8 * (v % (CPC / 8)), t = t0 + vt;
-    const int n = t < len ? ct.n - vc : 0;
-    float x[8], d[8], g[8], z[8];
-    fetch8<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, n);
-    fetch8<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, n);
-    fetch8<T, VEC>(g, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, n);
-    if (a.z) fetch8<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, n);
+  for (int k = 0; k < 2; ++k) bias[k] = vc + k < ct.n ? bias_of(a, c + k) : 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool ok = k < n;
+  for (int i = 0; i < kPiece / S::ROWS; ++i) {
+    const int vt = tid / S::HP + i * S::ROWS, t = t0 + vt, n = t < len ? ct.n - vc : 0;
+    float x[2], d[2], g[2], z[2];
+    fetch2<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + c, n);
+    fetch2<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + c, n);
+    fetch2<T, VEC>(g, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + c, n);
+    if (a.z) fetch2<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + c, n);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
       d[k] += bias[k];
       if (a.softplus) d[k] = softplus_f(d[k]);
-      d[k] = ok ? d[k] : 0.f;
-      x[k] = ok ? d[k] * x[k] : 0.f;
+      d[k] = k < n ? d[k] : 0.f;
+      x[k] = k < n ? d[k] * x[k] : 0.f;
       if (a.z) g[k] *= z[k] * sigmoid_f(z[k]);
     }
-#pragma unroll
-    for (int k = 0; k < 8; k += 2)
-      *reinterpret_cast<float4*>(s_u + vt * CPC + vc + k) = make_float4(d[k], x[k], d[k + 1], x[k + 1]);
-#pragma unroll
-    for (int k = 0; k < 8; k += 4)
-      *reinterpret_cast<float4*>(s_dy + vt * CPC + vc + k) = make_float4(g[k], g[k + 1], g[k + 2], g[k + 3]);
+    *reinterpret_cast<float4*>(s_u + vt * S::CPC + vc) = make_float4(d[0], x[0], d[1], x[1]);
+    *reinterpret_cast<float2*>(s_dy + vt * S::CPC + vc) = make_float2(g[0], g[1]);
   }
 #pragma unroll
   for (int e0 = 0; e0 < kPiece * N; e0 += kThreads) {
@@ -399,6 +448,12 @@ __device__ __forceinline__ void load_piece(const ScanArgs& a, const ChannelTile&
     s_B[e] = in ? to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n]) : 0.f;
     s_C[e] = in ? to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n]) : 0.f;
   }
+}
+
+// Where channel c of token t is in an array of [kPiece][CPC]: the rows turn, so that the lanes
+// of a channel pair, which write neighbouring tokens, meet in no bank.
+template <int N> __device__ __forceinline__ int turned(int t, int c) {
+  return t * Shape<N>::CPC + ((c + t * Shape<N>::CW) & (Shape<N>::CPC - 1));
 }
 
 template <int N> constexpr int piece_floats() {   // of load_piece
@@ -475,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
   float* s_C = s_B + kPiece * N;
   float* s_h = s_C + kPiece * N;                       // states at the sub-tiles' starts
   float* s_y = s_h + 8 * kThreads * (kPiece / kSub);   // sum_n C h
-  float* s_bc = s_y + kPiece * CPC;                    // [warp][kSub][2N] sums over a warp's channels
+  float* s_bc = s_y + kPiece * S::CPC;                  // [warp][kSub][2N] sums over a warp's channels
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = 2 * (tid / LPC);
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const int tile = blockIdx.x % tiles;
@@ -531,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
       if (a.z) {
         lane_sums<TG, LPC, 1>(y[0], lane);
         lane_sums<TG, LPC, 1>(y[1], lane);
-        *reinterpret_cast<float2*>(s_y + (s * kSub + g + part * TG / LPC) * CPC + ch) =
+        *reinterpret_cast<float2*>(s_y + turned<N>(s * kSub + g + part * TG / LPC, ch)) =
             make_float2(y[0][0], y[1][0]);
       }
     }
@@ -597,50 +652,56 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (i < real) store4(a.hs + (row + i) * N + 4 * part, dA[i]);
-  // dx, ddt, dz of 8 channels per thread and token; the sums over the piece for dD and d bias
-  float sd[8] = {}, sb[8] = {}, skip[8], bias[8];
-  const int vc = 8 * (tid % (CPC / 8)), n = ct.n - vc;
+  // dx, ddt, dz of two channels per thread and token; the sums over the piece for dD and d bias
+  float sd[2] = {}, sb[2] = {}, skip[2], bias[2];
+  const int vc = 2 * (tid % S::HP), n = ct.n - vc;
+  const long long vch = ct.c0 + vc;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    skip[k] = k < n && a.Dskip ? a.Dskip[ct.c0 + vc + k] : 0.f;
-    bias[k] = k < n ? bias_of(a, ct.c0 + vc + k) : 0.f;
+  for (int k = 0; k < 2; ++k) {
+    skip[k] = k < n && a.Dskip ? a.Dskip[vch + k] : 0.f;
+    bias[k] = k < n ? bias_of(a, vch + k) : 0.f;
   }
-  for (int vt = tid / (CPC / 8); vt < kPiece; vt += kThreads / (CPC / 8)) {
+#pragma unroll 4
+  for (int vt = tid / S::HP; vt < kPiece; vt += S::ROWS) {
     const int t = t0 + vt;
     if (t >= a.T || n <= 0) break;
     const int nr = t < len ? n : 0;
-    float x[8], d[8], gy[8], z[8], dx[8], ddt[8], dz[8];
-    fetch8<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + ct.c0 + vc, nr);
-    if (a.softplus) fetch8<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + ct.c0 + vc, nr);
-    fetch8<T, VEC>(gy, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + ct.c0 + vc, nr);
-    if (a.z) fetch8<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + ct.c0 + vc, nr);
+    float x[2], d[2], gy[2], z[2], dx[2], ddt[2], dz[2];
+    fetch2<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + vch, nr);
+    if (a.softplus) fetch2<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + vch, nr);
+    fetch2<T, VEC>(gy, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + vch, nr);
+    if (a.z) fetch2<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + vch, nr);
+    const float4 u4 = *reinterpret_cast<const float4*>(s_u + vt * CPC + vc);   // dt, sum g B
+    const float2 e2 = *reinterpret_cast<const float2*>(s_dy + vt * CPC + vc);
+    float2 y2 = make_float2(0.f, 0.f);
+    if (a.z) y2 = *reinterpret_cast<const float2*>(s_y + turned<N>(vt, vc));
+    const float dt[2] = {u4.x, u4.z}, gB[2] = {u4.y, u4.w}, eA[2] = {e2.x, e2.y}, y[2] = {y2.x, y2.y};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const bool ok = k < nr;
-      const float2 u = s_u[vt * CPC + vc + k];   // dt, sum g B
       float dy = gy[k];
       if (a.z) {
-        const float sg = sigmoid_f(z[k]), y = s_y[vt * CPC + vc + k] + skip[k] * x[k];
-        dz[k] = ok ? gy[k] * y * sg * (1.f + z[k] * (1.f - sg)) : 0.f;
+        const float sg = sigmoid_f(z[k]);
+        dz[k] = ok ? gy[k] * (y[k] + skip[k] * x[k]) * sg * (1.f + z[k] * (1.f - sg)) : 0.f;
         dy *= z[k] * sg;
       }
-      dx[k] = ok ? u.y * u.x + skip[k] * dy : 0.f;
-      ddt[k] = ok ? s_dy[vt * CPC + vc + k] + u.y * x[k] : 0.f;
+      dx[k] = ok ? gB[k] * dt[k] + skip[k] * dy : 0.f;
+      ddt[k] = ok ? eA[k] + gB[k] * x[k] : 0.f;
       if (a.softplus && ok) ddt[k] *= sigmoid_f(d[k] + bias[k]);
       sd[k] += ok ? dy * x[k] : 0.f;
       sb[k] += ddt[k];
     }
-    const long long o = ((long long)b * a.T + t) * a.D + ct.c0 + vc;
-    store8<T, VEC>(static_cast<T*>(a.g.dx) + o, n, dx);
-    store8<T, VEC>(static_cast<T*>(a.g.ddt) + o, n, ddt);
-    if (a.z) store8<T, VEC>(static_cast<T*>(a.g.dz) + o, n, dz);
+    const long long o = ((long long)b * a.T + t) * a.D + vch;
+    store2<T, VEC>(static_cast<T*>(a.g.dx) + o, n, dx);
+    store2<T, VEC>(static_cast<T*>(a.g.ddt) + o, n, ddt);
+    if (a.z) store2<T, VEC>(static_cast<T*>(a.g.dz) + o, n, dz);
   }
   __syncthreads();
-  constexpr int R = kThreads / (CPC / 8);   // rows of partial sums, over the piece's buffers
+  constexpr int R = S::ROWS;   // rows of partial sums, over the piece's buffers
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    sm[(tid / (CPC / 8)) * CPC + vc + k] = sd[k];
-    sm[(R + tid / (CPC / 8)) * CPC + vc + k] = sb[k];
+  for (int k = 0; k < 2; ++k) {
+    sm[(tid / S::HP) * CPC + vc + k] = sd[k];
+    sm[(R + tid / S::HP) * CPC + vc + k] = sb[k];
   }
   __syncthreads();
   for (int e = tid; e < 2 * CPC; e += kThreads) {
@@ -771,10 +832,10 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
   const long long grid = (long long)tiles_of(a.D, a.G, N) * a.B * a.n_piece;
   cudaError_t e = cudaSuccess;
   if (a.n_piece > 1) {
-    e = launch(scan_fwd_kernel<N, T, VEC, false>, grid, 4 * fwd_floats<N>(false), a, st);
+    e = launch(scan_fwd_kernel<N, T, VEC, false>, grid, kWarps * FwdTile<N, T, false>::kBytes, a, st);
     if (e == cudaSuccess) e = launch(scan_join_kernel, blocks((long long)a.B * a.D * N), 0, a, st);
   }
-  return e == cudaSuccess ? launch(scan_fwd_kernel<N, T, VEC, true>, grid, 4 * fwd_floats<N>(true), a, st) : e;
+  return e == cudaSuccess ? launch(scan_fwd_kernel<N, T, VEC, true>, grid, kWarps * FwdTile<N, T, true>::kBytes, a, st) : e;
 }
 
 template <int N, typename T, bool VEC>
@@ -803,9 +864,10 @@ cudaError_t step(const ScanArgs& a, cudaStream_t st) {
 
 bool vec_ok(const ScanArgs& a, int dtype) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  const int v = dtype == DR_FP32 ? 4 : 8;
-  return (a.D / a.G) % 8 == 0 && a.x_sb % v == 0 && a.x_st % v == 0 && a.dt_sb % v == 0 && a.dt_st % v == 0 &&
-         (!a.z || (a.z_sb % v == 0 && a.z_st % v == 0)) && al(a.x) && al(a.dt) && al(a.z) && al(a.y) &&
+  const long long v = dtype == DR_FP32 ? 4 : 8;
+  return (a.D / a.G) % 8 == 0 &&
+         (a.x_sb | a.x_st | a.dt_sb | a.dt_st | a.B_sb | a.B_st | a.C_sb | a.C_st) % v == 0 &&
+         (!a.z || (a.z_sb | a.z_st) % v == 0) && al(a.x) && al(a.dt) && al(a.z) && al(a.Bm) && al(a.Cm) && al(a.y) &&
          al(a.d_y) && al(a.g.dx) && al(a.g.ddt) && al(a.g.dz);
 }
 
@@ -813,7 +875,7 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-// 16-byte accesses where every row starts on 16 bytes, single values otherwise.
+// Wide accesses where every row starts on 16 bytes, single values otherwise.
 #define DR_SCAN_CASE(N_, CALL)                                                    \
   case N_:                                                                        \
     if (dtype == DR_FP32)                                                         \

@@ -126,6 +126,7 @@ struct ScanArgs {
   // pieces along the tokens: number and length, the state at each piece's start
   // (first: at its end, from zero) and the sum of its time steps
   int n_piece, piece;
+  int span;                    // pieces that a warp of the backward's first pass walks
   float* hs;
   float* sum_dt;
   // backward

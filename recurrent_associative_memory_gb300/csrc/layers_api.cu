@@ -24,7 +24,7 @@ size_t conv_bwd_part_floats(const ConvArgs& a);
 size_t scan_fwd_workspace(const ScanArgs& a, int sms);
 cudaError_t launch_scan_fwd(ScanArgs a, int dtype, int sms, void* workspace, cudaStream_t st);
 size_t scan_bwd_workspace(const ScanArgs& a);
-cudaError_t launch_scan_bwd(ScanArgs a, int dtype, void* workspace, cudaStream_t st);
+cudaError_t launch_scan_bwd(ScanArgs a, int dtype, int sms, void* workspace, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t st);
 
 namespace {
@@ -327,7 +327,7 @@ int dr_selective_scan_bwd(const dr_scan* a, const void* x, const void* dt, const
   if (!aligned256(workspace)) return DR_ERR_ALIGN;
   r.d_y = d_y, r.d_hT = d_final_state, r.g = *g;
   if (!z) r.g.dz = nullptr;
-  return status_of(launch_scan_bwd(r, a->dtype, workspace, stream_of(stream)));
+  return status_of(launch_scan_bwd(r, a->dtype, sm_count(), workspace, stream_of(stream)));
 }
 
 int dr_selective_scan_step(const dr_scan* a, const void* x, const void* dt, const void* Bm, const void* Cm,

@@ -25,6 +25,8 @@
 // recomputes a few tokens' states at a time in registers and walks them backwards.
 // The sums over channels leave as one part per channel tile and are added in a fixed
 // order: no atomics.
+#include <algorithm>
+
 #include "layers.cuh"
 
 namespace dr {
@@ -33,6 +35,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPiece = 32;    // tokens of a backward piece
+constexpr int kEndsPerSM = 8; // CTAs of the backward's first pass
 constexpr int kTile = 16;     // tokens in shared memory at a time (forward)
 constexpr int kSub = 8;       // tokens whose states are in registers (backward)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -65,24 +68,9 @@ __device__ __forceinline__ float softplus_f(float v) {
 // without a conflict of banks (8 channels a thread cost a third of the time there).
 template <typename T> struct alignas(2 * sizeof(T)) Raw2 { T v[2]; };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw2<T> fetch2(const T* p, int n) {
-  Raw2<T> r;
-  if constexpr (VEC) {
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint32_t*>(&r) = n > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-    else
-      *reinterpret_cast<uint2*>(&r) = n > 0 ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r.v[i] = i < n ? p[i] : from_f<T>(0.f);
-  }
-  return r;
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void fetch2(float (&f)[2], const T* p, int n) {
-  const Raw2<T> r = fetch2<T, VEC>(p, n);
+template <typename T>
+__device__ __forceinline__ void widen2(float (&f)[2], const T* p) {
+  const Raw2<T> r = *reinterpret_cast<const Raw2<T>*>(p);
   f[0] = to_f<T>(r.v[0]), f[1] = to_f<T>(r.v[1]);
 }
 
@@ -98,36 +86,37 @@ __device__ __forceinline__ void store2(T* p, int n, const float (&f)[2]) {
   }
 }
 
-// Rows t0 .. t0 + kTile - 1 of `width` neighbouring values, src at row 0, into shared memory by
-// one warp: in 16-byte pieces, or as wide as a row, that go on in the background; zeros in
-// place of rows from t_real on and of values from n on.
-template <typename T, bool VEC, int WIDTH>
-__device__ __forceinline__ void fetch_rows(T* dst, const T* src, long long stride, int t0, int t_real, int n, int lane) {
+// ROWS rows from t0 on of WIDTH neighbouring values, src at row 0, into shared memory by
+// `THREADS` threads: in 16-byte pieces, or as wide as a row, that go on in the background;
+// zeros in place of rows from t_real on and of values from n on.
+template <typename T, bool VEC, int WIDTH, int ROWS = kTile, int THREADS = 32>
+__device__ __forceinline__ void fetch_rows(T* dst, const T* src, long long stride, int t0, int t_real, int n, int tid) {
   if constexpr (VEC) {
-    constexpr int ROW = WIDTH * sizeof(T), CB = ROW < 16 ? ROW : 16, PER = ROW / CB, ALL = kTile * PER;
+    constexpr int ROW = WIDTH * sizeof(T), CB = ROW < 16 ? ROW : 16, PER = ROW / CB, ALL = ROWS * PER;
 #pragma unroll
-    for (int e0 = 0; e0 < ALL; e0 += 32) {
-      const int e = e0 + lane, t = t0 + e / PER, k = e % PER * (CB / (int)sizeof(T));
+    for (int e0 = 0; e0 < ALL; e0 += THREADS) {
+      const int e = e0 + tid, t = t0 + e / PER, k = e % PER * (CB / (int)sizeof(T));
       const bool in = t < t_real && k < n;
-      if (ALL % 32 == 0 || e < ALL)
+      if (ALL % THREADS == 0 || e < ALL)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
                          static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + e * CB),
                      "l"(in ? src + t * stride + k : src), "n"(CB), "r"(in ? CB : 0)
                      : "memory");
     }
   } else {
-    for (int e = lane; e < kTile * WIDTH; e += 32) {
+    for (int e = tid; e < ROWS * WIDTH; e += THREADS) {
       const int t = t0 + e / WIDTH, k = e % WIDTH;
       dst[e] = t < t_real && k < n ? src[t * stride + k] : from_f<T>(0.f);
     }
   }
 }
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// kTile rows of N values to fp32, by one warp
-template <int N, typename T>
-__device__ __forceinline__ void widen_rows(float* dst, const T* src, int lane) {
+// ROWS rows of N values to fp32
+template <int N, typename T, int ROWS = kTile, int THREADS = 32>
+__device__ __forceinline__ void widen_rows(float* dst, const T* src, int tid) {
 #pragma unroll
-  for (int e = 4 * lane; e < kTile * N; e += 128) {
+  for (int e = 4 * tid; e < ROWS * N; e += 4 * THREADS) {
     float4 f;
     if constexpr (sizeof(T) == 2) {
       const uint2 r = *reinterpret_cast<const uint2*>(src + e);
@@ -288,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 3 : N == 32 ? 4 : 
   T* now = raw;
   T* next = raw + W::kRaw;
   for (int t0 = t_begin; t0 < t_end; t0 += TT) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    fetched();
     __syncwarp();
     if (t0 + TT < t_end) fetch(next, t0 + TT);
     const Raw2<T>* x_in = reinterpret_cast<const Raw2<T>*>(now + vt * WC + vc);   // a lane's: 16 pairs apart
@@ -412,42 +401,23 @@ __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
 
 // ------------------------------------------------------------------ backward
 
-// One piece's tokens in shared memory: (dt, dt x), dy behind the gate, B and C.
-template <int N, typename T, bool VEC>
-__device__ __forceinline__ void load_piece(const ScanArgs& a, const ChannelTile& ct, int b, int t0, int len,
-                                           float2* s_u, float* s_dy, float* s_B, float* s_C) {
-  using S = Shape<N>;
-  const int tid = threadIdx.x, vc = 2 * (tid % S::HP);
-  const long long c = ct.c0 + vc;
-  float bias[2];
+// dt, dt x and dy behind the gate of a lane's pair of channels
+template <typename T>
+__device__ __forceinline__ void widen_steps(const ScanArgs& a, const T* x_in, const T* d_in, const T* g_in, const T* z_in,
+                                            const float (&bias)[2], int n, float2* u, float* dy) {
+  float x[2], d[2], g[2], z[2];
+  widen2(x, x_in), widen2(d, d_in), widen2(g, g_in);
+  if (a.z) widen2(z, z_in);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) bias[k] = vc + k < ct.n ? bias_of(a, c + k) : 0.f;
-#pragma unroll
-  for (int i = 0; i < kPiece / S::ROWS; ++i) {
-    const int vt = tid / S::HP + i * S::ROWS, t = t0 + vt, n = t < len ? ct.n - vc : 0;
-    float x[2], d[2], g[2], z[2];
-    fetch2<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + c, n);
-    fetch2<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + c, n);
-    fetch2<T, VEC>(g, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + c, n);
-    if (a.z) fetch2<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + c, n);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      d[k] += bias[k];
-      if (a.softplus) d[k] = softplus_f(d[k]);
-      d[k] = k < n ? d[k] : 0.f;
-      x[k] = k < n ? d[k] * x[k] : 0.f;
-      if (a.z) g[k] *= z[k] * sigmoid_f(z[k]);
-    }
-    *reinterpret_cast<float4*>(s_u + vt * S::CPC + vc) = make_float4(d[0], x[0], d[1], x[1]);
-    *reinterpret_cast<float2*>(s_dy + vt * S::CPC + vc) = make_float2(g[0], g[1]);
+  for (int k = 0; k < 2; ++k) {   // nothing of a token that is not there
+    d[k] += bias[k];
+    if (a.softplus) d[k] = softplus_f(d[k]);
+    d[k] = k < n ? d[k] : 0.f;
+    x[k] *= d[k];
+    if (a.z) g[k] *= z[k] * sigmoid_f(z[k]);
   }
-#pragma unroll
-  for (int e0 = 0; e0 < kPiece * N; e0 += kThreads) {
-    const int e = e0 + tid, t = t0 + e / N, n = e % N;
-    const bool in = t < len;
-    s_B[e] = in ? to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + t * a.B_st + ct.g * N + n]) : 0.f;
-    s_C[e] = in ? to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + t * a.C_st + ct.g * N + n]) : 0.f;
-  }
+  *reinterpret_cast<float4*>(u) = make_float4(d[0], x[0], d[1], x[1]);
+  *reinterpret_cast<float2*>(dy) = make_float2(g[0], g[1]);
 }
 
 // Where channel c of token t is in an array of [kPiece][CPC]: the rows turn, so that the lanes
@@ -456,66 +426,116 @@ template <int N> __device__ __forceinline__ int turned(int t, int c) {
   return t * Shape<N>::CPC + ((c + t * Shape<N>::CW) & (Shape<N>::CPC - 1));
 }
 
-template <int N> constexpr int piece_floats() {   // of load_piece
-  return kPiece * (3 * Shape<N>::CPC + 2 * N);
-}
-
 __device__ __forceinline__ void load_dy(const float* p, f2 (&dy)[2]) {
   const float2 v = *reinterpret_cast<const float2*>(p);
   dy[0] = pack2(v.x, v.x), dy[1] = pack2(v.y, v.y);
 }
 
-// A piece's end state from zero, the gradient that reaches its start, its sum of dt.
+// One warp's shared memory: (dt, dt x), dy, B and C in fp32; two tiles as loaded: x, dt, dy,
+// z, B, C.
+template <int N, typename T> struct EndsTile {
+  static constexpr int WC = Shape<N>::WC;
+  static constexpr int kRaw = kTile * (4 * WC + 2 * N);
+  static constexpr int kBytes = 4 * kTile * (3 * WC + 2 * N) + 2 * kRaw * (int)sizeof(T);
+};
+
+// Of `span` pieces one after the other: the end state from zero, the gradient that reaches
+// the piece's start, its sum of dt.  The warps never wait for each other.
 template <int N, typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 5) scan_bwd_ends_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) scan_bwd_ends_kernel(ScanArgs a) {
   using S = Shape<N>;
-  constexpr int CPC = S::CPC, LPC = S::LPC;
+  using W = EndsTile<N, T>;
+  constexpr int CPC = S::CPC, LPC = S::LPC, WC = S::WC, TT = kTile;
   extern __shared__ __align__(16) float sm[];
-  float2* s_u = reinterpret_cast<float2*>(sm);
-  float* s_dy = sm + 2 * kPiece * CPC;
-  float* s_B = s_dy + kPiece * CPC;
-  float* s_C = s_B + kPiece * N;
-  const int tid = threadIdx.x, part = tid % LPC, ch = 2 * (tid / LPC);
-  const int tiles = gridDim.x / (a.B * a.n_piece);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = 2 * (tid / LPC);
+  float2* s_u = reinterpret_cast<float2*>(reinterpret_cast<char*>(sm) + warp * W::kBytes);
+  float* s_dy = reinterpret_cast<float*>(s_u + TT * WC);
+  float* s_B = s_dy + TT * WC;
+  float* s_C = s_B + TT * N;
+  T* now = reinterpret_cast<T*>(s_C + TT * N);
+  T* next = now + W::kRaw;
+  const int n_span = (a.n_piece + a.span - 1) / a.span, tiles = gridDim.x / (a.B * n_span);
   const ChannelTile ct(a, CPC, blockIdx.x % tiles);
-  const int piece = (blockIdx.x / tiles) % a.n_piece, b = blockIdx.x / tiles / a.n_piece;
+  const int p0 = (blockIdx.x / tiles) % n_span * a.span, b = blockIdx.x / tiles / n_span;
+  const int t_end = min(a.n_piece, p0 + a.span) * kPiece, t_real = real_len(a.lens, b, a.T);
   const int c = ct.c0 + ch, real = ct.n - ch;
+  const int wc = ct.c0 + warp * WC, wn = ct.n - warp * WC;   // the warp's channels
+  if (wn <= 0) return;
   const f2 one = pack2(1.f, 1.f);
   Four A2[2], h[2] = {both(0), both(0)}, e[2] = {both(0), both(0)}, cp[2] = {both(one), both(one)};
   float sum[2] = {0.f, 0.f};
   load_rates<N>(a, c, real, part, A2);
-  load_piece<N, T, VEC>(a, ct, b, piece * kPiece, real_len(a.lens, b, a.T), s_u, s_dy, s_B, s_C);
-  __syncthreads();
+  const int vt = lane / S::CW, vc = 2 * (lane % S::CW), n = wn - vc;
+  float bias[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) bias[i] = i < n ? bias_of(a, wc + vc + i) : 0.f;
+  auto fetch = [&](T* r, int t0) {
+    fetch_rows<T, VEC, WC>(r, static_cast<const T*>(a.x) + b * a.x_sb + wc, a.x_st, t0, t_real, wn, lane);
+    fetch_rows<T, VEC, WC>(r + TT * WC, static_cast<const T*>(a.dt) + b * a.dt_sb + wc, a.dt_st, t0, t_real, wn, lane);
+    fetch_rows<T, VEC, WC>(r + 2 * TT * WC, static_cast<const T*>(a.d_y) + (long long)b * a.T * a.D + wc, a.D, t0, t_real,
+                           wn, lane);
+    if (a.z)
+      fetch_rows<T, VEC, WC>(r + 3 * TT * WC, static_cast<const T*>(a.z) + b * a.z_sb + wc, a.z_st, t0, t_real, wn, lane);
+    fetch_rows<T, VEC, N>(r + 4 * TT * WC, static_cast<const T*>(a.Bm) + b * a.B_sb + ct.g * N, a.B_st, t0, t_real, N,
+                          lane);
+    fetch_rows<T, VEC, N>(r + TT * (4 * WC + N), static_cast<const T*>(a.Cm) + b * a.C_sb + ct.g * N, a.C_st, t0, t_real,
+                          N, lane);
+  };
+  fetch(now, p0 * kPiece);
+  for (int t0 = p0 * kPiece; t0 < t_end; t0 += TT) {
+    fetched();
+    __syncwarp();
+    if (t0 + TT < t_end) fetch(next, t0 + TT);
+#pragma unroll
+    for (int i = 0; i < TT / LPC; ++i) {
+      const int t = vt + i * LPC, at = t * WC + vc;
+      widen_steps<T>(a, now + at, now + TT * WC + at, now + 2 * TT * WC + at, now + 3 * TT * WC + at, bias,
+                     t0 + t < t_real ? n : 0, s_u + at, s_dy + at);
+    }
+    widen_rows<N>(s_B, now + 4 * TT * WC, lane);
+    widen_rows<N>(s_C, now + TT * (4 * WC + N), lane);
+    __syncwarp();
 #pragma unroll 4
-  for (int t = 0; t < kPiece; ++t) {
-    const Steps u = load_steps(s_u + t * CPC + ch);
-    f2 dy[2];
-    load_dy(s_dy + t * CPC + ch, dy);
-    const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
+    for (int t = 0; t < TT; ++t) {
+      const Steps u = load_steps(s_u + t * WC + 2 * (lane / LPC));
+      f2 dy[2];
+      load_dy(s_dy + t * WC + 2 * (lane / LPC), dy);
+      const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Four x = exp2_4(mul(A2[i], u.dt[i]));
+        h[i] = fma(x, h[i], mul(B, u.dx[i]));
+        cp[i] = mul(cp[i], x);
+        e[i] = fma(cp[i], mul(C, dy[i]), e[i]);
+        float d, same;
+        unpack2(u.dt[i], d, same);
+        sum[i] += d;
+      }
+    }
+    __syncwarp();
+    T* const was = now;
+    now = next, next = was;
+    if ((t0 + TT) % kPiece) continue;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const Four x = exp2_4(mul(A2[i], u.dt[i]));
-      h[i] = fma(x, h[i], mul(B, u.dx[i]));
-      cp[i] = mul(cp[i], x);
-      e[i] = fma(cp[i], mul(C, dy[i]), e[i]);
-      float d, same;
-      unpack2(u.dt[i], d, same);
-      sum[i] += d;
+      const long long row = ((long long)b * a.n_piece + t0 / kPiece) * a.D + c + i;
+      if (i < real) {
+        store4(a.hs + row * N + 4 * part, h[i]);
+        store4(a.es + row * N + 4 * part, e[i]);
+        if (part == 0) a.sum_dt[row] = sum[i];
+      }
+      h[i] = both(0), e[i] = both(0), cp[i] = both(one), sum[i] = 0.f;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i >= real) break;
-    const long long row = ((long long)b * a.n_piece + piece) * a.D + c + i;
-    store4(a.hs + row * N + 4 * part, h[i]);
-    store4(a.es + row * N + 4 * part, e[i]);
-    if (part == 0) a.sum_dt[row] = sum[i];
   }
 }
 
-template <int N> constexpr int bwd_smem() {
+// A piece's x, dt, dy and z as loaded lie where its states are put later, and come a second
+// time for the gradients of the inputs when the states have been read; B and C as loaded lie
+// where the sums are put.
+template <int N, typename T> constexpr int bwd_smem() {
   using S = Shape<N>;
-  return 4 * (piece_floats<N>() + kPiece * S::CPC + kWarps * kSub * 2 * N + 8 * kThreads * (kPiece / kSub));
+  const int states = 4 * 8 * kThreads * (kPiece / kSub), raw = 4 * kPiece * S::CPC * (int)sizeof(T);
+  return 4 * (kPiece * (4 * S::CPC + 2 * N) + kWarps * kSub * 2 * N) + (raw > states ? raw : states);
 }
 
 template <int N, typename T, bool VEC>
@@ -528,9 +548,9 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
   float* s_dy = sm + 2 * kPiece * CPC;                 // dy, then sum_n g a h A
   float* s_B = s_dy + kPiece * CPC;
   float* s_C = s_B + kPiece * N;
-  float* s_h = s_C + kPiece * N;                       // states at the sub-tiles' starts
-  float* s_y = s_h + 8 * kThreads * (kPiece / kSub);   // sum_n C h
-  float* s_bc = s_y + kPiece * S::CPC;                  // [warp][kSub][2N] sums over a warp's channels
+  float* s_y = s_C + kPiece * N;                       // sum_n C h
+  float* s_bc = s_y + kPiece * CPC;                    // [warp][kSub][2N] sums over a warp's channels
+  float* s_h = s_bc + kWarps * kSub * 2 * N;           // states at the sub-tiles' starts
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, part = tid % LPC, ch = 2 * (tid / LPC);
   const int tiles = gridDim.x / (a.B * a.n_piece);
   const int tile = blockIdx.x % tiles;
@@ -547,7 +567,41 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
       h[i] = load4(a.hs + (row + i) * N + 4 * part);
       gc[i] = load4(a.es + (row + i) * N + 4 * part);
     }
-  load_piece<N, T, VEC>(a, ct, b, t0, len, s_u, s_dy, s_B, s_C);
+  T* raw = reinterpret_cast<T*>(s_h);
+  auto fetch = [&] {
+    constexpr int ALL = kPiece * CPC;
+    auto rows = [&](int i, const void* p, long long sb, long long st) {
+      fetch_rows<T, VEC, CPC, kPiece, kThreads>(raw + i * ALL, static_cast<const T*>(p) + b * sb + ct.c0, st, t0, len, ct.n,
+                                                tid);
+    };
+    rows(0, a.x, a.x_sb, a.x_st);
+    rows(1, a.dt, a.dt_sb, a.dt_st);
+    rows(2, a.d_y, (long long)a.T * a.D, a.D);
+    if (a.z) rows(3, a.z, a.z_sb, a.z_st);
+  };
+  fetch();
+  T* raw_B = reinterpret_cast<T*>(s_y);
+  T* raw_C = raw_B + kPiece * N;
+  fetch_rows<T, VEC, N, kPiece, kThreads>(raw_B, static_cast<const T*>(a.Bm) + b * a.B_sb + ct.g * N, a.B_st, t0, len, N,
+                                          tid);
+  fetch_rows<T, VEC, N, kPiece, kThreads>(raw_C, static_cast<const T*>(a.Cm) + b * a.C_sb + ct.g * N, a.C_st, t0, len, N,
+                                          tid);
+  // between the piece as loaded and the walk a thread has every ROWS-th token, channels vc, vc + 1
+  const int vc = 2 * (tid % S::HP), n = ct.n - vc;
+  float bias[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) bias[k] = k < n ? bias_of(a, ct.c0 + vc + k) : 0.f;
+  fetched();
+  __syncthreads();
+#pragma unroll 4
+  for (int vt = tid / S::HP; vt < kPiece; vt += S::ROWS) {
+    const int at = vt * CPC + vc;
+    constexpr int ALL = kPiece * CPC;
+    widen_steps<T>(a, raw + at, raw + ALL + at, raw + 2 * ALL + at, raw + 3 * ALL + at, bias, t0 + vt < len ? n : 0,
+                   s_u + at, s_dy + at);
+  }
+  widen_rows<N, T, kPiece, kThreads>(s_B, raw_B, tid);
+  widen_rows<N, T, kPiece, kThreads>(s_C, raw_C, tid);
   __syncthreads();
   // the state at each sub-tile's start
   float* own = s_h + 4 * tid;   // [sub][channel][thread][4]
@@ -590,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
             make_float2(y[0][0], y[1][0]);
       }
     }
-    __syncthreads();   // the last sub-tile's s_bc has been read
+    __syncthreads();   // the last sub-tile's s_bc has been read, and at s = 0 every state of s_h
+    if (s == 0) fetch();
 #pragma unroll
     for (int g = kSub - TG; g >= 0; g -= TG) {
       float q[2][2 * TG];   // token k: sum g B, sum e A
@@ -653,24 +708,21 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
   for (int i = 0; i < 2; ++i)
     if (i < real) store4(a.hs + (row + i) * N + 4 * part, dA[i]);
   // dx, ddt, dz of two channels per thread and token; the sums over the piece for dD and d bias
-  float sd[2] = {}, sb[2] = {}, skip[2], bias[2];
-  const int vc = 2 * (tid % S::HP), n = ct.n - vc;
-  const long long vch = ct.c0 + vc;
+  float sd[2] = {}, sb[2] = {}, skip[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    skip[k] = k < n && a.Dskip ? a.Dskip[vch + k] : 0.f;
-    bias[k] = k < n ? bias_of(a, vch + k) : 0.f;
-  }
+  for (int k = 0; k < 2; ++k) skip[k] = k < n && a.Dskip ? a.Dskip[ct.c0 + vc + k] : 0.f;
+  fetched();
+  __syncthreads();
 #pragma unroll 4
   for (int vt = tid / S::HP; vt < kPiece; vt += S::ROWS) {
     const int t = t0 + vt;
     if (t >= a.T || n <= 0) break;
     const int nr = t < len ? n : 0;
     float x[2], d[2], gy[2], z[2], dx[2], ddt[2], dz[2];
-    fetch2<T, VEC>(x, static_cast<const T*>(a.x) + b * a.x_sb + t * a.x_st + vch, nr);
-    if (a.softplus) fetch2<T, VEC>(d, static_cast<const T*>(a.dt) + b * a.dt_sb + t * a.dt_st + vch, nr);
-    fetch2<T, VEC>(gy, static_cast<const T*>(a.d_y) + ((long long)b * a.T + t) * a.D + vch, nr);
-    if (a.z) fetch2<T, VEC>(z, static_cast<const T*>(a.z) + b * a.z_sb + t * a.z_st + vch, nr);
+    constexpr int ALL = kPiece * CPC;
+    const T* in = raw + vt * CPC + vc;
+    widen2(x, in), widen2(d, in + ALL), widen2(gy, in + 2 * ALL);
+    if (a.z) widen2(z, in + 3 * ALL);
     const float4 u4 = *reinterpret_cast<const float4*>(s_u + vt * CPC + vc);   // dt, sum g B
     const float2 e2 = *reinterpret_cast<const float2*>(s_dy + vt * CPC + vc);
     float2 y2 = make_float2(0.f, 0.f);
@@ -691,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
       sd[k] += ok ? dy * x[k] : 0.f;
       sb[k] += ddt[k];
     }
-    const long long o = ((long long)b * a.T + t) * a.D + vch;
+    const long long o = ((long long)b * a.T + t) * a.D + ct.c0 + vc;
     store2<T, VEC>(static_cast<T*>(a.g.dx) + o, n, dx);
     store2<T, VEC>(static_cast<T*>(a.g.ddt) + o, n, ddt);
     if (a.z) store2<T, VEC>(static_cast<T*>(a.g.dz) + o, n, dz);
@@ -839,12 +891,15 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
 }
 
 template <int N, typename T, bool VEC>
-cudaError_t bwd(const ScanArgs& a, cudaStream_t st) {
+cudaError_t bwd(ScanArgs a, int sms, cudaStream_t st) {
   const int tiles = tiles_of(a.D, a.G, N);
   const long long grid = (long long)tiles * a.B * a.n_piece;
-  cudaError_t e = launch(scan_bwd_ends_kernel<N, T, VEC>, grid, 4 * piece_floats<N>(), a, st);
+  // a warp walks several pieces where there are many: DR_SPAN
+  a.span = static_cast<int>(std::max(1LL, std::min<long long>(8, grid / (kEndsPerSM * sms))));
+  cudaError_t e = launch(scan_bwd_ends_kernel<N, T, VEC>, (long long)tiles * a.B * ((a.n_piece + a.span - 1) / a.span),
+                         kWarps * EndsTile<N, T>::kBytes, a, st);
   if (e == cudaSuccess) e = launch(scan_join_kernel, 2LL * blocks((long long)a.B * a.D * N), 0, a, st);
-  if (e == cudaSuccess) e = launch(scan_bwd_kernel<N, T, VEC>, grid, bwd_smem<N>(), a, st);
+  if (e == cudaSuccess) e = launch(scan_bwd_kernel<N, T, VEC>, grid, bwd_smem<N, T>(), a, st);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.B * a.n_piece, cols = (long long)a.D * N;
   column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), 32 * kRowThreads, 0, st>>>(a.hs, rows, cols, cols,
@@ -895,11 +950,11 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 void scan_fwd_pieces(const ScanArgs& a, int sms, int* n_piece, int* piece) {
   const long long rows = (long long)tiles_of(a.D, a.G, a.N) * a.B;
   const int tile = 32;   // of tokens; pieces are whole tiles
-  long long n = 4LL * sms / rows;
+  long long n = 12LL * sms / rows;
   const long long most = (a.T + 2 * tile - 1) / (2 * tile);
   if (n > most) n = most;
   *n_piece = 1, *piece = a.T;
-  if (n < 3) return;
+  if (3 * rows > 4LL * sms || n < 3) return;
   const long long len = ((a.T + n - 1) / n + tile - 1) / tile * tile;
   *piece = static_cast<int>(len);
   *n_piece = static_cast<int>((a.T + len - 1) / len);
@@ -932,7 +987,7 @@ size_t scan_bwd_workspace(const ScanArgs& a) {
          align256((size_t)8 * tiles_of(a.D, a.G, a.N) * a.B * a.T * a.N);
 }
 
-cudaError_t launch_scan_bwd(ScanArgs a, int dtype, void* workspace, cudaStream_t st) {
+cudaError_t launch_scan_bwd(ScanArgs a, int dtype, int sms, void* workspace, cudaStream_t st) {
   a.piece = kPiece;
   a.n_piece = (a.T + kPiece - 1) / kPiece;
   const size_t rows = (size_t)a.B * a.n_piece * a.D;
@@ -947,7 +1002,7 @@ cudaError_t launch_scan_bwd(ScanArgs a, int dtype, void* workspace, cudaStream_t
   a.sum_dt = take(4 * rows);
   a.part_d = take(8 * rows);
   a.part_bc = take(0);
-#define DR_CALL(N_, T_, V_) (bwd<N_, T_, V_>(a, st))
+#define DR_CALL(N_, T_, V_) (bwd<N_, T_, V_>(a, sms, st))
   DR_SCAN_DISPATCH(DR_CALL)
 #undef DR_CALL
 }

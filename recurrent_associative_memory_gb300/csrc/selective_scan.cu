@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 3 : N == 32 ? 4 : 
 
 // Joins the pieces: hs becomes the state at each piece's start; for the backward, whose
 // blocks are twice as many, es the gradient at each piece's end, and the gradient of the
-// initial state.  One thread per state; kBatch pieces are loaded ahead of the chain that
-// goes through them.
+// initial state.  One thread per state; the next kBatch pieces are loaded ahead of the chain
+// that goes through these.
 __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
   constexpr int kBatch = 8;
   const long long per = (long long)a.D * a.N, all = a.B * per;
@@ -374,27 +374,39 @@ __global__ void __launch_bounds__(kThreads) scan_join_kernel(ScanArgs a) {
   const bool back = blockIdx.x >= half;
   const long long e = (long long)(back ? blockIdx.x - half : blockIdx.x) * kThreads + threadIdx.x;
   if (e >= all) return;
-  const long long b = e / per, cn = e % per, c = cn / a.N;
+  const long long b = e / per, cn = e % per, c = cn / a.N, first = b * a.n_piece + (back ? a.n_piece - 1 : 0);
   const float A2 = a.A[cn] * kLog2e;
-  float* s = (back ? a.es : a.hs) + b * a.n_piece * per + cn;
-  const float* sd = a.sum_dt + b * a.n_piece * a.D + c;
+  const long long ds = back ? -per : per, dd = back ? -a.D : a.D;
+  float* s = (back ? a.es : a.hs) + first * per + cn;
+  const float* in = s;
+  const float* sd = a.sum_dt + first * a.D + c;
   const float* from = back ? a.d_hT : a.h0;
   float h = from ? from[e] : 0.f;
-  for (int p0 = 0; p0 < a.n_piece; p0 += kBatch) {
-    float end[kBatch], d[kBatch];
+  float end[2][kBatch], d[2][kBatch];
+  int left = a.n_piece;   // to load
+  auto load = [&](int i) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int p = back ? a.n_piece - 1 - p0 - k : p0 + k;
-      const bool in = p0 + k < a.n_piece;
-      end[k] = in ? s[p * per] : 0.f;
-      d[k] = in ? sd[(long long)p * a.D] : 0.f;
+      if (k < left) end[i][k] = *in, d[i][k] = *sd;
+      in += ds, sd += dd;
     }
+    left -= kBatch;
+  };
+  auto chain = [&](int i, int n) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (p0 + k >= a.n_piece) break;
-      s[(back ? a.n_piece - 1 - p0 - k : p0 + k) * per] = h;
-      h = ex2(A2 * d[k]) * h + end[k];
+      if (k >= n) break;
+      *s = h;
+      s += ds;
+      h = ex2(A2 * d[i][k]) * h + end[i][k];
     }
+  };
+  load(0);
+  for (int n = a.n_piece; n > 0; n -= 2 * kBatch) {
+    load(1);
+    chain(0, n);
+    load(0);
+    chain(1, n - kBatch);
   }
   if (back && a.g.d_init_state) a.g.d_init_state[e] = h;
 }
@@ -799,7 +811,10 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
   const int k = div_mod(e, 2 * a.N, q), g = div_mod(q, a.G, bt);
   const int per = tiles / a.G;
   float v = 0.f;
-  for (int i = 0; i < per; ++i) v += a.part_bc[((g * per + i) * bt_n + bt) * 2 * a.N + k];
+  const float* in = a.part_bc + ((long long)g * per * bt_n + bt) * 2 * a.N + k;
+  const long long step = bt_n * 2 * a.N;
+#pragma unroll 16
+  for (int i = 0; i < per; ++i) v += in[i * step];
   T* o = static_cast<T*>(k < a.N ? a.g.dB : a.g.dC);
   o[(bt * a.G + g) * a.N + k % a.N] = from_f<T>(v);
 }

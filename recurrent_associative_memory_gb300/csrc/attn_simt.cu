@@ -23,37 +23,54 @@ constexpr int kThreads = 256;
 template <int D> constexpr int pitch() { return D + 4; }
 constexpr int kPP = kT + 4;   // row pitch of the P / dS tile
 
-// rows [r0, r0 + 64) of a strided [*, D] matrix to shared memory as fp32; rows at
-// or past n read as zero
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, long long st, int r0, int n) {
-  for (int e = threadIdx.x; e < kT * D / 8; e += kThreads) {
-    const int r = e / (D / 8), c = 8 * (e % (D / 8));
-    float f[8];
-    load8<T, true>(src + (long long)(r0 + r) * st + c, r0 + r < n ? 8 : 0, f);
-    float* p = dst + r * pitch<D>() + c;
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+// rows [r0, r0 + ROWS) of a strided [*, D] matrix to shared memory as fp32; rows at or past
+// n read as zero.  fetch() loads them, put() stores them: what lies between hides the way.
+template <int D, typename T, int ROWS = kT> struct Tile {
+  static constexpr int NC = ROWS * D / 8 / kThreads;   // 8 values at a time
+  static_assert(NC * kThreads * 8 == ROWS * D, "whole rounds of loads");
+  const int tid = threadIdx.x % kThreads;
+  float f[NC][8];
+  __device__ __forceinline__ void fetch(const T* src, long long st, int r0, int n) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int e = tid + i * kThreads, r = r0 + e / (D / 8);
+      load8<T>(src + (long long)r * st + 8 * (e % (D / 8)), r < n ? 8 : 0, f[i]);
+    }
   }
+  __device__ __forceinline__ void put(float* dst) const {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int e = tid + i * kThreads;
+      float* p = dst + e / (D / 8) * pitch<D>() + 8 * (e % (D / 8));
+      *reinterpret_cast<float4*>(p) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
+    }
+  }
+};
+template <int D, typename T, int ROWS = kT>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, long long st, int r0, int n) {
+  Tile<D, T, ROWS> t;
+  t.fetch(src, st, r0, n);
+  t.put(dst);
 }
 
 // s[i][j] = sum_c a[ty + 16 i][c] b[tx + 16 j][c]
-template <int D>
-__device__ __forceinline__ void product_abt(float (&s)[4][4], const float* a, const float* b, int ty,
+template <int D, int RI>
+__device__ __forceinline__ void product_abt(float (&s)[RI][4], const float* a, const float* b, int ty,
                                             int tx) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
-    float4 x[4], y[4];
+    float4 x[RI], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * pitch<D>() + c);
+    for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * pitch<D>() + c);
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * pitch<D>() + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         s[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
@@ -62,35 +79,37 @@ __device__ __forceinline__ void product_abt(float (&s)[4][4], const float* a, co
 
 // o[i][..] += sum_r p[ty + 16 i][r] b[r][columns of tx]; the columns of tx are
 // 4 tx + 64 m (m < D / 64)
-template <int D>
-__device__ __forceinline__ void product_pb(float (&o)[4][D / 16], const float* p, const float* b, int ty,
+template <int D, int RI>
+__device__ __forceinline__ void product_pb(float (&o)[RI][D / 16], const float* p, const float* b, int ty,
                                            int tx) {
-#pragma unroll 4
-  for (int r = 0; r < kT; ++r) {
-    float4 y[D / 64];
+#pragma unroll 2
+  for (int r0 = 0; r0 < kT; r0 += 4) {
+    float w[RI][4];
 #pragma unroll
-    for (int m = 0; m < D / 64; ++m)
-      y[m] = *reinterpret_cast<const float4*>(b + r * pitch<D>() + 4 * tx + 64 * m);
+    for (int i = 0; i < RI; ++i)
+      *reinterpret_cast<float4*>(w[i]) = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPP + r0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w = p[(ty + 16 * i) * kPP + r];
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int m = 0; m < D / 64; ++m) {
-        o[i][4 * m] += w * y[m].x;
-        o[i][4 * m + 1] += w * y[m].y;
-        o[i][4 * m + 2] += w * y[m].z;
-        o[i][4 * m + 3] += w * y[m].w;
+        const float4 y = *reinterpret_cast<const float4*>(b + (r0 + r) * pitch<D>() + 4 * tx + 64 * m);
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+          o[i][4 * m] += w[i][r] * y.x;
+          o[i][4 * m + 1] += w[i][r] * y.y;
+          o[i][4 * m + 2] += w[i][r] * y.z;
+          o[i][4 * m + 3] += w[i][r] * y.w;
+        }
       }
-    }
   }
 }
 
-template <int D, typename T>
+template <int D, typename T, int RI>
 __device__ __forceinline__ void store_rows(T* dst, long long st, int r0, int n,
-                                           const float (&o)[4][D / 16], const float (&f)[4], int ty,
+                                           const float (&o)[RI][D / 16], const float (&f)[RI], int ty,
                                            int tx) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     const int r = r0 + ty + 16 * i;
     if (r >= n) continue;
 #pragma unroll
@@ -112,36 +131,52 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
+// 16 RI query rows; the next tile's keys and values are on their way while this one's are used.
+// KS groups of 256 threads take every KS-th tile of keys each, with their own m, l and o, and
+// join them at the end: more warps where the rows leave one CTA per SM.
+template <int D, typename T, int RI, int KS>
+__global__ void __launch_bounds__(KS * kThreads) attn_fwd_simt_kernel(AttnArgs a) {
+  constexpr int kRows = 16 * RI;
   extern __shared__ float sm[];
   float* sQ = sm;
-  float* sK = sQ + kT * pitch<D>();
+  const int group = threadIdx.x / kThreads;
+  float* sK = sQ + kRows * pitch<D>() + group * (2 * kT * pitch<D>() + kRows * kPP);
   float* sV = sK + kT * pitch<D>();
   float* sP = sV + kT * pitch<D>();
-  const int n_tile = (a.T + kT - 1) / kT;
-  const int i0 = (blockIdx.x % n_tile) * kT;
+  auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kThreads) : "memory"); };
+  const int n_tile = (a.T + kRows - 1) / kRows;
+  const int i0 = (blockIdx.x % n_tile) * kRows;
   const int h = (blockIdx.x / n_tile) % a.H, b = blockIdx.x / n_tile / a.H;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int ty = threadIdx.x % kThreads / 16, tx = threadIdx.x % 16;
   const int len = real_len(a.lens, b, a.S);
   const T* kp = static_cast<const T*>(a.k) + b * a.k_sb + (h / a.G) * a.k_sh;
   const T* vp = static_cast<const T*>(a.v) + b * a.v_sb + (h / a.G) * a.v_sh;
-  load_tile<D, T>(sQ, static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh, a.q_st, i0, a.T);
-  const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kT, a.T) - 1, len, a.window, a.n_sink, kT);
-  float o[4][D / 16] = {}, m[4], l[4];
+  const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kRows, a.T) - 1, len, a.window, a.n_sink, kT);
+  Tile<D, T> k, v;
+  if (group < tiles.n) {
+    k.fetch(kp, a.k_st, tiles[group] * kT, len);
+    v.fetch(vp, a.v_st, tiles[group] * kT, len);
+  }
+  if (group == 0) load_tile<D, T, kRows>(sQ, static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh, a.q_st, i0, a.T);
+  __syncthreads();
+  float o[RI][D / 16] = {}, m[RI], l[RI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  for (int i = 0; i < RI; ++i) m[i] = -INFINITY, l[i] = 0.f;
   const float s2 = a.scale * 1.4426950408889634f;   // logits in base 2
-  for (int n = 0; n < tiles.n; ++n) {
+  for (int n = group; n < tiles.n; n += KS) {
     const int j0 = tiles[n] * kT;
-    __syncthreads();
-    load_tile<D, T>(sK, kp, a.k_st, j0, len);
-    load_tile<D, T>(sV, vp, a.v_st, j0, len);
-    __syncthreads();
-    float s[4][4];
-    product_abt<D>(s, sQ, sK, ty, tx);
+    group_sync();
+    k.put(sK);
+    v.put(sV);
+    group_sync();
+    if (n + KS < tiles.n) {
+      k.fetch(kp, a.k_st, tiles[n + KS] * kT, len);
+      v.fetch(vp, a.v_st, tiles[n + KS] * kT, len);
+    }
+    float s[RI][4];
+    product_abt<D, RI>(s, sQ, sK, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
       const int p = a.q_start + i0 + ty + 16 * i;
       float mx = m[i];
 #pragma unroll
@@ -165,19 +200,45 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
       for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
     }
     __syncwarp();   // a row's 16 threads are in one warp
-    product_pb<D>(o, sP, sV, ty, tx);
+    product_pb<D, RI>(o, sP, sV, ty, tx);
   }
-  float f[4];
+  if constexpr (KS == 2) {
+    constexpr int V = RI * (D / 16 + 2);
+    float* other = sm + kRows * pitch<D>() + (threadIdx.x % kThreads);   // [V][kThreads], over the first group's tiles
+    static_assert(V * kThreads <= 2 * kT * pitch<D>(), "the second group's results fit");
+    __syncthreads();
+    if (group == 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RI; ++i) {
+        other[(2 * i) * kThreads] = m[i], other[(2 * i + 1) * kThreads] = l[i];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) other[(2 * RI + i * (D / 16) + c) * kThreads] = o[i][c];
+      }
+    }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const float m1 = other[(2 * i) * kThreads], mx = fmaxf(m[i], m1), at = mx == -INFINITY ? 0.f : mx;
+      const float f0 = ex2(m[i] - at), f1 = ex2(m1 - at);
+      l[i] = l[i] * f0 + other[(2 * i + 1) * kThreads] * f1;
+      m[i] = mx;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        o[i][c] = o[i][c] * f0 + other[(2 * RI + i * (D / 16) + c) * kThreads] * f1;
+    }
+  }
+  float f[RI];
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
     f[i] = l[i] != 0.f ? 1.f / l[i] : 0.f;
     const int r = i0 + ty + 16 * i;
     if (a.lse && tx == 0 && r < a.T)
       a.lse[((long long)b * a.H + h) * a.T + r] =
           l[i] != 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
   }
-  store_rows<D, T>(static_cast<T*>(a.out) + ((long long)b * a.T * a.H + h) * D, (long long)a.H * D, i0,
-                   a.T, o, f, ty, tx);
+  store_rows<D, T, RI>(static_cast<T*>(a.out) + ((long long)b * a.T * a.H + h) * D, (long long)a.H * D, i0,
+                       a.T, o, f, ty, tx);
 }
 
 // delta = rowsum(dO * O), one warp per row
@@ -230,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
     load_tile<D, T>(sV, vp, a.v_st, j0, len);
     __syncthreads();
     float s[4][4], g[4][4];
-    product_abt<D>(s, sQ, sK, ty, tx);
-    product_abt<D>(g, sO, sV, ty, tx);
+    product_abt<D, 4>(s, sQ, sK, ty, tx);
+    product_abt<D, 4>(g, sO, sV, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int p = a.q_start + i0 + ty + 16 * i;
@@ -243,10 +304,10 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
       }
     }
     __syncwarp();
-    product_pb<D>(o, sP, sK, ty, tx);
+    product_pb<D, 4>(o, sP, sK, ty, tx);
   }
   const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-  store_rows<D, T>(static_cast<T*>(a.dq) + out0, out_st, i0, a.T, o, f, ty, tx);
+  store_rows<D, T, 4>(static_cast<T*>(a.dq) + out0, out_st, i0, a.T, o, f, ty, tx);
 }
 
 template <int D, typename T>
@@ -282,8 +343,8 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
       }
       __syncthreads();
       float s[4][4], t[4][4];
-      product_abt<D>(s, sK, sQ, ty, tx);   // [key][query]
-      product_abt<D>(t, sV, sO, ty, tx);
+      product_abt<D, 4>(s, sK, sQ, ty, tx);   // [key][query]
+      product_abt<D, 4>(t, sV, sO, ty, tx);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -294,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] = s[i][j];
         }
       __syncwarp();
-      product_pb<D>(dv, sP, sO, ty, tx);
+      product_pb<D, 4>(dv, sP, sO, ty, tx);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -303,20 +364,20 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] =
               s[i][j] != 0.f ? s[i][j] * (t[i][j] - sL[kT + tx + 16 * j]) : 0.f;
       __syncwarp();
-      product_pb<D>(dk, sP, sQ, ty, tx);
+      product_pb<D, 4>(dk, sP, sQ, ty, tx);
     }
   }
   const long long o0 = ((long long)b * a.S * a.Hkv + hk) * D, st = (long long)a.Hkv * D;
   const float fk[4] = {a.scale, a.scale, a.scale, a.scale}, fv[4] = {1.f, 1.f, 1.f, 1.f};
-  store_rows<D, T>(static_cast<T*>(a.dk) + o0, st, j0, a.S, dk, fk, ty, tx);
-  store_rows<D, T>(static_cast<T*>(a.dv) + o0, st, j0, a.S, dv, fv, ty, tx);
+  store_rows<D, T, 4>(static_cast<T*>(a.dk) + o0, st, j0, a.S, dk, fk, ty, tx);
+  store_rows<D, T, 4>(static_cast<T*>(a.dv) + o0, st, j0, a.S, dv, fv, ty, tx);
 }
 
 template <typename K>
-cudaError_t launch(K kernel, long long grid, int smem, const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch(K kernel, long long grid, int threads, int smem, const AttnArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+  kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -327,23 +388,31 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
   attn_delta_kernel<D, T><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch(attn_dq_simt_kernel<D, T>, (long long)a.B * a.H * ((a.T + kT - 1) / kT), 4 * tile + p, a, st);
+  e = launch(attn_dq_simt_kernel<D, T>, (long long)a.B * a.H * ((a.T + kT - 1) / kT), kThreads, 4 * tile + p, a, st);
   if (e != cudaSuccess) return e;
   return launch(attn_dkv_simt_kernel<D, T>, (long long)a.B * a.Hkv * ((a.S + kT - 1) / kT),
-                4 * tile + p + 2 * kT * 4, a, st);
+                kThreads, 4 * tile + p + 2 * kT * 4, a, st);
 }
 
+template <int D, typename T, int RI, int KS>
+cudaError_t fwd_rows(const AttnArgs& a, cudaStream_t st) {
+  return launch(attn_fwd_simt_kernel<D, T, RI, KS>, (long long)a.B * a.H * ((a.T + 16 * RI - 1) / (16 * RI)), KS * kThreads,
+                (16 * RI * pitch<D>() + KS * (2 * kT * pitch<D>() + 16 * RI * kPP)) * 4, a, st);
+}
+
+// 64 rows per CTA reuse a tile of keys most; where those leave SMs without one, 32 rows, and
+// at d 64, where the registers allow it, two groups of threads over the tiles of keys.
 template <int D, typename T>
-cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
-  return launch(attn_fwd_simt_kernel<D, T>, (long long)a.B * a.H * ((a.T + kT - 1) / kT),
-                (3 * kT * pitch<D>() + kT * kPP) * 4, a, st);
+cudaError_t fwd(const AttnArgs& a, int sms, cudaStream_t st) {
+  const bool few = (long long)a.B * a.H * ((a.T + 63) / 64) < sms;
+  return few ? fwd_rows<D, T, 2, D == 64 ? 2 : 1>(a, st) : fwd_rows<D, T, 4, 1>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == DR_FP32) return a.d == 64 ? fwd<64, float>(a, st) : fwd<128, float>(a, st);
-  return a.d == 64 ? fwd<64, __nv_bfloat16>(a, st) : fwd<128, __nv_bfloat16>(a, st);
+cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, int sms, cudaStream_t st) {
+  if (dtype == DR_FP32) return a.d == 64 ? fwd<64, float>(a, sms, st) : fwd<128, float>(a, sms, st);
+  return a.d == 64 ? fwd<64, __nv_bfloat16>(a, sms, st) : fwd<128, __nv_bfloat16>(a, sms, st);
 }
 
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st) {

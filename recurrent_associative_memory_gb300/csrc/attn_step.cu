@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
   float q[GB][8], o[GB][8], m[GB], l[GB];
 #pragma unroll
   for (int g = 0; g < GB; ++g) {
-    load8<T, true>(static_cast<const T*>(a.q) + ((long long)b * a.H + h0 + g) * D + c0, g < nh ? 8 : 0, q[g]);
+    load8<T>(static_cast<const T*>(a.q) + ((long long)b * a.H + h0 + g) * D + c0, g < nh ? 8 : 0, q[g]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) q[g][c] *= a.scale * 1.4426950408889634f, o[g][c] = 0.f;
     m[g] = -INFINITY, l[g] = 0.f;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * KPW + sub;
-      load8<T, true>(kc + (long long)j * D + c0, j < end ? 8 : 0, kf[u]);
+      load8<T>(kc + (long long)j * D + c0, j < end ? 8 : 0, kf[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * KPW + sub;
       float vf[8];
-      load8<T, true>(vc + (long long)j * D + c0, j < end ? 8 : 0, vf);
+      load8<T>(vc + (long long)j * D + c0, j < end ? 8 : 0, vf);
 #pragma unroll
       for (int g = 0; g < GB; ++g)
 #pragma unroll
@@ -444,10 +444,10 @@ __global__ void __launch_bounds__(kThreads) cache_fill_kernel(AttnArgs a, T* kc,
   }
   if (p >= len) return;
   float f[8];
-  load8<T, true>(static_cast<const T*>(a.k) + b * a.k_sb + p * a.k_st + hk * a.k_sh + c, 8, f);
-  store8<T, true>(kc + row * a.d + c, 8, f);
-  load8<T, true>(static_cast<const T*>(a.v) + b * a.v_sb + p * a.v_st + hk * a.v_sh + c, 8, f);
-  store8<T, true>(vc + row * a.d + c, 8, f);
+  load8<T>(static_cast<const T*>(a.k) + b * a.k_sb + p * a.k_st + hk * a.k_sh + c, 8, f);
+  store8<T>(kc + row * a.d + c, f);
+  load8<T>(static_cast<const T*>(a.v) + b * a.v_sb + p * a.v_st + hk * a.v_sh + c, 8, f);
+  store8<T>(vc + row * a.d + c, f);
 }
 
 }  // namespace

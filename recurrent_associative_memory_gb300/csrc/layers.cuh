@@ -198,16 +198,13 @@ __device__ __forceinline__ float sigmoid_f(float x) {   // far below zero: 1 / i
   return r;
 }
 
-// 8 consecutive values <-> fp32; VEC: 16-byte aligned, otherwise value by value
-// up to n of them (the rest are 0 / not stored)
-template <typename T, bool VEC>
+// 8 consecutive values, 16-byte aligned, to fp32; zeros where n <= 0
+template <typename T>
 __device__ __forceinline__ void load8(const T* p, int n, float (&f)[8]) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    if (n <= 0) {
+  if (n <= 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-      return;
-    }
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  } else if constexpr (sizeof(T) == 2) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -215,25 +212,16 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&f)[8]) {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-  } else if constexpr (VEC) {
-    if (n <= 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-      return;
-    }
+  } else {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f<T>(p[i]) : 0.f;
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&f)[8]) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    if (n <= 0) return;
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 2) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -241,14 +229,9 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&f)[8]) {
       w[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else if constexpr (VEC) {
-    if (n <= 0) return;
+  } else {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = from_f<T>(f[i]);
   }
 }
 

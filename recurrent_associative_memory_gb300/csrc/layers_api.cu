@@ -8,7 +8,7 @@
 
 namespace dr {
 
-cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_attn_fwd_simt(const AttnArgs& a, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, int dtype, cudaStream_t st);
 bool attn_tc_supported(const AttnArgs& a, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, int sms, cudaStream_t st);
@@ -179,7 +179,7 @@ int dr_window_attn_fwd(const dr_attn* a, const void* q, const void* k, const voi
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = out, r.lse = lse;
   if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, sm_count(), stream_of(stream)));
-  return status_of(launch_attn_fwd_simt(r, a->dtype, stream_of(stream)));
+  return status_of(launch_attn_fwd_simt(r, a->dtype, sm_count(), stream_of(stream)));
 }
 
 size_t dr_window_attn_bwd_workspace_bytes(const dr_attn* a) {

@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
 constexpr int kStepRounds = 4;
 
 template <int N, typename T>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) scan_step_kernel(ScanArgs a) {
   constexpr int LPC = N / 4, PER = kThreads / LPC, CPC = kStepRounds * PER;
   __shared__ __align__(16) float s_B[N], s_C[N];
   const int tiles = gridDim.x / a.B, b = blockIdx.x / tiles;
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
   const int tid = threadIdx.x, part = tid % LPC;
   const float* h0 = a.h0 + ((long long)b * a.D + ct.c0) * N;
   Four h[kStepRounds], A[kStepRounds];
-  float x[kStepRounds], dt[kStepRounds];
+  float x[kStepRounds], dt[kStepRounds], skip[kStepRounds], z[kStepRounds];
 #pragma unroll
   for (int r = 0; r < kStepRounds; ++r) {
     const int k = r * PER + tid / LPC, c = ct.c0 + k;
@@ -844,6 +844,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
     A[r] = real ? load4(a.A + (long long)c * N + 4 * part) : both(0);
     x[r] = real ? to_f<T>(static_cast<const T*>(a.x)[b * a.x_sb + c]) : 0.f;
     dt[r] = real ? to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + bias_of(a, c) : 0.f;
+    skip[r] = real && a.Dskip ? a.Dskip[c] : 0.f;
+    z[r] = real && a.z ? to_f<T>(static_cast<const T*>(a.z)[b * a.z_sb + c]) : 0.f;
   }
   for (int e = tid; e < 2 * N; e += kThreads) {
     const int n = e % N;
@@ -866,11 +868,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
     if (k >= ct.n) continue;
     store4(a.hT + ((long long)b * a.D + c) * N + 4 * part, h[r]);
     if (part) continue;
-    if (a.Dskip) y += a.Dskip[c] * x[r];
-    if (a.z) {
-      const float z = to_f<T>(static_cast<const T*>(a.z)[b * a.z_sb + c]);
-      y *= z * sigmoid_f(z);
-    }
+    y += skip[r] * x[r];
+    if (a.z) y *= z[r] * sigmoid_f(z[r]);
     static_cast<T*>(a.y)[(long long)b * a.D + c] = from_f<T>(y);
   }
 }

@@ -5,6 +5,8 @@
 // neighbouring channels (a warp's row is 128 bytes of bf16) and walks a run of kRun
 // tokens with the last K - 1 inputs in registers; kAhead tokens are loaded, as they are,
 // while the kAhead before them are computed, so that enough bytes are under way.
+#include <type_traits>
+
 #include "layers.cuh"
 
 namespace dr {
@@ -115,22 +117,29 @@ __global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvArgs a) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) now[i] = next[i];
     if (tb + kAhead < last) fetch(tb + kAhead);
-    const bool plain = tb + kAhead <= min(last, len) && (!a.s1 || tb + kAhead <= state0);
+    auto walk = [&](auto is_plain) {
+      constexpr bool plain = decltype(is_plain)::value;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int t = tb + i;
-      if (!plain && t >= last) break;
-      x[K - 1] = pair_of(now[i]);
-      f2 u = filtered<K>(w, bias, x);
-      if (a.silu) u = mul2(u, sigmoid2(u));
-      if (!plain && t >= len) u = 0;
-      store_ch<T, CH>(y, u);
-      y += a.D;
-      if (!plain && a.s1 && t >= state0 && t < len)
-        store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[K - 1]);
+      for (int i = 0; i < kAhead; ++i) {
+        const int t = tb + i;
+        if (!plain && t >= last) break;
+        x[K - 1] = pair_of(now[i]);
+        f2 u = filtered<K>(w, bias, x);
+        if (a.silu) u = mul2(u, sigmoid2(u));
+        if (!plain && t >= len) u = 0;
+        store_ch<T, CH>(y, u);
+        y += a.D;
+        if (!plain && a.s1 && t >= state0 && t < len)
+          store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[K - 1]);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1];
-    }
+        for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1];
+      }
+    };
+    // every token real, before the final state's
+    if (tb + kAhead <= min(last, len) && (!a.s1 || tb + kAhead <= state0))
+      walk(std::true_type());
+    else
+      walk(std::false_type());
   }
 }
 
@@ -180,44 +189,49 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) xr[i] = xn[i], gr[i] = gn[i];
       if (tb + kAhead < last + K - 1) fetch(tb + kAhead);
+      auto walk = [&](auto is_plain) {
+        constexpr bool plain = decltype(is_plain)::value;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int t = tb + i;
+          if (!plain && t >= last + K - 1) break;
+          const bool in = plain || t < loads;
+          x[K - 1] = in ? pair_of(xr[i]) : 0ull;
+          f2 g = in ? pair_of(gr[i]) : 0ull;
+          if (a.silu) {   // silu'(u) = s (1 + u (1 - s))
+            const f2 u = filtered<K>(w, bias, x), s = sigmoid2(u);
+            g = mul2(g, mul2(s, fma2(u, fma2(s, minus, one), one)));
+          }
+          du[K - 1] = g;
+          if (plain || t < last) {
+            dw[K] = add2(dw[K], g);
+#pragma unroll
+            for (int j = 0; j < K; ++j) dw[j] = fma2(g, x[j], dw[j]);
+          }
+          // du[j] holds du_{t-K+1+j}: row t-K+1 is complete
+          const int r = t - (K - 1);
+          if (plain || r >= first) {
+            f2 o = mul2(w[K - 1], du[0]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) o = fma2(w[K - 1 - j], du[j], o);
+            const int f = r - (len - (K - 1));   // its place in the final state
+            if (!plain && a.d_s1 && f >= 0 && f < K - 1)
+              o = add2(o, load_ch<T, CH>(static_cast<const T*>(a.d_s1) + ((long long)b * (K - 1) + f) * a.D + c, true));
+            if (plain || r >= 0)
+              store_ch<T, CH>(dx, o);
+            else if (a.d_s0)
+              store_ch<T, CH>(static_cast<T*>(a.d_s0) + ((long long)b * (K - 1) + r + K - 1) * a.D + c, o);
+          }
+          dx += a.D;
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1], du[j] = du[j + 1];
+        }
+      };
       // every token real, within the run, behind its first rows, before the final state's
-      const bool plain =
-          tb + kAhead <= min(last, len) && tb - (K - 1) >= t0 && (!a.d_s1 || tb + kAhead <= len - (K - 1));
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int t = tb + i;
-        if (!plain && t >= last + K - 1) break;
-        const bool in = plain || t < loads;
-        x[K - 1] = in ? pair_of(xr[i]) : 0ull;
-        f2 g = in ? pair_of(gr[i]) : 0ull;
-        if (a.silu) {   // silu'(u) = s (1 + u (1 - s))
-          const f2 u = filtered<K>(w, bias, x), s = sigmoid2(u);
-          g = mul2(g, mul2(s, fma2(u, fma2(s, minus, one), one)));
-        }
-        du[K - 1] = g;
-        if (plain || t < last) {
-          dw[K] = add2(dw[K], g);
-#pragma unroll
-          for (int j = 0; j < K; ++j) dw[j] = fma2(g, x[j], dw[j]);
-        }
-        // du[j] holds du_{t-K+1+j}: row t-K+1 is complete
-        const int r = t - (K - 1);
-        if (plain || r >= first) {
-          f2 o = mul2(w[K - 1], du[0]);
-#pragma unroll
-          for (int j = 1; j < K; ++j) o = fma2(w[K - 1 - j], du[j], o);
-          const int f = r - (len - (K - 1));   // its place in the final state
-          if (!plain && a.d_s1 && f >= 0 && f < K - 1)
-            o = add2(o, load_ch<T, CH>(static_cast<const T*>(a.d_s1) + ((long long)b * (K - 1) + f) * a.D + c, true));
-          if (plain || r >= 0)
-            store_ch<T, CH>(dx, o);
-          else if (a.d_s0)
-            store_ch<T, CH>(static_cast<T*>(a.d_s0) + ((long long)b * (K - 1) + r + K - 1) * a.D + c, o);
-        }
-        dx += a.D;
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1], du[j] = du[j + 1];
-      }
+      if (tb + kAhead <= min(last, len) && tb - (K - 1) >= t0 && (!a.d_s1 || tb + kAhead <= len - (K - 1)))
+        walk(std::true_type());
+      else
+        walk(std::false_type());
     }
   }
 #pragma unroll

@@ -5,8 +5,8 @@
 //   rows   -lse log2(e) and -delta of every query row, padded to whole tiles of 64 (rows
 //          that see nothing get -infinity, which makes their P zero by itself)
 //   dK/dV  a CTA owns 128 keys of a key/value head and walks the 64-row query tiles of
-//          the group's heads that see them:  S^T = K Q^T and dP^T = V dO^T into TMEM, one
-//          thread per key forms P^T and dS^T in bf16 in their place, and from there they
+//          the group's heads that see them:  S^T = K Q^T and dP^T = V dO^T into TMEM, two
+//          threads per key form P^T and dS^T in bf16 in their place, and from there they
 //          are the A operands of  dV += P^T dO,  dK += dS^T Q  (Q and dO rows as the k axis)
 //   dQ     a CTA owns 128 query rows and walks 64-key tiles: S, dP, dS in place,
 //          dQ += dS K
@@ -15,6 +15,9 @@
 // the softmax warpgroup of one tile work while the tensor cores run the other's products.
 // The sinks' keys are seen by every later row: rows that see nothing else of key tile 0
 // are cut into pieces of their own, whose sums are joined in a fixed order at the end.
+// d 128, 16 heads over 4, window 512, B2 T4096 (forward 58 us before it): rows 17 us, dK/dV 90,
+// dQ 76, sinks 6.  A step of 64 rows takes 1650 to 1800 cycles for products of 1280 (dK/dV)
+// or 1024 (dQ): the chain S -> softmax -> sums of a slot, and two slots only half hide it.
 // Rounding: P and dS to bf16 as operands, the gradients once at the end.
 #include <limits.h>
 

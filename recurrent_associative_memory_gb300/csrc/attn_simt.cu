@@ -12,6 +12,10 @@
 //     o <- o exp(m - m') + P V;  lse = m + log l
 //   dQ: P = exp(s - lse), dS = P (dO V^T - delta), dQ += dS K
 //   dK, dV over the query heads of the group: dV += P^T dO, dK += dS^T Q
+// The reads of shared memory bound it: 8 of 16 bytes for 64 multiply-adds of a thread (6 for
+// 32 at 32 rows).  fp32 forward, B2 H6 T333 d64, window 257: 27 us, 9.8 TFLOP/s.
+// bf16 with strides that no tensor map holds comes here too (everything fp32 but the
+// operands as loaded and the outputs).
 #include "layers.cuh"
 
 namespace dr {

@@ -1,10 +1,14 @@
 // short_conv.cu — short causal convolution, one filter of K taps per channel, with
 // bias and SiLU: forward, backward, one token.
 //
-// Bandwidth-bound: 2 K multiply-adds per value read and written.  A thread owns CH = 2
+// 2 K multiply-adds and two calls of the special units per value read and written: the
+// bytes' 20 us and the instructions' 22 are about the same.  A thread owns CH = 2
 // neighbouring channels (a warp's row is 128 bytes of bf16) and walks a run of kRun
 // tokens with the last K - 1 inputs in registers; kAhead tokens are loaded, as they are,
 // while the kAhead before them are computed, so that enough bytes are under way.
+// Sums are fp32; outputs are rounded once.
+//   B8 T2048 D2048 K4 bf16: forward 28 us (4.7 TB/s), backward 53 us (3.8 TB/s) and 4 of sums;
+//   runs of 32 or 128 tokens cost 8 to 12 us more, 4 or 16 tokens ahead 18 to 60.
 #include <type_traits>
 
 #include "layers.cuh"
@@ -32,7 +36,9 @@ __device__ __forceinline__ Raw<T, CH> raw_ch(const T* p) { return *reinterpret_c
 __device__ __forceinline__ f2 pair_of(Raw<__nv_bfloat16, 2> r) {
   return pack2(__uint_as_float(r.v << 16), __uint_as_float(r.v & 0xFFFF0000u));
 }
-__device__ __forceinline__ f2 pair_of(Raw<__nv_bfloat16, 1> r) { return pack2(__uint_as_float((uint32_t)r.v << 16), 0.f); }
+__device__ __forceinline__ f2 pair_of(Raw<__nv_bfloat16, 1> r) {
+  return pack2(__uint_as_float((uint32_t)r.v << 16), 0.f);
+}
 __device__ __forceinline__ f2 pair_of(Raw<float, 2> r) { return r.v; }
 __device__ __forceinline__ f2 pair_of(Raw<float, 1> r) { return pack2(r.v, 0.f); }
 
@@ -83,7 +89,7 @@ __device__ __forceinline__ f2 sigmoid2(f2 u) {
 }
 
 template <int K, typename T, int CH>
-__global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_kernel(ConvArgs a) {
   const int groups = a.D / CH, runs = (a.T + kRun - 1) / kRun;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
   long long r, rb;

@@ -15,10 +15,13 @@
 // the softmax warpgroup of one tile work while the tensor cores run the other's products.
 // The sinks' keys are seen by every later row: rows that see nothing else of key tile 0
 // are cut into pieces of their own, whose sums are joined in a fixed order at the end.
-// d 128, 16 heads over 4, window 512, B2 T4096 (forward 58 us before it): rows 17 us, dK/dV 90,
-// dQ 76, sinks 6.  A step of 64 rows takes 1650 to 1800 cycles for products of 1280 (dK/dV)
-// or 1024 (dQ): the chain S -> softmax -> sums of a slot, and two slots only half hide it.
-// Rounding: P and dS to bf16 as operands, the gradients once at the end.
+// d 128, 16 heads over 4, window 512, B2 T4096 (forward 57 us before it): rows 17 us, dK/dV
+// 107, dQ 87, sinks 6.  A step of 64 rows takes about 2000 cycles for products of 1536 (dK/dV)
+// or 1280 (dQ): the chain S -> softmax -> sums of a slot, and two slots only half hide it.
+// Rounding: P to bf16 as an operand.  dS as two bf16, itself and what its rounding left, in
+// products of their own (16 us of the 200): P (dP - delta) cancels, delta is taken from a
+// rounded O, and one bf16 on top left dQ and dK 1.6 times as far off as their own rounding
+// does, where this leaves 1.15 times.  The gradients are rounded once at the end.
 #include <limits.h>
 
 #include "attn_tc.cuh"
@@ -52,6 +55,22 @@ constexpr int kMostStages = 4;
 // Column of k-step k of P or dS: each thread leaves its 32 values, packed in 16 columns,
 // over the first of the 32 that it read, so the two threads of a row need no barrier.
 __host__ __device__ constexpr uint32_t half_col(int k) { return (k >> 1) * kHalf + (k & 1) * 8; }
+
+// A thread's 32 values of dS as bf16 and, in the other 16 columns, what that rounding left.
+__device__ __forceinline__ void put_split(uint32_t to, const float (&g)[kHalf]) {
+#pragma unroll
+  for (int h = 0; h < kHalf / 2; h += 8) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = g[2 * (h + k)], y = g[2 * (h + k) + 1];
+      hi[k] = tc::pack_bf16(x, y);
+      lo[k] = tc::pack_bf16(x - __uint_as_float(hi[k] << 16), y - __uint_as_float(hi[k] & 0xffff0000u));
+    }
+    tmem_st8(to + h, hi);
+    tmem_st8(to + kHalf / 2 + h, lo);
+  }
+}
 
 __device__ __forceinline__ bool bounded(uint64_t* bar, uint32_t parity) {
   if (wait_phase(bar, parity)) return true;
@@ -191,6 +210,9 @@ __device__ __forceinline__ bool sums_item(Pipe& q, uint8_t* sm, uint32_t tm, Wal
 #pragma unroll
       for (int k = 0; k < kN / 16; ++k)
         mma_bf16_ta(tm + 256 + D, p + 64 + half_col(k), dA + step_mnmajor(k), ID_ACC, j > 0 || k > 0);
+#pragma unroll
+      for (int k = 0; k < kN / 16; ++k)
+        mma_bf16_ta(tm + 256 + D, p + 64 + kHalf / 2 + half_col(k), dA + step_mnmajor(k), ID_ACC, true);
       mma_commit(&q.free[slot]);
       mma_commit(&q.empty[st]);
       if (j == n - 1) mma_commit(&q.acc_full);
@@ -366,9 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
         }
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-        tmem_st16(tS + 64 + c0, pk);
+        put_split(tS + 64 + c0, g);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&q.p[w]);
@@ -514,9 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kHalf; ++c) g[c] = word & (1u << c) ? g[c] : 0.f;
         }
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 2) pk[c / 2] = tc::pack_bf16(g[c], g[c + 1]);
-        tmem_st16(tS + 64 + c0, pk);
+        put_split(tS + 64 + c0, g);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&q.p[w]);

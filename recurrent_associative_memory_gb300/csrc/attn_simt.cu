@@ -13,7 +13,8 @@
 //   dQ: P = exp(s - lse), dS = P (dO V^T - delta), dQ += dS K
 //   dK, dV over the query heads of the group: dV += P^T dO, dK += dS^T Q
 // The reads of shared memory bound it: 8 of 16 bytes for 64 multiply-adds of a thread (6 for
-// 32 at 32 rows).  fp32 forward, B2 H6 T333 d64, window 257: 27 us, 9.8 TFLOP/s.
+// 32 at 32 rows).  fp32 forward, B4 H8 T1024 d64, window
+// 257: 108 us, 18 TFLOP/s.
 // bf16 with strides that no tensor map holds comes here too (everything fp32 but the
 // operands as loaded and the outputs).
 #include "layers.cuh"
@@ -405,7 +406,9 @@ cudaError_t fwd_rows(const AttnArgs& a, cudaStream_t st) {
 }
 
 // 64 rows per CTA reuse a tile of keys most; where those leave SMs without one, 32 rows, and
-// at d 64, where the registers allow it, two groups of threads over the tiles of keys.
+// at d 64, where the registers allow it, two groups of threads over the tiles of keys.  fp32,
+// 32 rows / 64: B2 H6 T333 d64, window 257 (72 CTAs of 64) 23 / 33 us, B1 at d128 (36) 42 / 57,
+// B4 H8 T1024 (512) 141 / 108, B8 H16 T1024, window 512 (2048) 737 / 543.
 template <int D, typename T>
 cudaError_t fwd(const AttnArgs& a, int sms, cudaStream_t st) {
   const bool few = (long long)a.B * a.H * ((a.T + 63) / 64) < sms;

@@ -10,7 +10,8 @@
 //         where multiply-adds on the CUDA cores take 96 at G = 4
 //   fp32  CUDA cores
 // Long caches of few sequences are cut into pieces of the slots, joined by a second launch.
-//   bf16, d 128, 16 heads over 4: B256, 1028 slots at most, ragged (272 MB) 66 us, 4.1 TB/s;
+//   bf16, d 128, 16 heads over 4: B256, 1028 slots at most, ragged (272 MB) 66 us, 4.1 TB/s, all full (539 MB)
+//   111 us, 4.9 TB/s;
 //   B1, 32772 slots (67 MB, which the L2 holds) 15 us on the GPU, 11 + 3 of the join.
 // Scores, sums and O are fp32; P is rounded to bf16 as an operand, its sum l is not; the
 // outputs once.
@@ -458,6 +459,9 @@ __global__ void __launch_bounds__(kThreads) cache_fill_kernel(AttnArgs a, T* kc,
 }  // namespace
 
 // Pieces along the slots: as many as fill three CTAs on every SM, of 128 slots at least.
+// bf16, d 128, 16 heads over 4, for one / three / six CTAs per SM / without pieces:
+// B1 32772 slots 16.1 / 14.8 / 20.9 / 467 us, B4 4100 slots 11.4 / 10.9 / 13.0 / 49,
+// B16 1028 slots 11.8 / 10.1 / 13.0 / 15.7; B256 is one piece either way.
 int attn_step_pieces(const AttnStepArgs& a, int dtype, int sms) {
   const int heads = dtype == DR_FP32 ? 4 : (a.G <= 8 ? 8 : 16);   // of one CTA
   const long long rows = (long long)a.B * a.Hkv * ((a.G + heads - 1) / heads);

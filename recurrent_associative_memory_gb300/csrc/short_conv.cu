@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
     load_filter<K, CH>(a, c, w, bias);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      x[j] = load_in<K, T, CH>(a, b, t0 - (K - 1) + j, c);
+      const int t = t0 - (K - 1) + j;   // nothing from behind the end: 0 times it may be NaN
+      x[j] = t < len ? load_in<K, T, CH>(a, b, t, c) : 0ull;
       du[j] = 0;
     }
     for (int tb = t0; tb < last + K - 1; tb += kAhead) {

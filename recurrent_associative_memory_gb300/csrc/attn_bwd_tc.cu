@@ -14,7 +14,8 @@
 // adds its dQ parts to memory, would depend on the order of atomics.  Two TMEM slots let
 // the softmax warpgroup of one tile work while the tensor cores run the other's products.
 // The sinks' keys are seen by every later row: rows that see nothing else of key tile 0
-// are cut into pieces of their own, whose sums are joined in a fixed order at the end.
+// are cut into pieces of their own, whose sums are joined in a fixed order at the end (one CTA
+// walking all of them: 510 us for the training step below instead of 268).
 // d 128, 16 heads over 4, window 512, B2 T4096 (forward 57 us before it): rows 17 us, dK/dV
 // 107, dQ 87, sinks 6.  A step of 64 rows takes about 2000 cycles for products of 1536 (dK/dV)
 // or 1280 (dQ): the chain S -> softmax -> sums of a slot, and two slots only half hide it.

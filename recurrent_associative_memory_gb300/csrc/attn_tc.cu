@@ -69,7 +69,9 @@ struct Item {
         set0(a, i0, len),
         set1(a, i0 + kM, len),
         tiles(a.q_start + i0, a.q_start + min(i0 + 2 * kM, a.T) - 1, len, a.window, a.n_sink, kM) {}
-  // a tile outside every row's window is there for its sinks only
+  // a tile outside every row's window is there for its sinks only: of up to 32 (the smallest
+  // tile of keys) the product and softmax of 32 keys do (60 us instead of 68 for B2 T4096
+  // above, 214 instead of 221 for T16384)
   __device__ __forceinline__ bool sinks_only(const AttnArgs& a, int tile) const {
     return tile < tiles.n_first && a.n_sink - tile * kM <= 32;
   }

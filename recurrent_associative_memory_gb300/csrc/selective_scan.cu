@@ -825,56 +825,60 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
 
 // ------------------------------------------------------------------ one token
 
-// Four states per lane as above; the state is read once and written once.  A CTA owns
-// kStepRounds x kThreads / LPC channels of one sequence and one group, all of its states'
-// loads issued before the first is used.
-constexpr int kStepRounds = 4;
+// Four states per lane as above; the state is read once and written once.  A thread owns
+// one channel of kStepSeqs sequences, whose rates it reads once; all loads are issued before
+// the first is used.
+//   B256 D4096 N16 bf16 (143 MB): 32.8 us, 4.4 TB/s; two sequences 36.9, eight 59 us, the rates
+//   read for every sequence 36.1.
+constexpr int kStepSeqs = 4;
 
 template <int N, typename T>
-__global__ void __launch_bounds__(kThreads, 7) scan_step_kernel(ScanArgs a) {
-  constexpr int LPC = N / 4, PER = kThreads / LPC, CPC = kStepRounds * PER;
-  __shared__ __align__(16) float s_B[N], s_C[N];
-  const int tiles = gridDim.x / a.B, b = blockIdx.x / tiles;
+__global__ void __launch_bounds__(kThreads, 8) scan_step_kernel(ScanArgs a) {
+  constexpr int LPC = N / 4, CPC = kThreads / LPC;
+  __shared__ __align__(16) float s_bc[kStepSeqs][2 * N];
+  const int blocks = (a.B + kStepSeqs - 1) / kStepSeqs, tiles = gridDim.x / blocks;
+  const int b0 = blockIdx.x / tiles * kStepSeqs;
   const ChannelTile ct(a, CPC, blockIdx.x % tiles);
-  const int tid = threadIdx.x, part = tid % LPC;
-  const float* h0 = a.h0 + ((long long)b * a.D + ct.c0) * N;
-  Four h[kStepRounds], A[kStepRounds];
-  float x[kStepRounds], dt[kStepRounds], skip[kStepRounds], z[kStepRounds];
+  const int tid = threadIdx.x, part = tid % LPC, k = tid / LPC, c = ct.c0 + k;
+  const bool mine = k < ct.n;
+  Four h[kStepSeqs];
+  float x[kStepSeqs], dt[kStepSeqs], z[kStepSeqs];
 #pragma unroll
-  for (int r = 0; r < kStepRounds; ++r) {
-    const int k = r * PER + tid / LPC, c = ct.c0 + k;
-    const bool real = k < ct.n;
-    h[r] = real ? load4(h0 + k * N + 4 * part) : both(0);
-    A[r] = real ? load4(a.A + (long long)c * N + 4 * part) : both(0);
+  for (int r = 0; r < kStepSeqs; ++r) {
+    const long long b = b0 + r;
+    const bool real = mine && b < a.B;
+    h[r] = real ? load4(a.h0 + (b * a.D + c) * N + 4 * part) : both(0);
     x[r] = real ? to_f<T>(static_cast<const T*>(a.x)[b * a.x_sb + c]) : 0.f;
-    dt[r] = real ? to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) + bias_of(a, c) : 0.f;
-    skip[r] = real && a.Dskip ? a.Dskip[c] : 0.f;
+    dt[r] = real ? to_f<T>(static_cast<const T*>(a.dt)[b * a.dt_sb + c]) : 0.f;
     z[r] = real && a.z ? to_f<T>(static_cast<const T*>(a.z)[b * a.z_sb + c]) : 0.f;
   }
-  for (int e = tid; e < 2 * N; e += kThreads) {
-    const int n = e % N;
-    if (e < N)
-      s_B[n] = to_f<T>(static_cast<const T*>(a.Bm)[b * a.B_sb + ct.g * N + n]);
-    else
-      s_C[n] = to_f<T>(static_cast<const T*>(a.Cm)[b * a.C_sb + ct.g * N + n]);
+  const f2 k2 = pack2(kLog2e, kLog2e);
+  const Four A2 = mine ? mul(load4(a.A + (long long)c * N + 4 * part), k2) : both(0);
+  const float bias = mine ? bias_of(a, c) : 0.f, skip = mine && a.Dskip ? a.Dskip[c] : 0.f;
+  for (int e = tid; e < kStepSeqs * 2 * N; e += kThreads) {
+    const int r = e / (2 * N), n = e % N;
+    const long long b = min(b0 + r, a.B - 1);
+    s_bc[r][e % (2 * N)] = to_f<T>(e % (2 * N) < N ? static_cast<const T*>(a.Bm)[b * a.B_sb + ct.g * N + n]
+                                                   : static_cast<const T*>(a.Cm)[b * a.C_sb + ct.g * N + n]);
   }
   __syncthreads();
-  const Four B = load4(s_B + 4 * part), C = load4(s_C + 4 * part);
-  const f2 k2 = pack2(kLog2e, kLog2e);
 #pragma unroll
-  for (int r = 0; r < kStepRounds; ++r) {
-    const int k = r * PER + tid / LPC, c = ct.c0 + k;
-    const float d = a.softplus ? softplus_f(dt[r]) : dt[r], dx = d * x[r];
-    h[r] = fma(exp2_4(mul(mul(A[r], k2), pack2(d, d))), h[r], mul(B, pack2(dx, dx)));
+  for (int r = 0; r < kStepSeqs; ++r) {
+    const long long b = b0 + r;
+    const Four B = load4(s_bc[r] + 4 * part), C = load4(s_bc[r] + N + 4 * part);
+    float d = dt[r] + bias;
+    if (a.softplus) d = softplus_f(d);
+    const float dx = d * x[r];
+    h[r] = fma(exp2_4(mul(A2, pack2(d, d))), h[r], mul(B, pack2(dx, dx)));
     float y = dot(C, h[r]);
 #pragma unroll
     for (int w = LPC / 2; w >= 1; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-    if (k >= ct.n) continue;
-    store4(a.hT + ((long long)b * a.D + c) * N + 4 * part, h[r]);
+    if (!mine || b >= a.B) continue;
+    store4(a.hT + (b * a.D + c) * N + 4 * part, h[r]);
     if (part) continue;
-    y += skip[r] * x[r];
+    y += skip * x[r];
     if (a.z) y *= z[r] * sigmoid_f(z[r]);
-    static_cast<T*>(a.y)[(long long)b * a.D + c] = from_f<T>(y);
+    static_cast<T*>(a.y)[b * a.D + c] = from_f<T>(y);
   }
 }
 
@@ -931,9 +935,9 @@ cudaError_t bwd(ScanArgs a, int sms, cudaStream_t st) {
 
 template <int N, typename T>
 cudaError_t step(const ScanArgs& a, cudaStream_t st) {
-  constexpr int cpc = kStepRounds * kThreads / (N / 4);
+  constexpr int cpc = kThreads / (N / 4);
   const long long tiles = (long long)a.G * ((a.D / a.G + cpc - 1) / cpc);
-  return launch(scan_step_kernel<N, T>, tiles * a.B, 0, a, st);
+  return launch(scan_step_kernel<N, T>, tiles * ((a.B + kStepSeqs - 1) / kStepSeqs), 0, a, st);
 }
 
 bool vec_ok(const ScanArgs& a, int dtype) {

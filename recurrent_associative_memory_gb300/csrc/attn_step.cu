@@ -10,8 +10,8 @@
 //         where multiply-adds on the CUDA cores take 96 at G = 4
 //   fp32  CUDA cores
 // Long caches of few sequences are cut into pieces of the slots, joined by a second launch.
-//   bf16, d 128, 16 heads over 4: B256, 1028 slots at most, ragged (272 MB) 66 us, 4.1 TB/s, all full (539 MB)
-//   111 us, 4.9 TB/s;
+//   bf16, d 128, 16 heads over 4: B256, 1028 slots at most, ragged (272 MB) 62 us, 4.4 TB/s, all full (539 MB)
+//   105 us, 5.1 TB/s;
 //   B1, 32772 slots (67 MB, which the L2 holds) 15 us on the GPU, 11 + 3 of the join.
 // Scores, sums and O are fp32; P is rounded to bf16 as an operand, its sum l is not; the
 // outputs once.
@@ -169,6 +169,17 @@ __global__ void __launch_bounds__(kThreads) attn_step_simt_kernel(AttnStepArgs a
 
 // ------------------------------------------------------------------ bf16
 
+// A piece of a cache row.  ONCE: it leaves no copy in L1, where nothing reads it again.
+template <bool ONCE>
+__device__ __forceinline__ uint4 cache16(const __nv_bfloat16* p) {
+  if constexpr (!ONCE) return *reinterpret_cast<const uint4*>(p);
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
 
@@ -197,7 +208,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 //                the slots 2t, 2t+1, 2t+8, 2t+9, and product e of a block takes channel e
 //                of each lane's 8
 // R = 1: the rows 8 .. 15 are not there and share two registers that stay 0.
-template <int D, int R>
+template <int D, int R, bool ONCE>
 __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_kernel(AttnStepArgs a) {
   using T = __nv_bfloat16;
   constexpr int HB = 8 * R, KS = D / 32, VF = D / 64;
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int j = j0 + 8 * u + g;
-        k[u][s] = j < end ? *reinterpret_cast<const uint4*>(kc + (long long)j * D + 32 * s + 8 * t) : zero;
+        k[u][s] = j < end ? cache16<ONCE>(kc + (long long)j * D + 32 * s + 8 * t) : zero;
       }
   };
   load_k(begin + 16 * warp);
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(kMmaThreads, R == 1 ? 3 : 2) attn_step_mma_ker
 #pragma unroll
       for (int f = 0; f < VF; ++f) {
         const int j = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
-        v[f][u] = j < end ? *reinterpret_cast<const uint4*>(vc + (long long)j * D + 64 * f + 8 * g) : zero;
+        v[f][u] = j < end ? cache16<ONCE>(vc + (long long)j * D + 64 * f + 8 * g) : zero;
       }
     float s[2][4];
 #pragma unroll
@@ -420,10 +431,15 @@ cudaError_t step_fp32(const AttnStepArgs& a, cudaStream_t st) {
   return step<D, 4>(a, st);
 }
 
+// Whole sequences to a CTA fill the SMs several times over, and their rows need no place in L1:
+// B256, 1028 slots at most, 62 us instead of 67; in pieces (B1, 32772 slots) 19 instead of 15.
 template <int D, int R>
 cudaError_t step_mma(const AttnStepArgs& a, cudaStream_t st) {
   const long long grid = (long long)a.B * a.Hkv * ((a.G + 8 * R - 1) / (8 * R)) * a.n_piece;
-  attn_step_mma_kernel<D, R><<<static_cast<unsigned>(grid), kMmaThreads, 0, st>>>(a);
+  if (a.n_piece == 1)
+    attn_step_mma_kernel<D, R, true><<<static_cast<unsigned>(grid), kMmaThreads, 0, st>>>(a);
+  else
+    attn_step_mma_kernel<D, R, false><<<static_cast<unsigned>(grid), kMmaThreads, 0, st>>>(a);
   return join<D, __nv_bfloat16>(a, st);
 }
 

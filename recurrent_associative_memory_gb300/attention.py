@@ -19,7 +19,7 @@ from __future__ import annotations
 import torch
 
 from . import dr
-from .tensors import activations, call, check, check_rows, ptr, scratch
+from .tensors import activations, call, check, check_rows, on_stream, ptr, scratch
 
 __all__ = ["window_attn_fwd", "window_attn_bwd", "window_attn_step", "window_cache",
            "window_cache_fill"]
@@ -49,6 +49,7 @@ def _scale(scale):
     return scale
 
 
+@on_stream
 def window_attn_fwd(q, k, v, window, n_sink=0, *, q_start=0, lens=None, scale=None, want_lse=False,
                     out=None, lse=None, stream=None):
     """Returns (out [B,T,H,d], lse fp32 [B,H,T] or None).
@@ -65,10 +66,11 @@ def window_attn_fwd(q, k, v, window, n_sink=0, *, q_start=0, lens=None, scale=No
         check(lse, "lse", (a.B, a.H, a.T), torch.float32, dev)
     elif want_lse:
         lse = q.new_empty((a.B, a.H, a.T), dtype=torch.float32)
-    call("dr_window_attn_fwd", dev, stream, dr.dr_window_attn_fwd, a, q, k, v, out, lse)
+    call("dr_window_attn_fwd", dev, dr.dr_window_attn_fwd, a, q, k, v, out, lse)
     return out, lse
 
 
+@on_stream
 def window_attn_bwd(q, k, v, out, lse, d_out, window, n_sink=0, *, q_start=0, lens=None, scale=None,
                     workspace="auto", grads=None, stream=None):
     """Returns dict(dq [B,T,H,d], dk, dv [B,S,Hkv,d]) in q's type, from the forward's out
@@ -84,7 +86,7 @@ def window_attn_bwd(q, k, v, out, lse, d_out, window, n_sink=0, *, q_start=0, le
         else:
             check(g[name], name, t.shape, q.dtype, dev)
     ws, n = scratch(dr.dr_window_attn_bwd_workspace_bytes, a, q, dev, workspace)
-    call("dr_window_attn_bwd", dev, stream, dr.dr_window_attn_bwd, a, q, k, v, out, lse, d_out,
+    call("dr_window_attn_bwd", dev, dr.dr_window_attn_bwd, a, q, k, v, out, lse, d_out,
          g["dq"], g["dk"], g["dv"], ws, n)
     return g
 
@@ -101,14 +103,16 @@ def _check_cache(k_cache, v_cache, B, Hkv, slots, d, dtype, dev):
     check(v_cache, "v_cache", (B, Hkv, slots, d), dtype, dev)
 
 
+@on_stream
 def window_cache_fill(k, v, k_cache, v_cache, window, n_sink=0, *, lens=None, stream=None):
     """Lays a prompt's k, v [B,S,Hkv,d] out in the caches, for decoding to go on at position
     lens[b] (default S)."""
     a, dev = _describe(k, k, v, window, n_sink, 0, lens, None)
     _check_cache(k_cache, v_cache, a.B, a.Hkv, n_sink + window, a.d, k.dtype, dev)
-    call("dr_window_cache_fill", dev, stream, dr.dr_window_cache_fill, a, k, v, k_cache, v_cache)
+    call("dr_window_cache_fill", dev, dr.dr_window_cache_fill, a, k, v, k_cache, v_cache)
 
 
+@on_stream
 def window_attn_step(q, k, v, k_cache, v_cache, pos, window, n_sink=0, *, scale=None, out=None,
                      workspace="auto", stream=None):
     """One token per sequence: writes k, v [B,Hkv,d] at positions pos (int32 [B], on the
@@ -130,6 +134,6 @@ def window_attn_step(q, k, v, k_cache, v_cache, pos, window, n_sink=0, *, scale=
     else:
         check(out, "out", q.shape, q.dtype, dev)
     ws, n = scratch(dr.dr_window_attn_step_workspace_bytes, a, q, dev, workspace)
-    call("dr_window_attn_step", dev, stream, dr.dr_window_attn_step, a, q, k, v, k_cache, v_cache,
+    call("dr_window_attn_step", dev, dr.dr_window_attn_step, a, q, k, v, k_cache, v_cache,
          pos, out, ws, n)
     return out

@@ -21,7 +21,7 @@ from __future__ import annotations
 import torch
 
 from . import dr
-from .tensors import activations, call, check, check_rows, ptr, scratch
+from .tensors import activations, call, check, check_rows, on_stream, ptr, scratch
 
 __all__ = ["short_conv_fwd", "short_conv_bwd", "short_conv_step", "selective_scan_fwd",
            "selective_scan_bwd", "selective_scan_step"]
@@ -61,6 +61,7 @@ def _conv(x, weight, bias, silu, lens, dims):
     return dr.DrConv(code, x.shape[0], x.shape[1], D, K, silu, ptr(lens), sb, st), dev
 
 
+@on_stream
 def short_conv_fwd(x, weight, bias=None, *, silu=True, init_state=None, lens=None, want_final=True,
                    y=None, final_state=None, stream=None):
     """x [B,T,D] (any batch and token strides), weight fp32 [D,K], bias fp32 [D], init_state
@@ -73,11 +74,12 @@ def short_conv_fwd(x, weight, bias=None, *, silu=True, init_state=None, lens=Non
     y = _given_or_new(y, "y", x.shape, x.dtype, x, dev)
     if want_final or final_state is not None:
         final_state = _given_or_new(final_state, "final_state", state, x.dtype, x, dev)
-    call("dr_short_conv_fwd", dev, stream, dr.dr_short_conv_fwd, a, x, weight, bias, init_state, y,
+    call("dr_short_conv_fwd", dev, dr.dr_short_conv_fwd, a, x, weight, bias, init_state, y,
          final_state)
     return y, final_state
 
 
+@on_stream
 def short_conv_bwd(x, weight, bias, d_y, *, silu=True, init_state=None, d_final_state=None,
                    lens=None, workspace="auto", grads=None, stream=None):
     """Returns dict(dx [B,T,D] in x's type, dweight fp32 [D,K], dbias fp32 [D]) and with
@@ -94,11 +96,12 @@ def short_conv_bwd(x, weight, bias, d_y, *, silu=True, init_state=None, d_final_
         shapes["dinit_state"] = (state, x.dtype)
     g = _gradients(grads, shapes, x, dev)
     ws, n = scratch(dr.dr_short_conv_bwd_workspace_bytes, a, x, dev, workspace)
-    call("dr_short_conv_bwd", dev, stream, dr.dr_short_conv_bwd, a, x, weight, bias, init_state, d_y,
+    call("dr_short_conv_bwd", dev, dr.dr_short_conv_bwd, a, x, weight, bias, init_state, d_y,
          d_final_state, g["dx"], g["dweight"], g["dbias"], g.get("dinit_state"), ws, n)
     return g
 
 
+@on_stream
 def short_conv_step(x, weight, bias, state, *, silu=True, state_out=None, y=None, stream=None):
     """One token: x [B,D], state [B,K-1,D].  The new state goes to ``state_out`` (default: in
     place).  Returns (y [B,D], the new state)."""
@@ -110,7 +113,7 @@ def short_conv_step(x, weight, bias, state, *, silu=True, state_out=None, y=None
     else:
         check(state_out, "state_out", shape, x.dtype, dev)
     y = _given_or_new(y, "y", x.shape, x.dtype, x, dev)
-    call("dr_short_conv_step", dev, stream, dr.dr_short_conv_step, a, x, weight, bias, state,
+    call("dr_short_conv_step", dev, dr.dr_short_conv_step, a, x, weight, bias, state,
          state_out, y)
     return y, state_out
 
@@ -153,6 +156,7 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, softplus, lens, dims):
                      A.data_ptr(), ptr(D), ptr(dt_bias), *strides), dev
 
 
+@on_stream
 def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus=True,
                        init_state=None, lens=None, want_final=True, y=None, final_state=None,
                        workspace="auto", stream=None):
@@ -168,11 +172,12 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus
     if want_final or final_state is not None:
         final_state = _given_or_new(final_state, "final_state", state, torch.float32, x, dev)
     ws, n = scratch(dr.dr_selective_scan_fwd_workspace_bytes, a, x, dev, workspace)
-    call("dr_selective_scan_fwd", dev, stream, dr.dr_selective_scan_fwd, a, x, dt, B, C, z,
+    call("dr_selective_scan_fwd", dev, dr.dr_selective_scan_fwd, a, x, dt, B, C, z,
          init_state, y, final_state, ws, n)
     return y, final_state
 
 
+@on_stream
 def selective_scan_bwd(x, dt, A, B, C, d_y, D=None, z=None, dt_bias=None, *, softplus=True,
                        init_state=None, d_final_state=None, lens=None, workspace="auto",
                        grads=None, stream=None):
@@ -200,11 +205,12 @@ def selective_scan_bwd(x, dt, A, B, C, d_y, D=None, z=None, dt_bias=None, *, sof
     gs = dr.DrScanGrads(*(ptr(g.get(n)) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD",
                                                   "ddt_bias", "dinit_state")))
     ws, n = scratch(dr.dr_selective_scan_bwd_workspace_bytes, a, x, dev, workspace)
-    call("dr_selective_scan_bwd", dev, stream, dr.dr_selective_scan_bwd, a, x, dt, B, C, z,
+    call("dr_selective_scan_bwd", dev, dr.dr_selective_scan_bwd, a, x, dt, B, C, z,
          init_state, d_y, d_final_state, gs, ws, n)
     return g
 
 
+@on_stream
 def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus=True,
                         state_out=None, y=None, stream=None):
     """One token: x, dt, z [B,D], B, C [B,G,N], state fp32 [B,D,N].  The new state goes to
@@ -217,6 +223,6 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, 
     else:
         check(state_out, "state_out", shape, torch.float32, dev)
     y = _given_or_new(y, "y", x.shape, x.dtype, x, dev)
-    call("dr_selective_scan_step", dev, stream, dr.dr_selective_scan_step, a, x, dt, B, C, z, state,
+    call("dr_selective_scan_step", dev, dr.dr_selective_scan_step, a, x, dt, B, C, z, state,
          state_out, y)
     return y, state_out

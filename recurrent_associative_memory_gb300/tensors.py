@@ -8,6 +8,8 @@ costs one short expression, and only a wrong one pays for its message.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import dr
@@ -74,15 +76,32 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def call(name, device, stream, fn, *args):
-    """``fn(*args, stream)`` with ``device`` current, on ``stream`` (None: the current one of
-    that device); raises ``dr.DrError`` for a status other than DR_OK."""
+def call(name, device, fn, *args):
+    """``fn(*args, stream)`` with ``device`` current, on its current stream; raises
+    ``dr.DrError`` for a status other than DR_OK."""
     if device != _current_device():
         with torch.cuda.device(device):
-            return call(name, device, stream, fn, *args)
-    status = fn(*args, _current_stream(device) if stream is None else stream)
+            return call(name, device, fn, *args)
+    status = fn(*args, _current_stream(device))
     if status:
         dr.check(status, name)
+
+
+def on_stream(fn):
+    """With a ``stream``, ``fn`` runs as if that were the current one: what it allocates belongs
+    to that stream, so neither its scratch nor its outputs are memory that the current stream
+    still uses or may be given while the call's kernels run."""
+    @functools.wraps(fn)
+    def run(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        kw["stream"] = None
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return run
 
 
 def scratch(size_of, description, x, device, workspace):

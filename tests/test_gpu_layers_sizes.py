@@ -77,3 +77,32 @@ def test_attention_gradients_are_little_further_off_than_their_rounding(mods, T,
     for name, most in (("dq", 1.25), ("dk", 1.25), ("dv", 2 ** 0.5)):
         off = np.linalg.norm(np64(g[name]) - grads[name]) / np.linalg.norm(grads[name])
         assert off < most * 2.0 ** -9, (name, off)
+
+
+def test_scratch_of_a_call_on_another_stream_is_left_alone(mods):  # noqa: F811
+    """While a call waits on a busy stream, the current stream allocates and overwrites blocks
+    of every size that the call took: its results are those of a quiet call."""
+    attention, ssm = mods
+    q, k, v, do = qkv(3, 2, 300, 300, 4, 2, 128, torch.bfloat16)
+    s = scan_inputs(4, 1, 1500, 24, 16, 1, torch.bfloat16)
+    dy = randn(torch.Generator().manual_seed(5), 1, 1500, 24, dtype=torch.bfloat16)
+    out, lse = attention.window_attn_fwd(q, k, v, 40, 4, want_lse=True)
+
+    def work(stream):
+        g = attention.window_attn_bwd(q, k, v, out, lse, do, 40, 4, stream=stream)
+        y, end = ssm.selective_scan_fwd(**s, stream=stream)
+        r = ssm.selective_scan_bwd(**s, d_y=dy, stream=stream)
+        return [*(g[n] for n in sorted(g)), y, end, *(r[n] for n in sorted(r) if r[n] is not None)]
+
+    want = [t.clone() for t in work(None)]
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for side in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        stream = side if isinstance(side, torch.cuda.Stream) else torch.cuda.ExternalStream(side)
+        with torch.cuda.stream(stream):
+            for _ in range(60):
+                busy = busy @ busy * 1e-4
+        got = work(side)
+        taken = [torch.full((n,), math.nan, device="cuda") for n in [2 ** i for i in range(7, 20)] * 4]
+        torch.cuda.synchronize()
+        assert taken and all(torch.equal(a, b) for a, b in zip(got, want))

@@ -25,7 +25,7 @@
 //                   one warp for both tiles spends 2300 cycles of a step on its waits.)
 //                   They issue P V and the next S of their tile in turns: interleaved, both
 //                   tiles would finish together and their softmax would run at the same time.
-// d 128, 16 heads over 4, window 2048, B1 T16384: 214 us, 1210 TFLOP/s; window 1024, B2 T4096
+// d 128, 16 heads over 4, window 2048, B1 T16384: 217 us, 1190 TFLOP/s; window 1024, B2 T4096
 // with ragged lengths 60 us, 1010.  The softmax's instructions and the waits between it and
 // the products bound it: a step takes about 3200 cycles.
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.

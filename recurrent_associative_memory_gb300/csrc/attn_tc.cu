@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e) o[e] *= f;
           tmem_st16(tO + c, reinterpret_cast<uint32_t*>(o));
         }
+        tmem_st_wait();   // a second call in the same tile loads what this one stored
       };
 
       auto one_tile = [&](auto cols, int j0) {   // cols.value keys from j0

@@ -177,6 +177,7 @@ __device__ __forceinline__ bool scores_item(Pipe& q, uint8_t* sm, uint32_t tm, W
     const uint32_t gi = at.steps, slot = gi & 1, st = gi % kStages, s = tm + 128 * slot;
     if (!all_wait(&q.full[st], (gi / kStages) & 1)) return false;
     if (gi >= 2 && !all_wait(&q.free[slot], ((gi >> 1) - 1) & 1)) return false;
+    tc_fence_after();   // the slot's columns have been read and its operands used
     const uint64_t dA = desc_kmajor(A + st * L::kTile), dB = desc_kmajor(B + st * L::kTile);
     if (elect_one()) {
 #pragma unroll

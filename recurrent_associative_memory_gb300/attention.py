@@ -11,7 +11,8 @@ constant size, ``window_cache_fill`` lays a prompt's keys and values out in it a
 ``window_attn_step`` takes it one token further.
 
 The functions allocate outputs and call ``dr``; they compute nothing themselves.
-Work runs on ``stream`` (default: the current one) of q's device.
+Work runs on ``stream``, a stream of q's device (a torch stream or a raw handle; default:
+the current one), and the tensors passed in may be let go as soon as the call is back.
 """
 
 from __future__ import annotations

@@ -13,7 +13,8 @@ and a form for single tokens that takes the state one token further.  ``lens`` i
 and leave the state alone.
 
 The functions allocate outputs and call ``dr``; they compute nothing themselves.
-Work runs on ``stream`` (default: the current one) of x's device.
+Work runs on ``stream``, a stream of x's device (a torch stream or a raw handle; default:
+the current one), and the tensors passed in may be let go as soon as the call is back.
 """
 
 from __future__ import annotations

@@ -9,6 +9,7 @@ costs one short expression, and only a wrong one pays for its message.
 from __future__ import annotations
 
 import functools
+import inspect
 
 import torch
 
@@ -88,19 +89,33 @@ def call(name, device, fn, *args):
 
 
 def on_stream(fn):
-    """With a ``stream``, ``fn`` runs as if that were the current one: what it allocates belongs
-    to that stream, so neither its scratch nor its outputs are memory that the current stream
-    still uses or may be given while the call's kernels run."""
+    """With a ``stream``, of the device of ``fn``'s first tensor (a torch stream or a raw handle),
+    ``fn`` runs as if that were the current one: what it allocates belongs to that stream, so
+    neither its scratch nor its outputs are memory that the current stream still uses or may be
+    given while the call's kernels run.  The memory of tensors that are passed in is not given
+    to others either before what the call put on the stream is done; that they are ready when
+    the stream gets there is the caller's part."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def run(*args, **kw):
         stream = kw.get("stream")
         if stream is None:
             return fn(*args, **kw)
         kw["stream"] = None
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream)
+        device = getattr(args[0] if args else kw.get(first), "device", None)
+        if device is None or device.type != "cuda":
+            return fn(*args, **kw)   # refused there
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
-            return fn(*args, **kw)
+            result = fn(*args, **kw)
+        for t in (*args, *kw.values(), *(kw.get("grads") or {}).values()):
+            if torch.is_tensor(t):
+                t.record_stream(stream)
+        return result
     return run
 
 

@@ -416,6 +416,8 @@ int dr_window_cache_fill(const dr_attn *a, const void *k, const void *v, void *k
  *     u_t[c] = bias[c] + sum_{j<K} weight[c,j] x_{t-K+1+j}[c];   y = u or u sigmoid(u)
  * Tokens before the first come from init_state [B,K-1,D] (oldest first, x's type;
  * NULL: zero).  Rows at and after lens[b] give y = 0 and are not part of the state.
+ * The forward's and the step's new state may be written over the old one (the same
+ * buffer); nothing else may overlap what a call writes.
  */
 typedef struct dr_conv {
   int dtype;               /* dr_dtype of x, y, states and their gradients            */
@@ -427,7 +429,7 @@ typedef struct dr_conv {
 } dr_conv;
 
 /* Forward.  x [B,T,D] with a's strides; weight fp32 [D,K]; bias fp32 [D] or NULL;
- * y [B,T,D]; final_state [B,K-1,D] or NULL: the last K-1 inputs. */
+ * y [B,T,D]; final_state [B,K-1,D] or NULL: the last K-1 inputs; may be init_state. */
 int dr_short_conv_fwd(const dr_conv *a, const void *x, const float *weight, const float *bias,
                       const void *init_state, void *y, void *final_state, dr_stream_t stream);
 

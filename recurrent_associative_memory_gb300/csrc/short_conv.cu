@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
   const int t0 = div_mod(r, runs, rb) * kRun, last = min(t0 + kRun, a.T);
   if (rb >= a.B) return;
   const int b = rb;
-  const int len = real_len(a.lens, b, a.T), state0 = len - (K - 1);
+  const int len = real_len(a.lens, b, a.T);
   f2 w[K], bias, x[K];
   const T* xp = static_cast<const T*>(a.x) + b * a.x_sb + t0 * a.x_st + c;
   T* y = static_cast<T*>(a.y) + ((long long)b * a.T + t0) * a.D + c;
@@ -113,10 +113,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
   load_filter<K, CH>(a, c, w, bias);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
-    const int t = t0 - (K - 1) + j;
-    x[j] = load_in<K, T, CH>(a, b, t, c);
-    if (a.s1 && t < 0 && t >= state0)   // a short sequence keeps some of its initial state
-      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[j]);
+    x[j] = load_in<K, T, CH>(a, b, t0 - (K - 1) + j, c);
+  }
+  // The final state, by the thread that alone reads the initial one: they may be one buffer.
+  // Row j of it is input len - (K - 1) + j, in a short sequence a row of the initial state at
+  // or behind j.
+  if (t0 == 0 && a.s1) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + j) * a.D + c,
+                      load_in<K, T, CH>(a, b, len - (K - 1) + j, c));
   }
   for (int tb = t0; tb < last; tb += kAhead) {
     Raw<T, CH> now[kAhead];
@@ -135,14 +141,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
         if (!plain && t >= len) u = 0;
         store_ch<T, CH>(y, u);
         y += a.D;
-        if (!plain && a.s1 && t >= state0 && t < len)
-          store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + t - state0) * a.D + c, x[K - 1]);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1];
       }
     };
-    // every token real, before the final state's
-    if (tb + kAhead <= min(last, len) && (!a.s1 || tb + kAhead <= state0))
+    if (tb + kAhead <= min(last, len))   // every token real
       walk(std::true_type());
     else
       walk(std::false_type());

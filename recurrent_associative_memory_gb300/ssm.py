@@ -67,7 +67,7 @@ def short_conv_fwd(x, weight, bias=None, *, silu=True, init_state=None, lens=Non
                    y=None, final_state=None, stream=None):
     """x [B,T,D] (any batch and token strides), weight fp32 [D,K], bias fp32 [D], init_state
     [B,K-1,D] in x's type (the inputs before the first token, oldest first; None: zeros).
-    Returns (y [B,T,D], final_state [B,K-1,D] or None)."""
+    ``final_state`` may be ``init_state``.  Returns (y [B,T,D], final_state [B,K-1,D] or None)."""
     a, dev = _conv(x, weight, bias, silu, lens, 3)
     state = (a.B, a.K - 1, a.D)
     if init_state is not None:

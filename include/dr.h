@@ -435,7 +435,7 @@ int dr_short_conv_fwd(const dr_conv *a, const void *x, const float *weight, cons
 
 /* Backward from d_y [B,T,D]: dx [B,T,D], d_weight fp32 [D,K], d_bias fp32 [D] or
  * NULL, d_init_state [B,K-1,D] (x's type) or NULL.  d_final_state [B,K-1,D] or NULL
- * is the gradient of the final state. */
+ * is the gradient of the final state; d_init_state must be another buffer. */
 int dr_short_conv_bwd(const dr_conv *a, const void *x, const float *weight, const float *bias,
                       const void *init_state, const void *d_y, const void *d_final_state, void *dx,
                       float *d_weight, float *d_bias, void *d_init_state, void *workspace,

@@ -265,6 +265,8 @@ int dr_short_conv_bwd(const dr_conv* a, const void* x, const float* weight, cons
   if (!a || !x || !weight || !d_y || !dx || !d_weight) return DR_ERR_NULL;
   int st = check_conv(a);
   if (st != DR_OK) return st;
+  // the first tokens' threads write the one, the last tokens' read the other
+  if (d_init_state && d_init_state == d_final_state) return DR_ERR_ARG;
   ConvArgs r = conv_args(a, x, weight, bias, init_state);
   if (!workspace || workspace_bytes < 4 * conv_bwd_part_floats(r)) return DR_ERR_WORKSPACE;
   if (!aligned256(workspace)) return DR_ERR_ALIGN;

@@ -43,7 +43,7 @@ int vec_of(int dtype) { return dtype == DR_FP32 ? 4 : 8; }
 cudaStream_t stream_of(dr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 int status_of(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CUDA; }
 
-// SMs of the current device; 0 where there is none
+// SMs of the current device; 0 where there is none, and no launch is cut for it
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -176,10 +176,12 @@ int dr_window_attn_fwd(const dr_attn* a, const void* q, const void* k, const voi
   int st = check_attn(a);
   if (st != DR_OK) return st;
   if (!aligned16(q, k, v, out) || !strides_ok(a, true)) return DR_ERR_ALIGN;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = out, r.lse = lse;
-  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, sm_count(), stream_of(stream)));
-  return status_of(launch_attn_fwd_simt(r, a->dtype, sm_count(), stream_of(stream)));
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_fwd_tc(r, sms, stream_of(stream)));
+  return status_of(launch_attn_fwd_simt(r, a->dtype, sms, stream_of(stream)));
 }
 
 size_t dr_window_attn_bwd_workspace_bytes(const dr_attn* a) {
@@ -196,10 +198,12 @@ int dr_window_attn_bwd(const dr_attn* a, const void* q, const void* k, const voi
   if (!aligned16(q, k, v, out, d_out, dq, dk, dv) || !strides_ok(a, true)) return DR_ERR_ALIGN;
   if (!workspace || workspace_bytes < attn_bwd_workspace(a)) return DR_ERR_WORKSPACE;
   if (!aligned256(workspace)) return DR_ERR_ALIGN;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   AttnArgs r = attn_args(a);
   r.q = q, r.k = k, r.v = v, r.out = const_cast<void*>(out), r.lse = const_cast<float*>(lse);
   r.d_out = d_out, r.dq = dq, r.dk = dk, r.dv = dv;
-  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_bwd_tc(r, sm_count(), workspace, stream_of(stream)));
+  if (attn_tc_supported(r, a->dtype)) return status_of(launch_attn_bwd_tc(r, sms, workspace, stream_of(stream)));
   r.delta = static_cast<float*>(workspace);
   return status_of(launch_attn_bwd_simt(r, a->dtype, stream_of(stream)));
 }
@@ -218,8 +222,10 @@ int dr_window_attn_step(const dr_attn* a, const void* q, const void* k, const vo
   int st = check_step(a, &s);
   if (st != DR_OK) return st;
   if (!aligned16(q, k, v, k_cache, v_cache, out)) return DR_ERR_ALIGN;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   if (workspace) {
-    s.n_piece = attn_step_pieces(s, a->dtype, sm_count());
+    s.n_piece = attn_step_pieces(s, a->dtype, sms);
     if (workspace_bytes < step_workspace(s, s.n_piece)) return DR_ERR_WORKSPACE;
     if (!aligned256(workspace)) return DR_ERR_ALIGN;
   }
@@ -302,6 +308,7 @@ int dr_selective_scan_fwd(const dr_scan* a, const void* x, const void* dt, const
   ScanArgs r = scan_args(a, x, dt, Bm, Cm, z, init_state);
   r.y = y, r.hT = final_state;
   const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   if (workspace) {
     const size_t need = scan_fwd_workspace(r, sms);
     if (workspace_bytes < need) return DR_ERR_WORKSPACE;
@@ -327,9 +334,11 @@ int dr_selective_scan_bwd(const dr_scan* a, const void* x, const void* dt, const
   ScanArgs r = scan_args(a, x, dt, Bm, Cm, z, init_state);
   if (!workspace || workspace_bytes < scan_bwd_workspace(r)) return DR_ERR_WORKSPACE;
   if (!aligned256(workspace)) return DR_ERR_ALIGN;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   r.d_y = d_y, r.d_hT = d_final_state, r.g = *g;
   if (!z) r.g.dz = nullptr;
-  return status_of(launch_scan_bwd(r, a->dtype, sm_count(), workspace, stream_of(stream)));
+  return status_of(launch_scan_bwd(r, a->dtype, sms, workspace, stream_of(stream)));
 }
 
 int dr_selective_scan_step(const dr_scan* a, const void* x, const void* dt, const void* Bm, const void* Cm,

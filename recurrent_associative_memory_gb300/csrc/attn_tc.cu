@@ -9,12 +9,12 @@
 // the other's P V and next S.  S and P V of a tile wait for each other, so a step is the
 // longer of four products (2048 cycles at d = 128) and the softmax's latency plus two.
 // To keep that latency short, a tile's exponentials take a reference m from the tiles
-// before it: any m is right as long as nothing overflows (the final division takes it out),
-// and P up to 2^64 is far inside the range of bf16 and fp32.  Where a row's maximum passes
-// 2^8, m is raised before the next tile; where it passes 2^64 (or m is not set: the first
-// tile), the tile is taken again.  P V of the first 64 keys starts while the second 64 are
-// still exponentials.  Raising m rescales O; S of tile n is issued behind P V of tile n - 1,
-// so a thread that has S may touch O.
+// before it: any m is right as long as nothing overflows (the final division takes it out).
+// m is set 2^8 above a row's maximum, so that P stays at most 1 and P V within what the sum of
+// |v| allows; where a maximum passes m (or m is not set: the first tile), the tile is taken
+// again.  P V of the first 64 keys starts while the second 64 are still exponentials.  Raising
+// m rescales O; S of tile n is issued behind P V of tile n - 1, so a thread that has S may
+// touch O.
 // The CTAs stay: one per SM walks the work items, and the next item's Q, K and V are on their
 // way while the last one's softmax and stores run.
 //   warps 0-3, 4-7  softmax and epilogue of the tiles 0 and 1
@@ -45,8 +45,7 @@ constexpr int kThreads = 384;   // three warpgroups; the third has an idle warp
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "a larger sum would wait for ever");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;   // and the one after it
-constexpr float kRaise = 8.f;    // log2 of P above which m is raised for the tiles to come
-constexpr float kAgain = 64.f;   // and above which this tile is taken again
+constexpr float kAbove = 8.f;   // what m is set above a row's maximum, in base 2
 
 template <int D> struct Smem {
   static constexpr int kTile = kM * D * 2;                  // bytes of 128 rows
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item x(a, n_block, it);
       const int i = x.i0 + w * kM + row, p = a.q_start + i;
       const int p0 = a.q_start + x.i0 + w * kM, p1 = p0 + kM - 1;
-      float m = -INFINITY, l = 0.f, grow = 0.f;   // m and what it is raised by, in base 2
+      float m = -INFINITY, l = 0.f;   // m in base 2
       bool any = false;
 
       auto rescale = [&](float f) {   // l and O, of all rows of the warp
@@ -152,17 +151,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e) o[e] *= f;
           tmem_st16(tO + c, reinterpret_cast<uint32_t*>(o));
         }
-        tmem_st_wait();   // a second call in the same tile loads what this one stored
+        tmem_st_wait();   // a second call loads what this one stored
       };
 
       auto one_tile = [&](auto cols, int j0) {   // cols.value keys from j0
         constexpr int NC = decltype(cols)::value, NA = NC < 64 ? NC : 64;
         const bool whole = j0 + NC - 1 <= p0 && j0 + NC <= x.len && p1 - j0 < a.window;
-        if (__any_sync(0xffffffffu, grow > 0.f)) {
-          m += grow;
-          rescale(ex2(-grow));
-          grow = 0.f;
-        }
         float s[NC];
         uint32_t pk[NA / 2];
         f2 sum[2], aa;
@@ -201,11 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
           const float top = c2 * max3(max3(mx[0], mx[1], mx[2]), mx[3],
                                       max3(max3(s[NC - 4], s[NC - 3], s[NC - 2]), s[NC - 1], -INFINITY));
-          const bool far = top - m > kAgain;   // true too where nothing was summed so far
-          grow = top - m > kRaise ? top - m : 0.f;
+          const bool far = top > m;   // true too where nothing was summed so far
           if (!__any_sync(0xffffffffu, far)) break;
-          rescale(far && m != -INFINITY ? ex2(m - top) : 1.f);
-          if (far) m = top;
+          rescale(far && m != -INFINITY ? ex2(m - (top + kAbove)) : 1.f);
+          if (far) m = top + kAbove;
         }
 #pragma unroll
         for (int c = 0; c < NA / 2; c += 16) tmem_st16(tS + c, pk + c);

@@ -53,3 +53,12 @@ def test_rows_of_a_warp_that_grow_and_jump(mods, bits, window, n_sink, d):  # no
     than 2^64 in the next: both rescale the sums, one after the other."""
     q, k, v = rising(700, d, bits, 3.0, seed=len(bits) + d)
     check(mods[0], q, k, v, window, n_sink, 3.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [[(0, 0), (40, 60)], [(0, 0), (7, 3), (14, 11), (50, 19), (56, 80)]])
+def test_large_values_behind_a_jump_of_the_scores_stay_finite(mods, bits, d):  # noqa: F811
+    """Values of about 2^112: what is summed stays below 2^128 as long as no probability passes
+    1 by much, whatever the scores do."""
+    q, k, v = rising(600, d, bits, 3.0, seed=d)
+    check(mods[0], q, k, v * 2.0 ** 112, 600, 0, 3.0)

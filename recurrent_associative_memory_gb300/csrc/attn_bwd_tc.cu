@@ -301,7 +301,7 @@ struct KeyItem {
     far = item < a.n_far;
     piece = far ? 1 + item : 0;
     j0 = far ? 0 : (item - a.n_far) * kM;
-    len = uniform(real_len(a.lens, b, a.S));
+    len = uniform(real_len(a.lens, b, a.reach));
     int i_end;   // i_begin is a multiple of kN
     if (far) {
       i_begin = a.far_first + item * a.far_rows;
@@ -480,7 +480,7 @@ struct RowItem {
         i0(it / a.H % n_block * kM),
         b(it / a.H / n_block),
         hk(h / a.G),
-        len(uniform(real_len(a.lens, b, a.S))),
+        len(uniform(real_len(a.lens, b, a.reach))),
         tiles(a.q_start + i0, a.q_start + min(i0 + kM, a.T) - 1, len, a.window, a.n_sink, kN) {}
 };
 

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(KS * kThreads) attn_fwd_simt_kernel(AttnArgs a
   const int i0 = (blockIdx.x % n_tile) * kRows;
   const int h = (blockIdx.x / n_tile) % a.H, b = blockIdx.x / n_tile / a.H;
   const int ty = threadIdx.x % kThreads / 16, tx = threadIdx.x % 16;
-  const int len = real_len(a.lens, b, a.S);
+  const int len = real_len(a.lens, b, a.reach);
   const T* kp = static_cast<const T*>(a.k) + b * a.k_sb + (h / a.G) * a.k_sh;
   const T* vp = static_cast<const T*>(a.v) + b * a.v_sb + (h / a.G) * a.v_sh;
   const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kRows, a.T) - 1, len, a.window, a.n_sink, kT);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
   const int i0 = (blockIdx.x % n_tile) * kT;
   const int h = (blockIdx.x / n_tile) % a.H, b = blockIdx.x / n_tile / a.H;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int len = real_len(a.lens, b, a.S);
+  const int len = real_len(a.lens, b, a.reach);
   const T* kp = static_cast<const T*>(a.k) + b * a.k_sb + (h / a.G) * a.k_sh;
   const T* vp = static_cast<const T*>(a.v) + b * a.v_sb + (h / a.G) * a.v_sh;
   const long long out0 = ((long long)b * a.T * a.H + h) * D, out_st = (long long)a.H * D;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
   const int j0 = (blockIdx.x % n_tile) * kT;
   const int hk = (blockIdx.x / n_tile) % a.Hkv, b = blockIdx.x / n_tile / a.Hkv;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int len = real_len(a.lens, b, a.S);
+  const int len = real_len(a.lens, b, a.reach);
   load_tile<D, T>(sK, static_cast<const T*>(a.k) + b * a.k_sb + hk * a.k_sh, a.k_st, j0, len);
   load_tile<D, T>(sV, static_cast<const T*>(a.v) + b * a.v_sb + hk * a.v_sh, a.v_st, j0, len);
   const QueryRows rows(j0, min(j0 + kT, a.S) - 1, len, a.window, a.n_sink, a.q_start, a.T);

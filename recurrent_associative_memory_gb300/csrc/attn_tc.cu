@@ -64,7 +64,7 @@ struct Item {
         i0(it / a.H % n_block * 2 * kM),
         b(it / a.H / n_block),
         hk(h / a.G),
-        len(uniform(real_len(a.lens, b, a.S))),
+        len(uniform(real_len(a.lens, b, a.reach))),
         set0(a, i0, len),
         set1(a, i0 + kM, len),
         tiles(a.q_start + i0, a.q_start + min(i0 + 2 * kM, a.T) - 1, len, a.window, a.n_sink, kM) {}

@@ -17,6 +17,7 @@ struct AttnArgs {
   const int* lens;
   int B, T, S, H, Hkv, d, G;   // G = H / Hkv query heads per key/value head
   int window, n_sink, q_start; // window clamped to q_start + T
+  int reach;                   // keys up to the last query's position: min(S, q_start + T)
   float scale;
   long long q_sb, q_st, q_sh, k_sb, k_st, k_sh, v_sb, v_st, v_sh;
   // backward

@@ -90,6 +90,8 @@ AttnArgs attn_args(const dr_attn* a) {
   r.n_sink = a->n_sink, r.q_start = a->q_start;
   // positions reach q_start + T - 1: a wider window sees the same keys
   r.window = a->window < a->q_start + a->T ? a->window : a->q_start + a->T;
+  // and keys from there on are nobody's: whatever they hold, no kernel multiplies by it
+  r.reach = a->S < a->q_start + a->T ? a->S : a->q_start + a->T;
   r.scale = a->scale > 0.f ? a->scale : 1.f / sqrtf(static_cast<float>(a->d));
   r.q_sb = a->q_sb, r.q_st = a->q_st, r.q_sh = a->q_sh;
   r.k_sb = a->k_sb, r.k_st = a->k_st, r.k_sh = a->k_sh;

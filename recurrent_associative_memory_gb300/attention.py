@@ -26,6 +26,18 @@ __all__ = ["window_attn_fwd", "window_attn_bwd", "window_attn_step", "window_cac
            "window_cache_fill"]
 
 
+_MOST = 0x7fffffff
+
+
+def _limits(window, n_sink, q_start=0):
+    """The three as C ints.  A window wider than every position is the widest one."""
+    if window > _MOST:
+        window = _MOST
+    if not (-_MOST <= window and -_MOST <= n_sink <= _MOST and -_MOST <= q_start <= _MOST):
+        raise ValueError(f"window {window}, n_sink {n_sink} and q_start {q_start} must fit 32 bits")
+    return window, n_sink, q_start
+
+
 def _describe(q, k, v, window, n_sink, q_start, lens, scale):
     """The call's dr_attn and its device, its tensors checked."""
     code, dev = activations(q, "q", 4)
@@ -38,7 +50,7 @@ def _describe(q, k, v, window, n_sink, q_start, lens, scale):
     if lens is not None:
         check(lens, "lens", (B,), torch.int32, dev)
     qs, ks, vs = q.stride(), k.stride(), v.stride()
-    return dr.DrAttn(code, B, T, S, H, Hkv, d, window, n_sink, q_start, _scale(scale), ptr(lens),
+    return dr.DrAttn(code, B, T, S, H, Hkv, d, *_limits(window, n_sink, q_start), _scale(scale), ptr(lens),
                      qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), dev
 
 
@@ -129,7 +141,7 @@ def window_attn_step(q, k, v, k_cache, v_cache, pos, window, n_sink=0, *, scale=
     check(v, "v", (B, Hkv, d), q.dtype, dev)
     check(pos, "pos", (B,), torch.int32, dev)
     _check_cache(k_cache, v_cache, B, Hkv, n_sink + window, d, q.dtype, dev)
-    a = dr.DrAttn(code, B, 1, 1, H, Hkv, d, window, n_sink, 0, _scale(scale))
+    a = dr.DrAttn(code, B, 1, 1, H, Hkv, d, *_limits(window, n_sink), _scale(scale))
     if out is None:
         out = q.new_empty(q.shape)
     else:

@@ -176,7 +176,8 @@ __device__ __forceinline__ uint4 cache16(const __nv_bfloat16* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");   // behind the barrier after which the new token's row is there
   return r;
 }
 

@@ -352,6 +352,13 @@ const char *dr_chunk_fwd_path(int variant, int dtype, int dk, int dv, int chunk)
  *     s_j = scale q.k_j;  lse = log sum_j exp(s_j);  out = sum_j exp(s_j - lse) v_j
  * A row that sees no key has out = 0 and lse = -infinity.  H query heads share
  * Hkv key/value heads, H / Hkv neighbouring query heads each.
+ * lens bounds the keys, not the rows: a row at or behind lens[b] sees what its window
+ * and the sinks hold before lens[b], has an output, and its d_out reaches dk and dv.  A
+ * caller that pads its sequences passes d_out = 0 there.  Keys at or behind lens[b], or
+ * behind the last row's position, may hold anything.
+ * bf16 with strides that no tensor map holds (zero, negative or 2^40 bytes on: expanded
+ * tensors) is right too, on the CUDA cores: tens of times slower than a copy to plain
+ * strides beforehand.
  */
 typedef struct dr_attn {
   int dtype;               /* dr_dtype of q, k, v, out and their gradients             */

@@ -5,6 +5,11 @@ A query at position p sees key j where ``j <= p``, ``j < lens[b]`` and
 ``n_sink``.  A row that sees nothing gives 0 (log-sum-exp -inf).  Heads have 64
 or 128 channels, and H query heads share Hkv key/value heads.
 
+``lens`` bounds the keys, not the rows: a padded row at ``p >= lens[b]`` still sees the
+keys before ``lens[b]`` that its window holds.  Its output is not 0, and its ``d_out``
+reaches dk and dv, so that has to be 0 there.  (The convolution and the scan in ``ssm``
+give 0 behind a sequence's end and take no gradient from there.)
+
 ``window_attn_fwd`` / ``window_attn_bwd`` run a prompt, the next piece of one
 (``q_start``) or a training step.  For decoding, ``window_cache`` makes a cache of
 constant size, ``window_cache_fill`` lays a prompt's keys and values out in it and
@@ -68,7 +73,8 @@ def window_attn_fwd(q, k, v, window, n_sink=0, *, q_start=0, lens=None, scale=No
     """Returns (out [B,T,H,d], lse fp32 [B,H,T] or None).
 
     q [B,T,H,d] stands at positions q_start .. q_start+T-1; k, v [B,S,Hkv,d] at 0 .. S-1.
-    They may be slices with any batch, token and head strides of whole 16 bytes.
+    They may be slices with any batch, token and head strides of whole 16 bytes; expanded
+    ones (stride 0) run on the CUDA cores, in bf16 far slower than a contiguous copy.
     ``lens`` int32 [B]: the sequences' real keys.  ``scale``: default 1/sqrt(d)."""
     a, dev = _describe(q, k, v, window, n_sink, q_start, lens, scale)
     if out is None:

@@ -13,10 +13,11 @@
 //   dQ: P = exp(s - lse), dS = P (dO V^T - delta), dQ += dS K
 //   dK, dV over the query heads of the group: dV += P^T dO, dK += dS^T Q
 // The reads of shared memory bound it: 8 of 16 bytes for 64 multiply-adds of a thread (6 for
-// 32 at 32 rows).  fp32 forward, B4 H8 T1024 d64, window
-// 257: 108 us, 18 TFLOP/s.
+// 32 at 32 rows).  fp32, B4 H8 T1024 d64, window 257: forward 115 us, 17 TFLOP/s, backward 461;
+// B2 T4096 H16 over 4 d128, window 512: 1225 and 7280.
 // bf16 with strides that no tensor map holds comes here too (everything fp32 but the
-// operands as loaded and the outputs).
+// operands as loaded and the outputs): the second forward, keys expanded over the batch, takes
+// 1190 us where the tensor cores take 57.
 #include "layers.cuh"
 
 namespace dr {
@@ -315,6 +316,20 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
   store_rows<D, T, 4>(static_cast<T*>(a.dq) + out0, out_st, i0, a.T, o, f, ty, tx);
 }
 
+// A key's sums go over G heads x the rows that see it, thousands of terms: a tile's 64 are
+// summed by themselves first.  (One after the other n terms leave an error of about
+// sqrt(n / 6) units, 1e-6 at n = 1640; in tiles 3e-7.  461 us at B4 H8 T1024 d64, window 257,
+// either way.)
+template <int D>
+__device__ __forceinline__ void add_product_pb(float (&o)[4][D / 16], const float* p, const float* b, int ty, int tx) {
+  float t[4][D / 16] = {};
+  product_pb<D, 4>(t, p, b, ty, tx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[i][c] += t[i][c];
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
   extern __shared__ float sm[];
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] = s[i][j];
         }
       __syncwarp();
-      product_pb<D, 4>(dv, sP, sO, ty, tx);
+      add_product_pb<D>(dv, sP, sO, ty, tx);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] =
               s[i][j] != 0.f ? s[i][j] * (t[i][j] - sL[kT + tx + 16 * j]) : 0.f;
       __syncwarp();
-      product_pb<D, 4>(dk, sP, sQ, ty, tx);
+      add_product_pb<D>(dk, sP, sQ, ty, tx);
     }
   }
   const long long o0 = ((long long)b * a.S * a.Hkv + hk) * D, st = (long long)a.Hkv * D;

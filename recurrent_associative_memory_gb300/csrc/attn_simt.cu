@@ -110,6 +110,20 @@ __device__ __forceinline__ void product_pb(float (&o)[RI][D / 16], const float* 
   }
 }
 
+// o[i][..] = o[i][..] f[i] + that sum.  Sums go over thousands of terms (a key's over G heads x
+// the rows that see it); one after the other, n terms leave an error of about sqrt(n / 6) units,
+// 1e-6 at n = 1640.  A tile's 64 by themselves first: 3e-7, in the same time.
+template <int D, int RI>
+__device__ __forceinline__ void add_product_pb(float (&o)[RI][D / 16], const float (&f)[RI], const float* p,
+                                               const float* b, int ty, int tx) {
+  float t[RI][D / 16] = {};
+  product_pb<D, RI>(t, p, b, ty, tx);
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[i][c] = o[i][c] * f[i] + t[i][c];
+}
+
 template <int D, typename T, int RI>
 __device__ __forceinline__ void store_rows(T* dst, long long st, int r0, int n,
                                            const float (&o)[RI][D / 16], const float (&f)[RI], int ty,
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(KS * kThreads) attn_fwd_simt_kernel(AttnArgs a
       k.fetch(kp, a.k_st, tiles[n + KS] * kT, len);
       v.fetch(vp, a.v_st, tiles[n + KS] * kT, len);
     }
-    float s[RI][4];
+    float s[RI][4], f[RI];
     product_abt<D, RI>(s, sQ, sK, ty, tx);
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(KS * kThreads) attn_fwd_simt_kernel(AttnArgs a
       }
       mx = row_max(mx);
       const float at = mx == -INFINITY ? 0.f : mx;   // a row that has seen nothing yet
-      const float f = ex2(m[i] - at);
+      f[i] = ex2(m[i] - at);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -200,13 +214,11 @@ __global__ void __launch_bounds__(KS * kThreads) attn_fwd_simt_kernel(AttnArgs a
         sum += s[i][j];
         sP[(ty + 16 * i) * kPP + tx + 16 * j] = s[i][j];
       }
-      l[i] = l[i] * f + row_sum(sum);
+      l[i] = l[i] * f[i] + row_sum(sum);
       m[i] = mx;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
     }
     __syncwarp();   // a row's 16 threads are in one warp
-    product_pb<D, RI>(o, sP, sV, ty, tx);
+    add_product_pb<D, RI>(o, f, sP, sV, ty, tx);
   }
   if constexpr (KS == 2) {
     constexpr int V = RI * (D / 16 + 2);
@@ -284,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
   load_tile<D, T>(sO, static_cast<const T*>(a.d_out) + out0, out_st, i0, a.T);
   const KeyTiles tiles(a.q_start + i0, a.q_start + min(i0 + kT, a.T) - 1, len, a.window, a.n_sink, kT);
   float o[4][D / 16] = {}, lse[4], delta[4];
+  const float one[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = min(i0 + ty + 16 * i, a.T - 1);
@@ -310,24 +323,10 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnArgs a) {
       }
     }
     __syncwarp();
-    product_pb<D, 4>(o, sP, sK, ty, tx);
+    add_product_pb<D, 4>(o, one, sP, sK, ty, tx);
   }
   const float f[4] = {a.scale, a.scale, a.scale, a.scale};
   store_rows<D, T, 4>(static_cast<T*>(a.dq) + out0, out_st, i0, a.T, o, f, ty, tx);
-}
-
-// A key's sums go over G heads x the rows that see it, thousands of terms: a tile's 64 are
-// summed by themselves first.  (One after the other n terms leave an error of about
-// sqrt(n / 6) units, 1e-6 at n = 1640; in tiles 3e-7.  461 us at B4 H8 T1024 d64, window 257,
-// either way.)
-template <int D>
-__device__ __forceinline__ void add_product_pb(float (&o)[4][D / 16], const float* p, const float* b, int ty, int tx) {
-  float t[4][D / 16] = {};
-  product_pb<D, 4>(t, p, b, ty, tx);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[i][c] += t[i][c];
 }
 
 template <int D, typename T>
@@ -348,6 +347,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
   load_tile<D, T>(sV, static_cast<const T*>(a.v) + b * a.v_sb + hk * a.v_sh, a.v_st, j0, len);
   const QueryRows rows(j0, min(j0 + kT, a.S) - 1, len, a.window, a.n_sink, a.q_start, a.T);
   float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+  const float one[4] = {1.f, 1.f, 1.f, 1.f};
   for (int g = 0; g < a.G; ++g) {
     const int h = hk * a.G + g;
     const T* qp = static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] = s[i][j];
         }
       __syncwarp();
-      add_product_pb<D>(dv, sP, sO, ty, tx);
+      add_product_pb<D, 4>(dv, one, sP, sO, ty, tx);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -384,13 +384,13 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(AttnArgs a) {
           sP[(ty + 16 * i) * kPP + tx + 16 * j] =
               s[i][j] != 0.f ? s[i][j] * (t[i][j] - sL[kT + tx + 16 * j]) : 0.f;
       __syncwarp();
-      add_product_pb<D>(dk, sP, sQ, ty, tx);
+      add_product_pb<D, 4>(dk, one, sP, sQ, ty, tx);
     }
   }
   const long long o0 = ((long long)b * a.S * a.Hkv + hk) * D, st = (long long)a.Hkv * D;
-  const float fk[4] = {a.scale, a.scale, a.scale, a.scale}, fv[4] = {1.f, 1.f, 1.f, 1.f};
+  const float fk[4] = {a.scale, a.scale, a.scale, a.scale};
   store_rows<D, T, 4>(static_cast<T*>(a.dk) + o0, st, j0, a.S, dk, fk, ty, tx);
-  store_rows<D, T, 4>(static_cast<T*>(a.dv) + o0, st, j0, a.S, dv, fv, ty, tx);
+  store_rows<D, T, 4>(static_cast<T*>(a.dv) + o0, st, j0, a.S, dv, one, ty, tx);
 }
 
 template <typename K>

@@ -203,6 +203,12 @@ __device__ __forceinline__ Four fma(const Four& x, f2 y, const Four& z) {
   return {fma2(x.a, y, z.a), fma2(x.b, y, z.b)};
 }
 __device__ __forceinline__ Four exp2_4(const Four& x) { return {ex2_2(x.a), ex2_2(x.b)}; }
+// exp2 of the rates times the time step.  A state goes through the product of thousands of
+// decays, and ex2.approx rounds low: by 1e-8 to 3e-8 on average for exponents of -0.4 to -0.005,
+// 2e-6 of a state after 100 tokens.  kUp in the exponent, where the multiply-add takes it for
+// nothing, leaves 1e-8 either way (7e-7); exp2(kUp) is 1, so that dt = 0 keeps a state as it is.
+constexpr float kUp = 2e-8f;
+__device__ __forceinline__ Four decay(const Four& A2, f2 dt) { return exp2_4(fma(A2, dt, both(pack2(kUp, kUp)))); }
 // sum over the four of x y
 __device__ __forceinline__ float dot(const Four& x, const Four& y) { return sum2(fma2(x.a, y.a, mul2(x.b, y.b))); }
 
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, FULL ? (N == 64 ? 3 : N == 32 ? 4 : 
         if (FULL) C = load4(s_C + (g + k) * N + 4 * part);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          h[i] = fma(exp2_4(mul(A2[i], u.dt[i])), h[i], mul(B, u.dx[i]));
+          h[i] = fma(decay(A2[i], u.dt[i]), h[i], mul(B, u.dx[i]));
           if (FULL) {
             y[i][k] = dot(C, h[i]);
           } else {
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_ends_kernel(ScanArgs a) 
       const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const Four x = exp2_4(mul(A2[i], u.dt[i]));
+        const Four x = decay(A2[i], u.dt[i]);
         h[i] = fma(x, h[i], mul(B, u.dx[i]));
         cp[i] = mul(cp[i], x);
         e[i] = fma(cp[i], mul(C, dy[i]), e[i]);
@@ -645,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
       const Steps u = load_steps(s_u + t * CPC + ch);
       const Four B = load4(s_B + t * N + 4 * part);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) h[i] = fma(exp2_4(mul(A2[i], u.dt[i])), h[i], mul(B, u.dx[i]));
+      for (int i = 0; i < 2; ++i) h[i] = fma(decay(A2[i], u.dt[i]), h[i], mul(B, u.dx[i]));
     }
   }
 #pragma unroll 1
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
         const Four B = load4(s_B + t * N + 4 * part), C = load4(s_C + t * N + 4 * part);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          hh[g + k + 1][i] = fma(exp2_4(mul(A2[i], u.dt[i])), hh[g + k][i], mul(B, u.dx[i]));
+          hh[g + k + 1][i] = fma(decay(A2[i], u.dt[i]), hh[g + k][i], mul(B, u.dx[i]));
           y[i][k] = dot(C, hh[g + k + 1][i]);
         }
       }
@@ -693,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(ScanArgs a) {
           q[i][2 * k] = dot(gi, B);
           sB = i ? fma(gi, u.dx[i], sB) : mul(gi, u.dx[i]);
           sC = i ? fma(hh[g + k + 1][i], dy[i], sC) : mul(hh[g + k + 1][i], dy[i]);
-          gc[i] = mul(gi, exp2_4(mul(A2[i], u.dt[i])));
+          gc[i] = mul(gi, decay(A2[i], u.dt[i]));
           const Four e = mul(gc[i], hh[g + k][i]);
           q[i][2 * k + 1] = dot(e, A2[i]);
           dA[i] = fma(e, u.dt[i], dA[i]);
@@ -843,7 +849,9 @@ __global__ void __launch_bounds__(kThreads) scan_bc_kernel(ScanArgs a, int tiles
 // one channel of kStepSeqs sequences, whose rates it reads once; all loads are issued before
 // the first is used.
 //   B256 D4096 N16 bf16 (143 MB): 32.8 us, 4.4 TB/s; two sequences 36.9, eight 59 us, the rates
-//   read for every sequence 36.1.
+//   read for every sequence 36.1.  64 % of the issue slots are taken (DRAM 41 %): each of a
+//   channel's N / 4 lanes forms its time step and its gate.  Fewer rows were not tuned for:
+//   B64 D4096 14 us, B16 D2048 8, B1 D2048 6.
 constexpr int kStepSeqs = 4;
 
 template <int N, typename T>
@@ -883,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 8) scan_step_kernel(ScanArgs a) {
     float d = dt[r] + bias;
     if (a.softplus) d = softplus_f<T>(d);
     const float dx = d * x[r];
-    h[r] = fma(exp2_4(mul(A2, pack2(d, d))), h[r], mul(B, pack2(dx, dx)));
+    h[r] = fma(decay(A2, pack2(d, d)), h[r], mul(B, pack2(dx, dx)));
     float y = dot(C, h[r]);
 #pragma unroll
     for (int w = LPC / 2; w >= 1; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);

@@ -13,8 +13,8 @@
 //   dQ: P = exp(s - lse), dS = P (dO V^T - delta), dQ += dS K
 //   dK, dV over the query heads of the group: dV += P^T dO, dK += dS^T Q
 // The reads of shared memory bound it: 8 of 16 bytes for 64 multiply-adds of a thread (6 for
-// 32 at 32 rows).  fp32, B4 H8 T1024 d64, window 257: forward 115 us, 17 TFLOP/s, backward 461;
-// B2 T4096 H16 over 4 d128, window 512: 1225 and 7280.
+// 32 at 32 rows).  fp32, B4 H8 T1024 d64, window 257: forward 115 us, 17 TFLOP/s, backward 459;
+// B2 T4096 H16 over 4 d128, window 512: 1215 and 7270.
 // bf16 with strides that no tensor map holds comes here too (everything fp32 but the
 // operands as loaded and the outputs): the second forward, keys expanded over the batch, takes
 // 1190 us where the tensor cores take 57.

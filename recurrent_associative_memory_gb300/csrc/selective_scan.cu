@@ -54,10 +54,10 @@ template <int N> struct Shape {
 };
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|).  log1p(e) / e over [0, 1] is a polynomial of
-// degree 8, fitted to the least largest relative error by reweighted least squares (3e-8; in fp32
-// arithmetic 1.7e-7).  fp32
-// takes the type's exponential, bf16 the approximate one, whose exponent is |v| 2^-24 off.  (A
-// base-2 logarithm of 1 + e in its place is 2^-18.5 off at e = 1/16, 1.2e-6 of dA.)
+// degree 8, fitted to the least largest relative error by reweighted least squares (3e-8; in
+// fp32 arithmetic 1.7e-7).  fp32 takes the type's exponential, bf16 the approximate one, whose
+// exponent is |v| 2^-24 off.  (A base-2 logarithm of 1 + e in its place is 2^-18.5 off at e =
+// 1/16, 1.2e-6 of dA.)
 template <typename T>
 __device__ __forceinline__ float softplus_f(float v) {
   const float e = sizeof(T) == 4 ? expf(-fabsf(v)) : ex2(-fabsf(v) * kLog2e);

@@ -26,7 +26,7 @@
 //                   They issue P V and the next S of their tile in turns: interleaved, both
 //                   tiles would finish together and their softmax would run at the same time.
 // d 128, 16 heads over 4, window 2048, B1 T16384: 215 us, 1200 TFLOP/s; window 1024, B2 T4096
-// with lengths from half to all of it 62 to 70 us as they fall, 50 GFLOP of visible pairs on
+// with lengths from half to all of it 58 to 70 us as they fall, 50 GFLOP of visible pairs on
 // average, 750 TFLOP/s.  The softmax's instructions and the waits between it and
 // the products bound it: a step takes about 3200 cycles.
 // Rounding: P to bf16 (the sum l takes it in fp32), O once at the end.

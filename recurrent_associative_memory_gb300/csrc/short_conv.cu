@@ -116,15 +116,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
   for (int j = 0; j < K - 1; ++j) {
     x[j] = load_in<K, T, CH>(a, b, t0 - (K - 1) + j, c);
   }
-  // The final state, by the thread that alone reads the initial one: they may be one buffer.
-  // Row j of it is input len - (K - 1) + j, in a short sequence a row of the initial state at
-  // or behind j.
-  if (t0 == 0 && a.s1) {
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + j) * a.D + c,
-                      load_in<K, T, CH>(a, b, len - (K - 1) + j, c));
-  }
   for (int tb = t0; tb < last; tb += kAhead) {
     Raw<T, CH> now[kAhead];
 #pragma unroll
@@ -150,6 +141,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) conv_fwd_ker
       walk(std::true_type());
     else
       walk(std::false_type());
+  }
+  // The final state, by the thread that alone reads the initial one: they may be one buffer.
+  // Row j of it is input len - (K - 1) + j, in a short sequence a row of the initial state at
+  // or behind j.
+  if (t0 == 0 && a.s1) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+      store_ch<T, CH>(static_cast<T*>(a.s1) + ((long long)b * (K - 1) + j) * a.D + c,
+                      load_in<K, T, CH>(a, b, len - (K - 1) + j, c));
   }
 }
 

@@ -516,6 +516,97 @@ int dr_selective_scan_step(const dr_scan *a, const void *x, const void *dt, cons
                            const void *Cm, const void *z, const float *state, float *state_out,
                            void *y, dr_stream_t stream);
 
+/* ======================================================================
+ * What stands around a mixer in a block: the matrix product with its bias,
+ * activation and residual, and the norms before and after the mixer with its
+ * gate and the scale of what it adds to the residual stream.  The rules are
+ * those of the layers above.
+ * ====================================================================== */
+
+/* Activations and gates: none x; relu max(x, 0); silu x sigmoid(x);
+ * gelu_tanh x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))); sigmoid. */
+typedef enum {
+  DR_ACT_NONE = 0, DR_ACT_RELU = 1, DR_ACT_SILU = 2, DR_ACT_GELU_TANH = 3, DR_ACT_SIGMOID = 4
+} dr_act;
+
+/*
+ * Matrix product with its epilogue, M rows of K channels to N:
+ *     y = act(x W + bias) + residual
+ * Every product is summed in fp32 and y is rounded once.  Few rows (single tokens)
+ * take kernels of their own; which ones is decided by the sizes alone.
+ */
+typedef struct dr_linear {
+  int dtype;               /* dr_dtype of everything but the slope                    */
+  int act;                 /* dr_act                                                  */
+  int M, K, N;             /* rows, channels in, channels out; K, N up to 2^24        */
+  int w_transposed;        /* 0: W[k,n] at k w_s + n;  1: at n w_s + k                */
+  long long x_s, w_s, r_s; /* row strides of x, W and residual; rows are contiguous   */
+} dr_linear;
+
+/* Forward.  x [M,K], weight as above, bias [N] or NULL, residual [M,N] or NULL; y [M,N]
+ * contiguous, which may be residual (the same rows).  slope [M,N] or NULL (contiguous)
+ * receives act'(x W + bias), which the backward pass takes: fp16 for DR_BF16, fp32 for
+ * DR_FP32.  Pointers other than bias 16-byte aligned.  Needs its workspace. */
+int dr_linear_fwd(const dr_linear *a, const void *x, const void *weight, const void *bias,
+                  const void *residual, void *y, void *slope, void *workspace,
+                  size_t workspace_bytes, dr_stream_t stream);
+/* Bytes of the forward's workspace (256-byte aligned) on the current device; 0 where none
+ * is needed. */
+size_t dr_linear_fwd_workspace_bytes(const dr_linear *a);
+
+/* Backward from d_y [M,N] (contiguous): with d = d_y * slope (d_y where act is DR_ACT_NONE;
+ * slope may be NULL then)
+ *     dx = d W^T [M,K];  d_weight = x^T d (contiguous, in W's order: [K,N] or, transposed,
+ *     [N,K]);  d_bias [N] = sum of d over the rows
+ * each NULL where it is not wanted; x may be NULL without d_weight, weight without dx.  d is
+ * an operand of both products in its type, d_bias sums it before that rounding.  The
+ * residual's gradient is d_y itself. */
+int dr_linear_bwd(const dr_linear *a, const void *x, const void *weight, const void *d_y,
+                  const void *slope, void *dx, void *d_weight, void *d_bias, void *workspace,
+                  size_t workspace_bytes, dr_stream_t stream);
+size_t dr_linear_bwd_workspace_bytes(const dr_linear *a);
+
+/*
+ * The norms around a block, over rows of D channels:
+ *     n(x; w) = w x / sqrt(mean(x^2) + eps)
+ *     h' = h + scale f(gate) u,   u = n(branch; post_weight) or branch
+ *     y  = n(h'; pre_weight)
+ * h is the residual stream and branch what the block's mixer has given.  y is the norm of
+ * h' as it was summed, before it is rounded to the stream's type.
+ */
+typedef struct dr_block_norm {
+  int dtype;               /* dr_dtype of branch, gate, y and their gradients         */
+  int h_dtype;             /* of h, h' and their gradients: dtype, or DR_FP32         */
+  int M, D;                /* rows; channels, up to 8192                              */
+  int post_norm;           /* 1: the branch's norm is taken                           */
+  int gate_act;            /* dr_act: the gate's function f                           */
+  float eps;               /* >= 0                                                    */
+  long long h_s, b_s, g_s; /* row strides of h, branch and gate; rows are contiguous  */
+} dr_block_norm;
+
+/* Forward.  h [M,D]; branch [M,D] or NULL (only y is formed then, from h); gate [M,D] or
+ * NULL (1); scale, post_weight, pre_weight fp32 [D] or NULL (1); h_out [M,D], needed with
+ * branch, which may be h where h_s is D; y [M,D] or NULL.  h_out and y are contiguous. */
+int dr_block_norm_fwd(const dr_block_norm *a, const void *h, const void *branch, const void *gate,
+                      const float *scale, const float *post_weight, const float *pre_weight,
+                      void *h_out, void *y, dr_stream_t stream);
+
+/* Gradients (contiguous, overwritten; NULL where they are not wanted). */
+typedef struct dr_block_norm_grads {
+  void *dh;                /* [M,D] in the stream's type                              */
+  void *dbranch, *dgate;   /* [M,D] in the activations' type                          */
+  float *dscale, *dpost_weight, *dpre_weight;   /* [D]                                */
+} dr_block_norm_grads;
+
+/* Backward from d_h (of h', in the stream's type) and d_y [M,D] (contiguous; one of them
+ * may be NULL: 0) and the forward's inputs: h as it was before the call.  The workspace
+ * (256-byte aligned) is needed for the gradients over [D]. */
+int dr_block_norm_bwd(const dr_block_norm *a, const void *h, const void *branch, const void *gate,
+                      const float *scale, const float *post_weight, const float *pre_weight,
+                      const void *d_h, const void *d_y, const dr_block_norm_grads *g,
+                      void *workspace, size_t workspace_bytes, dr_stream_t stream);
+size_t dr_block_norm_bwd_workspace_bytes(const dr_block_norm *a);
+
 #ifdef __cplusplus
 }
 #endif

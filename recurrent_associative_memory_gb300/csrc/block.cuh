@@ -1,0 +1,91 @@
+// block.cuh — argument blocks and device helpers of what stands around a mixer: the
+// matrix product with its epilogue, and the norms with gate and residual scale.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "layers.cuh"
+
+namespace dr {
+
+// y = act(x W + bias) + residual; M rows, K -> N channels.  W[k, n] stands at k w_s + n, or
+// (w_t) at n w_s + k.
+struct LinearArgs {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* res;
+  void* y;
+  void* slope;                 // act'(x W + bias), fp16 (bf16 types) or fp32; may be null
+  int M, K, N, act, w_t;
+  long long x_s, w_s, r_s;
+  // backward
+  const void* d_y;             // [M,N]
+  void* dx;
+  void* dw;
+  void* db;
+};
+
+// h' = h + scale f(gate) n(branch);  y = n(h')
+struct BlockNormArgs {
+  const void* h;
+  const void* branch;
+  const void* gate;
+  const float* scale;
+  const float* post_w;
+  const float* pre_w;
+  void* h_out;
+  void* y;
+  int M, D, gate_act, post_norm;
+  float eps, inv_d;
+  long long h_s, b_s, g_s;
+  // backward
+  const void* d_h;
+  const void* d_y;
+  void* dh;
+  void* db;
+  void* dg;
+  float* part;                 // [blocks][3][D]: of scale, post_w, pre_w
+};
+
+// f(x) and f'(x).  Behind +-30 a sigmoid is 0 or 1 to fp32, so the products with 1 - s take x
+// from there on as it is at the border: they stay 0 instead of 0 times infinity.
+template <int ACT> __device__ __forceinline__ float act_of(float x) {
+  if constexpr (ACT == DR_ACT_RELU) return x > 0.f ? x : x == x ? 0.f : x;
+  if constexpr (ACT == DR_ACT_SILU) return x * sigmoid_f(x);
+  if constexpr (ACT == DR_ACT_SIGMOID) return sigmoid_f(x);
+  if constexpr (ACT == DR_ACT_GELU_TANH) {
+    const float c = fminf(fmaxf(x, -30.f), 30.f);
+    const float s = sigmoid_f(c * fmaf(0.07135481283f, c * c, 1.595769122f));   // 0.5 + 0.5 tanh(u) = sigmoid(2 u)
+    return x * s;
+  }
+  return x;
+}
+
+template <int ACT> __device__ __forceinline__ float act_of(float x, float& slope) {
+  const float c = fminf(fmaxf(x, -30.f), 30.f);
+  if constexpr (ACT == DR_ACT_RELU) {
+    slope = x > 0.f ? 1.f : 0.f;
+    return x > 0.f ? x : x == x ? 0.f : x;
+  }
+  if constexpr (ACT == DR_ACT_SILU) {
+    const float s = sigmoid_f(x);
+    slope = s * fmaf(c, 1.f - s, 1.f);
+    return x * s;
+  }
+  if constexpr (ACT == DR_ACT_SIGMOID) {
+    const float s = sigmoid_f(x);
+    slope = s * (1.f - s);
+    return s;
+  }
+  if constexpr (ACT == DR_ACT_GELU_TANH) {
+    const float cc = c * c;
+    const float s = sigmoid_f(c * fmaf(0.07135481283f, cc, 1.595769122f));
+    slope = fmaf(c * s * (1.f - s), fmaf(0.21406443849f, cc, 1.595769122f), s);
+    return x * s;
+  }
+  slope = 1.f;
+  return x;
+}
+
+}  // namespace dr

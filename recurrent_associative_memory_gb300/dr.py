@@ -31,6 +31,7 @@ DR_GDN, DR_KLA, DR_PGDN, DR_KDN, DR_KDA, DR_PKDA, DR_IKDN, DR_EKDN = 0, 1, 2, 3,
 VARIANT_IDS = {"gdn": DR_GDN, "kla": DR_KLA, "pgdn": DR_PGDN, "kdn": DR_KDN, "kda": DR_KDA,
                "pkda": DR_PKDA, "ikdn": DR_IKDN, "ekdn": DR_EKDN}
 DR_FP32, DR_BF16 = 0, 1
+ACT_IDS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "sigmoid": 4}
 STATUS = {0: "DR_OK", -1: "DR_ERR_NULL", -2: "DR_ERR_SHAPE", -3: "DR_ERR_DTYPE",
           -4: "DR_ERR_ALIGN", -5: "DR_ERR_WORKSPACE", -6: "DR_ERR_CUDA", -7: "DR_ERR_TIMEOUT",
           -8: "DR_ERR_NONFINITE", -9: "DR_ERR_UNSUPPORTED", -10: "DR_ERR_ARG"}
@@ -355,3 +356,75 @@ def dr_selective_scan_step(a: DrScan, x, dt, Bm, Cm, z, state, state_out, y, str
     return _lib.dr_selective_scan_step(ctypes.byref(a), _ptr(x), _ptr(dt), _ptr(Bm), _ptr(Cm),
                                        _ptr(z), _ptr(state), _ptr(state_out), _ptr(y),
                                        _stream(stream))
+
+
+# ---------------------------------------------------------------- what stands around a mixer
+
+
+class DrLinear(ctypes.Structure):
+    """Mirror of ``dr_linear``."""
+    _fields_ = [(n, c_int) for n in ("dtype", "act", "M", "K", "N", "w_transposed")] + [
+        (n, c_longlong) for n in ("x_s", "w_s", "r_s")]
+
+
+class DrBlockNorm(ctypes.Structure):
+    """Mirror of ``dr_block_norm``."""
+    _fields_ = [(n, c_int) for n in ("dtype", "h_dtype", "M", "D", "post_norm", "gate_act")] + [
+        ("eps", c_float)] + [(n, c_longlong) for n in ("h_s", "b_s", "g_s")]
+
+
+class DrBlockNormGrads(ctypes.Structure):
+    """Mirror of ``dr_block_norm_grads``."""
+    _fields_ = [(n, c_void_p) for n in ("dh", "dbranch", "dgate", "dscale", "dpost_weight",
+                                        "dpre_weight")]
+
+
+_declare("dr_linear_fwd", "s" + "p" * 7 + "np", DrLinear)
+_declare("dr_linear_fwd_workspace_bytes", "s", DrLinear, c_size_t)
+_declare("dr_linear_bwd", "s" + "p" * 8 + "np", DrLinear)
+_declare("dr_linear_bwd_workspace_bytes", "s", DrLinear, c_size_t)
+_declare("dr_block_norm_fwd", "s" + "p" * 9, DrBlockNorm)
+_declare("dr_block_norm_bwd", "s" + "p" * 8 + "ppnp", DrBlockNorm)
+_declare("dr_block_norm_bwd_workspace_bytes", "s", DrBlockNorm, c_size_t)
+
+
+def dr_linear_fwd(a: DrLinear, x, weight, bias, residual, y, slope, workspace=None,
+                  workspace_bytes: int = 0, stream=None) -> int:
+    return _lib.dr_linear_fwd(ctypes.byref(a), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual),
+                              _ptr(y), _ptr(slope), _ptr(workspace), workspace_bytes,
+                              _stream(stream))
+
+
+def dr_linear_fwd_workspace_bytes(a: DrLinear) -> int:
+    return _lib.dr_linear_fwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_linear_bwd(a: DrLinear, x, weight, d_y, slope, dx, d_weight, d_bias, workspace=None,
+                  workspace_bytes: int = 0, stream=None) -> int:
+    return _lib.dr_linear_bwd(ctypes.byref(a), _ptr(x), _ptr(weight), _ptr(d_y), _ptr(slope),
+                              _ptr(dx), _ptr(d_weight), _ptr(d_bias), _ptr(workspace),
+                              workspace_bytes, _stream(stream))
+
+
+def dr_linear_bwd_workspace_bytes(a: DrLinear) -> int:
+    return _lib.dr_linear_bwd_workspace_bytes(ctypes.byref(a))
+
+
+def dr_block_norm_fwd(a: DrBlockNorm, h, branch, gate, scale, post_weight, pre_weight, h_out, y,
+                      stream=None) -> int:
+    return _lib.dr_block_norm_fwd(ctypes.byref(a), _ptr(h), _ptr(branch), _ptr(gate), _ptr(scale),
+                                  _ptr(post_weight), _ptr(pre_weight), _ptr(h_out), _ptr(y),
+                                  _stream(stream))
+
+
+def dr_block_norm_bwd(a: DrBlockNorm, h, branch, gate, scale, post_weight, pre_weight, d_h, d_y,
+                      grads: DrBlockNormGrads, workspace=None, workspace_bytes: int = 0,
+                      stream=None) -> int:
+    return _lib.dr_block_norm_bwd(ctypes.byref(a), _ptr(h), _ptr(branch), _ptr(gate), _ptr(scale),
+                                  _ptr(post_weight), _ptr(pre_weight), _ptr(d_h), _ptr(d_y),
+                                  ctypes.byref(grads), _ptr(workspace), workspace_bytes,
+                                  _stream(stream))
+
+
+def dr_block_norm_bwd_workspace_bytes(a: DrBlockNorm) -> int:
+    return _lib.dr_block_norm_bwd_workspace_bytes(ctypes.byref(a))

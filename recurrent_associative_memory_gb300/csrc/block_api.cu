@@ -8,9 +8,10 @@
 
 namespace dr {
 
-cudaError_t launch_linear_fwd_simt(const LinearArgs& a, int dtype, cudaStream_t st);
-size_t linear_bwd_workspace_simt(const LinearArgs& a, int dtype, bool slope, bool bias);
-cudaError_t launch_linear_bwd_simt(const LinearArgs& a, int dtype, void* workspace, cudaStream_t st);
+size_t linear_fwd_workspace(const LinearArgs& a, int dtype);
+cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st);
+size_t linear_bwd_workspace(const LinearArgs& a, int dtype, bool act);
+cudaError_t launch_linear_bwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st);
 int block_norm_bwd_blocks(const BlockNormArgs& a, int sms);
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype, cudaStream_t st);
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, float* d_scale, float* d_post,
@@ -80,7 +81,8 @@ using namespace dr;
 extern "C" {
 
 size_t dr_linear_fwd_workspace_bytes(const dr_linear* a) {
-  return 0;
+  if (!a || check_linear(a) != DR_OK) return 0;
+  return linear_fwd_workspace(linear_args(a), a->dtype);
 }
 
 int dr_linear_fwd(const dr_linear* a, const void* x, const void* weight, const void* bias, const void* residual, void* y,
@@ -89,15 +91,19 @@ int dr_linear_fwd(const dr_linear* a, const void* x, const void* weight, const v
   int st = check_linear(a);
   if (st != DR_OK) return st;
   if (!aligned(16, x, weight, residual, y, slope)) return DR_ERR_ALIGN;
-  if (!sm_count()) return DR_ERR_CUDA;
+  const size_t need = dr_linear_fwd_workspace_bytes(a);
+  if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
+  if (!aligned(256, workspace)) return DR_ERR_ALIGN;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   LinearArgs r = linear_args(a);
   r.x = x, r.w = weight, r.bias = bias, r.res = residual, r.y = y, r.slope = slope;
-  return status_of(launch_linear_fwd_simt(r, a->dtype, stream_of(stream)));
+  return status_of(launch_linear_fwd(r, a->dtype, sms, workspace, stream_of(stream)));
 }
 
 size_t dr_linear_bwd_workspace_bytes(const dr_linear* a) {
   if (!a || check_linear(a) != DR_OK) return 0;
-  return linear_bwd_workspace_simt(linear_args(a), a->dtype, a->act != DR_ACT_NONE, true);
+  return linear_bwd_workspace(linear_args(a), a->dtype, a->act != DR_ACT_NONE);
 }
 
 int dr_linear_bwd(const dr_linear* a, const void* x, const void* weight, const void* d_y, const void* slope, void* dx,
@@ -110,11 +116,12 @@ int dr_linear_bwd(const dr_linear* a, const void* x, const void* weight, const v
   const size_t need = dr_linear_bwd_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
-  if (!sm_count()) return DR_ERR_CUDA;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   LinearArgs r = linear_args(a);
   r.x = x, r.w = weight, r.d_y = d_y, r.slope = a->act != DR_ACT_NONE ? const_cast<void*>(slope) : nullptr;
   r.dx = dx, r.dw = d_weight, r.db = d_bias;
-  return status_of(launch_linear_bwd_simt(r, a->dtype, workspace, stream_of(stream)));
+  return status_of(launch_linear_bwd(r, a->dtype, sms, workspace, stream_of(stream)));
 }
 
 int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch, const void* gate, const float* scale,

@@ -1,0 +1,268 @@
+// linear_pair.cu — the matrix product on tcgen05, tiles of 256 rows by BN columns over a pair
+// of CTAs.
+//
+// Each CTA of a pair holds 128 rows of A and half of B's columns; one MMA of the pair
+// multiplies 256 x BN x 16 from both shared memories, so that a stage of 64 k moves
+// (128 + BN / 2) x 128 bytes into each SM for 512 (BN = 256) cycles of products: 64 bytes a
+// cycle, where one CTA by itself would need 96.  Accumulators are two buffers of BN columns of
+// TMEM: while the epilogue reads one, the next tile's products go to the other.
+//   warps 0-3  epilogue: rows 32 w .. of the CTA's 128, a thread per row
+//   warp 4     TMA: this CTA's part of each stage, counted on the first CTA's barrier
+//   warp 5     the MMAs, in the first CTA of the pair
+// The pairs stay: one per two SMs walks the tiles, eight tiles of rows at a time, so that
+// neighbours in time share columns of B and rows of A in L2.
+#include <type_traits>
+
+#include "linear_tc.cuh"
+
+namespace dr {
+namespace {
+
+using namespace lin;
+
+constexpr int kThreads = 192, kEpilogueWarps = 4, kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kGroup = 8;   // tiles of rows that are walked together
+
+template <int BN> struct Smem {
+  static constexpr int kA = 128 * kBK * 2, kB = BN / 2 * kBK * 2, kStage = kA + kB;
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int oBias = kStages * kStage;                  // fp32, each epilogue warp's [BN]
+  static constexpr int oTurn = oBias + kEpilogueWarps * BN * 4;   // and [32][33]: rows to columns
+  static constexpr int kBytes = oTurn + kEpilogueWarps * 32 * 33 * 4 + 1024;
+};
+
+struct Tiles {
+  int m, n;   // numbers of tiles
+  __device__ __forceinline__ void at(int t, int& tm, int& tn) const {
+    const int per = kGroup * n, g = t / per, r = t - g * per, size = min(kGroup, m - g * kGroup);
+    tn = r / size;
+    tm = g * kGroup + r - tn * size;
+  }
+};
+
+// T: the type of C, bias and residual; FULL: with bias, activation, residual, slope
+template <int BN, bool A_MN, bool B_MN, typename T, bool FULL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Epilogue e,
+                       Tiles tiles, int n_k) {
+  using L = Smem<BN>;
+  using S = typename std::conditional<sizeof(T) == 2, __half, float>::type;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[2], b_free[2], b_end;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&b_acc[i], 1), mbar_init(&b_free[i], 2 * kEpilogueWarps);
+    mbar_init(&b_end, 1);
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == kMmaWarp) pair_tmem_alloc(&s_tmem, 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = uniform(s_tmem);
+  const int n_tile = tiles.m * tiles.n, first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  auto give_up = [&] {
+    s_abort = 1;
+    set_status(DR_ERR_TIMEOUT);
+    return false;
+  };
+  auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return all(wait_phase(bar, parity) || give_up()); };
+
+  if (warp < kEpilogueWarps) {   // ------------------------------------------------ epilogue
+    float* turn = reinterpret_cast<float*>(sm + L::oTurn) + warp * 32 * 33;
+    int it = 0;
+    for (int t = first; t < n_tile; t += step, ++it) {
+      int tm, tn;
+      tiles.at(t, tm, tn);
+      const int buf = it & 1, n0 = tn * BN;
+      const int m0 = tm * 256 + rank * 128 + warp * 32, m = m0 + lane;
+      float* bias = reinterpret_cast<float*>(sm + L::oBias) + warp * BN;   // a warp's own: no barrier to be left at
+      if constexpr (FULL) {
+        for (int c = lane; c < BN; c += 32)
+          bias[c] = e.bias && n0 + c < e.N ? to_f(static_cast<const T*>(e.bias)[n0 + c]) : 0.f;
+        __syncwarp();
+      }
+      const bool live = m < e.M;
+      const T* res = FULL && e.res && live ? static_cast<const T*>(e.res) + m * e.r_m + n0 : nullptr;
+      T* C = static_cast<T*>(e.C) + (long long)m * e.N + n0;
+      S* slope = FULL && e.slope ? static_cast<S*>(e.slope) + (long long)m * e.N + n0 : nullptr;
+      Raw16<T> r[2];
+      auto ahead = [&](int c) {   // the residual of columns c .. c + 31
+        if (!FULL || !res || !e.vec) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 16 * h < BN && n0 + c + 16 * h < e.N) r[h].load(res + c + 16 * h);
+      };
+      ahead(0);
+      if (!wait(&b_acc[buf], (it / 2) & 1)) break;
+      tc_fence_after();
+      for (int c = 0; c < BN && n0 + c < e.N; c += 32) {
+        float v[32];
+        tmem_ld32(tmem + buf * BN + c + (static_cast<uint32_t>(warp * 32) << 16), reinterpret_cast<uint32_t*>(v));
+        tmem_ld_wait();
+        if (e.vec) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[16], s[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = v[16 * h + i];
+            if constexpr (FULL) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + c + 16 * h + i);
+                x[i] += b.x, x[i + 1] += b.y, x[i + 2] += b.z, x[i + 3] += b.w;
+              }
+              act_all(e.act, slope != nullptr, x, s);
+              if (res) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] += r[h][i];
+              }
+            }
+            if (live && n0 + c + 16 * h < e.N) {
+              put16(C + c + 16 * h, x);
+              if (FULL && slope) put16(slope + c + 16 * h, s);
+            }
+          }
+          ahead(c + 32);
+        } else {   // rows on any address: a lane takes a column, and rows are stored one by one
+#pragma unroll
+          for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+          __syncwarp();
+          const int n = n0 + c + lane;
+          if (n < e.N) {
+            const float b = FULL ? bias[c + lane] : 0.f;
+#pragma unroll 4
+            for (int i = 0; i < 32 && m0 + i < e.M; ++i) {
+              float x = turn[i * 33 + lane] + b, s = 1.f;
+              if constexpr (FULL) {
+                x = act_any(e.act, x, s);
+                if (e.slope) static_cast<S*>(e.slope)[(m0 + i) * (long long)e.N + n] = static_cast<S>(s);
+                if (e.res) x += to_f(static_cast<const T*>(e.res)[(m0 + i) * e.r_m + n]);
+              }
+              static_cast<T*>(e.C)[(m0 + i) * (long long)e.N + n] = from_f<T>(x);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (elect_one()) arrive_remote(map_rank(smem_u32(&b_free[buf]), 0));
+    }
+  } else if (warp == kLoadWarp) {   // --------------------------------------------- loads
+    uint32_t n = 0;
+    bool ok = true;
+    for (int t = first; t < n_tile && ok; t += step) {
+      int tm, tn;
+      tiles.at(t, tm, tn);
+      const int m0 = tm * 256 + rank * 128, n0 = tn * BN + rank * (BN / 2);
+      for (int k = 0; k < n_k; ++k, ++n) {
+        const uint32_t s = n % NS;
+        if (n >= NS && !(ok = wait(&b_empty[s], (n / NS - 1) & 1))) break;
+        if (elect_one()) {
+          uint8_t* a = sm + s * L::kStage;
+          uint8_t* b = a + L::kA;
+          const uint32_t bar = map_rank(smem_u32(&b_full[s]), 0);
+          if (rank == 0) mbar_expect_tx(&b_full[s], 2 * L::kStage);
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pair_load(a + i * 8192, &tmA, bar, m0 + 64 * i, k * kBK);
+          } else {
+            pair_load(a, &tmA, bar, k * kBK, m0);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int i = 0; i < BN / 128; ++i) pair_load(b + i * 8192, &tmB, bar, n0 + 64 * i, k * kBK);
+          } else {
+            pair_load(b, &tmB, bar, k * kBK, n0);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // no copy may be in flight when the pair ends, nor the MMAs' word that a stage is free: the
+    // first CTA's barriers count both's copies, each CTA's own the MMAs'
+    const uint32_t last = n > NS ? n - NS : 0;
+    if (rank == 0)
+      for (uint32_t i = last; i < n; ++i) wait_phase(&b_full[i % NS], (i / NS) & 1);
+    if (ok)
+      for (uint32_t i = last; i < n; ++i) wait_phase(&b_empty[i % NS], (i / NS) & 1);
+  } else if (rank == 0) {   // ------------------------------------------------------ MMAs
+    constexpr uint32_t ID = idesc_bf16(256, BN, A_MN, B_MN);
+    const uint32_t a0 = smem_u32(sm), b0 = a0 + L::kA;
+    const uint64_t da = desc_sw128(a0, A_MN ? 8192 : 0, 1024), db = desc_sw128(b0, B_MN ? 8192 : 0, 1024);
+    uint32_t n = 0;
+    int it = 0;
+    bool ok = true;
+    for (int t = first; t < n_tile && ok; t += step, ++it) {
+      const int buf = it & 1;
+      if (it >= 2 && !(ok = all(wait_cluster(&b_free[buf], (it / 2 - 1) & 1) || give_up()))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * BN;
+      for (int k = 0; k < n_k; ++k, ++n) {
+        const uint32_t s = n % NS;
+        if (!(ok = wait(&b_full[s], (n / NS) & 1))) break;
+        tc_fence_after();
+        const uint32_t at = (s * L::kStage) >> 4;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j)
+            pair_mma(d, da + at + j * (A_MN ? 128 : 2), db + at + j * (B_MN ? 128 : 2), ID, k > 0 || j > 0);
+          pair_commit(&b_empty[s]);
+        }
+        __syncwarp();
+      }
+      if (ok && elect_one()) pair_commit(&b_acc[buf]);
+      __syncwarp();
+    }
+    if (elect_one()) pair_commit(&b_end, 1);   // no MMA may be under way when the pair ends
+    __syncwarp();
+    wait_phase(&b_end, 0);
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();   // nothing of this CTA is read or counted on any more
+  tc_fence_after();
+  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 2 * BN);
+}
+
+template <int BN, bool A_MN, bool B_MN, typename T, bool FULL>
+cudaError_t go(const Operand& A, const Operand& B, const Epilogue& e, int sms, cudaStream_t st) {
+  CUtensorMap a, b;
+  if (!make_operand_map(&a, A, 128) || !make_operand_map(&b, B, BN / 2)) return cudaErrorInvalidValue;
+  auto* kernel = linear_pair_kernel<BN, A_MN, B_MN, T, FULL>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<BN>::kBytes);
+  if (err != cudaSuccess) return err;
+  const Tiles t{(A.rows + 255) / 256, (B.rows + BN - 1) / BN};
+  const int pairs = static_cast<int>(min((long long)t.m * t.n, sms / 2LL));
+  kernel<<<2 * pairs, kThreads, Smem<BN>::kBytes, st>>>(a, b, e, t, (A.k + kBK - 1) / kBK);
+  return cudaGetLastError();
+}
+
+template <int BN, typename T>
+cudaError_t by_order(const Operand& A, const Operand& B, const Epilogue& e, bool full, int sms, cudaStream_t st) {
+  if (full) return B.mn ? go<BN, false, true, T, true>(A, B, e, sms, st) : go<BN, false, false, T, true>(A, B, e, sms, st);
+  if (A.mn) return go<BN, true, true, T, false>(A, B, e, sms, st);
+  return B.mn ? go<BN, false, true, T, false>(A, B, e, sms, st) : go<BN, false, false, T, false>(A, B, e, sms, st);
+}
+
+}  // namespace
+
+// `full`: a forward product, A K-major; otherwise C alone, and A MN-major only if B is too
+cudaError_t launch_linear_pair(const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full, int sms,
+                               cudaStream_t st) {
+  return by_order<256, __nv_bfloat16>(A, B, e, full, sms, st);
+}
+
+}  // namespace dr

@@ -126,8 +126,6 @@ __global__ void __launch_bounds__(256) join_bias_kernel(const float* part, int b
   }
 }
 
-size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
-
 }  // namespace
 
 cudaError_t launch_linear_fwd_simt(const LinearArgs& a, int dtype, cudaStream_t st) {
@@ -135,42 +133,37 @@ cudaError_t launch_linear_fwd_simt(const LinearArgs& a, int dtype, cudaStream_t 
   return gemm(g, dtype, st);
 }
 
-// d_y * slope, then the parts of the bias's gradient
-size_t linear_bwd_workspace_simt(const LinearArgs& a, int dtype, bool slope, bool bias) {
-  size_t n = 0;
-  if (slope) n += round256((size_t)a.M * a.N * (dtype == DR_FP32 ? 4 : 2));
-  if (bias) n += round256((a.M + size_t(kRows) - 1) / kRows * a.N * 4);
-  return n;
-}
-
-cudaError_t launch_linear_bwd_simt(const LinearArgs& a, int dtype, void* workspace, cudaStream_t st) {
-  const void* d = a.d_y;
-  const int blocks = (a.M + kRows - 1) / kRows;
-  if (a.slope || a.db) {
-    void* out = a.slope ? workspace : nullptr;
-    float* part = a.db ? reinterpret_cast<float*>(static_cast<char*>(workspace) + linear_bwd_workspace_simt(a, dtype, a.slope, false)) : nullptr;
-    const dim3 grid(blocks, (a.N + 31) / 32);
-    if (dtype == DR_FP32)
-      slope_kernel<float, float><<<grid, 256, 0, st>>>(static_cast<const float*>(a.d_y), static_cast<const float*>(a.slope),
-                                                       static_cast<float*>(out), part, a.M, a.N);
-    else
-      slope_kernel<__nv_bfloat16, __half><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(a.d_y),
-                                                                static_cast<const __half*>(a.slope),
-                                                                static_cast<__nv_bfloat16*>(out), part, a.M, a.N);
-    if (out) d = out;
-    if (part) {
-      if (dtype == DR_FP32) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
-      else join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
-    }
-  }
+// dx and dw from d [M,N]
+cudaError_t launch_linear_bwd_simt(const LinearArgs& a, const void* d, int dtype, cudaStream_t st) {
   const long long w_k = a.w_t ? 1 : a.w_s, w_n = a.w_t ? a.w_s : 1;
-  cudaError_t e = cudaGetLastError();
-  if (a.dx && e == cudaSuccess)
+  cudaError_t e = cudaSuccess;
+  if (a.dx)
     e = gemm(Gemm{d, a.w, a.dx, nullptr, nullptr, nullptr, a.M, a.K, a.N, a.N, 1, w_n, w_k, a.K, 0, DR_ACT_NONE}, dtype, st);
   if (a.dw && e == cudaSuccess)
     e = a.w_t ? gemm(Gemm{d, a.x, a.dw, nullptr, nullptr, nullptr, a.N, a.K, a.M, 1, a.N, a.x_s, 1, a.K, 0, DR_ACT_NONE}, dtype, st)
               : gemm(Gemm{a.x, d, a.dw, nullptr, nullptr, nullptr, a.K, a.N, a.M, 1, a.x_s, a.N, 1, a.N, 0, DR_ACT_NONE}, dtype, st);
   return e;
+}
+
+// d = d_y * slope [M,N] (null: not kept) and the bias's gradient (null: not wanted), over
+// part [linear_slope_blocks(M)][N]
+int linear_slope_blocks(int M) { return static_cast<int>((M + (long long)kRows - 1) / kRows); }
+
+cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* d, float* part, cudaStream_t st) {
+  const int blocks = linear_slope_blocks(a.M);
+  const dim3 grid(blocks, (a.N + 31) / 32);
+  if (dtype == DR_FP32)
+    slope_kernel<float, float><<<grid, 256, 0, st>>>(static_cast<const float*>(a.d_y), static_cast<const float*>(a.slope),
+                                                     static_cast<float*>(d), part, a.M, a.N);
+  else
+    slope_kernel<__nv_bfloat16, __half><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(a.d_y),
+                                                              static_cast<const __half*>(a.slope),
+                                                              static_cast<__nv_bfloat16*>(d), part, a.M, a.N);
+  if (a.db) {
+    if (dtype == DR_FP32) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
+    else join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace dr

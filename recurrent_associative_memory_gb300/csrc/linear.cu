@@ -3,12 +3,17 @@
 
 namespace dr {
 
-cudaError_t launch_linear_fwd_simt(const LinearArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_linear_bwd_simt(const LinearArgs& a, const void* d, int dtype, cudaStream_t st);
+cudaError_t launch_linear_pack(const void* src, long long stride, int rows, int cols, int dtype, void* dst, int pitch,
+                               long long piece, int sms, cudaStream_t st);
 int linear_slope_blocks(int M);
-cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* d, float* part, cudaStream_t st);
+cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int pitch, long long piece, float* part,
+                                cudaStream_t st);
 cudaError_t launch_linear_pair(const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full, int sms,
                                cudaStream_t st);
+cudaError_t launch_linear_few_bf16(int tn, const lin::Operand& M, const lin::Operand& N, const lin::Epilogue& e, bool full,
+                                   int split, cudaStream_t st);
+cudaError_t launch_linear_few_fp32(int tn, const lin::Operand& M, const lin::Operand& N, const lin::Epilogue& e, bool full,
+                                   int split, cudaStream_t st);
 
 namespace {
 
@@ -16,64 +21,120 @@ using lin::Epilogue;
 using lin::Operand;
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 template <typename... P> bool on32(const P*... p) { return (((reinterpret_cast<uintptr_t>(p) | ...)) & 31) == 0; }
 
-// x and W of a product y = x W
-Operand rows_of(const void* p, int rows, int k, long long s) { return {p, rows, k, s, false}; }
-Operand weight_of(const LinearArgs& a) { return {a.w, a.N, a.K, a.w_s, !a.w_t}; }
-
-struct BwdPlan {
-  size_t d, part, bytes;   // offsets: d_y * slope, the bias's parts
+// A matrix as a tensor map has to find it: in place, or as a copy in the workspace (fp32: its
+// pieces).
+struct Packed {
+  bool copy;
+  int rows, cols, pitch;
+  long long stride, piece;
+  size_t bytes;
+  Packed(int dtype, int rows_, int cols_, long long s) : rows(rows_), cols(cols_), stride(s) {
+    copy = dtype == DR_FP32 || (rows > 1 && (s <= 0 || s % 8 || s >= (1LL << 38)));
+    pitch = (cols + 7) / 8 * 8;
+    piece = dtype == DR_FP32 ? (long long)rows * pitch : 0;
+    bytes = copy ? round256((size_t)rows * pitch * (dtype == DR_FP32 ? 6 : 2)) : 0;
+  }
+  cudaError_t make(const void*& p, void* to, int dtype, int sms, cudaStream_t st) {
+    if (!copy) return cudaSuccess;
+    cudaError_t e = launch_linear_pack(p, stride, rows, cols, dtype, to, pitch, piece, sms, st);
+    p = to, stride = pitch;
+    return e;
+  }
+  // k along the columns, or along the rows
+  Operand k_cols(const void* p) const { return {p, rows, cols, stride, false, piece}; }
+  Operand k_rows(const void* p) const { return {p, cols, rows, stride, true, piece}; }
 };
 
-BwdPlan bwd_plan(const LinearArgs& a, int dtype, bool act) {
-  BwdPlan p{};
-  p.d = 0;
-  p.part = act ? round256((size_t)a.M * a.N * (dtype == DR_FP32 ? 4 : 2)) : 0;
-  p.bytes = p.part + round256((size_t)linear_slope_blocks(a.M) * a.N * 4);
-  return p;
+Packed pack_x(const LinearArgs& a, int dtype) { return {dtype, a.M, a.K, a.x_s}; }
+Packed pack_w(const LinearArgs& a, int dtype) { return {dtype, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, a.w_s}; }
+
+// C[m,n] = sum over k of A[m,k] B[n,k], and its epilogue where `full`.
+// Which kernel: the time that each one's SMs need for its stages, by the bytes that a stage
+// brings into an SM (64 a cycle), and what a launch costs besides.
+cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, int dtype, int sms, cudaStream_t st) {
+  const bool fp32 = dtype == DR_FP32;
+  const int es = fp32 ? 4 : 2;
+  const long long n_k = ceil_div(A.k, lin::kBK), times = fp32 ? lin::kPairs : 1;
+  const int bn = fp32 ? 128 : 256;
+  const long long pair_tiles = ceil_div(A.rows, 256) * ceil_div(B.rows, bn);
+  long long best = ceil_div(pair_tiles, sms / 2) * (n_k * times * (256 + bn)) + 6000;
+  int tn = 0, split = 1;
+  const long long n_tiles = ceil_div(B.rows, 128);
+  for (int t = A.mn ? 64 : 16; t <= (fp32 ? 64 : 128); t *= 2) {
+    const long long tiles = n_tiles * ceil_div(A.rows, t);
+    if (tiles > 8LL * sms) continue;
+    for (int s = 1; s <= 8 && s <= n_k; ++s) {
+      const long long cost = ceil_div(tiles * s, sms) * (ceil_div(n_k, s) * times * (128 + t) * 2) + (s > 1 ? 4500 : 3500);
+      if (cost < best) best = cost, tn = t, split = s;
+    }
+  }
+  if (tn) return (fp32 ? launch_linear_few_fp32 : launch_linear_few_bf16)(tn, A, B, e, full, split, st);
+  e.vec = e.N * es % 32 == 0 && on32(e.C, e.res) && on32(e.slope) && (!e.res || e.r_m * es % 32 == 0);
+  return launch_linear_pair(A, B, e, full, sms, st);
 }
+
+struct BwdPlan {
+  Packed x, w;
+  bool keep_d;
+  int pitch;                           // of d
+  long long piece;
+  size_t o_x, o_w, o_d, o_part, bytes;
+  BwdPlan(const LinearArgs& a, int dtype, bool act) : x(pack_x(a, dtype)), w(pack_w(a, dtype)) {
+    const bool fp32 = dtype == DR_FP32;
+    pitch = (a.N + 7) / 8 * 8;
+    keep_d = act || fp32 || (a.N % 8 != 0 && a.M > 1);
+    piece = fp32 ? (long long)a.M * pitch : 0;
+    o_x = 0, o_w = x.bytes, o_d = o_w + w.bytes;
+    o_part = o_d + (keep_d ? round256((size_t)a.M * pitch * (fp32 ? 6 : 2)) : 0);
+    bytes = o_part + round256((size_t)linear_slope_blocks(a.M) * a.N * 4);
+  }
+};
 
 }  // namespace
 
-size_t linear_fwd_workspace(const LinearArgs& a, int dtype) { return 0; }
+size_t linear_fwd_workspace(const LinearArgs& a, int dtype) { return pack_x(a, dtype).bytes + pack_w(a, dtype).bytes; }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st) {
-  const Operand x = rows_of(a.x, a.M, a.K, a.x_s), w = weight_of(a);
-  if (dtype == DR_BF16 && operand_ok(x) && operand_ok(w)) {
-    Epilogue e{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, a.r_s, 0};
-    e.vec = a.N % 16 == 0 && on32(a.y, a.slope, a.res) && (!a.res || a.r_s % 16 == 0);
-    return launch_linear_pair(x, w, e, true, sms, st);
-  }
-  return launch_linear_fwd_simt(a, dtype, st);
+  char* ws = static_cast<char*>(workspace);
+  Packed px = pack_x(a, dtype), pw = pack_w(a, dtype);
+  const void *x = a.x, *w = a.w;
+  cudaError_t e = px.make(x, ws, dtype, sms, st);
+  if (e == cudaSuccess) e = pw.make(w, ws + px.bytes, dtype, sms, st);
+  if (e != cudaSuccess) return e;
+  return product(px.k_cols(x), a.w_t ? pw.k_cols(w) : pw.k_rows(w),
+                 Epilogue{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, a.r_s, 0}, true, dtype, sms, st);
 }
 
-size_t linear_bwd_workspace(const LinearArgs& a, int dtype, bool act) { return bwd_plan(a, dtype, act).bytes; }
+size_t linear_bwd_workspace(const LinearArgs& a, int dtype, bool act) { return BwdPlan(a, dtype, act).bytes; }
 
 cudaError_t launch_linear_bwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st) {
-  const BwdPlan p = bwd_plan(a, dtype, a.slope != nullptr);
+  BwdPlan p(a, dtype, a.slope != nullptr);
   char* ws = static_cast<char*>(workspace);
-  const void* d = a.d_y;
+  const bool keep = p.keep_d && (a.dx || a.dw);
   cudaError_t e = cudaSuccess;
-  if (a.slope || a.db) {
-    e = launch_linear_slope(a, dtype, a.slope ? ws + p.d : nullptr, a.db ? reinterpret_cast<float*>(ws + p.part) : nullptr, st);
-    if (e != cudaSuccess) return e;
-    if (a.slope) d = ws + p.d;
+  if (keep || a.db)
+    e = launch_linear_slope(a, dtype, keep ? ws + p.o_d : nullptr, p.pitch, p.piece,
+                            a.db ? reinterpret_cast<float*>(ws + p.o_part) : nullptr, st);
+  const void* d = keep ? ws + p.o_d : a.d_y;
+  const Operand rows{d, a.M, a.N, keep ? p.pitch : a.N, false, p.piece};   // k along the channels out
+  const Operand cols{d, a.N, a.M, keep ? p.pitch : a.N, true, p.piece};    // k along the tokens
+  if (a.dx && e == cudaSuccess) {   // dx[m,k] = sum over n of d[m,n] W[k,n]
+    const void* w = a.w;
+    e = p.w.make(w, ws + p.o_w, dtype, sms, st);
+    if (e == cudaSuccess)
+      e = product(rows, a.w_t ? p.w.k_rows(w) : p.w.k_cols(w), Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K}, false,
+                  dtype, sms, st);
   }
-  const bool tc = dtype == DR_BF16 && operand_ok(rows_of(a.x, a.M, a.K, a.x_s)) && operand_ok(weight_of(a)) && a.N % 8 == 0;
-  if (!tc) return launch_linear_bwd_simt(a, d, dtype, st);
-  if (a.dx) {   // dx[m,k] = sum over n of d[m,n] W[k,n]
-    const Operand W{a.w, a.K, a.N, a.w_s, a.w_t != 0};
-    e = launch_linear_pair(rows_of(d, a.M, a.N, a.N), W, Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K, 0, 0,
-                           a.K % 16 == 0 && on32(a.dx)}, false, sms, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.dw) {   // dw[k,n] = sum over m of x[m,k] d[m,n]
-    const Operand X{a.x, a.K, a.M, a.x_s, true}, D{d, a.N, a.M, a.N, true};
-    const int rows = a.w_t ? a.N : a.K, cols = a.w_t ? a.K : a.N;
-    e = launch_linear_pair(a.w_t ? D : X, a.w_t ? X : D, Epilogue{a.dw, nullptr, nullptr, nullptr, rows, cols, 0, 0,
-                           cols % 16 == 0 && on32(a.dw)}, false, sms, st);
+  if (a.dw && e == cudaSuccess) {   // dw[k,n] = sum over m of x[m,k] d[m,n], in W's order
+    const void* x = a.x;
+    e = p.x.make(x, ws + p.o_x, dtype, sms, st);
+    if (e == cudaSuccess)
+      e = product(a.w_t ? cols : p.x.k_rows(x), a.w_t ? p.x.k_rows(x) : cols,
+                  Epilogue{a.dw, nullptr, nullptr, nullptr, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N}, false, dtype, sms, st);
   }
   return e;
 }

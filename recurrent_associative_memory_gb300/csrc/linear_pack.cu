@@ -1,0 +1,164 @@
+// linear_pack.cu — operands of the tensor-core products that memory does not hold as they
+// need them, and the gradient at the product.
+//
+// An fp32 value becomes three bf16 ones, x = p0 + p1 + p2 with p0 = bf16(x), p1 = bf16(x - p0),
+// p2 = bf16(x - p0 - p1): 24 bits, so that six products of pieces keep an fp32 product's
+// precision at a sixth of the bf16 rate, five times what the CUDA cores do.  bf16 rows whose
+// stride no tensor map takes are copied to one that it does.
+// The gradient at the product, d = d_y * slope, is formed once for both backward products, in
+// the same layout, and the bias's gradient is summed from it in fp32 on the way.
+#include "linear_tc.cuh"
+
+namespace dr {
+namespace {
+
+constexpr int kRows = 64;    // of a block's tile, by 256 columns
+
+template <typename T, bool VEC> __device__ __forceinline__ void read8(const T* p, int n, float (&f)[8]) {
+  if constexpr (VEC) {
+    load8(p, n, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
+  }
+}
+template <bool VEC> __device__ __forceinline__ void read8(const __half* p, int n, float (&f)[8]) {
+  if constexpr (VEC) {
+    const uint4 u = n > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(h[i]);
+      f[2 * i] = v.x, f[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? __half2float(p[i]) : 0.f;
+  }
+}
+
+// The pieces of 8 values, to dst, dst + piece, ...
+template <typename T> __device__ __forceinline__ void write_pieces(__nv_bfloat16* dst, long long piece, float (&f)[8]) {
+#pragma unroll
+  for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = tc::pack_bf16(f[2 * i], f[2 * i + 1]);
+      f[2 * i] -= __uint_as_float(w[i] << 16);
+      f[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint4*>(dst + p * piece) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// rows x cols, columns contiguous -> pieces with rows of `pitch`
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) pack_kernel(const T* src, long long stride, int rows, int cols, __nv_bfloat16* dst,
+                                                   int pitch, long long piece) {
+  const long long per = pitch / 8, n = rows * per;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    long long r;
+    const int c = 8 * div_mod(i, static_cast<int>(per), r);
+    float f[8];
+    read8<T, VEC>(src + r * stride + c, cols - c, f);
+    write_pieces<T>(dst + r * pitch + c, piece, f);
+  }
+}
+
+// d = d_y * slope [M,N] in pieces with rows of `pitch` (dst null: not kept), and the columns'
+// sums of each block's rows, part [row blocks][N] (null: not wanted).  A warp takes 256 columns
+// of a row, 8 warps the rows in turns.
+template <typename T, typename S, bool VEC>
+__global__ void __launch_bounds__(256) slope_kernel(const T* d_y, const S* slope, __nv_bfloat16* dst, int pitch,
+                                                    long long piece, float* part, int M, int N) {
+  __shared__ float buf[8][256];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col_blocks = (N + 255) / 256;
+  const int c = blockIdx.x % col_blocks * 256 + lane * 8;
+  const long long rb = blockIdx.x / col_blocks;
+  float sum[8] = {};
+  if (c < N) {
+#pragma unroll 4
+    for (int i = warp; i < kRows; i += 8) {
+      const long long m = rb * kRows + i;
+      if (m >= M) break;
+      float f[8], s[8];
+      read8<T, VEC>(d_y + m * N + c, N - c, f);
+      if (slope) {
+        if constexpr (sizeof(S) == 2) read8<VEC>(slope + m * N + c, N - c, s);
+        else read8<S, VEC>(slope + m * N + c, N - c, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= s[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+      if (dst) write_pieces<T>(dst + m * pitch + c, piece, f);
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) buf[warp][j * 32 + lane] = sum[j];
+  __syncthreads();
+  const int j = threadIdx.x / 32, n = blockIdx.x % col_blocks * 256 + lane * 8 + j;
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += buf[w][j * 32 + lane];
+  if (n < N) part[rb * N + n] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) join_bias_kernel(const float* part, int blocks, int N, T* db) {
+  __shared__ float buf[8][32];
+  const int lane = threadIdx.x % 32, g = threadIdx.x / 32, n = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (n < N)
+    for (int b = g; b < blocks; b += 8) s += part[(long long)b * N + n];
+  buf[g][lane] = s;
+  __syncthreads();
+  if (g == 0 && n < N) {
+    for (int i = 1; i < 8; ++i) s += buf[i][lane];
+    db[n] = from_f<T>(s);
+  }
+}
+
+template <typename T>
+void pack(const void* src, long long stride, int rows, int cols, void* dst, int pitch, long long piece, int sms, cudaStream_t st) {
+  const long long n = (long long)rows * (pitch / 8), most = 16LL * sms;
+  const unsigned grid = static_cast<unsigned>(min(most, (n + 255) / 256));
+  const bool vec = cols % 8 == 0 && stride % (16 / (int)sizeof(T)) == 0;
+  auto* k = vec ? pack_kernel<T, true> : pack_kernel<T, false>;
+  k<<<grid, 256, 0, st>>>(static_cast<const T*>(src), stride, rows, cols, static_cast<__nv_bfloat16*>(dst), pitch, piece);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pack(const void* src, long long stride, int rows, int cols, int dtype, void* dst, int pitch,
+                               long long piece, int sms, cudaStream_t st) {
+  if (dtype == DR_FP32) pack<float>(src, stride, rows, cols, dst, pitch, piece, sms, st);
+  else pack<__nv_bfloat16>(src, stride, rows, cols, dst, pitch, piece, sms, st);
+  return cudaGetLastError();
+}
+
+int linear_slope_blocks(int M) { return static_cast<int>((M + (long long)kRows - 1) / kRows); }
+
+// d into dst (or not, null) and the bias's gradient over part (or not, null)
+cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int pitch, long long piece, float* part,
+                                cudaStream_t st) {
+  const int blocks = linear_slope_blocks(a.M);
+  const unsigned grid = static_cast<unsigned>(blocks * ((a.N + 255LL) / 256));
+  const bool vec = a.N % 8 == 0;
+  auto* d = static_cast<__nv_bfloat16*>(dst);
+  if (dtype == DR_FP32) {
+    auto* k = vec ? slope_kernel<float, float, true> : slope_kernel<float, float, false>;
+    k<<<grid, 256, 0, st>>>(static_cast<const float*>(a.d_y), static_cast<const float*>(a.slope), d, pitch, piece, part, a.M, a.N);
+    if (part) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
+  } else {
+    auto* k = vec ? slope_kernel<__nv_bfloat16, __half, true> : slope_kernel<__nv_bfloat16, __half, false>;
+    k<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(a.d_y), static_cast<const __half*>(a.slope), d, pitch, piece,
+                            part, a.M, a.N);
+    if (part) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace dr

@@ -6,9 +6,10 @@
 // (128 + BN / 2) x 128 bytes into each SM for 512 (BN = 256) cycles of products: 64 bytes a
 // cycle, where one CTA by itself would need 96.  Accumulators are two buffers of BN columns of
 // TMEM: while the epilogue reads one, the next tile's products go to the other.
-//   warps 0-3  epilogue: rows 32 w .. of the CTA's 128, a thread per row
-//   warp 4     TMA: this CTA's part of each stage, counted on the first CTA's barrier
-//   warp 5     the MMAs, in the first CTA of the pair
+//   warps 0-7  epilogue: rows 32 (w mod 4) .. of the CTA's 128, a thread per row, and half of
+//              the columns each
+//   warp 8     TMA: this CTA's part of each stage, counted on the first CTA's barrier
+//   warp 9     the MMAs, in the first CTA of the pair
 // The pairs stay: one per two SMs walks the tiles, eight tiles of rows at a time, so that
 // neighbours in time share columns of B and rows of A in L2.
 #include <type_traits>
@@ -20,15 +21,15 @@ namespace {
 
 using namespace lin;
 
-constexpr int kThreads = 192, kEpilogueWarps = 4, kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 320, kEpilogueWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kGroup = 8;   // tiles of rows that are walked together
 
 template <int BN> struct Smem {
   static constexpr int kA = 128 * kBK * 2, kB = BN / 2 * kBK * 2, kStage = kA + kB;
   static constexpr int kStages = BN == 256 ? 6 : 8;
-  static constexpr int oBias = kStages * kStage;                  // fp32, each epilogue warp's [BN]
-  static constexpr int oTurn = oBias + kEpilogueWarps * BN * 4;   // and [32][33]: rows to columns
-  static constexpr int kBytes = oTurn + kEpilogueWarps * 32 * 33 * 4 + 1024;
+  static constexpr int oBias = kStages * kStage;                  // fp32, each epilogue warp's [BN / 2]
+  static constexpr int oTurn = oBias + kEpilogueWarps * BN / 2 * 4;   // and [32][17]: rows to columns
+  static constexpr int kBytes = oTurn + kEpilogueWarps * 32 * 17 * 4 + 1024;
 };
 
 struct Tiles {
@@ -48,6 +49,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using L = Smem<BN>;
   using S = typename std::conditional<sizeof(T) == 2, __half, float>::type;
   constexpr int NS = L::kStages;
+  constexpr bool FP32 = sizeof(T) == 4;
+  const Stages<FP32> stages{n_k};
+  const int n_chunk = stages.chunks();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[2], b_free[2], b_end;
@@ -80,16 +84,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) { return all(wait_phase(bar, parity) || give_up()); };
 
   if (warp < kEpilogueWarps) {   // ------------------------------------------------ epilogue
-    float* turn = reinterpret_cast<float*>(sm + L::oTurn) + warp * 32 * 33;
-    int it = 0;
-    for (int t = first; t < n_tile; t += step, ++it) {
+    constexpr int NC = BN / 2;   // columns of this warp
+    const int part = warp / 4, row0 = warp % 4 * 32;
+    float* turn = reinterpret_cast<float*>(sm + L::oTurn) + warp * 32 * 17;
+    int it = 0;   // accumulators gone by
+    bool ok = true;
+    for (int t = first; t < n_tile && ok; t += step) {
       int tm, tn;
       tiles.at(t, tm, tn);
-      const int buf = it & 1, n0 = tn * BN;
-      const int m0 = tm * 256 + rank * 128 + warp * 32, m = m0 + lane;
-      float* bias = reinterpret_cast<float*>(sm + L::oBias) + warp * BN;   // a warp's own: no barrier to be left at
+      const int n0 = tn * BN + part * NC;
+      const int m0 = tm * 256 + rank * 128 + row0, m = m0 + lane;
+      float* bias = reinterpret_cast<float*>(sm + L::oBias) + warp * NC;   // a warp's own: no barrier to be left at
       if constexpr (FULL) {
-        for (int c = lane; c < BN; c += 32)
+        for (int c = lane; c < NC; c += 32)
           bias[c] = e.bias && n0 + c < e.N ? to_f(static_cast<const T*>(e.bias)[n0 + c]) : 0.f;
         __syncwarp();
       }
@@ -99,18 +106,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       S* slope = FULL && e.slope ? static_cast<S*>(e.slope) + (long long)m * e.N + n0 : nullptr;
       Raw16<T> r[2];
       auto ahead = [&](int c) {   // the residual of columns c .. c + 31
-        if (!FULL || !res || !e.vec) return;
+        if (!FULL || FP32 || !res || !e.vec) return;   // fp32: its sums have the registers
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (c + 16 * h < BN && n0 + c + 16 * h < e.N) r[h].load(res + c + 16 * h);
+          if (c + 16 * h < NC && n0 + c + 16 * h < e.N) r[h].load(res + c + 16 * h);
       };
       ahead(0);
-      if (!wait(&b_acc[buf], (it / 2) & 1)) break;
-      tc_fence_after();
-      for (int c = 0; c < BN && n0 + c < e.N; c += 32) {
-        float v[32];
-        tmem_ld32(tmem + buf * BN + c + (static_cast<uint32_t>(warp * 32) << 16), reinterpret_cast<uint32_t*>(v));
-        tmem_ld_wait();
+      auto emit = [&](int c, const float* v) {   // columns c .. c + 31
         if (e.vec) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -125,6 +127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
               act_all(e.act, slope != nullptr, x, s);
               if (res) {
+                if (FP32 && n0 + c + 16 * h < e.N) r[h].load(res + c + 16 * h);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] += r[h][i];
               }
@@ -137,28 +140,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ahead(c + 32);
         } else {   // rows on any address: a lane takes a column, and rows are stored one by one
 #pragma unroll
-          for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
-          __syncwarp();
-          const int n = n0 + c + lane;
-          if (n < e.N) {
-            const float b = FULL ? bias[c + lane] : 0.f;
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) turn[lane * 17 + i] = v[16 * h + i];
+            __syncwarp();
+            const int at = c + 16 * h + lane % 16, n = n0 + at;
+            if (n < e.N) {
+              const float b = FULL ? bias[at] : 0.f;
 #pragma unroll 4
-            for (int i = 0; i < 32 && m0 + i < e.M; ++i) {
-              float x = turn[i * 33 + lane] + b, s = 1.f;
-              if constexpr (FULL) {
-                x = act_any(e.act, x, s);
-                if (e.slope) static_cast<S*>(e.slope)[(m0 + i) * (long long)e.N + n] = static_cast<S>(s);
-                if (e.res) x += to_f(static_cast<const T*>(e.res)[(m0 + i) * e.r_m + n]);
+              for (int i = lane / 16; i < 32 && m0 + i < e.M; i += 2) {
+                float x = turn[i * 17 + lane % 16] + b, s = 1.f;
+                if constexpr (FULL) {
+                  x = act_any(e.act, x, s);
+                  if (e.slope) static_cast<S*>(e.slope)[(m0 + i) * (long long)e.N + n] = static_cast<S>(s);
+                  if (e.res) x += to_f(static_cast<const T*>(e.res)[(m0 + i) * e.r_m + n]);
+                }
+                static_cast<T*>(e.C)[(m0 + i) * (long long)e.N + n] = from_f<T>(x);
               }
-              static_cast<T*>(e.C)[(m0 + i) * (long long)e.N + n] = from_f<T>(x);
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
+      };
+      const uint32_t lanes = static_cast<uint32_t>(row0) << 16;
+      auto release = [&](int buf) {
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one()) arrive_remote(map_rank(smem_u32(&b_free[buf]), 0));
+      };
+      if constexpr (FP32) {
+        float acc[NC];
+        for (int i = 0; i < n_chunk && ok; ++i, ++it) {
+          const int buf = it & 1;
+          if (!(ok = wait(&b_acc[buf], (it / 2) & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NC; c += 32) {
+            float v[32];
+            tmem_ld32(tmem + buf * BN + part * NC + c + lanes, reinterpret_cast<uint32_t*>(v));
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) acc[c + x] = i ? acc[c + x] + v[x] : v[x];
+          }
+          release(buf);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < NC; c += 32)
+          if (n0 + c < e.N) emit(c, acc + c);
+      } else {
+        const int buf = it & 1;
+        if (!(ok = wait(&b_acc[buf], (it / 2) & 1))) break;
+        tc_fence_after();
+        for (int c = 0; c < NC && n0 + c < e.N; c += 32) {
+          float v[32];
+          tmem_ld32(tmem + buf * BN + part * NC + c + lanes, reinterpret_cast<uint32_t*>(v));
+          tmem_ld_wait();
+          emit(c, v);
+        }
+        release(buf);
+        ++it;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (elect_one()) arrive_remote(map_rank(smem_u32(&b_free[buf]), 0));
     }
   } else if (warp == kLoadWarp) {   // --------------------------------------------- loads
     uint32_t n = 0;
@@ -167,7 +209,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int tm, tn;
       tiles.at(t, tm, tn);
       const int m0 = tm * 256 + rank * 128, n0 = tn * BN + rank * (BN / 2);
-      for (int k = 0; k < n_k; ++k, ++n) {
+      for (int i = 0, chunk = 0; chunk < n_chunk; ++n) {
+        int k, pa, pb;
+        stages.at(chunk, i, k, pa, pb);
+        if (++i == stages.of(chunk)) i = 0, ++chunk;
         const uint32_t s = n % NS;
         if (n >= NS && !(ok = wait(&b_empty[s], (n / NS - 1) & 1))) break;
         if (elect_one()) {
@@ -177,15 +222,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_expect_tx(&b_full[s], 2 * L::kStage);
           if constexpr (A_MN) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) pair_load(a + i * 8192, &tmA, bar, m0 + 64 * i, k * kBK);
+            for (int h = 0; h < 2; ++h) pair_load(a + h * 8192, &tmA, bar, m0 + 64 * h, k * kBK, pa);
           } else {
-            pair_load(a, &tmA, bar, k * kBK, m0);
+            pair_load(a, &tmA, bar, k * kBK, m0, pa);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int i = 0; i < BN / 128; ++i) pair_load(b + i * 8192, &tmB, bar, n0 + 64 * i, k * kBK);
+            for (int h = 0; h < BN / 128; ++h) pair_load(b + h * 8192, &tmB, bar, n0 + 64 * h, k * kBK, pb);
           } else {
-            pair_load(b, &tmB, bar, k * kBK, n0);
+            pair_load(b, &tmB, bar, k * kBK, n0, pb);
           }
         }
         __syncwarp();
@@ -205,26 +250,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t n = 0;
     int it = 0;
     bool ok = true;
-    for (int t = first; t < n_tile && ok; t += step, ++it) {
-      const int buf = it & 1;
-      if (it >= 2 && !(ok = all(wait_cluster(&b_free[buf], (it / 2 - 1) & 1) || give_up()))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * BN;
-      for (int k = 0; k < n_k; ++k, ++n) {
-        const uint32_t s = n % NS;
-        if (!(ok = wait(&b_full[s], (n / NS) & 1))) break;
+    for (int t = first; t < n_tile && ok; t += step) {
+      for (int chunk = 0; chunk < n_chunk && ok; ++chunk, ++it) {
+        const int buf = it & 1, n_stage = stages.of(chunk);
+        if (it >= 2 && !(ok = all(wait_cluster(&b_free[buf], (it / 2 - 1) & 1) || give_up()))) break;
         tc_fence_after();
-        const uint32_t at = (s * L::kStage) >> 4;
-        if (elect_one()) {
+        const uint32_t d = tmem + buf * BN;
+        for (int i = 0; i < n_stage; ++i, ++n) {
+          const uint32_t s = n % NS;
+          if (!(ok = wait(&b_full[s], (n / NS) & 1))) break;
+          tc_fence_after();
+          const uint32_t at = (s * L::kStage) >> 4;
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            pair_mma(d, da + at + j * (A_MN ? 128 : 2), db + at + j * (B_MN ? 128 : 2), ID, k > 0 || j > 0);
-          pair_commit(&b_empty[s]);
+            for (int j = 0; j < kBK / 16; ++j)
+              pair_mma(d, da + at + j * (A_MN ? 128 : 2), db + at + j * (B_MN ? 128 : 2), ID, i > 0 || j > 0);
+            pair_commit(&b_empty[s]);
+          }
+          __syncwarp();
         }
+        if (ok && elect_one()) pair_commit(&b_acc[buf]);
         __syncwarp();
       }
-      if (ok && elect_one()) pair_commit(&b_acc[buf]);
-      __syncwarp();
     }
     if (elect_one()) pair_commit(&b_end, 1);   // no MMA may be under way when the pair ends
     __syncwarp();
@@ -262,6 +309,8 @@ cudaError_t by_order(const Operand& A, const Operand& B, const Epilogue& e, bool
 // `full`: a forward product, A K-major; otherwise C alone, and A MN-major only if B is too
 cudaError_t launch_linear_pair(const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full, int sms,
                                cudaStream_t st) {
+  // fp32 keeps a tile's sums in registers: 128 of them per thread
+  if (A.piece) return by_order<128, float>(A, B, e, full, sms, st);
   return by_order<256, __nv_bfloat16>(A, B, e, full, sms, st);
 }
 

@@ -21,12 +21,21 @@ using attn::wait_phase;
 constexpr int kBK = 64;     // k of a stage: 128 bytes, the swizzle's width
 
 // One operand: rows x k, bf16.  Rows (K-major) or steps of k (MN-major) are `stride` apart.
+// An fp32 operand comes as three of them, `piece` apart, whose sum it is: bf16(x), bf16 of
+// what that leaves, and again.
 struct Operand {
   const void* p;
   int rows, k;
   long long stride;
   bool mn;
+  long long piece = 0;   // 0: bf16
 };
+
+// The products of pieces that an fp32 product takes, the smallest first (piece 1 is about 2^-8
+// of piece 0, piece 2 2^-16; what is left out is below 2^-25 of a term).
+constexpr int kPairs = 6;
+__host__ __device__ constexpr int piece_a(int i) { return (0x021010 >> (4 * (kPairs - 1 - i))) & 15; }
+__host__ __device__ constexpr int piece_b(int i) { return (0x201100 >> (4 * (kPairs - 1 - i))) & 15; }
 
 struct Epilogue {
   void* C;
@@ -42,11 +51,12 @@ inline bool make_operand_map(CUtensorMap* m, const Operand& o, int box_rows) {
   tc::EncodeTiledFn enc = tc::get_encode();
   if (!enc) return false;
   const cuuint64_t inner = o.mn ? o.rows : o.k, outer = o.mn ? o.k : o.rows;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(outer > 1 ? 2 * o.stride : (2 * inner + 15) / 16 * 16)};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(o.mn ? kBK : box_rows)};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(o.p), dims, strides, box, es,
+  cuuint64_t dims[3] = {inner, outer, o.piece ? 3u : 1u};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(outer > 1 ? 2 * o.stride : (2 * inner + 15) / 16 * 16),
+                           static_cast<cuuint64_t>(o.piece ? 2 * o.piece : 16)};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(o.mn ? kBK : box_rows), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -99,18 +109,18 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
 }
 
 // A box into this CTA's shared memory, its bytes counted on a barrier of either CTA.
-__device__ __forceinline__ void pair_load(void* dst, const void* tmap, uint32_t bar, int c0, int c1) {
+__device__ __forceinline__ void pair_load(void* dst, const void* tmap, uint32_t bar, int c0, int c1, int c2) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-__device__ __forceinline__ void load_2d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1) {
+__device__ __forceinline__ void load_box(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
           smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t ncols) {
@@ -137,6 +147,29 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t ranks = 3) {
       "h"(ranks)
       : "memory");
 }
+
+// ---------------------------------------------------------------- stages
+
+// Walks the stages of one tile's sum: stage -> (pieces, k).  bf16 has one product of n_k
+// stages.  fp32 takes them in chunks of kChunk k-steps, each of them all six products: a
+// chunk's sum leaves TMEM and is added up in registers, as the tensor cores cut every addition
+// to the accumulator's 24 bits, which over thousands of k comes to 1e-5.
+constexpr int kChunk = 2;
+template <bool FP32> struct Stages {
+  int n_k;
+  __device__ __forceinline__ int chunks() const { return FP32 ? (n_k + kChunk - 1) / kChunk : 1; }
+  __device__ __forceinline__ int k_of(int chunk) const { return FP32 ? min(kChunk, n_k - chunk * kChunk) : n_k; }
+  __device__ __forceinline__ int of(int chunk) const { return FP32 ? kPairs * k_of(chunk) : n_k; }
+  __device__ __forceinline__ void at(int chunk, int i, int& k, int& pa, int& pb) const {
+    if constexpr (FP32) {
+      const int per = k_of(chunk), p = per == kChunk ? i / kChunk : i;
+      k = chunk * kChunk + i - p * per;
+      pa = piece_a(p), pb = piece_b(p);
+    } else {
+      k = i, pa = pb = 0;
+    }
+  }
+};
 
 // ---------------------------------------------------------------- epilogue
 

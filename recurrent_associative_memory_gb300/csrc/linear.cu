@@ -8,8 +8,8 @@ cudaError_t launch_linear_pack(const void* src, long long stride, int rows, int 
 int linear_slope_blocks(int M);
 cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int pitch, long long piece, float* part,
                                 cudaStream_t st);
-cudaError_t launch_linear_pair(const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full, int sms,
-                               cudaStream_t st);
+cudaError_t launch_linear_pair(int bn, const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full,
+                               int sms, cudaStream_t st);
 cudaError_t launch_linear_few_bf16(int tn, const lin::Operand& M, const lin::Operand& N, const lin::Epilogue& e, bool full,
                                    int split, cudaStream_t st);
 cudaError_t launch_linear_few_fp32(int tn, const lin::Operand& M, const lin::Operand& N, const lin::Epilogue& e, bool full,
@@ -52,29 +52,47 @@ struct Packed {
 Packed pack_x(const LinearArgs& a, int dtype) { return {dtype, a.M, a.K, a.x_s}; }
 Packed pack_w(const LinearArgs& a, int dtype) { return {dtype, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, a.w_s}; }
 
+// Cycles of one 64-k step of a tile of m x n in an SM: its products, or the bytes that it
+// brings in at 64 a cycle.  fp32 takes six products of three pieces.
+long long step_cycles(bool fp32, int m, int n, int rows_here, int cols_here) {
+  const long long mma = (long long)m * n / 64, load = (rows_here + cols_here) * 2LL;
+  return fp32 ? (6 * mma > 3 * load ? 6 * mma : 3 * load) : mma > load ? mma : load;
+}
+
 // C[m,n] = sum over k of A[m,k] B[n,k], and its epilogue where `full`.
-// Which kernel: the time that each one's SMs need for its stages, by the bytes that a stage
-// brings into an SM (64 a cycle), and what a launch costs besides.
+// Which kernel: the one whose busiest SM needs the fewest cycles for its tiles, or for the
+// operands out of memory (3500 bytes a cycle), and for what a kernel costs besides: start,
+// first loads and the last epilogue.  Clusters of several CTAs leave SMs unused (a GPC's number
+// of SMs is no multiple of theirs; eight of 200 KB hardly find their place), and a second wave
+// of the small kernel waits for the first.  Both sides, bf16, us with 4 us of events: M512
+// K4096 N4096 pairs of 256 x 128 23.5, of 256 x 256 30.7, small 26.6; M128 22.5, 30, and small,
+// 128 rows cut in four, 16.4; M64 N16384 36.8, 34.1, small, 64 rows, 28.7, cut in two 34.8.
 cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, int dtype, int sms, cudaStream_t st) {
   const bool fp32 = dtype == DR_FP32;
   const int es = fp32 ? 4 : 2;
-  const long long n_k = ceil_div(A.k, lin::kBK), times = fp32 ? lin::kPairs : 1;
-  const int bn = fp32 ? 128 : 256;
-  const long long pair_tiles = ceil_div(A.rows, 256) * ceil_div(B.rows, bn);
-  long long best = ceil_div(pair_tiles, sms / 2) * (n_k * times * (256 + bn)) + 6000;
-  int tn = 0, split = 1;
+  const long long n_k = ceil_div(A.k, lin::kBK);
+  const long long memory = ((long long)A.rows + B.rows) * A.k * (fp32 ? 6 : 2) / 3500;
+  long long best = 0;
+  int bn = 0, tn = 0, split = 1;
+  auto offer = [&](long long work, long long fixed, int bn_, int tn_, int split_) {
+    const long long cost = (work > memory ? work : memory) + fixed;
+    if (!best || cost < best) best = cost, bn = bn_, tn = tn_, split = split_;
+  };
+  for (int b = fp32 ? 128 : 256; b >= 128; b /= 2)
+    offer(ceil_div(ceil_div(A.rows, 256) * ceil_div(B.rows, b), sms / 2) * n_k * step_cycles(fp32, 128, b, 128, b / 2),
+          b == 256 ? 17000 : 11500, b, 0, 1);
   const long long n_tiles = ceil_div(B.rows, 128);
-  for (int t = A.mn ? 64 : 16; t <= (fp32 ? 64 : 128); t *= 2) {
+  for (int t = A.mn ? 64 : 16; t <= 128; t *= 2) {
     const long long tiles = n_tiles * ceil_div(A.rows, t);
-    if (tiles > 8LL * sms) continue;
-    for (int s = 1; s <= 8 && s <= n_k; ++s) {
-      const long long cost = ceil_div(tiles * s, sms) * (ceil_div(n_k, s) * times * (128 + t) * 2) + (s > 1 ? 4500 : 3500);
-      if (cost < best) best = cost, tn = t, split = s;
+    if (tiles > 4LL * sms) continue;
+    for (int s = 1; s <= 6 && s <= n_k; ++s) {
+      const long long waves = ceil_div(tiles * s, s > 1 ? sms * 21 / 25 : sms);
+      offer(waves * ceil_div(n_k, s) * step_cycles(fp32, 128, t, 128, t), 10500 + 12 * t + (waves - 1) * 14000, 0, t, s);
     }
   }
   if (tn) return (fp32 ? launch_linear_few_fp32 : launch_linear_few_bf16)(tn, A, B, e, full, split, st);
   e.vec = e.N * es % 32 == 0 && on32(e.C, e.res) && on32(e.slope) && (!e.res || e.r_m * es % 32 == 0);
-  return launch_linear_pair(A, B, e, full, sms, st);
+  return launch_linear_pair(bn, A, B, e, full, sms, st);
 }
 
 struct BwdPlan {

@@ -6,11 +6,10 @@
 // read once.  The sum over k is cut over the S CTAs of a cluster, each of which leaves its
 // part of C in its shared memory; they add them up in the ranks' order, each for its share of
 // the rows, so the result does not depend on which CTA is first.
-//   warps 0-3  the accumulator to shared memory, then the sums and the epilogue
-//   warp 4     TMA, 3 to 6 stages of 64 k
-//   warp 5     the MMAs
-// About 100 KB of shared memory: two CTAs per SM, so that one's loads cover the other's start
-// and end.  Weights are what bounds it: every stage is 16 KB of them.
+//   warps 0-7  the accumulator to shared memory, then the sums and the epilogue, a row per warp
+//   warp 8     TMA, 6 to 11 stages of 64 k
+//   warp 9     the MMAs
+// Weights are what bounds it, 16 KB of each stage, so an SM keeps 200 KB of them under way.
 #pragma once
 
 #include <type_traits>
@@ -20,28 +19,66 @@
 namespace dr {
 namespace lin {
 
-constexpr int kFewThreads = 192, kFewLoadWarp = 4, kFewMmaWarp = 5;
+constexpr int kFewThreads = 320, kFewWarps = 8, kFewLoadWarp = 8, kFewMmaWarp = 9;
 
 template <int TN> struct FewSmem {
   static constexpr int kN = 128 * kBK * 2, kM = TN * kBK * 2, kStage = kN + kM;
-  static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : 3;
+  static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : TN == 64 ? 8 : 6;
   static constexpr int kBytes = kStages * kStage + 1024;
   static_assert(TN * 128 * 4 <= kStages * kStage, "the parts of C take the stages' place");
 };
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 
 struct FewGrid {
   int tiles_m, split;   // tiles of rows; CTAs over k
 };
 
-__device__ __forceinline__ float2 load_peer2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 load_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
+}
+
+// 4 neighbouring values; `whole`: at once, else those below n
+template <typename T> __device__ __forceinline__ void get4(const T* p, bool whole, int n, float (&v)[4]) {
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  }
+}
+template <typename T> __device__ __forceinline__ void put4(T* p, bool whole, int n, const float (&v)[4]) {
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = static_cast<T>(v[i]);
+  } else if constexpr (std::is_same<T, __half>::value) {
+    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
 }
 
 // N_MN, M_MN: the operands of C's columns and rows are MN-major
 template <int TN, bool N_MN, bool M_MN, typename T, bool FULL>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmN, const __grid_constant__ CUtensorMap tmM, Epilogue e,
                       FewGrid g, int n_k) {
   static_assert(!M_MN || TN >= 64, "a swizzled row of an MN-major operand is 64 of its rows");
@@ -57,12 +94,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const int rank = blockIdx.x % g.split, tile = blockIdx.x / g.split;
   const int m0 = tile % g.tiles_m * TN, n0 = tile / g.tiles_m * 128;
   const int k0 = static_cast<int>((long long)n_k * rank / g.split);
-  const Stages<FP32> stages{static_cast<int>((long long)n_k * (rank + 1) / g.split) - k0};
-  const int n_chunk = stages.chunks();
+  const Walk<FP32> walk{static_cast<int>((long long)n_k * (rank + 1) / g.split) - k0};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&b_acc[i], 1), mbar_init(&b_free[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&b_acc[i], 1), mbar_init(&b_free[i], kFewWarps);
     mbar_init(&b_end, 1);
     fence_mbar_init();
   }
@@ -78,33 +114,28 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   };
   float* part = reinterpret_cast<float*>(sm);   // [TN][128]
 
-  if (warp < 4) {   // ------------------------------------------------------ accumulators
-    const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    constexpr int C = TN < 32 ? TN : 32;
-    float acc[FP32 ? TN : C];
+  if (warp < kFewWarps) {   // ---------------------------------------------- accumulators
+    constexpr int H = TN / 2, C = H < 32 ? H : 32;   // columns of a warp, and at once
+    const int c0 = warp / 4 * H, row = warp % 4 * 32 + lane;
+    const uint32_t at = tmem + c0 + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+    float acc[FP32 ? H : C];
     bool ok = true;
     auto load = [&](uint32_t from, float* v) {
-      if constexpr (C == 32) {
-        tmem_ld32(from, reinterpret_cast<uint32_t*>(v));
-      } else {
-        float w[16];
-        tmem_ld16(from, w);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = w[i];
-      }
+      if constexpr (C == 32) tmem_ld32(from, reinterpret_cast<uint32_t*>(v));
+      else if constexpr (C == 16) tmem_ld16(from, reinterpret_cast<float(&)[16]>(*v));
+      else tmem_ld8(from, reinterpret_cast<uint32_t*>(v));
       tmem_ld_wait();
     };
     auto keep = [&](int c, const float* v) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) part[(c + i) * 128 + warp * 32 + lane] = v[i];
+      for (int i = 0; i < C; ++i) part[(c0 + c + i) * 128 + row] = v[i];
     };
-    for (int i = 0; i < n_chunk && ok; ++i) {
+    for (int i = 0; i < walk.sums() && ok; ++i) {
       if (!(ok = wait(&b_acc[i & 1], (i / 2) & 1))) break;
       tc_fence_after();
       if constexpr (FP32) {
 #pragma unroll
-        for (int c = 0; c < TN; c += C) {
+        for (int c = 0; c < H; c += C) {
           float v[C];
           load(at + (i & 1) * kCols + c, v);
 #pragma unroll
@@ -114,7 +145,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         __syncwarp();
         if (elect_one()) mbar_arrive(&b_free[i & 1]);
       } else {
-        for (int c = 0; c < TN; c += C) {
+        for (int c = 0; c < H; c += C) {
           load(at + c, acc);
           keep(c, acc);
         }
@@ -122,37 +153,36 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
     }
     if constexpr (FP32) {
-      // the last chunk's products are done, so nothing reads or fills a stage any more
+      // the last products are done, so nothing reads or fills a stage any more
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < TN; c += C) keep(c, acc + c);
+        for (int c = 0; c < H; c += C) keep(c, acc + c);
       }
     }
   } else if (warp == kFewLoadWarp) {   // ---------------------------------------------- loads
     uint32_t n = 0;
     bool ok = true;
-    for (int i = 0, chunk = 0; chunk < n_chunk; ++n) {
-      int k, pm, pn;
-      stages.at(chunk, i, k, pm, pn);
-      if (++i == stages.of(chunk)) i = 0, ++chunk;
+    for (int i = 0; i < walk.stages(); ++i, ++n) {
+      int k, piece;
+      walk.at(i, k, piece);
       const uint32_t s = n % NS;
       if (n >= NS && !(ok = wait(&b_empty[s], (n / NS - 1) & 1))) break;
       if (elect_one()) {
-        uint8_t* pn_ = sm + s * L::kStage;
-        uint8_t* pm_ = pn_ + L::kN;
+        uint8_t* pn = sm + s * L::kStage;
+        uint8_t* pm = pn + L::kN;
         const int kc = (k0 + k) * kBK;
         mbar_expect_tx(&b_full[s], L::kStage);
         if constexpr (N_MN) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) load_box(pn_ + h * 8192, &tmN, &b_full[s], n0 + 64 * h, kc, pn);
+          for (int h = 0; h < 2; ++h) load_box(pn + h * 8192, &tmN, &b_full[s], n0 + 64 * h, kc, piece);
         } else {
-          load_box(pn_, &tmN, &b_full[s], kc, n0, pn);
+          load_box(pn, &tmN, &b_full[s], kc, n0, piece);
         }
         if constexpr (M_MN) {
 #pragma unroll
-          for (int h = 0; h < TN / 64; ++h) load_box(pm_ + h * 8192, &tmM, &b_full[s], m0 + 64 * h, kc, pm);
+          for (int h = 0; h < TN / 64; ++h) load_box(pm + h * 8192, &tmM, &b_full[s], m0 + 64 * h, kc, piece);
         } else {
-          load_box(pm_, &tmM, &b_full[s], kc, m0, pm);
+          load_box(pm, &tmM, &b_full[s], kc, m0, piece);
         }
       }
       __syncwarp();
@@ -165,24 +195,30 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const uint64_t da = desc_sw128(a0, N_MN ? 8192 : 0, 1024), db = desc_sw128(b0, M_MN ? 8192 : 0, 1024);
     uint32_t n = 0;
     bool ok = true;
-    for (int chunk = 0; chunk < n_chunk && ok; ++chunk) {
-      const int buf = chunk & 1, n_stage = stages.of(chunk);
-      if (FP32 && chunk >= 2 && !(ok = wait(&b_free[buf], (chunk / 2 - 1) & 1))) break;
+    for (int i = 0; i < walk.sums() && ok; ++i) {
+      const int buf = i & 1;
+      if (FP32 && i >= 2 && !(ok = wait(&b_free[buf], (i / 2 - 1) & 1))) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * kCols;
-      for (int i = 0; i < n_stage; ++i, ++n) {
-        const uint32_t s = n % NS;
-        if (!(ok = wait(&b_full[s], (n / NS) & 1))) break;
+      auto full = [&](uint32_t s, uint32_t parity) {
+        const bool there = wait(&b_full[s], parity);
         tc_fence_after();
-        const uint32_t at = (s * L::kStage) >> 4;
+        return there;
+      };
+      auto mma = [&](uint32_t sa, uint32_t sb, bool first) {
+        const uint64_t a = da + ((sa * L::kStage) >> 4), b = db + ((sb * L::kStage) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
-            mma_bf16(d, da + at + j * (N_MN ? 128 : 2), db + at + j * (M_MN ? 128 : 2), ID, i > 0 || j > 0);
-          mma_commit(&b_empty[s]);
+            mma_bf16(d, a + j * (N_MN ? 128 : 2), b + j * (M_MN ? 128 : 2), ID, !first || j > 0);
         }
         __syncwarp();
-      }
+      };
+      auto free = [&](uint32_t s) {
+        if (elect_one()) mma_commit(&b_empty[s]);
+        __syncwarp();
+      };
+      ok = products<FP32, NS>(walk.n_k, n, full, mma, free);
       if (ok && elect_one()) mma_commit(&b_acc[buf]);
       __syncwarp();
     }
@@ -195,53 +231,46 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   cluster_sync();   // every part is there
   tc_fence_after();
   if (warp == kFewMmaWarp) tmem_dealloc(tmem, (FP32 ? 2 : 1) * kCols);
-  if (warp < 4) {   // ------------------------------------------------- sums and epilogue
-    const int nl = threadIdx.x % 64 * 2, n = n0 + nl;
-    const bool two = e.vec && n + 1 < e.N;
-    float bias[2] = {0.f, 0.f};
-    if constexpr (FULL) {
-      if (e.bias) {
-        if (n < e.N) bias[0] = to_f(static_cast<const T*>(e.bias)[n]);
-        if (n + 1 < e.N) bias[1] = to_f(static_cast<const T*>(e.bias)[n + 1]);
+  const int n = n0 + lane * 4, left = e.N - n;
+  if (warp < kFewWarps && left > 0) {   // ----------------------------- sums and epilogue
+    const bool whole = e.vec && left >= 4;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (FULL && e.bias) get4(static_cast<const T*>(e.bias) + n, false, left, bias);
+    const uint32_t mine = smem_u32(part) + lane * 16;
+    constexpr int B = TN / kFewWarps < 4 ? TN / kFewWarps : 4;   // rows at once: their loads are under way together
+    const int rows = min(TN, e.M - m0);
+    for (int p = rank * kFewWarps + warp; p < rows; p += B * g.split * kFewWarps) {
+      float x[B][4], r[B][4];
+      int ml[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        ml[b] = min(p + b * g.split * kFewWarps, rows - 1);   // behind the last row: that one again, not stored
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[b][i] = bias[i];
+        if (FULL && e.res) get4(static_cast<const T*>(e.res) + (m0 + ml[b]) * e.r_m + n, whole, left, r[b]);
       }
-    }
-    const uint32_t mine = smem_u32(part) + nl * 4;
-#pragma unroll 2
-    for (int p = rank; p < TN / 2; p += g.split) {   // pairs of rows, in turns over the CTAs
-      const int ml = 2 * p + threadIdx.x / 64, m = m0 + ml;
-      if (m >= e.M || n >= e.N) continue;
-      float2 v = make_float2(0.f, 0.f);
-      for (int r = 0; r < g.split; ++r) {
-        const float2 u = load_peer2(map_rank(mine + ml * 512, r));
-        v.x += u.x, v.y += u.y;
+      for (int c = 0; c < g.split; ++c) {
+        const uint32_t from = map_rank(mine, c);
+        float4 u[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) u[b] = load_peer(from + ml[b] * 512);
+#pragma unroll
+        for (int b = 0; b < B; ++b) x[b][0] += u[b].x, x[b][1] += u[b].y, x[b][2] += u[b].z, x[b][3] += u[b].w;
       }
-      float x[2] = {v.x + bias[0], v.y + bias[1]}, s[2];
-      const long long at = m * (long long)e.N + n;
-      T* C = static_cast<T*>(e.C) + at;
-      if constexpr (FULL) {
-        act_all(e.act, e.slope != nullptr, x, s);
-        if (e.slope) {
-          S* q = static_cast<S*>(e.slope) + at;
-          if (two) {
-            if constexpr (FP32) *reinterpret_cast<float2*>(q) = make_float2(s[0], s[1]);
-            else *reinterpret_cast<__half2*>(q) = __floats2half2_rn(s[0], s[1]);
-          } else {
-            q[0] = static_cast<S>(s[0]);
-            if (n + 1 < e.N) q[1] = static_cast<S>(s[1]);
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (p + b * g.split * kFewWarps >= rows) break;
+        const long long at = (m0 + ml[b]) * (long long)e.N + n;
+        if constexpr (FULL) {
+          float s[4];
+          act_all(e.act, e.slope != nullptr, x[b], s);
+          if (e.slope) put4(static_cast<S*>(e.slope) + at, whole, left, s);
+          if (e.res) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[b][i] += r[b][i];
           }
         }
-        if (e.res) {
-          const T* q = static_cast<const T*>(e.res) + m * e.r_m + n;
-          x[0] += to_f(q[0]);
-          if (n + 1 < e.N) x[1] += to_f(q[1]);
-        }
-      }
-      if (two) {
-        if constexpr (FP32) *reinterpret_cast<float2*>(C) = make_float2(x[0], x[1]);
-        else *reinterpret_cast<uint32_t*>(C) = tc::pack_bf16(x[0], x[1]);
-      } else {
-        C[0] = from_f<T>(x[0]);
-        if (n + 1 < e.N) C[1] = from_f<T>(x[1]);
+        put4(static_cast<T*>(e.C) + at, whole, left, x[b]);
       }
     }
   }
@@ -257,7 +286,7 @@ cudaError_t few(const Operand& M, const Operand& N, Epilogue e, int split, cudaS
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<TN>::kBytes);
   if (err != cudaSuccess) return err;
   const FewGrid g{(M.rows + TN - 1) / TN, split};
-  e.vec = e.N % 2 == 0;   // pairs of columns at once
+  e.vec = e.N % 4 == 0 && (!e.res || e.r_m % 4 == 0);   // four columns at once
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = split, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -285,10 +314,8 @@ cudaError_t few_by_tile(int tn, const Operand& M, const Operand& N, const Epilog
     case 16: return few_by_order<16, T>(M, N, e, full, split, st);
     case 32: return few_by_order<32, T>(M, N, e, full, split, st);
     case 64: return few_by_order<64, T>(M, N, e, full, split, st);
-    default: break;
+    default: return few_by_order<128, T>(M, N, e, full, split, st);
   }
-  if constexpr (sizeof(T) == 2) return few_by_order<128, T>(M, N, e, full, split, st);
-  return cudaErrorInvalidValue;   // 128 sums per thread do not fit an fp32 kernel's registers
 }
 
 }  // namespace lin

@@ -50,8 +50,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using S = typename std::conditional<sizeof(T) == 2, __half, float>::type;
   constexpr int NS = L::kStages;
   constexpr bool FP32 = sizeof(T) == 4;
-  const Stages<FP32> stages{n_k};
-  const int n_chunk = stages.chunks();
+  const Walk<FP32> walk{n_k};
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[2], b_free[2], b_end;
@@ -170,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       if constexpr (FP32) {
         float acc[NC];
-        for (int i = 0; i < n_chunk && ok; ++i, ++it) {
+        for (int i = 0; i < n_k && ok; ++i, ++it) {
           const int buf = it & 1;
           if (!(ok = wait(&b_acc[buf], (it / 2) & 1))) break;
           tc_fence_after();
@@ -209,10 +208,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int tm, tn;
       tiles.at(t, tm, tn);
       const int m0 = tm * 256 + rank * 128, n0 = tn * BN + rank * (BN / 2);
-      for (int i = 0, chunk = 0; chunk < n_chunk; ++n) {
-        int k, pa, pb;
-        stages.at(chunk, i, k, pa, pb);
-        if (++i == stages.of(chunk)) i = 0, ++chunk;
+      for (int i = 0; i < walk.stages(); ++i, ++n) {
+        int k, piece;
+        walk.at(i, k, piece);
         const uint32_t s = n % NS;
         if (n >= NS && !(ok = wait(&b_empty[s], (n / NS - 1) & 1))) break;
         if (elect_one()) {
@@ -222,15 +220,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_expect_tx(&b_full[s], 2 * L::kStage);
           if constexpr (A_MN) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) pair_load(a + h * 8192, &tmA, bar, m0 + 64 * h, k * kBK, pa);
+            for (int h = 0; h < 2; ++h) pair_load(a + h * 8192, &tmA, bar, m0 + 64 * h, k * kBK, piece);
           } else {
-            pair_load(a, &tmA, bar, k * kBK, m0, pa);
+            pair_load(a, &tmA, bar, k * kBK, m0, piece);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int h = 0; h < BN / 128; ++h) pair_load(b + h * 8192, &tmB, bar, n0 + 64 * h, k * kBK, pb);
+            for (int h = 0; h < BN / 128; ++h) pair_load(b + h * 8192, &tmB, bar, n0 + 64 * h, k * kBK, piece);
           } else {
-            pair_load(b, &tmB, bar, k * kBK, n0, pb);
+            pair_load(b, &tmB, bar, k * kBK, n0, piece);
           }
         }
         __syncwarp();
@@ -251,24 +249,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0;
     bool ok = true;
     for (int t = first; t < n_tile && ok; t += step) {
-      for (int chunk = 0; chunk < n_chunk && ok; ++chunk, ++it) {
-        const int buf = it & 1, n_stage = stages.of(chunk);
+      for (int i = 0; i < walk.sums() && ok; ++i, ++it) {
+        const int buf = it & 1;
         if (it >= 2 && !(ok = all(wait_cluster(&b_free[buf], (it / 2 - 1) & 1) || give_up()))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
-        for (int i = 0; i < n_stage; ++i, ++n) {
-          const uint32_t s = n % NS;
-          if (!(ok = wait(&b_full[s], (n / NS) & 1))) break;
+        auto full = [&](uint32_t s, uint32_t parity) {
+          const bool there = wait(&b_full[s], parity);
           tc_fence_after();
-          const uint32_t at = (s * L::kStage) >> 4;
+          return there;
+        };
+        auto mma = [&](uint32_t sa, uint32_t sb, bool first) {
+          const uint64_t a = da + ((sa * L::kStage) >> 4), b = db + ((sb * L::kStage) >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < kBK / 16; ++j)
-              pair_mma(d, da + at + j * (A_MN ? 128 : 2), db + at + j * (B_MN ? 128 : 2), ID, i > 0 || j > 0);
-            pair_commit(&b_empty[s]);
+              pair_mma(d, a + j * (A_MN ? 128 : 2), b + j * (B_MN ? 128 : 2), ID, !first || j > 0);
           }
           __syncwarp();
-        }
+        };
+        auto free = [&](uint32_t s) {
+          if (elect_one()) pair_commit(&b_empty[s]);
+          __syncwarp();
+        };
+        ok = products<FP32, NS>(n_k, n, full, mma, free);
         if (ok && elect_one()) pair_commit(&b_acc[buf]);
         __syncwarp();
       }
@@ -297,7 +301,7 @@ cudaError_t go(const Operand& A, const Operand& B, const Epilogue& e, int sms, c
   return cudaGetLastError();
 }
 
-template <int BN, typename T>
+template <typename T, int BN>
 cudaError_t by_order(const Operand& A, const Operand& B, const Epilogue& e, bool full, int sms, cudaStream_t st) {
   if (full) return B.mn ? go<BN, false, true, T, true>(A, B, e, sms, st) : go<BN, false, false, T, true>(A, B, e, sms, st);
   if (A.mn) return go<BN, true, true, T, false>(A, B, e, sms, st);
@@ -306,12 +310,13 @@ cudaError_t by_order(const Operand& A, const Operand& B, const Epilogue& e, bool
 
 }  // namespace
 
-// `full`: a forward product, A K-major; otherwise C alone, and A MN-major only if B is too
-cudaError_t launch_linear_pair(const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full, int sms,
-                               cudaStream_t st) {
-  // fp32 keeps a tile's sums in registers: 128 of them per thread
-  if (A.piece) return by_order<128, float>(A, B, e, full, sms, st);
-  return by_order<256, __nv_bfloat16>(A, B, e, full, sms, st);
+// `full`: a forward product, A K-major; otherwise C alone, and A MN-major only if B is too.
+// bn: columns of a tile, 128 or 256 (fp32: 128, as a tile's sums stay in registers)
+cudaError_t launch_linear_pair(int bn, const lin::Operand& A, const lin::Operand& B, const lin::Epilogue& e, bool full,
+                               int sms, cudaStream_t st) {
+  if (A.piece) return by_order<float, 128>(A, B, e, full, sms, st);
+  return bn == 128 ? by_order<__nv_bfloat16, 128>(A, B, e, full, sms, st)
+                   : by_order<__nv_bfloat16, 256>(A, B, e, full, sms, st);
 }
 
 }  // namespace dr

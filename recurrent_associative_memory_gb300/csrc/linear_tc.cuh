@@ -31,12 +31,6 @@ struct Operand {
   long long piece = 0;   // 0: bf16
 };
 
-// The products of pieces that an fp32 product takes, the smallest first (piece 1 is about 2^-8
-// of piece 0, piece 2 2^-16; what is left out is below 2^-25 of a term).
-constexpr int kPairs = 6;
-__host__ __device__ constexpr int piece_a(int i) { return (0x021010 >> (4 * (kPairs - 1 - i))) & 15; }
-__host__ __device__ constexpr int piece_b(int i) { return (0x201100 >> (4 * (kPairs - 1 - i))) & 15; }
-
 struct Epilogue {
   void* C;
   const void* bias;
@@ -150,26 +144,50 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t ranks = 3) {
 
 // ---------------------------------------------------------------- stages
 
-// Walks the stages of one tile's sum: stage -> (pieces, k).  bf16 has one product of n_k
-// stages.  fp32 takes them in chunks of kChunk k-steps, each of them all six products: a
-// chunk's sum leaves TMEM and is added up in registers, as the tensor cores cut every addition
-// to the accumulator's 24 bits, which over thousands of k comes to 1e-5.
-constexpr int kChunk = 2;
-template <bool FP32> struct Stages {
+// A stage holds 64 k of both operands.  bf16: the n_k stages of a tile in turns, one
+// accumulator.  fp32: three stages per 64 k, the pieces 2, 1 and 0 of both operands, and six
+// products of them, the smallest first (piece 1 is about 2^-8 of piece 0, piece 2 2^-16; what
+// is left out is below 2^-25 of a term).  Their sum leaves TMEM after every 64 k and is added
+// up in registers: the tensor cores cut each addition to the accumulator's 24 bits, which
+// over thousands of k comes to 1e-5.
+template <bool FP32> struct Walk {
   int n_k;
-  __device__ __forceinline__ int chunks() const { return FP32 ? (n_k + kChunk - 1) / kChunk : 1; }
-  __device__ __forceinline__ int k_of(int chunk) const { return FP32 ? min(kChunk, n_k - chunk * kChunk) : n_k; }
-  __device__ __forceinline__ int of(int chunk) const { return FP32 ? kPairs * k_of(chunk) : n_k; }
-  __device__ __forceinline__ void at(int chunk, int i, int& k, int& pa, int& pb) const {
-    if constexpr (FP32) {
-      const int per = k_of(chunk), p = per == kChunk ? i / kChunk : i;
-      k = chunk * kChunk + i - p * per;
-      pa = piece_a(p), pb = piece_b(p);
-    } else {
-      k = i, pa = pb = 0;
-    }
+  __device__ __forceinline__ int sums() const { return FP32 ? n_k : 1; }      // accumulators per tile
+  __device__ __forceinline__ int stages() const { return FP32 ? 3 * n_k : n_k; }
+  __device__ __forceinline__ void at(int i, int& k, int& piece) const {
+    if constexpr (FP32) k = i / 3, piece = 2 - (i - 3 * k);
+    else k = i, piece = 0;
   }
 };
+
+// The products of one accumulator: full(stage) waits for a stage, mma(stage of A, stage of B,
+// first of all) issues one product, free(stage) gives a stage back.  n counts stages.
+template <bool FP32, int NS, typename Full, typename Mma, typename Free>
+__device__ __forceinline__ bool products(int n_k, uint32_t& n, Full&& full, Mma&& mma, Free&& free) {
+  if constexpr (FP32) {
+    const uint32_t s2 = n % NS, s1 = (n + 1) % NS, s0 = (n + 2) % NS;
+    for (int i = 0; i < 3; ++i)
+      if (!full((n + i) % NS, ((n + i) / NS) & 1)) return false;
+    mma(s0, s2, true);
+    mma(s2, s0, false);
+    free(s2);
+    mma(s1, s1, false);
+    mma(s0, s1, false);
+    mma(s1, s0, false);
+    free(s1);
+    mma(s0, s0, false);
+    free(s0);
+    n += 3;
+  } else {
+    for (int i = 0; i < n_k; ++i, ++n) {
+      const uint32_t s = n % NS;
+      if (!full(s, (n / NS) & 1)) return false;
+      mma(s, s, i == 0);
+      free(s);
+    }
+  }
+  return true;
+}
 
 // ---------------------------------------------------------------- epilogue
 

@@ -52,11 +52,13 @@ struct Packed {
 Packed pack_x(const LinearArgs& a, int dtype) { return {dtype, a.M, a.K, a.x_s}; }
 Packed pack_w(const LinearArgs& a, int dtype) { return {dtype, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, a.w_s}; }
 
-// Cycles of one 64-k step of a tile of m x n in an SM: its products, or the bytes that it
-// brings in at 64 a cycle.  fp32 takes six products of three pieces.
-long long step_cycles(bool fp32, int m, int n, int rows_here, int cols_here) {
-  const long long mma = (long long)m * n / 64, load = (rows_here + cols_here) * 2LL;
-  return fp32 ? (6 * mma > 3 * load ? 6 * mma : 3 * load) : mma > load ? mma : load;
+// Cycles of one 64-k step of a tile of m x n in an SM that holds `rows` rows of operands for it:
+// its products, or what shared memory takes in (128 bytes a row at 64 a cycle from L2, and as
+// it writes 128 a cycle) and gives to the tensor cores.  fp32 takes six products of three
+// pieces.
+long long step_cycles(bool fp32, int m, int n, int rows) {
+  const long long mma = (long long)m * n / 64;
+  return fp32 ? (6 * mma > 9LL * rows ? 6 * mma : 9LL * rows) : mma > 2LL * rows ? mma : 2LL * rows;
 }
 
 // C[m,n] = sum over k of A[m,k] B[n,k], and its epilogue where `full`.
@@ -79,7 +81,7 @@ cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, i
     if (!best || cost < best) best = cost, bn = bn_, tn = tn_, split = split_;
   };
   for (int b = fp32 ? 128 : 256; b >= 128; b /= 2)
-    offer(ceil_div(ceil_div(A.rows, 256) * ceil_div(B.rows, b), sms / 2) * n_k * step_cycles(fp32, 128, b, 128, b / 2),
+    offer(ceil_div(ceil_div(A.rows, 256) * ceil_div(B.rows, b), sms / 2) * n_k * step_cycles(fp32, 128, b, 128 + b / 2),
           b == 256 ? 17000 : 11500, b, 0, 1);
   const long long n_tiles = ceil_div(B.rows, 128);
   for (int t = A.mn ? 64 : 16; t <= 128; t *= 2) {
@@ -87,7 +89,7 @@ cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, i
     if (tiles > 4LL * sms) continue;
     for (int s = 1; s <= 6 && s <= n_k; ++s) {
       const long long waves = ceil_div(tiles * s, s > 1 ? sms * 21 / 25 : sms);
-      offer(waves * ceil_div(n_k, s) * step_cycles(fp32, 128, t, 128, t), 10500 + 12 * t + (waves - 1) * 14000, 0, t, s);
+      offer(waves * ceil_div(n_k, s) * step_cycles(fp32, 128, t, 128 + t), 10500 + 12 * t + (waves - 1) * 14000, 0, t, s);
     }
   }
   if (tn) return (fp32 ? launch_linear_few_fp32 : launch_linear_few_bf16)(tn, A, B, e, full, split, st);

@@ -13,7 +13,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* wor
 size_t linear_bwd_workspace(const LinearArgs& a, int dtype, bool act);
 cudaError_t launch_linear_bwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st);
 int block_norm_bwd_blocks(const BlockNormArgs& a, int sms);
-cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype, cudaStream_t st);
+cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, cudaStream_t st);
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, float* d_scale, float* d_post,
                                   float* d_pre, cudaStream_t st);
 
@@ -132,11 +132,12 @@ int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch,
   if (!branch && (gate || scale || h_out || a->post_norm)) return DR_ERR_ARG;
   if ((post_weight && !a->post_norm) || (pre_weight && !y)) return DR_ERR_ARG;
   if (y == h || (h_out && y == h_out)) return DR_ERR_ARG;
-  if (!sm_count()) return DR_ERR_CUDA;
+  const int sms = sm_count();
+  if (!sms) return DR_ERR_CUDA;
   BlockNormArgs r = block_norm_args(a);
   r.h = h, r.branch = branch, r.gate = gate, r.scale = scale, r.post_w = post_weight, r.pre_w = pre_weight;
   r.h_out = h_out, r.y = y;
-  return status_of(launch_block_norm_fwd(r, a->dtype, a->h_dtype, stream_of(stream)));
+  return status_of(launch_block_norm_fwd(r, a->dtype, a->h_dtype, sms, stream_of(stream)));
 }
 
 size_t dr_block_norm_bwd_workspace_bytes(const dr_block_norm* a) {

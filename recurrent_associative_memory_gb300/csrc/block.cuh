@@ -45,7 +45,7 @@ struct BlockNormArgs {
   void* dh;
   void* db;
   void* dg;
-  float* part;                 // [blocks][3][D]: of scale, post_w, pre_w
+  float* part;                 // [blocks][2][D]: of scale and post_w, of pre_w
 };
 
 // f(x) and f'(x).  Behind +-30 a sigmoid is 0 or 1 to fp32, so the products with 1 - s take x

@@ -142,7 +142,7 @@ int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch,
 
 size_t dr_block_norm_bwd_workspace_bytes(const dr_block_norm* a) {
   if (!a || check_block_norm(a) != DR_OK) return 0;
-  return (static_cast<size_t>(block_norm_bwd_blocks(block_norm_args(a), sm_count())) * 3 * a->D * 4 + 255) & ~size_t(255);
+  return (static_cast<size_t>(block_norm_bwd_blocks(block_norm_args(a), sm_count())) * 2 * a->D * 4 + 255) & ~size_t(255);
 }
 
 int dr_block_norm_bwd(const dr_block_norm* a, const void* h, const void* branch, const void* gate, const float* scale,

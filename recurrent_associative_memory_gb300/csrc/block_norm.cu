@@ -9,13 +9,13 @@
 // summed, before its rounding to the stream's type, and the backward pass sums it again from
 // the same inputs, so nothing but h', y and the gradients is ever rounded.
 //
-// Backward, with t = dy pre_w, n = h' rstd:
-//   dh' = d_h + rstd (t - n mean(t n))      dpre_w  = sum over rows of dy n
-//   du  = dh' scale f(gate)                 dscale  = sum of dh' f(gate) u
-//   dgate = dh' scale u f'(gate)            dpost_w = sum of du v,  v = branch rstd(branch)
-//   dbranch = rstd(branch) (du post_w - v mean(du post_w v))
-// A thread keeps its columns over all of its block's rows, so the weights' sums stay in
-// registers; the blocks leave one partial sum each, which a second kernel joins in order.
+// Backward, with t = dy pre_w, n = h' rstd(h'), v = branch rstd(branch), c = scale post_w:
+//   dh' = d_h + rstd (t - n mean(t n))        dpre_w  = sum over rows of dy n
+//   q   = dh' f(gate) c                       S = sum of dh' f(gate) v
+//   dgate = dh' c v f'(gate)                  dscale = post_w S,  dpost_w = scale S
+//   dbranch = rstd(branch) (q - v mean(q v))
+// A thread keeps its columns over all of its block's rows, so the two sums stay in registers;
+// the blocks leave one partial sum each, which a second kernel joins in order.
 #include <type_traits>
 
 #include "block.cuh"
@@ -24,14 +24,13 @@
 namespace dr {
 namespace {
 
-constexpr int kE = 8;            // columns per thread
 constexpr int kMaxStages = 8;
 
-// A thread's columns of a row: 8 neighbours where rows start on 16 bytes, else one of every
-// tpr so that a warp's accesses stay next to each other.
-template <int VEC> struct Columns {
+// A thread's E columns of a row: groups of 8 neighbours where rows start on 16 bytes, else one
+// of every tpr so that a warp's accesses stay next to each other.
+template <int VEC, int E> struct Columns {
   int D, tpr, t;
-  __device__ __forceinline__ int at(int e) const { return VEC == 8 ? 8 * t + e : e * tpr + t; }
+  __device__ __forceinline__ int at(int e) const { return VEC == 8 ? (e / 8 * tpr + t) * 8 + e % 8 : e * tpr + t; }
 };
 
 // Rows come into shared memory by background copies of the whole 16-byte units inside them;
@@ -47,35 +46,48 @@ struct RowCopy {
   }
 };
 
-// A thread's values of a row whose copy stands at `at` in shared memory.
-template <typename T, int VEC>
-__device__ __forceinline__ void row_values(const RowCopy& r, uint32_t at, const Columns<VEC>& c, float (&f)[kE]) {
+// A thread's values of row `row`, from its copy at `at` in shared memory (WIDE), or from memory.
+template <typename T, bool WIDE, int VEC, int E>
+__device__ __forceinline__ void row_values(const void* base, long long row, long long stride, uint32_t at,
+                                           const Columns<VEC, E>& c, f2 (&r)[E / 2]) {
+  float f[E];
   if constexpr (VEC == 8) {
-    if (8 * c.t >= c.D) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) f[e] = 0.f;
-      return;
-    }
-    uint32_t w[2 * sizeof(T)];
+    for (int g = 0; g < E; g += 8) {
+      const int n = c.at(g);
+      if (n >= c.D) {
 #pragma unroll
-    for (int i = 0; i < 2 * (int)sizeof(T); i += 4)
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "r"(at + 8 * c.t * (int)sizeof(T) + 4 * i)
-                   : "memory");
+        for (int e = 0; e < 8; ++e) f[g + e] = 0.f;
+        continue;
+      }
+      uint32_t w[2 * sizeof(T)];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      if constexpr (sizeof(T) == 2) f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-      else f[e] = __uint_as_float(w[e]);
+      for (int i = 0; i < 2 * (int)sizeof(T); i += 4) {
+        if constexpr (WIDE) {
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                       : "r"(at + n * (int)sizeof(T) + 4 * i)
+                       : "memory");
+        } else {
+          const uint4 u = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row * stride + n)[i / 4];
+          w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 2) f[g + e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+        else f[g + e] = __uint_as_float(w[e]);
+      }
     }
   } else {
-    const uint32_t head = static_cast<uint32_t>(r.lo - r.p);   // bytes before the first unit
+    const RowCopy rc(base, row, stride, c.D, sizeof(T));
+    const uint32_t head = static_cast<uint32_t>(rc.lo - rc.p);   // bytes before the first unit
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
+    for (int e = 0; e < E; ++e) {
       f[e] = 0.f;
       if (c.at(e) >= c.D) continue;
-      const uint32_t b = c.at(e) * (uint32_t)sizeof(T), in = b - head;   // below the row's start: huge
-      if (in < r.bytes) {
+      const uint32_t b = c.at(e) * (uint32_t)sizeof(T), in = b - head;   // below the first unit: huge
+      if (WIDE && in < rc.bytes) {
         if constexpr (sizeof(T) == 2) {
           uint16_t v;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at + in) : "memory");
@@ -84,71 +96,121 @@ __device__ __forceinline__ void row_values(const RowCopy& r, uint32_t at, const 
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + in) : "memory");
         }
       } else {
-        f[e] = to_f(*reinterpret_cast<const T*>(r.p + b));
+        f[e] = to_f(*reinterpret_cast<const T*>(rc.p + b));
       }
     }
   }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
-template <int VEC> __device__ __forceinline__ void load_vector(const float* p, const Columns<VEC>& c, float (&f)[kE]) {
+// Values in pairs: two fp32 operations per instruction, as instructions are what bounds these
+// kernels next to memory.
+__device__ __forceinline__ f2 both(float x) { return pack2(x, x); }
+template <int P> __device__ __forceinline__ void fill(f2 (&r)[P], float x) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) r[i] = both(x);
+}
+template <int P> __device__ __forceinline__ float dot(const f2 (&x)[P], const f2 (&y)[P]) {
+  f2 a = mul2(x[0], y[0]), b = mul2(x[1], y[1]);
+#pragma unroll
+  for (int i = 2; i < P; i += 2) a = fma2(x[i], y[i], a), b = fma2(x[i + 1], y[i + 1], b);
+  return sum2(add2(a, b));
+}
+template <int P, typename F> __device__ __forceinline__ void pairs(F&& f) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) f(i);
+}
+
+template <int VEC, int E> __device__ __forceinline__ void load_vector(const float* p, const Columns<VEC, E>& c, f2 (&r)[E / 2]) {
+  float f[E];
   if constexpr (VEC == 8) {
-    load8(p + 8 * c.t, 8 * c.t < c.D ? 1 : 0, f);
+#pragma unroll
+    for (int g = 0; g < E; g += 8)
+      load8(p + c.at(g), c.at(g) < c.D ? 1 : 0, reinterpret_cast<float(&)[8]>(f[g]));
   } else {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) f[e] = c.at(e) < c.D ? p[c.at(e)] : 0.f;
+    for (int e = 0; e < E; ++e) f[e] = c.at(e) < c.D ? p[c.at(e)] : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store_row(T* p, const Columns<VEC>& c, const float (&f)[kE]) {
+template <typename T, int VEC, int E>
+__device__ __forceinline__ void store_row(T* p, const Columns<VEC, E>& c, const f2 (&r)[E / 2]) {
+  float f[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) unpack2(r[i], f[2 * i], f[2 * i + 1]);
   if constexpr (VEC == 8) {
-    if (8 * c.t < c.D) store8(p + 8 * c.t, f);
+#pragma unroll
+    for (int g = 0; g < E; g += 8)
+      if (c.at(g) < c.D) store8(p + c.at(g), reinterpret_cast<float(&)[8]>(f[g]));
   } else {
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
+    for (int e = 0; e < E; ++e)
       if (c.at(e) < c.D) p[c.at(e)] = from_f<T>(f[e]);
   }
 }
 
-// The ring of rows of a row slot: its first thread issues a row's copies, counted on the
-// slot's barrier of that stage, `stages` rows ahead of the one that is worked on.
+// The rows of a block.  WIDE: one at a time, through a ring of `stages` of them in shared
+// memory.  Tensor i of a row is copied by warp i, once the block has passed a barrier behind
+// the reads of the row whose place it takes: the first one of the next row.  (To issue a copy
+// takes a few hundred cycles: one thread for all of them holds the block up, M16384 D4096
+// forward 156 us instead of XXX; a warp of its own costs the others 32 registers each.)
+// Otherwise straight from memory.
 template <int N> struct Ring {
-  uint64_t* bar;            // [stages], of this slot
-  uint32_t at, stage_bytes; // shared memory of stage 0 of this slot; from stage to stage
+  uint64_t* full;
+  uint32_t at, stage_bytes;   // shared memory of stage 0; from stage to stage
   int stages;
   const void* base[N];
   long long stride[N];
-  uint32_t off[N];          // of the tensors in a stage
+  uint32_t off[N];            // of the tensors in a stage
   int es[N];
+  int stage;
+  uint32_t parity;
   bool lost;
 
-  __device__ __forceinline__ void issue(long long row, int stage, int D) {
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (base[i]) bytes += RowCopy(base[i], row, stride[i], D, es[i]).bytes;
-    umma::mbar_expect_tx(bar + stage, bytes);
+  // One thread of a warp: that warp's tensor of a row.
+  __device__ __forceinline__ void issue(int warp, long long row, int s, int D) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (!base[i]) continue;
+      if (i != warp || !base[i]) continue;
       const RowCopy r(base[i], row, stride[i], D, es[i]);
+      umma::mbar_expect_tx(full + s, r.bytes);
       if (r.bytes)
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                at + stage * stage_bytes + off[i]),
-            "l"(r.lo), "r"(r.bytes), "r"(umma::smem_u32(bar + stage))
-            : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         at + s * stage_bytes + off[i]),
+                     "l"(r.lo), "r"(r.bytes), "r"(umma::smem_u32(full + s))
+                     : "memory");
     }
   }
   // Bounded; after one that gave up none waits any more, and what comes out means nothing.
-  __device__ __forceinline__ void wait(int stage, uint32_t parity) {
-    if (lost || umma::mbar_wait(bar + stage, parity, 2000000000ull)) return;
+  __device__ __forceinline__ void wait() {
+    if (lost || umma::mbar_wait(full + stage, parity, 2000000000ull)) return;
     lost = true;
     set_status(DR_ERR_TIMEOUT);
   }
-  template <typename T, int VEC>
-  __device__ __forceinline__ void get(int i, long long row, int stage, const Columns<VEC>& c, float (&f)[kE]) const {
-    row_values<T>(RowCopy(base[i], row, stride[i], c.D, sizeof(T)), at + stage * stage_bytes + off[i], c, f);
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) stage = 0, parity ^= 1;
+  }
+  // Behind the first barrier of `row`: the place of the row before goes to the one `stages`
+  // further on.
+  __device__ __forceinline__ void refill(long long row, long long first, long long step, int M, int D) {
+    const long long to = row + (stages - 1) * step;
+    if (threadIdx.x < 32 * N && threadIdx.x % 32 == 0 && row > first && to < M)
+      issue(threadIdx.x / 32, to, stage == 0 ? stages - 1 : stage - 1, D);
+  }
+  // No copy may be in flight when the block ends; only after a wait that gave up there can be.
+  __device__ __forceinline__ void drain() {
+    if (!lost) return;
+    for (int i = 0; i < stages; ++i) {
+      umma::mbar_wait(full + stage, parity, 500000000ull);
+      next();
+    }
+  }
+  template <typename T, bool WIDE, int VEC, int E>
+  __device__ __forceinline__ void get(int i, long long row, const Columns<VEC, E>& c, f2 (&r)[E / 2]) const {
+    row_values<T, WIDE>(base[i], row, stride[i], at + stage * stage_bytes + off[i], c, r);
   }
 };
 
@@ -156,348 +218,321 @@ template <int N> struct Ring {
 // threads stay within a warp; a wider one has its block to itself and goes through shared
 // memory, two buffers in turn so that one barrier does: whoever writes a buffer again has
 // passed the other one's barrier, which everyone reached after reading the first.
-template <int N> __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2][64], int& turn) {
+template <bool WIDE, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2][64], int& turn) {
   static_assert(N <= 2, "");
+  auto over_lanes = [&](int most) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < tpr) {
+    for (int o = 16; o > 0; o >>= 1)
+      if (WIDE || o < most) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      }
+  };
+  over_lanes(tpr);
+  if constexpr (WIDE) {
+    float* buf = bufs[turn];
+    turn ^= 1;
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[i * 32 + threadIdx.x / 32] = v[i];
     }
-  if (tpr <= 32) return;
-  float* buf = bufs[turn];
-  turn ^= 1;
-  const int warps = tpr / 32, warp = threadIdx.x / 32;
-  if (threadIdx.x % 32 == 0) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += buf[i * 32 + w];
-    v[i] = s;
+    for (int i = 0; i < N; ++i) v[i] = lane * 32 < tpr ? buf[i * 32 + lane] : 0.f;
+    over_lanes(32);
   }
 }
 
-template <bool SLOPE> __device__ __forceinline__ void gate_of(int act, const float (&z)[kE], float (&f)[kE], float (&s)[kE]) {
-  auto each = [&](auto one) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) one(e);
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+  float a, b;
+  unpack2(add2(ex2_2(mul2(x, both(-1.4426950408889634f))), both(1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pack2(a, b);
+}
+
+// f(z), and f'(z) where SLOPE: s (1 - s) of a sigmoid s, s + z s (1 - s) of z s.
+template <bool SLOPE, int P> __device__ __forceinline__ void gate_of(int act, const f2 (&z)[P], f2 (&f)[P], f2 (&d)[P]) {
+  auto scalar = [&](auto code) {
+    pairs<P>([&](int i) {
+      float x[2], s[2];
+      unpack2(z[i], x[0], x[1]);
+      x[0] = act_of<decltype(code)::value>(x[0], s[0]), x[1] = act_of<decltype(code)::value>(x[1], s[1]);
+      f[i] = pack2(x[0], x[1]);
+      if constexpr (SLOPE) d[i] = pack2(s[0], s[1]);
+    });
   };
-  switch (act) {
-    case DR_ACT_RELU: each([&](int e) { f[e] = SLOPE ? act_of<DR_ACT_RELU>(z[e], s[e]) : act_of<DR_ACT_RELU>(z[e]); }); break;
-    case DR_ACT_SILU: each([&](int e) { f[e] = SLOPE ? act_of<DR_ACT_SILU>(z[e], s[e]) : act_of<DR_ACT_SILU>(z[e]); }); break;
-    case DR_ACT_GELU_TANH:
-      each([&](int e) { f[e] = SLOPE ? act_of<DR_ACT_GELU_TANH>(z[e], s[e]) : act_of<DR_ACT_GELU_TANH>(z[e]); });
-      break;
-    case DR_ACT_SIGMOID:
-      each([&](int e) { f[e] = SLOPE ? act_of<DR_ACT_SIGMOID>(z[e], s[e]) : act_of<DR_ACT_SIGMOID>(z[e]); });
-      break;
-    default: each([&](int e) { f[e] = z[e], s[e] = 1.f; });
+  if (act == DR_ACT_SILU) {
+    pairs<P>([&](int i) {
+      const f2 s = sigmoid2(z[i]);
+      f[i] = mul2(z[i], s);
+      if constexpr (SLOPE) d[i] = add2(s, fma2(f[i], mul2(s, both(-1.f)), f[i]));
+    });
+  } else if (act == DR_ACT_SIGMOID) {
+    pairs<P>([&](int i) {
+      f[i] = sigmoid2(z[i]);
+      if constexpr (SLOPE) d[i] = fma2(f[i], mul2(f[i], both(-1.f)), f[i]);
+    });
+  } else if (act == DR_ACT_RELU) {
+    scalar(std::integral_constant<int, DR_ACT_RELU>{});
+  } else if (act == DR_ACT_GELU_TANH) {
+    scalar(std::integral_constant<int, DR_ACT_GELU_TANH>{});
+  } else {
+    scalar(std::integral_constant<int, DR_ACT_NONE>{});
   }
 }
 
 // How a launch lays the rows' copies out.
 struct RingLayout {
   int stages;
-  uint32_t slot_bytes;   // of all tensors of a row
+  uint32_t stage_bytes;
 };
 
-// Sets a slot's ring up and starts its first rows.
-template <int N, int VEC>
-__device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[32 * kMaxStages], const RingLayout& l, const Columns<VEC>& c,
-                                      int rows, int slot, long long row, long long step, int M) {
+constexpr int kNarrow = 128;   // threads of a block whose rows are up to 32 threads each
+
+template <int N, int VEC, int E>
+__device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages], const RingLayout& l,
+                                      const Columns<VEC, E>& c, long long row, long long step, int M) {
   extern __shared__ __align__(16) uint8_t dynamic[];
-  ring.bar = bars + slot * l.stages;
-  ring.at = umma::smem_u32(dynamic) + slot * l.slot_bytes;
-  ring.stage_bytes = rows * l.slot_bytes;
+  ring.full = bars;
+  ring.at = umma::smem_u32(dynamic);
+  ring.stage_bytes = l.stage_bytes;
   ring.stages = l.stages;
-  ring.lost = false;
+  ring.stage = 0, ring.parity = 0, ring.lost = false;
   uint32_t at = 0;
+  int there = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     ring.off[i] = at;
-    if (ring.base[i]) at += (c.D * ring.es[i] + 15) / 16 * 16;
+    if (ring.base[i]) at += (c.D * ring.es[i] + 15) / 16 * 16, ++there;
   }
-  if (c.t == 0) {
-    for (int i = 0; i < l.stages; ++i) umma::mbar_init(ring.bar + i, 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < l.stages; ++i) umma::mbar_init(ring.full + i, there);
     umma::fence_mbar_init();
-    for (int i = 0; i < l.stages && row + i * step < M; ++i) ring.issue(row + i * step, i, c.D);
   }
   __syncthreads();
+  if (threadIdx.x % 32 == 0)
+    for (int i = 0; i < l.stages && row + i * step < M; ++i) ring.issue(threadIdx.x / 32, row + i * step, i, c.D);
 }
 
-// A row has been read by all of its threads: its place goes to the row `stages` further on.
-template <int N, int VEC>
-__device__ __forceinline__ void next(Ring<N>& ring, const Columns<VEC>& c, long long row, long long step, int M, int& stage,
-                                     uint32_t& parity) {
-  if (c.tpr > 32) __syncthreads();
-  else __syncwarp();
-  if (c.t == 0 && row + ring.stages * step < M) ring.issue(row + ring.stages * step, stage, c.D);
-  if (++stage == ring.stages) stage = 0, parity ^= 1;
-}
-
-// No copy may be in flight when the block ends; only after a wait that gave up there can be.
-template <int N, int VEC>
-__device__ __forceinline__ void drain(Ring<N>& ring, const Columns<VEC>& c, long long row, long long step, int M, int stage,
-                                      uint32_t parity) {
-  if (!ring.lost || c.t != 0) return;
-  for (int i = 0; i < ring.stages && row + i * step < M; ++i) {
-    umma::mbar_wait(ring.bar + stage, parity, 2000000000ull);
-    if (++stage == ring.stages) stage = 0, parity ^= 1;
-  }
-}
-
-// Threads on an SM, by the registers that they need: 64 forward, 128 backward and where the
-// columns of a thread are not neighbours.
-constexpr int fwd_threads(int vec, int size) { return vec == 8 || size > 512 ? 1024 : 512; }
-constexpr int bwd_threads(int size) { return size > 512 ? 1024 : 512; }
-
-// THREADS: the largest block that the kernel is built for.
-template <typename TA, typename TH, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, fwd_threads(VEC, THREADS) / THREADS)
-    block_norm_fwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
+// THREADS: kNarrow, or the largest block that the kernel is built for; BLOCKS of them on an SM.
+template <typename TA, typename TH, int VEC, int E, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
+  constexpr bool WIDE = THREADS != kNarrow;
+  constexpr int P = E / 2;
+  using Row = f2[P];
   __shared__ float buf[2][64];
-  __shared__ uint64_t bars[32 * kMaxStages];
-  int turn = 0, stage = 0;
-  uint32_t parity = 0;
-  const Columns<VEC> c{a.D, tpr, static_cast<int>(threadIdx.x) % tpr};
-  const int rows = blockDim.x / tpr, slot = threadIdx.x / tpr;
-  const long long step = (long long)gridDim.x * rows;
-  long long row = (long long)blockIdx.x * rows + slot;
+  __shared__ uint64_t bars[kMaxStages];
+  int turn = 0;
+  const Columns<VEC, E> c{a.D, tpr, WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % tpr};
+  const int rows = WIDE ? 1 : kNarrow / tpr;
+  const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
   Ring<3> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s;
   ring.es[0] = sizeof(TH), ring.es[1] = ring.es[2] = sizeof(TA);
-  start(ring, bars, l, c, rows, slot, row, step, a.M);
-  float ws[kE], wy[kE];   // scale post_w; pre_w
-#pragma unroll
-  for (int e = 0; e < kE; ++e) ws[e] = wy[e] = 1.f;
+  if (WIDE) start(ring, bars, l, c, first, step, a.M);
+  Row ws, wy;   // scale post_w; pre_w
+  fill(ws, 1.f), fill(wy, 1.f);
   if (a.pre_w) load_vector(a.pre_w, c, wy);
   if (a.scale) load_vector(a.scale, c, ws);
   if (a.post_w) {
-    float w[kE];
+    Row w;
     load_vector(a.post_w, c, w);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) ws[e] *= w[e];
+    pairs<P>([&](int i) { ws[i] = mul2(ws[i], w[i]); });
   }
+  long long row = first + (WIDE ? 0 : threadIdx.x / tpr);
   // rows of other slots of the same warp may end earlier: those go on with zeros
-  for (long long r0 = (long long)blockIdx.x * rows; r0 < a.M; r0 += step, row += step) {
-    const bool live = row < a.M;
-    float h[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) h[e] = 0.f;
+  for (long long r0 = first; r0 < a.M; r0 += step, row += step) {
+    const bool live = WIDE || row < a.M;
+    Row h, u, f;
+    if (!WIDE) fill(h, 0.f), fill(u, 0.f), fill(f, 0.f);
+    if (WIDE) ring.wait();
     if (live) {
-      ring.wait(stage, parity);
-      ring.template get<TH>(0, row, stage, c, h);
+      if (a.branch) ring.template get<TA, WIDE>(1, row, c, u);
+      ring.template get<TH, WIDE>(0, row, c, h);
+      if (a.gate) {
+        Row z, none;
+        ring.template get<TA, WIDE>(2, row, c, z);
+        gate_of<false>(a.gate_act, z, f, none);
+      }
     }
     if (a.branch) {
-      float u[kE];
-#pragma unroll
-      for (int e = 0; e < kE; ++e) u[e] = 0.f;
-      if (live) ring.template get<TA>(1, row, stage, c, u);
       float rstd = 1.f;
       if (a.post_norm) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s[0] = fmaf(u[e], u[e], s[0]);
-        row_sums(s, tpr, buf, turn);
+        float s[1] = {dot(u, u)};
+        row_sums<WIDE>(s, tpr, buf, turn);
         rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
       }
-      if (a.gate && live) {
-        float z[kE], f[kE], none[kE];
-        ring.template get<TA>(2, row, stage, c, z);
-        gate_of<false>(a.gate_act, z, f, none);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) u[e] *= f[e];
-      }
-#pragma unroll
-      for (int e = 0; e < kE; ++e) h[e] = fmaf(u[e] * rstd, ws[e], h[e]);
+      if (a.gate) pairs<P>([&](int i) { u[i] = mul2(u[i], f[i]); });
+      pairs<P>([&](int i) { h[i] = fma2(mul2(u[i], both(rstd)), ws[i], h[i]); });
+      if (live) store_row(static_cast<TH*>(a.h_out) + row * a.D, c, h);
     }
-    next(ring, c, row, step, a.M, stage, parity);
-    if (live && a.branch) store_row(static_cast<TH*>(a.h_out) + row * a.D, c, h);
     if (a.y) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int e = 0; e < kE; ++e) s[0] = fmaf(h[e], h[e], s[0]);
-      row_sums(s, tpr, buf, turn);
+      float s[1] = {dot(h, h)};
+      row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-#pragma unroll
-      for (int e = 0; e < kE; ++e) h[e] *= rstd * wy[e];
+      if (WIDE) ring.refill(row, first, step, a.M, a.D);
+      pairs<P>([&](int i) { h[i] = mul2(h[i], mul2(both(rstd), wy[i])); });
       if (live) store_row(static_cast<TA*>(a.y) + row * a.D, c, h);
+    } else if (WIDE) {
+      __syncthreads();
+      ring.refill(row, first, step, a.M, a.D);
     }
+    if (WIDE) ring.next();
   }
-  drain(ring, c, row, step, a.M, stage, parity);
+  if (WIDE) ring.drain();
 }
 
-template <typename TA, typename TH, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, bwd_threads(THREADS) / THREADS)
-    block_norm_bwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
+template <typename TA, typename TH, int VEC, int E, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
+  constexpr bool WIDE = THREADS != kNarrow;
+  constexpr int P = E / 2;
+  using Row = f2[P];
   __shared__ float buf[2][64];
-  __shared__ uint64_t bars[32 * kMaxStages];
-  int turn = 0, stage = 0;
-  uint32_t parity = 0;
-  const Columns<VEC> c{a.D, tpr, static_cast<int>(threadIdx.x) % tpr};
-  const int D = a.D, rows = blockDim.x / tpr, slot = threadIdx.x / tpr;
-  const long long step = (long long)gridDim.x * rows;
-  long long row = (long long)blockIdx.x * rows + slot;
+  __shared__ uint64_t bars[kMaxStages];
+  int turn = 0;
+  const Columns<VEC, E> c{a.D, tpr, WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % tpr};
+  const int D = a.D, rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
+  const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
   Ring<5> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate, ring.base[3] = a.d_y, ring.base[4] = a.d_h;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s, ring.stride[3] = ring.stride[4] = D;
   ring.es[0] = ring.es[4] = sizeof(TH), ring.es[1] = ring.es[2] = ring.es[3] = sizeof(TA);
-  start(ring, bars, l, c, rows, slot, row, step, a.M);
-  float sum_s[kE] = {}, sum_q[kE] = {}, sum_p[kE] = {};   // of scale, post_w, pre_w
-  for (long long r0 = (long long)blockIdx.x * rows; r0 < a.M; r0 += step, row += step) {
-    const bool live = row < a.M;
+  if (WIDE) start(ring, bars, l, c, first, step, a.M);
+  Row sum_s, sum_p, ws, wy;   // S, the sum of dpre_w; scale post_w, pre_w
+  fill(sum_s, 0.f), fill(sum_p, 0.f), fill(ws, 1.f), fill(wy, 1.f);
+  if (a.pre_w) load_vector(a.pre_w, c, wy);
+  if (a.scale) load_vector(a.scale, c, ws);
+  if (a.post_w) {
+    Row w;
+    load_vector(a.post_w, c, w);
+    pairs<P>([&](int i) { ws[i] = mul2(ws[i], w[i]); });
+  }
+  long long row = first + slot;
+  for (long long r0 = first; r0 < a.M; r0 += step, row += step) {
+    const bool live = WIDE || row < a.M;
     // a row that is none: zeros, so that it adds nothing to any sum
-    float h[kE], u[kE], v[kE], f[kE], fs[kE], w[kE], g[kE];
+    Row h, v, f, vs, g;   // vs: v f'(gate)
     float rstd_b = 1.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) h[e] = u[e] = v[e] = g[e] = fs[e] = 0.f, f[e] = 1.f;
-    if (live) {
-      ring.wait(stage, parity);
-      ring.template get<TH>(0, row, stage, c, h);
-    }
-    if (a.branch) {   // h' again; u the branch's norm with its weight, v without it
-      if (live) ring.template get<TA>(1, row, stage, c, v);
-      if (a.gate && live) {
-        float z[kE];
-        ring.template get<TA>(2, row, stage, c, z);
-        gate_of<true>(a.gate_act, z, f, fs);
-      }
+    if (!WIDE) fill(h, 0.f), fill(v, 0.f);
+    if (WIDE) ring.wait();
+    if (live) ring.template get<TH, WIDE>(0, row, c, h);
+    if (a.branch) {   // h' again
+      if (live) ring.template get<TA, WIDE>(1, row, c, v);
       if (a.post_norm) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s[0] = fmaf(v[e], v[e], s[0]);
-        row_sums(s, tpr, buf, turn);
+        float s[1] = {dot(v, v)};
+        row_sums<WIDE>(s, tpr, buf, turn);
         rstd_b = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-#pragma unroll
-        for (int e = 0; e < kE; ++e) v[e] *= rstd_b;
+        pairs<P>([&](int i) { v[i] = mul2(v[i], both(rstd_b)); });
       }
-#pragma unroll
-      for (int e = 0; e < kE; ++e) u[e] = v[e];
-      if (a.post_w) {
-        load_vector(a.post_w, c, w);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) u[e] *= w[e];
+      fill(f, 1.f), fill(vs, 0.f);
+      if (a.gate && live) {
+        Row z;
+        ring.template get<TA, WIDE>(2, row, c, z);
+        gate_of<true>(a.gate_act, z, f, vs);
+        pairs<P>([&](int i) { vs[i] = mul2(vs[i], v[i]); });
       }
-#pragma unroll
-      for (int e = 0; e < kE; ++e) w[e] = 1.f;
-      if (a.scale) load_vector(a.scale, c, w);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) h[e] = fmaf(w[e] * f[e], u[e], h[e]);
+      pairs<P>([&](int i) { h[i] = fma2(mul2(f[i], v[i]), ws[i], h[i]); });
     }
-    if (a.d_h && live) ring.template get<TH>(4, row, stage, c, g);
     if (a.d_y) {
-      float dy[kE], s[2] = {0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < kE; ++e) dy[e] = 0.f, w[e] = 1.f;
-      if (live) ring.template get<TA>(3, row, stage, c, dy);
-      if (a.pre_w) load_vector(a.pre_w, c, w);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        s[0] = fmaf(h[e], h[e], s[0]);
-        s[1] = fmaf(dy[e] * w[e], h[e], s[1]);
-      }
-      row_sums(s, tpr, buf, turn);
+      Row dy, t;
+      if (!WIDE) fill(dy, 0.f);
+      if (live) ring.template get<TA, WIDE>(3, row, c, dy);
+      pairs<P>([&](int i) { t[i] = mul2(dy[i], wy[i]); });
+      float s[2] = {dot(h, h), dot(t, h)};
+      row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      const float k = s[1] * a.inv_d * rstd * rstd * rstd;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        sum_p[e] = fmaf(dy[e], h[e] * rstd, sum_p[e]);
-        g[e] = fmaf(dy[e] * w[e], rstd, fmaf(-k, h[e], g[e]));
+      const f2 k = both(-s[1] * a.inv_d * rstd * rstd), r2 = both(rstd);
+      pairs<P>([&](int i) {
+        h[i] = mul2(h[i], r2);
+        sum_p[i] = fma2(dy[i], h[i], sum_p[i]);
+        t[i] = fma2(t[i], r2, mul2(k, h[i]));
+      });
+      if (a.d_h) {
+        if (!WIDE) fill(g, 0.f);
+        if (live) ring.template get<TH, WIDE>(4, row, c, g);
+        pairs<P>([&](int i) { g[i] = add2(g[i], t[i]); });
+      } else {
+        pairs<P>([&](int i) { g[i] = t[i]; });
       }
+    } else {
+      if (!WIDE) fill(g, 0.f);
+      if (live) ring.template get<TH, WIDE>(4, row, c, g);
+      if (WIDE) __syncthreads();
     }
-    next(ring, c, row, step, a.M, stage, parity);
+    if (WIDE) ring.refill(row, first, step, a.M, D), ring.next();
     if (live && a.dh) store_row(static_cast<TH*>(a.dh) + row * D, c, g);
     if (!a.branch) continue;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) w[e] = 1.f;
-    if (a.scale) load_vector(a.scale, c, w);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      sum_s[e] = fmaf(g[e] * f[e], u[e], sum_s[e]);
-      fs[e] *= g[e] * w[e] * u[e];
-      g[e] *= w[e] * f[e];   // du from here on
-      sum_q[e] = fmaf(g[e], v[e], sum_q[e]);
-    }
-    if (live && a.dg) store_row(static_cast<TA*>(a.dg) + row * D, c, fs);
+    pairs<P>([&](int i) {
+      const f2 x = mul2(g[i], ws[i]);
+      sum_s[i] = fma2(g[i], mul2(f[i], v[i]), sum_s[i]);
+      vs[i] = mul2(x, vs[i]);
+      g[i] = mul2(x, f[i]);   // q from here on
+    });
+    if (live && a.dg) store_row(static_cast<TA*>(a.dg) + row * D, c, vs);
     if (a.post_norm) {
-      if (a.post_w) {
-        load_vector(a.post_w, c, w);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) g[e] *= w[e];
-      }
-      float s[1] = {0.f};
-#pragma unroll
-      for (int e = 0; e < kE; ++e) s[0] = fmaf(g[e], v[e], s[0]);
-      row_sums(s, tpr, buf, turn);
-      const float k = s[0] * a.inv_d;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) g[e] = rstd_b * fmaf(-k, v[e], g[e]);
+      float s[1] = {dot(g, v)};
+      row_sums<WIDE>(s, tpr, buf, turn);
+      const f2 k = both(-s[0] * a.inv_d * rstd_b), r2 = both(rstd_b);
+      pairs<P>([&](int i) { g[i] = fma2(k, v[i], mul2(r2, g[i])); });
     }
     if (live && a.db) store_row(static_cast<TA*>(a.db) + row * D, c, g);
   }
-  drain(ring, c, row, step, a.M, stage, parity);
+  if (WIDE) ring.drain();
   if (!a.part) return;
-  // rows of a warp first, then one after another over the slots of the block
-  extern __shared__ __align__(16) uint8_t dynamic[];   // the ring's place: [rows][3][D]
-  float* slots = reinterpret_cast<float*>(dynamic);
-  float* part = a.part + (long long)blockIdx.x * 3 * D;
-  auto each = [&](auto use) {
+  float ss[E], sp[E];
+  pairs<P>([&](int i) {
+    unpack2(sum_s[i], ss[2 * i], ss[2 * i + 1]);
+    unpack2(sum_p[i], sp[2 * i], sp[2 * i + 1]);
+  });
+  float* part = a.part + (long long)blockIdx.x * 2 * D;
+  auto each = [&](float* to) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      if (c.at(e) < D) use(e, c.at(e));
+    for (int e = 0; e < E; ++e) {
+      const int n = c.at(e);
+      if (n < D) to[n] = ss[e], to[D + n] = sp[e];
     }
   };
-  if (rows == 1) {
-    each([&](int e, int n) { part[n] = sum_s[e], part[D + n] = sum_q[e], part[2 * D + n] = sum_p[e]; });
-    return;
-  }
-  __syncthreads();
-  each([&](int e, int n) {
-    float* p = slots + (long long)slot * 3 * D;
-    p[n] = sum_s[e], p[D + n] = sum_q[e], p[2 * D + n] = sum_p[e];
-  });
-  __syncthreads();
-  for (int c = threadIdx.x; c < 3 * D; c += blockDim.x) {
-    float s = 0.f;
-    for (int i = 0; i < rows; ++i) s += slots[i * 3 * D + c];
-    part[c] = s;
+  if constexpr (WIDE) {
+    each(part);
+  } else {   // the block's rows, one after another
+    extern __shared__ __align__(16) uint8_t dynamic[];   // [rows][2][D]
+    float* slots = reinterpret_cast<float*>(dynamic);
+    each(slots + slot * 2 * D);
+    __syncthreads();
+    for (int n = threadIdx.x; n < 2 * D; n += kNarrow) {
+      float s = 0.f;
+      for (int i = 0; i < rows; ++i) s += slots[i * 2 * D + n];
+      part[n] = s;
+    }
   }
 }
 
-// out[c] = sum over the blocks of part[block][which][c]: 8 groups of threads over the blocks,
-// joined in order
-__global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int blocks, int D, float* o0, float* o1, float* o2) {
+// The sums over the blocks of part[block][which][D], 8 groups of threads over the blocks, joined
+// in order: which 0 is S, of dscale and dpost_w, 1 is dpre_w.
+__global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int blocks, int D, const float* scale,
+                                                         const float* post_w, float* d_scale, float* d_post, float* d_pre) {
   __shared__ float buf[8][32];
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32, which = blockIdx.y;
-  float* out = which == 0 ? o0 : which == 1 ? o1 : o2;
-  if (!out) return;
+  if (which == 0 ? !d_scale && !d_post : !d_pre) return;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < D)
-    for (int b = g; b < blocks; b += 8) s += part[((long long)b * 3 + which) * D + c];
+    for (int b = g; b < blocks; b += 8) s += part[((long long)b * 2 + which) * D + c];
   buf[g][lane] = s;
   __syncthreads();
-  if (g == 0 && c < D) {
-    for (int i = 1; i < 8; ++i) s += buf[i][lane];
-    out[c] = s;
+  if (g != 0 || c >= D) return;
+  for (int i = 1; i < 8; ++i) s += buf[i][lane];
+  if (which == 1) {
+    d_pre[c] = s;
+    return;
   }
+  if (d_scale) d_scale[c] = post_w ? s * post_w[c] : s;
+  if (d_post) d_post[c] = scale ? s * scale[c] : s;
 }
-
-// threads per row: a power of two from 4 to 32, whole warps from there on, which have their
-// block to themselves
-int threads_of(int D) {
-  const int n = (D + kE - 1) / kE;
-  if (n > 32) return (n + 31) / 32 * 32;
-  int t = 4;
-  while (t < n) t *= 2;
-  return t;
-}
-int rows_of(int tpr) { return tpr <= 32 ? 128 / tpr : 1; }
 
 bool vectors(const BlockNormArgs& a, int es_a, int es_h) {
   auto ok = [](const void* p, long long s, int es) { return !p || ((reinterpret_cast<uintptr_t>(p) | (s * es)) & 15) == 0; };
@@ -508,45 +543,44 @@ bool vectors(const BlockNormArgs& a, int es_a, int es_h) {
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// types, width of an access and largest block of a call
-template <typename F> void by_type(int dtype, int h_dtype, bool vec, int threads, F&& go) {
-  auto size = [&](auto ta, auto th, auto v) {
-    if (threads <= 256) go(ta, th, v, Int<256>{});
-    else if (threads <= 512) go(ta, th, v, Int<512>{});
-    else go(ta, th, v, Int<1024>{});
-  };
+template <typename F> void by_type(int dtype, int h_dtype, bool vec, F&& go) {
   auto types = [&](auto v) {
-    if (dtype == DR_FP32) size(float{}, float{}, v);
-    else if (h_dtype == DR_FP32) size(__nv_bfloat16{}, float{}, v);
-    else size(__nv_bfloat16{}, __nv_bfloat16{}, v);
+    if (dtype == DR_FP32) go(float{}, float{}, v);
+    else if (h_dtype == DR_FP32) go(__nv_bfloat16{}, float{}, v);
+    else go(__nv_bfloat16{}, __nv_bfloat16{}, v);
   };
   if (vec) types(Int<8>{});
   else types(Int<1>{});
 }
 
-// A launch: blocks that stay on every SM, and the rows on their way in what
-// each of them has of its shared memory.
+// A launch: blocks that stay on every SM, and the rows on their way in what each of them has of
+// its shared memory.
 struct Plan {
   int tpr, threads, grid;
   RingLayout ring;
   size_t smem;
-  Plan(const BlockNormArgs& a, int sms, bool bwd, int vec, int row_bytes, bool sums) {
-    tpr = threads_of(a.D);
-    const int rows = rows_of(tpr);
-    threads = tpr * rows;
-    const int size = threads <= 256 ? 256 : threads <= 512 ? 512 : 1024;
-    const int blocks = (bwd ? bwd_threads(size) : fwd_threads(vec, size)) / size;
-    const long long most = (a.M + rows - 1LL) / rows;
-    grid = static_cast<int>(most < (long long)sms * blocks ? most : (long long)sms * blocks);
-    ring.slot_bytes = row_bytes;
-    const long long stage = (long long)rows * row_bytes, there = (224 * 1024) / blocks - 4096;
-    ring.stages = static_cast<int>(there / stage < kMaxStages ? there / stage : kMaxStages);
-    if (ring.stages < 1) ring.stages = 1;
-    const long long steps = (most + grid - 1) / (grid ? grid : 1);
-    if (ring.stages > steps && steps > 0) ring.stages = static_cast<int>(steps);
-    smem = ring.stages * stage;
-    const size_t parts = sums && rows > 1 ? sizeof(float) * rows * 3 * a.D : 0;
-    if (smem < parts) smem = parts;
+  Plan(const BlockNormArgs& a, int sms, int e, int blocks, int row_bytes, bool sums) {
+    const int n = (a.D + e - 1) / e;
+    int rows = 1;
+    smem = 0;
+    if (n <= 32) {
+      for (tpr = 4; tpr < n; tpr *= 2) {}
+      rows = kNarrow / tpr, threads = kNarrow;
+      if (sums) smem = sizeof(float) * rows * 2 * a.D;
+    } else {
+      tpr = threads = (n + 31) / 32 * 32;
+      if (threads < 32 * 5) threads = tpr = 32 * 5;   // a warp for each tensor's copies
+    }
+    const long long most = (a.M + rows - 1LL) / rows, there = (long long)sms * blocks;
+    grid = static_cast<int>(most < there ? most : there);
+    ring.stage_bytes = row_bytes, ring.stages = 1;
+    if (n > 32) {
+      const long long fit = ((224 * 1024) / blocks - 2048) / row_bytes, need = (most + grid - 1) / (grid ? grid : 1);
+      ring.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
+      if (ring.stages > need) ring.stages = static_cast<int>(need);
+      if (ring.stages < 1) ring.stages = 1;
+      smem = (size_t)ring.stages * row_bytes;
+    }
   }
 };
 
@@ -564,31 +598,57 @@ template <typename K> cudaError_t launch(K* kernel, const Plan& p, const BlockNo
   return cudaGetLastError();
 }
 
+// Columns per thread, the largest block and the blocks on an SM, by the row's length.
+template <typename F> void fwd_shape(int D, F&& go) {
+  if (D <= 256) go(Int<8>{}, Int<kNarrow>{}, Int<8>{});
+  else if (D <= 2048) go(Int<8>{}, Int<256>{}, Int<4>{});
+  else if (D <= 4096) go(Int<16>{}, Int<256>{}, Int<2>{});
+  else go(Int<16>{}, Int<512>{}, Int<1>{});
+}
+template <typename F> void bwd_shape(int D, F&& go) {
+  if (D <= 256) go(Int<8>{}, Int<kNarrow>{}, Int<4>{});
+  else if (D <= 2048) go(Int<8>{}, Int<256>{}, Int<2>{});
+  else if (D <= 4096) go(Int<8>{}, Int<512>{}, Int<1>{});
+  else go(Int<16>{}, Int<512>{}, Int<1>{});
+}
+
 }  // namespace
 
-int block_norm_bwd_blocks(const BlockNormArgs& a, int sms) { return Plan(a, sms, true, 8, 16, false).grid; }
+int block_norm_bwd_blocks(const BlockNormArgs& a, int sms) {
+  int n = 0;
+  bwd_shape(a.D, [&](auto e, auto, auto blocks) { n = Plan(a, sms, e, blocks, 16, false).grid; });
+  return n;
+}
 
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, cudaStream_t st) {
   const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2;
-  const bool vec = vectors(a, es_a, es_h);
-  const Plan p(a, sms, false, vec ? 8 : 1, row_bytes(a, es_a, es_h), false);
-  cudaError_t e = cudaSuccess;
-  by_type(dtype, h_dtype, vec, p.threads, [&](auto ta, auto th, auto v, auto n) {
-    e = launch(block_norm_fwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(n)::value>, p, a, st);
+  cudaError_t err = cudaSuccess;
+  by_type(dtype, h_dtype, vectors(a, es_a, es_h), [&](auto ta, auto th, auto v) {
+    fwd_shape(a.D, [&](auto e, auto threads, auto blocks) {
+      err = launch(block_norm_fwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(e)::value,
+                                         decltype(threads)::value, decltype(blocks)::value>,
+                   Plan(a, sms, e, blocks, row_bytes(a, es_a, es_h), false), a, st);
+    });
   });
-  return e;
+  return err;
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, float* d_scale, float* d_post,
                                   float* d_pre, cudaStream_t st) {
   const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2;
-  const Plan p(a, sms, true, 8, row_bytes(a, es_a, es_h), a.part != nullptr);
-  cudaError_t e = cudaSuccess;
-  by_type(dtype, h_dtype, vectors(a, es_a, es_h), p.threads, [&](auto ta, auto th, auto v, auto n) {
-    e = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(n)::value>, p, a, st);
+  cudaError_t err = cudaSuccess;
+  int grid = 0;
+  by_type(dtype, h_dtype, vectors(a, es_a, es_h), [&](auto ta, auto th, auto v) {
+    bwd_shape(a.D, [&](auto e, auto threads, auto blocks) {
+      const Plan p(a, sms, e, blocks, row_bytes(a, es_a, es_h), a.part != nullptr);
+      grid = p.grid;
+      err = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(e)::value,
+                                         decltype(threads)::value, decltype(blocks)::value>,
+                   p, a, st);
+    });
   });
-  if (e != cudaSuccess || !a.part) return e;
-  join_parts_kernel<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(a.part, p.grid, a.D, d_scale, d_post, d_pre);
+  if (err != cudaSuccess || !a.part) return err;
+  join_parts_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, st>>>(a.part, grid, a.D, a.scale, a.post_w, d_scale, d_post, d_pre);
   return cudaGetLastError();
 }
 

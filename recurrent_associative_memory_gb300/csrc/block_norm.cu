@@ -25,51 +25,71 @@ namespace dr {
 namespace {
 
 constexpr int kMaxStages = 8;
+constexpr int kMaxRow = 8192;     // 512 threads of 16 columns
 
-// A thread's E columns of a row: groups of 8 neighbours where rows start on 16 bytes, else one
-// of every tpr so that a warp's accesses stay next to each other.
-template <int VEC, int E> struct Columns {
-  int D, tpr, t;
-  __device__ __forceinline__ int at(int e) const { return VEC == 8 ? (e / 8 * tpr + t) * 8 + e % 8 : e * tpr + t; }
+// How a thread's E columns stand.
+//   kEven  groups of 8 neighbours; the row's length is a multiple of 8
+//   kOdd   groups of 8, cut where the row's values stand at multiples of 8 of the tensor.  In a
+//          row of odd length that is `phase` columns before its start, and the first and the
+//          last group are not whole.  A block's rows are a multiple of 8 apart, so the phase
+//          and with it a thread's columns are the same in all of them.
+//   kApart one column of every tpr, for rows that do not stand so
+enum { kEven, kOdd, kApart };
+template <int ORDER, int E> struct Columns {
+  int D, tpr, t, phase_;
+  __device__ __forceinline__ int phase() const { return ORDER == kOdd ? phase_ : 0; }
+  __device__ __forceinline__ int at(int e) const {
+    return ORDER == kApart ? e * tpr + t : (e / 8 * tpr + t) * 8 + e % 8 - phase();
+  }
+  __device__ __forceinline__ bool in(int n) const { return (ORDER != kOdd || n >= 0) && n < D; }
+  // of a group from n on
+  __device__ __forceinline__ bool whole(int n) const { return ORDER == kEven ? n < D : n >= 0 && n + 8 <= D; }
 };
 
-// Rows come into shared memory by background copies of the whole 16-byte units inside them;
-// the few values before the first and after the last unit are read where they are.
+// Rows come into shared memory by background copies, from their first group on.  What a group
+// holds of the neighbouring rows is copied along; behind the tensor's last row nothing is, only
+// the whole 16 bytes before its end.
 struct RowCopy {
-  uintptr_t p, lo;   // the row, its first whole unit
-  uint32_t bytes;    // of whole units
-  __device__ __forceinline__ RowCopy(const void* base, long long row, long long stride, int D, int es) {
-    p = reinterpret_cast<uintptr_t>(base) + row * stride * es;
-    lo = (p + 15) & ~uintptr_t(15);
-    const uintptr_t hi = (p + static_cast<uint32_t>(D) * es) & ~uintptr_t(15);
-    bytes = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+  uintptr_t lo;
+  uint32_t bytes;
+  __device__ __forceinline__ RowCopy(const void* base, long long row, long long stride, int D, int phase, int es, int M) {
+    lo = reinterpret_cast<uintptr_t>(base) + (row * stride - phase) * es;
+    const uint32_t all = static_cast<uint32_t>(phase + D) * es;
+    bytes = row == M - 1 ? all & ~15u : (all + 8 * es - 1) / (8 * es) * (8 * es);
   }
 };
+// what a row's copy takes of shared memory
+__host__ __device__ __forceinline__ int copy_bytes(int D, int es) { return (D % 8 ? D / 8 + 2 : D / 8) * 8 * es; }
 
-// A thread's values of row `row`, from its copy at `at` in shared memory (WIDE), or from memory.
-template <typename T, bool WIDE, int VEC, int E>
-__device__ __forceinline__ void row_values(const void* base, long long row, long long stride, uint32_t at,
-                                           const Columns<VEC, E>& c, f2 (&r)[E / 2]) {
+// A thread's values of row `row`, from its copy at `at` in shared memory (RING), or from memory.
+template <typename T, bool RING, int ORDER, int E>
+__device__ __forceinline__ void row_values(const void* base, long long row, long long stride, uint32_t at, int M,
+                                           const Columns<ORDER, E>& c, f2 (&r)[E / 2]) {
   float f[E];
-  if constexpr (VEC == 8) {
+  const T* p = static_cast<const T*>(base) + row * stride;
+  auto one = [&](int n) { return c.in(n) ? to_f(p[n]) : 0.f; };
+  if constexpr (ORDER != kApart) {
 #pragma unroll
     for (int g = 0; g < E; g += 8) {
       const int n = c.at(g);
-      if (n >= c.D) {
+      uint32_t w[2 * sizeof(T)];
+      // a ring's copy does not hold what lies behind the row (threads that have no columns), nor
+      // of the tensor's last row a group that is not whole
+      const bool apart = RING && ORDER == kOdd ? n >= c.D || (row == M - 1 && !c.whole(n)) : !c.whole(n);
+      if (apart) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[g + e] = 0.f;
+        for (int e = 0; e < 8; ++e) f[g + e] = ORDER == kEven ? 0.f : one(n + e);
         continue;
       }
-      uint32_t w[2 * sizeof(T)];
 #pragma unroll
       for (int i = 0; i < 2 * (int)sizeof(T); i += 4) {
-        if constexpr (WIDE) {
+        if constexpr (RING) {
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                       : "r"(at + n * (int)sizeof(T) + 4 * i)
+                       : "r"(at + (n + c.phase()) * (int)sizeof(T) + 4 * i)
                        : "memory");
         } else {
-          const uint4 u = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row * stride + n)[i / 4];
+          const uint4 u = reinterpret_cast<const uint4*>(p + n)[i / 4];
           w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
         }
       }
@@ -78,27 +98,14 @@ __device__ __forceinline__ void row_values(const void* base, long long row, long
         if constexpr (sizeof(T) == 2) f[g + e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
         else f[g + e] = __uint_as_float(w[e]);
       }
-    }
-  } else {
-    const RowCopy rc(base, row, stride, c.D, sizeof(T));
-    const uint32_t head = static_cast<uint32_t>(rc.lo - rc.p);   // bytes before the first unit
+      if (RING && ORDER == kOdd && !c.whole(n)) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      f[e] = 0.f;
-      if (c.at(e) >= c.D) continue;
-      const uint32_t b = c.at(e) * (uint32_t)sizeof(T), in = b - head;   // below the first unit: huge
-      if (WIDE && in < rc.bytes) {
-        if constexpr (sizeof(T) == 2) {
-          uint16_t v;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at + in) : "memory");
-          f[e] = __uint_as_float(static_cast<uint32_t>(v) << 16);
-        } else {
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + in) : "memory");
-        }
-      } else {
-        f[e] = to_f(*reinterpret_cast<const T*>(rc.p + b));
+        for (int e = 0; e < 8; ++e) f[g + e] = c.in(n + e) ? f[g + e] : 0.f;
       }
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = one(c.at(e));
   }
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
@@ -122,41 +129,46 @@ template <int P, typename F> __device__ __forceinline__ void pairs(F&& f) {
   for (int i = 0; i < P; ++i) f(i);
 }
 
-template <int VEC, int E> __device__ __forceinline__ void load_vector(const float* p, const Columns<VEC, E>& c, f2 (&r)[E / 2]) {
+template <int ORDER, int E> __device__ __forceinline__ void load_vector(const float* p, const Columns<ORDER, E>& c, f2 (&r)[E / 2]) {
   float f[E];
-  if constexpr (VEC == 8) {
 #pragma unroll
-    for (int g = 0; g < E; g += 8)
-      load8(p + c.at(g), c.at(g) < c.D ? 1 : 0, reinterpret_cast<float(&)[8]>(f[g]));
-  } else {
+  for (int g = 0; g < E; g += 8) {
+    if constexpr (ORDER == kEven) {
+      const bool in = c.at(g) < c.D;   // on any address
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = c.at(e) < c.D ? p[c.at(e)] : 0.f;
+      for (int e = 0; e < 8; ++e) f[g + e] = in ? p[c.at(g) + e] : 0.f;
+    } else {
+#pragma unroll
+      for (int e = g; e < g + 8; ++e) f[e] = c.in(c.at(e)) ? p[c.at(e)] : 0.f;
+    }
   }
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void store_row(T* p, const Columns<VEC, E>& c, const f2 (&r)[E / 2]) {
+template <typename T, int ORDER, int E>
+__device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, const f2 (&r)[E / 2]) {
   float f[E];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) unpack2(r[i], f[2 * i], f[2 * i + 1]);
-  if constexpr (VEC == 8) {
 #pragma unroll
-    for (int g = 0; g < E; g += 8)
-      if (c.at(g) < c.D) store8(p + c.at(g), reinterpret_cast<float(&)[8]>(f[g]));
-  } else {
+  for (int g = 0; g < E; g += 8) {
+    const int n = c.at(g);
+    if (ORDER != kApart && c.whole(n)) {
+      store8(p + n, reinterpret_cast<float(&)[8]>(f[g]));
+    } else if (ORDER != kEven) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (c.at(e) < c.D) p[c.at(e)] = from_f<T>(f[e]);
+      for (int e = g; e < g + 8; ++e)
+        if (c.in(c.at(e))) p[c.at(e)] = from_f<T>(f[e]);
+    }
   }
 }
 
-// The rows of a block.  WIDE: one at a time, through a ring of `stages` of them in shared
+// The rows of a block.  RING: one at a time, through a ring of `stages` of them in shared
 // memory.  Tensor i of a row is copied by warp i, once the block has passed a barrier behind
 // the reads of the row whose place it takes: the first one of the next row.  (To issue a copy
 // takes a few hundred cycles: one thread for all of them holds the block up, M16384 D4096
-// forward 156 us instead of XXX; a warp of its own costs the others 32 registers each.)
+// forward 156 us instead of 103; a warp of its own costs the others their registers.)
 // Otherwise straight from memory.
 template <int N> struct Ring {
   uint64_t* full;
@@ -165,17 +177,17 @@ template <int N> struct Ring {
   const void* base[N];
   long long stride[N];
   uint32_t off[N];            // of the tensors in a stage
-  int es[N];
+  int es[N], M;
   int stage;
   uint32_t parity;
   bool lost;
 
   // One thread of a warp: that warp's tensor of a row.
-  __device__ __forceinline__ void issue(int warp, long long row, int s, int D) {
+  __device__ __forceinline__ void issue(int warp, long long row, int s, int D, int phase) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (i != warp || !base[i]) continue;
-      const RowCopy r(base[i], row, stride[i], D, es[i]);
+      const RowCopy r(base[i], row, stride[i], D, phase, es[i], M);
       umma::mbar_expect_tx(full + s, r.bytes);
       if (r.bytes)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -195,10 +207,10 @@ template <int N> struct Ring {
   }
   // Behind the first barrier of `row`: the place of the row before goes to the one `stages`
   // further on.
-  __device__ __forceinline__ void refill(long long row, long long first, long long step, int M, int D) {
+  __device__ __forceinline__ void refill(long long row, long long first, long long step, int D, int phase) {
     const long long to = row + (stages - 1) * step;
     if (threadIdx.x < 32 * N && threadIdx.x % 32 == 0 && row > first && to < M)
-      issue(threadIdx.x / 32, to, stage == 0 ? stages - 1 : stage - 1, D);
+      issue(threadIdx.x / 32, to, stage == 0 ? stages - 1 : stage - 1, D, phase);
   }
   // No copy may be in flight when the block ends; only after a wait that gave up there can be.
   __device__ __forceinline__ void drain() {
@@ -208,40 +220,48 @@ template <int N> struct Ring {
       next();
     }
   }
-  template <typename T, bool WIDE, int VEC, int E>
-  __device__ __forceinline__ void get(int i, long long row, const Columns<VEC, E>& c, f2 (&r)[E / 2]) const {
-    row_values<T, WIDE>(base[i], row, stride[i], at + stage * stage_bytes + off[i], c, r);
+  template <typename T, bool RING, int ORDER, int E>
+  __device__ __forceinline__ void get(int i, long long row, const Columns<ORDER, E>& c, f2 (&r)[E / 2]) const {
+    row_values<T, RING>(base[i], row, stride[i], at + stage * stage_bytes + off[i], M, c, r);
   }
 };
 
-// N sums over the threads of a row at once, the same in each of them.  Rows of up to 32
-// threads stay within a warp; a wider one has its block to itself and goes through shared
+// One or two sums over the threads of a row at once, the same in each of them.  Rows of up to
+// 32 threads stay within a warp; a wider one has its block to itself and goes through shared
 // memory, two buffers in turn so that one barrier does: whoever writes a buffer again has
 // passed the other one's barrier, which everyone reached after reading the first.
+// Two sums share the shuffles: after the first each half of a warp has one of them.
 template <bool WIDE, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2][64], int& turn) {
+__device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2][32], int& turn) {
   static_assert(N <= 2, "");
-  auto over_lanes = [&](int most) {
+  if constexpr (!WIDE) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      if (WIDE || o < most) {
+      if (o < tpr) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
       }
-  };
-  over_lanes(tpr);
-  if constexpr (WIDE) {
+  } else {
     float* buf = bufs[turn];
     turn ^= 1;
-    const int lane = threadIdx.x % 32;
-    if (lane == 0) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const bool up = lane & 16;
+    auto half = [&](float x) {   // over the 16 lanes
 #pragma unroll
-      for (int i = 0; i < N; ++i) buf[i * 32 + threadIdx.x / 32] = v[i];
-    }
+      for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      return x;
+    };
+    float x;
+    if constexpr (N == 2) x = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    else x = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    x = half(x);
+    if (lane % 16 == 0 && (N == 2 || !up)) buf[(up ? 16 : 0) + warp] = x;
     __syncthreads();
+    // 16 warps at most: a sum's parts are one half's
+    x = (lane & 15) * 32 < tpr && (N == 2 || !up) ? buf[lane] : 0.f;
+    x = half(x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane * 32 < tpr ? buf[i * 32 + lane] : 0.f;
-    over_lanes(32);
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, 16 * i);
   }
 }
 
@@ -292,21 +312,22 @@ struct RingLayout {
 
 constexpr int kNarrow = 128;   // threads of a block whose rows are up to 32 threads each
 
-template <int N, int VEC, int E>
+template <int N, int ORDER, int E>
 __device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages], const RingLayout& l,
-                                      const Columns<VEC, E>& c, long long row, long long step, int M) {
+                                      const Columns<ORDER, E>& c, long long row, long long step, int M) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   ring.full = bars;
   ring.at = umma::smem_u32(dynamic);
   ring.stage_bytes = l.stage_bytes;
   ring.stages = l.stages;
+  ring.M = M;
   ring.stage = 0, ring.parity = 0, ring.lost = false;
   uint32_t at = 0;
   int there = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     ring.off[i] = at;
-    if (ring.base[i]) at += (c.D * ring.es[i] + 15) / 16 * 16, ++there;
+    if (ring.base[i]) at += copy_bytes(c.D, ring.es[i]), ++there;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) umma::mbar_init(ring.full + i, there);
@@ -314,26 +335,28 @@ __device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages
   }
   __syncthreads();
   if (threadIdx.x % 32 == 0)
-    for (int i = 0; i < l.stages && row + i * step < M; ++i) ring.issue(threadIdx.x / 32, row + i * step, i, c.D);
+    for (int i = 0; i < l.stages && row + i * step < M; ++i) ring.issue(threadIdx.x / 32, row + i * step, i, c.D, c.phase());
 }
 
+__device__ __forceinline__ int phase_of(long long row, int D) { return static_cast<int>(row * D & 7); }
+
 // THREADS: kNarrow, or the largest block that the kernel is built for; BLOCKS of them on an SM.
-template <typename TA, typename TH, int VEC, int E, int THREADS, int BLOCKS>
+template <typename TA, typename TH, int ORDER, int E, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
-  constexpr bool WIDE = THREADS != kNarrow;
+  constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart;
   constexpr int P = E / 2;
   using Row = f2[P];
-  __shared__ float buf[2][64];
+  __shared__ float buf[2][32];
   __shared__ uint64_t bars[kMaxStages];
   int turn = 0;
-  const Columns<VEC, E> c{a.D, tpr, WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % tpr};
-  const int rows = WIDE ? 1 : kNarrow / tpr;
+  const int rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
   const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
+  const Columns<ORDER, E> c{a.D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, a.D)};
   Ring<3> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s;
   ring.es[0] = sizeof(TH), ring.es[1] = ring.es[2] = sizeof(TA);
-  if (WIDE) start(ring, bars, l, c, first, step, a.M);
+  if (RING) start(ring, bars, l, c, first, step, a.M);
   Row ws, wy;   // scale post_w; pre_w
   fill(ws, 1.f), fill(wy, 1.f);
   if (a.pre_w) load_vector(a.pre_w, c, wy);
@@ -343,19 +366,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
     load_vector(a.post_w, c, w);
     pairs<P>([&](int i) { ws[i] = mul2(ws[i], w[i]); });
   }
-  long long row = first + (WIDE ? 0 : threadIdx.x / tpr);
+  long long row = first + slot;
   // rows of other slots of the same warp may end earlier: those go on with zeros
   for (long long r0 = first; r0 < a.M; r0 += step, row += step) {
     const bool live = WIDE || row < a.M;
     Row h, u, f;
     if (!WIDE) fill(h, 0.f), fill(u, 0.f), fill(f, 0.f);
-    if (WIDE) ring.wait();
+    if (RING) ring.wait();
     if (live) {
-      if (a.branch) ring.template get<TA, WIDE>(1, row, c, u);
-      ring.template get<TH, WIDE>(0, row, c, h);
+      if (a.branch) ring.template get<TA, RING>(1, row, c, u);
+      ring.template get<TH, RING>(0, row, c, h);
       if (a.gate) {
         Row z, none;
-        ring.template get<TA, WIDE>(2, row, c, z);
+        ring.template get<TA, RING>(2, row, c, z);
         gate_of<false>(a.gate_act, z, f, none);
       }
     }
@@ -374,34 +397,34 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
       float s[1] = {dot(h, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      if (WIDE) ring.refill(row, first, step, a.M, a.D);
+      if (RING) ring.refill(row, first, step, a.D, c.phase());
       pairs<P>([&](int i) { h[i] = mul2(h[i], mul2(both(rstd), wy[i])); });
       if (live) store_row(static_cast<TA*>(a.y) + row * a.D, c, h);
-    } else if (WIDE) {
+    } else if (RING) {
       __syncthreads();
-      ring.refill(row, first, step, a.M, a.D);
+      ring.refill(row, first, step, a.D, c.phase());
     }
-    if (WIDE) ring.next();
+    if (RING) ring.next();
   }
-  if (WIDE) ring.drain();
+  if (RING) ring.drain();
 }
 
-template <typename TA, typename TH, int VEC, int E, int THREADS, int BLOCKS>
+template <typename TA, typename TH, int ORDER, int E, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
-  constexpr bool WIDE = THREADS != kNarrow;
+  constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart;
   constexpr int P = E / 2;
   using Row = f2[P];
-  __shared__ float buf[2][64];
+  __shared__ float buf[2][32];
   __shared__ uint64_t bars[kMaxStages];
   int turn = 0;
-  const Columns<VEC, E> c{a.D, tpr, WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % tpr};
   const int D = a.D, rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
   const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
+  const Columns<ORDER, E> c{D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, D)};
   Ring<5> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate, ring.base[3] = a.d_y, ring.base[4] = a.d_h;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s, ring.stride[3] = ring.stride[4] = D;
   ring.es[0] = ring.es[4] = sizeof(TH), ring.es[1] = ring.es[2] = ring.es[3] = sizeof(TA);
-  if (WIDE) start(ring, bars, l, c, first, step, a.M);
+  if (RING) start(ring, bars, l, c, first, step, a.M);
   Row sum_s, sum_p, ws, wy;   // S, the sum of dpre_w; scale post_w, pre_w
   fill(sum_s, 0.f), fill(sum_p, 0.f), fill(ws, 1.f), fill(wy, 1.f);
   if (a.pre_w) load_vector(a.pre_w, c, wy);
@@ -418,29 +441,31 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
     Row h, v, f, vs, g;   // vs: v f'(gate)
     float rstd_b = 1.f;
     if (!WIDE) fill(h, 0.f), fill(v, 0.f);
-    if (WIDE) ring.wait();
-    if (live) ring.template get<TH, WIDE>(0, row, c, h);
+    if (RING) ring.wait();
+    if (live) ring.template get<TH, RING>(0, row, c, h);
     if (a.branch) {   // h' again
-      if (live) ring.template get<TA, WIDE>(1, row, c, v);
+      if (live) ring.template get<TA, RING>(1, row, c, v);
       if (a.post_norm) {
         float s[1] = {dot(v, v)};
         row_sums<WIDE>(s, tpr, buf, turn);
         rstd_b = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
         pairs<P>([&](int i) { v[i] = mul2(v[i], both(rstd_b)); });
       }
-      fill(f, 1.f), fill(vs, 0.f);
-      if (a.gate && live) {
+      if (a.gate) {
         Row z;
-        ring.template get<TA, WIDE>(2, row, c, z);
+        if (!WIDE) fill(z, 0.f);
+        if (live) ring.template get<TA, RING>(2, row, c, z);
         gate_of<true>(a.gate_act, z, f, vs);
         pairs<P>([&](int i) { vs[i] = mul2(vs[i], v[i]); });
+      } else {
+        fill(f, 1.f);
       }
       pairs<P>([&](int i) { h[i] = fma2(mul2(f[i], v[i]), ws[i], h[i]); });
     }
     if (a.d_y) {
       Row dy, t;
       if (!WIDE) fill(dy, 0.f);
-      if (live) ring.template get<TA, WIDE>(3, row, c, dy);
+      if (live) ring.template get<TA, RING>(3, row, c, dy);
       pairs<P>([&](int i) { t[i] = mul2(dy[i], wy[i]); });
       float s[2] = {dot(h, h), dot(t, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
@@ -453,23 +478,23 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       });
       if (a.d_h) {
         if (!WIDE) fill(g, 0.f);
-        if (live) ring.template get<TH, WIDE>(4, row, c, g);
+        if (live) ring.template get<TH, RING>(4, row, c, g);
         pairs<P>([&](int i) { g[i] = add2(g[i], t[i]); });
       } else {
         pairs<P>([&](int i) { g[i] = t[i]; });
       }
     } else {
       if (!WIDE) fill(g, 0.f);
-      if (live) ring.template get<TH, WIDE>(4, row, c, g);
-      if (WIDE) __syncthreads();
+      if (live) ring.template get<TH, RING>(4, row, c, g);
+      if (RING) __syncthreads();
     }
-    if (WIDE) ring.refill(row, first, step, a.M, D), ring.next();
+    if (RING) ring.refill(row, first, step, D, c.phase()), ring.next();
     if (live && a.dh) store_row(static_cast<TH*>(a.dh) + row * D, c, g);
     if (!a.branch) continue;
     pairs<P>([&](int i) {
       const f2 x = mul2(g[i], ws[i]);
       sum_s[i] = fma2(g[i], mul2(f[i], v[i]), sum_s[i]);
-      vs[i] = mul2(x, vs[i]);
+      if (a.gate) vs[i] = mul2(x, vs[i]);
       g[i] = mul2(x, f[i]);   // q from here on
     });
     if (live && a.dg) store_row(static_cast<TA*>(a.dg) + row * D, c, vs);
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
     }
     if (live && a.db) store_row(static_cast<TA*>(a.db) + row * D, c, g);
   }
-  if (WIDE) ring.drain();
+  if (RING) ring.drain();
   if (!a.part) return;
   float ss[E], sp[E];
   pairs<P>([&](int i) {
@@ -493,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int n = c.at(e);
-      if (n < D) to[n] = ss[e], to[D + n] = sp[e];
+      if (c.in(n)) to[n] = ss[e], to[D + n] = sp[e];
     }
   };
   if constexpr (WIDE) {
@@ -534,33 +559,38 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int 
   if (d_post) d_post[c] = scale ? s * scale[c] : s;
 }
 
-bool vectors(const BlockNormArgs& a, int es_a, int es_h) {
-  auto ok = [](const void* p, long long s, int es) { return !p || ((reinterpret_cast<uintptr_t>(p) | (s * es)) & 15) == 0; };
-  return a.D % 8 == 0 && ok(a.h, a.h_s, es_h) && ok(a.branch, a.b_s, es_a) && ok(a.gate, a.g_s, es_a) &&
-         ok(a.h_out, 0, es_h) && ok(a.y, 0, es_a) && ok(a.scale, 0, 4) && ok(a.post_w, 0, 4) && ok(a.pre_w, 0, 4) &&
-         ok(a.d_h, 0, es_h) && ok(a.d_y, 0, es_a) && ok(a.dh, 0, es_h) && ok(a.db, 0, es_a) && ok(a.dg, 0, es_a);
+// Do all rows start at multiples of 8 values of tensors on 16 bytes, or all equally far from
+// one?  (Contiguous tensors of any row length do.)
+int order_of(const BlockNormArgs& a) {
+  auto ok = [&](const void* p, long long s) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (a.M == 1 || ((s - a.D) % 8 == 0 && (s >= a.D || a.D % 8 == 0))));
+  };
+  const bool groups = ok(a.h, a.h_s) && ok(a.branch, a.b_s) && ok(a.gate, a.g_s) && ok(a.h_out, a.D) && ok(a.y, a.D) &&
+                      ok(a.d_h, a.D) && ok(a.d_y, a.D) && ok(a.dh, a.D) && ok(a.db, a.D) && ok(a.dg, a.D);
+  return !groups || (a.D % 8 && a.D + 7 > kMaxRow) ? kApart : a.D % 8 ? kOdd : kEven;
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-template <typename F> void by_type(int dtype, int h_dtype, bool vec, F&& go) {
+template <typename F> void by_type(int dtype, int h_dtype, int order, F&& go) {
   auto types = [&](auto v) {
     if (dtype == DR_FP32) go(float{}, float{}, v);
     else if (h_dtype == DR_FP32) go(__nv_bfloat16{}, float{}, v);
     else go(__nv_bfloat16{}, __nv_bfloat16{}, v);
   };
-  if (vec) types(Int<8>{});
-  else types(Int<1>{});
+  if (order == kEven) types(Int<kEven>{});
+  else if (order == kOdd) types(Int<kOdd>{});
+  else types(Int<kApart>{});
 }
 
-// A launch: blocks that stay on every SM, and the rows on their way in what each of them has of
-// its shared memory.
+// A launch: blocks that stay on every SM, in the place of `threads`, and the rows on their way
+// in what each of them has of its shared memory.
 struct Plan {
   int tpr, threads, grid;
   RingLayout ring;
   size_t smem;
-  Plan(const BlockNormArgs& a, int sms, int e, int blocks, int row_bytes, bool sums) {
-    const int n = (a.D + e - 1) / e;
+  Plan(const BlockNormArgs& a, int sms, int order, int e, int place, int row_bytes, bool sums) {
+    const int n = (a.D + (order == kOdd ? 7 : 0) + e - 1) / e;   // with the most that a phase adds
     int rows = 1;
     smem = 0;
     if (n <= 32) {
@@ -568,13 +598,16 @@ struct Plan {
       rows = kNarrow / tpr, threads = kNarrow;
       if (sums) smem = sizeof(float) * rows * 2 * a.D;
     } else {
-      tpr = threads = (n + 31) / 32 * 32;
-      if (threads < 32 * 5) threads = tpr = 32 * 5;   // a warp for each tensor's copies
+      tpr = (n + 31) / 32 * 32;
+      if (tpr < 32 * 5) tpr = 32 * 5;   // a warp for each tensor's copies
+      threads = tpr;
     }
+    const int blocks = place / threads;
     const long long most = (a.M + rows - 1LL) / rows, there = (long long)sms * blocks;
     grid = static_cast<int>(most < there ? most : there);
+    if (order == kOdd && grid < most) grid = grid / 8 * 8;   // a block's rows have one phase
     ring.stage_bytes = row_bytes, ring.stages = 1;
-    if (n > 32) {
+    if (n > 32 && order != kApart) {
       const long long fit = ((224 * 1024) / blocks - 2048) / row_bytes, need = (most + grid - 1) / (grid ? grid : 1);
       ring.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
       if (ring.stages > need) ring.stages = static_cast<int>(need);
@@ -585,7 +618,7 @@ struct Plan {
 };
 
 int row_bytes(const BlockNormArgs& a, int es_a, int es_h) {
-  auto of = [&](const void* p, int es) { return p ? (a.D * es + 15) / 16 * 16 : 0; };
+  auto of = [&](const void* p, int es) { return p ? copy_bytes(a.D, es) : 0; };
   return of(a.h, es_h) + of(a.branch, es_a) + of(a.gate, es_a) + of(a.d_y, es_a) + of(a.d_h, es_h);
 }
 
@@ -598,14 +631,17 @@ template <typename K> cudaError_t launch(K* kernel, const Plan& p, const BlockNo
   return cudaGetLastError();
 }
 
-// Columns per thread, the largest block and the blocks on an SM, by the row's length.
-template <typename F> void fwd_shape(int D, F&& go) {
+// Columns per thread, the largest block and how many of them an SM's registers hold, by the
+// row's length.
+template <typename F> void fwd_shape(int D, int order, F&& go) {
+  D += order == kOdd ? 7 : 0;
   if (D <= 256) go(Int<8>{}, Int<kNarrow>{}, Int<8>{});
-  else if (D <= 2048) go(Int<8>{}, Int<256>{}, Int<4>{});
+  else if (D <= 2048) go(Int<8>{}, Int<256>{}, Int<3>{});
   else if (D <= 4096) go(Int<16>{}, Int<256>{}, Int<2>{});
   else go(Int<16>{}, Int<512>{}, Int<1>{});
 }
-template <typename F> void bwd_shape(int D, F&& go) {
+template <typename F> void bwd_shape(int D, int order, F&& go) {
+  D += order == kOdd ? 7 : 0;
   if (D <= 256) go(Int<8>{}, Int<kNarrow>{}, Int<4>{});
   else if (D <= 2048) go(Int<8>{}, Int<256>{}, Int<2>{});
   else if (D <= 4096) go(Int<8>{}, Int<512>{}, Int<1>{});
@@ -614,20 +650,25 @@ template <typename F> void bwd_shape(int D, F&& go) {
 
 }  // namespace
 
+// the most that any order of the columns takes
 int block_norm_bwd_blocks(const BlockNormArgs& a, int sms) {
   int n = 0;
-  bwd_shape(a.D, [&](auto e, auto, auto blocks) { n = Plan(a, sms, e, blocks, 16, false).grid; });
+  for (int order : {kEven, kOdd, kApart})
+    bwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
+      const int g = Plan(a, sms, order, e, threads * blocks, 16, false).grid;
+      n = n > g ? n : g;
+    });
   return n;
 }
 
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, cudaStream_t st) {
-  const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2;
+  const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2, order = order_of(a);
   cudaError_t err = cudaSuccess;
-  by_type(dtype, h_dtype, vectors(a, es_a, es_h), [&](auto ta, auto th, auto v) {
-    fwd_shape(a.D, [&](auto e, auto threads, auto blocks) {
-      err = launch(block_norm_fwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(e)::value,
+  by_type(dtype, h_dtype, order, [&](auto ta, auto th, auto o) {
+    fwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
+      err = launch(block_norm_fwd_kernel<decltype(ta), decltype(th), decltype(o)::value, decltype(e)::value,
                                          decltype(threads)::value, decltype(blocks)::value>,
-                   Plan(a, sms, e, blocks, row_bytes(a, es_a, es_h), false), a, st);
+                   Plan(a, sms, order, e, threads * blocks, row_bytes(a, es_a, es_h), false), a, st);
     });
   });
   return err;
@@ -635,14 +676,14 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype, int sms, float* d_scale, float* d_post,
                                   float* d_pre, cudaStream_t st) {
-  const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2;
+  const int es_a = dtype == DR_FP32 ? 4 : 2, es_h = h_dtype == DR_FP32 ? 4 : 2, order = order_of(a);
   cudaError_t err = cudaSuccess;
   int grid = 0;
-  by_type(dtype, h_dtype, vectors(a, es_a, es_h), [&](auto ta, auto th, auto v) {
-    bwd_shape(a.D, [&](auto e, auto threads, auto blocks) {
-      const Plan p(a, sms, e, blocks, row_bytes(a, es_a, es_h), a.part != nullptr);
+  by_type(dtype, h_dtype, order, [&](auto ta, auto th, auto o) {
+    bwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
+      const Plan p(a, sms, order, e, threads * blocks, row_bytes(a, es_a, es_h), a.part != nullptr);
       grid = p.grid;
-      err = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(v)::value, decltype(e)::value,
+      err = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(o)::value, decltype(e)::value,
                                          decltype(threads)::value, decltype(blocks)::value>,
                    p, a, st);
     });

@@ -32,27 +32,45 @@ __all__ = ["linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd"]
 
 _SLOPES = {torch.bfloat16: torch.float16, torch.float32: torch.float32}
 _FP32 = torch.float32
+_empty, _empty_like = torch.empty, torch.empty_like
 
+
+# A call is a few microseconds of GPU work: what follows spends its time on the usual case.
 
 def _given_or_new(t, name, shape, dtype, like, dev):
+    """A contiguous tensor; ``like`` is on device dev."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        if like.shape == shape and like.dtype is dtype and like.is_contiguous():
+            return _empty_like(like)
+        return _empty(shape, dtype=dtype, device=like.device)
     check(t, name, shape, dtype, dev)
     return t
 
 
 def _rows(t, name):
     """(rows, row stride) of a tensor of 2 or 3 dimensions as one list of rows."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 2:
-        return shape[0], stride[0]
+        return shape[0], t.stride(0)
     B, T = shape[0], shape[1]
-    if B == 1 or stride[0] == T * stride[1]:
-        return B * T, stride[1]
+    sb, st, _ = t.stride()
+    if B == 1 or sb == T * st:
+        return B * T, st
     if T == 1:
-        return B, stride[0]
-    raise ValueError(f"{name} must step evenly over its rows: batch stride {stride[0]} is not "
-                     f"{T} tokens of {stride[1]}")
+        return B, sb
+    raise ValueError(f"{name} must step evenly over its rows: batch stride {sb} is not "
+                     f"{T} tokens of {st}")
+
+
+def _row_stride(t, name, shape, dtype, dev):
+    """As ``check_rows``, and the row stride."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return shape[-1]
+    except AttributeError:
+        pass
+    check_rows(t, name, shape, dtype, dev)
+    return _rows(t, name)[1]
 
 
 def _act(name, what):
@@ -62,9 +80,18 @@ def _act(name, what):
     return code
 
 
-def _dims(t):
+def _first(t, name):
+    """(dr_dtype, device, rows, row stride) of a call's first tensor."""
+    try:
+        code, dev, shape = DTYPES[t.dtype], t.get_device(), t.shape
+        if dev >= 0 and t.is_contiguous() and 2 <= len(shape) <= 3:
+            D = shape[-1]
+            return code, dev, shape[0] if len(shape) == 2 else shape[0] * shape[1], D
+    except (AttributeError, KeyError):
+        pass
     d = t.dim() if torch.is_tensor(t) else 2
-    return d if d == 3 else 2
+    code, dev = activations(t, name, d if d == 3 else 2)
+    return code, dev, *_rows(t, name)
 
 
 # ------------------------------------------------------------------ matrix product
@@ -72,12 +99,12 @@ def _dims(t):
 def _linear(x, weight, act):
     """The call's dr_linear and its device, its tensors checked; a weight [K,N] may be the
     transpose of a matrix [N,K] (``w.t()``)."""
-    code, dev = activations(x, "x", _dims(x))
+    code, dev, M, xs = _first(x, "x")
     if not torch.is_tensor(weight) or weight.dim() != 2 or weight.shape[0] != x.shape[-1]:
         raise ValueError(f"weight must be a tensor [{x.shape[-1]}, N]")
     K, N = weight.shape
     s0, s1 = weight.stride()
-    if weight.dtype is not x.dtype or weight.device != x.device:
+    if weight.dtype is not x.dtype or weight.get_device() != dev:
         raise TypeError(f"weight must be {x.dtype} on {x.device}, got {weight.dtype} on {weight.device}")
     if s1 == 1 or N == 1 and s0 != 1:
         t, ws = 0, s0
@@ -85,7 +112,6 @@ def _linear(x, weight, act):
         t, ws = 1, s1
     else:
         raise ValueError("weight must have contiguous rows or contiguous columns")
-    M, xs = _rows(x, "x")
     return dr.DrLinear(code, _act(act, "act"), M, K, N, t, xs, ws, 0), dev
 
 
@@ -102,9 +128,8 @@ def linear_fwd(x, weight, bias=None, *, act="none", residual=None, want_slope=Fa
     if bias is not None:
         check(bias, "bias", (a.N,), x.dtype, dev)
     if residual is not None:
-        check_rows(residual, "residual", shape, x.dtype, dev)
-        a.r_s = _rows(residual, "residual")[1]
-    y = _given_or_new(y, "y", shape, x.dtype, x, dev)
+        a.r_s = _row_stride(residual, "residual", shape, x.dtype, dev)
+    y = _given_or_new(y, "y", shape, x.dtype, x if residual is None else residual, dev)
     if (want_slope or slope is not None) and a.act:
         slope = _given_or_new(slope, "slope", shape, _SLOPES[x.dtype], x, dev)
     else:
@@ -150,26 +175,26 @@ def linear_bwd(x, weight, d_y, *, slope=None, want_dx=True, want_dweight=True, w
 
 def _block_norm(h, branch, gate, gate_act, scale, post_norm, post_weight, pre_weight, eps, dtype):
     """The call's dr_block_norm, its device and the activations' type, its tensors checked."""
-    h_code, dev = activations(h, "h", _dims(h))
+    h_code, dev, M, hs = _first(h, "h")
+    shape, bs, gs = h.shape, 0, 0
+    D = shape[-1]
     if branch is not None:
-        if dtype is not None and torch.is_tensor(branch) and dtype is not branch.dtype:
-            raise TypeError(f"dtype {dtype} is not the branch's, {branch.dtype}")
-        code, _ = activations(branch, "branch", h.dim())
-        check_rows(branch, "branch", h.shape, branch.dtype, dev)
-        dtype = branch.dtype
+        kind = getattr(branch, "dtype", None)
+        if dtype is not None and kind is not None and dtype is not kind:
+            raise TypeError(f"dtype {dtype} is not the branch's, {kind}")
+        code = DTYPES.get(kind)
+        if code is None:
+            activations(branch, "branch", len(shape))
+        bs = _row_stride(branch, "branch", shape, kind, dev)
+        dtype = kind
     else:
         dtype = h.dtype if dtype is None else dtype
         code = DTYPES.get(dtype)
         if code is None:
             raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    M, hs = _rows(h, "h")
-    D = h.shape[-1]
-    a = dr.DrBlockNorm(code, h_code, M, D, bool(post_norm), _act(gate_act, "gate_act"), eps, hs, 0, 0)
-    if branch is not None:
-        a.b_s = _rows(branch, "branch")[1]
     if gate is not None:
-        check_rows(gate, "gate", h.shape, dtype, dev)
-        a.g_s = _rows(gate, "gate")[1]
+        gs = _row_stride(gate, "gate", shape, dtype, dev)
+    a = dr.DrBlockNorm(code, h_code, M, D, 1 if post_norm else 0, _act(gate_act, "gate_act"), eps, hs, bs, gs)
     for t, name in ((scale, "scale"), (post_weight, "post_weight"), (pre_weight, "pre_weight")):
         if t is not None:
             check(t, name, (D,), _FP32, dev)
@@ -187,7 +212,7 @@ def block_norm_fwd(h, branch=None, *, gate=None, gate_act="none", scale=None, po
     a, dev, dtype = _block_norm(h, branch, gate, gate_act, scale, post_norm, post_weight,
                                 pre_weight, eps, dtype)
     if want_y or y is not None:
-        y = _given_or_new(y, "y", h.shape, dtype, h, dev)
+        y = _given_or_new(y, "y", h.shape, dtype, h if branch is None else branch, dev)
     if branch is not None:
         h_out = _given_or_new(h_out, "h_out", h.shape, h.dtype, h, dev)
     elif h_out is not None:
@@ -222,7 +247,7 @@ def block_norm_bwd(h, branch=None, *, d_h=None, d_y=None, gate=None, gate_act="n
             ("dpost_weight", post_weight, vec, _FP32),
             ("dpre_weight", None if d_y is None else pre_weight, vec, _FP32)):
         if there is not None:
-            g[name] = _given_or_new(given.get(name), name, shape, kind, h, dev)
+            g[name] = _given_or_new(given.get(name), name, shape, kind, there, dev)
     ws, n = (scratch(dr.dr_block_norm_bwd_workspace_bytes, a, h, dev, workspace)
              if "dscale" in g or "dpost_weight" in g or "dpre_weight" in g else (None, 0))
     out = dr.DrBlockNormGrads(*(ptr(g.get(k)) for k in _GRADS))

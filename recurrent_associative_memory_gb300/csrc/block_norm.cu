@@ -61,54 +61,47 @@ struct RowCopy {
 // what a row's copy takes of shared memory
 __host__ __device__ __forceinline__ int copy_bytes(int D, int es) { return (D % 8 ? D / 8 + 2 : D / 8) * 8 * es; }
 
-// A thread's values of row `row`, from its copy at `at` in shared memory (RING), or from memory.
+// 8 of a thread's values of row `row`, from e on, from its copy at `at` in shared memory (RING), or from memory.
 template <typename T, bool RING, int ORDER, int E>
 __device__ __forceinline__ void row_values(const void* base, long long row, long long stride, uint32_t at, int M,
-                                           const Columns<ORDER, E>& c, f2 (&r)[E / 2]) {
-  float f[E];
+                                           const Columns<ORDER, E>& c, int e0, f2 (&r)[4]) {
+  float f[8];
   const T* p = static_cast<const T*>(base) + row * stride;
-  auto one = [&](int n) { return c.in(n) ? to_f(p[n]) : 0.f; };
-  if constexpr (ORDER != kApart) {
+  const int n = c.at(e0);
+  if constexpr (ORDER == kApart) {
 #pragma unroll
-    for (int g = 0; g < E; g += 8) {
-      const int n = c.at(g);
-      uint32_t w[2 * sizeof(T)];
-      // a ring's copy does not hold what lies behind the row (threads that have no columns), nor
-      // of the tensor's last row a group that is not whole
-      const bool apart = RING && ORDER == kOdd ? n >= c.D || (row == M - 1 && !c.whole(n)) : !c.whole(n);
-      if (apart) {
+    for (int e = 0; e < 8; ++e) f[e] = c.in(c.at(e0 + e)) ? to_f(p[c.at(e0 + e)]) : 0.f;
+  } else if (RING && ORDER == kOdd ? n >= c.D || (row == M - 1 && !c.whole(n)) : !c.whole(n)) {
+    // a ring's copy does not hold what lies behind the row (threads that have no columns), nor
+    // of the tensor's last row a group that is not whole
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[g + e] = ORDER == kEven ? 0.f : one(n + e);
-        continue;
-      }
+    for (int e = 0; e < 8; ++e) f[e] = ORDER != kEven && c.in(n + e) ? to_f(p[n + e]) : 0.f;
+  } else {
+    uint32_t w[2 * sizeof(T)];
 #pragma unroll
-      for (int i = 0; i < 2 * (int)sizeof(T); i += 4) {
-        if constexpr (RING) {
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                       : "r"(at + (n + c.phase()) * (int)sizeof(T) + 4 * i)
-                       : "memory");
-        } else {
-          const uint4 u = reinterpret_cast<const uint4*>(p + n)[i / 4];
-          w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (sizeof(T) == 2) f[g + e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-        else f[g + e] = __uint_as_float(w[e]);
-      }
-      if (RING && ORDER == kOdd && !c.whole(n)) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[g + e] = c.in(n + e) ? f[g + e] : 0.f;
+    for (int i = 0; i < 2 * (int)sizeof(T); i += 4) {
+      if constexpr (RING) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                     : "r"(at + (n + c.phase()) * (int)sizeof(T) + 4 * i)
+                     : "memory");
+      } else {
+        const uint4 u = reinterpret_cast<const uint4*>(p + n)[i / 4];
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
       }
     }
-  } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = one(c.at(e));
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 2) f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+      else f[e] = __uint_as_float(w[e]);
+    }
+    if (RING && ORDER == kOdd && !c.whole(n)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = c.in(n + e) ? f[e] : 0.f;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
 // Values in pairs: two fp32 operations per instruction, as instructions are what bounds these
@@ -129,39 +122,44 @@ template <int P, typename F> __device__ __forceinline__ void pairs(F&& f) {
   for (int i = 0; i < P; ++i) f(i);
 }
 
-template <int ORDER, int E> __device__ __forceinline__ void load_vector(const float* p, const Columns<ORDER, E>& c, f2 (&r)[E / 2]) {
-  float f[E];
+// The same 8 of a vector over the channels, on any address.
+template <int ORDER, int E>
+__device__ __forceinline__ void load_vector(const float* p, const Columns<ORDER, E>& c, int e0, f2 (&r)[4]) {
+  float f[8];
+  if (ORDER != kApart && c.whole(c.at(e0)) && (reinterpret_cast<uintptr_t>(p + c.at(e0)) & 15) == 0) {
+    load8(p + c.at(e0), 1, f);
+  } else {
 #pragma unroll
-  for (int g = 0; g < E; g += 8) {
-    if constexpr (ORDER == kEven) {
-      const bool in = c.at(g) < c.D;   // on any address
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[g + e] = in ? p[c.at(g) + e] : 0.f;
-    } else {
-#pragma unroll
-      for (int e = g; e < g + 8; ++e) f[e] = c.in(c.at(e)) ? p[c.at(e)] : 0.f;
-    }
+    for (int e = 0; e < 8; ++e) f[e] = c.in(c.at(e0 + e)) ? p[c.at(e0 + e)] : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) r[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
 template <typename T, int ORDER, int E>
-__device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, const f2 (&r)[E / 2]) {
-  float f[E];
+__device__ __forceinline__ void store_group(T* p, const Columns<ORDER, E>& c, int e0, const f2 (&r)[4]) {
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) unpack2(r[i], f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) unpack2(r[i], f[2 * i], f[2 * i + 1]);
+  const int n = c.at(e0);
+  if (ORDER != kApart && c.whole(n)) {
+    store8(p + n, f);
+  } else if (ORDER != kEven) {
 #pragma unroll
-  for (int g = 0; g < E; g += 8) {
-    const int n = c.at(g);
-    if (ORDER != kApart && c.whole(n)) {
-      store8(p + n, reinterpret_cast<float(&)[8]>(f[g]));
-    } else if (ORDER != kEven) {
-#pragma unroll
-      for (int e = g; e < g + 8; ++e)
-        if (c.in(c.at(e))) p[c.at(e)] = from_f<T>(f[e]);
-    }
+    for (int e = 0; e < 8; ++e)
+      if (c.in(c.at(e0 + e))) p[c.at(e0 + e)] = from_f<T>(f[e]);
   }
+}
+
+// All E of them.
+template <int ORDER, int E> __device__ __forceinline__ void load_vector(const float* p, const Columns<ORDER, E>& c, f2 (&r)[E / 2]) {
+#pragma unroll
+  for (int g = 0; g < E; g += 8) load_vector(p, c, g, reinterpret_cast<f2(&)[4]>(r[g / 2]));
+}
+template <typename T, int ORDER, int E>
+__device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, const f2 (&r)[E / 2]) {
+#pragma unroll
+  for (int g = 0; g < E; g += 8) store_group(p, c, g, reinterpret_cast<const f2(&)[4]>(r[g / 2]));
 }
 
 // The rows of a block.  RING: one at a time, through a ring of `stages` of them in shared
@@ -221,8 +219,13 @@ template <int N> struct Ring {
     }
   }
   template <typename T, bool RING, int ORDER, int E>
+  __device__ __forceinline__ void get(int i, long long row, const Columns<ORDER, E>& c, int e0, f2 (&r)[4]) const {
+    row_values<T, RING>(base[i], row, stride[i], at + stage * stage_bytes + off[i], M, c, e0, r);
+  }
+  template <typename T, bool RING, int ORDER, int E>
   __device__ __forceinline__ void get(int i, long long row, const Columns<ORDER, E>& c, f2 (&r)[E / 2]) const {
-    row_values<T, RING>(base[i], row, stride[i], at + stage * stage_bytes + off[i], M, c, r);
+#pragma unroll
+    for (int g = 0; g < E; g += 8) get<T, RING>(i, row, c, g, reinterpret_cast<f2(&)[4]>(r[g / 2]));
   }
 };
 
@@ -409,9 +412,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
   if (RING) ring.drain();
 }
 
+// Two rows of all five tensors have to fit an SM's shared memory.  With fp32 among them, rows of
+// more than 4096 columns (16 per thread) would not: those are read from memory.
+template <typename TH, int E> __host__ __device__ constexpr bool ring_holds() { return sizeof(TH) == 2 || E == 8; }
+
 template <typename TA, typename TH, int ORDER, int E, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
-  constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart;
+  constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart && ring_holds<TH, E>();
   constexpr int P = E / 2;
   using Row = f2[P];
   __shared__ float buf[2][32];
@@ -536,27 +543,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   }
 }
 
-// The sums over the blocks of part[block][which][D], 8 groups of threads over the blocks, joined
+// The sums over the blocks of part[block][which][D], 32 groups of threads over the blocks, joined
 // in order: which 0 is S, of dscale and dpost_w, 1 is dpre_w.
-__global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int blocks, int D, const float* scale,
-                                                         const float* post_w, float* d_scale, float* d_post, float* d_pre) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(1024) join_parts_kernel(const float* part, int blocks, int D, const float* scale,
+                                                          const float* post_w, float* d_scale, float* d_post, float* d_pre) {
+  __shared__ float buf[32][33];
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32, which = blockIdx.y;
   if (which == 0 ? !d_scale && !d_post : !d_pre) return;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < D)
-    for (int b = g; b < blocks; b += 8) s += part[((long long)b * 2 + which) * D + c];
+    for (int b = g; b < blocks; b += 32) s += part[((long long)b * 2 + which) * D + c];
   buf[g][lane] = s;
   __syncthreads();
-  if (g != 0 || c >= D) return;
-  for (int i = 1; i < 8; ++i) s += buf[i][lane];
+  s = buf[lane][g];   // a warp per column now
+  s = warp_sum(s);
+  const int n = blockIdx.x * 32 + g;
+  if (lane != 0 || n >= D) return;
   if (which == 1) {
-    d_pre[c] = s;
+    d_pre[n] = s;
     return;
   }
-  if (d_scale) d_scale[c] = post_w ? s * post_w[c] : s;
-  if (d_post) d_post[c] = scale ? s * scale[c] : s;
+  if (d_scale) d_scale[n] = post_w ? s * post_w[n] : s;
+  if (d_post) d_post[n] = scale ? s * scale[n] : s;
 }
 
 // Do all rows start at multiples of 8 values of tensors on 16 bytes, or all equally far from
@@ -583,35 +592,37 @@ template <typename F> void by_type(int dtype, int h_dtype, int order, F&& go) {
   else types(Int<kApart>{});
 }
 
-// A launch: blocks that stay on every SM, in the place of `threads`, and the rows on their way
-// in what each of them has of its shared memory.
+// A launch: blocks that stay on every SM, in the place of `place` threads, and the rows on their
+// way in what each of them has of its shared memory, two at least (a row's place goes to the
+// next but one while the next is worked on); for that fewer blocks share an SM.
 struct Plan {
   int tpr, threads, grid;
   RingLayout ring;
   size_t smem;
-  Plan(const BlockNormArgs& a, int sms, int order, int e, int place, int row_bytes, bool sums) {
+  Plan(const BlockNormArgs& a, int sms, int order, int e, int place, bool with_ring, int row_bytes, bool sums) {
     const int n = (a.D + (order == kOdd ? 7 : 0) + e - 1) / e;   // with the most that a phase adds
     int rows = 1;
-    smem = 0;
     if (n <= 32) {
       for (tpr = 4; tpr < n; tpr *= 2) {}
       rows = kNarrow / tpr, threads = kNarrow;
-      if (sums) smem = sizeof(float) * rows * 2 * a.D;
     } else {
       tpr = (n + 31) / 32 * 32;
       if (tpr < 32 * 5) tpr = 32 * 5;   // a warp for each tensor's copies
       threads = tpr;
     }
-    const int blocks = place / threads;
+    with_ring = with_ring && n > 32 && order != kApart;
+    int blocks = place / threads;
+    auto fit = [&] { return ((224 * 1024) / blocks - 2048) / row_bytes; };
+    while (with_ring && blocks > 1 && fit() < 2) --blocks;
     const long long most = (a.M + rows - 1LL) / rows, there = (long long)sms * blocks;
     grid = static_cast<int>(most < there ? most : there);
     if (order == kOdd && grid < most) grid = grid / 8 * 8;   // a block's rows have one phase
-    ring.stage_bytes = row_bytes, ring.stages = 1;
-    if (n > 32 && order != kApart) {
-      const long long fit = ((224 * 1024) / blocks - 2048) / row_bytes, need = (most + grid - 1) / (grid ? grid : 1);
-      ring.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
+    ring.stage_bytes = row_bytes, ring.stages = 0;
+    smem = sums && n <= 32 ? sizeof(float) * rows * 2 * a.D : 0;   // the block's rows' sums
+    if (with_ring && grid) {
+      const long long need = (most + grid - 1) / grid;
+      ring.stages = fit() < kMaxStages ? fit() : kMaxStages;
       if (ring.stages > need) ring.stages = static_cast<int>(need);
-      if (ring.stages < 1) ring.stages = 1;
       smem = (size_t)ring.stages * row_bytes;
     }
   }
@@ -655,7 +666,7 @@ int block_norm_bwd_blocks(const BlockNormArgs& a, int sms) {
   int n = 0;
   for (int order : {kEven, kOdd, kApart})
     bwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
-      const int g = Plan(a, sms, order, e, threads * blocks, 16, false).grid;
+      const int g = Plan(a, sms, order, e, threads * blocks, false, 16, false).grid;
       n = n > g ? n : g;
     });
   return n;
@@ -668,7 +679,7 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, int dtype, int h_dtype
     fwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
       err = launch(block_norm_fwd_kernel<decltype(ta), decltype(th), decltype(o)::value, decltype(e)::value,
                                          decltype(threads)::value, decltype(blocks)::value>,
-                   Plan(a, sms, order, e, threads * blocks, row_bytes(a, es_a, es_h), false), a, st);
+                   Plan(a, sms, order, e, threads * blocks, true, row_bytes(a, es_a, es_h), false), a, st);
     });
   });
   return err;
@@ -681,7 +692,8 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype
   int grid = 0;
   by_type(dtype, h_dtype, order, [&](auto ta, auto th, auto o) {
     bwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
-      const Plan p(a, sms, order, e, threads * blocks, row_bytes(a, es_a, es_h), a.part != nullptr);
+      const Plan p(a, sms, order, e, threads * blocks, ring_holds<decltype(th), decltype(e)::value>(),
+                   row_bytes(a, es_a, es_h), a.part != nullptr);
       grid = p.grid;
       err = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(o)::value, decltype(e)::value,
                                          decltype(threads)::value, decltype(blocks)::value>,
@@ -689,7 +701,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype
     });
   });
   if (err != cudaSuccess || !a.part) return err;
-  join_parts_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, st>>>(a.part, grid, a.D, a.scale, a.post_w, d_scale, d_post, d_pre);
+  join_parts_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, st>>>(a.part, grid, a.D, a.scale, a.post_w, d_scale, d_post, d_pre);
   return cudaGetLastError();
 }
 

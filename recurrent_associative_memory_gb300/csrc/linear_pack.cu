@@ -106,19 +106,19 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* d_y, const S* slope
   if (n < N) part[rb * N + n] = s;
 }
 
+// db = the sums over the row blocks, 32 groups of threads over them
 template <typename T>
-__global__ void __launch_bounds__(256) join_bias_kernel(const float* part, int blocks, int N, T* db) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(1024) join_bias_kernel(const float* part, int blocks, int N, T* db) {
+  __shared__ float buf[32][33];
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32, n = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (n < N)
-    for (int b = g; b < blocks; b += 8) s += part[(long long)b * N + n];
+    for (int b = g; b < blocks; b += 32) s += part[(long long)b * N + n];
   buf[g][lane] = s;
   __syncthreads();
-  if (g == 0 && n < N) {
-    for (int i = 1; i < 8; ++i) s += buf[i][lane];
-    db[n] = from_f<T>(s);
-  }
+  s = warp_sum(buf[lane][g]);   // a warp per column now
+  const int m = blockIdx.x * 32 + g;
+  if (lane == 0 && m < N) db[m] = from_f<T>(s);
 }
 
 template <typename T>
@@ -151,12 +151,12 @@ cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int p
   if (dtype == DR_FP32) {
     auto* k = vec ? slope_kernel<float, float, true> : slope_kernel<float, float, false>;
     k<<<grid, 256, 0, st>>>(static_cast<const float*>(a.d_y), static_cast<const float*>(a.slope), d, pitch, piece, part, a.M, a.N);
-    if (part) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
+    if (part) join_bias_kernel<<<(a.N + 31) / 32, 1024, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
   } else {
     auto* k = vec ? slope_kernel<__nv_bfloat16, __half, true> : slope_kernel<__nv_bfloat16, __half, false>;
     k<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(a.d_y), static_cast<const __half*>(a.slope), d, pitch, piece,
                             part, a.M, a.N);
-    if (part) join_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
+    if (part) join_bias_kernel<<<(a.N + 31) / 32, 1024, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
   }
   return cudaGetLastError();
 }

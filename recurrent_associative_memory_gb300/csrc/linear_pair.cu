@@ -140,22 +140,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {   // rows on any address: a lane takes a column, and rows are stored one by one
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const int at = c + 16 * h + lane % 16, n = n0 + at;
+            const bool in = n < e.N;
+            const float b = FULL && in ? bias[at] : 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) turn[lane * 17 + i] = v[16 * h + i];
             __syncwarp();
-            const int at = c + 16 * h + lane % 16, n = n0 + at;
-            if (n < e.N) {
-              const float b = FULL ? bias[at] : 0.f;
-#pragma unroll 4
-              for (int i = lane / 16; i < 32 && m0 + i < e.M; i += 2) {
-                float x = turn[i * 17 + lane % 16] + b, s = 1.f;
-                if constexpr (FULL) {
-                  x = act_any(e.act, x, s);
-                  if (e.slope) static_cast<S*>(e.slope)[(m0 + i) * (long long)e.N + n] = static_cast<S>(s);
-                  if (e.res) x += to_f(static_cast<const T*>(e.res)[(m0 + i) * e.r_m + n]);
-                }
-                static_cast<T*>(e.C)[(m0 + i) * (long long)e.N + n] = from_f<T>(x);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {   // 8 rows at once, so that their loads are
+              float x[8], s[8], r[8];
+              const int m1 = m0 + 16 * q + lane / 16;
+              auto there = [&](int i) { return in && m1 + 2 * i < e.M; };
+              if (FULL && e.res) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = there(i) ? to_f(static_cast<const T*>(e.res)[(m1 + 2 * i) * e.r_m + n]) : 0.f;
               }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = turn[(16 * q + lane / 16 + 2 * i) * 17 + lane % 16] + b;
+              if constexpr (FULL) {
+                act_all(e.act, e.slope != nullptr, x, s);
+                if (e.slope) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (there(i)) static_cast<S*>(e.slope)[(m1 + 2 * i) * (long long)e.N + n] = static_cast<S>(s[i]);
+                }
+                if (e.res) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] += r[i];
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (there(i)) static_cast<T*>(e.C)[(m1 + 2 * i) * (long long)e.N + n] = from_f<T>(x[i]);
             }
             __syncwarp();
           }

@@ -208,16 +208,6 @@ __device__ __forceinline__ void load32(const void* p, uint32_t* v) {
                : "memory");
 }
 
-__device__ __forceinline__ float act_any(int act, float x, float& s) {
-  switch (act) {
-    case DR_ACT_RELU: return act_of<DR_ACT_RELU>(x, s);
-    case DR_ACT_SILU: return act_of<DR_ACT_SILU>(x, s);
-    case DR_ACT_GELU_TANH: return act_of<DR_ACT_GELU_TANH>(x, s);
-    case DR_ACT_SIGMOID: return act_of<DR_ACT_SIGMOID>(x, s);
-    default: s = 1.f; return x;
-  }
-}
-
 // f over n values, with their slopes or without
 template <int N> __device__ __forceinline__ void act_all(int act, bool want, float (&v)[N], float (&s)[N]) {
   auto with = [&](auto code) {

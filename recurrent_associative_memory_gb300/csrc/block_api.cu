@@ -27,6 +27,7 @@ constexpr long long kMaxBlocks = 0x7fffffffLL;  // of one launch
 template <typename... P> bool aligned(unsigned n, const P*... p) {
   return (((reinterpret_cast<uintptr_t>(p) | ...)) & (n - 1)) == 0;
 }
+unsigned bytes_of(int dtype) { return dtype == DR_FP32 ? 4 : 2; }
 bool dtype_ok(int t) { return t == DR_FP32 || t == DR_BF16; }
 bool act_ok(int t) { return t >= DR_ACT_NONE && t <= DR_ACT_SIGMOID; }
 cudaStream_t stream_of(dr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -90,7 +91,7 @@ int dr_linear_fwd(const dr_linear* a, const void* x, const void* weight, const v
   if (!a || !x || !weight || !y) return DR_ERR_NULL;
   int st = check_linear(a);
   if (st != DR_OK) return st;
-  if (!aligned(16, x, weight, residual, y, slope)) return DR_ERR_ALIGN;
+  if (!aligned(16, x, weight, residual, y, slope) || !aligned(bytes_of(a->dtype), bias)) return DR_ERR_ALIGN;
   const size_t need = dr_linear_fwd_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
@@ -112,7 +113,7 @@ int dr_linear_bwd(const dr_linear* a, const void* x, const void* weight, const v
   if (a->act != DR_ACT_NONE && !slope) return DR_ERR_NULL;
   int st = check_linear(a);
   if (st != DR_OK) return st;
-  if (!aligned(16, x, weight, d_y, slope, dx, d_weight)) return DR_ERR_ALIGN;
+  if (!aligned(16, x, weight, d_y, slope, dx, d_weight) || !aligned(bytes_of(a->dtype), d_bias)) return DR_ERR_ALIGN;
   const size_t need = dr_linear_bwd_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
@@ -132,6 +133,9 @@ int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch,
   if (!branch && (gate || scale || h_out || a->post_norm)) return DR_ERR_ARG;
   if ((post_weight && !a->post_norm) || (pre_weight && !y)) return DR_ERR_ARG;
   if (y == h || (h_out && y == h_out)) return DR_ERR_ARG;
+  if (!aligned(bytes_of(a->dtype), branch, gate, y) || !aligned(bytes_of(a->h_dtype), h, h_out) ||
+      !aligned(4, scale, post_weight, pre_weight))
+    return DR_ERR_ALIGN;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
   BlockNormArgs r = block_norm_args(a);
@@ -155,6 +159,9 @@ int dr_block_norm_bwd(const dr_block_norm* a, const void* h, const void* branch,
   if ((post_weight && !a->post_norm) || (g->dgate && !gate) || (g->dscale && !scale) || (g->dpost_weight && !post_weight) ||
       (g->dpre_weight && (!pre_weight || !d_y)))
     return DR_ERR_ARG;
+  if (!aligned(bytes_of(a->dtype), branch, gate, d_y, g->dbranch, g->dgate) || !aligned(bytes_of(a->h_dtype), h, d_h, g->dh) ||
+      !aligned(4, scale, post_weight, pre_weight, g->dscale, g->dpost_weight, g->dpre_weight))
+    return DR_ERR_ALIGN;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
   BlockNormArgs r = block_norm_args(a);

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* d_y, const S* slope
         if constexpr (sizeof(S) == 2) read8<VEC>(slope + m * N + c, N - c, s);
         else read8<S, VEC>(slope + m * N + c, N - c, s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= s[j];
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], s[j]);   // the same d, kept or only summed
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += f[j];

@@ -26,3 +26,9 @@ def test_a_prompt_is_not_changed_by_its_neighbours():
         alone, _ = model.prefill(tokens[b:b + 1, :n].contiguous(), lens[b:b + 1])
         ref = both[b, :n].float()
         assert float((alone[0].float() - ref).norm() / ref.norm()) < 4.7e-2
+
+
+def test_decoding_continues_the_prompt_with_channel_layers():
+    """Six layers and the unembedding: 3 (6 + 1) 2^-8 = 8.2e-2."""
+    from recurrent_associative_memory_gb300 import hybrid
+    assert hybrid.main(channels=3) < 8.2e-2

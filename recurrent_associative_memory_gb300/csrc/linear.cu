@@ -3,8 +3,7 @@
 
 namespace dr {
 
-cudaError_t launch_linear_pack(const void* src, long long stride, int rows, int cols, int dtype, void* dst, int pitch,
-                               long long piece, int sms, cudaStream_t st);
+cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, cudaStream_t st);
 int linear_slope_blocks(int M);
 cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int pitch, long long piece, float* part,
                                 cudaStream_t st);
@@ -38,11 +37,10 @@ struct Packed {
     piece = dtype == DR_FP32 ? (long long)rows * pitch : 0;
     bytes = copy ? round256((size_t)rows * pitch * (dtype == DR_FP32 ? 6 : 2)) : 0;
   }
-  cudaError_t make(const void*& p, void* to, int dtype, int sms, cudaStream_t st) {
-    if (!copy) return cudaSuccess;
-    cudaError_t e = launch_linear_pack(p, stride, rows, cols, dtype, to, pitch, piece, sms, st);
+  PackJob job(const void*& p, void* to) {   // p: where it is to be found from then on
+    const PackJob j{p, to, stride, piece, rows, cols, pitch};
     p = to, stride = pitch;
-    return e;
+    return j;
   }
   // k along the columns, or along the rows
   Operand k_cols(const void* p) const { return {p, rows, cols, stride, false, piece}; }
@@ -50,6 +48,16 @@ struct Packed {
 };
 
 Packed pack_x(const LinearArgs& a, int dtype) { return {dtype, a.M, a.K, a.x_s}; }
+// The copies that one or both of two matrices need.
+cudaError_t make(Packed* a, const void** pa, void* to_a, Packed* b, const void** pb, void* to_b, int dtype, int sms,
+                 cudaStream_t st) {
+  PackJob j[2]{};
+  int n = 0;
+  if (a && a->copy) j[n++] = a->job(*pa, to_a);
+  if (b && b->copy) j[n++] = b->job(*pb, to_b);
+  return n ? launch_linear_pack(j[0], j[1], dtype, sms, st) : cudaSuccess;
+}
+
 Packed pack_w(const LinearArgs& a, int dtype) { return {dtype, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, a.w_s}; }
 
 // Cycles of one 64-k step of a tile of m x n in an SM that holds `rows` rows of operands for it:
@@ -63,8 +71,8 @@ long long step_cycles(bool fp32, int m, int n, int rows) {
 
 // C[m,n] = sum over k of A[m,k] B[n,k], and its epilogue where `full`.
 // Which kernel: the one whose busiest SM needs the fewest cycles for its tiles, or for the
-// operands out of memory (3500 bytes a cycle), and for what a kernel costs besides: start,
-// first loads and the last epilogue.  Clusters of several CTAs leave SMs unused (a GPC's number
+// operands out of memory (3500 bytes a cycle; a quarter of the shorter of the two does not
+// overlap), and for what a kernel costs besides: start, first loads and the last epilogue.  Clusters of several CTAs leave SMs unused (a GPC's number
 // of SMs is no multiple of theirs; eight of 200 KB hardly find their place), and a second wave
 // of the small kernel waits for the first.  Both sides, bf16, us with 4 us of events: M512
 // K4096 N4096 pairs of 256 x 128 23.5, of 256 x 256 30.7, small 26.6; M128 22.5, 30, and small,
@@ -77,18 +85,19 @@ cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, i
   long long best = 0;
   int bn = 0, tn = 0, split = 1;
   auto offer = [&](long long work, long long fixed, int bn_, int tn_, int split_) {
-    const long long cost = (work > memory ? work : memory) + fixed;
+    const long long cost = (work > memory ? work + memory / 4 : memory + work / 4) + fixed;
     if (!best || cost < best) best = cost, bn = bn_, tn = tn_, split = split_;
   };
   for (int b = fp32 ? 128 : 256; b >= 128; b /= 2)
     offer(ceil_div(ceil_div(A.rows, 256) * ceil_div(B.rows, b), sms / 2) * n_k * step_cycles(fp32, 128, b, 128 + b / 2),
           b == 256 ? 17000 : 11500, b, 0, 1);
   const long long n_tiles = ceil_div(B.rows, 128);
-  for (int t = A.mn ? 64 : 16; t <= 128; t *= 2) {
+  for (int t : {16, 32, 64, 96, 128, 160, 192, 256}) {
+    if ((A.mn && t % 64) || (fp32 && t > 192)) continue;
     const long long tiles = n_tiles * ceil_div(A.rows, t);
     if (tiles > 4LL * sms) continue;
     for (int s = 1; s <= 6 && s <= n_k; ++s) {
-      const long long waves = ceil_div(tiles * s, s > 1 ? sms * 21 / 25 : sms);
+      const long long waves = ceil_div(tiles * s, s > 1 ? sms * 27 / 32 : sms);
       offer(waves * ceil_div(n_k, s) * step_cycles(fp32, 128, t, 128 + t), 10500 + 12 * t + (waves - 1) * 14000, 0, t, s);
     }
   }
@@ -122,8 +131,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* wor
   char* ws = static_cast<char*>(workspace);
   Packed px = pack_x(a, dtype), pw = pack_w(a, dtype);
   const void *x = a.x, *w = a.w;
-  cudaError_t e = px.make(x, ws, dtype, sms, st);
-  if (e == cudaSuccess) e = pw.make(w, ws + px.bytes, dtype, sms, st);
+  cudaError_t e = make(&px, &x, ws, &pw, &w, ws + px.bytes, dtype, sms, st);
   if (e != cudaSuccess) return e;
   return product(px.k_cols(x), a.w_t ? pw.k_cols(w) : pw.k_rows(w),
                  Epilogue{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, a.r_s, 0}, true, dtype, sms, st);
@@ -142,20 +150,15 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, int dtype, int sms, void* wor
   const void* d = keep ? ws + p.o_d : a.d_y;
   const Operand rows{d, a.M, a.N, keep ? p.pitch : a.N, false, p.piece};   // k along the channels out
   const Operand cols{d, a.N, a.M, keep ? p.pitch : a.N, true, p.piece};    // k along the tokens
-  if (a.dx && e == cudaSuccess) {   // dx[m,k] = sum over n of d[m,n] W[k,n]
-    const void* w = a.w;
-    e = p.w.make(w, ws + p.o_w, dtype, sms, st);
-    if (e == cudaSuccess)
-      e = product(rows, a.w_t ? p.w.k_rows(w) : p.w.k_cols(w), Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K}, false,
-                  dtype, sms, st);
-  }
-  if (a.dw && e == cudaSuccess) {   // dw[k,n] = sum over m of x[m,k] d[m,n], in W's order
-    const void* x = a.x;
-    e = p.x.make(x, ws + p.o_x, dtype, sms, st);
-    if (e == cudaSuccess)
-      e = product(a.w_t ? cols : p.x.k_rows(x), a.w_t ? p.x.k_rows(x) : cols,
-                  Epilogue{a.dw, nullptr, nullptr, nullptr, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N}, false, dtype, sms, st);
-  }
+  const void *x = a.x, *w = a.w;
+  if (e == cudaSuccess)
+    e = make(a.dw ? &p.x : nullptr, &x, ws + p.o_x, a.dx ? &p.w : nullptr, &w, ws + p.o_w, dtype, sms, st);
+  if (a.dx && e == cudaSuccess)   // dx[m,k] = sum over n of d[m,n] W[k,n]
+    e = product(rows, a.w_t ? p.w.k_rows(w) : p.w.k_cols(w), Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K}, false,
+                dtype, sms, st);
+  if (a.dw && e == cudaSuccess)   // dw[k,n] = sum over m of x[m,k] d[m,n], in W's order
+    e = product(a.w_t ? cols : p.x.k_rows(x), a.w_t ? p.x.k_rows(x) : cols,
+                Epilogue{a.dw, nullptr, nullptr, nullptr, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N}, false, dtype, sms, st);
   return e;
 }
 

@@ -7,7 +7,7 @@
 // part of C in its shared memory; they add them up in the ranks' order, each for its share of
 // the rows, so the result does not depend on which CTA is first.
 //   warps 0-7  the accumulator to shared memory, then the sums and the epilogue, a row per warp
-//   warp 8     TMA, 6 to 11 stages of 64 k
+//   warp 8     TMA, 4 to 11 stages of 64 k
 //   warp 9     the MMAs
 // Weights are what bounds it, 16 KB of each stage, so an SM keeps 200 KB of them under way.
 #pragma once
@@ -23,8 +23,9 @@ constexpr int kFewThreads = 320, kFewWarps = 8, kFewLoadWarp = 8, kFewMmaWarp = 
 
 template <int TN> struct FewSmem {
   static constexpr int kN = 128 * kBK * 2, kM = TN * kBK * 2, kStage = kN + kM;
-  static constexpr int kStages = TN == 16 ? 11 : TN == 32 ? 10 : TN == 64 ? 8 : 6;
+  static constexpr int kStages = 200 * 1024 / kStage;
   static constexpr int kBytes = kStages * kStage + 1024;
+  static_assert(kStages >= 4, "fp32 takes three of them at once");
   static_assert(TN * 128 * 4 <= kStages * kStage, "the parts of C take the stages' place");
 };
 
@@ -81,11 +82,14 @@ template <int TN, bool N_MN, bool M_MN, typename T, bool FULL>
 __global__ void __launch_bounds__(kFewThreads, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmN, const __grid_constant__ CUtensorMap tmM, Epilogue e,
                       FewGrid g, int n_k) {
-  static_assert(!M_MN || TN >= 64, "a swizzled row of an MN-major operand is 64 of its rows");
+  static_assert(!M_MN || TN % 64 == 0, "a swizzled row of an MN-major operand is 64 of its rows");
   using L = FewSmem<TN>;
   using S = typename std::conditional<sizeof(T) == 2, __half, float>::type;
   constexpr bool FP32 = sizeof(T) == 4;
-  constexpr int NS = L::kStages, kCols = TN < 32 ? 32 : TN;   // TMEM columns of an accumulator
+  constexpr int NS = L::kStages;
+  constexpr int kCols = FP32 ? TN : 0;                                          // to the second accumulator
+  constexpr int kAll = FP32 ? 2 * TN : TN;
+  constexpr int kTmem = kAll <= 32 ? 32 : kAll <= 64 ? 64 : kAll <= 128 ? 128 : kAll <= 256 ? 256 : 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[2], b_free[2], b_end;
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     mbar_init(&b_end, 1);
     fence_mbar_init();
   }
-  if (warp == kFewMmaWarp) tmem_alloc(&s_tmem, (FP32 ? 2 : 1) * kCols);
+  if (warp == kFewMmaWarp) tmem_alloc(&s_tmem, kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   float* part = reinterpret_cast<float*>(sm);   // [TN][128]
 
   if (warp < kFewWarps) {   // ---------------------------------------------- accumulators
-    constexpr int H = TN / 2, C = H < 32 ? H : 32;   // columns of a warp, and at once
+    constexpr int H = TN / 2, C = H % 32 == 0 ? 32 : H % 16 == 0 ? 16 : 8;   // columns of a warp, and at once
     const int c0 = warp / 4 * H, row = warp % 4 * 32 + lane;
     const uint32_t at = tmem + c0 + (static_cast<uint32_t>(warp % 4 * 32) << 16);
     float acc[FP32 ? H : C];
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncwarp();
   cluster_sync();   // every part is there
   tc_fence_after();
-  if (warp == kFewMmaWarp) tmem_dealloc(tmem, (FP32 ? 2 : 1) * kCols);
+  if (warp == kFewMmaWarp) tmem_dealloc(tmem, kTmem);
   const int n = n0 + lane * 4, left = e.N - n;
   if (warp < kFewWarps && left > 0) {   // ----------------------------- sums and epilogue
     const bool whole = e.vec && left >= 4;
@@ -299,10 +303,10 @@ cudaError_t few(const Operand& M, const Operand& N, Epilogue e, int split, cudaS
   return cudaLaunchKernelEx(&cfg, kernel, tn, tm, e, g, (N.k + kBK - 1) / kBK);
 }
 
-template <int TN, typename T>
+template <typename T, int TN>
 cudaError_t few_by_order(const Operand& M, const Operand& N, const Epilogue& e, bool full, int split, cudaStream_t st) {
   if (full) return N.mn ? few<TN, true, false, T, true>(M, N, e, split, st) : few<TN, false, false, T, true>(M, N, e, split, st);
-  if constexpr (TN >= 64) {
+  if constexpr (TN % 64 == 0) {
     if (M.mn) return few<TN, true, true, T, false>(M, N, e, split, st);
   }
   return N.mn ? few<TN, true, false, T, false>(M, N, e, split, st) : few<TN, false, false, T, false>(M, N, e, split, st);
@@ -311,11 +315,17 @@ cudaError_t few_by_order(const Operand& M, const Operand& N, const Epilogue& e, 
 template <typename T>
 cudaError_t few_by_tile(int tn, const Operand& M, const Operand& N, const Epilogue& e, bool full, int split, cudaStream_t st) {
   switch (tn) {
-    case 16: return few_by_order<16, T>(M, N, e, full, split, st);
-    case 32: return few_by_order<32, T>(M, N, e, full, split, st);
-    case 64: return few_by_order<64, T>(M, N, e, full, split, st);
-    default: return few_by_order<128, T>(M, N, e, full, split, st);
+    case 16: return few_by_order<T, 16>(M, N, e, full, split, st);
+    case 32: return few_by_order<T, 32>(M, N, e, full, split, st);
+    case 64: return few_by_order<T, 64>(M, N, e, full, split, st);
+    case 96: return few_by_order<T, 96>(M, N, e, full, split, st);
+    case 128: return few_by_order<T, 128>(M, N, e, full, split, st);
+    case 160: return few_by_order<T, 160>(M, N, e, full, split, st);
+    case 192: return few_by_order<T, 192>(M, N, e, full, split, st);
+    default: break;
   }
+  if constexpr (sizeof(T) == 2) return few_by_order<T, 256>(M, N, e, full, split, st);
+  return cudaErrorInvalidValue;   // 128 sums per thread take more registers than it has
 }
 
 }  // namespace lin

@@ -52,18 +52,27 @@ template <typename T> __device__ __forceinline__ void write_pieces(__nv_bfloat16
   }
 }
 
-// rows x cols, columns contiguous -> pieces with rows of `pitch`
+// rows x cols, columns contiguous -> pieces with rows of `pitch`; two matrices at once, the
+// blocks shared out by their sizes
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) pack_kernel(const T* src, long long stride, int rows, int cols, __nv_bfloat16* dst,
-                                                   int pitch, long long piece) {
-  const long long per = pitch / 8, n = rows * per;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+__device__ __forceinline__ void pack_one(const PackJob& j, long long i, long long step) {
+  const long long per = j.pitch / 8, n = j.rows * per;
+  for (; i < n; i += step) {
     long long r;
     const int c = 8 * div_mod(i, static_cast<int>(per), r);
     float f[8];
-    read8<T, VEC>(src + r * stride + c, cols - c, f);
-    write_pieces<T>(dst + r * pitch + c, piece, f);
+    read8<T, VEC>(static_cast<const T*>(j.src) + r * j.stride + c, j.cols - c, f);
+    write_pieces<T>(static_cast<__nv_bfloat16*>(j.dst) + r * j.pitch + c, j.piece, f);
   }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(PackJob a, PackJob b, int blocks_a) {
+  const bool first = static_cast<int>(blockIdx.x) < blocks_a;
+  const PackJob& j = first ? a : b;
+  const long long at = (long long)(blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
+  const long long step = (long long)(first ? blocks_a : gridDim.x - blocks_a) * 256;
+  if (j.cols % 8 == 0 && j.stride % (16 / (int)sizeof(T)) == 0) pack_one<T, true>(j, at, step);
+  else pack_one<T, false>(j, at, step);
 }
 
 // d = d_y * slope [M,N] in pieces with rows of `pitch` (dst null: not kept), and the columns'
@@ -121,21 +130,17 @@ __global__ void __launch_bounds__(1024) join_bias_kernel(const float* part, int 
   if (lane == 0 && m < N) db[m] = from_f<T>(s);
 }
 
-template <typename T>
-void pack(const void* src, long long stride, int rows, int cols, void* dst, int pitch, long long piece, int sms, cudaStream_t st) {
-  const long long n = (long long)rows * (pitch / 8), most = 16LL * sms;
-  const unsigned grid = static_cast<unsigned>(min(most, (n + 255) / 256));
-  const bool vec = cols % 8 == 0 && stride % (16 / (int)sizeof(T)) == 0;
-  auto* k = vec ? pack_kernel<T, true> : pack_kernel<T, false>;
-  k<<<grid, 256, 0, st>>>(static_cast<const T*>(src), stride, rows, cols, static_cast<__nv_bfloat16*>(dst), pitch, piece);
-}
-
 }  // namespace
 
-cudaError_t launch_linear_pack(const void* src, long long stride, int rows, int cols, int dtype, void* dst, int pitch,
-                               long long piece, int sms, cudaStream_t st) {
-  if (dtype == DR_FP32) pack<float>(src, stride, rows, cols, dst, pitch, piece, sms, st);
-  else pack<__nv_bfloat16>(src, stride, rows, cols, dst, pitch, piece, sms, st);
+// One or two (b.src null: one) copies in one launch.
+cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, cudaStream_t st) {
+  auto blocks = [&](const PackJob& j) {
+    const long long n = j.src ? ((long long)j.rows * (j.pitch / 8) + 255) / 256 : 0;
+    return static_cast<int>(min(n, 16LL * sms));
+  };
+  const int na = blocks(a), nb = blocks(b);
+  if (dtype == DR_FP32) pack_kernel<float><<<na + nb, 256, 0, st>>>(a, b, na);
+  else pack_kernel<__nv_bfloat16><<<na + nb, 256, 0, st>>>(a, b, na);
   return cudaGetLastError();
 }
 

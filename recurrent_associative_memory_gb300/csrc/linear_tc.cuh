@@ -10,6 +10,16 @@
 #include "block.cuh"
 
 namespace dr {
+
+// A copy of a matrix, its columns contiguous, with rows of `pitch` (fp32: three of them,
+// `piece` apart).
+struct PackJob {
+  const void* src;
+  void* dst;
+  long long stride, piece;
+  int rows, cols, pitch;
+};
+
 namespace lin {
 
 using namespace umma;

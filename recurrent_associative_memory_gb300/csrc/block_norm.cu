@@ -164,9 +164,10 @@ __device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, cons
 
 // The rows of a block.  RING: one at a time, through a ring of `stages` of them in shared
 // memory.  Tensor i of a row is copied by warp i, once the block has passed a barrier behind
-// the reads of the row whose place it takes: the first one of the next row.  (To issue a copy
-// takes a few hundred cycles: one thread for all of them holds the block up, M16384 D4096
-// forward 156 us instead of 103; a warp of its own costs the others their registers.)
+// the reads of the row whose place it takes: the first one of the next row.  (What a copy costs
+// its warp, the others wait for: issued by one thread for all tensors M16384 D4096 forward took
+// 156 us instead of 103, and with the addresses formed for each row M8192 D4096 backward 143
+// instead of 137.  A warp of its own would cost the others their registers.)
 // Otherwise straight from memory.
 template <int N> struct Ring {
   uint64_t* full;
@@ -179,20 +180,22 @@ template <int N> struct Ring {
   int stage;
   uint32_t parity;
   bool lost;
+  // this warp's tensor: where its next copy comes from, and the one after it; its place in a
+  // stage; the bytes of a row, and of the tensor's last one
+  uintptr_t from;
+  long long from_step;
+  uint32_t to, bytes, last_bytes;
+  bool mine;
 
-  // One thread of a warp: that warp's tensor of a row.
-  __device__ __forceinline__ void issue(int warp, long long row, int s, int D, int phase) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i != warp || !base[i]) continue;
-      const RowCopy r(base[i], row, stride[i], D, phase, es[i], M);
-      umma::mbar_expect_tx(full + s, r.bytes);
-      if (r.bytes)
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         at + s * stage_bytes + off[i]),
-                     "l"(r.lo), "r"(r.bytes), "r"(umma::smem_u32(full + s))
-                     : "memory");
-    }
+  // One thread of a warp: that warp's tensor of `row`, the rows in their order.
+  __device__ __forceinline__ void issue(long long row, int s) {
+    const uint32_t n = row == M - 1 ? last_bytes : bytes;
+    umma::mbar_expect_tx(full + s, n);
+    if (n)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       to + s * stage_bytes),
+                   "l"(from), "r"(n), "r"(umma::smem_u32(full + s))
+                   : "memory");
   }
   // Bounded; after one that gave up none waits any more, and what comes out means nothing.
   __device__ __forceinline__ void wait() {
@@ -205,10 +208,12 @@ template <int N> struct Ring {
   }
   // Behind the first barrier of `row`: the place of the row before goes to the one `stages`
   // further on.
-  __device__ __forceinline__ void refill(long long row, long long first, long long step, int D, int phase) {
-    const long long to = row + (stages - 1) * step;
-    if (threadIdx.x < 32 * N && threadIdx.x % 32 == 0 && row > first && to < M)
-      issue(threadIdx.x / 32, to, stage == 0 ? stages - 1 : stage - 1, D, phase);
+  __device__ __forceinline__ void refill(long long row, long long first, long long step) {
+    const long long next = row + (stages - 1) * step;
+    if (mine && row > first && next < M) {
+      if (threadIdx.x % 32 == 0) issue(next, stage == 0 ? stages - 1 : stage - 1);
+      from += from_step;
+    }
   }
   // No copy may be in flight when the block ends; only after a wait that gave up there can be.
   __device__ __forceinline__ void drain() {
@@ -327,18 +332,32 @@ __device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages
   ring.stage = 0, ring.parity = 0, ring.lost = false;
   uint32_t at = 0;
   int there = 0;
+  ring.mine = false;
+  ring.from = 0, ring.from_step = 0, ring.to = ring.bytes = ring.last_bytes = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     ring.off[i] = at;
-    if (ring.base[i]) at += copy_bytes(c.D, ring.es[i]), ++there;
+    if (!ring.base[i]) continue;
+    if (static_cast<int>(threadIdx.x / 32) == i) {
+      const RowCopy usual(ring.base[i], row, ring.stride[i], c.D, c.phase(), ring.es[i], -1);
+      ring.mine = true;
+      ring.from = usual.lo, ring.from_step = step * ring.stride[i] * ring.es[i];
+      ring.to = ring.at + at;
+      ring.bytes = usual.bytes;
+      ring.last_bytes = RowCopy(ring.base[i], M - 1, ring.stride[i], c.D, c.phase(), ring.es[i], M).bytes;
+    }
+    at += copy_bytes(c.D, ring.es[i]), ++there;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) umma::mbar_init(ring.full + i, there);
     umma::fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x % 32 == 0)
-    for (int i = 0; i < l.stages && row + i * step < M; ++i) ring.issue(threadIdx.x / 32, row + i * step, i, c.D, c.phase());
+  if (ring.mine)
+    for (int i = 0; i < l.stages && row + i * step < M; ++i) {
+      if (threadIdx.x % 32 == 0) ring.issue(row + i * step, i);
+      ring.from += ring.from_step;
+    }
 }
 
 __device__ __forceinline__ int phase_of(long long row, int D) { return static_cast<int>(row * D & 7); }
@@ -400,12 +419,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
       float s[1] = {dot(h, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      if (RING) ring.refill(row, first, step, a.D, c.phase());
+      if (RING) ring.refill(row, first, step);
       pairs<P>([&](int i) { h[i] = mul2(h[i], mul2(both(rstd), wy[i])); });
       if (live) store_row(static_cast<TA*>(a.y) + row * a.D, c, h);
     } else if (RING) {
       __syncthreads();
-      ring.refill(row, first, step, a.D, c.phase());
+      ring.refill(row, first, step);
     }
     if (RING) ring.next();
   }
@@ -495,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       if (live) ring.template get<TH, RING>(4, row, c, g);
       if (RING) __syncthreads();
     }
-    if (RING) ring.refill(row, first, step, D, c.phase()), ring.next();
+    if (RING) ring.refill(row, first, step), ring.next();
     if (live && a.dh) store_row(static_cast<TH*>(a.dh) + row * D, c, g);
     if (!a.branch) continue;
     pairs<P>([&](int i) {

@@ -124,6 +124,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const uint32_t at = tmem + c0 + (static_cast<uint32_t>(warp % 4 * 32) << 16);
     float acc[FP32 ? H : C];
     bool ok = true;
+    if (FULL && e.res) {   // the rows that this warp finishes
+      const int c = n0 + lane * (128 / (int)sizeof(T));
+      if (lane < (int)sizeof(T) && c < e.N)
+        for (int p = rank * kFewWarps + warp; p < TN && m0 + p < e.M; p += g.split * kFewWarps)
+          to_l2(static_cast<const T*>(e.res) + (m0 + p) * e.r_m + c);
+    }
     auto load = [&](uint32_t from, float* v) {
       if constexpr (C == 32) tmem_ld32(from, reinterpret_cast<uint32_t*>(v));
       else if constexpr (C == 16) tmem_ld16(from, reinterpret_cast<float(&)[16]>(*v));

@@ -103,6 +103,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const T* res = FULL && e.res && live ? static_cast<const T*>(e.res) + m * e.r_m + n0 : nullptr;
       T* C = static_cast<T*>(e.C) + (long long)m * e.N + n0;
       S* slope = FULL && e.slope ? static_cast<S*>(e.slope) + (long long)m * e.N + n0 : nullptr;
+      if (res && !e.vec)
+        for (int c = 0; c < NC && n0 + c < e.N; c += 128 / (int)sizeof(T)) to_l2(res + c);
       Raw16<T> r[2];
       auto ahead = [&](int c) {   // the residual of columns c .. c + 31
         if (!FULL || FP32 || !res || !e.vec) return;   // fp32: its sums have the registers

@@ -533,7 +533,9 @@ typedef enum {
  * Matrix product with its epilogue, M rows of K channels to N:
  *     y = act(x W + bias) + residual
  * Every product is summed in fp32 and y is rounded once.  Few rows (single tokens)
- * take kernels of their own; which ones is decided by the sizes alone.
+ * take kernels of their own; which ones is decided by the sizes alone.  A row that holds NaN
+ * or an infinity makes no other row different; in fp32 an infinity, or a value that the
+ * largest bf16 (3.39e38) does not reach, may come out as NaN.
  */
 typedef struct dr_linear {
   int dtype;               /* dr_dtype of everything but the slope                    */

@@ -239,17 +239,22 @@ def block_norm_bwd(h, branch=None, *, d_h=None, d_y=None, gate=None, gate_act="n
         check(d_h, "d_h", h.shape, h.dtype, dev)
     if d_y is not None:
         check(d_y, "d_y", h.shape, dtype, dev)
-    vec, given = (a.D,), dict(grads or {})
-    g = {}
-    for name, there, shape, kind in (
-            ("dh", h, h.shape, h.dtype), ("dbranch", branch, h.shape, dtype),
-            ("dgate", gate, h.shape, dtype), ("dscale", scale, vec, _FP32),
-            ("dpost_weight", post_weight, vec, _FP32),
-            ("dpre_weight", None if d_y is None else pre_weight, vec, _FP32)):
-        if there is not None:
-            g[name] = _given_or_new(given.get(name), name, shape, kind, there, dev)
-    ws, n = (scratch(dr.dr_block_norm_bwd_workspace_bytes, a, h, dev, workspace)
-             if "dscale" in g or "dpost_weight" in g or "dpre_weight" in g else (None, 0))
+    given = grads or {}
+    g = {"dh": _given_or_new(given.get("dh"), "dh", h.shape, h.dtype, h, dev)}
+    if branch is not None:
+        g["dbranch"] = _given_or_new(given.get("dbranch"), "dbranch", h.shape, dtype, branch, dev)
+    if gate is not None:
+        g["dgate"] = _given_or_new(given.get("dgate"), "dgate", h.shape, dtype, gate, dev)
+    names = [n for n, t in (("dscale", scale), ("dpost_weight", post_weight),
+                            ("dpre_weight", None if d_y is None else pre_weight)) if t is not None]
+    ws, n = None, 0
+    if names:
+        if any(n in given for n in names):
+            for name in names:
+                g[name] = _given_or_new(given.get(name), name, (a.D,), _FP32, h, dev)
+        else:                                  # three small ones are one allocation
+            g.update(zip(names, _empty((len(names), a.D), dtype=_FP32, device=h.device).unbind()))
+        ws, n = scratch(dr.dr_block_norm_bwd_workspace_bytes, a, h, dev, workspace)
     out = dr.DrBlockNormGrads(*(ptr(g.get(k)) for k in _GRADS))
     call("dr_block_norm_bwd", dev, dr.dr_block_norm_bwd, a, h, branch, gate, scale, post_weight,
          pre_weight, d_h, d_y, out, ws, n)

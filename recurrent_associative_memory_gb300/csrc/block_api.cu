@@ -30,6 +30,8 @@ template <typename... P> bool aligned(unsigned n, const P*... p) {
 unsigned bytes_of(int dtype) { return dtype == DR_FP32 ? 4 : 2; }
 bool dtype_ok(int t) { return t == DR_FP32 || t == DR_BF16; }
 bool act_ok(int t) { return t >= DR_ACT_NONE && t <= DR_ACT_SIGMOID; }
+// is p one of the others?
+template <typename... P> bool among(const void* p, const P*... q) { return p && ((p == static_cast<const void*>(q)) || ...); }
 cudaStream_t stream_of(dr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 int status_of(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CUDA; }
 
@@ -95,6 +97,9 @@ int dr_linear_fwd(const dr_linear* a, const void* x, const void* weight, const v
   const size_t need = dr_linear_fwd_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
+  // a tile's rows are read by other tiles too; a residual's value only where it is added
+  if (among(y, x, weight) || among(slope, x, weight, residual, y) || (y == residual && a->M > 1 && a->r_s != a->N))
+    return DR_ERR_ARG;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
   LinearArgs r = linear_args(a);
@@ -117,6 +122,9 @@ int dr_linear_bwd(const dr_linear* a, const void* x, const void* weight, const v
   const size_t need = dr_linear_bwd_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
+  if (among(dx, x, weight, d_y, slope, d_weight, d_bias) || among(d_weight, x, weight, d_y, slope, d_bias) ||
+      among(d_bias, x, weight, d_y, slope))
+    return DR_ERR_ARG;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
   LinearArgs r = linear_args(a);
@@ -132,7 +140,8 @@ int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch,
   if (st != DR_OK) return st;
   if (!branch && (gate || scale || h_out || a->post_norm)) return DR_ERR_ARG;
   if ((post_weight && !a->post_norm) || (pre_weight && !y)) return DR_ERR_ARG;
-  if (y == h || (h_out && y == h_out)) return DR_ERR_ARG;
+  if (among(y, h, branch, gate, h_out) || among(h_out, branch, gate) || (h_out == h && a->M > 1 && a->h_s != a->D))
+    return DR_ERR_ARG;
   if (!aligned(bytes_of(a->dtype), branch, gate, y) || !aligned(bytes_of(a->h_dtype), h, h_out) ||
       !aligned(4, scale, post_weight, pre_weight))
     return DR_ERR_ALIGN;

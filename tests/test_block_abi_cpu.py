@@ -12,6 +12,7 @@ from test_layers_abi_cpu import A, MIS, dr, test_struct_layout_matches_c as layo
 
 BIG = 1 << 45
 OTHER = A + (1 << 16)
+FAR = [A + (i << 16) for i in range(12)]   # aligned addresses of which no two are one
 
 
 @pytest.mark.parametrize("c_name,py_name", [("dr_linear", "DrLinear"), ("dr_block_norm", "DrBlockNorm"),
@@ -52,7 +53,7 @@ def test_linear_pointers(dr):  # noqa: F811
         assert dr.dr_linear_fwd(a, *p, stream=0) == dr.DR_ERR_ALIGN
     need = dr.dr_linear_fwd_workspace_bytes(fp)
     assert need >= 6 * (5 * 64 + 64 * 48)
-    assert dr.dr_linear_fwd(fp, A, A, None, None, A, None, None, 0, stream=0) == dr.DR_ERR_WORKSPACE
+    assert dr.dr_linear_fwd(fp, A, A, None, None, OTHER, None, None, 0, stream=0) == dr.DR_ERR_WORKSPACE
     assert dr.dr_linear_fwd(fp, A, A, None, None, A, None, A, need - 1, stream=0) == dr.DR_ERR_WORKSPACE
     assert dr.dr_linear_fwd(fp, A, A, None, None, A, None, A + 16, need, stream=0) == dr.DR_ERR_ALIGN
     s = linear(dr, act=2)
@@ -69,6 +70,32 @@ def test_linear_pointers(dr):  # noqa: F811
         p = [A] * 7
         p[i] = MIS
         assert dr.dr_linear_bwd(s, *p, A, BIG, stream=0) == dr.DR_ERR_ALIGN
+
+
+def test_one_buffer_for_two(dr):  # noqa: F811
+    """Outputs over inputs that other blocks still read, or over each other."""
+    a = linear(dr, N=64, act=2)
+    names = ("x", "weight", "bias", "residual", "y", "slope")
+    at = dict(zip(names, FAR))
+    fwd = lambda a, **kw: dr.dr_linear_fwd(a, *({**at, **kw}[n] for n in names), None, 0, stream=0)  # noqa: E731
+    for out, of in (("y", "x"), ("y", "weight"), ("slope", "x"), ("slope", "weight"), ("slope", "residual"), ("slope", "y")):
+        assert fwd(a, **{out: at[of]}) == dr.DR_ERR_ARG, (out, of)
+    wide = linear(dr, N=64, r_s=72)
+    assert fwd(wide, y=at["residual"]) == dr.DR_ERR_ARG
+    back = ("x", "weight", "d_y", "slope", "dx", "d_weight", "d_bias")
+    there = dict(zip(back, FAR))
+    for out in back[4:]:
+        for of in back:
+            if of != out:
+                p = {**there, out: there[of]}
+                assert dr.dr_linear_bwd(a, *(p[n] for n in back), FAR[10], BIG, stream=0) == dr.DR_ERR_ARG, (out, of)
+    n = norm(dr, h_s=72)
+    parts = ("h", "branch", "gate", "scale", "post_weight", "pre_weight", "h_out", "y")
+    place = dict(zip(parts, FAR))
+    for out, of in (("y", "h"), ("y", "branch"), ("y", "gate"), ("y", "h_out"), ("h_out", "branch"), ("h_out", "gate"),
+                    ("h_out", "h")):   # the last: rows further apart than what is written
+        p = {**place, out: place[of]}
+        assert dr.dr_block_norm_fwd(n, *(p[k] for k in parts), stream=0) == dr.DR_ERR_ARG, (out, of)
 
 
 def test_linear_workspace(dr):  # noqa: F811
@@ -136,7 +163,7 @@ def test_alignment_of_single_values(dr):  # noqa: F811
     assert dr.dr_linear_bwd(a, A, A, A, None, A, A, A + 1, A, BIG, stream=0) == dr.DR_ERR_ALIGN
     n = norm(dr, h_dtype=dr.DR_FP32)
     for i in range(8):
-        p = [A, A, A, A, A, A, A, OTHER]
+        p = FAR[:8]
         p[i] += 2 if i in (0, 3, 4, 5, 6) else 1
         assert dr.dr_block_norm_fwd(n, *p, stream=0) == dr.DR_ERR_ALIGN
         for j in range(6):
@@ -158,14 +185,14 @@ def test_block_norm_workspace_where_there_is_no_device(dr):  # noqa: F811
 CALLS = """
 import sys
 sys.path[:0] = [{tests!r}, {root!r}]
-from test_block_abi_cpu import A, BIG, OTHER, linear, norm
+from test_block_abi_cpu import A, BIG, FAR, linear, norm
 from recurrent_associative_memory_gb300 import dr
 for dtype in (dr.DR_BF16, dr.DR_FP32):
     a, s = linear(dr, dtype=dtype), linear(dr, dtype=dtype, act=3)
-    print(dr.dr_linear_fwd(a, A, A, A, A, A, A, A, BIG, stream=0))
-    print(dr.dr_linear_bwd(s, A, A, A, A, A, A, A, A, BIG, stream=0))
+    print(dr.dr_linear_fwd(a, *FAR[:6], A, BIG, stream=0))
+    print(dr.dr_linear_bwd(s, *FAR[:7], FAR[8], BIG, stream=0))
     n, g = norm(dr, dtype=dtype, h_dtype=dr.DR_FP32), dr.DrBlockNormGrads(*[A] * 6)
-    print(dr.dr_block_norm_fwd(n, A, A, A, A, A, A, A, OTHER, stream=0))
+    print(dr.dr_block_norm_fwd(n, *FAR[:8], stream=0))
     print(dr.dr_block_norm_bwd(n, A, A, A, A, A, A, A, A, g, A, BIG, stream=0))
 """
 

@@ -13,6 +13,8 @@ cudaError_t launch_linear_few_bf16(int tn, const lin::Operand& M, const lin::Ope
                                    int split, cudaStream_t st);
 cudaError_t launch_linear_few_fp32(int tn, const lin::Operand& M, const lin::Operand& N, const lin::Epilogue& e, bool full,
                                    int split, cudaStream_t st);
+bool linear_rows_supported(const LinearArgs& a, int dtype);
+cudaError_t launch_linear_rows(const LinearArgs& a, int sms, cudaStream_t st);
 
 namespace {
 
@@ -125,9 +127,12 @@ struct BwdPlan {
 
 }  // namespace
 
-size_t linear_fwd_workspace(const LinearArgs& a, int dtype) { return pack_x(a, dtype).bytes + pack_w(a, dtype).bytes; }
+size_t linear_fwd_workspace(const LinearArgs& a, int dtype) {
+  return linear_rows_supported(a, dtype) ? 0 : pack_x(a, dtype).bytes + pack_w(a, dtype).bytes;
+}
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* workspace, cudaStream_t st) {
+  if (linear_rows_supported(a, dtype)) return launch_linear_rows(a, sms, st);
   char* ws = static_cast<char*>(workspace);
   Packed px = pack_x(a, dtype), pw = pack_w(a, dtype);
   const void *x = a.x, *w = a.w;

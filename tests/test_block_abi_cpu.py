@@ -42,7 +42,7 @@ def test_linear_refuses(dr, kw, want):  # noqa: F811
 
 
 def test_linear_pointers(dr):  # noqa: F811
-    a, fp = linear(dr), linear(dr, dtype=dr.DR_FP32)
+    a, fp = linear(dr), linear(dr, dtype=dr.DR_FP32, M=20)
     for i in (0, 1, 4):
         p = [A, A, None, None, A, None]
         p[i] = None
@@ -52,7 +52,7 @@ def test_linear_pointers(dr):  # noqa: F811
         p[i] = MIS
         assert dr.dr_linear_fwd(a, *p, stream=0) == dr.DR_ERR_ALIGN
     need = dr.dr_linear_fwd_workspace_bytes(fp)
-    assert need >= 6 * (5 * 64 + 64 * 48)
+    assert need >= 6 * (20 * 64 + 64 * 48)
     assert dr.dr_linear_fwd(fp, A, A, None, None, OTHER, None, None, 0, stream=0) == dr.DR_ERR_WORKSPACE
     assert dr.dr_linear_fwd(fp, A, A, None, None, A, None, A, need - 1, stream=0) == dr.DR_ERR_WORKSPACE
     assert dr.dr_linear_fwd(fp, A, A, None, None, A, None, A + 16, need, stream=0) == dr.DR_ERR_ALIGN
@@ -107,7 +107,9 @@ def test_linear_workspace(dr):  # noqa: F811
     assert size(linear(dr, M=1, x_s=3)) == 0
     assert size(linear(dr, w_s=50)) >= 2 * 64 * 48
     assert size(linear(dr, N=47, w_s=47)) >= 2 * 64 * 48
-    assert dr.dr_linear_fwd_workspace_bytes(linear(dr, dtype=dr.DR_FP32, K=63)) % 256 == 0
+    assert size(linear(dr, dtype=dr.DR_FP32, M=9)) >= 6 * (9 * 64 + 64 * 48) and size(linear(dr, dtype=dr.DR_FP32, M=8)) == 0
+    assert size(linear(dr, dtype=dr.DR_FP32, M=8, w_s=50)) > 0   # rows that no 16 bytes start
+    assert size(linear(dr, dtype=dr.DR_FP32, M=40, K=63)) % 256 == 0
 
 
 def norm(dr, **kw):  # noqa: F811

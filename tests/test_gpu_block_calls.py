@@ -128,8 +128,9 @@ def test_linear_refuses(block, dtype):  # noqa: F811
     with pytest.raises(dr.DrError):
         block.linear_fwd(x[:0], w)
     if dtype is FP:
+        block.linear_fwd(x[:8], w, workspace=None)   # so few rows take none
         with pytest.raises(dr.DrError):
-            block.linear_fwd(x, w, workspace=None)
+            block.linear_fwd(linear_case(3, 20, 32, 24, dtype)["x"], w, workspace=None)
     with pytest.raises(dr.DrError):
         block.linear_fwd(torch.zeros(4 * 32 + 1, dtype=dtype, device="cuda")[1:].view(4, 32), w)
     torch.cuda.synchronize()

@@ -245,15 +245,13 @@ def block_norm_bwd(h, branch=None, *, d_h=None, d_y=None, gate=None, gate_act="n
         g["dbranch"] = _given_or_new(given.get("dbranch"), "dbranch", h.shape, dtype, branch, dev)
     if gate is not None:
         g["dgate"] = _given_or_new(given.get("dgate"), "dgate", h.shape, dtype, gate, dev)
-    names = [n for n, t in (("dscale", scale), ("dpost_weight", post_weight),
-                            ("dpre_weight", None if d_y is None else pre_weight)) if t is not None]
-    ws, n = None, 0
-    if names:
-        if any(n in given for n in names):
-            for name in names:
-                g[name] = _given_or_new(given.get(name), name, (a.D,), _FP32, h, dev)
-        else:                                  # three small ones are one allocation
-            g.update(zip(names, _empty((len(names), a.D), dtype=_FP32, device=h.device).unbind()))
+    ws, n, vec = None, 0, (a.D,)
+    for name, t in (("dscale", scale), ("dpost_weight", post_weight),
+                    ("dpre_weight", None if d_y is None else pre_weight)):
+        if t is not None:
+            g[name] = _given_or_new(given.get(name), name, vec, _FP32, t, dev)
+            n = 1
+    if n:
         ws, n = scratch(dr.dr_block_norm_bwd_workspace_bytes, a, h, dev, workspace)
     out = dr.DrBlockNormGrads(*(ptr(g.get(k)) for k in _GRADS))
     call("dr_block_norm_bwd", dev, dr.dr_block_norm_bwd, a, h, branch, gate, scale, post_weight,

@@ -132,6 +132,6 @@ def scratch(size_of, description, x, device, workspace):
                 n = size_of(description)
         else:
             n = size_of(description)
-        return (x.new_empty(n, dtype=torch.uint8), n) if n else (None, 0)
+        return (torch.empty(n, dtype=torch.uint8, device=x.device), n) if n else (None, 0)
     check(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
     return workspace, workspace.numel()

@@ -5,7 +5,9 @@ include/dr.h).  ``dr`` is its ctypes binding, ``runner`` allocates outputs and
 calls it, ``workloads`` draws the seeded synthetic inputs, ``build`` compiles
 the library.  ``attention`` (sliding window with sinks) and ``ssm`` (short
 causal convolution, selective scan) are the layers that stand next to the
-recurrence in a hybrid stack, and ``hybrid`` is such a stack.  Importing ``dr``
+recurrence in a hybrid stack, ``block`` what stands around a mixer
+(projections with their epilogue, norms with gate and residual scale), and
+``hybrid`` is such a stack.  Importing ``dr``
 (or what calls it) requires the built library.
 """
 

@@ -574,7 +574,9 @@ size_t dr_linear_bwd_workspace_bytes(const dr_linear *a);
  *     h' = h + scale f(gate) u,   u = n(branch; post_weight) or branch
  *     y  = n(h'; pre_weight)
  * h is the residual stream and branch what the block's mixer has given.  y is the norm of
- * h' as it was summed, before it is rounded to the stream's type.
+ * h' as it was summed, before it is rounded to the stream's type.  Squares are summed in
+ * fp32: a row whose sum passes its range (values from 1e18 on) has a norm of 0.  With eps 0 a
+ * row of zeros has NaN.
  */
 typedef struct dr_block_norm {
   int dtype;               /* dr_dtype of branch, gate, y and their gradients         */

@@ -82,6 +82,7 @@ template <int ACT> __device__ __forceinline__ float act_of(float x, float& slope
     const float cc = c * c;
     const float s = sigmoid_f(c * fmaf(0.07135481283f, cc, 1.595769122f));
     slope = fmaf(c * s * (1.f - s), fmaf(0.21406443849f, cc, 1.595769122f), s);
+    slope = x == x ? slope : x;
     return x * s;
   }
   slope = 1.f;

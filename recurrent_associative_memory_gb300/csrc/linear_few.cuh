@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s_tmem);
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    bool ok = wait_phase(bar, parity);
+  auto wait = [&](uint64_t* bar, uint32_t parity, int sum = 0) {
+    const bool ok = wait_sum(bar, parity, sum);
     if (!ok) set_status(DR_ERR_TIMEOUT);
     return __all_sync(0xffffffffu, ok) != 0;
   };
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int i = 0; i < C; ++i) part[(c0 + c + i) * 128 + row] = v[i];
     };
     for (int i = 0; i < walk.sums() && ok; ++i) {
-      if (!(ok = wait(&b_acc[i & 1], (i / 2) & 1))) break;
+      if (!(ok = wait(&b_acc[i & 1], (i / 2) & 1, FP32 ? 0 : n_k))) break;
       tc_fence_after();
       if constexpr (FP32) {
 #pragma unroll
@@ -306,7 +306,9 @@ cudaError_t few(const Operand& M, const Operand& N, Epilogue e, int split, cudaS
   cfg.dynamicSmemBytes = FewSmem<TN>::kBytes;
   cfg.stream = st;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tn, tm, e, g, (N.k + kBK - 1) / kBK);
+  err = cudaLaunchKernelEx(&cfg, kernel, tn, tm, e, g, (N.k + kBK - 1) / kBK);
+  if (err != cudaSuccess) cudaGetLastError();   // it is returned here, not by the next call
+  return err;
 }
 
 template <typename T, int TN>

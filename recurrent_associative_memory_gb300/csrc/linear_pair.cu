@@ -207,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (n0 + c < e.N) emit(c, acc + c);
       } else {
         const int buf = it & 1;
-        if (!(ok = wait(&b_acc[buf], (it / 2) & 1))) break;
+        if (!(ok = all(wait_sum(&b_acc[buf], (it / 2) & 1, n_k) || give_up()))) break;
         tc_fence_after();
         for (int c = 0; c < NC && n0 + c < e.N; c += 32) {
           float v[32];

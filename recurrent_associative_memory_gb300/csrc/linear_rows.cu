@@ -137,7 +137,9 @@ template <int MT, bool W_T> cudaError_t go(const Rows& a, const Epilogue& e, lon
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_rows_kernel<MT, W_T>, a, e);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, linear_rows_kernel<MT, W_T>, a, e);
+  if (err != cudaSuccess) cudaGetLastError();   // it is returned here, not by the next call
+  return err;
 }
 
 }  // namespace

@@ -116,6 +116,13 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// For an accumulator of n_k stages: the longest sums take seconds.
+__device__ __forceinline__ bool wait_sum(uint64_t* bar, uint32_t parity, int n_k) {
+  for (int i = 0; i <= n_k >> 20; ++i)
+    if (wait_phase(bar, parity)) return true;
+  return false;
+}
+
 // A box into this CTA's shared memory, its bytes counted on a barrier of either CTA.
 __device__ __forceinline__ void pair_load(void* dst, const void* tmap, uint32_t bar, int c0, int c1, int c2) {
   asm volatile(

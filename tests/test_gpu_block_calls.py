@@ -169,6 +169,19 @@ def test_linear_large_values(block):  # noqa: F811
                     np.testing.assert_allclose(np64(s), slope, atol=2e-3 if dtype is BF else 1e-5)
 
 
+@DT
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "sigmoid"])
+def test_linear_nan_reaches_its_slopes(block, act, dtype):  # noqa: F811
+    for M in (5, 300):
+        c = linear_case(M, M, 64, 136, dtype)
+        c["x"][2, 3] = math.nan
+        y, s = block.linear_fwd(c["x"], c["w"], c["bias"], act=act, want_slope=True)
+        rest = [i for i in range(M) if i != 2]
+        assert y[2].isnan().all() and s[2].isnan().all() and y[rest].isfinite().all() and s[rest].isfinite().all()
+        g = block.linear_bwd(c["x"], c["w"], c["d_y"], slope=s)
+        assert g["dx"][2].isnan().all() and g["dx"][rest].isfinite().all() and g["dweight"].isnan().all()
+
+
 # ------------------------------------------------------------------ norms around a block
 
 @TYPES

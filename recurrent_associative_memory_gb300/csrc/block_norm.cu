@@ -163,8 +163,9 @@ __device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, cons
 }
 
 // The rows of a block.  RING: one at a time, through a ring of `stages` of them in shared
-// memory.  Tensor i of a row is copied by warp i, once the block has passed a barrier behind
-// the reads of the row whose place it takes: the first one of the next row.  (What a copy costs
+// memory.  Tensor i of a row is copied by a thread of warp i (blocks of fewer warps: by a second
+// one of a warp), once the block has passed a barrier behind the reads of the row whose place it
+// takes: the first one of the next row.  (What a copy costs
 // its warp, the others wait for: issued by one thread for all tensors M16384 D4096 forward took
 // 156 us instead of 103, and with the addresses formed for each row M8192 D4096 backward 143
 // instead of 137.  A warp of its own would cost the others their registers.)
@@ -180,14 +181,14 @@ template <int N> struct Ring {
   int stage;
   uint32_t parity;
   bool lost;
-  // this warp's tensor: where its next copy comes from, and the one after it; its place in a
+  // this thread's tensor: where its next copy comes from, and the one after it; its place in a
   // stage; the bytes of a row, and of the tensor's last one
   uintptr_t from;
   long long from_step;
   uint32_t to, bytes, last_bytes;
   bool mine;
 
-  // One thread of a warp: that warp's tensor of `row`, the rows in their order.
+  // This thread's tensor of `row`, the rows in their order.
   __device__ __forceinline__ void issue(long long row, int s) {
     const uint32_t n = row == M - 1 ? last_bytes : bytes;
     umma::mbar_expect_tx(full + s, n);
@@ -211,7 +212,7 @@ template <int N> struct Ring {
   __device__ __forceinline__ void refill(long long row, long long first, long long step) {
     const long long next = row + (stages - 1) * step;
     if (mine && row > first && next < M) {
-      if (threadIdx.x % 32 == 0) issue(next, stage == 0 ? stages - 1 : stage - 1);
+      issue(next, stage == 0 ? stages - 1 : stage - 1);
       from += from_step;
     }
   }
@@ -338,7 +339,7 @@ __device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages
   for (int i = 0; i < N; ++i) {
     ring.off[i] = at;
     if (!ring.base[i]) continue;
-    if (static_cast<int>(threadIdx.x / 32) == i) {
+    if (static_cast<int>(threadIdx.x / 32 + threadIdx.x % 32 * (c.tpr / 32)) == i) {
       const RowCopy usual(ring.base[i], row, ring.stride[i], c.D, c.phase(), ring.es[i], -1);
       ring.mine = true;
       ring.from = usual.lo, ring.from_step = step * ring.stride[i] * ring.es[i];
@@ -355,7 +356,7 @@ __device__ __forceinline__ void start(Ring<N>& ring, uint64_t (&bars)[kMaxStages
   __syncthreads();
   if (ring.mine)
     for (int i = 0; i < l.stages && row + i * step < M; ++i) {
-      if (threadIdx.x % 32 == 0) ring.issue(row + i * step, i);
+      ring.issue(row + i * step, i);
       ring.from += ring.from_step;
     }
 }
@@ -625,9 +626,7 @@ struct Plan {
       for (tpr = 4; tpr < n; tpr *= 2) {}
       rows = kNarrow / tpr, threads = kNarrow;
     } else {
-      tpr = (n + 31) / 32 * 32;
-      if (tpr < 32 * 5) tpr = 32 * 5;   // a warp for each tensor's copies
-      threads = tpr;
+      tpr = threads = (n + 31) / 32 * 32;
     }
     with_ring = with_ring && n > 32 && order != kApart;
     int blocks = place / threads;

@@ -37,13 +37,21 @@ constexpr int kMaxRow = 8192;     // 512 threads of 16 columns
 enum { kEven, kOdd, kApart };
 template <int ORDER, int E> struct Columns {
   int D, tpr, t, phase_;
+  uint32_t valid;   // kOdd: which of its columns are the row's, a bit for each
+  __device__ __forceinline__ Columns(int D_, int tpr_, int t_, int phase) : D(D_), tpr(tpr_), t(t_), phase_(phase), valid(0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (ORDER == kOdd && in(at(e))) valid |= 1u << e;
+  }
   __device__ __forceinline__ int phase() const { return ORDER == kOdd ? phase_ : 0; }
   __device__ __forceinline__ int at(int e) const {
     return ORDER == kApart ? e * tpr + t : (e / 8 * tpr + t) * 8 + e % 8 - phase();
   }
   __device__ __forceinline__ bool in(int n) const { return (ORDER != kOdd || n >= 0) && n < D; }
-  // of a group from n on
-  __device__ __forceinline__ bool whole(int n) const { return ORDER == kEven ? n < D : n >= 0 && n + 8 <= D; }
+  // of the group from column e0 on, which is column n of the row
+  __device__ __forceinline__ bool whole(int e0, int n) const {
+    return ORDER == kEven ? n < D : (valid >> e0 & 255u) == 255u;
+  }
 };
 
 // Rows come into shared memory by background copies, from their first group on.  What a group
@@ -71,19 +79,20 @@ __device__ __forceinline__ void row_values(const void* base, long long row, long
   if constexpr (ORDER == kApart) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = c.in(c.at(e0 + e)) ? to_f(p[c.at(e0 + e)]) : 0.f;
-  } else if (RING && ORDER == kOdd ? n >= c.D || (row == M - 1 && !c.whole(n)) : !c.whole(n)) {
-    // a ring's copy does not hold what lies behind the row (threads that have no columns), nor
-    // of the tensor's last row a group that is not whole
+  } else if (RING && ORDER == kOdd ? row == M - 1 && !c.whole(e0, n) : !c.whole(e0, n)) {
+    // a ring's copy does not hold a group of the tensor's last row that is not whole
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = ORDER != kEven && c.in(n + e) ? to_f(p[n + e]) : 0.f;
   } else {
     uint32_t w[2 * sizeof(T)];
+    // a thread without columns reads those of the row's first group, and no bit of it stays
+    const int from = ORDER == kOdd && n >= c.D ? 0 : n + c.phase();
 #pragma unroll
     for (int i = 0; i < 2 * (int)sizeof(T); i += 4) {
       if constexpr (RING) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                     : "r"(at + (n + c.phase()) * (int)sizeof(T) + 4 * i)
+                     : "r"(at + from * (int)sizeof(T) + 4 * i)
                      : "memory");
       } else {
         const uint4 u = reinterpret_cast<const uint4*>(p + n)[i / 4];
@@ -92,12 +101,12 @@ __device__ __forceinline__ void row_values(const void* base, long long row, long
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(T) == 2) f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-      else f[e] = __uint_as_float(w[e]);
-    }
-    if (RING && ORDER == kOdd && !c.whole(n)) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = c.in(n + e) ? f[e] : 0.f;
+      uint32_t x;
+      if constexpr (sizeof(T) == 2) x = e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
+      else x = w[e];
+      // what is copied along of the neighbouring rows may be anything
+      if (RING && ORDER == kOdd) x &= static_cast<uint32_t>(static_cast<int32_t>(c.valid << (31 - e0 - e)) >> 31);
+      f[e] = __uint_as_float(x);
     }
   }
 #pragma unroll
@@ -126,7 +135,7 @@ template <int P, typename F> __device__ __forceinline__ void pairs(F&& f) {
 template <int ORDER, int E>
 __device__ __forceinline__ void load_vector(const float* p, const Columns<ORDER, E>& c, int e0, f2 (&r)[4]) {
   float f[8];
-  if (ORDER != kApart && c.whole(c.at(e0)) && (reinterpret_cast<uintptr_t>(p + c.at(e0)) & 15) == 0) {
+  if (ORDER != kApart && c.whole(e0, c.at(e0)) && (reinterpret_cast<uintptr_t>(p + c.at(e0)) & 15) == 0) {
     load8(p + c.at(e0), 1, f);
   } else {
 #pragma unroll
@@ -142,9 +151,13 @@ __device__ __forceinline__ void store_group(T* p, const Columns<ORDER, E>& c, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack2(r[i], f[2 * i], f[2 * i + 1]);
   const int n = c.at(e0);
-  if (ORDER != kApart && c.whole(n)) {
+  if (ORDER != kApart && c.whole(e0, n)) {
     store8(p + n, f);
-  } else if (ORDER != kEven) {
+  } else if (ORDER == kOdd) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c.valid >> (e0 + e) & 1u) p[n + e] = from_f<T>(f[e]);
+  } else if (ORDER == kApart) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c.in(c.at(e0 + e))) p[c.at(e0 + e)] = from_f<T>(f[e]);
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
   int turn = 0;
   const int rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
   const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
-  const Columns<ORDER, E> c{a.D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, a.D)};
+  const Columns<ORDER, E> c(a.D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, a.D));
   Ring<3> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s;
@@ -446,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   int turn = 0;
   const int D = a.D, rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
   const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
-  const Columns<ORDER, E> c{D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, D)};
+  const Columns<ORDER, E> c(D, tpr, static_cast<int>(threadIdx.x) - slot * tpr, phase_of(first + slot, D));
   Ring<5> ring;
   ring.base[0] = a.h, ring.base[1] = a.branch, ring.base[2] = a.gate, ring.base[3] = a.d_y, ring.base[4] = a.d_h;
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s, ring.stride[3] = ring.stride[4] = D;

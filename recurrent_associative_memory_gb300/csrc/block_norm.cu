@@ -16,6 +16,10 @@
 //   dbranch = rstd(branch) (q - v mean(q v))
 // A thread keeps its columns over all of its block's rows, so the two sums stay in registers;
 // the blocks leave one partial sum each, which a second kernel joins in order.
+//
+// bf16 with every part: forward M16384 D4096 106 us, 6.3 TB/s, memory bounds it; backward M8192
+// D4096 129 us, 4.1 TB/s: instructions (570 per warp and row) and three barriers a row, with 16
+// warps on an SM as the registers allow.
 #include <type_traits>
 
 #include "block.cuh"
@@ -178,11 +182,10 @@ __device__ __forceinline__ void store_row(T* p, const Columns<ORDER, E>& c, cons
 // The rows of a block.  RING: one at a time, through a ring of `stages` of them in shared
 // memory.  Tensor i of a row is copied by a thread of warp i (blocks of fewer warps: by a second
 // one of a warp), once the block has passed a barrier behind the reads of the row whose place it
-// takes: the first one of the next row.  (What a copy costs
-// its warp, the others wait for: issued by one thread for all tensors M16384 D4096 forward took
-// 156 us instead of 103, and with the addresses formed for each row M8192 D4096 backward 143
-// instead of 137.  A warp of its own would cost the others their registers.)
-// Otherwise straight from memory.
+// takes: the first one of the next row.  (What a copy costs its warp, the others wait for: issued
+// by one thread for all tensors M16384 D4096 forward took 156 us instead of 103, and with the
+// addresses formed for each row M8192 D4096 backward 143 instead of 137.  A warp of its own
+// would cost the others their registers.)  Otherwise straight from memory.
 template <int N> struct Ring {
   uint64_t* full;
   uint32_t at, stage_bytes;   // shared memory of stage 0; from stage to stage

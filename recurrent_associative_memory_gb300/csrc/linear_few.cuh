@@ -9,7 +9,8 @@
 //   warps 0-7  the accumulator to shared memory, then the sums and the epilogue, a row per warp
 //   warp 8     TMA, 4 to 11 stages of 64 k
 //   warp 9     the MMAs
-// Weights are what bounds it, 16 KB of each stage, so an SM keeps 200 KB of them under way.
+// Weights are what bounds it, 16 KB of each stage, so an SM keeps 200 KB of them under way: bf16
+// M64 K4096 N16384 29 us, 4.7 TB/s with the start and the end of its one wave; M1 K2048 N2048 8.6.
 #pragma once
 
 #include <type_traits>

@@ -4,8 +4,10 @@
 // Each CTA of a pair holds 128 rows of A and half of B's columns; one MMA of the pair
 // multiplies 256 x BN x 16 from both shared memories, so that a stage of 64 k moves
 // (128 + BN / 2) x 128 bytes into each SM for 512 (BN = 256) cycles of products: 64 bytes a
-// cycle, where one CTA by itself would need 96.  Accumulators are two buffers of BN columns of
-// TMEM: while the epilogue reads one, the next tile's products go to the other.
+// cycle, where one CTA by itself would need 96.  Accumulators take all of TMEM, two buffers of
+// 256 columns or four of 128: while the epilogue reads one, the products go on in the next.
+// (fp32, whose epilogue takes no more sums of 64 k while it stores a tile: M2048 K1024 N4096 with
+// all gradients 269 us with two buffers, 264 with four.)
 //   warps 0-7  epilogue: rows 32 (w mod 4) .. of the CTA's 128, a thread per row, and half of
 //              the columns each
 //   warp 8     TMA: this CTA's part of each stage, counted on the first CTA's barrier
@@ -51,23 +53,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        Tiles tiles, int n_k) {
   using L = Smem<BN>;
   using S = typename std::conditional<sizeof(T) == 2, __half, float>::type;
-  constexpr int NS = L::kStages;
+  constexpr int NS = L::kStages, NB = 512 / BN;
   constexpr bool FP32 = sizeof(T) == 4;
   const Walk<FP32> walk{n_k};
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[2], b_free[2], b_end;
+  __shared__ uint64_t b_full[NS], b_empty[NS], b_acc[NB], b_free[NB], b_end;
   __shared__ uint32_t s_tmem;
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&b_acc[i], 1), mbar_init(&b_free[i], 2 * kEpilogueWarps);
+    for (int i = 0; i < NB; ++i) mbar_init(&b_acc[i], 1), mbar_init(&b_free[i], 2 * kEpilogueWarps);
     mbar_init(&b_end, 1);
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) pair_tmem_alloc(&s_tmem, 2 * BN);
+  if (warp == kMmaWarp) pair_tmem_alloc(&s_tmem, NB * BN);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -188,8 +190,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (FP32) {
         float acc[NC];
         for (int i = 0; i < n_k && ok; ++i, ++it) {
-          const int buf = it & 1;
-          if (!(ok = wait(&b_acc[buf], (it / 2) & 1))) break;
+          const int buf = it % NB;
+          if (!(ok = wait(&b_acc[buf], (it / NB) & 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < NC; c += 32) {
@@ -206,8 +208,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < NC; c += 32)
           if (n0 + c < e.N) emit(c, acc + c);
       } else {
-        const int buf = it & 1;
-        if (!(ok = all(wait_sum(&b_acc[buf], (it / 2) & 1, n_k) || give_up()))) break;
+        const int buf = it % NB;
+        if (!(ok = all(wait_sum(&b_acc[buf], (it / NB) & 1, n_k) || give_up()))) break;
         tc_fence_after();
         for (int c = 0; c < NC && n0 + c < e.N; c += 32) {
           float v[32];
@@ -268,8 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int t = first; t < n_tile && ok; t += step) {
       for (int i = 0; i < walk.sums() && ok; ++i, ++it) {
-        const int buf = it & 1;
-        if (it >= 2 && !(ok = all(wait_cluster(&b_free[buf], (it / 2 - 1) & 1) || give_up()))) break;
+        const int buf = it % NB;
+        if (it >= NB && !(ok = all(wait_cluster(&b_free[buf], (it / NB - 1) & 1) || give_up()))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
         auto full = [&](uint32_t s, uint32_t parity) {
@@ -303,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();   // nothing of this CTA is read or counted on any more
   tc_fence_after();
-  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 2 * BN);
+  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, NB * BN);
 }
 
 template <int BN, bool A_MN, bool B_MN, typename T, bool FULL>

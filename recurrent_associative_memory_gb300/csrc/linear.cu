@@ -104,7 +104,7 @@ cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, i
     }
   }
   if (tn) return (fp32 ? launch_linear_few_fp32 : launch_linear_few_bf16)(tn, A, B, e, full, split, st);
-  e.vec = e.N * es % 32 == 0 && on32(e.C, e.res) && on32(e.slope) && (!e.res || e.r_m * es % 32 == 0);
+  e.vec = e.N % 16 == 0 && on32(e.C, e.res) && on32(e.slope) && (!e.res || e.r_m * es % 32 == 0);
   return launch_linear_pair(bn, A, B, e, full, sms, st);
 }
 

@@ -48,7 +48,8 @@ struct Epilogue {
   void* slope;
   int M, N, act;
   long long r_m;       // C and the slope have rows of N
-  int vec;             // 32-byte accesses: every row of C, res and slope starts on 32 bytes
+  int vec;             // 16 columns at once by 32-byte accesses: N is a multiple of 16, every row of C, res
+                       // and slope starts on 32 bytes
 };
 
 inline bool make_operand_map(CUtensorMap* m, const Operand& o, int box_rows) {

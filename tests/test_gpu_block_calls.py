@@ -106,6 +106,29 @@ def test_linear_buffers(block, dtype):  # noqa: F811
 
 
 @DT
+@pytest.mark.parametrize("M,K,N", [(3000, 520, 264), (2600, 1032, 2056), (5000, 24, 40), (3001, 515, 1028), (2600, 136, 1112)])
+def test_linear_writes_no_more(block, M, K, N, dtype):  # noqa: F811
+    """Rows of every remainder of 16 columns: nothing behind a result is written, and the same
+    bits come each time."""
+    c = linear_case(M, M, K, N, dtype)
+    S = torch.float16 if dtype is BF else torch.float32
+
+    def run():
+        flat = {k: torch.full((rows * cols + 256,), 7.0, dtype=t, device="cuda")
+                for k, rows, cols, t in (("y", M, N, dtype), ("slope", M, N, S), ("dx", M, K, dtype), ("dweight", K, N, dtype))}
+        buf = {k: f[:-256].view(-1, K if k == "dx" else N) for k, f in flat.items()}
+        block.linear_fwd(c["x"], c["w"], c["bias"], act="silu", residual=c["residual"], y=buf["y"], slope=buf["slope"])
+        block.linear_bwd(c["x"], c["w"], c["d_y"], slope=buf["slope"], grads={k: buf[k] for k in ("dx", "dweight")})
+        for k, f in flat.items():
+            assert bool((f[-256:] == 7).all()), k
+        return flat
+
+    first, again = run(), run()
+    assert all(torch.equal(first[k], again[k]) for k in first)
+    check_linear(block, c, "silu")
+
+
+@DT
 def test_linear_refuses(block, dtype):  # noqa: F811
     c = linear_case(3, 10, 32, 24, dtype)
     x, w, b = c["x"], c["w"], c["bias"]

@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   using Row = f2[P];
   __shared__ float buf[2][32];
   __shared__ uint64_t bars[kMaxStages];
+  let_next_start();
   int turn = 0;
   const int D = a.D, rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
   const long long step = (long long)gridDim.x * rows, first = (long long)blockIdx.x * rows;
@@ -584,6 +585,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
 __global__ void __launch_bounds__(1024) join_parts_kernel(const float* part, int blocks, int D, const float* scale,
                                                           const float* post_w, float* d_scale, float* d_post, float* d_pre) {
   __shared__ float buf[32][33];
+  wait_for_last();
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32, which = blockIdx.y;
   if (which == 0 ? !d_scale && !d_post : !d_pre) return;
   const int c = blockIdx.x * 32 + lane;
@@ -735,8 +737,8 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype
     });
   });
   if (err != cudaSuccess || !a.part) return err;
-  join_parts_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, st>>>(a.part, grid, a.D, a.scale, a.post_w, d_scale, d_post, d_pre);
-  return cudaGetLastError();
+  return launch_in_call(true, join_parts_kernel, dim3((a.D + 31) / 32, 2), 1024, 0, st, 0, a.part, grid, a.D, a.scale, a.post_w,
+                        d_scale, d_post, d_pre);
 }
 
 }  // namespace dr

@@ -3,7 +3,7 @@
 
 namespace dr {
 
-cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, cudaStream_t st);
+cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, bool after, cudaStream_t st);
 int linear_slope_blocks(int M);
 cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int pitch, long long piece, float* part,
                                 cudaStream_t st);
@@ -20,6 +20,7 @@ namespace {
 
 using lin::Epilogue;
 using lin::Operand;
+using lin::Place;
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -52,12 +53,15 @@ struct Packed {
 Packed pack_x(const LinearArgs& a, int dtype) { return {dtype, a.M, a.K, a.x_s}; }
 // The copies that one or both of two matrices need.
 cudaError_t make(Packed* a, const void** pa, void* to_a, Packed* b, const void** pb, void* to_b, int dtype, int sms,
-                 cudaStream_t st) {
+                 Place& place, cudaStream_t st) {
   PackJob j[2]{};
   int n = 0;
   if (a && a->copy) j[n++] = a->job(*pa, to_a);
   if (b && b->copy) j[n++] = b->job(*pb, to_b);
-  return n ? launch_linear_pack(j[0], j[1], dtype, sms, st) : cudaSuccess;
+  if (!n) return cudaSuccess;
+  const bool after = place != lin::kFirst;
+  place = lin::kAfter;
+  return launch_linear_pack(j[0], j[1], dtype, sms, after, st);
 }
 
 Packed pack_w(const LinearArgs& a, int dtype) { return {dtype, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, a.w_s}; }
@@ -136,10 +140,11 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, int dtype, int sms, void* wor
   char* ws = static_cast<char*>(workspace);
   Packed px = pack_x(a, dtype), pw = pack_w(a, dtype);
   const void *x = a.x, *w = a.w;
-  cudaError_t e = make(&px, &x, ws, &pw, &w, ws + px.bytes, dtype, sms, st);
+  Place place = lin::kFirst;
+  cudaError_t e = make(&px, &x, ws, &pw, &w, ws + px.bytes, dtype, sms, place, st);
   if (e != cudaSuccess) return e;
   return product(px.k_cols(x), a.w_t ? pw.k_cols(w) : pw.k_rows(w),
-                 Epilogue{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, a.r_s, 0}, true, dtype, sms, st);
+                 Epilogue{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, place, a.r_s}, true, dtype, sms, st);
 }
 
 size_t linear_bwd_workspace(const LinearArgs& a, int dtype, bool act) { return BwdPlan(a, dtype, act).bytes; }
@@ -149,21 +154,23 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, int dtype, int sms, void* wor
   char* ws = static_cast<char*>(workspace);
   const bool keep = p.keep_d && (a.dx || a.dw);
   cudaError_t e = cudaSuccess;
+  Place place = lin::kFirst;
   if (keep || a.db)
-    e = launch_linear_slope(a, dtype, keep ? ws + p.o_d : nullptr, p.pitch, p.piece,
+    place = lin::kAfter, e = launch_linear_slope(a, dtype, keep ? ws + p.o_d : nullptr, p.pitch, p.piece,
                             a.db ? reinterpret_cast<float*>(ws + p.o_part) : nullptr, st);
   const void* d = keep ? ws + p.o_d : a.d_y;
   const Operand rows{d, a.M, a.N, keep ? p.pitch : a.N, false, p.piece};   // k along the channels out
   const Operand cols{d, a.N, a.M, keep ? p.pitch : a.N, true, p.piece};    // k along the tokens
   const void *x = a.x, *w = a.w;
   if (e == cudaSuccess)
-    e = make(a.dw ? &p.x : nullptr, &x, ws + p.o_x, a.dx ? &p.w : nullptr, &w, ws + p.o_w, dtype, sms, st);
+    e = make(a.dw ? &p.x : nullptr, &x, ws + p.o_x, a.dx ? &p.w : nullptr, &w, ws + p.o_w, dtype, sms, place, st);
   if (a.dx && e == cudaSuccess)   // dx[m,k] = sum over n of d[m,n] W[k,n]
-    e = product(rows, a.w_t ? p.w.k_rows(w) : p.w.k_cols(w), Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K}, false,
+    e = product(rows, a.w_t ? p.w.k_rows(w) : p.w.k_cols(w), Epilogue{a.dx, nullptr, nullptr, nullptr, a.M, a.K, 0, place}, false,
                 dtype, sms, st);
   if (a.dw && e == cudaSuccess)   // dw[k,n] = sum over m of x[m,k] d[m,n], in W's order
     e = product(a.w_t ? cols : p.x.k_rows(x), a.w_t ? p.x.k_rows(x) : cols,
-                Epilogue{a.dw, nullptr, nullptr, nullptr, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N}, false, dtype, sms, st);
+                Epilogue{a.dw, nullptr, nullptr, nullptr, a.w_t ? a.N : a.K, a.w_t ? a.K : a.N, 0, a.dx ? lin::kBeside : place},
+                false, dtype, sms, st);
   return e;
 }
 

@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (e.place != kBeside) wait_for_last(), let_next_start();
   const uint32_t tmem = uniform(s_tmem);
   auto wait = [&](uint64_t* bar, uint32_t parity, int sum = 0) {
     const bool ok = wait_sum(bar, parity, sum);
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   __syncwarp();
   cluster_sync();   // nobody reads this CTA's part any more
+  if (e.place == kBeside) wait_for_last();   // whoever waits for this kernel waits for that one too
 }
 
 template <int TN, bool N_MN, bool M_MN, typename T, bool FULL>
@@ -298,18 +300,8 @@ cudaError_t few(const Operand& M, const Operand& N, Epilogue e, int split, cudaS
   if (err != cudaSuccess) return err;
   const FewGrid g{(M.rows + TN - 1) / TN, split};
   e.vec = e.N % 4 == 0 && (!e.res || e.r_m % 4 == 0);   // four columns at once
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(g.tiles_m * ((N.rows + 127LL) / 128) * split));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = FewSmem<TN>::kBytes;
-  cfg.stream = st;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kernel, tn, tm, e, g, (N.k + kBK - 1) / kBK);
-  if (err != cudaSuccess) cudaGetLastError();   // it is returned here, not by the next call
-  return err;
+  return launch_in_call(e.place != kFirst, kernel, dim3(static_cast<unsigned>(g.tiles_m * ((N.rows + 127LL) / 128) * split)),
+                        kFewThreads, FewSmem<TN>::kBytes, st, split, tn, tm, e, g, (N.k + kBK - 1) / kBK);
 }
 
 template <typename T, int TN>

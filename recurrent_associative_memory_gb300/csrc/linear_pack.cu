@@ -68,12 +68,14 @@ __device__ __forceinline__ void pack_one(const PackJob& j, long long i, long lon
 }
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(PackJob a, PackJob b, int blocks_a) {
+  let_next_start();
   const bool first = static_cast<int>(blockIdx.x) < blocks_a;
   const PackJob& j = first ? a : b;
   const long long at = (long long)(blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
   const long long step = (long long)(first ? blocks_a : gridDim.x - blocks_a) * 256;
   if (j.cols % 8 == 0 && j.stride % (16 / (int)sizeof(T)) == 0) pack_one<T, true>(j, at, step);
   else pack_one<T, false>(j, at, step);
+  wait_for_last();   // nothing here reads what that one writes, but whoever waits for this waits for both
 }
 
 // d = d_y * slope [M,N] in pieces with rows of `pitch` (dst null: not kept), and the columns'
@@ -82,6 +84,7 @@ __global__ void __launch_bounds__(256) pack_kernel(PackJob a, PackJob b, int blo
 template <typename T, typename S, bool VEC>
 __global__ void __launch_bounds__(256) slope_kernel(const T* d_y, const S* slope, __nv_bfloat16* dst, int pitch,
                                                     long long piece, float* part, int M, int N) {
+  let_next_start();
   __shared__ float buf[8][256];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col_blocks = (N + 255) / 256;
   const int c = blockIdx.x % col_blocks * 256 + lane * 8;
@@ -120,6 +123,8 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* d_y, const S* slope
 template <typename T>
 __global__ void __launch_bounds__(1024) join_bias_kernel(const float* part, int blocks, int N, T* db) {
   __shared__ float buf[32][33];
+  let_next_start();
+  wait_for_last();
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32, n = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (n < N)
@@ -134,15 +139,14 @@ __global__ void __launch_bounds__(1024) join_bias_kernel(const float* part, int 
 }  // namespace
 
 // One or two (b.src null: one) copies in one launch.
-cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, cudaStream_t st) {
+cudaError_t launch_linear_pack(const PackJob& a, const PackJob& b, int dtype, int sms, bool after, cudaStream_t st) {
   auto blocks = [&](const PackJob& j) {
     const long long n = j.src ? ((long long)j.rows * (j.pitch / 8) + 255) / 256 : 0;
     return static_cast<int>(min(n, 16LL * sms));
   };
   const int na = blocks(a), nb = blocks(b);
-  if (dtype == DR_FP32) pack_kernel<float><<<na + nb, 256, 0, st>>>(a, b, na);
-  else pack_kernel<__nv_bfloat16><<<na + nb, 256, 0, st>>>(a, b, na);
-  return cudaGetLastError();
+  return launch_in_call(after, dtype == DR_FP32 ? pack_kernel<float> : pack_kernel<__nv_bfloat16>, na + nb, 256, 0, st, 0, a,
+                        b, na);
 }
 
 int linear_slope_blocks(int M) { return static_cast<int>((M + (long long)kRows - 1) / kRows); }
@@ -154,17 +158,16 @@ cudaError_t launch_linear_slope(const LinearArgs& a, int dtype, void* dst, int p
   const unsigned grid = static_cast<unsigned>(blocks * ((a.N + 255LL) / 256));
   const bool vec = a.N % 8 == 0;
   auto* d = static_cast<__nv_bfloat16*>(dst);
-  if (dtype == DR_FP32) {
-    auto* k = vec ? slope_kernel<float, float, true> : slope_kernel<float, float, false>;
-    k<<<grid, 256, 0, st>>>(static_cast<const float*>(a.d_y), static_cast<const float*>(a.slope), d, pitch, piece, part, a.M, a.N);
-    if (part) join_bias_kernel<<<(a.N + 31) / 32, 1024, 0, st>>>(part, blocks, a.N, static_cast<float*>(a.db));
-  } else {
-    auto* k = vec ? slope_kernel<__nv_bfloat16, __half, true> : slope_kernel<__nv_bfloat16, __half, false>;
-    k<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(a.d_y), static_cast<const __half*>(a.slope), d, pitch, piece,
-                            part, a.M, a.N);
-    if (part) join_bias_kernel<<<(a.N + 31) / 32, 1024, 0, st>>>(part, blocks, a.N, static_cast<__nv_bfloat16*>(a.db));
-  }
-  return cudaGetLastError();
+  auto go = [&](auto* kernel, auto t, auto s) {
+    using T = decltype(t);
+    cudaError_t e = launch_in_call(false, kernel, grid, 256, 0, st, 0, static_cast<const T*>(a.d_y),
+                                   static_cast<const decltype(s)*>(a.slope), d, pitch, piece, part, a.M, a.N);
+    if (e != cudaSuccess || !part) return e;
+    return launch_in_call(true, join_bias_kernel<T>, (a.N + 31) / 32, 1024, 0, st, 0, part, blocks, a.N, static_cast<T*>(a.db));
+  };
+  if (dtype == DR_FP32) return go(vec ? slope_kernel<float, float, true> : slope_kernel<float, float, false>, 0.f, 0.f);
+  using B = __nv_bfloat16;
+  return go(vec ? slope_kernel<B, __half, true> : slope_kernel<B, __half, false>, B{}, __half{});
 }
 
 }  // namespace dr

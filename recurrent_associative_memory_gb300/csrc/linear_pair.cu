@@ -74,6 +74,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  if (e.place != kBeside) wait_for_last(), let_next_start();
   const uint32_t tmem = uniform(s_tmem);
   const int n_tile = tiles.m * tiles.n, first = blockIdx.x / 2, step = gridDim.x / 2;
 
@@ -306,6 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();   // nothing of this CTA is read or counted on any more
   tc_fence_after();
   if (warp == kMmaWarp) pair_tmem_dealloc(tmem, NB * BN);
+  if (e.place == kBeside) wait_for_last();   // whoever waits for this kernel waits for that one too
 }
 
 template <int BN, bool A_MN, bool B_MN, typename T, bool FULL>
@@ -317,8 +319,8 @@ cudaError_t go(const Operand& A, const Operand& B, const Epilogue& e, int sms, c
   if (err != cudaSuccess) return err;
   const Tiles t{(A.rows + 255) / 256, (B.rows + BN - 1) / BN};
   const int pairs = static_cast<int>(min((long long)t.m * t.n, sms / 2LL));
-  kernel<<<2 * pairs, kThreads, Smem<BN>::kBytes, st>>>(a, b, e, t, (A.k + kBK - 1) / kBK);
-  return cudaGetLastError();
+  return launch_in_call(e.place != kFirst, kernel, 2 * pairs, kThreads, Smem<BN>::kBytes, st, 0, a, b, e, t,
+                        (A.k + kBK - 1) / kBK);
 }
 
 template <typename T, int BN>

@@ -158,7 +158,7 @@ cudaError_t launch_linear_rows(const LinearArgs& a, int sms, cudaStream_t st) {
   int split = 1;
   while (split < 8 && tiles * split < 2LL * sms && 128LL * 2 * split <= a.K) split *= 2;
   const Rows r{static_cast<const float*>(a.x), static_cast<const float*>(a.w), a.x_s, a.w_s, a.K, split};
-  const Epilogue e{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, a.r_s, 0};
+  const Epilogue e{a.y, a.bias, a.res, a.slope, a.M, a.N, a.act, lin::kFirst, a.r_s};
   auto order = [&](auto mt) {
     constexpr int MT = decltype(mt)::value;
     return a.w_t ? go<MT, true>(r, e, tiles, st) : go<MT, false>(r, e, tiles, st);

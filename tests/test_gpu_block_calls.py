@@ -129,6 +129,34 @@ def test_linear_writes_no_more(block, M, K, N, dtype):  # noqa: F811
 
 
 @DT
+@pytest.mark.parametrize("M,K,N", [(3000, 520, 264), (700, 2000, 1100), (300, 4000, 24), (90, 64, 2000)])
+def test_linear_gradients_read_at_once(block, M, K, N, dtype):  # noqa: F811
+    """What the stream does next finds every gradient done, dx (the first product) too, and the
+    next call on the same workspace and buffers leaves those before as they were."""
+    from recurrent_associative_memory_gb300 import dr
+    a = dr.DrLinear(int(dtype is BF), 2, M, K, N, 0, K, N, 0)
+    ws = torch.empty(dr.dr_linear_bwd_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    cases, want = [linear_case(M + i, M, K, N, dtype) for i in range(3)], []
+    for c in cases:
+        c["slope"] = block.linear_fwd(c["x"], c["w"], c["bias"], act="silu", want_slope=True)[1]
+        torch.cuda.synchronize()
+        g = block.linear_bwd(c["x"], c["w"], c["d_y"], slope=c["slope"])
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in g.items()})
+    buffers = {k: torch.empty_like(v) for k, v in want[0].items()}
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        c = cases[i % 3]
+        for b in buffers.values():
+            b.fill_(float("nan"))
+        block.linear_bwd(c["x"], c["w"], c["d_y"], slope=c["slope"], grads=buffers, workspace=ws)
+        got.append({k: buffers[k].clone() for k in ("dx", "dbias", "dweight")})
+    for i, g in enumerate(got):
+        assert all(torch.equal(g[k], want[i % 3][k]) for k in g), i
+
+
+@DT
 def test_linear_refuses(block, dtype):  # noqa: F811
     c = linear_case(3, 10, 32, 24, dtype)
     x, w, b = c["x"], c["w"], c["bias"]

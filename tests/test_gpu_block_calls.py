@@ -106,7 +106,8 @@ def test_linear_buffers(block, dtype):  # noqa: F811
 
 
 @DT
-@pytest.mark.parametrize("M,K,N", [(3000, 520, 264), (2600, 1032, 2056), (5000, 24, 40), (3001, 515, 1028), (2600, 136, 1112)])
+@pytest.mark.parametrize("M,K,N", [(3000, 520, 264), (2600, 1032, 2056), (5000, 24, 40), (3001, 515, 1028), (2600, 136, 1112),
+                                   (1, 264, 132), (7, 77, 515), (8, 520, 1028), (60, 1032, 130), (201, 333, 777)])
 def test_linear_writes_no_more(block, M, K, N, dtype):  # noqa: F811
     """Rows of every remainder of 16 columns: nothing behind a result is written, and the same
     bits come each time."""
@@ -276,6 +277,25 @@ def test_norm_strides(block, D, dtype, h_dtype):  # noqa: F811
     y, _ = block.block_norm_fwd(plain["h"], one.expand(shape))
     y2, _ = block.block_norm_fwd(plain["h"], one.expand(shape).contiguous())
     np.testing.assert_allclose(np64(y), np64(y2), rtol=2.0 ** -7 if dtype is BF else 1e-5, atol=1e-5)
+
+
+@TYPES
+@pytest.mark.parametrize("M,D", [(1, 7), (5, 264), (3, 1111), (40, 333), (2, 4097), (333, 24), (700, 8192), (401, 2047)])
+def test_norm_writes_no_more(block, M, D, dtype, h_dtype):  # noqa: F811
+    """Neither before nor behind a result, on 16 bytes (264 values) or not."""
+    c, d = norm_case(M, M, D, dtype, h_dtype)
+    n = M * D
+    types = dict(h_out=h_dtype, y=dtype, dh=h_dtype, dbranch=dtype, dgate=dtype)
+    for pad in (264, 259):
+        flat = {k: torch.full((n + 2 * pad,), 7.0, dtype=t, device="cuda") for k, t in types.items()}
+        flat |= {k: torch.full((D + 2 * pad,), 7.0, device="cuda") for k in ("dscale", "dpost_weight", "dpre_weight")}
+        buf = {k: f[pad:-pad].view((M, D) if k in types else (D,)) for k, f in flat.items()}
+        kw = dict(gate_act="silu", post_norm=True)
+        block.block_norm_fwd(**c, **kw, h_out=buf["h_out"], y=buf["y"])
+        block.block_norm_bwd(**c, **d, **kw, grads={k: b for k, b in buf.items() if k[0] == "d"})
+        for k, f in flat.items():
+            assert bool((f[:pad] == 7).all()) and bool((f[-pad:] == 7).all()), k
+            assert bool((buf[k] != 7).any()), k
 
 
 @TYPES

@@ -251,11 +251,19 @@ template <int N> struct Ring {
   }
 };
 
+__device__ __forceinline__ void clear(float (&bufs)[2][32]) {   // the parts of warps that a block has not
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) bufs[i / 32][i % 32] = 0.f;
+  __syncthreads();
+}
+
 // One or two sums over the threads of a row at once, the same in each of them.  Rows of up to
 // 32 threads stay within a warp; a wider one has its block to itself and goes through shared
 // memory, two buffers in turn so that one barrier does: whoever writes a buffer again has
 // passed the other one's barrier, which everyone reached after reading the first.
-// Two sums share the shuffles: after the first each half of a warp has one of them.
+// Two sums share the shuffles: after the first each half of a warp has one of them.  One sum's
+// parts every thread adds up for itself, 16 values at the same addresses for all: shorter than
+// four more shuffles (bf16 M32768 D1024 70 + 126 -> 66 + 122 us, M2731 D1111 35 -> 33), two
+// sums' were not (M65536 D300 153 us, so 162).
 template <bool WIDE, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2][32], int& turn) {
   static_assert(N <= 2, "");
@@ -282,11 +290,24 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (&bufs)[2
     x = half(x);
     if (lane % 16 == 0 && (N == 2 || !up)) buf[(up ? 16 : 0) + warp] = x;
     __syncthreads();
-    // 16 warps at most: a sum's parts are one half's
-    x = (lane & 15) * 32 < tpr && (N == 2 || !up) ? buf[lane] : 0.f;
-    x = half(x);
+    if constexpr (N == 1) {
+      f2 q[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, 16 * i);
+      for (int i = 0; i < 4; ++i) {
+        const float4 u = reinterpret_cast<const float4*>(buf)[i];
+        q[2 * i] = pack2(u.x, u.y), q[2 * i + 1] = pack2(u.z, u.w);
+      }
+#pragma unroll
+      for (int n = 4; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) q[i] = add2(q[i], q[i + n]);
+      unpack2(q[0], v[0], x);
+      v[0] += x;
+    } else {   // 16 warps at most: a sum's parts are one half's
+      x = half((lane & 15) * 32 < tpr ? buf[lane] : 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, 16 * i);
+    }
   }
 }
 
@@ -385,7 +406,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
   constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart;
   constexpr int P = E / 2;
   using Row = f2[P];
-  __shared__ float buf[2][32];
+  __shared__ __align__(16) float buf[2][32];
+  if (WIDE) clear(buf);
   __shared__ uint64_t bars[kMaxStages];
   int turn = 0;
   const int rows = WIDE ? 1 : kNarrow / tpr, slot = WIDE ? 0 : threadIdx.x / tpr;
@@ -457,7 +479,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart && ring_holds<TH, E>();
   constexpr int P = E / 2;
   using Row = f2[P];
-  __shared__ float buf[2][32];
+  __shared__ __align__(16) float buf[2][32];
+  if (WIDE) clear(buf);
   __shared__ uint64_t bars[kMaxStages];
   let_next_start();
   int turn = 0;

@@ -477,6 +477,7 @@ template <typename TH, int E> __host__ __device__ constexpr bool ring_holds() { 
 template <typename TA, typename TH, int ORDER, int E, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
   constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart && ring_holds<TH, E>();
+  constexpr bool AGAIN = RING && E > 8;   // the branch is read twice, not kept (182 -> 168 us)
   constexpr int P = E / 2;
   using Row = f2[P];
   __shared__ __align__(16) float buf[2][32];
@@ -492,20 +493,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   ring.stride[0] = a.h_s, ring.stride[1] = a.b_s, ring.stride[2] = a.g_s, ring.stride[3] = ring.stride[4] = D;
   ring.es[0] = ring.es[4] = sizeof(TH), ring.es[1] = ring.es[2] = ring.es[3] = sizeof(TA);
   if (RING) start(ring, bars, l, c, first, step, a.M);
-  Row sum_s, sum_p, ws, wy;   // S, the sum of dpre_w; scale post_w, pre_w
-  fill(sum_s, 0.f), fill(sum_p, 0.f), fill(ws, 1.f), fill(wy, 1.f);
-  if (a.pre_w) load_vector(a.pre_w, c, wy);
-  if (a.scale) load_vector(a.scale, c, ws);
+  Row sum_s, sum_p;   // S, the sum of dpre_w
+  Row ws_r, wy_r;     // scale post_w, pre_w
+  fill(sum_s, 0.f), fill(sum_p, 0.f), fill(ws_r, 1.f), fill(wy_r, 1.f);
+  if (a.pre_w) load_vector(a.pre_w, c, wy_r);
+  if (a.scale) load_vector(a.scale, c, ws_r);
   if (a.post_w) {
     Row w;
     load_vector(a.post_w, c, w);
-    pairs<P>([&](int i) { ws[i] = mul2(ws[i], w[i]); });
+    pairs<P>([&](int i) { ws_r[i] = mul2(ws_r[i], w[i]); });
   }
+  // 16 columns' weights would be spilled: they stay in shared memory behind the ring, where each
+  // thread reads its own (bf16 M4096 D8192 217 -> 182 us, M2048 with an fp32 stream 150 -> 129)
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  f2* own = reinterpret_cast<f2*>(dynamic + (RING ? l.stages * l.stage_bytes : 0)) + threadIdx.x;
+  if (E > 8)
+    pairs<P>([&](int i) { own[i * blockDim.x] = ws_r[i], own[(P + i) * blockDim.x] = wy_r[i]; });
+  auto ws = [&](int i) { return E > 8 ? own[i * blockDim.x] : ws_r[i]; };
+  auto wy = [&](int i) { return E > 8 ? own[(P + i) * blockDim.x] : wy_r[i]; };
   long long row = first + slot;
   for (long long r0 = first; r0 < a.M; r0 += step, row += step) {
     const bool live = WIDE || row < a.M;
     // a row that is none: zeros, so that it adds nothing to any sum
-    Row h, v, f, vs, g;   // vs: v f'(gate)
+    Row h, v, f, vs, g;   // vs: v f'(gate); AGAIN: f'(gate) until v is there again
     float rstd_b = 1.f;
     if (!WIDE) fill(h, 0.f), fill(v, 0.f);
     if (RING) ring.wait();
@@ -523,17 +533,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
         if (!WIDE) fill(z, 0.f);
         if (live) ring.template get<TA, RING>(2, row, c, z);
         gate_of<true>(a.gate_act, z, f, vs);
-        pairs<P>([&](int i) { vs[i] = mul2(vs[i], v[i]); });
+        if (!AGAIN) pairs<P>([&](int i) { vs[i] = mul2(vs[i], v[i]); });
       } else {
         fill(f, 1.f);
       }
-      pairs<P>([&](int i) { h[i] = fma2(mul2(f[i], v[i]), ws[i], h[i]); });
+      pairs<P>([&](int i) { h[i] = fma2(mul2(f[i], v[i]), ws(i), h[i]); });
     }
     if (a.d_y) {
       Row dy, t;
       if (!WIDE) fill(dy, 0.f);
       if (live) ring.template get<TA, RING>(3, row, c, dy);
-      pairs<P>([&](int i) { t[i] = mul2(dy[i], wy[i]); });
+      pairs<P>([&](int i) { t[i] = mul2(dy[i], wy(i)); });
       float s[2] = {dot(h, h), dot(t, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
@@ -555,11 +565,20 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       if (live) ring.template get<TH, RING>(4, row, c, g);
       if (RING) __syncthreads();
     }
-    if (RING) ring.refill(row, first, step), ring.next();
+    if (RING) ring.refill(row, first, step);
+    if (RING && !AGAIN) ring.next();
     if (live && a.dh) store_row(static_cast<TH*>(a.dh) + row * D, c, g);
-    if (!a.branch) continue;
+    if (!a.branch) {
+      if (RING && AGAIN) ring.next();
+      continue;
+    }
+    if (AGAIN) {
+      ring.template get<TA, RING>(1, row, c, v);
+      if (a.post_norm) pairs<P>([&](int i) { v[i] = mul2(v[i], both(rstd_b)); });
+      if (a.gate) pairs<P>([&](int i) { vs[i] = mul2(vs[i], v[i]); });
+    }
     pairs<P>([&](int i) {
-      const f2 x = mul2(g[i], ws[i]);
+      const f2 x = mul2(g[i], ws(i));
       sum_s[i] = fma2(g[i], mul2(f[i], v[i]), sum_s[i]);
       if (a.gate) vs[i] = mul2(x, vs[i]);
       g[i] = mul2(x, f[i]);   // q from here on
@@ -571,6 +590,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       const f2 k = both(-s[0] * a.inv_d * rstd_b), r2 = both(rstd_b);
       pairs<P>([&](int i) { g[i] = fma2(k, v[i], mul2(r2, g[i])); });
     }
+    if (RING && AGAIN) ring.next();
     if (live && a.db) store_row(static_cast<TA*>(a.db) + row * D, c, g);
   }
   if (RING) ring.drain();
@@ -591,8 +611,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   if constexpr (WIDE) {
     each(part);
   } else {   // the block's rows, one after another
-    extern __shared__ __align__(16) uint8_t dynamic[];   // [rows][2][D]
-    float* slots = reinterpret_cast<float*>(dynamic);
+    float* slots = reinterpret_cast<float*>(dynamic);   // [rows][2][D]
     each(slots + slot * 2 * D);
     __syncthreads();
     for (int n = threadIdx.x; n < 2 * D; n += kNarrow) {
@@ -656,11 +675,13 @@ template <typename F> void by_type(int dtype, int h_dtype, int order, F&& go) {
 // A launch: blocks that stay on every SM, in the place of `place` threads, and the rows on their
 // way in what each of them has of its shared memory, two at least (a row's place goes to the
 // next but one while the next is worked on); for that fewer blocks share an SM.
+constexpr int kShared = 227 * 1024 - 512;   // of an SM, for what a launch asks for
+
 struct Plan {
   int tpr, threads, grid;
   RingLayout ring;
   size_t smem;
-  Plan(const BlockNormArgs& a, int sms, int order, int e, int place, bool with_ring, int row_bytes, bool sums) {
+  Plan(const BlockNormArgs& a, int sms, int order, int e, int place, bool with_ring, int row_bytes, bool sums, int own = 0) {
     const int n = (a.D + (order == kOdd ? 7 : 0) + e - 1) / e;   // with the most that a phase adds
     int rows = 1;
     if (n <= 32) {
@@ -671,7 +692,7 @@ struct Plan {
     }
     with_ring = with_ring && n > 32 && order != kApart;
     int blocks = place / threads;
-    auto fit = [&] { return ((224 * 1024) / blocks - 2048) / row_bytes; };
+    auto fit = [&] { return (blocks > 1 ? kShared / blocks - 2048 : kShared - own * threads) / row_bytes; };
     while (with_ring && blocks > 1 && fit() < 2) --blocks;
     const long long most = (a.M + rows - 1LL) / rows, there = (long long)sms * blocks;
     grid = static_cast<int>(most < there ? most : there);
@@ -684,6 +705,7 @@ struct Plan {
       if (ring.stages > need) ring.stages = static_cast<int>(need);
       smem = (size_t)ring.stages * row_bytes;
     }
+    smem += own * threads;
   }
 };
 
@@ -694,7 +716,7 @@ int row_bytes(const BlockNormArgs& a, int es_a, int es_h) {
 
 template <typename K> cudaError_t launch(K* kernel, const Plan& p, const BlockNormArgs& a, cudaStream_t st) {
   if (p.smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
     if (e != cudaSuccess) return e;
   }
   kernel<<<p.grid, p.threads, p.smem, st>>>(a, p.ring, p.tpr);
@@ -717,6 +739,9 @@ template <typename F> void bwd_shape(int D, int order, F&& go) {
   else if (D <= 4096) go(Int<8>{}, Int<512>{}, Int<1>{});
   else go(Int<16>{}, Int<512>{}, Int<1>{});
 }
+
+// Bytes of shared memory that a thread of the backward keeps its weights in.
+constexpr int bwd_own(int e) { return e > 8 ? 2 * 4 * e : 0; }
 
 }  // namespace
 
@@ -752,7 +777,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, int h_dtype
   by_type(dtype, h_dtype, order, [&](auto ta, auto th, auto o) {
     bwd_shape(a.D, order, [&](auto e, auto threads, auto blocks) {
       const Plan p(a, sms, order, e, threads * blocks, ring_holds<decltype(th), decltype(e)::value>(),
-                   row_bytes(a, es_a, es_h), a.part != nullptr);
+                   row_bytes(a, es_a, es_h), a.part != nullptr, bwd_own(e));
       grid = p.grid;
       err = launch(block_norm_bwd_kernel<decltype(ta), decltype(th), decltype(o)::value, decltype(e)::value,
                                          decltype(threads)::value, decltype(blocks)::value>,

@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       if (a.post_norm) {
         float s[1] = {dot(v, v)};
         row_sums<WIDE>(s, tpr, buf, turn);
+        if (RING) ring.refill(row, first, step);
         rstd_b = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
         pairs<P>([&](int i) { v[i] = mul2(v[i], both(rstd_b)); });
       }
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       if (live) ring.template get<TH, RING>(4, row, c, g);
       if (RING) __syncthreads();
     }
-    if (RING) ring.refill(row, first, step);
+    if (RING && !(a.branch && a.post_norm)) ring.refill(row, first, step);
     if (RING && !AGAIN) ring.next();
     if (live && a.dh) store_row(static_cast<TH*>(a.dh) + row * D, c, g);
     if (!a.branch) {

@@ -404,6 +404,10 @@ __device__ __forceinline__ int phase_of(long long row, int D) { return static_ca
 template <typename TA, typename TH, int ORDER, int E, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNormArgs a, RingLayout l, int tpr) {
   constexpr bool WIDE = THREADS != kNarrow, RING = WIDE && ORDER != kApart;
+  // fp32 rows fill the ring with two of them: the next copies begin as soon as they can, behind the
+  // first of two sums (M4096 D4096 66 -> 59 us); bf16 ones, four and more, only waited for their
+  // issue there (M8192 D4096 59 -> 61)
+  constexpr bool EARLY = RING && sizeof(TA) == 4;
   constexpr int P = E / 2;
   using Row = f2[P];
   __shared__ __align__(16) float buf[2][32];
@@ -448,6 +452,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
       if (a.post_norm) {
         float s[1] = {dot(u, u)};
         row_sums<WIDE>(s, tpr, buf, turn);
+        if (EARLY) ring.refill(row, first, step);
         rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
       }
       if (a.gate) pairs<P>([&](int i) { u[i] = mul2(u[i], f[i]); });
@@ -458,10 +463,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_fwd_kernel(BlockNo
       float s[1] = {dot(h, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
       const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      if (RING) ring.refill(row, first, step);
+      if (RING && !(EARLY && a.branch && a.post_norm)) ring.refill(row, first, step);
       pairs<P>([&](int i) { h[i] = mul2(h[i], mul2(both(rstd), wy[i])); });
       if (live) store_row(static_cast<TA*>(a.y) + row * a.D, c, h);
-    } else if (RING) {
+    } else if (RING && !(EARLY && a.branch && a.post_norm)) {
       __syncthreads();
       ring.refill(row, first, step);
     }

@@ -17,8 +17,8 @@
 // A thread keeps its columns over all of its block's rows, so the two sums stay in registers;
 // the blocks leave one partial sum each, which a second kernel joins in order.
 //
-// bf16 with every part: forward M16384 D4096 106 us, 6.3 TB/s, memory bounds it; backward M8192
-// D4096 129 us, 4.1 TB/s: instructions (570 per warp and row) and three barriers a row, with 16
+// bf16 with every part: forward M16384 D4096 104 us, 6.4 TB/s, memory bounds it; backward M8192
+// D4096 125 us, 4.3 TB/s: instructions (570 per warp and row) and three barriers a row, with 16
 // warps on an SM as the registers allow.
 #include <type_traits>
 

@@ -14,9 +14,9 @@
 //   warp 9     the MMAs, in the first CTA of the pair
 // The pairs stay: one per two SMs walks the tiles, eight tiles of rows at a time, so that
 // neighbours in time share columns of B and rows of A in L2.
-// bf16 M8192 K4096 N4096 with a residual: 150 us, 1830 TFLOP/s, the tensor cores 83 % busy; on
-// end, at the power limit, 174 us.  fp32 (three pieces, six products, sums in registers) M4096
-// K4096 N4096: 485 us, 283 TFLOP/s; BN is 128 there, as a warp's 128 columns of 256 spill (800 us).
+// bf16 M8192 K4096 N4096 with a residual: 148 us, 1860 TFLOP/s, the tensor cores 85 % busy; on
+// end, at the power limit, 172 us.  fp32 (three pieces, six products, sums in registers) M4096
+// K4096 N4096: 469 us, 293 TFLOP/s; BN is 128 there, as a warp's 128 columns of 256 spill (800 us).
 #include <type_traits>
 
 #include "linear_tc.cuh"

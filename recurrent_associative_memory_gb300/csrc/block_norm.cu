@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
   long long row = first + slot;
   for (long long r0 = first; r0 < a.M; r0 += step, row += step) {
     const bool live = WIDE || row < a.M;
-    // a row that is none: zeros, so that it adds nothing to any sum
+    // a row that is none: zeros, and norms of 0 (1 / sqrt(0 + eps) is none where eps is 0), so that
+    // it adds nothing to any sum
     Row h, v, f, vs, g;   // vs: v f'(gate); AGAIN: f'(gate) until v is there again
     float rstd_b = 1.f;
     if (!WIDE) fill(h, 0.f), fill(v, 0.f);
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
         float s[1] = {dot(v, v)};
         row_sums<WIDE>(s, tpr, buf, turn);
         if (RING) ring.refill(row, first, step);
-        rstd_b = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+        rstd_b = live ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.f;
         pairs<P>([&](int i) { v[i] = mul2(v[i], both(rstd_b)); });
       }
       if (a.gate) {
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_norm_bwd_kernel(BlockNo
       pairs<P>([&](int i) { t[i] = mul2(dy[i], wy(i)); });
       float s[2] = {dot(h, h), dot(t, h)};
       row_sums<WIDE>(s, tpr, buf, turn);
-      const float rstd = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+      const float rstd = live ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.f;
       const f2 k = both(-s[1] * a.inv_d * rstd * rstd), r2 = both(rstd);
       pairs<P>([&](int i) {
         h[i] = mul2(h[i], r2);

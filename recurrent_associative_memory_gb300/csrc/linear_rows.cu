@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(Rows a, Epilogue 
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(lin::map_rank(at, r)) : "memory");
       v += u;
     }
-    float x[1] = {v + (e.bias ? static_cast<const float*>(e.bias)[n] : 0.f)}, s[1] = {1.f};
+    float x[1] = {v + (e.bias ? static_cast<const float*>(e.bias)[n] : 0.f)}, s[1];
     lin::act_all(e.act, e.slope != nullptr, x, s);
     const long long to = m * (long long)e.N + n;
     if (e.slope) static_cast<float*>(e.slope)[to] = s[0];

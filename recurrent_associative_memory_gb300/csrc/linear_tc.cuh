@@ -255,7 +255,11 @@ template <int N> __device__ __forceinline__ void act_all(int act, bool want, flo
     case DR_ACT_SILU: with(std::integral_constant<int, DR_ACT_SILU>{}); break;
     case DR_ACT_GELU_TANH: with(std::integral_constant<int, DR_ACT_GELU_TANH>{}); break;
     case DR_ACT_SIGMOID: with(std::integral_constant<int, DR_ACT_SIGMOID>{}); break;
-    default: break;
+    default:   // x itself, and a slope of 1
+      if (want) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = 1.f;
+      }
   }
 }
 

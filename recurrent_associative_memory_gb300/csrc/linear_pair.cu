@@ -98,6 +98,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int m0 = tm * 256 + rank * 128 + row0, m = m0 + lane;
       float* bias = reinterpret_cast<float*>(sm + L::oBias) + warp * NC;   // a warp's own: no barrier to be left at
       if constexpr (FULL) {
+        __syncwarp();   // every lane has read the last tile's: those without a row get here first
         for (int c = lane; c < NC; c += 32)
           bias[c] = e.bias && n0 + c < e.N ? to_f(static_cast<const T*>(e.bias)[n0 + c]) : 0.f;
         __syncwarp();

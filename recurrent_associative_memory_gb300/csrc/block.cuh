@@ -77,8 +77,10 @@ cudaError_t launch_in_call(bool after, void (*kernel)(P...), dim3 grid, int thre
   return e;
 }
 
-// f(x) and f'(x).  Behind +-30 a sigmoid is 0 or 1 to fp32, so the products with 1 - s take x
-// from there on as it is at the border: they stay 0 instead of 0 times infinity.
+// f(x) and f'(x).  The products with 1 - s take x as it is at a border behind which they are 0 to
+// fp32: they stay 0 instead of 0 times infinity.  Of a sigmoid s of x itself that is above 30,
+// where s is 1, and below -88, where s is 0 (it is cut below fp32's normal values, from -87.3 on;
+// at -60 it is 8.8e-27 and counts).  Gelu's sigmoid is one of a cube, and 0 or 1 behind +-30.
 template <int ACT> __device__ __forceinline__ float act_of(float x) {
   if constexpr (ACT == DR_ACT_RELU) return x > 0.f ? x : x == x ? 0.f : x;
   if constexpr (ACT == DR_ACT_SILU) return x * sigmoid_f(x);
@@ -92,7 +94,7 @@ template <int ACT> __device__ __forceinline__ float act_of(float x) {
 }
 
 template <int ACT> __device__ __forceinline__ float act_of(float x, float& slope) {
-  const float c = fminf(fmaxf(x, -30.f), 30.f);
+  const float c = fminf(fmaxf(x, ACT == DR_ACT_SILU ? -88.f : -30.f), 30.f);
   if constexpr (ACT == DR_ACT_RELU) {
     slope = x > 0.f ? 1.f : 0.f;
     return x > 0.f ? x : x == x ? 0.f : x;

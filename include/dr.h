@@ -533,9 +533,12 @@ typedef enum {
  * Matrix product with its epilogue, M rows of K channels to N:
  *     y = act(x W + bias) + residual
  * Every product is summed in fp32 and y is rounded once.  Few rows (single tokens)
- * take kernels of their own; which ones is decided by the sizes alone.  A row that holds NaN
+ * take kernels of their own.  The sizes decide which ones, in fp32 with up to 8 rows also
+ * whether the weight's rows stand on 16 bytes (w_s a multiple of 4): its values may be summed
+ * in another order where they do not, and the workspace differs.  A row that holds NaN
  * or an infinity makes no other row different; in fp32 an infinity, or a value that the
- * largest bf16 (3.39e38) does not reach, may come out as NaN.
+ * largest bf16 (3.39e38) does not reach, may come out as NaN, and values below 2^-100 may
+ * count with fewer bits.
  */
 typedef struct dr_linear {
   int dtype;               /* dr_dtype of everything but the slope                    */

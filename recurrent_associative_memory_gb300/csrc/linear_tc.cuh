@@ -73,13 +73,6 @@ inline bool make_operand_map(CUtensorMap* m, const Operand& o, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Can a tensor map hold it?  (A single row or step needs no stride.)
-inline bool operand_ok(const Operand& o) {
-  const int outer = o.mn ? o.k : o.rows;
-  return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 &&
-         (outer == 1 || (o.stride > 0 && o.stride % 8 == 0 && o.stride < (1LL << 38)));
-}
-
 // ---------------------------------------------------------------- a pair of CTAs
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -551,7 +551,8 @@ typedef struct dr_linear {
 /* Forward.  x [M,K], weight as above, bias [N] or NULL, residual [M,N] or NULL; y [M,N]
  * contiguous, which may be residual (the same rows).  slope [M,N] or NULL (contiguous)
  * receives act'(x W + bias), which the backward pass takes: fp16 for DR_BF16, fp32 for
- * DR_FP32.  Pointers other than bias 16-byte aligned.  Needs its workspace. */
+ * DR_FP32.  Pointers other than bias 16-byte aligned; no other two buffers are one where
+ * either is written.  Needs its workspace. */
 int dr_linear_fwd(const dr_linear *a, const void *x, const void *weight, const void *bias,
                   const void *residual, void *y, void *slope, void *workspace,
                   size_t workspace_bytes, dr_stream_t stream);
@@ -593,7 +594,8 @@ typedef struct dr_block_norm {
 
 /* Forward.  h [M,D]; branch [M,D] or NULL (only y is formed then, from h); gate [M,D] or
  * NULL (1); scale, post_weight, pre_weight fp32 [D] or NULL (1); h_out [M,D], needed with
- * branch, which may be h where h_s is D; y [M,D] or NULL.  h_out and y are contiguous. */
+ * branch, which may be h where h_s is D; y [M,D] or NULL.  h_out and y are contiguous; no
+ * other two buffers are one where either is written. */
 int dr_block_norm_fwd(const dr_block_norm *a, const void *h, const void *branch, const void *gate,
                       const float *scale, const float *post_weight, const float *pre_weight,
                       void *h_out, void *y, dr_stream_t stream);
@@ -606,7 +608,9 @@ typedef struct dr_block_norm_grads {
 } dr_block_norm_grads;
 
 /* Backward from d_h (of h', in the stream's type) and d_y [M,D] (contiguous; one of them
- * may be NULL: 0) and the forward's inputs: h as it was before the call.  The workspace
+ * may be NULL: 0) and the forward's inputs: h as it was before the call.  dh may be d_h or,
+ * where h_s is D, h; dbranch may be branch and dgate gate, where b_s or g_s is D; a gradient
+ * in the buffer of another one or of any other input is refused (DR_ERR_ARG).  The workspace
  * (256-byte aligned) is needed for the gradients over [D]. */
 int dr_block_norm_bwd(const dr_block_norm *a, const void *h, const void *branch, const void *gate,
                       const float *scale, const float *post_weight, const float *pre_weight,

@@ -68,6 +68,27 @@ int check_block_norm(const dr_block_norm* a) {
   return DR_OK;
 }
 
+// No gradient in the buffer of another one or of an input.  A row's dh may go over its d_h or h,
+// its dbranch over its branch and its dgate over its gate: whoever stores a value has read what
+// stood there, and nobody else reads it.
+bool norm_grads_apart(const dr_block_norm* a, const void* h, const void* branch, const void* gate, const float* scale,
+                      const float* post_weight, const float* pre_weight, const void* d_h, const void* d_y,
+                      const dr_block_norm_grads* g) {
+  auto rows = [&](const void* grad, const void* of, long long stride) {   // of's rows where they are not grad's
+    return grad && grad == of && a->M > 1 && stride != a->D;
+  };
+  if (rows(g->dh, h, a->h_s) || rows(g->dbranch, branch, a->b_s) || rows(g->dgate, gate, a->g_s)) return false;
+  const void* const grads[] = {g->dh, g->dbranch, g->dgate, g->dscale, g->dpost_weight, g->dpre_weight};
+  for (int i = 0; i < 6; ++i) {
+    const void* p = grads[i];
+    for (int j = i + 1; j < 6; ++j)
+      if (p && p == grads[j]) return false;
+    if (among(p, scale, post_weight, pre_weight, d_y)) return false;
+    if ((i != 0 && among(p, h, d_h)) || (i != 1 && among(p, branch)) || (i != 2 && among(p, gate))) return false;
+  }
+  return true;
+}
+
 BlockNormArgs block_norm_args(const dr_block_norm* a) {
   BlockNormArgs r{};
   r.M = a->M, r.D = a->D, r.gate_act = a->gate_act, r.post_norm = a->post_norm ? 1 : 0;
@@ -98,7 +119,8 @@ int dr_linear_fwd(const dr_linear* a, const void* x, const void* weight, const v
   if (need && (!workspace || workspace_bytes < need)) return DR_ERR_WORKSPACE;
   if (!aligned(256, workspace)) return DR_ERR_ALIGN;
   // a tile's rows are read by other tiles too; a residual's value only where it is added
-  if (among(y, x, weight) || among(slope, x, weight, residual, y) || (y == residual && a->M > 1 && a->r_s != a->N))
+  if (among(y, x, weight, bias) || among(slope, x, weight, bias, residual, y) ||
+      (y == residual && a->M > 1 && a->r_s != a->N))
     return DR_ERR_ARG;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
@@ -140,7 +162,8 @@ int dr_block_norm_fwd(const dr_block_norm* a, const void* h, const void* branch,
   if (st != DR_OK) return st;
   if (!branch && (gate || scale || h_out || a->post_norm)) return DR_ERR_ARG;
   if ((post_weight && !a->post_norm) || (pre_weight && !y)) return DR_ERR_ARG;
-  if (among(y, h, branch, gate, h_out) || among(h_out, branch, gate) || (h_out == h && a->M > 1 && a->h_s != a->D))
+  if (among(y, h, branch, gate, scale, post_weight, pre_weight, h_out) ||
+      among(h_out, branch, gate, scale, post_weight, pre_weight) || (h_out == h && a->M > 1 && a->h_s != a->D))
     return DR_ERR_ARG;
   if (!aligned(bytes_of(a->dtype), branch, gate, y) || !aligned(bytes_of(a->h_dtype), h, h_out) ||
       !aligned(4, scale, post_weight, pre_weight))
@@ -173,6 +196,7 @@ int dr_block_norm_bwd(const dr_block_norm* a, const void* h, const void* branch,
     return DR_ERR_ALIGN;
   const int sms = sm_count();
   if (!sms) return DR_ERR_CUDA;
+  if (!norm_grads_apart(a, h, branch, gate, scale, post_weight, pre_weight, d_h, d_y, g)) return DR_ERR_ARG;
   BlockNormArgs r = block_norm_args(a);
   if (g->dscale || g->dpost_weight || g->dpre_weight) {
     if (!workspace || workspace_bytes < dr_block_norm_bwd_workspace_bytes(a)) return DR_ERR_WORKSPACE;

@@ -151,19 +151,19 @@ def linear_bwd(x, weight, d_y, *, slope=None, want_dx=True, want_dweight=True, w
     check(d_y, "d_y", shape, x.dtype, dev)
     if slope is not None:
         check(slope, "slope", shape, _SLOPES[x.dtype], dev)
-    g = dict(grads or {})
+    given, g = grads or {}, {}
     if want_dx:
-        g["dx"] = _given_or_new(g.get("dx"), "dx", x.shape, x.dtype, x, dev)
+        g["dx"] = _given_or_new(given.get("dx"), "dx", x.shape, x.dtype, x, dev)
     if want_dweight:
+        dw = given.get("dweight")
         if a.w_transposed:
-            given = g.get("dweight")
-            if given is not None:
-                check(given.t(), "dweight.t()", (a.N, a.K), x.dtype, dev)
-            g["dweight"] = x.new_empty((a.N, a.K)).t() if given is None else given
+            if dw is not None:
+                check(dw.t(), "dweight.t()", (a.N, a.K), x.dtype, dev)
+            g["dweight"] = x.new_empty((a.N, a.K)).t() if dw is None else dw
         else:
-            g["dweight"] = _given_or_new(g.get("dweight"), "dweight", (a.K, a.N), x.dtype, x, dev)
+            g["dweight"] = _given_or_new(dw, "dweight", (a.K, a.N), x.dtype, x, dev)
     if want_dbias:
-        g["dbias"] = _given_or_new(g.get("dbias"), "dbias", (a.N,), x.dtype, x, dev)
+        g["dbias"] = _given_or_new(given.get("dbias"), "dbias", (a.N,), x.dtype, x, dev)
     ws, n = scratch(dr.dr_linear_bwd_workspace_bytes, a, x, dev, workspace)
     call("dr_linear_bwd", dev, dr.dr_linear_bwd, a, x, weight, d_y, slope,
          g["dx"] if want_dx else None, g["dweight"] if want_dweight else None,

@@ -543,7 +543,7 @@ typedef enum {
 typedef struct dr_linear {
   int dtype;               /* dr_dtype of everything but the slope                    */
   int act;                 /* dr_act                                                  */
-  int M, K, N;             /* rows, channels in, channels out; K, N up to 2^24        */
+  int M, K, N;             /* rows, up to 2^31 - 512; channels in and out, up to 2^24 */
   int w_transposed;        /* 0: W[k,n] at k w_s + n;  1: at n w_s + k                */
   long long x_s, w_s, r_s; /* row strides of x, W and residual; rows are contiguous   */
 } dr_linear;

@@ -21,6 +21,7 @@ namespace {
 
 constexpr long long kMaxElements = 1LL << 40;   // of one tensor
 constexpr int kMaxChannels = 1 << 24;           // of a matrix product
+constexpr int kMaxRows = INT_MAX - 511;         // and its rows: the last tile, of 256 at most, counts in an int too
 constexpr int kMaxRow = 8192;                   // channels of a norm
 constexpr long long kMaxBlocks = 0x7fffffffLL;  // of one launch
 
@@ -46,7 +47,7 @@ int sm_count() {
 int check_linear(const dr_linear* a) {
   if (!dtype_ok(a->dtype)) return DR_ERR_DTYPE;
   if (!act_ok(a->act)) return DR_ERR_ARG;
-  if (a->M < 1 || a->K < 1 || a->N < 1 || a->K > kMaxChannels || a->N > kMaxChannels) return DR_ERR_SHAPE;
+  if (a->M < 1 || a->K < 1 || a->N < 1 || a->M > kMaxRows || a->K > kMaxChannels || a->N > kMaxChannels) return DR_ERR_SHAPE;
   if (a->M >= kMaxElements / a->K || a->M >= kMaxElements / a->N || (long long)a->K * a->N >= kMaxElements) return DR_ERR_SHAPE;
   // blocks of the launches: tiles of 64 by 64
   const long long m = (a->M + 63LL) / 64, k = (a->K + 63LL) / 64, n = (a->N + 63LL) / 64;

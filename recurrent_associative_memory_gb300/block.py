@@ -28,7 +28,9 @@ import torch
 from . import dr
 from .tensors import DTYPES, activations, call, check, check_rows, on_stream, ptr, scratch
 
-__all__ = ["linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd"]
+__all__ = ["linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd", "MAX_CHANNELS"]
+
+MAX_CHANNELS = 8192   # of a norm's row
 
 _SLOPES = {torch.bfloat16: torch.float16, torch.float32: torch.float32}
 _FP32 = torch.float32

@@ -40,6 +40,24 @@ def _project(x, weight, **kw):
     return block.linear_fwd(x, weight, **kw)[0]
 
 
+def _norm(x):
+    return torch.nn.functional.rms_norm(x.float(), x.shape[-1:])
+
+
+def _join(h, o=None, *, gate=None, gate_act="none", scale=None, post_norm=False, post_weight=None):
+    """The end of a block that gave o (None: the first one begins) and the start of the next: (the
+    norm of h', h').  Rows wider than the norms' kernels take go through plain operations."""
+    if h.shape[-1] <= block.MAX_CHANNELS:
+        return block.block_norm_fwd(h, o, gate=gate, gate_act=gate_act, scale=scale, post_norm=post_norm,
+                                    post_weight=post_weight, eps=EPS)
+    if o is not None:
+        u = _norm(o) * post_weight if post_norm else o.float()
+        if gate is not None:
+            u = u * (torch.sigmoid(gate.float()) if gate_act == "sigmoid" else gate.float())
+        h = (h.float() + (u if scale is None else u * scale)).to(h.dtype)
+    return _norm(h).to(h.dtype), h
+
+
 class _Layer:
     end = {}     # how its block adds what it gives to the stream, besides the layer's gate
 
@@ -192,10 +210,10 @@ class HybridStack:
         """tokens [B,T], lens int32 [B]: (logits [B,T,vocab], state) after each sequence's
         lens[b] tokens.  Logits past a sequence's end mean nothing."""
         h, states = self.embed[tokens], []
-        x, _ = block.block_norm_fwd(h, eps=EPS)
+        x, _ = _join(h)
         for layer in self.layers:
             o, state = layer.prefill(x, lens)
-            x, h = block.block_norm_fwd(h, o, gate=layer.gate(x), eps=EPS, **layer.end)
+            x, h = _join(h, o, gate=layer.gate(x), **layer.end)
             states.append(state)
         return _project(x, self.unembed), (states, lens.clone())
 
@@ -203,10 +221,10 @@ class HybridStack:
         """One token [B] per sequence: logits [B,vocab]; the state goes on in place."""
         states, pos = state
         h = self.embed[tokens]
-        x, _ = block.block_norm_fwd(h, eps=EPS)
+        x, _ = _join(h)
         for layer, s in zip(self.layers, states):
             o = layer.step(x, s, pos)
-            x, h = block.block_norm_fwd(h, o, gate=layer.gate(x), eps=EPS, **layer.end)
+            x, h = _join(h, o, gate=layer.gate(x), **layer.end)
         pos += 1
         return _project(x, self.unembed)
 

@@ -86,7 +86,7 @@ inline int order_of(const BlockNormArgs& a) {
 
 // A launch: blocks that stay on every SM, in the place of `place` threads, and the rows on their
 // way in what each of them has of its shared memory, two at least (a row's place goes to the
-// next but one while the next is worked on); for that fewer blocks share an SM.
+// next but one while the next is worked on): so much there is at every length.
 constexpr int kShared = 227 * 1024 - 512;   // of an SM, for what a launch asks for
 
 struct Plan {
@@ -103,9 +103,8 @@ struct Plan {
       tpr = threads = (n + 31) / 32 * 32;
     }
     with_ring = with_ring && n > 32 && order != kApart;
-    int blocks = place / threads;
+    const int blocks = place / threads;
     auto fit = [&] { return (blocks > 1 ? kShared / blocks - 2048 : kShared - own * threads) / row_bytes; };
-    while (with_ring && blocks > 1 && fit() < 2) --blocks;
     const long long most = (a.M + rows - 1LL) / rows, there = (long long)sms * blocks;
     grid = static_cast<int>(most < there ? most : there);
     if (order == kOdd && grid < most) grid = grid / 8 * 8;   // a block's rows have one phase

@@ -550,9 +550,9 @@ typedef struct dr_linear {
 
 /* Forward.  x [M,K], weight as above, bias [N] or NULL, residual [M,N] or NULL; y [M,N]
  * contiguous, which may be residual (the same rows).  slope [M,N] or NULL (contiguous)
- * receives act'(x W + bias), which the backward pass takes: fp16 for DR_BF16, fp32 for
- * DR_FP32.  Pointers other than bias 16-byte aligned; no other two buffers are one where
- * either is written.  Needs its workspace. */
+ * receives act'(x W + bias), which the backward pass takes (1 with DR_ACT_NONE): fp16 for
+ * DR_BF16, so in steps of 2^-24 near 0, fp32 for DR_FP32.  Pointers other than bias 16-byte
+ * aligned; no other two buffers are one where either is written.  Needs its workspace. */
 int dr_linear_fwd(const dr_linear *a, const void *x, const void *weight, const void *bias,
                   const void *residual, void *y, void *slope, void *workspace,
                   size_t workspace_bytes, dr_stream_t stream);
@@ -580,7 +580,7 @@ size_t dr_linear_bwd_workspace_bytes(const dr_linear *a);
  * h is the residual stream and branch what the block's mixer has given.  y is the norm of
  * h' as it was summed, before it is rounded to the stream's type.  Squares are summed in
  * fp32: a row whose sum passes its range (values from 1e18 on) has a norm of 0.  With eps 0 a
- * row of zeros has NaN.
+ * row whose squares are 0 in fp32 (zeros, or values below 1e-23) has NaN or infinities.
  */
 typedef struct dr_block_norm {
   int dtype;               /* dr_dtype of branch, gate, y and their gradients         */

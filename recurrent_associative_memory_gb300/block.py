@@ -207,8 +207,9 @@ def _block_norm(h, branch, gate, gate_act, scale, post_norm, post_weight, pre_we
 def block_norm_fwd(h, branch=None, *, gate=None, gate_act="none", scale=None, post_norm=False,
                    post_weight=None, pre_weight=None, eps=1e-6, want_y=True, dtype=None, y=None,
                    h_out=None, stream=None):
-    """h, branch, gate [M,D] or [B,T,D]; scale, post_weight, pre_weight fp32 [D].  branch and
-    gate share a type, h has the same or fp32.  ``post_norm``: the branch's norm is taken.
+    """h, branch, gate [M,D] or [B,T,D], D up to ``MAX_CHANNELS``; scale, post_weight, pre_weight
+    fp32 [D].  branch and gate share a type, h has the same or fp32.  ``post_norm``: the branch's
+    norm is taken.
     Without a branch y is the norm of h, in ``dtype`` (default: h's).  ``h_out`` may be h.
     Returns (y or None without ``want_y``, h'); h' is h itself without a branch."""
     a, dev, dtype = _block_norm(h, branch, gate, gate_act, scale, post_norm, post_weight,
@@ -234,7 +235,8 @@ def block_norm_bwd(h, branch=None, *, d_h=None, d_y=None, gate=None, gate_act="n
     """The forward's inputs (h as it was before the call) and the gradients of its outputs: d_h
     [..,D] in h's type, d_y in the branch's; one of them may be None (0).  Returns dict(dh, and
     where the input is given dbranch, dgate, dscale, dpost_weight and, with d_y, dpre_weight);
-    the last three fp32 [D].  ``grads`` may hold output tensors under these names."""
+    the last three fp32 [D].  ``grads`` may hold output tensors under these names; dh may be d_h or
+    h, dbranch branch and dgate gate, no other two may be one."""
     a, dev, dtype = _block_norm(h, branch, gate, gate_act, scale, post_norm, post_weight,
                                 pre_weight, eps, dtype)
     if d_h is not None:

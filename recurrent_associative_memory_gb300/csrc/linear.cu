@@ -78,11 +78,18 @@ long long step_cycles(bool fp32, int m, int n, int rows) {
 // C[m,n] = sum over k of A[m,k] B[n,k], and its epilogue where `full`.
 // Which kernel: the one whose busiest SM needs the fewest cycles for its tiles, or for the
 // operands out of memory (3500 bytes a cycle; a quarter of the shorter of the two does not
-// overlap), and for what a kernel costs besides: start, first loads and the last epilogue.  Clusters of several CTAs leave SMs unused (a GPC's number
-// of SMs is no multiple of theirs; eight of 200 KB hardly find their place), and a second wave
-// of the small kernel waits for the first.  Both sides, bf16, us with 4 us of events: M512
-// K4096 N4096 pairs of 256 x 128 23.5, of 256 x 256 30.7, small 26.6; M128 22.5, 30, and small,
-// 128 rows cut in four, 16.4; M64 N16384 36.8, 34.1, small, 64 rows, 28.7, cut in two 34.8.
+// overlap), and for what a kernel costs besides: start, first loads and the last epilogue.
+// Clusters of several CTAs leave SMs unused (a GPC's number of SMs is no multiple of theirs; eight
+// of 200 KB hardly find their place), and a second wave of the small kernel waits for the first.
+// Both sides, bf16, us with 4 us of events: M512 K4096 N4096 pairs of 256 x 128 23.5, of 256 x 256
+// 30.7, small 26.6; M128 22.5, 30, and small, 128 rows cut in four, 16.4; M64 N16384 36.8, 34.1,
+// small, 64 rows, 28.7, cut in two 34.8.
+// Its constants are fitted, so it misses here and there.  With every offer timed, in graphs of 24
+// calls, at 85 sizes (M 1 to 1024, K512 N512 to K4096 N16384 and K8192 N2048; fp32 M 16 to 1024),
+// the choice is within 10 % of the best at 76; elsewhere it mostly cuts K too often: bf16 M64 K512
+// N1536 32 rows cut in four 6.2 us, 16 in two 4.9; M512 K512 N512 64 in four 6.7, 32 in two 5.4;
+// M512 K2048 N2048 256 in four 12.3, pairs of 256 x 128 9.9; fp32 M300 K512 N1536 13.6, 64 in two
+// 10.9.
 cudaError_t product(const Operand& A, const Operand& B, Epilogue e, bool full, int dtype, int sms, cudaStream_t st) {
   const bool fp32 = dtype == DR_FP32;
   const int es = fp32 ? 4 : 2;

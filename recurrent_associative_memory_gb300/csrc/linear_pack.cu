@@ -8,6 +8,13 @@
 // The gradient at the product, d = d_y * slope, is formed once for both backward products, in
 // the same layout, and the bias's gradient is summed from it in fp32 on the way (bf16 M8192 N8192
 // 66 us, 6.1 TB/s).
+//
+// bf16 rounds d to its type, as a gradient that is handed from one bf16 operator to the next is:
+// dx and dW are 2.4e-3 off (relative, over all of M8192 K2048 N8192), 1.7e-3 if d were exact.  A
+// second piece of d would give that and double both products, 162 us each of the call's 516.  The
+// slope is fp16: at most 2^-11 off where it counts, next to d's 2^-8.  Its steps of 2^-24 at the
+// bottom leave slopes below 7.6e-6 (a sigmoid's from |x| = 11.8 on, SiLU's from x = -14.4) fewer
+// bits than bf16 has and those below 3e-8 none: at most 2^-25 |d_y| of d.
 #include "linear_tc.cuh"
 
 namespace dr {

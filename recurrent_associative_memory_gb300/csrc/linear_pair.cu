@@ -17,6 +17,8 @@
 // bf16 M8192 K4096 N4096 with a residual: 148 us, 1860 TFLOP/s, the tensor cores 85 % busy; on
 // end, at the power limit, 172 us.  fp32 (three pieces, six products, sums in registers) M4096
 // K4096 N4096: 469 us, 293 TFLOP/s; BN is 128 there, as a warp's 128 columns of 256 spill (800 us).
+// Ten warps are three on a partition, so each has 168 registers, the two that load and issue too;
+// fp32 with the whole epilogue spills 208 bytes of them at that (the gradients' products none).
 #include <type_traits>
 
 #include "linear_tc.cuh"

@@ -148,6 +148,8 @@ template <int MT, bool W_T> cudaError_t go(const Rows& a, const Epilogue& e, lon
 //   K2048 N2048   1 row 12, 8 rows 16; 16 rows 25, as [N,K] 39;  pieces 22.5 for any of them
 //   K4096 N16384  1 row 45, 8 rows 76; 16 rows 125, as [N,K] 268;  pieces 176
 //   K8192 N1024   8 rows 33; 16 rows 52, as [N,K] 59;  pieces 43
+// So 16 rows would gain for a wide weight as [K,N] (125 for 176) and lose for narrower ones and as
+// [N,K]: 8 is where every size and order gains.
 bool linear_rows_supported(const LinearArgs& a, int dtype) {
   return dtype == DR_FP32 && a.M <= 8 && a.w_s % 4 == 0 && a.w_s >= 0;
 }
